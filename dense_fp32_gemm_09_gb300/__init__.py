@@ -3,6 +3,9 @@
 Thin Python face of the C ABI in ``include/sgemm.h``.  PyTorch supplies device
 memory and streams; every step of the product runs in the library's kernels.
 The library is loaded on first use and its absence is an error.
+
+Around the product: 4-bit operands and their tensor-core product (``mx4``), and the norms
+of a gated residual block with their gradients (``norms``).
 """
 from __future__ import annotations
 
@@ -14,7 +17,24 @@ from ._abi import (SGEMM_ERR_INVALID_ARG, SGEMM_ERR_LAUNCH, SGEMM_ERR_UNSUPPORTE
 __all__ = ["sgemm", "sgemm_run", "sgemm_run_ws", "sgemm_run_with", "sgemm_run_host",
            "sgemm_run_noalloc", "sgemm_run_ex", "sgemm_run_op",
            "sgemm_query_config", "sgemm_workspace_size", "kernel_table", "launch_count",
-           "SgemmError", "load"]
+           "SgemmError", "load",
+           "Mx4", "mx4_quantize", "mx4_dequantize", "mx4_matmul",
+           "norm_before", "norm_before_backward", "norm_after", "norm_after_backward"]
+
+_BLOCK_OPS = {name: module for module, names in (
+    ("mx4", ("Mx4", "mx4_quantize", "mx4_dequantize", "mx4_matmul")),
+    ("norms", ("norm_before", "norm_before_backward", "norm_after", "norm_after_backward")),
+) for name in names}
+
+
+def __getattr__(name):
+    # These modules need torch, which the rest of the package imports only when called.
+    if name in _BLOCK_OPS:
+        import importlib
+        value = getattr(importlib.import_module(f".{_BLOCK_OPS[name]}", __name__), name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _stream_handle(stream) -> int:

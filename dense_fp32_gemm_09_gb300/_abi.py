@@ -33,7 +33,7 @@ class SgemmConfig(ctypes.Structure):
 
 
 # name -> (restype, argtypes)
-_i, _sz, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_i, _sz, _vp, _f = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
 _RUN = [_i, _i, _i, _vp, _i, _vp, _i, _vp, _i]
 SIGNATURES = {
     "sgemm_run": (_i, _RUN + [_vp]),
@@ -57,6 +57,14 @@ SIGNATURES = {
     "sgemm_tf32x3_prepare": (_i, _RUN[:7] + [_vp, _sz, _vp]),
     "sgemm_tf32x3_multiply": (_i, [_i, _i, _i, ctypes.c_float, ctypes.c_float, _vp, _i, _vp, _sz,
                                    _vp]),
+    "sgemm_mx4_sizes": (_i, [_i, _i, _i, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+    "sgemm_mx4_quantize": (_i, [_i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp]),
+    "sgemm_mx4_dequantize": (_i, [_i, _i, _i, _vp, _vp, _vp, _i, _vp, _i, _vp]),
+    "sgemm_mx4_matmul": (_i, [_i, _i, _i, _i, _f] + [_vp] * 6 + [_f, _i, _vp, _i, _vp]),
+    "sgemm_norm_forward": (_i, [_i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _f, _f,
+                                _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp]),
+    "sgemm_norm_backward": (_i, [_i, _i, _i] + [_vp, _i] * 3 + [_vp, _vp, _vp, _i, _vp, _vp, _i,
+                                 _vp, _i, _f] + [_vp, _i] * 3 + [_vp, _vp, _vp]),
     "sgemm_device_status": (_i, []),
     "sgemm_selftest_bounded_wait": (_i, [_i]),
     "sgemm_schedule_check": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(SgemmConfig)]),

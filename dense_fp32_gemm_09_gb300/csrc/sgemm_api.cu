@@ -944,6 +944,55 @@ int check_operands(int transa, int transb, int M, int N, int K, const float* A, 
     return check_args_op(transa, transb, M, N, K, A, lda, B, ldb, C, ldc);
 }
 
+int current_device_sms(int* sms) {
+    // Kept per device; 0: not asked yet.  The compute capability never changes, so
+    // these outlive sgemm_shutdown.
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) {
+        const int n = known[dev].load(std::memory_order_relaxed);
+        if (n > 0) {
+            *sms = n;
+            return SGEMM_OK;
+        }
+    }
+    int major = 0, minor = 0, count = 0;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) {
+        set_error("device query", e);
+        cudaGetLastError();
+        return SGEMM_ERR_UNSUPPORTED;
+    }
+    if (major != 10 || minor != 3) {
+        std::snprintf(t_last_error, sizeof(t_last_error),
+                      "device %d is sm_%d%d; this library is built for sm_103a only", dev, major,
+                      minor);
+        return SGEMM_ERR_UNSUPPORTED;
+    }
+    if (dev < kMaxDevices) known[dev].store(count, std::memory_order_relaxed);
+    *sms = count;
+    return SGEMM_OK;
+}
+
+void count_launches(int n) {
+    g_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed);
+}
+
+int stream_workspace(cudaStream_t stream, size_t need, void** out,
+                     std::unique_lock<std::mutex>* hold) {
+    return library_workspace(stream, need, out, hold);
+}
+
+bool byte_ranges_overlap(const void* p, long long n, const void* q, long long m) {
+    if (p == nullptr || q == nullptr || n <= 0 || m <= 0) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + static_cast<uintptr_t>(m) && b < a + static_cast<uintptr_t>(n);
+}
+
 void set_last_error_message(const char* msg) {
     std::snprintf(t_last_error, sizeof(t_last_error), "%s", msg);
 }

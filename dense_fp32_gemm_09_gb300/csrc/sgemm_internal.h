@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/sgemm.h"
 #include "sgemm_args.h"
 
@@ -60,5 +62,77 @@ int tf32x3_multiply(int M, int N, int K, float alpha, float beta, float* C, long
 int tf32x3_tile_width(int M, int N, int K, int sms);
 int tf32x3_query(int M, int N, int K, int sms, sgemm_config* out);
 
+// The current device's SM count; SGEMM_ERR_UNSUPPORTED (with a message) unless it is
+// an sm_103 GPU.
+int current_device_sms(int* sms);
+// Adds to sgemm_launch_count.
+void count_launches(int n);
+// The library-owned workspace of (current device, stream), at least `need` bytes; the
+// lock is held until the caller has queued its launches.
+int stream_workspace(cudaStream_t stream, size_t need, void** out,
+                     std::unique_lock<std::mutex>* hold);
+bool byte_ranges_overlap(const void* p, long long n, const void* q, long long m);
+
+// ----------------------------------------------------------------------------
+// 4-bit operands (sgemm_mx4.cu, sgemm_mx4_matmul.cu) and norms (sgemm_norm.cu);
+// checked arguments of one call (sgemm_block_api.cu).
+// ----------------------------------------------------------------------------
+struct Mx4Quantize {
+    int trans, rows, cols, dtype, format;   // rows x cols: the quantised matrix
+    const void* X;
+    long long ldx;
+    const float* tensor_scale;
+    uint8_t *codes, *scales;
+};
+struct Mx4Dequantize {
+    int rows, cols, dtype, format;
+    const uint8_t *codes, *scales;
+    const float* tensor_scale;
+    void* Y;
+    long long ldy;
+};
+struct Mx4Matmul {
+    int M, N, K, dtype, format;
+    float alpha, beta;
+    const uint8_t *a_codes, *a_scales, *b_codes, *b_scales;
+    const float *a_ts, *b_ts;
+    void* C;
+    long long ldc;
+};
+struct NormForward {
+    int rows, cols, dtype, weight_dtype;
+    const void* block;        // null: no norm after, u = residual
+    const void* residual;
+    const void* weight;       // null: 1
+    const void* gate;         // null: 1; ldg 0: one row for all
+    long long ldb, ldr, ldg, ldy, ldh;
+    float scale, eps;
+    void* y;                  // null: not stored
+    float* rstd;
+    int next;                 // 1: the next block's norm too
+    const void* next_weight;
+    void* h;
+    float* next_rstd;
+    int format;               // -1: h in the input's type, else 4-bit
+    uint8_t *codes, *scales;
+    const float* tensor_scale;
+};
+struct NormBackward {
+    int rows, cols, dtype, weight_dtype;
+    const void *dy, *dh, *y, *block, *gate, *weight, *next_weight;
+    const float *rstd, *next_rstd;
+    long long lddy, lddh, ldy, ldb, ldg, lddx, lddb, lddg;
+    float scale;
+    void *dx, *dblock, *dgate;
+    float *dweight, *dnext_weight;
+    float* partial;           // the blocks' column sums
+};
+cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream);
+cudaError_t launch_mx4_dequantize(const Mx4Dequantize& q, cudaStream_t stream);
+cudaError_t launch_mx4_matmul(const Mx4Matmul& p, cudaStream_t stream);
+cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stream);
+size_t norm_backward_workspace(const NormBackward& p, int sms);
+cudaError_t launch_norm_backward(const NormBackward& p, int sms, cudaStream_t stream,
+                                 int* launches);
 
 }  // namespace sgemm

@@ -312,6 +312,105 @@ SGEMM_API int sgemm_tf32x3_multiply(int M, int N, int K, float alpha, float beta
                                     int ldc, const void* ws, size_t ws_bytes,
                                     sgemm_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit operands.  A rows x cols matrix is held as e2m1 codes (0, .5, 1, 1.5, 2, 3,
+ * 4, 6, with a sign) and one 8-bit scale for each block of consecutive columns:
+ *
+ *   SGEMM_NVFP4  blocks of 16, e4m3 scale s, and one fp32 scale ts for the whole
+ *                matrix (a device float; NULL means 1): value = code * s * ts.
+ *                s = amax / (6 ts) rounded to e4m3, at most 448; codes are x / (s ts)
+ *                rounded to the nearest e2m1 value (ties to even, at most 6).  A
+ *                block whose scale rounds to 0 has codes 0.
+ *   SGEMM_MXFP4  blocks of 32, scale 2^e with e = floor(log2 amax) - 2, at least -127:
+ *                value = code * 2^e; codes are x / 2^e rounded the same way.
+ *
+ * A block that holds an infinity or a NaN gets a NaN scale: all of it is NaN.
+ *
+ * Layout (rows and columns padded to 128):
+ *   codes   [rows/128][cols/32][128 rows][16 bytes], the even column in a byte's low half;
+ *   scales  [rows/128][blocks/4][row % 32][row/32 % 4][4 blocks], one byte each (e4m3, or
+ *           e + 127).
+ * Codes and scales of padded columns are zeros, those of padded rows are not written
+ * and do not matter.  Both buffers are 16-byte aligned device memory of
+ * sgemm_mx4_sizes() bytes.  rows and cols may each be at most 2^30.
+ * ------------------------------------------------------------------------- */
+typedef enum { SGEMM_F32 = 0, SGEMM_BF16 = 1, SGEMM_F16 = 2 } sgemm_dtype;
+typedef enum { SGEMM_NOT_QUANTIZED = -1, SGEMM_NVFP4 = 0, SGEMM_MXFP4 = 1 } sgemm_mx4_format;
+
+/* Bytes of the two buffers of a rows x cols matrix (host only). */
+SGEMM_API int sgemm_mx4_sizes(int rows, int cols, int format, size_t* codes, size_t* scales);
+
+/* Quantises X (`dtype`, leading dimension ldx in elements).  trans == 0: X is rows x cols;
+ * trans == 1: X is stored cols x rows and its transpose is quantised (blocks run along
+ * X's columns).  Any alignment of X to its elements.  Asynchronous on `stream`; one
+ * launch, no workspace.  rows == 0 or cols == 0 is a no-op. */
+SGEMM_API int sgemm_mx4_quantize(int trans, int rows, int cols, int dtype, const void* X, int ldx,
+                                 int format, const float* tensor_scale, void* codes, void* scales,
+                                 sgemm_stream_t stream);
+
+/* Y (rows x cols, `dtype`) = the values held: (code * s) * ts in fp32, rounded once. */
+SGEMM_API int sgemm_mx4_dequantize(int rows, int cols, int format, const void* codes,
+                                   const void* scales, const float* tensor_scale, int dtype,
+                                   void* Y, int ldy, sgemm_stream_t stream);
+
+/* C (M x N, `dtype`) = f * sum_k A[m,k] B[n,k] + beta * C with f = alpha * ts of A * ts of
+ * B; A is M x K, B is N x K (a layer's weight with one row per output), both in `format`.
+ * Sums are held in fp32 and rounded once to C's type.  BLAS conventions as for
+ * sgemm_run_ex: beta == 0 does not read C, alpha == 0 or K == 0 does not read A or B. */
+SGEMM_API int sgemm_mx4_matmul(int M, int N, int K, int format, float alpha, const void* a_codes,
+                               const void* a_scales, const float* a_tensor_scale,
+                               const void* b_codes, const void* b_scales,
+                               const float* b_tensor_scale, float beta, int dtype, void* C, int ldc,
+                               sgemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms around a residual block, over rows of `cols` numbers of `dtype`:
+ *
+ *   after:   r  = (mean(block^2) + eps)^-1/2
+ *            u  = residual + scale * gate * (block * r * weight)          stored as y
+ *   before:  r' = (mean(u^2) + eps)^-1/2
+ *            h  = u * r' * next_weight
+ *
+ * Without `block` u is `residual` (the norm before a block alone: y, rstd, weight and
+ * gate are NULL); with next == 0 the second half is left out (h, next_rstd and
+ * next_weight are NULL).  All arithmetic is fp32 and h is computed from u before it is
+ * rounded.  With a 4-bit `format` h is quantised as by sgemm_mx4_quantize, straight from
+ * fp32 to `codes` and `scales`, and h is NULL; else format is SGEMM_NOT_QUANTIZED.  Weights are of `weight_dtype`,
+ * NULL for ones; gate is NULL for ones, ldg == 0 one row shared by all rows.  r and r'
+ * go to rstd and next_rstd (fp32, one per row).  Outputs must not overlap inputs.
+ * Leading dimensions count elements; any alignment to the element.
+ * cols == 0 is SGEMM_ERR_INVALID_ARG, rows == 0 a no-op. */
+SGEMM_API int sgemm_norm_forward(int rows, int cols, int dtype, const void* block, int ldb,
+                                 const void* residual, int ldr, const void* weight,
+                                 const void* next_weight, int weight_dtype, const void* gate,
+                                 int ldg, float scale, float eps, void* y, int ldy, float* rstd,
+                                 int next, void* h, int ldh, float* next_rstd, int format,
+                                 const float* tensor_scale, void* codes, void* scales,
+                                 sgemm_stream_t stream);
+
+/* Gradients of the above from dy (of y; NULL for zeros) and dh (of h; NULL without a next
+ * norm), y and the saved rstd and next_rstd:
+ *
+ *   t            = dy + r' (next_weight dh - n' mean(next_weight dh n')),  n' = y r'   -> dx
+ *   g            = scale * gate * t
+ *   dblock       = r (weight g - n mean(weight g n)),  n = block r
+ *   dgate        = scale * t * n * weight     (fp32 sums over the rows where ldg == 0)
+ *   dweight      = sum over rows of g n       (fp32)
+ *   dnext_weight = sum over rows of dh n'     (fp32)
+ *
+ * dx is the gradient of `residual` (it may be NULL without dh: it is dy).  Without
+ * `block` only dx and dnext_weight are computed.  dgate, dweight and dnext_weight may be
+ * NULL.  The sums over rows are deterministic (a fixed order, no atomics) and use the
+ * library's workspace of the stream.  rows == 0 writes zeros to them. */
+SGEMM_API int sgemm_norm_backward(int rows, int cols, int dtype, const void* dy, int lddy,
+                                  const void* dh, int lddh, const void* y, int ldy,
+                                  const float* next_rstd, const void* next_weight,
+                                  const void* block, int ldb, const float* rstd,
+                                  const void* weight, int weight_dtype, const void* gate, int ldg,
+                                  float scale, void* dx, int lddx, void* dblock, int lddb,
+                                  void* dgate, int lddg, float* dweight, float* dnext_weight,
+                                  sgemm_stream_t stream);
+
 /* Synchronous: reads and clears the device flag that a bounded wait in a
  * tensor-core kernel sets when it gives up; returns SGEMM_ERR_TIMEOUT if it was
  * set, SGEMM_OK otherwise.  Call after synchronising the work in question. */
