@@ -231,7 +231,7 @@ int sgemm_mx4_matmul(int M, int N, int K, int format, float alpha, const void* a
             p.K = 0;
             p.a_ts = p.b_ts = nullptr;
         }
-        return launched(launch_mx4_matmul(p, reinterpret_cast<cudaStream_t>(stream)),
+        return launched(launch_mx4_matmul(p, sms, reinterpret_cast<cudaStream_t>(stream)),
                         "sgemm_mx4_matmul");
     });
 }

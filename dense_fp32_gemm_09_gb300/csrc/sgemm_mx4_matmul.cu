@@ -1,7 +1,30 @@
-// Product of two 4-bit matrices: C = alpha * ta * tb * A . B^T + beta * C
-// (sgemm_mx4_matmul).
+// Product of two 4-bit matrices: C = f * A . B^T + beta * C with f = alpha * ta * tb
+// (sgemm_mx4_matmul), on the tensor cores' block-scaled 4-bit form.
+//
+// tcgen05.mma kind::mxf4nvf4 multiplies 64 columns of codes at a time, each block of 16
+// (nvfp4) or 32 (mxfp4) scaled by the product of its two scales, and adds to fp32 sums
+// in tensor memory.  The weight B (N rows) is the instruction's 128-row operand and the
+// activations A (M rows) its column operand, so that a lane of tensor memory holds one
+// column n of C: the 32 lanes of a warp then store 32 neighbours of one row of C, at any
+// alignment, and few rows of A cost a narrow instruction instead of empty lanes.
+//
+// One CTA computes a 128 (n) x BQ (m) tile, or its share of the tile's K range: the CTAs
+// of a cluster take consecutive ranges and sum their parts in distributed shared memory
+// in rank order, so the result does not depend on timing.
+//   warp 0, one thread: bulk copies of slabs 256 columns deep into a ring.  The stored
+//     layout is already the operand layout (no swizzle), so a slab is one copy per
+//     operand and one for its scales.
+//   warp 1, one thread: tcgen05.cp of the scales to tensor memory, then four MMAs a slab.
+//     Each stage has its own scale columns: they are overwritten only after the stage's
+//     MMAs have completed, as its shared memory is.
+//   all four warps: the epilogue, one lane of tensor memory per thread.
+// Every wait is bounded; one that gives up sets the device status word and the CTA
+// drains, meets its cluster's barriers and exits.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
+#include "sgemm_async.cuh"
 #include "sgemm_internal.h"
 #include "sgemm_mx4.cuh"
 
@@ -9,63 +32,372 @@ namespace sgemm {
 namespace {
 
 using namespace mx4;
+using async::mbar_expect_tx;
+using async::mbar_fence_init;
+using async::mbar_init;
+using async::mbar_wait;
+using async::su32;
 
-// One block computes 16 x 16 elements of C, 32 columns of A and B at a time.
-template <typename T, int FORMAT>
-__global__ void __launch_bounds__(256) mx4_matmul_kernel(const Mx4Matmul p) {
-    __shared__ float sa[16][33], sb[16][33];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int chunks = chunks_of(p.K), groups = groups_of(p.K, FORMAT);
-    const long long m0 = blockIdx.y * 16LL, n0 = blockIdx.x * 16LL;
-    float acc = 0.0f;
-    for (int chunk = 0; chunk < (p.K + 31) / 32; ++chunk) {
-        if (threadIdx.x < 128) {
-            const bool a = threadIdx.x < 64;
-            const int r = (threadIdx.x & 63) >> 2, i = threadIdx.x & 3;
-            const long long row = (a ? m0 : n0) + r;
-            float v[8] = {};
-            if (row < (a ? p.M : p.N)) {
-                const uint8_t* codes = a ? p.a_codes : p.b_codes;
-                const uint8_t* scales = a ? p.a_scales : p.b_scales;
-                decode8(*reinterpret_cast<const uint32_t*>(
-                            codes + code_offset(row, chunk, chunks) + 4 * i), v);
-                const float s = scale_decode<FORMAT>(
-                    scales[scale_offset(row, (32 * chunk + 8 * i) / block_of(FORMAT), groups)]);
+constexpr int kMaxStages = 8;
+constexpr int kSlabChunks = 8;    // 256 columns a slab
+constexpr int kGroup = 8;
+
+struct MatmulPlan {
+    Mx4Matmul p;
+    int chunks, slabs, stages, split, tmem_cols, tiles_n, tiles_m;
+    int* status;
+};
+
+template <int FORMAT> constexpr int kChunksPerGroup = FORMAT == kNvfp4 ? 2 : 4;
+template <int FORMAT> constexpr int kSlabGroups = kSlabChunks / kChunksPerGroup<FORMAT>;
+// Shared memory of a stage: codes of both operands, then their scales.
+template <int FORMAT, int BQ> constexpr int kStageBytes =
+    kSlabChunks * (2048 + BQ * 16) + 2 * kSlabGroups<FORMAT> * 512;
+// Tensor-memory columns of a stage's scales: four per 128 rows and group.
+template <int FORMAT> constexpr int kStageCols = 8 * kSlabGroups<FORMAT>;
+
+// Operand tile without swizzle: 8 rows x 16 bytes contiguous, `lead` bytes from one
+// 16-byte column to the next, 128 bytes from one group of 8 rows to the next.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t lead) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(128 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;                      // descriptor version
+    return d;
+}
+// Instruction: e2m1 x e2m1, K = 64, M = 128, N = bq; the scales' type.
+template <int FORMAT>
+__host__ __device__ constexpr uint32_t mx4_idesc(int bq) {
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(bq >> 3) << 17) |
+           (FORMAT == kMxfp4 ? 1u << 23 : 0u) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
+template <int FORMAT>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (FORMAT == kNvfp4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+            "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X "
+            "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= s;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) (a ? sa : sb)[r][8 * i + j] = v[j];
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 32; ++k) acc = fmaf(sa[ty][k], sb[tx][k], acc);
-        __syncthreads();
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_c(const Mx4Matmul& p, float f, float acc, long long m,
+                                        long long n) {
+    const long long at = m * p.ldc + n;
+    if (p.dtype == kF32) {
+        float* c = static_cast<float*>(p.C) + at;
+        *c = p.beta == 0.0f ? f * acc : fmaf(f, acc, p.beta * *c);
+    } else if (p.dtype == kBf16) {
+        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
+        *c = from_float<__nv_bfloat16>(p.beta == 0.0f ? f * acc
+                                                      : fmaf(f, acc, p.beta * to_float(*c)));
+    } else {
+        __half* c = static_cast<__half*>(p.C) + at;
+        *c = from_float<__half>(p.beta == 0.0f ? f * acc : fmaf(f, acc, p.beta * to_float(*c)));
     }
-    const long long m = m0 + ty, n = n0 + tx;
-    if (m >= p.M || n >= p.N) return;
+}
+
+// grid: tiles x split CTAs; clusters of split.
+template <int FORMAT, int BQ>
+__global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
+    constexpr int kP = kSlabChunks * 2048, kQ = kSlabChunks * BQ * 16;
+    constexpr int kSf = kSlabGroups<FORMAT> * 512;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar;
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_s;
+    const Mx4Matmul& p = pl.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(blockIdx.x) % pl.split;
+    // Tiles run along m in groups of kGroup, then along n, so that the CTAs at work at
+    // one time share few operand rows.
+    const int tile = static_cast<int>(blockIdx.x) / pl.split;
+    const int group = tile / (kGroup * pl.tiles_n), in = tile - group * kGroup * pl.tiles_n;
+    const int high = min(kGroup, pl.tiles_m - group * kGroup);
+    const long long n0 = in / high * 128LL;
+    const long long m0 = static_cast<long long>(group * kGroup + in % high) * BQ;
+    const int first = static_cast<int>(static_cast<long long>(pl.slabs) * rank / pl.split);
+    const int last = static_cast<int>(static_cast<long long>(pl.slabs) * (rank + 1) / pl.split);
+    volatile int* abort_flag = &abort_s;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < pl.stages; ++s) {
+            mbar_init(su32(&full_bar[s]), 1);
+            mbar_init(su32(&empty_bar[s]), 1);
+        }
+        mbar_init(su32(&done_bar), 1);
+        abort_s = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         su32(&tmem_base_s)),
+                     "r"(pl.tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_base_s;
+    const uint32_t smem0 = su32(smem);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int groups = pl.chunks / kChunksPerGroup<FORMAT>;
+            const uint8_t* pc = p.b_codes + (n0 >> 7) * pl.chunks * 2048;
+            const uint8_t* ps = p.b_scales + (n0 >> 7) * groups * 512;
+            const uint8_t* qc = p.a_codes + (m0 >> 7) * pl.chunks * 2048 + (m0 & 127) * 16;
+            const uint8_t* qs = p.a_scales + (m0 >> 7) * groups * 512;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            int issued = 0;
+            for (int s = first; s < last; ++s) {
+                if (!mbar_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) {
+                    ok = false;
+                    break;
+                }
+                const int c0 = s * kSlabChunks, nc = min(kSlabChunks, pl.chunks - c0);
+                const int ng = nc / kChunksPerGroup<FORMAT>, g0 = c0 / kChunksPerGroup<FORMAT>;
+                const uint32_t fb = su32(&full_bar[stage]);
+                const uint32_t base = smem0 + stage * kStageBytes<FORMAT, BQ>;
+                mbar_expect_tx(fb, nc * (2048 + BQ * 16) + 2 * ng * 512);
+                bulk_load(base, pc + c0 * 2048LL, nc * 2048, fb);
+                bulk_load(base + kP + kQ, ps + g0 * 512LL, ng * 512, fb);
+                if (BQ == 128) {
+                    bulk_load(base + kP, qc + c0 * 2048LL, nc * 2048, fb);
+                } else {
+                    for (int c = 0; c < nc; ++c)
+                        bulk_load(base + kP + c * BQ * 16, qc + (c0 + c) * 2048LL, BQ * 16, fb);
+                }
+                bulk_load(base + kP + kQ + kSf, qs + g0 * 512LL, ng * 512, fb);
+                ++issued;
+                if (++stage == pl.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) {   // giving up: copies in flight land before the CTA exits
+                volatile int no_abort = 0;
+                for (int i = max(0, issued - pl.stages); i < issued; ++i)
+                    mbar_wait(su32(&full_bar[i % pl.stages]), (i / pl.stages) & 1, &no_abort,
+                              nullptr);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int s = first; s < last; ++s) {
+                if (!mbar_wait(su32(&full_bar[stage]), phase, abort_flag, pl.status)) break;
+                fence_after();
+                const int nc = min(kSlabChunks, pl.chunks - s * kSlabChunks);
+                const uint32_t base = smem0 + stage * kStageBytes<FORMAT, BQ>;
+                const uint32_t sfp = tmem + BQ + stage * kStageCols<FORMAT>;
+                const uint32_t sfq = sfp + kStageCols<FORMAT> / 2;
+                for (int g = 0; g < nc / kChunksPerGroup<FORMAT>; ++g) {
+                    copy_scales(sfp + 4 * g, operand_desc(base + kP + kQ + 512 * g, 128));
+                    copy_scales(sfq + 4 * g, operand_desc(base + kP + kQ + kSf + 512 * g, 128));
+                }
+                for (int j = 0; j < nc / 2; ++j) {
+                    // nvfp4: a group of four scales per instruction; mxfp4: two of a group.
+                    const int g = FORMAT == kNvfp4 ? j : j / 2;
+                    const uint32_t id = FORMAT == kNvfp4 ? 0u : 2u * (j & 1);
+                    mma<FORMAT>(tmem, operand_desc(base + j * 4096, 2048),
+                                operand_desc(base + kP + j * 2 * BQ * 16, BQ * 16),
+                                mx4_idesc<FORMAT>(BQ) | id << 4 | id << 29, sfp + 4 * g,
+                                sfq + 4 * g, s != first || j != 0);
+                }
+                commit(su32(&empty_bar[stage]));
+                if (++stage == pl.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            commit(su32(&done_bar));
+        }
+    }
+    __syncwarp();
+    const bool ok = __all_sync(0xFFFFFFFFu,
+                               mbar_wait(su32(&done_bar), 0, abort_flag, pl.status));
+    fence_after();
     float f = p.alpha;
     if (p.a_ts) f *= __ldg(p.a_ts);
     if (p.b_ts) f *= __ldg(p.b_ts);
-    T* c = static_cast<T*>(p.C) + m * p.ldc + n;
-    *c = from_float<T>(p.beta == 0.0f ? f * acc : fmaf(f, acc, p.beta * to_float(*c)));
+    const long long n = n0 + threadIdx.x;
+    const uint32_t mine = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    float* const part = reinterpret_cast<float*>(smem + pl.stages * kStageBytes<FORMAT, BQ>);
+#pragma unroll 1
+    for (int j = 0; j < BQ && m0 + j < p.M; j += 16) {
+        float v[16];
+        __syncwarp();
+        tmem_ld16(mine + j, v);
+        if (pl.split > 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(j + i) * 128 + threadIdx.x] = v[i];
+        } else if (ok && n < p.N) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (m0 + j + i < p.M) store_c(p, f, v[i], m0 + j + i, n);
+        }
+    }
+    // Tensor memory goes back before the cluster is waited for: a CTA that holds some
+    // while it waits for one that waits for some would end neither.
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(pl.tmem_cols)
+                     : "memory");
+    }
+    if (pl.split > 1) {
+        cluster_arrive();
+        cluster_wait();
+        const int own = BQ / pl.split;     // rank r sums columns [r, r + 1) * own
+        const uint32_t red = su32(part);
+        for (int c = rank * own; c < (rank + 1) * own && m0 + c < p.M; ++c) {
+            float acc = 0.0f;
+            for (int r = 0; r < pl.split; ++r) {
+                uint32_t remote;
+                float v;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                    : "=r"(remote) : "r"(red + (c * 128 + threadIdx.x) * 4), "r"(r));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+                acc += v;
+            }
+            if (ok && n < p.N) store_c(p, f, acc, m0 + c, n);
+        }
+        cluster_arrive();                  // its parts stay until the others have read them
+        cluster_wait();
+    }
+    asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// C = beta * C where there is nothing to multiply (K == 0 or alpha == 0).
+__global__ void __launch_bounds__(256) mx4_scale_kernel(const Mx4Matmul p) {
+    const long long total = static_cast<long long>(p.M) * p.N;
+    for (long long e = blockIdx.x * 256LL + threadIdx.x; e < total; e += gridDim.x * 256LL)
+        store_c(p, 0.0f, 0.0f, e / p.N, e % p.N);
+}
+
+template <int FORMAT, int BQ>
+cudaError_t launch_tile(const Mx4Matmul& p, int sms, cudaStream_t stream) {
+    MatmulPlan pl{};
+    pl.p = p;
+    pl.chunks = chunks_of(p.K);
+    pl.slabs = (pl.chunks + kSlabChunks - 1) / kSlabChunks;
+    const long long tiles_n = (p.N + 127) / 128, tiles_m = (p.M + BQ - 1) / BQ;
+    const long long tiles = tiles_n * tiles_m;
+    if (tiles > 0x7FFFFFFF / kGroup) return cudaErrorInvalidConfiguration;
+    pl.tiles_n = static_cast<int>(tiles_n);
+    pl.tiles_m = static_cast<int>(tiles_m);
+    pl.split = 1;
+    while (pl.split < 8 && tiles * pl.split * 2 <= sms && pl.split * 2 <= pl.slabs) pl.split *= 2;
+    constexpr int kMost = 220 * 1024;
+    const int red = pl.split > 1 ? BQ * 512 : 0;
+    const int per = (pl.slabs + pl.split - 1) / pl.split;
+    pl.stages = std::min({per, kMaxStages, (kMost - red) / kStageBytes<FORMAT, BQ>});
+    const int cols = BQ + pl.stages * kStageCols<FORMAT>;
+    pl.tmem_cols = 32;
+    while (pl.tmem_cols < cols) pl.tmem_cols *= 2;
+    // No more CTAs to an SM, by their shared memory, than find tensor memory there.
+    const int resident = 512 / pl.tmem_cols;
+    const int least = 228 * 1024 / (resident + 1);
+    const int smem = std::max(pl.stages * kStageBytes<FORMAT, BQ> + red,
+                              resident == 1 ? 116 * 1024 : least);
+    pl.status = status_word_ptr();
+    auto kernel = mx4_matmul_kernel<FORMAT, BQ>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMost);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = static_cast<unsigned>(pl.split);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(static_cast<unsigned>(tiles * pl.split));
+    c.blockDim = dim3(128);
+    c.dynamicSmemBytes = static_cast<size_t>(smem);
+    c.stream = stream;
+    c.attrs = at;
+    c.numAttrs = 2;
+    return cudaLaunchKernelEx(&c, kernel, pl);
+}
+
+template <int FORMAT>
+cudaError_t launch_format(const Mx4Matmul& p, int sms, cudaStream_t stream) {
+    if (p.M <= 16) return launch_tile<FORMAT, 16>(p, sms, stream);
+    if (p.M <= 32) return launch_tile<FORMAT, 32>(p, sms, stream);
+    if (p.M <= 64) return launch_tile<FORMAT, 64>(p, sms, stream);
+    return launch_tile<FORMAT, 128>(p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_mx4_matmul(const Mx4Matmul& p, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>((p.N + 15) / 16), static_cast<unsigned>((p.M + 15) / 16));
-    const bool nv = p.format == kNvfp4;
-    if (p.dtype == kF32)
-        nv ? mx4_matmul_kernel<float, kNvfp4><<<grid, 256, 0, stream>>>(p)
-           : mx4_matmul_kernel<float, kMxfp4><<<grid, 256, 0, stream>>>(p);
-    else if (p.dtype == kBf16)
-        nv ? mx4_matmul_kernel<__nv_bfloat16, kNvfp4><<<grid, 256, 0, stream>>>(p)
-           : mx4_matmul_kernel<__nv_bfloat16, kMxfp4><<<grid, 256, 0, stream>>>(p);
-    else
-        nv ? mx4_matmul_kernel<__half, kNvfp4><<<grid, 256, 0, stream>>>(p)
-           : mx4_matmul_kernel<__half, kMxfp4><<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_mx4_matmul(const Mx4Matmul& p, int sms, cudaStream_t stream) {
+    if (p.K == 0) {
+        if (p.beta == 1.0f) return cudaSuccess;
+        const long long blocks = (static_cast<long long>(p.M) * p.N + 255) / 256;
+        mx4_scale_kernel<<<static_cast<unsigned>(std::min<long long>(blocks, 8LL * sms)), 256, 0,
+                           stream>>>(p);
+        return cudaGetLastError();
+    }
+    return p.format == kNvfp4 ? launch_format<kNvfp4>(p, sms, stream)
+                              : launch_format<kMxfp4>(p, sms, stream);
 }
 
 }  // namespace sgemm
