@@ -130,6 +130,7 @@ struct NormBackward {
 cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream);
 cudaError_t launch_mx4_dequantize(const Mx4Dequantize& q, cudaStream_t stream);
 cudaError_t launch_mx4_matmul(const Mx4Matmul& p, int sms, cudaStream_t stream);
+cudaError_t launch_mx4_pair(const Mx4Matmul& p, int sms, cudaStream_t stream);
 cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stream);
 size_t norm_backward_workspace(const NormBackward& p, int sms);
 cudaError_t launch_norm_backward(const NormBackward& p, int sms, cudaStream_t stream,

@@ -24,9 +24,7 @@
 
 #include <algorithm>
 
-#include "sgemm_async.cuh"
-#include "sgemm_internal.h"
-#include "sgemm_mx4.cuh"
+#include "sgemm_mx4_tc.cuh"
 
 namespace sgemm {
 namespace {
@@ -39,7 +37,6 @@ using async::mbar_wait;
 using async::su32;
 
 constexpr int kMaxStages = 8;
-constexpr int kSlabChunks = 8;    // 256 columns a slab
 constexpr int kGroup = 8;
 
 struct MatmulPlan {
@@ -48,103 +45,11 @@ struct MatmulPlan {
     int* status;
 };
 
-template <int FORMAT> constexpr int kChunksPerGroup = FORMAT == kNvfp4 ? 2 : 4;
-template <int FORMAT> constexpr int kSlabGroups = kSlabChunks / kChunksPerGroup<FORMAT>;
 // Shared memory of a stage: codes of both operands, then their scales.
 template <int FORMAT, int BQ> constexpr int kStageBytes =
     kSlabChunks * (2048 + BQ * 16) + 2 * kSlabGroups<FORMAT> * 512;
 // Tensor-memory columns of a stage's scales: four per 128 rows and group.
 template <int FORMAT> constexpr int kStageCols = 8 * kSlabGroups<FORMAT>;
-
-// Operand tile without swizzle: 8 rows x 16 bytes contiguous, `lead` bytes from one
-// 16-byte column to the next, 128 bytes from one group of 8 rows to the next.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t lead) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>(128 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;                      // descriptor version
-    return d;
-}
-// Instruction: e2m1 x e2m1, K = 64, M = 128, N = bq; the scales' type.
-template <int FORMAT>
-__host__ __device__ constexpr uint32_t mx4_idesc(int bq) {
-    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(bq >> 3) << 17) |
-           (FORMAT == kMxfp4 ? 1u << 23 : 0u) | (static_cast<uint32_t>(128 >> 4) << 24);
-}
-template <int FORMAT>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                    uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    if constexpr (FORMAT == kNvfp4)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
-            "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-            "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X "
-            "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-            "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-}
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-            "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void fence_before() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void store_c(const Mx4Matmul& p, float f, float acc, long long m,
-                                        long long n) {
-    const long long at = m * p.ldc + n;
-    if (p.dtype == kF32) {
-        float* c = static_cast<float*>(p.C) + at;
-        *c = p.beta == 0.0f ? f * acc : fmaf(f, acc, p.beta * *c);
-    } else if (p.dtype == kBf16) {
-        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
-        *c = from_float<__nv_bfloat16>(p.beta == 0.0f ? f * acc
-                                                      : fmaf(f, acc, p.beta * to_float(*c)));
-    } else {
-        __half* c = static_cast<__half*>(p.C) + at;
-        *c = from_float<__half>(p.beta == 0.0f ? f * acc : fmaf(f, acc, p.beta * to_float(*c)));
-    }
-}
 
 // grid: tiles x split CTAs; clusters of split.
 template <int FORMAT, int BQ>
@@ -178,13 +83,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
         abort_s = 0;
         mbar_fence_init();
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         su32(&tmem_base_s)),
-                     "r"(pl.tmem_cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 1) tmem_alloc<1>(su32(&tmem_base_s), pl.tmem_cols);
     fence_before();
     __syncthreads();
     fence_after();
@@ -247,25 +146,25 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
                 const uint32_t sfp = tmem + BQ + stage * kStageCols<FORMAT>;
                 const uint32_t sfq = sfp + kStageCols<FORMAT> / 2;
                 for (int g = 0; g < nc / kChunksPerGroup<FORMAT>; ++g) {
-                    copy_scales(sfp + 4 * g, operand_desc(base + kP + kQ + 512 * g, 128));
-                    copy_scales(sfq + 4 * g, operand_desc(base + kP + kQ + kSf + 512 * g, 128));
+                    copy_scales<1>(sfp + 4 * g, operand_desc(base + kP + kQ + 512 * g, 128));
+                    copy_scales<1>(sfq + 4 * g, operand_desc(base + kP + kQ + kSf + 512 * g, 128));
                 }
                 for (int j = 0; j < nc / 2; ++j) {
                     // nvfp4: a group of four scales per instruction; mxfp4: two of a group.
                     const int g = FORMAT == kNvfp4 ? j : j / 2;
                     const uint32_t id = FORMAT == kNvfp4 ? 0u : 2u * (j & 1);
-                    mma<FORMAT>(tmem, operand_desc(base + j * 4096, 2048),
+                    mma<FORMAT, 1>(tmem, operand_desc(base + j * 4096, 2048),
                                 operand_desc(base + kP + j * 2 * BQ * 16, BQ * 16),
-                                mx4_idesc<FORMAT>(BQ) | id << 4 | id << 29, sfp + 4 * g,
+                                mx4_idesc<FORMAT>(128, BQ) | id << 4 | id << 29, sfp + 4 * g,
                                 sfq + 4 * g, s != first || j != 0);
                 }
-                commit(su32(&empty_bar[stage]));
+                commit<1>(su32(&empty_bar[stage]));
                 if (++stage == pl.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
-            commit(su32(&done_bar));
+            commit<1>(su32(&done_bar));
         }
     }
     __syncwarp();
@@ -298,9 +197,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     __syncthreads();
     if (warp == 1) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(pl.tmem_cols)
-                     : "memory");
+        tmem_dealloc<1>(tmem, pl.tmem_cols);
     }
     if (pl.split > 1) {
         cluster_arrive();
@@ -383,6 +280,8 @@ cudaError_t launch_format(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     if (p.M <= 16) return launch_tile<FORMAT, 16>(p, sms, stream);
     if (p.M <= 32) return launch_tile<FORMAT, 32>(p, sms, stream);
     if (p.M <= 64) return launch_tile<FORMAT, 64>(p, sms, stream);
+    const long long pair_tiles = ((p.N + 255LL) / 256) * ((p.M + 255LL) / 256);
+    if (p.M > 128 && p.N > 128 && pair_tiles * 4 >= sms) return launch_mx4_pair(p, sms, stream);
     return launch_tile<FORMAT, 128>(p, sms, stream);
 }
 

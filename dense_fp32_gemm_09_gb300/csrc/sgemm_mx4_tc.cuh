@@ -1,0 +1,142 @@
+// Tensor-core and bulk-copy wrappers of the 4-bit product's kernels (G: CTAs of one MMA).
+#pragma once
+
+#include "sgemm_async.cuh"
+#include "sgemm_internal.h"
+#include "sgemm_mx4.cuh"
+
+namespace sgemm {
+namespace mx4 {
+
+constexpr int kSlabChunks = 8;    // a slab: 256 columns of the operands
+template <int FORMAT> constexpr int kChunksPerGroup = FORMAT == kNvfp4 ? 2 : 4;
+template <int FORMAT> constexpr int kSlabGroups = kSlabChunks / kChunksPerGroup<FORMAT>;
+
+// Shared-memory operand without swizzle: 8 rows x 16 bytes contiguous, `lead` bytes from
+// one 16-byte column to the next, 128 bytes from one group of 8 rows to the next.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t lead) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(128 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;                      // descriptor version
+    return d;
+}
+// Instruction: e2m1 x e2m1, K = 64, M rows by N columns; the scales' type.
+template <int FORMAT>
+__host__ __device__ constexpr uint32_t mx4_idesc(int M, int N) {
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (FORMAT == kMxfp4 ? 1u << 23 : 0u) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+#define SGEMM_MX4_MMA(GROUP, VEC)                                                          \
+    asm volatile(                                                                          \
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                   \
+        "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC " "  \
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),      \
+        "r"(sfa), "r"(sfb), "r"(accumulate) : "memory")
+template <int FORMAT, int G>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (FORMAT == kNvfp4 && G == 1) SGEMM_MX4_MMA("1", "4X");
+    if constexpr (FORMAT == kNvfp4 && G == 2) SGEMM_MX4_MMA("2", "4X");
+    if constexpr (FORMAT == kMxfp4 && G == 1) SGEMM_MX4_MMA("1", "2X");
+    if constexpr (FORMAT == kMxfp4 && G == 2) SGEMM_MX4_MMA("2", "2X");
+}
+#undef SGEMM_MX4_MMA
+// 512 bytes of scales (128 rows, four blocks) to four tensor-memory columns of each lane
+// quarter; with G == 2 in both CTAs, each from its own shared memory.
+template <int G>
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
+    if constexpr (G == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                     : "memory");
+}
+// Arrives on `bar` (of both CTAs with G == 2) when the MMAs issued so far have completed.
+template <int G>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (G == 1)
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+            ".multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+template <int G>
+__device__ __forceinline__ void tmem_alloc(uint32_t result, int cols) {
+    if constexpr (G == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         result), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         result), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int G>
+__device__ __forceinline__ void tmem_dealloc(uint32_t tmem, int cols) {
+    if constexpr (G == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+                     : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols)
+                     : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_c(const Mx4Matmul& p, float f, float acc, long long m,
+                                        long long n) {
+    const long long at = m * p.ldc + n;
+    if (p.dtype == kF32) {
+        float* c = static_cast<float*>(p.C) + at;
+        *c = p.beta == 0.0f ? f * acc : fmaf(f, acc, p.beta * *c);
+    } else if (p.dtype == kBf16) {
+        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(p.C) + at;
+        *c = from_float<__nv_bfloat16>(p.beta == 0.0f ? f * acc
+                                                      : fmaf(f, acc, p.beta * to_float(*c)));
+    } else {
+        __half* c = static_cast<__half*>(p.C) + at;
+        *c = from_float<__half>(p.beta == 0.0f ? f * acc : fmaf(f, acc, p.beta * to_float(*c)));
+    }
+}
+
+
+}  // namespace mx4
+}  // namespace sgemm

@@ -180,7 +180,8 @@ def random_stored(sg, rows, cols, fmt, seed, exact):
 MNK = [(1, 1, 1), (1, 16, 16), (1, 300, 100), (2, 128, 64), (7, 129, 257), (16, 256, 128),
        (17, 100, 4096), (33, 384, 95), (64, 64, 1000), (100, 257, 33), (128, 128, 128),
        (129, 130, 160), (200, 333, 511), (256, 512, 768), (300, 1000, 97), (513, 255, 640),
-       (1, 5000, 2048), (5, 64, 7000), (1000, 40, 200), (700, 900, 384)]
+       (1, 5000, 2048), (5, 64, 7000), (1000, 40, 200), (700, 900, 384),
+       (1537, 1793, 640), (2049, 2047, 1111), (1300, 3000, 64), (4100, 1000, 1920)]
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
