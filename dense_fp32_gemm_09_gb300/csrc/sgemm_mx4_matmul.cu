@@ -33,7 +33,6 @@ using namespace mx4;
 using async::mbar_expect_tx;
 using async::mbar_fence_init;
 using async::mbar_init;
-using async::mbar_wait;
 using async::su32;
 
 constexpr int kMaxStages = 8;
@@ -61,7 +60,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     const Mx4Matmul& p = pl.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index();
     const int rank = static_cast<int>(blockIdx.x) % pl.split;
     // Tiles run along m in groups of kGroup, then along n, so that the CTAs at work at
     // one time share few operand rows.
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int groups = pl.chunks / kChunksPerGroup<FORMAT>;
             const uint8_t* pc = p.b_codes + (n0 >> 7) * pl.chunks * 2048;
             const uint8_t* ps = p.b_scales + (n0 >> 7) * groups * 512;
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
             bool ok = true;
             int issued = 0;
             for (int s = first; s < last; ++s) {
-                if (!mbar_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) {
+                if (!pipe_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) {
                     ok = false;
                     break;
                 }
@@ -130,33 +129,40 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
             if (!ok) {   // giving up: copies in flight land before the CTA exits
                 volatile int no_abort = 0;
                 for (int i = max(0, issued - pl.stages); i < issued; ++i)
-                    mbar_wait(su32(&full_bar[i % pl.stages]), (i / pl.stages) & 1, &no_abort,
+                    pipe_wait(su32(&full_bar[i % pl.stages]), (i / pl.stages) & 1, &no_abort,
                               nullptr);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
+            const uint64_t p_desc = operand_desc(smem0, 2048);
+            const uint64_t q_desc = operand_desc(smem0 + kP, BQ * 16);
+            const uint64_t scales_desc = operand_desc(smem0 + kP + kQ, 128);
             int stage = 0;
             uint32_t phase = 0;
             for (int s = first; s < last; ++s) {
-                if (!mbar_wait(su32(&full_bar[stage]), phase, abort_flag, pl.status)) break;
+                if (!pipe_wait(su32(&full_bar[stage]), phase, abort_flag, pl.status)) break;
                 fence_after();
                 const int nc = min(kSlabChunks, pl.chunks - s * kSlabChunks);
-                const uint32_t base = smem0 + stage * kStageBytes<FORMAT, BQ>;
+                // Descriptors count shared memory in units of 16 bytes.
+                const uint32_t at = stage * (kStageBytes<FORMAT, BQ> / 16);
                 const uint32_t sfp = tmem + BQ + stage * kStageCols<FORMAT>;
                 const uint32_t sfq = sfp + kStageCols<FORMAT> / 2;
-                for (int g = 0; g < nc / kChunksPerGroup<FORMAT>; ++g) {
-                    copy_scales<1>(sfp + 4 * g, operand_desc(base + kP + kQ + 512 * g, 128));
-                    copy_scales<1>(sfq + 4 * g, operand_desc(base + kP + kQ + kSf + 512 * g, 128));
+#pragma unroll
+                for (int g = 0; g < kSlabGroups<FORMAT>; ++g) {
+                    if (g * kChunksPerGroup<FORMAT> >= nc) break;
+                    copy_scales<1>(sfp + 4 * g, scales_desc + at + 32 * g);
+                    copy_scales<1>(sfq + 4 * g, scales_desc + at + (kSf + 512 * g) / 16);
                 }
-                for (int j = 0; j < nc / 2; ++j) {
+#pragma unroll
+                for (int j = 0; j < kSlabChunks / 2; ++j) {
+                    if (2 * j >= nc) break;
                     // nvfp4: a group of four scales per instruction; mxfp4: two of a group.
                     const int g = FORMAT == kNvfp4 ? j : j / 2;
                     const uint32_t id = FORMAT == kNvfp4 ? 0u : 2u * (j & 1);
-                    mma<FORMAT, 1>(tmem, operand_desc(base + j * 4096, 2048),
-                                operand_desc(base + kP + j * 2 * BQ * 16, BQ * 16),
-                                mx4_idesc<FORMAT>(128, BQ) | id << 4 | id << 29, sfp + 4 * g,
-                                sfq + 4 * g, s != first || j != 0);
+                    mma<FORMAT, 1>(tmem, p_desc + at + j * 256, q_desc + at + j * 2 * BQ,
+                                   mx4_idesc<FORMAT>(128, BQ) | id << 4 | id << 29, sfp + 4 * g,
+                                   sfq + 4 * g, s != first || j != 0);
                 }
                 commit<1>(su32(&empty_bar[stage]));
                 if (++stage == pl.stages) {
@@ -169,7 +175,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     }
     __syncwarp();
     const bool ok = __all_sync(0xFFFFFFFFu,
-                               mbar_wait(su32(&done_bar), 0, abort_flag, pl.status));
+                               pipe_wait(su32(&done_bar), 0, abort_flag, pl.status));
     fence_after();
     float f = p.alpha;
     if (p.a_ts) f *= __ldg(p.a_ts);

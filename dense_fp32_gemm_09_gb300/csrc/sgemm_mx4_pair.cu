@@ -27,7 +27,6 @@ using async::mbar_arrive;
 using async::mbar_expect_tx;
 using async::mbar_fence_init;
 using async::mbar_init;
-using async::mbar_wait;
 using async::su32;
 
 constexpr int kThreads = 320, kEpilogueWarps = 8;
@@ -63,8 +62,12 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
 }
+// Relaxed: what it announces was not written by this thread (bulk copies, which the
+// barrier has already seen complete) or is ordered by the tcgen05 fence before it (reads of
+// tensor memory).  A release would also wait for the thread's copies in flight: 400
+// instead of 183 us for the copies alone at 8192^3.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                  : "memory");
 }
 
@@ -77,7 +80,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     const Mx4Matmul& p = pl.p;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x) & 1;
     const int pairs = static_cast<int>(gridDim.x) >> 1;
     const int tiles = pl.tiles_n * pl.tiles_m;
@@ -106,7 +109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int groups = pl.chunks / kChunksPerGroup<FORMAT>;
             const long long row_blocks_m = (static_cast<long long>(p.M) + 127) >> 7;
             const long long row_blocks_n = (static_cast<long long>(p.N) + 127) >> 7;
@@ -125,7 +128,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint8_t* qs0 = p.a_scales + q0 * groups * 512;
                 const uint8_t* qs1 = p.a_scales + q1 * groups * 512;
                 for (int s = 0; s < pl.slabs; ++s) {
-                    if (!mbar_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) {
+                    if (!pipe_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) {
                         ok = false;
                         break;
                     }
@@ -151,50 +154,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) {   // giving up: copies in flight land before the CTA exits
                 volatile int no_abort = 0;
                 for (int i = max(0, issued - kStages); i < issued; ++i)
-                    mbar_wait(su32(&full_bar[i % kStages]), (i / kStages) & 1, &no_abort, nullptr);
+                    pipe_wait(su32(&full_bar[i % kStages]), (i / kStages) & 1, &no_abort, nullptr);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
+            const uint64_t p_desc = operand_desc(smem0, 2048);
+            const uint64_t q_desc = operand_desc(smem0 + kCodes, 2048);
+            const uint64_t scales_desc = operand_desc(smem0 + 2 * kCodes, 128);
             int stage = 0;
             uint32_t phase = 0, turn = 0;
             bool ok = true;
             for (int t = start; t < tiles && ok; t += pairs) {
                 // The previous tile's sums have left tensor memory (first: at once).
                 if (rank == 0 &&
-                    !mbar_wait(su32(&free_bar), turn ^ 1u, abort_flag, pl.status)) break;
+                    !pipe_wait(su32(&free_bar), turn ^ 1u, abort_flag, pl.status)) break;
                 turn ^= 1u;
                 fence_after();
                 for (int s = 0; s < pl.slabs; ++s) {
-                    if (!mbar_wait(su32(&full_bar[stage]), phase, abort_flag, pl.status)) {
+                    if (!pipe_wait(su32(&full_bar[stage]), phase, abort_flag, pl.status)) {
                         ok = false;
                         break;
                     }
                     if (rank == 1) {
                         arrive_cluster(in_first_cta(su32(&peer_bar[stage])));
                     } else {
-                        if (!mbar_wait(su32(&peer_bar[stage]), phase, abort_flag, pl.status)) {
+                        if (!pipe_wait(su32(&peer_bar[stage]), phase, abort_flag, pl.status)) {
                             ok = false;
                             break;
                         }
                         fence_after();
                         const int nc = min(kSlabChunks, pl.chunks - s * kSlabChunks);
-                        const uint32_t base = smem0 + stage * kStageBytes<FORMAT>;
-                        const uint32_t sf = base + 2 * kCodes;
+                        // Descriptors count shared memory in units of 16 bytes.
+                        const uint32_t at16 = stage * (kStageBytes<FORMAT> / 16);
                         const uint32_t sfp = tmem + kTile + stage * kStageCols<FORMAT>;
                         const uint32_t sfq = sfp + 4 * kSlabGroups<FORMAT>;
-                        for (int g = 0; g < nc / kChunksPerGroup<FORMAT>; ++g) {
-                            copy_scales<2>(sfp + 4 * g, operand_desc(sf + 512 * g, 128));
+#pragma unroll
+                        for (int g = 0; g < kSlabGroups<FORMAT>; ++g) {
+                            if (g * kChunksPerGroup<FORMAT> >= nc) break;
+                            copy_scales<2>(sfp + 4 * g, scales_desc + at16 + 32 * g);
                             copy_scales<2>(sfq + 8 * g,
-                                           operand_desc(sf + kSf<FORMAT> + 512 * g, 128));
+                                           scales_desc + at16 + (kSf<FORMAT> + 512 * g) / 16);
                             copy_scales<2>(sfq + 8 * g + 4,
-                                           operand_desc(sf + 2 * kSf<FORMAT> + 512 * g, 128));
+                                           scales_desc + at16 + (2 * kSf<FORMAT> + 512 * g) / 16);
                         }
-                        for (int j = 0; j < nc / 2; ++j) {
+#pragma unroll
+                        for (int j = 0; j < kSlabChunks / 2; ++j) {
+                            if (2 * j >= nc) break;
                             const int g = FORMAT == kNvfp4 ? j : j / 2;
                             const uint32_t id = FORMAT == kNvfp4 ? 0u : 2u * (j & 1);
-                            mma<FORMAT, 2>(tmem, operand_desc(base + j * 4096, 2048),
-                                           operand_desc(base + kCodes + j * 4096, 2048),
+                            mma<FORMAT, 2>(tmem, p_desc + at16 + j * 256, q_desc + at16 + j * 256,
                                            mx4_idesc<FORMAT>(256, kTile) | id << 4 | id << 29,
                                            sfp + 4 * g, sfq + 8 * g, s != 0 || j != 0);
                         }
@@ -217,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t turn = 0;
         for (int t = start; t < tiles; t += pairs) {
             const bool ok = __all_sync(
-                0xFFFFFFFFu, mbar_wait(su32(&done_bar), turn, abort_flag, pl.status));
+                0xFFFFFFFFu, pipe_wait(su32(&done_bar), turn, abort_flag, pl.status));
             if (!ok) break;
             turn ^= 1u;
             fence_after();

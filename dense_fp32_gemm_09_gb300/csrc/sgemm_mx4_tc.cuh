@@ -12,6 +12,50 @@ constexpr int kSlabChunks = 8;    // a slab: 256 columns of the operands
 template <int FORMAT> constexpr int kChunksPerGroup = FORMAT == kNvfp4 ? 2 : 4;
 template <int FORMAT> constexpr int kSlabGroups = kSlabChunks / kChunksPerGroup<FORMAT>;
 
+// As async::mbar_wait, with its time limit, but the thread sleeps in the hardware until
+// the phase completes or kSleepNs have passed: polls and reads of the global timer by the
+// waiting warps slow down the two threads that feed the tensor cores.
+constexpr unsigned kSleepNs = 1000000;
+__device__ __forceinline__ bool pipe_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSleepNs)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int* status) {
+    if (pipe_try(bar, parity)) return true;
+    const unsigned long long t0 = async::gtimer();
+    for (unsigned i = 0; i < async::kMaxSpins; ++i) {
+        if (pipe_try(bar, parity)) return true;
+        if (*abort) return false;
+        if (async::gtimer() - t0 > async::kWaitNs) break;
+    }
+    if (status) atomicExch(status, async::kStatusWaitTimeout);
+    *abort = 1;
+    return false;
+}
+
+// True in one thread of the (whole) warp.  Unlike a test of the lane number it tells the
+// compiler that one thread runs what follows, whose tensor-core instructions take their
+// operands from uniform registers: without it each is wrapped in a loop over the lanes
+// (measured per instruction: 47 against 10 cycles for a copy of scales).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ int warp_index() {
+    return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+}
+
 // Shared-memory operand without swizzle: 8 rows x 16 bytes contiguous, `lead` bytes from
 // one 16-byte column to the next, 128 bytes from one group of 8 rows to the next.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t lead) {
