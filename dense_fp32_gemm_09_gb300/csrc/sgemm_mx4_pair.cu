@@ -29,7 +29,7 @@ using async::mbar_fence_init;
 using async::mbar_init;
 using async::su32;
 
-constexpr int kThreads = 320, kEpilogueWarps = 8;
+constexpr int kThreads = 352, kEpilogueWarps = 8;
 constexpr int kTile = 256;
 constexpr int kStages = 5;
 constexpr int kGroup = 8;        // tiles of m a raster group
@@ -40,13 +40,31 @@ template <int FORMAT> constexpr int kStageBytes = 2 * kCodes + 3 * kSf<FORMAT>;
 template <int FORMAT> constexpr int kStageCols = 12 * kSlabGroups<FORMAT>;
 constexpr int kTmemCols = 512;
 static_assert(kTile + kStages * kStageCols<kNvfp4> <= kTmemCols, "tensor memory");
-static_assert(kStages * kStageBytes<kNvfp4> <= 220 * 1024, "shared memory");
+constexpr int kStageC = 2 * 32 * 128 * 4;    // staging of C: 32 rows of each half, fp32
+static_assert(kStages * kStageBytes<kNvfp4> + kStageC <= 226 * 1024, "shared memory");
 
 struct PairPlan {
     Mx4Matmul p;
     int chunks, slabs, tiles_n, tiles_m;
+    int c_vec;             // 1: rows of C are 16-byte aligned
     int* status;
 };
+
+// Position in the ring of stages.
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+__device__ __forceinline__ long long slabs_of_pair(const PairPlan& pl, int start, int pairs,
+                                                   int tiles) {
+    return start < tiles ? ((tiles - 1 - start) / pairs + 1) * static_cast<long long>(pl.slabs) : 0;
+}
 
 struct Tile {
     long long n0, m0;
@@ -71,11 +89,61 @@ __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
                  : "memory");
 }
 
+__device__ __forceinline__ bool all_of_half(int barrier, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"(barrier), "r"(static_cast<uint32_t>(ok)) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void sync_half(int barrier) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(barrier) : "memory");
+}
+
+// 32 rows of C by 128 columns, a lane per column, of one half's four warps: through shared
+// memory, so that the stores are 16 bytes a lane and whole 128-byte lines of C.
+template <typename T>
+__device__ __forceinline__ void store_part(const Mx4Matmul& p, bool c_vec, float f, const float (&v)[32],
+                                           long long m0, long long n0, uint8_t* stage, int half,
+                                           int quarter) {
+    constexpr int kVec = 16 / sizeof(T), kPerRow = 128 / kVec, kRows = 128 / kPerRow;
+    const int lane = threadIdx.x & 31, me = 32 * quarter + lane;
+    T* const s = reinterpret_cast<T*>(stage);
+    T* const C = static_cast<T*>(p.C);
+    const bool scaled = p.beta != 0.0f && n0 + me < p.N;
+    auto value = [&](float acc, int i) {
+        if (scaled && m0 + i < p.M)
+            return fmaf(f, acc, p.beta * to_float(C[(m0 + i) * p.ldc + n0 + me]));
+        return f * acc;
+    };
+    sync_half(1 + half);     // the previous part has been read
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i * 128 + me] = from_float<T>(value(v[i], i));
+    sync_half(1 + half);
+    const int col = me % kPerRow * kVec;
+    const bool vec = c_vec && n0 + col + kVec <= p.N;
+#pragma unroll
+    for (int i = 0; i < 32; i += kRows) {
+        const int row = i + me / kPerRow;
+        if (m0 + row >= p.M) continue;
+        T* c = C + (m0 + row) * p.ldc + n0 + col;
+        const T* from = s + row * 128 + col;
+        if (vec) {
+            *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(from);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                if (n0 + col + k < p.N) c[k] = from[k];
+        }
+    }
+}
+
 template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx4_pair_kernel(const PairPlan pl) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full_bar[kStages], peer_bar[kStages], empty_bar[kStages];
+    __shared__ __align__(8) uint64_t full_bar[kStages], ready_bar[kStages], empty_bar[kStages];
     __shared__ __align__(8) uint64_t done_bar, free_bar;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
@@ -90,7 +158,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(su32(&full_bar[s]), 1);
-            mbar_init(su32(&peer_bar[s]), 1);
+            mbar_init(su32(&ready_bar[s]), 2);
             mbar_init(su32(&empty_bar[s]), 1);
         }
         mbar_init(su32(&done_bar), 1);
@@ -113,8 +181,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int groups = pl.chunks / kChunksPerGroup<FORMAT>;
             const long long row_blocks_m = (static_cast<long long>(p.M) + 127) >> 7;
             const long long row_blocks_n = (static_cast<long long>(p.N) + 127) >> 7;
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
+            Ring ring;
+            int issued = 0;
             bool ok = true;
             for (int t = start; t < tiles && ok; t += pairs) {
                 const Tile at = tile_at(pl, t);
@@ -128,15 +196,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint8_t* qs0 = p.a_scales + q0 * groups * 512;
                 const uint8_t* qs1 = p.a_scales + q1 * groups * 512;
                 for (int s = 0; s < pl.slabs; ++s) {
-                    if (!pipe_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) {
+                    if (!pipe_wait(su32(&empty_bar[ring.stage]), ring.phase ^ 1u, abort_flag, pl.status)) {
                         ok = false;
                         break;
                     }
                     const int c0 = s * kSlabChunks, nc = min(kSlabChunks, pl.chunks - c0);
                     const int ng = nc / kChunksPerGroup<FORMAT>;
                     const long long g0 = c0 / kChunksPerGroup<FORMAT>;
-                    const uint32_t fb = su32(&full_bar[stage]);
-                    const uint32_t base = smem0 + stage * kStageBytes<FORMAT>;
+                    const uint32_t fb = su32(&full_bar[ring.stage]);
+                    const uint32_t base = smem0 + ring.stage * kStageBytes<FORMAT>;
                     mbar_expect_tx(fb, 2 * nc * 2048 + 3 * ng * 512);
                     bulk_load(base, pc + c0 * 2048LL, nc * 2048, fb);
                     bulk_load(base + kCodes, qc + c0 * 2048LL, nc * 2048, fb);
@@ -145,10 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     bulk_load(sf + kSf<FORMAT>, qs0 + g0 * 512, ng * 512, fb);
                     bulk_load(sf + 2 * kSf<FORMAT>, qs1 + g0 * 512, ng * 512, fb);
                     ++issued;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    ring.next();
                 }
             }
             if (!ok) {   // giving up: copies in flight land before the CTA exits
@@ -158,63 +223,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (elect_one()) {
+        if (rank == 0 && elect_one()) {
             const uint64_t p_desc = operand_desc(smem0, 2048);
             const uint64_t q_desc = operand_desc(smem0 + kCodes, 2048);
             const uint64_t scales_desc = operand_desc(smem0 + 2 * kCodes, 128);
-            int stage = 0;
-            uint32_t phase = 0, turn = 0;
-            bool ok = true;
+            // A stage has arrived in both CTAs: its scales to tensor memory.
+            auto take = [&](const Ring& r, bool ready) {
+                if (!ready &&
+                    !pipe_wait(su32(&ready_bar[r.stage]), r.phase, abort_flag, pl.status))
+                    return false;
+                fence_after();
+                const uint64_t at = scales_desc + r.stage * (kStageBytes<FORMAT> / 16);
+                const uint32_t sfp = tmem + kTile + r.stage * kStageCols<FORMAT>;
+                const uint32_t sfq = sfp + 4 * kSlabGroups<FORMAT>;
+#pragma unroll
+                for (int g = 0; g < kSlabGroups<FORMAT>; ++g) {
+                    copy_scales<2>(sfp + 4 * g, at + 32 * g);
+                    copy_scales<2>(sfq + 8 * g, at + (kSf<FORMAT> + 512 * g) / 16);
+                    copy_scales<2>(sfq + 8 * g + 4, at + (2 * kSf<FORMAT> + 512 * g) / 16);
+                }
+                return true;
+            };
+            auto multiply = [&](const Ring& r, int j, bool add) {
+                const uint32_t at = r.stage * (kStageBytes<FORMAT> / 16);
+                const uint32_t sfp = tmem + kTile + r.stage * kStageCols<FORMAT>;
+                const uint32_t sfq = sfp + 4 * kSlabGroups<FORMAT>;
+                // nvfp4: a group of four scales per instruction; mxfp4: two of a group.
+                const int g = FORMAT == kNvfp4 ? j : j / 2;
+                const uint32_t id = FORMAT == kNvfp4 ? 0u : 2u * (j & 1);
+                mma<FORMAT, 2>(tmem, p_desc + at + j * 256, q_desc + at + j * 256,
+                               mx4_idesc<FORMAT>(256, kTile) | id << 4 | id << 29,
+                               sfp + 4 * g, sfq + 8 * g, add);
+            };
+            Ring ring;
+            uint32_t turn = 0;
+            bool ready = false, ok = true;
             for (int t = start; t < tiles && ok; t += pairs) {
                 // The previous tile's sums have left tensor memory (first: at once).
-                if (rank == 0 &&
-                    !pipe_wait(su32(&free_bar), turn ^ 1u, abort_flag, pl.status)) break;
+                if (!pipe_wait(su32(&free_bar), turn ^ 1u, abort_flag, pl.status)) break;
                 turn ^= 1u;
-                fence_after();
                 for (int s = 0; s < pl.slabs; ++s) {
-                    if (!pipe_wait(su32(&full_bar[stage]), phase, abort_flag, pl.status)) {
+                    if (!take(ring, ready)) {
                         ok = false;
                         break;
                     }
-                    if (rank == 1) {
-                        arrive_cluster(in_first_cta(su32(&peer_bar[stage])));
-                    } else {
-                        if (!pipe_wait(su32(&peer_bar[stage]), phase, abort_flag, pl.status)) {
-                            ok = false;
-                            break;
-                        }
-                        fence_after();
-                        const int nc = min(kSlabChunks, pl.chunks - s * kSlabChunks);
-                        // Descriptors count shared memory in units of 16 bytes.
-                        const uint32_t at16 = stage * (kStageBytes<FORMAT> / 16);
-                        const uint32_t sfp = tmem + kTile + stage * kStageCols<FORMAT>;
-                        const uint32_t sfq = sfp + 4 * kSlabGroups<FORMAT>;
-#pragma unroll
-                        for (int g = 0; g < kSlabGroups<FORMAT>; ++g) {
-                            if (g * kChunksPerGroup<FORMAT> >= nc) break;
-                            copy_scales<2>(sfp + 4 * g, scales_desc + at16 + 32 * g);
-                            copy_scales<2>(sfq + 8 * g,
-                                           scales_desc + at16 + (kSf<FORMAT> + 512 * g) / 16);
-                            copy_scales<2>(sfq + 8 * g + 4,
-                                           scales_desc + at16 + (2 * kSf<FORMAT> + 512 * g) / 16);
-                        }
-#pragma unroll
-                        for (int j = 0; j < kSlabChunks / 2; ++j) {
-                            if (2 * j >= nc) break;
-                            const int g = FORMAT == kNvfp4 ? j : j / 2;
-                            const uint32_t id = FORMAT == kNvfp4 ? 0u : 2u * (j & 1);
-                            mma<FORMAT, 2>(tmem, p_desc + at16 + j * 256, q_desc + at16 + j * 256,
-                                           mx4_idesc<FORMAT>(256, kTile) | id << 4 | id << 29,
-                                           sfp + 4 * g, sfq + 8 * g, s != 0 || j != 0);
-                        }
-                        commit<2>(su32(&empty_bar[stage]));
+                    // The answer about the next stage arrives under this one's MMAs: the
+                    // thread's own time, 512 cycles a slab, is what it has least of.
+                    Ring ahead = ring;
+                    ahead.next();
+                    ready = pipe_peek(su32(&ready_bar[ahead.stage]), ahead.phase);
+                    multiply(ring, 0, s != 0);
+                    multiply(ring, 1, true);
+                    if (kSlabChunks * (s + 1) <= pl.chunks) {
+                        multiply(ring, 2, true);
+                        multiply(ring, 3, true);
                     }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    commit<2>(su32(&empty_bar[ring.stage]));
+                    ring = ahead;
                 }
-                if (rank == 0) commit<2>(su32(&done_bar));
+                commit<2>(su32(&done_bar));
+            }
+        }
+    } else if (warp == 10) {
+        if (elect_one()) {
+            Ring ring;
+            const long long total = slabs_of_pair(pl, start, pairs, tiles);
+            for (long long i = 0; i < total; ++i, ring.next()) {
+                if (!pipe_wait(su32(&full_bar[ring.stage]), ring.phase, abort_flag, pl.status))
+                    break;
+                arrive_cluster(in_first_cta(su32(&ready_bar[ring.stage])));
             }
         }
     } else {
@@ -223,30 +300,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float f = p.alpha;
         if (p.a_ts) f *= __ldg(p.a_ts);
         if (p.b_ts) f *= __ldg(p.b_ts);
+        uint8_t* const stage = smem + kStages * kStageBytes<FORMAT> + half * (kStageC / 2);
         uint32_t turn = 0;
         for (int t = start; t < tiles; t += pairs) {
-            const bool ok = __all_sync(
-                0xFFFFFFFFu, pipe_wait(su32(&done_bar), turn, abort_flag, pl.status));
+            // All four warps of this half go on, or none.
+            const bool ok = all_of_half(
+                1 + half, pipe_wait(su32(&done_bar), turn, abort_flag, pl.status));
             if (!ok) break;
             turn ^= 1u;
             fence_after();
             const Tile at = tile_at(pl, t);
-            float v[kCols / 16][16];
-#pragma unroll
-            for (int j = 0; j < kCols / 16; ++j)
-                tmem_ld16(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + half * kCols + 16 * j,
-                          v[j]);
+            float v[2][64];
+            const uint32_t mine =
+                tmem + (static_cast<uint32_t>(32 * quarter) << 16) + half * kCols;
+            tmem_ld64(mine, v[0]);
+            tmem_ld64(mine + 64, v[1]);
             fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(in_first_cta(su32(&free_bar)));
-            const long long n = at.n0 + 128 * rank + 32 * quarter + lane;
-            const long long m0 = at.m0 + half * kCols;
-            if (n < p.N) {
+            const long long n0 = at.n0 + 128 * rank, m0 = at.m0 + half * kCols;
 #pragma unroll
-                for (int j = 0; j < kCols / 16; ++j)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (m0 + 16 * j + i < p.M) store_c(p, f, v[j][i], m0 + 16 * j + i, n);
+            for (int j = 0; j < 4; ++j) {
+                if (m0 + 32 * j >= p.M || n0 >= p.N) break;
+                const float(&part)[32] = *reinterpret_cast<const float(*)[32]>(&v[j / 2][j % 2 * 32]);
+                if (p.dtype == kF32)
+                    store_part<float>(p, pl.c_vec, f, part, m0 + 32 * j, n0, stage, half, quarter);
+                else if (p.dtype == kBf16)
+                    store_part<__nv_bfloat16>(p, pl.c_vec, f, part, m0 + 32 * j, n0, stage, half,
+                                              quarter);
+                else
+                    store_part<__half>(p, pl.c_vec, f, part, m0 + 32 * j, n0, stage, half, quarter);
             }
         }
     }
@@ -273,7 +356,9 @@ cudaError_t launch_pair(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     pl.tiles_n = static_cast<int>(tn);
     pl.tiles_m = static_cast<int>(tm);
     pl.status = status_word_ptr();
-    constexpr int smem = kStages * kStageBytes<FORMAT>;
+    constexpr int smem = kStages * kStageBytes<FORMAT> + kStageC;
+    const int es = p.dtype == kF32 ? 4 : 2;
+    pl.c_vec = reinterpret_cast<uintptr_t>(p.C) % 16 == 0 && p.ldc * es % 16 == 0;
     auto kernel = mx4_pair_kernel<FORMAT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
