@@ -32,7 +32,7 @@ using async::su32;
 constexpr int kThreads = 352, kEpilogueWarps = 8;
 constexpr int kTile = 256;
 constexpr int kStages = 5;
-constexpr int kGroup = 8;        // tiles of m a raster group
+constexpr int kGroup = 16;       // tiles of m a raster group
 constexpr int kCodes = kSlabChunks * 2048;
 template <int FORMAT> constexpr int kSf = kSlabGroups<FORMAT> * 512;
 template <int FORMAT> constexpr int kStageBytes = 2 * kCodes + 3 * kSf<FORMAT>;
@@ -101,40 +101,38 @@ __device__ __forceinline__ void sync_half(int barrier) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(barrier) : "memory");
 }
 
-// 32 rows of C by 128 columns, a lane per column, of one half's four warps: through shared
-// memory, so that the stores are 16 bytes a lane and whole 128-byte lines of C.
+// 32 rows of C by 128 columns from the sums staged in shared memory (fp32, row by row) by
+// one half's four warps: 16 bytes a thread, whole 128-byte lines of C.
 template <typename T>
-__device__ __forceinline__ void store_part(const Mx4Matmul& p, bool c_vec, float f, const float (&v)[32],
-                                           long long m0, long long n0, uint8_t* stage, int half,
-                                           int quarter) {
+__device__ __forceinline__ void store_rows(const Mx4Matmul& p, bool c_vec, const float* staged,
+                                           long long m0, long long n0, int me) {
     constexpr int kVec = 16 / sizeof(T), kPerRow = 128 / kVec, kRows = 128 / kPerRow;
-    const int lane = threadIdx.x & 31, me = 32 * quarter + lane;
-    T* const s = reinterpret_cast<T*>(stage);
-    T* const C = static_cast<T*>(p.C);
-    const bool scaled = p.beta != 0.0f && n0 + me < p.N;
-    auto value = [&](float acc, int i) {
-        if (scaled && m0 + i < p.M)
-            return fmaf(f, acc, p.beta * to_float(C[(m0 + i) * p.ldc + n0 + me]));
-        return f * acc;
-    };
-    sync_half(1 + half);     // the previous part has been read
-#pragma unroll
-    for (int i = 0; i < 32; ++i) s[i * 128 + me] = from_float<T>(value(v[i], i));
-    sync_half(1 + half);
     const int col = me % kPerRow * kVec;
     const bool vec = c_vec && n0 + col + kVec <= p.N;
+#pragma unroll 2
+    for (int row = me / kPerRow; row < 32 && m0 + row < p.M; row += kRows) {
+        T* c = static_cast<T*>(p.C) + (m0 + row) * p.ldc + n0 + col;
+        float v[kVec];
 #pragma unroll
-    for (int i = 0; i < 32; i += kRows) {
-        const int row = i + me / kPerRow;
-        if (m0 + row >= p.M) continue;
-        T* c = C + (m0 + row) * p.ldc + n0 + col;
-        const T* from = s + row * 128 + col;
+        for (int k = 0; k < kVec; k += 4)
+            *reinterpret_cast<float4*>(v + k) =
+                *reinterpret_cast<const float4*>(staged + row * 128 + col + k);
         if (vec) {
-            *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(from);
+            alignas(16) T out[kVec];
+            if (p.beta != 0.0f) {
+                *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(c);
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) v[k] = fmaf(p.beta, to_float(out[k]), v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) out[k] = from_float<T>(v[k]);
+            *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(out);
         } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                if (n0 + col + k < p.N) c[k] = from[k];
+            for (int k = 0; k < kVec; ++k) {
+                if (n0 + col + k >= p.N) break;
+                c[k] = from_float<T>(p.beta == 0.0f ? v[k] : fmaf(p.beta, to_float(c[k]), v[k]));
+            }
         }
     }
 }
@@ -300,7 +298,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float f = p.alpha;
         if (p.a_ts) f *= __ldg(p.a_ts);
         if (p.b_ts) f *= __ldg(p.b_ts);
-        uint8_t* const stage = smem + kStages * kStageBytes<FORMAT> + half * (kStageC / 2);
+        float* const staged = reinterpret_cast<float*>(smem + kStages * kStageBytes<FORMAT> +
+                                                       half * (kStageC / 2));
         uint32_t turn = 0;
         for (int t = start; t < tiles; t += pairs) {
             // All four warps of this half go on, or none.
@@ -319,17 +318,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_cluster(in_first_cta(su32(&free_bar)));
             const long long n0 = at.n0 + 128 * rank, m0 = at.m0 + half * kCols;
+            const int me = 32 * quarter + lane;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (m0 + 32 * j >= p.M || n0 >= p.N) break;
-                const float(&part)[32] = *reinterpret_cast<const float(*)[32]>(&v[j / 2][j % 2 * 32]);
-                if (p.dtype == kF32)
-                    store_part<float>(p, pl.c_vec, f, part, m0 + 32 * j, n0, stage, half, quarter);
+                sync_half(1 + half);     // the previous part has been read
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    staged[i * 128 + me] = f * v[j / 2][j % 2 * 32 + i];
+                sync_half(1 + half);
+                const long long m = m0 + 32 * j;
+                if (p.dtype == kF32) store_rows<float>(p, pl.c_vec, staged, m, n0, me);
                 else if (p.dtype == kBf16)
-                    store_part<__nv_bfloat16>(p, pl.c_vec, f, part, m0 + 32 * j, n0, stage, half,
-                                              quarter);
-                else
-                    store_part<__half>(p, pl.c_vec, f, part, m0 + 32 * j, n0, stage, half, quarter);
+                    store_rows<__nv_bfloat16>(p, pl.c_vec, staged, m, n0, me);
+                else store_rows<__half>(p, pl.c_vec, staged, m, n0, me);
             }
         }
     }
