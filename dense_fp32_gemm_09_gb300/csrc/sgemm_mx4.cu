@@ -1,7 +1,17 @@
 // 4-bit quantisation and its inverse (sgemm_mx4_quantize, sgemm_mx4_dequantize).
+//
+// Both are passes over memory: 2 bytes a bf16 number one way and 0.56 the other.  A warp
+// takes 32 rows of 128 columns, as the rows 8 i + 0..7 of each of the four quarters of a
+// block of 128 rows, because those share the 16-byte pieces of the scale layout.  Four
+// lanes take a row's 32 columns, eight each: a load is 16 bytes a lane (32 for fp32) from
+// eight rows, a store of codes 128 contiguous bytes, and the scales leave as whole 16-byte
+// pieces; a block's largest magnitude costs one shuffle (nvfp4) or two.
+// The transpose needs no exchange: a thread takes one column of X down 64 rows, so that
+// a warp's loads run along X's rows and its stores are 512 contiguous bytes.
 #include <cuda_runtime.h>
 
 #include "sgemm_internal.h"
+#include "sgemm_launch.cuh"
 #include "sgemm_mx4.cuh"
 
 namespace sgemm {
@@ -9,139 +19,231 @@ namespace {
 
 using namespace mx4;
 
-// Codes of N numbers of one block whose scale byte is `byte`: each number over its
-// scale, rounded to the nearest e2m1 value.  A block with scale 0 has codes 0.
-template <int FORMAT, int N>
-__device__ __forceinline__ void block_codes(const float* x, uint32_t byte, float ts,
-                                            uint32_t* codes) {
-    const float d = FORMAT == kNvfp4 ? e4m3_decode(byte) * ts : e8m0_decode(byte);
-#pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = (FORMAT == kNvfp4 && d == 0.0f) ? 0.0f : __fdiv_rn(x[8 * i + j], d);
-        codes[i] = encode8(v);
-    }
+constexpr int kWarps = 4;
+
+// A warp's task: rows r0 + 32 j + lane / 4, j < 4, and columns [128 g, 128 g + 128).
+struct Task {
+    long long row;     // of j = 0
+    int quad, q;       // 128 columns; the lane's eight columns of each 32
+};
+__device__ __forceinline__ bool task_of(int rows, int quads, Task* t) {
+    const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const long long band = id / quads;           // 4 a block of 128 rows
+    const int lane = threadIdx.x & 31;
+    t->quad = static_cast<int>(id - band * quads);
+    t->q = lane & 3;
+    const long long r0 = (band >> 2) * 128 + (band & 3) * 8;
+    t->row = r0 + (lane >> 2);
+    return r0 < rows;
 }
 
-// One thread quantises 32 columns of one row; threads run along the rows, so that the
-// stores (and, for a transposed matrix, the loads) of a warp are contiguous.
-template <typename T, int FORMAT, bool TRANS>
-__global__ void __launch_bounds__(128) quantize_kernel(
+template <typename T, int FORMAT>
+__global__ void __launch_bounds__(32 * kWarps) quantize_kernel(
+    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks, int vec,
+    const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+    Task t;
+    const bool any = task_of(rows, chunks / 4, &t);
+    wait_previous();
+    if (!any) return;
+    const float ts = FORMAT == kNvfp4 && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+    uint32_t word[4][2] = {};      // four scale bytes of [quarter][half of the columns]
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const long long row = t.row + 32 * j;
+        if (t.row - (threadIdx.x & 31) / 4 + 32 * j >= rows) break;     // the whole warp
+        const bool live = row < rows;
+        float x[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int k = t.quad * 128 + c * 32 + t.q * 8;
+            load8(X + (live ? row : 0) * ldx + k, vec, live ? cols - k : 0, x[c]);
+        }
+        uint32_t mine = 0;          // this lane's block of each 32 columns
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t amax = magnitude8(x[c]);
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            const uint32_t byte = block_scale<FORMAT>(amax, 6.0f * ts);
+            mine |= byte << (8 * c);
+            const uint32_t packed = Divider<FORMAT>(byte, ts).codes(x[c]);
+            if (live)
+                *reinterpret_cast<uint32_t*>(codes + code_offset(row, 4 * t.quad + c, chunks) +
+                                             4 * t.q) = packed;
+        }
+        if (FORMAT == kNvfp4) {
+            // Lanes 0, 1 of four hold the first block of each 32 columns, 2, 3 the second.
+            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, 2);
+            const uint32_t a = t.q < 2 ? mine : other, b = t.q < 2 ? other : mine;
+            word[j][0] = __byte_perm(a, b, 0x5140);
+            word[j][1] = __byte_perm(a, b, 0x7362);
+        } else {
+            word[j][0] = mine;
+        }
+    }
+    const int groups = groups_of(cols, FORMAT);
+    constexpr int kGroups = FORMAT == kNvfp4 ? 2 : 1;
+    if (t.q < kGroups) {
+        uint8_t* at = scales + scale_offset(t.row, 4 * (t.quad * kGroups + t.q), groups);
+        *reinterpret_cast<uint4*>(at) =
+            t.q == 0 ? make_uint4(word[0][0], word[1][0], word[2][0], word[3][0])
+                     : make_uint4(word[0][1], word[1][1], word[2][1], word[3][1]);
+    }
+    launch_next();
+}
+
+template <typename T, int FORMAT>
+__global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
+    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+    const float* __restrict__ tensor_scale, int rows, int cols, int chunks, int vec,
+    T* __restrict__ Y, long long ldy) {
+    Task t;
+    const bool any = task_of(rows, chunks / 4, &t);
+    wait_previous();
+    if (!any) return;
+    const float ts = FORMAT == kNvfp4 && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+    const int groups = groups_of(cols, FORMAT);
+    constexpr int kGroups = FORMAT == kNvfp4 ? 2 : 1;
+    uint4 words[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+        words[g] = __ldg(reinterpret_cast<const uint4*>(
+            scales + scale_offset(t.row, 4 * (t.quad * kGroups + g), groups)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const long long row = t.row + 32 * j;
+        if (row >= rows) break;
+        uint32_t packed[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            packed[c] = __ldg(reinterpret_cast<const uint32_t*>(
+                codes + code_offset(row, 4 * t.quad + c, chunks) + 4 * t.q));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 w4 = words[FORMAT == kNvfp4 ? c / 2 : 0];
+            const uint32_t w = j == 0 ? w4.x : j == 1 ? w4.y : j == 2 ? w4.z : w4.w;
+            const int byte = FORMAT == kNvfp4 ? 2 * (c & 1) + (t.q >> 1) : c;
+            const float s = scale_decode<FORMAT>(w >> (8 * byte) & 0xFFu);
+            float v[8];
+            decode8(packed[c], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * s * ts;
+            const int k = t.quad * 128 + c * 32 + t.q * 8;
+            store8(Y + row * ldy + k, vec, cols - k, v);
+        }
+    }
+    launch_next();
+}
+
+// X stored cols x rows: a thread takes column `row` of X, 64 of its rows.
+template <typename T, int FORMAT>
+__global__ void __launch_bounds__(128) quantize_transposed_kernel(
     const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
     const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ scales) {
-    const long long row = blockIdx.x * 128LL + threadIdx.x;
+    const int pairs = chunks / 2;
+    const long long rb = blockIdx.x / pairs;
+    const int pair = static_cast<int>(blockIdx.x - rb * pairs);
+    const long long row = rb * 128 + threadIdx.x;
+    wait_previous();
     if (row >= rows) return;
-    const int groups = groups_of(cols, FORMAT);
     const float ts = FORMAT == kNvfp4 && tensor_scale ? __ldg(tensor_scale) : 1.0f;
-    for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
-        float x[32];
-        uint32_t packed[4];
+    uint32_t word = 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const int k = 32 * chunk + j;
-            x[j] = k >= cols ? 0.0f
-                             : to_float(TRANS ? X[k * ldx + row] : X[row * ldx + k]);
-        }
-        constexpr int B = block_of(FORMAT);
+    for (int c = 0; c < 2; ++c) {
+        float x[4][8];
+        const int k0 = pair * 64 + c * 32;
 #pragma unroll
-        for (int b = 0; b < 32 / B; ++b) {
-            uint32_t amax = 0;
+        for (int i = 0; i < 32; ++i)
+            x[i / 8][i % 8] = k0 + i < cols ? to_float(__ldg(X + (k0 + i) * ldx + row)) : 0.0f;
+        uint32_t m[4], packed[4];
 #pragma unroll
-            for (int j = 0; j < B; ++j)
-                amax = max(amax, __float_as_uint(x[b * B + j]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 4; ++i) m[i] = magnitude8(x[i]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            uint32_t amax = max(m[2 * b], m[2 * b + 1]);
+            if (FORMAT == kMxfp4) amax = max(max(m[0], m[1]), max(m[2], m[3]));
             const uint32_t byte = block_scale<FORMAT>(amax, 6.0f * ts);
-            block_codes<FORMAT, B>(x + b * B, byte, ts, packed + b * B / 8);
-            scales[scale_offset(row, chunk * (32 / B) + b, groups)] = static_cast<uint8_t>(byte);
+            const Divider<FORMAT> by(byte, ts);
+            packed[2 * b] = by.codes(x[2 * b]);
+            packed[2 * b + 1] = by.codes(x[2 * b + 1]);
+            if (FORMAT == kNvfp4) word |= byte << (8 * (2 * c + b));
+            else if (b == 0) word |= byte << (8 * c);
         }
-        *reinterpret_cast<uint4*>(codes + code_offset(row, chunk, chunks)) =
+        *reinterpret_cast<uint4*>(codes + code_offset(row, 2 * pair + c, chunks)) =
             make_uint4(packed[0], packed[1], packed[2], packed[3]);
     }
-    // mxfp4: a group of four scales spans 128 columns, as the padding does.
-}
-
-// value = code * scale (* tensor scale), rounded once to the output's type.
-template <typename T, int FORMAT>
-__global__ void __launch_bounds__(128) dequantize_kernel(
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-    const float* __restrict__ tensor_scale, int rows, int cols, int chunks, T* __restrict__ Y,
-    long long ldy) {
-    const long long row = blockIdx.x * 128LL + threadIdx.x;
-    if (row >= rows) return;
     const int groups = groups_of(cols, FORMAT);
-    const float ts = FORMAT == kNvfp4 && tensor_scale ? __ldg(tensor_scale) : 1.0f;
-    for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
-        const uint4 p = *reinterpret_cast<const uint4*>(codes + code_offset(row, chunk, chunks));
-        const uint32_t packed[4] = {p.x, p.y, p.z, p.w};
-        constexpr int B = block_of(FORMAT);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v[8];
-            decode8(packed[i], v);
-            const float s = scale_decode<FORMAT>(
-                scales[scale_offset(row, (32 * chunk + 8 * i) / B, groups)]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = 32 * chunk + 8 * i + j;
-                if (k < cols) Y[row * ldy + k] = from_float<T>(v[j] * s * ts);
-            }
-        }
-    }
-}
-
-template <typename T, int FORMAT>
-void quantize_launch(const Mx4Quantize& q, int chunks, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(row_blocks(q.rows)),
-                    static_cast<unsigned>(chunks < 65535 ? chunks : 65535));
-    const T* X = static_cast<const T*>(q.X);
-    if (q.trans)
-        quantize_kernel<T, FORMAT, true><<<grid, 128, 0, stream>>>(
-            X, q.ldx, q.rows, q.cols, chunks, q.tensor_scale, q.codes, q.scales);
+    if (FORMAT == kNvfp4)
+        *reinterpret_cast<uint32_t*>(scales + scale_offset(row, 4 * pair, groups)) = word;
     else
-        quantize_kernel<T, FORMAT, false><<<grid, 128, 0, stream>>>(
-            X, q.ldx, q.rows, q.cols, chunks, q.tensor_scale, q.codes, q.scales);
+        *reinterpret_cast<uint16_t*>(scales + scale_offset(row, 2 * pair, groups)) =
+            static_cast<uint16_t>(word);
+    launch_next();
+}
+
+// One warp per band of 32 rows (as above) and 128 columns.
+unsigned task_blocks(int rows, int chunks) {
+    const long long full = rows / 128, rest = rows % 128;
+    const long long bands = 4 * full + (rest >= 32 ? 4 : (rest + 7) / 8);
+    return static_cast<unsigned>((bands * (chunks / 4) + kWarps - 1) / kWarps);
+}
+bool fits_grid(long long blocks) { return blocks <= 0x7FFFFFFF; }
+
+template <typename T, int FORMAT>
+cudaError_t quantize_launch(const Mx4Quantize& q, cudaStream_t stream) {
+    const int chunks = chunks_of(q.cols);
+    const T* X = static_cast<const T*>(q.X);
+    if (q.trans) {
+        const long long blocks = row_blocks(q.rows) * (chunks / 2);
+        if (!fits_grid(blocks)) return cudaErrorInvalidConfiguration;
+        return launch_dependent(quantize_transposed_kernel<T, FORMAT>,
+                                dim3(static_cast<unsigned>(blocks)), 128, 0, stream, X, q.ldx,
+                                q.rows, q.cols, chunks, q.tensor_scale, q.codes, q.scales);
+    }
+    if (!fits_grid(row_blocks(q.rows) * (chunks / 4))) return cudaErrorInvalidConfiguration;
+    const int vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && q.ldx * sizeof(T) % 16 == 0;
+    return launch_dependent(quantize_kernel<T, FORMAT>, dim3(task_blocks(q.rows, chunks)),
+                            32 * kWarps, 0, stream, X, q.ldx, q.rows, q.cols, chunks, vec,
+                            q.tensor_scale, q.codes, q.scales);
 }
 
 template <typename T, int FORMAT>
-void dequantize_launch(const Mx4Dequantize& q, int chunks, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(row_blocks(q.rows)),
-                    static_cast<unsigned>(chunks < 65535 ? chunks : 65535));
-    dequantize_kernel<T, FORMAT><<<grid, 128, 0, stream>>>(
-        q.codes, q.scales, q.tensor_scale, q.rows, q.cols, chunks, static_cast<T*>(q.Y), q.ldy);
+cudaError_t dequantize_launch(const Mx4Dequantize& q, cudaStream_t stream) {
+    const int chunks = chunks_of(q.cols);
+    if (!fits_grid(row_blocks(q.rows) * (chunks / 4))) return cudaErrorInvalidConfiguration;
+    const int vec = reinterpret_cast<uintptr_t>(q.Y) % 16 == 0 && q.ldy * sizeof(T) % 16 == 0;
+    return launch_dependent(dequantize_kernel<T, FORMAT>, dim3(task_blocks(q.rows, chunks)),
+                            32 * kWarps, 0, stream, q.codes, q.scales, q.tensor_scale, q.rows,
+                            q.cols, chunks, vec, static_cast<T*>(q.Y), q.ldy);
+}
+
+template <typename Q, typename F, typename H, typename B>
+cudaError_t by_type(const Q& q, F f32, B bf16, H f16) {
+    return q.dtype == kF32 ? f32() : q.dtype == kBf16 ? bf16() : f16();
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream) {
-    const int chunks = chunks_of(q.cols);
-    const bool nv = q.format == kNvfp4;
-    if (q.dtype == kF32)
-        nv ? quantize_launch<float, kNvfp4>(q, chunks, stream)
-           : quantize_launch<float, kMxfp4>(q, chunks, stream);
-    else if (q.dtype == kBf16)
-        nv ? quantize_launch<__nv_bfloat16, kNvfp4>(q, chunks, stream)
-           : quantize_launch<__nv_bfloat16, kMxfp4>(q, chunks, stream);
-    else
-        nv ? quantize_launch<__half, kNvfp4>(q, chunks, stream)
-           : quantize_launch<__half, kMxfp4>(q, chunks, stream);
-    return cudaGetLastError();
+    if (q.format == kNvfp4)
+        return by_type(q, [&] { return quantize_launch<float, kNvfp4>(q, stream); },
+                       [&] { return quantize_launch<__nv_bfloat16, kNvfp4>(q, stream); },
+                       [&] { return quantize_launch<__half, kNvfp4>(q, stream); });
+    return by_type(q, [&] { return quantize_launch<float, kMxfp4>(q, stream); },
+                   [&] { return quantize_launch<__nv_bfloat16, kMxfp4>(q, stream); },
+                   [&] { return quantize_launch<__half, kMxfp4>(q, stream); });
 }
 
 cudaError_t launch_mx4_dequantize(const Mx4Dequantize& q, cudaStream_t stream) {
-    const int chunks = chunks_of(q.cols);
-    const bool nv = q.format == kNvfp4;
-    if (q.dtype == kF32)
-        nv ? dequantize_launch<float, kNvfp4>(q, chunks, stream)
-           : dequantize_launch<float, kMxfp4>(q, chunks, stream);
-    else if (q.dtype == kBf16)
-        nv ? dequantize_launch<__nv_bfloat16, kNvfp4>(q, chunks, stream)
-           : dequantize_launch<__nv_bfloat16, kMxfp4>(q, chunks, stream);
-    else
-        nv ? dequantize_launch<__half, kNvfp4>(q, chunks, stream)
-           : dequantize_launch<__half, kMxfp4>(q, chunks, stream);
-    return cudaGetLastError();
+    if (q.format == kNvfp4)
+        return by_type(q, [&] { return dequantize_launch<float, kNvfp4>(q, stream); },
+                       [&] { return dequantize_launch<__nv_bfloat16, kNvfp4>(q, stream); },
+                       [&] { return dequantize_launch<__half, kNvfp4>(q, stream); });
+    return by_type(q, [&] { return dequantize_launch<float, kMxfp4>(q, stream); },
+                   [&] { return dequantize_launch<__nv_bfloat16, kMxfp4>(q, stream); },
+                   [&] { return dequantize_launch<__half, kMxfp4>(q, stream); });
 }
 
 }  // namespace sgemm

@@ -122,5 +122,92 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax, float six_ts) {
     return e == 255 ? 255u : e < 2 ? 0u : e - 2;
 }
 
+// How numbers of a block are divided by its scale d = value of `byte` (* ts), correctly
+// rounded.  mxfp4: times 2^-e, exact.  nvfp4: q0 = x r with r = 1/d correctly rounded,
+// then q0 - r (q0 d - x), whose remainder an FMA gives exactly (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000", 1990); three instructions instead
+// of a division, which alone would take longer than the memory.  Where the remainder could
+// leave the normal range, or the quotient any (a scale at the top of e4m3), it is the
+// division itself.
+static __device__ __noinline__ float quotient(float x, float d) { return __fdiv_rn(x, d); }
+
+template <int FORMAT>
+struct Divider {
+    float d, r;
+    bool fast;
+    __device__ __forceinline__ Divider(uint32_t byte, float ts) {
+        if (FORMAT == kNvfp4) {
+            d = e4m3_decode(byte) * ts;
+            r = __frcp_rn(d);
+            fast = d > 0x1p-90f && d < 0x1p90f && byte < 0x7Eu;
+        } else {
+            d = 0.0f;
+            r = __uint_as_float((254u - byte) << 23);
+            fast = true;
+        }
+    }
+    // Codes of eight numbers; a scale of 0 has codes 0.
+    __device__ __forceinline__ uint32_t codes(const float (&x)[8]) const {
+        float v[8];
+        if (FORMAT == kMxfp4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = x[i] * r;
+            return encode8(v);
+        }
+        if (fast) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float q = x[i] * r;
+                v[i] = fmaf(fmaf(q, d, -x[i]), -r, q);     // these signs keep -0
+            }
+            return encode8(v);
+        }
+        if (d == 0.0f) return 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = quotient(x[i], d);
+        return encode8(v);
+    }
+};
+
+// Bits of the largest magnitude of eight numbers (NaN above infinity above the rest).
+__device__ __forceinline__ uint32_t magnitude8(const float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+// Eight consecutive elements as fp32: 16-byte loads where `vec` says that p is aligned for
+// them, else one by one; those from `left` on are 0.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, int left, float (&x)[8]) {
+    if (vec && left >= 8) {
+        alignas(16) T t[8];
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+            reinterpret_cast<uint4*>(t)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_float(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < left ? to_float(__ldg(p + i)) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool vec, int left, const float (&x)[8]) {
+    if (vec && left >= 8) {
+        alignas(16) T t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = from_float<T>(x[i]);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+            reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(t)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = from_float<T>(x[i]);
+    }
+}
+
 }  // namespace mx4
 }  // namespace sgemm

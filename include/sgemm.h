@@ -330,7 +330,7 @@ SGEMM_API int sgemm_tf32x3_multiply(int M, int N, int K, float alpha, float beta
  *   codes   [rows/128][cols/32][128 rows][16 bytes], the even column in a byte's low half;
  *   scales  [rows/128][blocks/4][row % 32][row/32 % 4][4 blocks], one byte each (e4m3, or
  *           e + 127).
- * Codes and scales of padded columns are zeros, those of padded rows are not written
+ * Codes and scales of padded columns are zeros, those of padded rows are anything
  * and do not matter.  Both buffers are 16-byte aligned device memory of
  * sgemm_mx4_sizes() bytes.  rows and cols may each be at most 2^30.
  * ------------------------------------------------------------------------- */
