@@ -6,6 +6,8 @@ two) consecutive columns.  ``include/sgemm.h`` states the formats and their layo
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _tensors as _t
@@ -31,7 +33,8 @@ class Mx4:
     """A quantised rows x cols matrix: its two buffers, its format and, for nvfp4, the
     scale of the whole tensor (one float32 on the device, None for 1)."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "fmt", "tensor_scale")
+    __slots__ = ("rows", "cols", "fmt", "tensor_scale", "device", "_codes", "_scales", "_both",
+                 "_ptrs")
 
     def __init__(self, codes, scales, rows: int, cols: int, fmt: str, tensor_scale=None):
         _format(fmt)
@@ -40,33 +43,55 @@ class Mx4:
             _t.cuda_tensor(t, name)
             if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
-        _t.same_device(scales, "scales", codes.device)
-        if tensor_scale is not None and fmt != "nvfp4":
-            raise ValueError("only nvfp4 has a tensor scale")
-        self.codes, self.scales, self.rows, self.cols, self.fmt = codes, scales, rows, cols, fmt
-        self.tensor_scale = _t.one_float(tensor_scale, "tensor_scale", codes.device)
+        self.device = codes.device
+        _t.same_device(scales, "scales", self.device)
+        if tensor_scale is not None:
+            if fmt != "nvfp4":
+                raise ValueError("only nvfp4 has a tensor scale")
+            _t.one_float(tensor_scale, "tensor_scale", self.device)
+        self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
+        self._codes, self._scales, self._both = codes, scales, None
+        self._ptrs = (codes.data_ptr(), scales.data_ptr(), _t.ptr(tensor_scale))
+
+    @classmethod
+    def _new(cls, call, rows: int, cols: int, fmt: str, tensor_scale):
+        """An unwritten matrix: one allocation, codes first."""
+        padded = -(-rows // 128) * -(-cols // 128)
+        codes = padded * 8192
+        q = cls.__new__(cls)
+        both = call.empty(codes + padded * (1024 if fmt == "nvfp4" else 512), torch.uint8)
+        at = both.data_ptr()
+        q.rows, q.cols, q.fmt, q.tensor_scale, q.device = rows, cols, fmt, tensor_scale, call.device
+        q._codes, q._scales, q._both = None, None, both
+        q._ptrs = (at, at + codes, None if tensor_scale is None else tensor_scale.data_ptr())
+        return q
+
+    def _views(self):
+        if self._codes is None:
+            codes, scales = mx4_shapes(self.rows, self.cols, self.fmt)
+            n = math.prod(codes)
+            self._codes = self._both[:n].view(codes)
+            self._scales = self._both[n:].view(scales)
+
+    @property
+    def codes(self):
+        self._views()
+        return self._codes
+
+    @property
+    def scales(self):
+        self._views()
+        return self._scales
 
     @property
     def shape(self):
         return self.rows, self.cols
-
-    @property
-    def device(self):
-        return self.codes.device
 
     def dequantize(self, dtype=torch.float32, *, stream=None):
         return mx4_dequantize(self, dtype, stream=stream)
 
     def __repr__(self):
         return f"Mx4({self.rows} x {self.cols}, {self.fmt}, {self.device})"
-
-
-def _empty(call, rows: int, cols: int, fmt: str, tensor_scale) -> Mx4:
-    codes, scales = mx4_shapes(rows, cols, fmt)
-    q = Mx4.__new__(Mx4)
-    q.codes, q.scales = call.empty(codes, torch.uint8), call.empty(scales, torch.uint8)
-    q.rows, q.cols, q.fmt, q.tensor_scale = rows, cols, fmt, tensor_scale
-    return q
 
 
 def mx4_quantize(x, fmt: str = "nvfp4", *, tensor_scale=None, stream=None) -> Mx4:
@@ -79,18 +104,18 @@ def mx4_quantize(x, fmt: str = "nvfp4", *, tensor_scale=None, stream=None) -> Mx
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, cols = x.shape
-    trans = int(not (cols <= 1 or x.stride(1) == 1))
+    trans = 0 if cols <= 1 or x.stride(1) == 1 else 1
     ld = _t.row_ld(x.t() if trans else x, "x")
     dt = _t.dtype_code(x.dtype, "x")
-    if tensor_scale is not None and fmt != "nvfp4":
-        raise ValueError("only nvfp4 has a tensor scale")
-    ts = _t.one_float(tensor_scale, "tensor_scale", x.device)
-    if max(rows, cols) > _t.INT_MAX:
-        raise ValueError("x: a size does not fit the library's 32-bit ints")
-    call = _t.Call(x.device, stream)
-    q = _empty(call, rows, cols, fmt, ts)
-    call.run("sgemm_mx4_quantize", trans, rows, cols, dt, x.data_ptr(), ld, code, _t.ptr(ts),
-             q.codes.data_ptr(), q.scales.data_ptr())
+    device = x.device
+    if tensor_scale is not None:
+        if fmt != "nvfp4":
+            raise ValueError("only nvfp4 has a tensor scale")
+        _t.one_float(tensor_scale, "tensor_scale", device)
+    call = _t.Call(device, stream)
+    q = Mx4._new(call, rows, cols, fmt, tensor_scale)
+    codes, scales, ts = q._ptrs
+    call.run("sgemm_mx4_quantize", trans, rows, cols, dt, x.data_ptr(), ld, code, ts, codes, scales)
     return q
 
 
@@ -105,8 +130,9 @@ def mx4_dequantize(q: Mx4, dtype=torch.float32, out=None, *, stream=None):
     else:
         ld = _t.matrix(out, "out", q.shape, None, q.device)
         dt = _t.dtype_code(out.dtype, "out")
-    call.run("sgemm_mx4_dequantize", q.rows, q.cols, FORMATS[q.fmt], q.codes.data_ptr(),
-             q.scales.data_ptr(), _t.ptr(q.tensor_scale), dt, out.data_ptr(), ld)
+    codes, scales, ts = q._ptrs
+    call.run("sgemm_mx4_dequantize", q.rows, q.cols, FORMATS[q.fmt], codes, scales, ts, dt,
+             out.data_ptr(), ld)
     return out
 
 
@@ -134,7 +160,8 @@ def mx4_matmul(a: Mx4, b: Mx4, out=None, *, dtype=torch.float32, alpha: float = 
     else:
         ld = _t.matrix(out, "out", (M, N), None, a.device)
         dt = _t.dtype_code(out.dtype, "out")
-    call.run("sgemm_mx4_matmul", M, N, a.cols, FORMATS[a.fmt], alpha, a.codes.data_ptr(),
-             a.scales.data_ptr(), _t.ptr(a.tensor_scale), b.codes.data_ptr(),
-             b.scales.data_ptr(), _t.ptr(b.tensor_scale), beta, dt, out.data_ptr(), ld)
+    a_codes, a_scales, a_ts = a._ptrs
+    b_codes, b_scales, b_ts = b._ptrs
+    call.run("sgemm_mx4_matmul", M, N, a.cols, FORMATS[a.fmt], alpha, a_codes, a_scales, a_ts,
+             b_codes, b_scales, b_ts, beta, dt, out.data_ptr(), ld)
     return out
