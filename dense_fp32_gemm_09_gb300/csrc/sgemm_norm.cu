@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(kThreads) norm_backward_wide(const NormBackwar
     }
 }
 
-// out[c] = sum over the blocks' partial sums; blockIdx.y: dw, dgate, dw'.  Eight groups of
-// lanes take every eighth block's sums, and are added in their order.
-__global__ void __launch_bounds__(256) norm_columns_kernel(const NormBackward p, int blocks) {
+// out[c] = sum over the blocks' partial sums; blockIdx.y: dw, dgate, dw'.  A warp takes
+// every 32nd block's sums of 32 columns; the warps' are added by a fixed tree.
+__global__ void __launch_bounds__(1024) norm_columns_kernel(const NormBackward p, int blocks) {
     float* out = blockIdx.y == 0 ? p.dweight
                  : blockIdx.y == 1 ? (p.ldg ? nullptr : static_cast<float*>(p.dgate))
                                    : p.dnext_weight;
-    __shared__ float part[8][32];
+    __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     wait_previous();
@@ -209,16 +209,17 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormBackward p,
     float s = 0.0f;
     if (c < p.cols) {
         const float* from = p.partial + static_cast<long long>(blockIdx.y) * p.cols + c;
-#pragma unroll 8
-        for (int i = slice; i < blocks; i += 8) s += from[i * 3LL * p.cols];
+#pragma unroll 4
+        for (int i = slice; i < blocks; i += 32) s += from[i * 3LL * p.cols];
     }
     part[slice][lane] = s;
     __syncthreads();
-    if (slice == 0 && c < p.cols) {
+    // A warp adds one column's 32 sums.
+    s = part[lane][slice];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += part[i][lane];
-        out[c] = s;
-    }
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    const int mine = blockIdx.x * 32 + slice;
+    if (lane == 0 && mine < p.cols) out[mine] = s;
 }
 
 // ----------------------------------------------------------------------------
@@ -251,30 +252,30 @@ struct RingBuilder {
     void also(const void* p, long long ld) {
         if (p != nullptr && !aligned_to(p, rows > 1 ? ld * elem : 0, 16)) whole = false;
     }
-    // `columns`: a thread's, eight or sixteen; `cached`: bytes of weights that the L1 cache,
-    // which is what shared memory leaves of the SM's 256 KB, should hold.
-    RingShape shape(int columns, long long extra, long long cached, int sms) {
-        const long long shared = std::max<long long>(kSharedPerSm - cached, kSharedPerSm / 2);
+    // `columns`: of a thread, 8 (up to 1024 threads of 64 registers) or more (up to 512 of
+    // 128); `least`: threads of a block.
+    RingShape shape(int columns, int most, int least, long long extra, int sms) {
         RingShape s{};
-        s.vector = align == 16 && whole && ring.row_bytes % 16 == 0;
+        s.ragged = align < 16 || !whole || ring.row_bytes % 16 != 0;
         ring.mode = align == 16 && ring.row_bytes % 16 == 0 ? kBulk
                     : align >= 4 && ring.row_bytes % 4 == 0 ? kCopy4 : kPlain;
-        s.columns = cols <= columns * 1024 ? columns : 16;
-        s.threads = 128;
-        while (s.threads < 1024 && s.threads * s.columns < cols) s.threads *= 2;
+        s.columns = columns;
+        s.most = most;
+        s.threads = least;
+        while (s.threads < most && s.threads * columns < cols) s.threads *= 2;
         const long long stage = static_cast<long long>(ring.n) * ring.pitch;
-        s.fits = cols <= 16 * 1024 && stage + extra <= kSharedPerSm;
+        s.fits = s.threads * columns >= cols && stage + extra <= kSharedPerSm;
         if (!s.fits) return s;
-        // 1024 threads an SM at 64 registers; two stages each at least, if they fit at all.
-        int per = 1024 / s.threads;
-        while (per > 1 && per * (2 * stage + extra) > shared) --per;
+        // As many as the registers hold; two stages each at least, if they fit at all.
+        int per = std::min(most / s.threads, 32);
+        while (per > 1 && per * (2 * stage + extra) > kSharedPerSm) --per;
         s.blocks_per_sm = per;
         s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * per));
         // No more stages than rows a block has.
-        const long long fit = (shared / per - extra) / stage;
+        const long long fit = (kSharedPerSm / per - extra) / stage;
         const long long own = (rows + s.grid - 1) / s.grid;
         ring.stages = static_cast<int>(
-            std::max(1LL, std::min({fit, own + 1, static_cast<long long>(kMaxStages)})));
+            std::max(1LL, std::min({fit, own, static_cast<long long>(kMaxStages)})));
         s.smem = static_cast<int>(ring.stages * stage + extra);
         ring.status = status_word_ptr();
         return s;
@@ -301,9 +302,15 @@ RingBuilder ring_of(const NormBackward& p) {
     return b;
 }
 
-// Eight columns a thread: their sums and one row's numbers fill 64 registers.
+// Sixteen columns a thread where the registers hold their sums (1024 threads an SM for the
+// norm before a block, 512 of 128 registers with the norm after it): what a row costs
+// beside its columns, some 300 instructions a thread, weighs half as much as with eight.
+// fp32 rows take eight, which give more loads in flight: 3001 x 2048 49 against 58 us, but
+// bf16 8192 x 8192 235 against 225.  Rows above 8192 columns take sixteen on 1024 threads,
+// whose sums then spill.
 RingShape backward_shape(const NormBackward& p, RingBuilder& b, int sms) {
-    return b.shape(8, 0, 4LL * p.cols * ((p.weight ? 1 : 0) + (p.next_weight ? 1 : 0)), sms);
+    if (p.block == nullptr || p.cols > 8 * 1024) return b.shape(16, 1024, 64, 0, sms);
+    return p.dtype == kF32 ? b.shape(8, 1024, 64, 0, sms) : b.shape(16, 512, 64, 0, sms);
 }
 
 // Blocks of the backward kernel (each keeps a set of column sums).
@@ -330,11 +337,11 @@ cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stre
     b.also(p.next_weight, 0);
     b.also(p.y, p.ldy);
     b.also(p.h, p.ldh);
-    // Sixteen columns a thread where that still gives a block several warps: two blocks an
-    // SM at 8192 columns, one's barriers under the other's work, where eight give one.
-    const RingShape s = b.shape(p.cols > 2048 ? 16 : 8,
-                                p.format >= 0 ? 128LL * chunks_of(p.cols) : 0,   // a row in fp32
-                                4LL * p.cols * ((p.weight ? 1 : 0) + (p.next_weight ? 1 : 0)), sms);
+    // Sixteen columns a thread: 121 against 149 us with eight at 8192 x 8192 with a gate.
+    // Few rows take eight, for latency: 6.7 against 7.7 us for one row of 4096.
+    const bool few = p.rows <= 2LL * sms && p.cols <= 8 * 1024;
+    const long long extra = p.format >= 0 && p.dtype == kF32 ? 128LL * chunks_of(p.cols) : 0;
+    const RingShape s = b.shape(few ? 8 : 16, 1024, 32, extra, sms);
     if (!s.fits) {
         const dim3 grid(static_cast<unsigned>(p.rows));
         if (p.dtype == kF32)
@@ -372,7 +379,7 @@ cudaError_t launch_norm_backward(const NormBackward& p, int sms, cudaStream_t st
     }
     if (e != cudaSuccess || !sums_columns(p)) return e;
     *launches = 2;
-    return launch_dependent(norm_columns_kernel, dim3((p.cols + 31) / 32, 3), 256, 0, stream, p,
+    return launch_dependent(norm_columns_kernel, dim3((p.cols + 31) / 32, 3), 1024, 0, stream, p,
                             grid);
 }
 

@@ -31,9 +31,9 @@ struct BackwardPlan {
 
 struct RingShape {
     int threads, grid, smem;
-    int columns;       // a thread's
+    int columns, most; // a thread's; threads that the kernel's registers allow on an SM
     int blocks_per_sm;
-    bool vector;       // 16-byte groups; else single columns, threads side by side
+    bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
     bool fits;
 };
 

@@ -46,8 +46,9 @@ __device__ __forceinline__ void ring_fill(const Ring& g, uint8_t* stage, uint64_
 }
 
 // Rows blockIdx.x, + gridDim.x, ... in turn.  `start` fills the ring; `row_ready` waits for
-// the current row's stage; `refill` (after a block-wide barrier that follows every read of
-// the previous row) reuses the previous row's stage.
+// the current row's stage.  Once a row, after a block-wide barrier that follows the last
+// read of a stage, that stage is filled again: the previous row's (refill_previous) or,
+// where the current row's inputs are read no more, its own (refill_this, a row earlier).
 struct RowLoop {
     const Ring& g;
     uint8_t* smem;
@@ -55,26 +56,35 @@ struct RowLoop {
     volatile int* abort;
     long long row, rows;
     int k = 0;                       // rows done
-    __device__ __forceinline__ uint8_t* stage_of(int i) const {
-        return smem + i % g.stages * (g.n * g.pitch);
-    }
+    int stage = 0;                   // k % stages
+    uint32_t phase = 0;              // k / stages % 2
     __device__ __forceinline__ void fill(int ahead) {
+        int s = stage + ahead;
+        if (s >= g.stages) s -= g.stages;
         const long long r = row + ahead * static_cast<long long>(gridDim.x);
-        if (r < rows) ring_fill(g, stage_of(k + ahead), bars + (k + ahead) % g.stages, r);
+        if (r < rows) ring_fill(g, smem + s * (g.n * g.pitch), bars + s, r);
+    }
+    __device__ __forceinline__ void commit() {
         if (g.mode == kCopy4) asm volatile("cp.async.commit_group;" ::: "memory");
     }
     __device__ __forceinline__ void start() {
-        for (int i = 0; i < g.stages - 1; ++i) fill(i);
+        if (g.stages == 1) return;
+        for (int i = 0; i < g.stages; ++i) {
+            fill(i);
+            commit();
+        }
     }
     __device__ __forceinline__ const uint8_t* row_ready() {
         if (g.stages == 1) {         // a row too wide for two: no overlap
             __syncthreads();
             fill(0);
+            commit();
         }
         if (g.mode == kBulk) {
-            pipe_wait(su32(bars + k % g.stages), k / g.stages & 1, abort, g.status);
+            pipe_wait(su32(bars + stage), phase, abort, g.status);
         } else {
-            // Groups are committed one a row: all but those of the rows after this one.
+            // One group a row, and with refill_previous an empty one at first: all but
+            // stages - 2 of the newest have arrived.
             if (g.mode == kCopy4) {
                 if (g.stages == 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
                 else if (g.stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -82,14 +92,25 @@ struct RowLoop {
             }
             __syncthreads();
         }
-        return stage_of(k);
+        return smem + stage * (g.n * g.pitch);
     }
-    __device__ __forceinline__ void refill() {
-        if (g.stages > 1) fill(g.stages - 1);
+    __device__ __forceinline__ void refill_previous() {
+        if (g.stages == 1) return;
+        if (k > 0) fill(g.stages - 1);
+        commit();
+    }
+    __device__ __forceinline__ void refill_this() {
+        if (g.stages == 1) return;
+        fill(g.stages);
+        commit();
     }
     __device__ __forceinline__ void next() {
         row += gridDim.x;
         ++k;
+        if (++stage == g.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
     }
 };
 
@@ -113,62 +134,176 @@ struct BlockSum {
     }
 };
 
-// VEC consecutive elements.  With VEC > 1 rows and weights are whole vectors, 16-byte
-// aligned (else the kernels for single columns run).
-template <typename T, int VEC>
-__device__ __forceinline__ void get(const T* p, float (&x)[VEC]) {
-    if constexpr (VEC == 1) {
-        x[0] = to_float(p[0]);
-    } else {
-        alignas(16) T t[VEC];
-        *reinterpret_cast<uint4*>(t) = *reinterpret_cast<const uint4*>(p);
+// Two fp32 numbers in a register pair, and the packed instructions on them: the kernels
+// issue about as many instructions as the memory leaves time for, so halving the
+// arithmetic shows.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float lo, float hi) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ Two twice(float v) { return two(v, v); }
+__device__ __forceinline__ float2 parts(Two v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum(Two v) {
+    const float2 f = parts(v);
+    return f.x + f.y;
+}
+
+// 16 bytes of a row as pairs, and back.
+template <typename T> constexpr int kPairs = 8 / sizeof(T);
+__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[2], float) {
+    x[0] = two(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = two(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[4], __nv_bfloat16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) x[j] = to_float(t[j]);
+    for (int i = 0; i < 4; ++i)      // a bf16 number is the high half of its fp32 one
+        x[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[4], __half) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[i] = two(f.x, f.y);
     }
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void put(T* p, const float (&x)[VEC]) {
-    if constexpr (VEC == 1) {
-        p[0] = from_float<T>(x[0]);
-    } else {
-        alignas(16) T t[VEC];
+__device__ __forceinline__ uint4 pack(const Two (&x)[2], float) {
+    const float2 a = parts(x[0]), b = parts(x[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                      __float_as_uint(b.y));
+}
+__device__ __forceinline__ uint4 pack(const Two (&x)[4], __nv_bfloat16) {
+    uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) t[j] = from_float<T>(x[j]);
-        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts(x[i]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const Two (&x)[4], __half) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts(x[i]);
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16 bytes of a row in shared memory, where every row starts on 16 bytes and is followed by
+// zeros up to the next 16.
+template <typename T>
+__device__ __forceinline__ void get(const T* p, Two (&x)[kPairs<T>]) {
+    unpack(*reinterpret_cast<const uint4*>(p), x, T());
+}
+// The same of a row of D columns in global memory, at column c.  RAGGED: any alignment to
+// the element, and the row may end inside.
+template <typename T, bool RAGGED>
+__device__ __forceinline__ void put(T* row, int c, int D, const Two (&x)[kPairs<T>]) {
+    if constexpr (RAGGED) {
+#pragma unroll
+        for (int j = 0; j < kPairs<T>; ++j) {
+            const float2 f = parts(x[j]);
+            if (c + 2 * j < D) row[c + 2 * j] = from_float<T>(f.x);
+            if (c + 2 * j + 1 < D) row[c + 2 * j + 1] = from_float<T>(f.y);
+        }
+    } else {
+        *reinterpret_cast<uint4*>(row + c) = pack(x, T());
     }
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void get_global(const T* p, float (&x)[VEC]) {
-    if constexpr (VEC == 1) {
-        x[0] = to_float(__ldg(p));
+// P pairs of a vector that all rows share (it stays in the L1 cache): 0 past its end.
+template <typename W, int P, bool RAGGED>
+__device__ __forceinline__ void get_shared(const W* p, int c, int D, Two (&x)[P]) {
+    if constexpr (RAGGED) {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            x[j] = two(c + 2 * j < D ? to_float(__ldg(p + c + 2 * j)) : 0.0f,
+                       c + 2 * j + 1 < D ? to_float(__ldg(p + c + 2 * j + 1)) : 0.0f);
+    } else if constexpr (2 * P * sizeof(W) == 8) {
+        // Four 2-byte weights with a vector of four fp32 numbers.
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + c));
+        Two t[4];
+        unpack(make_uint4(v.x, v.y, 0, 0), t, W());
+#pragma unroll
+        for (int j = 0; j < P; ++j) x[j] = t[j];
     } else {
-        // 8 or 16 bytes a load: four 2-byte weights go with a vector of four fp32 numbers.
-        using Piece = typename std::conditional<VEC * sizeof(T) == 8, uint2, uint4>::type;
-        alignas(16) T t[VEC];
+        constexpr int kEach = kPairs<W>;
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(VEC * sizeof(T) / sizeof(Piece)); ++i)
-            reinterpret_cast<Piece*>(t)[i] = __ldg(reinterpret_cast<const Piece*>(p) + i);
+        for (int i = 0; i < P / kEach; ++i) {
+            Two t[kEach];
+            unpack(__ldg(reinterpret_cast<const uint4*>(p + c) + i), t, W());
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) x[j] = to_float(t[j]);
+            for (int j = 0; j < kEach; ++j) x[i * kEach + j] = t[j];
+        }
     }
 }
-// Weights, the same for every row (they stay in the L1 cache); ones where there are none.
-template <int VEC>
-__device__ __forceinline__ void weights(const void* w, int type, int c, float (&x)[VEC]) {
+// Weights; ones where there are none.
+template <int P, bool RAGGED>
+__device__ __forceinline__ void weights(const void* w, int type, int c, int D, Two (&x)[P]) {
     if (w == nullptr) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) x[j] = 1.0f;
+        for (int j = 0; j < P; ++j) x[j] = twice(1.0f);
     } else if (type == kF32) {
-        get_global<float, VEC>(static_cast<const float*>(w) + c, x);
+        get_shared<float, P, RAGGED>(static_cast<const float*>(w), c, D, x);
     } else if (type == kBf16) {
-        get_global<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w) + c, x);
+        get_shared<__nv_bfloat16, P, RAGGED>(static_cast<const __nv_bfloat16*>(w), c, D, x);
     } else {
-        get_global<__half, VEC>(static_cast<const __half*>(w) + c, x);
+        get_shared<__half, P, RAGGED>(static_cast<const __half*>(w), c, D, x);
     }
 }
 
-// Codes and scales of a row of fp32 numbers in shared memory (zeros past its end): four
-// lanes take 32 columns, as in quantisation.
+// The padding after each row of each stage, which copies never touch, to zeros.
+__device__ __forceinline__ void ring_clear(const Ring& g, uint8_t* smem) {
+    const int pad = g.pitch - g.row_bytes;
+    for (int i = threadIdx.x; i < g.stages * g.n * pad; i += blockDim.x)
+        smem[(i / pad) * g.pitch + g.row_bytes + i % pad] = 0;
+}
+
+// Codes and scales of the columns 8 v .. 8 v + 7 of a row, `x`; zeros past the row's end.
+// Whole warps with consecutive v: four lanes take 32 columns, as in quantisation.
+template <int FORMAT>
+__device__ __forceinline__ void quantize8(const float (&x)[8], int v, int chunks, int groups,
+                                          const NormForward& p, long long row, float ts) {
+    const int lane = threadIdx.x & 31;
+    const bool live = v < 4 * chunks;
+    uint32_t amax = magnitude8(x);
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    const uint32_t byte = block_scale<FORMAT>(amax, 6.0f * ts);
+    const uint32_t packed = Divider<FORMAT>(byte, ts).codes(x);
+    if (live)
+        *reinterpret_cast<uint32_t*>(p.codes + code_offset(row, v >> 2, chunks) + 4 * (v & 3)) =
+            packed;
+    // Four blocks' bytes to the first of their lanes.
+    constexpr int kStep = FORMAT == kNvfp4 ? 2 : 4;
+    uint32_t word = byte;
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+        word |= __shfl_down_sync(0xFFFFFFFFu, byte, kStep * i) << (8 * i);
+    if (live && lane % (4 * kStep) == 0)
+        *reinterpret_cast<uint32_t*>(p.scales + scale_offset(row, v / kStep, groups)) = word;
+}
+// A row of fp32 numbers in shared memory (zeros past its end).
 template <int FORMAT>
 __device__ __forceinline__ void quantize_row(const float* h, const NormForward& p, long long row,
                                              float ts) {
@@ -184,31 +319,18 @@ __device__ __forceinline__ void quantize_row(const float* h, const NormForward& 
                                   : make_float4(0, 0, 0, 0);
             x[i] = t.x; x[i + 1] = t.y; x[i + 2] = t.z; x[i + 3] = t.w;
         }
-        uint32_t amax = magnitude8(x);
-        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        const uint32_t byte = block_scale<FORMAT>(amax, 6.0f * ts);
-        const uint32_t packed = Divider<FORMAT>(byte, ts).codes(x);
-        if (live)
-            *reinterpret_cast<uint32_t*>(p.codes + code_offset(row, v >> 2, chunks) + 4 * (v & 3)) =
-                packed;
-        // Four blocks' bytes to the first of their lanes.
-        constexpr int kStep = FORMAT == kNvfp4 ? 2 : 4;
-        uint32_t word = byte;
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-            word |= __shfl_down_sync(0xFFFFFFFFu, byte, kStep * i) << (8 * i);
-        if (live && lane % (4 * kStep) == 0)
-            *reinterpret_cast<uint32_t*>(p.scales + scale_offset(row, v / kStep, groups)) = word;
+        quantize8<FORMAT>(x, v, chunks, groups, p, row, ts);
     }
 }
 
 // ----------------------------------------------------------------------------
 // Forward: inputs block, residual, gate (a row each); N groups of VEC columns a thread
 // ----------------------------------------------------------------------------
-template <typename T, int VEC, int N, int WHAT>
-__global__ void __launch_bounds__(1024, 1) norm_forward_ring(const ForwardPlan pl) {
+template <typename T, bool RAGGED, int COLS, int WHAT>
+__global__ void __launch_bounds__(1024, 1)
+    norm_forward_ring(const ForwardPlan pl) {
     constexpr bool kAfter = WHAT != kBefore, kNext = WHAT != kAfterOnly;
+    constexpr int VEC = 16 / sizeof(T), P = VEC / 2, N = COLS / VEC;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kMaxStages];
     __shared__ float part[2][32];
@@ -222,8 +344,10 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring(const ForwardPlan p
         abort_s = 0;
         async::mbar_fence_init();
     }
-    if (p.format >= 0)
+    const int chunks = chunks_of(D), groups = p.format >= 0 ? groups_of(D, p.format) : 0;
+    if (VEC != 8 && p.format >= 0)
         for (int c = D + threadIdx.x; c < 32 * chunks_of(D); c += NT) hrow[c] = 0.0f;
+    ring_clear(ring, smem);
     __syncthreads();
     wait_previous();
     const float ts = p.tensor_scale ? __ldg(p.tensor_scale) : 1.0f;
@@ -237,72 +361,92 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring(const ForwardPlan p
         const T* const res = reinterpret_cast<const T*>(in);
         const T* const blk = reinterpret_cast<const T*>(in + ring.pitch);
         const T* const gate = reinterpret_cast<const T*>(in + 2 * ring.pitch);
-        float u[N][VEC];
-        float s = 0.0f;
+        Two u[N][P];
+        Two s = twice(0.0f);
         if constexpr (kAfter) {
-            float b[N][VEC];
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int c = (threadIdx.x + i * NT) * VEC;
-                if (c < D) {
-                    get<T, VEC>(blk + c, b[i]);
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) s = fmaf(b[i][j], b[i][j], s);
-                }
-            }
-            const float r = rsqrtf(block_sum(s) / static_cast<float>(D) + p.eps);
-            loop.refill();
-            if (threadIdx.x == 0) p.rstd[row] = r;
-            s = 0.0f;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
                 if (c >= D) continue;
-                float w[VEC], g[VEC];
-                weights<VEC>(p.weight, p.weight_dtype, c, w);
-                if (gate_rows) get<T, VEC>(gate + c, g);
-                else if (p.gate)
-                    get_global<T, VEC>(static_cast<const T*>(p.gate) + c, g);
-                get<T, VEC>(res + c, u[i]);
+                Two b[P];
+                get(blk + c, b);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    float n = b[i][j] * r * w[j];
-                    if (p.gate) n *= g[j];
-                    u[i][j] = fmaf(p.scale, n, u[i][j]);
-                    s = fmaf(u[i][j], u[i][j], s);
+                for (int j = 0; j < P; ++j) s = fma(b[j], b[j], s);
+            }
+            const float r = rsqrtf(block_sum(sum(s)) / static_cast<float>(D) + p.eps);
+            if constexpr (!kNext) loop.refill_previous();
+            if (threadIdx.x == 0) p.rstd[row] = r;
+            const Two sr = twice(p.scale * r);
+            s = twice(0.0f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = (threadIdx.x + i * NT) * VEC;
+                if (c >= D) continue;
+                Two n[P], w[P];
+                weights<P, RAGGED>(p.weight, p.weight_dtype, c, D, w);
+                get(blk + c, n);
+#pragma unroll
+                for (int j = 0; j < P; ++j) n[j] = mul(n[j], w[j]);
+                if (p.gate) {
+                    if (gate_rows) get(gate + c, w);
+                    else get_shared<T, P, RAGGED>(static_cast<const T*>(p.gate), c, D, w);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) n[j] = mul(n[j], w[j]);
                 }
-                put<T, VEC>(static_cast<T*>(p.y) + row * p.ldy + c, u[i]);
+                get(res + c, u[i]);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    u[i][j] = fma(n[j], sr, u[i][j]);
+                    s = fma(u[i][j], u[i][j], s);
+                }
+                put<T, RAGGED>(static_cast<T*>(p.y) + row * p.ldy, c, D, u[i]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
                 if (c >= D) continue;
-                get<T, VEC>(res + c, u[i]);
+                get(res + c, u[i]);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) s = fmaf(u[i][j], u[i][j], s);
+                for (int j = 0; j < P; ++j) s = fma(u[i][j], u[i][j], s);
             }
         }
         if constexpr (kNext) {
-            const float rn = rsqrtf(block_sum(s) / static_cast<float>(D) + p.eps);
-            if constexpr (!kAfter) loop.refill();
+            const float rn = rsqrtf(block_sum(sum(s)) / static_cast<float>(D) + p.eps);
+            loop.refill_this();          // what comes is made from u
             if (threadIdx.x == 0) p.next_rstd[row] = rn;
+            const Two rn2 = twice(rn);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
-                if (c >= D) continue;
-                float w[VEC];
-                weights<VEC>(p.next_weight, p.weight_dtype, c, w);
+                Two w[P];
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) w[j] = u[i][j] * rn * w[j];
+                for (int j = 0; j < P; ++j) w[j] = twice(0.0f);
+                if (c < D) {
+                    weights<P, RAGGED>(p.next_weight, p.weight_dtype, c, D, w);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) w[j] = mul(mul(u[i][j], rn2), w[j]);
+                }
                 if (p.format < 0) {
-                    put<T, VEC>(static_cast<T*>(p.h) + row * p.ldh + c, w);
-                } else {
+                    if (c < D) put<T, RAGGED>(static_cast<T*>(p.h) + row * p.ldh, c, D, w);
+                } else if constexpr (VEC == 8) {
+                    // A thread's eight columns are a lane's in quantisation; the threads
+                    // reach past the padded row.
+                    float x[8];
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) hrow[c + j] = w[j];
+                    for (int j = 0; j < P; ++j) {
+                        const float2 f = parts(w[j]);
+                        x[2 * j] = f.x;
+                        x[2 * j + 1] = f.y;
+                    }
+                    const int v = threadIdx.x + i * NT;
+                    if (p.format == kNvfp4) quantize8<kNvfp4>(x, v, chunks, groups, p, row, ts);
+                    else quantize8<kMxfp4>(x, v, chunks, groups, p, row, ts);
+                } else if (c < D) {
+                    *reinterpret_cast<uint4*>(hrow + c) = pack(w, 0.0f);     // zeros past D
                 }
             }
-            if (p.format >= 0) {
+            if (VEC != 8 && p.format >= 0) {
                 __syncthreads();
                 if (p.format == kNvfp4) quantize_row<kNvfp4>(hrow, p, row, ts);
                 else quantize_row<kMxfp4>(hrow, p, row, ts);
@@ -316,9 +460,11 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring(const ForwardPlan p
 // ----------------------------------------------------------------------------
 // Backward: inputs dy, dh, y, block, gate as far as they are there, in this order
 // ----------------------------------------------------------------------------
-template <typename T, int VEC, int N, int WHAT, bool SHARED>
-__global__ void __launch_bounds__(1024, 1) norm_backward_ring(const BackwardPlan pl) {
+template <typename T, bool RAGGED, int COLS, int THREADS, int WHAT, bool SHARED>
+__global__ void __launch_bounds__(THREADS, 1)
+    norm_backward_ring(const BackwardPlan pl) {
     constexpr bool kAfter = WHAT != kBefore, kNext = WHAT != kAfterOnly;
+    constexpr int VEC = 16 / sizeof(T), P = VEC / 2, N = COLS / VEC;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kMaxStages];
     __shared__ float part[2][32];
@@ -332,16 +478,22 @@ __global__ void __launch_bounds__(1024, 1) norm_backward_ring(const BackwardPlan
         abort_s = 0;
         async::mbar_fence_init();
     }
+    ring_clear(ring, smem);
     __syncthreads();
     wait_previous();
     const bool gate_rows = p.gate && p.ldg;
     RowLoop loop{ring, smem, bars, &abort_s, blockIdx.x, p.rows};
     BlockSum block_sum{part};
-    float sw[N][VEC] = {}, sg[SHARED ? N : 1][VEC] = {}, sn[N][VEC] = {};
+    Two sw[N][P] = {}, sg[SHARED ? N : 1][P] = {}, sn[N][P] = {};
     loop.start();
+    // A row's statistics are loaded a row ahead: nothing else hides that latency.
+    auto stat = [&](const float* v, long long row) { return row < p.rows ? __ldg(v + row) : 0.0f; };
+    float rn_ahead = kNext ? stat(p.next_rstd, loop.row) : 0.0f;
+    float r_ahead = kAfter ? stat(p.rstd, loop.row) : 0.0f;
     for (; loop.row < p.rows; loop.next()) {
-        const float rn = kNext ? __ldg(p.next_rstd + loop.row) : 0.0f;
-        const float r = kAfter ? __ldg(p.rstd + loop.row) : 0.0f;
+        const float rn = rn_ahead, r = r_ahead;
+        if (kNext) rn_ahead = stat(p.next_rstd, loop.row + gridDim.x);
+        if (kAfter) r_ahead = stat(p.rstd, loop.row + gridDim.x);
         const uint8_t* in = loop.row_ready();
         const long long row = loop.row;
         const T* const dy = reinterpret_cast<const T*>(in);
@@ -353,92 +505,113 @@ __global__ void __launch_bounds__(1024, 1) norm_backward_ring(const BackwardPlan
         const T* const blk = reinterpret_cast<const T*>(in);
         if (kAfter) in += ring.pitch;
         const T* const gate = reinterpret_cast<const T*>(in);
-        // Across a barrier a thread keeps t only; n', n and the weighted gradients are made
-        // again from shared memory, which costs less than the registers would.
-        float t[N][VEC];
-        float s = 0.0f;
+        // Across a barrier a thread keeps t (then w g) only; the rest is made again from
+        // shared memory, which costs less than the registers would.
+        Two t[N][P];
+        Two s = twice(0.0f);
         if constexpr (kNext) {
+            const Two rn2 = twice(rn);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
                 if (c >= D) continue;
-                float w[VEC], d[VEC], n[VEC];
-                weights<VEC>(p.next_weight, p.weight_dtype, c, w);
-                get<T, VEC>(dh + c, d);
-                get<T, VEC>(y + c, n);
+                Two w[P], d[P], n[P];
+                weights<P, RAGGED>(p.next_weight, p.weight_dtype, c, D, w);
+                get(dh + c, d);
+                get(y + c, n);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float dn = d[j] * (n[j] * rn);
-                    sn[i][j] += dn;
-                    s = fmaf(w[j], dn, s);
+                for (int j = 0; j < P; ++j) {
+                    const Two dn = mul(d[j], n[j]);
+                    sn[i][j] = fma(dn, rn2, sn[i][j]);
+                    s = fma(w[j], dn, s);
                 }
             }
-            const float mn = block_sum(s) * inv;
-            loop.refill();
-            s = 0.0f;
+            const float mn = block_sum(sum(s)) * rn * inv;
+            loop.refill_previous();
+            const Two k = twice(-rn * rn * mn);
+            s = twice(0.0f);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
                 if (c >= D) continue;
-                float w[VEC], d[VEC], n[VEC];
-                weights<VEC>(p.next_weight, p.weight_dtype, c, w);
-                get<T, VEC>(dh + c, d);
-                get<T, VEC>(y + c, n);
-                if (p.dy) get<T, VEC>(dy + c, t[i]);
+                Two w[P], d[P];
+                weights<P, RAGGED>(p.next_weight, p.weight_dtype, c, D, w);
+                get(dh + c, d);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float v = rn * fmaf(-n[j] * rn, mn, w[j] * d[j]);
-                    t[i][j] = p.dy ? t[i][j] + v : v;
+                for (int j = 0; j < P; ++j) w[j] = mul(w[j], d[j]);
+                if (p.dy) {
+                    get(dy + c, t[i]);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) t[i][j] = fma(w[j], rn2, t[i][j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < P; ++j) t[i][j] = mul(w[j], rn2);
                 }
-                put<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + c, t[i]);
+                get(y + c, d);
+#pragma unroll
+                for (int j = 0; j < P; ++j) t[i][j] = fma(d[j], k, t[i][j]);
+                put<T, RAGGED>(static_cast<T*>(p.dx) + row * p.lddx, c, D, t[i]);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
                 if (c >= D) continue;
-                get<T, VEC>(dy + c, t[i]);
-                if (p.dx)
-                    put<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + c, t[i]);
+                get(dy + c, t[i]);
+                if (p.dx) put<T, RAGGED>(static_cast<T*>(p.dx) + row * p.lddx, c, D, t[i]);
             }
         }
         if constexpr (kAfter) {
+            const Two sr = twice(p.scale * r);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
                 if (c >= D) continue;
-                float w[VEC], g[VEC], n[VEC];
-                weights<VEC>(p.weight, p.weight_dtype, c, w);
-                get<T, VEC>(blk + c, n);
-                if (gate_rows) get<T, VEC>(gate + c, g);
-                else if (p.gate)
-                    get_global<T, VEC>(static_cast<const T*>(p.gate) + c, g);
+                Two w[P], e[P];
+                weights<P, RAGGED>(p.weight, p.weight_dtype, c, D, w);
+                get(blk + c, e);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    n[j] *= r;
-                    t[i][j] *= p.scale;
-                    const float dg = t[i][j] * n[j] * w[j];
-                    if constexpr (SHARED) sg[i][j] += dg;
-                    if (p.gate) t[i][j] *= g[j];
-                    sw[i][j] = fmaf(t[i][j], n[j], sw[i][j]);
-                    t[i][j] *= w[j];                     // w g
-                    s = fmaf(t[i][j], n[j], s);
-                    w[j] = dg;
+                for (int j = 0; j < P; ++j) e[j] = mul(e[j], t[i][j]);       // t b
+                if (SHARED || gate_rows) {
+                    Two dg[P];
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        dg[j] = mul(e[j], w[j]);
+                        if constexpr (SHARED) sg[i][j] = fma(dg[j], sr, sg[i][j]);
+                        else dg[j] = mul(dg[j], sr);
+                    }
+                    if (!SHARED && p.dgate)
+                        put<T, RAGGED>(static_cast<T*>(p.dgate) + row * p.lddg, c, D, dg);
                 }
-                if (gate_rows && p.dgate)
-                    put<T, VEC>(static_cast<T*>(p.dgate) + row * p.lddg + c, w);
+                if (p.gate) {
+                    Two g[P];
+                    if (gate_rows) get(gate + c, g);
+                    else get_shared<T, P, RAGGED>(static_cast<const T*>(p.gate), c, D, g);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        e[j] = mul(e[j], g[j]);
+                        t[i][j] = mul(t[i][j], g[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    sw[i][j] = fma(e[j], sr, sw[i][j]);
+                    s = fma(e[j], w[j], s);
+                    t[i][j] = mul(t[i][j], w[j]);
+                }
             }
-            const float m = block_sum(s) * inv;
-            if constexpr (!kNext) loop.refill();
+            const float m = block_sum(sum(s)) * (p.scale * r) * inv;
+            if constexpr (!kNext) loop.refill_previous();
+            const Two k = twice(-r * r * m);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
                 if (c >= D) continue;
-                float n[VEC];
-                get<T, VEC>(blk + c, n);
+                Two n[P];
+                get(blk + c, n);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) n[j] = r * fmaf(-n[j] * r, m, t[i][j]);
-                put<T, VEC>(static_cast<T*>(p.dblock) + row * p.lddb + c, n);
+                for (int j = 0; j < P; ++j) n[j] = fma(t[i][j], sr, mul(n[j], k));
+                put<T, RAGGED>(static_cast<T*>(p.dblock) + row * p.lddb, c, D, n);
             }
         }
     }
@@ -450,9 +623,11 @@ __global__ void __launch_bounds__(1024, 1) norm_backward_ring(const BackwardPlan
             if (c >= D) continue;
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                if (kAfter && p.dweight) pw[c + j] = sw[i][j];
-                if constexpr (SHARED) pw[D + c + j] = sg[i][j];
-                if (kNext && p.dnext_weight) pw[2LL * D + c + j] = sn[i][j];
+                if (RAGGED && c + j >= D) break;
+                const auto part = [j](const Two& v) { return j % 2 ? parts(v).y : parts(v).x; };
+                if (kAfter && p.dweight) pw[c + j] = part(sw[i][j / 2]);
+                if constexpr (SHARED) pw[D + c + j] = part(sg[i][j / 2]);
+                if (kNext && p.dnext_weight) pw[2LL * D + c + j] = part(sn[i][j / 2]);
             }
         }
     }
@@ -472,38 +647,50 @@ cudaError_t launch_ring(K kernel, const P& plan, const RingShape& s, cudaStream_
     return launch_dependent(kernel, dim3(s.grid), s.threads, s.smem, stream, plan);
 }
 
-template <typename T, int VEC, int N>
+template <typename T, bool RAGGED, int COLS>
 cudaError_t forward_what(const ForwardPlan& pl, const RingShape& s, cudaStream_t st) {
-    if (!pl.p.block) return launch_ring(norm_forward_ring<T, VEC, N, kBefore>, pl, s, st);
-    if (!pl.p.next) return launch_ring(norm_forward_ring<T, VEC, N, kAfterOnly>, pl, s, st);
-    return launch_ring(norm_forward_ring<T, VEC, N, kBoth>, pl, s, st);
+    if (!pl.p.block) return launch_ring(norm_forward_ring<T, RAGGED, COLS, kBefore>, pl, s, st);
+    if (!pl.p.next) return launch_ring(norm_forward_ring<T, RAGGED, COLS, kAfterOnly>, pl, s, st);
+    return launch_ring(norm_forward_ring<T, RAGGED, COLS, kBoth>, pl, s, st);
 }
-template <typename T, int VEC, int N>
+template <typename T, bool RAGGED, int COLS, int THREADS>
 cudaError_t backward_what(const BackwardPlan& pl, const RingShape& s, cudaStream_t st) {
     const bool shared = pl.p.dgate && pl.p.ldg == 0;
-    if (!pl.p.block) return launch_ring(norm_backward_ring<T, VEC, N, kBefore, false>, pl, s, st);
+    if (!pl.p.block) {
+        if constexpr (COLS == 16 && THREADS == 1024)
+            return launch_ring(norm_backward_ring<T, RAGGED, 16, 1024, kBefore, false>, pl, s, st);
+        return cudaErrorInvalidConfiguration;
+    }
     if (!pl.p.dh)
-        return shared ? launch_ring(norm_backward_ring<T, VEC, N, kAfterOnly, true>, pl, s, st)
-                      : launch_ring(norm_backward_ring<T, VEC, N, kAfterOnly, false>, pl, s, st);
-    return shared ? launch_ring(norm_backward_ring<T, VEC, N, kBoth, true>, pl, s, st)
-                  : launch_ring(norm_backward_ring<T, VEC, N, kBoth, false>, pl, s, st);
+        return shared
+            ? launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kAfterOnly, true>, pl, s, st)
+            : launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kAfterOnly, false>, pl, s, st);
+    return shared
+        ? launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kBoth, true>, pl, s, st)
+        : launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kBoth, false>, pl, s, st);
 }
-// Eight or sixteen columns a thread.
+template <typename T, bool RAGGED>
+cudaError_t forward_rows(const ForwardPlan& pl, const RingShape& s, cudaStream_t st) {
+    return s.columns == 8 ? forward_what<T, RAGGED, 8>(pl, s, st)
+                          : forward_what<T, RAGGED, 16>(pl, s, st);
+}
+template <typename T, bool RAGGED>
+cudaError_t backward_rows(const BackwardPlan& pl, const RingShape& s, cudaStream_t st) {
+    if (s.columns == 8) {
+        if constexpr (sizeof(T) == 4) return backward_what<T, RAGGED, 8, 1024>(pl, s, st);
+        return cudaErrorInvalidConfiguration;
+    }
+    if (s.most == 1024) return backward_what<T, RAGGED, 16, 1024>(pl, s, st);
+    if constexpr (sizeof(T) == 2) return backward_what<T, RAGGED, 16, 512>(pl, s, st);
+    return cudaErrorInvalidConfiguration;
+}
 template <typename T>
 cudaError_t forward_ring(const ForwardPlan& pl, const RingShape& s, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    if (!s.vector) return s.columns <= 8 ? forward_what<T, 1, 8>(pl, s, st)
-                                         : forward_what<T, 1, 16>(pl, s, st);
-    return s.columns <= 8 ? forward_what<T, V, 8 / V>(pl, s, st)
-                          : forward_what<T, V, 16 / V>(pl, s, st);
+    return s.ragged ? forward_rows<T, true>(pl, s, st) : forward_rows<T, false>(pl, s, st);
 }
 template <typename T>
 cudaError_t backward_ring(const BackwardPlan& pl, const RingShape& s, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T);
-    if (!s.vector) return s.columns <= 8 ? backward_what<T, 1, 8>(pl, s, st)
-                                         : backward_what<T, 1, 16>(pl, s, st);
-    return s.columns <= 8 ? backward_what<T, V, 8 / V>(pl, s, st)
-                          : backward_what<T, V, 16 / V>(pl, s, st);
+    return s.ragged ? backward_rows<T, true>(pl, s, st) : backward_rows<T, false>(pl, s, st);
 }
 
 }  // namespace norm
