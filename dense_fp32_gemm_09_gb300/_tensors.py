@@ -90,6 +90,45 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_fast = None
+
+
+def fast():
+    """The compiled binding of the usual calls: each returns its outputs, a status of the
+    library where that is not 0, or None for a call that is not of the usual form."""
+    global _fast
+    if _fast is None:
+        import ctypes
+        import importlib.machinery
+        import importlib.util
+        import os
+
+        from . import build
+        lib = load()
+        if not os.path.exists(build.FAST_PATH):
+            raise RuntimeError(f"{build.FAST_PATH} is missing: build the library first "
+                               "(python -m dense_fp32_gemm_09_gb300.build)")
+        loader = importlib.machinery.ExtensionFileLoader("_fast_calls", build.FAST_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_fast_calls", loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "sgemm_mx4_quantize", "sgemm_mx4_dequantize", "sgemm_mx4_matmul",
+            "sgemm_norm_forward", "sgemm_norm_backward")))
+        _fast = module
+    return _fast
+
+
+def checked(result, name: str) -> None:
+    """Raises where a fast call returned a status instead of its outputs."""
+    if type(result) is int:
+        check(result, name)
+
+
+def current(device) -> bool:
+    return _current_device() == device.index
+
+
 _functions = {}
 
 

@@ -21,6 +21,8 @@ OUT_DIR = os.path.join(PKG_DIR, "_lib")
 OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB_NAME = "libsgemm_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
+FAST_SRC = os.path.join(PKG_DIR, "binding", "fast_calls.cpp")
+FAST_PATH = os.path.join(OUT_DIR, "_fast_calls.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -52,6 +54,36 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def _newer(path: str, files) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path)
+                                        for f in files)
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the binding of the usual calls (host code only, against the installed torch)."""
+    inputs = [FAST_SRC, os.path.join(INCLUDE, "sgemm.h"), os.path.abspath(__file__)]
+    if not force and _newer(FAST_PATH, inputs):
+        return FAST_PATH
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    os.makedirs(OUT_DIR, exist_ok=True)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    include = [INCLUDE, sysconfig.get_paths()["include"], cuda, *cpp_extension.include_paths()]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = FAST_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in include[1:]), f"-I{INCLUDE}", FAST_SRC, "-o", tmp,
+           f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {FAST_SRC}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, FAST_PATH)
+    return FAST_PATH
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(OBJ_DIR, os.path.basename(src).replace(".cu", ".o"))
     cmd = [nvcc(), *ARCH_FLAGS, *NVCC_FLAGS, "-c", src, "-o", obj]
@@ -68,11 +100,14 @@ def _compile(src: str, verbose: bool) -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if needed) and return the path of the shared library."""
     if not force and up_to_date():
+        build_binding()
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

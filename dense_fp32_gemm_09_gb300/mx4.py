@@ -57,13 +57,18 @@ class Mx4:
     def _new(cls, call, rows: int, cols: int, fmt: str, tensor_scale):
         """An unwritten matrix: one allocation, codes first."""
         padded = -(-rows // 128) * -(-cols // 128)
-        codes = padded * 8192
+        both = call.empty(padded * (9216 if fmt == "nvfp4" else 8704), torch.uint8)
+        return cls._of(both, rows, cols, fmt, tensor_scale)
+
+    @classmethod
+    def _of(cls, both, rows: int, cols: int, fmt: str, tensor_scale):
+        """The matrix in one buffer, codes first."""
         q = cls.__new__(cls)
-        both = call.empty(codes + padded * (1024 if fmt == "nvfp4" else 512), torch.uint8)
         at = both.data_ptr()
-        q.rows, q.cols, q.fmt, q.tensor_scale, q.device = rows, cols, fmt, tensor_scale, call.device
+        q.rows, q.cols, q.fmt, q.tensor_scale, q.device = rows, cols, fmt, tensor_scale, both.device
         q._codes, q._scales, q._both = None, None, both
-        q._ptrs = (at, at + codes, None if tensor_scale is None else tensor_scale.data_ptr())
+        q._ptrs = (at, at + -(-rows // 128) * -(-cols // 128) * 8192,
+                   None if tensor_scale is None else tensor_scale.data_ptr())
         return q
 
     def _views(self):
@@ -100,6 +105,11 @@ def mx4_quantize(x, fmt: str = "nvfp4", *, tensor_scale=None, stream=None) -> Mx
     ``tensor_scale`` (nvfp4 only) is one positive float32 on the device: usually
     amax(x) / (6 * 448), which puts the largest block scale at the top of e4m3."""
     code = _format(fmt)
+    if stream is None:
+        both = _t.fast().mx4_quantize(x, code, tensor_scale)
+        if both is not None:
+            _t.checked(both, "sgemm_mx4_quantize")
+            return Mx4._of(both, *x.shape, fmt, tensor_scale)
     _t.cuda_tensor(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
@@ -123,6 +133,11 @@ def mx4_dequantize(q: Mx4, dtype=torch.float32, out=None, *, stream=None):
     """The rows x cols numbers that `q` holds, rounded once to `dtype` (or into ``out``)."""
     if not isinstance(q, Mx4):
         raise TypeError("q must be an Mx4")
+    if stream is None and out is None and _t.current(q.device):
+        out = _t.fast().mx4_dequantize(q._ptrs, q.rows, q.cols, FORMATS[q.fmt],
+                                       _t.dtype_code(dtype, "dtype"))
+        _t.checked(out, "sgemm_mx4_dequantize")
+        return out
     call = _t.Call(q.device, stream)
     if out is None:
         dt, ld = _t.dtype_code(dtype, "dtype"), max(q.cols, 1)
@@ -151,6 +166,11 @@ def mx4_matmul(a: Mx4, b: Mx4, out=None, *, dtype=torch.float32, alpha: float = 
     if a.device != b.device:
         raise ValueError(f"a and b must be on one device: {a.device}, {b.device}")
     M, N = a.rows, b.rows
+    if stream is None and out is None and beta == 0.0 and _t.current(a.device):
+        out = _t.fast().mx4_matmul(a._ptrs, b._ptrs, M, N, a.cols, FORMATS[a.fmt], alpha,
+                                   _t.dtype_code(dtype, "dtype"))
+        _t.checked(out, "sgemm_mx4_matmul")
+        return out
     call = _t.Call(a.device, stream)
     if out is None:
         if beta != 0.0:

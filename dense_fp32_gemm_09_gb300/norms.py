@@ -52,9 +52,21 @@ def _gate(gate, x):
     return _t.matrix(gate, "gate", x.shape, x.dtype, x.device)
 
 
-def _forward(call, x, block, weight, gate, scale, eps, next_norm, next_weight, quantize,
+def _forward(stream, x, block, weight, gate, scale, eps, next_norm, next_weight, quantize,
              tensor_scale):
-    rows, cols, dt, ldr = _rows(x, "residual" if block is not None else "x")
+    if stream is None:
+        fmt = NOT_QUANTIZED if quantize is None else _mx4._format(quantize)
+        out = _t.fast().norm_forward(x, block, weight, gate, scale, eps, next_norm, next_weight,
+                                     fmt, tensor_scale)
+        if out is not None:
+            _t.checked(out, "sgemm_norm_forward")
+            if quantize is None:
+                return out
+            y, rstd, both, next_rstd = out
+            return y, rstd, _mx4.Mx4._of(both, *x.shape, quantize, tensor_scale), next_rstd
+    name = "residual" if block is not None else "x"
+    call = _t.Call(_t.cuda_tensor(x, name).device, stream)
+    rows, cols, dt, ldr = _rows(x, name)
     ldb = 0 if block is None else _t.matrix(block, "block", x.shape, x.dtype, x.device)
     wt = _weights(cols, x, ("weight", weight), ("next_weight", next_weight))
     ldg = _gate(gate, x)
@@ -88,8 +100,7 @@ def norm_before(x, weight=None, *, eps: float = 1e-6, quantize: str | None = Non
     (mean(x^2) + eps)^-1/2 per row.  ``x`` is a 2-D float32, bfloat16 or float16 CUDA view
     with unit column stride; ``weight`` (cols,) is float32 or of x's type.  With
     ``quantize="nvfp4"`` or ``"mxfp4"`` h is an ``Mx4``, quantised from float32."""
-    call = _t.Call(_t.cuda_tensor(x, "x").device, stream)
-    _, _, h, rstd = _forward(call, x, None, None, None, 1.0, eps, True, weight, quantize,
+    _, _, h, rstd = _forward(stream, x, None, None, None, 1.0, eps, True, weight, quantize,
                              tensor_scale)
     return h, rstd
 
@@ -103,20 +114,27 @@ def norm_after(block, residual, weight=None, *, gate=None, scale: float = 1.0, e
     With ``next_norm`` (implied by ``next_weight`` or ``quantize``) the norm before the
     next block runs in the same pass: (y, rstd, h, next_rstd), with h as in
     ``norm_before`` and computed from y before it is rounded."""
-    call = _t.Call(_t.cuda_tensor(residual, "residual").device, stream)
-    _t.cuda_tensor(block, "block")
+    if block is None:
+        raise TypeError("block must be a torch.Tensor")
     if next_norm is None:
         next_norm = next_weight is not None or quantize is not None
     elif not next_norm and (next_weight is not None or quantize is not None):
         raise ValueError("next_weight and quantize need the next norm")
     if not next_norm and tensor_scale is not None:
         raise ValueError("tensor_scale goes with quantize='nvfp4'")
-    out = _forward(call, residual, block, weight, gate, scale, eps, next_norm, next_weight,
+    out = _forward(stream, residual, block, weight, gate, scale, eps, next_norm, next_weight,
                    quantize, tensor_scale)
     return out if next_norm else out[:2]
 
 
-def _backward(call, ref, dy, dh, y, next_rstd, next_weight, block, rstd, weight, gate, scale):
+def _backward(stream, ref, dy, dh, y, next_rstd, next_weight, block, rstd, weight, gate, scale):
+    if stream is None:
+        out = _t.fast().norm_backward(ref, dy, dh, y, next_rstd, next_weight, block, rstd, weight,
+                                      gate, scale)
+        if out is not None:
+            _t.checked(out, "sgemm_norm_backward")
+            return out
+    call = _t.Call(_t.cuda_tensor(ref, "dy" if dy is not None else "dh").device, stream)
     rows, cols, dt, _ = _rows(ref, "dy" if dy is not None else "dh")
     check = lambda t, name: 0 if t is None else _t.matrix(t, name, ref.shape, ref.dtype, ref.device)
     lddy, lddh, ldy, ldb = check(dy, "dy"), check(dh, "dh"), check(y, "y"), check(block, "block")
@@ -148,9 +166,9 @@ def norm_before_backward(dh, x, rstd, weight=None, *, dy=None, stream=None):
     """(dx, dweight) of ``norm_before`` from the gradient of h; ``dy``, the gradient that
     reaches x past the block, is added to dx in the same pass.  dweight is float32 (None
     without a weight)."""
-    call = _t.Call(_t.cuda_tensor(dh, "dh").device, stream)
-    _t.cuda_tensor(x, "x")
-    dx, _, _, _, dw = _backward(call, dh, dy, dh, x, rstd, weight, None, None, None, None, 1.0)
+    if dh is None or x is None or rstd is None:
+        raise TypeError("dh, x and rstd must be torch.Tensors")
+    dx, _, _, _, dw = _backward(stream, dh, dy, dh, x, rstd, weight, None, None, None, None, 1.0)
     return dx, dw
 
 
@@ -164,11 +182,11 @@ def norm_after_backward(dy, block, rstd, weight=None, *, gate=None, scale: float
     and of a shared gate are float32 sums over the rows, in a fixed order; what was not
     given has the gradient None."""
     ref = dy if dy is not None else dh
-    call = _t.Call(_t.cuda_tensor(ref, "dy").device, stream)
-    _t.cuda_tensor(block, "block")
+    if ref is None or block is None or rstd is None:
+        raise TypeError("block, rstd and one of dy and dh must be torch.Tensors")
     if dh is None and (y is not None or next_rstd is not None or next_weight is not None):
         raise ValueError("y, next_rstd and next_weight go with dh")
     if dh is not None and (y is None or next_rstd is None):
         raise ValueError("dh needs y and next_rstd")
-    out = _backward(call, ref, dy, dh, y, next_rstd, next_weight, block, rstd, weight, gate, scale)
+    out = _backward(stream, ref, dy, dh, y, next_rstd, next_weight, block, rstd, weight, gate, scale)
     return out if dh is not None else (dy,) + out[1:]
