@@ -37,37 +37,76 @@ __device__ __forceinline__ bool task_of(int rows, int quads, Task* t) {
     return r0 < rows;
 }
 
-template <typename T, int FORMAT>
+// Eight consecutive elements as they are stored.
+template <typename T>
+struct Eight {
+    uint4 raw[sizeof(T) / 2];
+    // VEC: whole groups of eight, 16-byte aligned; else any alignment, zeros from `left` on.
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T* p, int left) {
+        if (VEC) {
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+                raw[i] = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p) + i)
+                                  : make_uint4(0, 0, 0, 0);
+        } else {
+            alignas(16) T t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = i < left ? __ldg(p + i) : T(0.0f);
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+                raw[i] = reinterpret_cast<const uint4*>(t)[i];
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_float(reinterpret_cast<const T*>(raw)[i]);
+    }
+};
+
+template <typename T, int FORMAT, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) quantize_kernel(
-    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks, int vec,
+    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
     const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ scales) {
     Task t;
     const bool any = task_of(rows, chunks / 4, &t);
     wait_previous();
     if (!any) return;
-    const float ts = FORMAT == kNvfp4 && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+    const TensorScale ts(FORMAT == kNvfp4 ? tensor_scale : nullptr);
     uint32_t word[4][2] = {};      // four scale bytes of [quarter][half of the columns]
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    const long long r0 = t.row - (threadIdx.x & 31) / 4;
+    // The next quarter's rows are on their way while this one's are divided.
+    Eight<T> ahead[4];
+    auto load = [&](int j) {
         const long long row = t.row + 32 * j;
-        if (t.row - (threadIdx.x & 31) / 4 + 32 * j >= rows) break;     // the whole warp
-        const bool live = row < rows;
-        float x[4][8];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int k = t.quad * 128 + c * 32 + t.q * 8;
-            load8(X + (live ? row : 0) * ldx + k, vec, live ? cols - k : 0, x[c]);
+            ahead[c].template load<VEC>(X + (row < rows ? row : 0) * ldx + k, row < rows ? cols - k : 0);
         }
+    };
+    load(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const long long row = t.row + 32 * j;
+        if (r0 + 32 * j >= rows) break;                                 // the whole warp
+        const bool live = row < rows;
+        Eight<T> now[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) now[c] = ahead[c];
+        if (j < 3 && r0 + 32 * (j + 1) < rows) load(j + 1);
         uint32_t mine = 0;          // this lane's block of each 32 columns
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            uint32_t amax = magnitude8(x[c]);
+            float x[8];
+            now[c].get(x);
+            uint32_t amax = magnitude8(x);
             amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            const uint32_t byte = block_scale<FORMAT>(amax, 6.0f * ts);
+            const uint32_t byte = block_scale<FORMAT>(amax, ts);
             mine |= byte << (8 * c);
-            const uint32_t packed = Divider<FORMAT>(byte, ts).codes(x[c]);
+            const uint32_t packed = Divider<FORMAT>(byte, ts).codes(x);
             if (live)
                 *reinterpret_cast<uint32_t*>(codes + code_offset(row, 4 * t.quad + c, chunks) +
                                              4 * t.q) = packed;
@@ -148,7 +187,7 @@ __global__ void __launch_bounds__(128) quantize_transposed_kernel(
     const long long row = rb * 128 + threadIdx.x;
     wait_previous();
     if (row >= rows) return;
-    const float ts = FORMAT == kNvfp4 && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+    const TensorScale ts(FORMAT == kNvfp4 ? tensor_scale : nullptr);
     uint32_t word = 0;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -164,7 +203,7 @@ __global__ void __launch_bounds__(128) quantize_transposed_kernel(
         for (int b = 0; b < 2; ++b) {
             uint32_t amax = max(m[2 * b], m[2 * b + 1]);
             if (FORMAT == kMxfp4) amax = max(max(m[0], m[1]), max(m[2], m[3]));
-            const uint32_t byte = block_scale<FORMAT>(amax, 6.0f * ts);
+            const uint32_t byte = block_scale<FORMAT>(amax, ts);
             const Divider<FORMAT> by(byte, ts);
             packed[2 * b] = by.codes(x[2 * b]);
             packed[2 * b + 1] = by.codes(x[2 * b + 1]);
@@ -203,10 +242,12 @@ cudaError_t quantize_launch(const Mx4Quantize& q, cudaStream_t stream) {
                                 q.rows, q.cols, chunks, q.tensor_scale, q.codes, q.scales);
     }
     if (!fits_grid(row_blocks(q.rows) * (chunks / 4))) return cudaErrorInvalidConfiguration;
-    const int vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && q.ldx * sizeof(T) % 16 == 0;
-    return launch_dependent(quantize_kernel<T, FORMAT>, dim3(task_blocks(q.rows, chunks)),
-                            32 * kWarps, 0, stream, X, q.ldx, q.rows, q.cols, chunks, vec,
-                            q.tensor_scale, q.codes, q.scales);
+    const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && q.cols % 8 == 0 &&
+                     (q.rows == 1 || q.ldx * sizeof(T) % 16 == 0);
+    return launch_dependent(vec ? quantize_kernel<T, FORMAT, true>
+                                : quantize_kernel<T, FORMAT, false>,
+                            dim3(task_blocks(q.rows, chunks)), 32 * kWarps, 0, stream, X, q.ldx,
+                            q.rows, q.cols, chunks, q.tensor_scale, q.codes, q.scales);
 }
 
 template <typename T, int FORMAT>

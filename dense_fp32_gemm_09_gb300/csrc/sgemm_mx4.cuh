@@ -107,38 +107,65 @@ __device__ __forceinline__ float scale_decode(uint32_t byte) {
     return FORMAT == kNvfp4 ? e4m3_decode(byte) : e8m0_decode(byte);
 }
 
+__device__ __forceinline__ float reciprocal(float v) {      // within an ulp
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+static __device__ __noinline__ float quotient(float x, float d) { return __fdiv_rn(x, d); }
+
+// x / d correctly rounded from r, the reciprocal of d to an ulp: q0 = x r, then
+// q0 - r (q0 d - x), whose remainder an FMA gives exactly (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000", 1990).  Three instructions instead of
+// a division, which alone would take longer than the memory.  x and the quotient must
+// be far from the ends of the range; the signs keep a quotient of -0.
+__device__ __forceinline__ float divide(float x, float d, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(q, d, -x), -r, q);
+}
+
+// The scale of a whole tensor, and what finding block scales with it needs.
+struct TensorScale {
+    float ts, six, r, cap;
+    bool usual;
+    __device__ __forceinline__ explicit TensorScale(const float* p) {
+        ts = p ? __ldg(p) : 1.0f;
+        six = 6.0f * ts;
+        usual = six > 0x1p-90f && six < 0x1p90f;
+        r = reciprocal(six);
+        cap = 512.0f * six;
+    }
+};
+
 // The scale byte of a block whose largest magnitude has the fp32 bits `amax` (the
 // largest of the magnitudes' bits, which is above 0x7f7fffff if any is infinite or
 // NaN: the scale is then a NaN, and with it every number of the block).
 //   nvfp4: amax / (6 ts) to e4m3, so that the largest code is about 6
 //   mxfp4: 2^(floor(log2 amax) - 2), which puts it in [4, 8); 6 and above saturate
 template <int FORMAT>
-__device__ __forceinline__ uint32_t block_scale(uint32_t amax, float six_ts) {
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax, const TensorScale& t) {
     if (FORMAT == kNvfp4) {
         if (amax > 0x7F7FFFFFu) return 0x7Fu;
-        return e4m3_encode(__fdiv_rn(__uint_as_float(amax), six_ts));
+        const float a = __uint_as_float(amax);
+        // Above 448 every quotient gives 448, so one past 512 may as well be 512.
+        if (t.usual) return e4m3_encode(divide(fminf(a, t.cap), t.six, t.r));
+        return e4m3_encode(quotient(a, t.six));
     }
     const uint32_t e = amax >> 23;
     return e == 255 ? 255u : e < 2 ? 0u : e - 2;
 }
 
 // How numbers of a block are divided by its scale d = value of `byte` (* ts), correctly
-// rounded.  mxfp4: times 2^-e, exact.  nvfp4: q0 = x r with r = 1/d correctly rounded,
-// then q0 - r (q0 d - x), whose remainder an FMA gives exactly (P. Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000", 1990); three instructions instead
-// of a division, which alone would take longer than the memory.  Where the remainder could
-// leave the normal range, or the quotient any (a scale at the top of e4m3), it is the
-// division itself.
-static __device__ __noinline__ float quotient(float x, float d) { return __fdiv_rn(x, d); }
-
+// rounded.  mxfp4: times 2^-e, exact.  nvfp4: divide() where the remainder stays in the
+// normal range and the quotient finite (a scale below the top of e4m3), else a division.
 template <int FORMAT>
 struct Divider {
     float d, r;
     bool fast;
-    __device__ __forceinline__ Divider(uint32_t byte, float ts) {
+    __device__ __forceinline__ Divider(uint32_t byte, const TensorScale& t) {
         if (FORMAT == kNvfp4) {
-            d = e4m3_decode(byte) * ts;
-            r = __frcp_rn(d);
+            d = e4m3_decode(byte) * t.ts;
+            r = reciprocal(d);
             fast = d > 0x1p-90f && d < 0x1p90f && byte < 0x7Eu;
         } else {
             d = 0.0f;
@@ -156,10 +183,7 @@ struct Divider {
         }
         if (fast) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q = x[i] * r;
-                v[i] = fmaf(fmaf(q, d, -x[i]), -r, q);     // these signs keep -0
-            }
+            for (int i = 0; i < 8; ++i) v[i] = divide(x[i], d, r);
             return encode8(v);
         }
         if (d == 0.0f) return 0u;

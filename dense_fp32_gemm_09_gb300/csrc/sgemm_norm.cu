@@ -68,7 +68,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_forward_wide(const NormForward p) {
     const int D = p.cols;
     wait_previous();
-    const float ts = p.tensor_scale ? __ldg(p.tensor_scale) : 1.0f;
+    const TensorScale scale(p.tensor_scale);
+    const float ts = scale.ts;
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T* b = static_cast<const T*>(p.block) + row * p.ldb;
         const T* res = static_cast<const T*>(p.residual) + row * p.ldr;
@@ -114,8 +115,8 @@ __global__ void __launch_bounds__(kThreads) norm_forward_wide(const NormForward 
             for (int j = 0; j < B; ++j)
                 if (i * B + j < D) amax = max(amax, __float_as_uint(h(i * B + j)) & 0x7FFFFFFFu);
             const bool nv = p.format == kNvfp4;
-            const uint32_t byte = nv ? block_scale<kNvfp4>(amax, 6.0f * ts)
-                                     : block_scale<kMxfp4>(amax, 1.0f);
+            const uint32_t byte = nv ? block_scale<kNvfp4>(amax, scale)
+                                     : block_scale<kMxfp4>(amax, scale);
             const float d = nv ? e4m3_decode(byte) * ts : e8m0_decode(byte);
             p.scales[scale_offset(row, i, groups)] = static_cast<uint8_t>(byte);
             for (int j = 0; j < B; j += 8) {

@@ -283,13 +283,14 @@ __device__ __forceinline__ void ring_clear(const Ring& g, uint8_t* smem) {
 // Whole warps with consecutive v: four lanes take 32 columns, as in quantisation.
 template <int FORMAT>
 __device__ __forceinline__ void quantize8(const float (&x)[8], int v, int chunks, int groups,
-                                          const NormForward& p, long long row, float ts) {
+                                          const NormForward& p, long long row,
+                                          const TensorScale& ts) {
     const int lane = threadIdx.x & 31;
     const bool live = v < 4 * chunks;
     uint32_t amax = magnitude8(x);
     amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
     if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    const uint32_t byte = block_scale<FORMAT>(amax, 6.0f * ts);
+    const uint32_t byte = block_scale<FORMAT>(amax, ts);
     const uint32_t packed = Divider<FORMAT>(byte, ts).codes(x);
     if (live)
         *reinterpret_cast<uint32_t*>(p.codes + code_offset(row, v >> 2, chunks) + 4 * (v & 3)) =
@@ -306,7 +307,7 @@ __device__ __forceinline__ void quantize8(const float (&x)[8], int v, int chunks
 // A row of fp32 numbers in shared memory (zeros past its end).
 template <int FORMAT>
 __device__ __forceinline__ void quantize_row(const float* h, const NormForward& p, long long row,
-                                             float ts) {
+                                             const TensorScale& ts) {
     const int chunks = chunks_of(p.cols), groups = groups_of(p.cols, FORMAT);
     const int lane = threadIdx.x & 31;
     // Whole warps: chunks is a multiple of 4 and a warp takes 8.
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(1024, 1)
     ring_clear(ring, smem);
     __syncthreads();
     wait_previous();
-    const float ts = p.tensor_scale ? __ldg(p.tensor_scale) : 1.0f;
+    const TensorScale ts(p.tensor_scale);
     const bool gate_rows = p.gate && p.ldg;
     RowLoop loop{ring, smem, bars, &abort_s, blockIdx.x, p.rows};
     BlockSum block_sum{part};
