@@ -132,11 +132,15 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_kernel(
     launch_next();
 }
 
-template <typename T, int FORMAT>
+// VEC: rows of Y are whole 16-byte groups of eight; else each warp lays its eight rows out in
+// shared memory, so that its stores are contiguous whatever the alignment (3001 x 1999: a
+// store of eight scattered pieces a lane took 30 us, @@ so).
+template <typename T, int FORMAT, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-    const float* __restrict__ tensor_scale, int rows, int cols, int chunks, int vec,
-    T* __restrict__ Y, long long ldy) {
+    const float* __restrict__ tensor_scale, int rows, int cols, int chunks, T* __restrict__ Y,
+    long long ldy) {
+    __shared__ __align__(16) T staged[VEC ? 1 : kWarps][8][VEC ? 8 : 136];
     Task t;
     const bool any = task_of(rows, chunks / 4, &t);
     wait_previous();
@@ -149,10 +153,12 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
     for (int g = 0; g < kGroups; ++g)
         words[g] = __ldg(reinterpret_cast<const uint4*>(
             scales + scale_offset(t.row, 4 * (t.quad * kGroups + g), groups)));
+    const int lane = threadIdx.x & 31, r8 = lane >> 2;
+    const long long r0 = t.row - r8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const long long row = t.row + 32 * j;
-        if (row >= rows) break;
+        if (r0 + 32 * j >= rows) break;                                 // the whole warp
         uint32_t packed[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -168,9 +174,21 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
             decode8(packed[c], v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = v[i] * s * ts;
-            const int k = t.quad * 128 + c * 32 + t.q * 8;
-            store8(Y + row * ldy + k, vec, cols - k, v);
+            const int k = c * 32 + t.q * 8;
+            if (!VEC) store8(&staged[threadIdx.x >> 5][r8][k], true, 8, v);
+            else if (row < rows && t.quad * 128 + k < cols)
+                store8(Y + row * ldy + t.quad * 128 + k, true, 8, v);
         }
+        if (VEC) continue;
+        __syncwarp();
+        for (int r = 0; r < 8 && r0 + 32 * j + r < rows; ++r) {
+            T* y = Y + (r0 + 32 * j + r) * ldy + t.quad * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t.quad * 128 + 32 * i + lane < cols)
+                    y[32 * i + lane] = staged[threadIdx.x >> 5][r][32 * i + lane];
+        }
+        __syncwarp();
     }
     launch_next();
 }
@@ -254,10 +272,13 @@ template <typename T, int FORMAT>
 cudaError_t dequantize_launch(const Mx4Dequantize& q, cudaStream_t stream) {
     const int chunks = chunks_of(q.cols);
     if (!fits_grid(row_blocks(q.rows) * (chunks / 4))) return cudaErrorInvalidConfiguration;
-    const int vec = reinterpret_cast<uintptr_t>(q.Y) % 16 == 0 && q.ldy * sizeof(T) % 16 == 0;
-    return launch_dependent(dequantize_kernel<T, FORMAT>, dim3(task_blocks(q.rows, chunks)),
-                            32 * kWarps, 0, stream, q.codes, q.scales, q.tensor_scale, q.rows,
-                            q.cols, chunks, vec, static_cast<T*>(q.Y), q.ldy);
+    const bool vec = reinterpret_cast<uintptr_t>(q.Y) % 16 == 0 && q.cols % 8 == 0 &&
+                     (q.rows == 1 || q.ldy * sizeof(T) % 16 == 0);
+    return launch_dependent(vec ? dequantize_kernel<T, FORMAT, true>
+                                : dequantize_kernel<T, FORMAT, false>,
+                            dim3(task_blocks(q.rows, chunks)), 32 * kWarps, 0, stream, q.codes,
+                            q.scales, q.tensor_scale, q.rows, q.cols, chunks,
+                            static_cast<T*>(q.Y), q.ldy);
 }
 
 template <typename Q, typename F, typename H, typename B>

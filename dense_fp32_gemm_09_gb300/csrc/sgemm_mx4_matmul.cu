@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sgemm_mx4_tc.cuh"
 
@@ -49,6 +50,26 @@ template <int FORMAT, int BQ> constexpr int kStageBytes =
     kSlabChunks * (2048 + BQ * 16) + 2 * kSlabGroups<FORMAT> * 512;
 // Tensor-memory columns of a stage's scales: four per 128 rows and group.
 template <int FORMAT> constexpr int kStageCols = 8 * kSlabGroups<FORMAT>;
+
+// Shared memory of the cluster's CTA `rank` at this CTA's address `at`.
+__device__ __forceinline__ uint32_t cluster_address(uint32_t at, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t at, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_address(at, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t at, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y) : "r"(cluster_address(at, rank)) : "memory");
+    return v;
+}
 
 // grid: tiles x split CTAs; clusters of split.
 template <int FORMAT, int BQ>
@@ -190,7 +211,9 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
         tmem_ld16(mine + j, v);
         if (pl.split > 1) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(j + i) * 128 + threadIdx.x] = v[i];
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(part + ((j + i) * 128 + 4 * threadIdx.x)) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else if (ok && n < p.N) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -208,19 +231,54 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     if (pl.split > 1) {
         cluster_arrive();
         cluster_wait();
-        const int own = BQ / pl.split;     // rank r sums columns [r, r + 1) * own
-        const uint32_t red = su32(part);
-        for (int c = rank * own; c < (rank + 1) * own && m0 + c < p.M; ++c) {
-            float acc = 0.0f;
+        // Rank r sums columns [r, r + 1) * own of the tile, four (or the two that it has) of
+        // a lane at a time: parts lie as [columns / 4][128 lanes][4].
+        const int own = BQ / pl.split, left = static_cast<int>(min(p.M - m0, BQ + 0LL));
+        const uint32_t red = su32(part) + 16 * threadIdx.x;
+        const int end = min((rank + 1) * own, left);
+        if (own >= 4) {
+            const auto sum = [&](auto split) {
+                constexpr int kSplit = decltype(split)::value;
+                constexpr int kOwn = BQ / kSplit, kStep = kOwn < 16 ? kOwn : 16;
+#pragma unroll 1
+                for (int c = rank * kOwn; c < end; c += kStep) {
+                    // All parts of 16 columns at once: a load takes the cluster's latency.
+                    float4 v[kSplit][kStep / 4];
+#pragma unroll
+                    for (int r = 0; r < kSplit; ++r)
+#pragma unroll
+                        for (int i = 0; i < kStep / 4; ++i)
+                            v[r][i] = cluster_load4(red + (c + 4 * i) * 512, r);
+#pragma unroll
+                    for (int i = 0; i < kStep / 4; ++i) {
+#pragma unroll
+                        for (int r = 1; r < kSplit; ++r) {
+                            v[0][i].x += v[r][i].x; v[0][i].y += v[r][i].y;
+                            v[0][i].z += v[r][i].z; v[0][i].w += v[r][i].w;
+                        }
+                        if (!ok || n >= p.N) continue;
+                        const int m = c + 4 * i;
+                        if (m < end) store_c(p, f, v[0][i].x, m0 + m, n);
+                        if (m + 1 < end) store_c(p, f, v[0][i].y, m0 + m + 1, n);
+                        if (m + 2 < end) store_c(p, f, v[0][i].z, m0 + m + 2, n);
+                        if (m + 3 < end) store_c(p, f, v[0][i].w, m0 + m + 3, n);
+                    }
+                }
+            };
+            if (pl.split == 2) sum(std::integral_constant<int, 2>());
+            else if (pl.split == 4) sum(std::integral_constant<int, 4>());
+            else if constexpr (BQ >= 32) sum(std::integral_constant<int, 8>());
+        } else if (rank * own < end) {
+            const int c = rank * own;
+            float2 acc = make_float2(0, 0);
             for (int r = 0; r < pl.split; ++r) {
-                uint32_t remote;
-                float v;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                    : "=r"(remote) : "r"(red + (c * 128 + threadIdx.x) * 4), "r"(r));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-                acc += v;
+                const float2 v = cluster_load2(red + (c & ~3) * 512 + (c & 3) * 4, r);
+                acc.x += v.x; acc.y += v.y;
             }
-            if (ok && n < p.N) store_c(p, f, acc, m0 + c, n);
+            if (ok && n < p.N) {
+                store_c(p, f, acc.x, m0 + c, n);
+                if (c + 1 < left) store_c(p, f, acc.y, m0 + c + 1, n);
+            }
         }
         cluster_arrive();                  // its parts stay until the others have read them
         cluster_wait();
