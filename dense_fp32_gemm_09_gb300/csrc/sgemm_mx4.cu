@@ -1,13 +1,12 @@
 // 4-bit quantisation and its inverse (sgemm_mx4_quantize, sgemm_mx4_dequantize).
 //
-// Both are passes over memory: 2 bytes a bf16 number one way and 0.56 the other.  A warp
-// takes 32 rows of 128 columns, as the rows 8 i + 0..7 of each of the four quarters of a
-// block of 128 rows, because those share the 16-byte pieces of the scale layout.  Four
-// lanes take a row's 32 columns, eight each: a load is 16 bytes a lane (32 for fp32) from
-// eight rows, a store of codes 128 contiguous bytes, and the scales leave as whole 16-byte
-// pieces; a block's largest magnitude costs one shuffle (nvfp4) or two.
-// The transpose needs no exchange: a thread takes one column of X down 64 rows, so that
-// a warp's loads run along X's rows and its stores are 512 contiguous bytes.
+// Both are passes over memory: 2 bytes a bf16 number one way and 0.56 the other, with some
+// ten instructions a number to spare.  A warp takes the same rows of each of the four
+// quarters of a block of 128 rows, because those share the 16-byte pieces of the scale
+// layout: its loads are 16 bytes a lane, its stores of codes contiguous, and the scales
+// leave in whole pieces.
+// The transpose needs no exchange: a thread takes a column of X (two of a 2-byte type) down
+// 64 rows, so that a warp's loads run along X's rows and its stores are contiguous.
 #include <cuda_runtime.h>
 
 #include "sgemm_internal.h"
@@ -21,7 +20,7 @@ using namespace mx4;
 
 constexpr int kWarps = 4;
 
-// A warp's task: rows r0 + 32 j + lane / 4, j < 4, and columns [128 g, 128 g + 128).
+// A warp's task (mxfp4, and reading back): rows r0 + 32 j + lane / 4, j < 4, columns [128 g, 128 g + 128).
 struct Task {
     long long row;     // of j = 0
     int quad, q;       // 128 columns; the lane's eight columns of each 32
@@ -58,23 +57,123 @@ struct Eight {
                 raw[i] = reinterpret_cast<const uint4*>(t)[i];
         }
     }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
+    __device__ __forceinline__ void get(Two (&x)[4]) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_float(reinterpret_cast<const T*>(raw)[i]);
+        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+            Two t[kPairs<T>];
+            unpack(raw[i], t, T());
+#pragma unroll
+            for (int k = 0; k < kPairs<T>; ++k) x[i * kPairs<T> + k] = t[k];
+        }
     }
 };
 
-template <typename T, int FORMAT, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) quantize_kernel(
+// Magnitude bits (as of fp32) of the largest of some stored elements: 2-byte types are compared two at
+// a time before they are widened (the order of the bits is that of the magnitudes).
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T, int N>
+__device__ __forceinline__ uint32_t magnitude(const uint4 (&raw)[N]) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            m = max(max(max(m, raw[i].x & 0x7FFFFFFFu), max(raw[i].y & 0x7FFFFFFFu,
+                                                          raw[i].z & 0x7FFFFFFFu)),
+                    raw[i].w & 0x7FFFFFFFu);
+        return m;
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            m = max_halves(m, max_halves(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu));
+            m = max_halves(m, max_halves(raw[i].z & 0x7FFF7FFFu, raw[i].w & 0x7FFF7FFFu));
+        }
+        const uint16_t top = static_cast<uint16_t>(max(m >> 16, m & 0xFFFFu));
+        return __float_as_uint(to_float(*reinterpret_cast<const T*>(&top)));
+    }
+}
+
+// nvfp4: a lane takes whole blocks of 16 columns, so that a scale is found once and without
+// an exchange.  A warp takes 64 rows (16 i + 0..15 of each quarter of 128) of 64 columns,
+// two lanes to 32 columns of a row.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps) quantize_nv_kernel(
     const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
     const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
     uint8_t* __restrict__ scales) {
+    const int groups = chunks / 2, lane = threadIdx.x & 31, q = lane & 1;
+    const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const long long band = id / groups;              // 2 a block of 128 rows
+    const int group = static_cast<int>(id - band * groups);
+    const long long r0 = (band >> 1) * 128 + (band & 1) * 16;
+    wait_previous();
+    if (r0 >= rows) return;
+    const TensorScale ts(tensor_scale);
+    Eight<T> ahead[2][2];
+    auto load = [&](int j) {
+        const long long row = r0 + 32 * j + (lane >> 1);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = group * 64 + c * 32 + q * 16 + 8 * h;
+                ahead[c][h].template load<VEC>(X + (row < rows ? row : 0) * ldx + k,
+                                               row < rows ? cols - k : 0);
+            }
+    };
+    load(0);
+    uint32_t word[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (r0 + 32 * j >= rows) break;                                 // the whole warp
+        const long long row = r0 + 32 * j + (lane >> 1);
+        Eight<T> now[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) now[c][h] = ahead[c][h];
+        if (j < 3 && r0 + 32 * (j + 1) < rows) load(j + 1);
+        uint32_t mine = 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t byte = block_scale<kNvfp4>(
+                max(magnitude<T>(now[c][0].raw), magnitude<T>(now[c][1].raw)), ts);
+            mine |= byte << (16 * c);
+            const Divider<kNvfp4> by(byte, ts);
+            Two x[4];
+            now[c][0].get(x);
+            const uint32_t low = by.codes(x);
+            now[c][1].get(x);
+            const uint32_t high = by.codes(x);
+            if (row < rows)
+                *reinterpret_cast<uint2*>(codes + code_offset(row, 2 * group + c, chunks) + 8 * q) =
+                    make_uint2(low, high);
+        }
+        // The lanes' blocks alternate: first, second of 32 columns, then of the next 32.
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+        word[j] = q ? other | mine << 8 : mine | other << 8;
+    }
+    if (q == 0)
+        *reinterpret_cast<uint4*>(scales + scale_offset(r0 + (lane >> 1), 4 * group, groups)) =
+            make_uint4(word[0], word[1], word[2], word[3]);
+    launch_next();
+}
+
+// mxfp4: four lanes take a row's 32 columns, eight each, a warp 32 rows of 128 columns.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps) quantize_mx_kernel(
+    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
     Task t;
     const bool any = task_of(rows, chunks / 4, &t);
     wait_previous();
     if (!any) return;
-    const TensorScale ts(FORMAT == kNvfp4 ? tensor_scale : nullptr);
-    uint32_t word[4][2] = {};      // four scale bytes of [quarter][half of the columns]
+    const TensorScale one(nullptr);
+    uint32_t word[4] = {};         // a row's four scale bytes, of each quarter
     const long long r0 = t.row - (threadIdx.x & 31) / 4;
     // The next quarter's rows are on their way while this one's are divided.
     Eight<T> ahead[4];
@@ -91,50 +190,59 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_kernel(
     for (int j = 0; j < 4; ++j) {
         const long long row = t.row + 32 * j;
         if (r0 + 32 * j >= rows) break;                                 // the whole warp
-        const bool live = row < rows;
         Eight<T> now[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) now[c] = ahead[c];
         if (j < 3 && r0 + 32 * (j + 1) < rows) load(j + 1);
-        uint32_t mine = 0;          // this lane's block of each 32 columns
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            float x[8];
-            now[c].get(x);
-            uint32_t amax = magnitude8(x);
+            uint32_t amax = magnitude<T>(now[c].raw);
             amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-            if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            const uint32_t byte = block_scale<FORMAT>(amax, ts);
-            mine |= byte << (8 * c);
-            const uint32_t packed = Divider<FORMAT>(byte, ts).codes(x);
-            if (live)
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            const uint32_t byte = block_scale<kMxfp4>(amax, one);
+            word[j] |= byte << (8 * c);
+            Two x[4];
+            now[c].get(x);
+            if (row < rows)
                 *reinterpret_cast<uint32_t*>(codes + code_offset(row, 4 * t.quad + c, chunks) +
-                                             4 * t.q) = packed;
-        }
-        if (FORMAT == kNvfp4) {
-            // Lanes 0, 1 of four hold the first block of each 32 columns, 2, 3 the second.
-            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, 2);
-            const uint32_t a = t.q < 2 ? mine : other, b = t.q < 2 ? other : mine;
-            word[j][0] = __byte_perm(a, b, 0x5140);
-            word[j][1] = __byte_perm(a, b, 0x7362);
-        } else {
-            word[j][0] = mine;
+                                             4 * t.q) = Divider<kMxfp4>(byte, one).codes(x);
         }
     }
-    const int groups = groups_of(cols, FORMAT);
-    constexpr int kGroups = FORMAT == kNvfp4 ? 2 : 1;
-    if (t.q < kGroups) {
-        uint8_t* at = scales + scale_offset(t.row, 4 * (t.quad * kGroups + t.q), groups);
-        *reinterpret_cast<uint4*>(at) =
-            t.q == 0 ? make_uint4(word[0][0], word[1][0], word[2][0], word[3][0])
-                     : make_uint4(word[0][1], word[1][1], word[2][1], word[3][1]);
-    }
+    if (t.q == 0)
+        *reinterpret_cast<uint4*>(scales + scale_offset(t.row, 4 * t.quad, chunks / 4)) =
+            make_uint4(word[0], word[1], word[2], word[3]);
     launch_next();
+}
+
+// Eight numbers a lane to consecutive places, by the whole warp.  fp32: neighbours exchange
+// halves, so that a store covers whole 32-byte sectors.
+template <typename T>
+__device__ __forceinline__ void store_whole(T* p, const float (&v)[8], bool live) {
+    if constexpr (sizeof(T) == 4) {
+        const bool odd = threadIdx.x & 1;
+        float4 mine, theirs;
+        float* m = &mine.x;
+        float* t = &theirs.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            t[i] = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[4 + i], 1);
+            m[i] = odd ? v[4 + i] : v[i];
+        }
+        // Lane 2i: its first half and its neighbour's; lane 2i + 1: the second halves.
+        const bool both = __shfl_xor_sync(0xFFFFFFFFu, live, 1);
+        float* at = reinterpret_cast<float*>(p) + (odd ? 4 : 0);
+        if (odd ? both : live)
+            *reinterpret_cast<float4*>(at - (odd ? 8 : 0)) = odd ? theirs : mine;
+        if (odd ? live : both)
+            *reinterpret_cast<float4*>(at + (odd ? 0 : 8)) = odd ? mine : theirs;
+    } else if (live) {
+        store8(p, true, 8, v);
+    }
 }
 
 // VEC: rows of Y are whole 16-byte groups of eight; else each warp lays its eight rows out in
 // shared memory, so that its stores are contiguous whatever the alignment (3001 x 1999: a
-// store of eight scattered pieces a lane took 30 us, @@ so).
+// store of eight scattered pieces a lane took 30 us, this 5.5).
 template <typename T, int FORMAT, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
@@ -176,8 +284,8 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
             for (int i = 0; i < 8; ++i) v[i] = v[i] * s * ts;
             const int k = c * 32 + t.q * 8;
             if (!VEC) store8(&staged[threadIdx.x >> 5][r8][k], true, 8, v);
-            else if (row < rows && t.quad * 128 + k < cols)
-                store8(Y + row * ldy + t.quad * 128 + k, true, 8, v);
+            else store_whole(Y + row * ldy + t.quad * 128 + k, v,
+                             row < rows && t.quad * 128 + k < cols);
         }
         if (VEC) continue;
         __syncwarp();
@@ -240,6 +348,73 @@ __global__ void __launch_bounds__(128) quantize_transposed_kernel(
     launch_next();
 }
 
+// The same for 2-byte types two columns at a time, where X's rows and the number of columns
+// allow 4-byte loads: 64 threads take 128 columns, so a warp loads 128 bytes of a row of X.
+template <typename T, int FORMAT>
+__global__ void __launch_bounds__(128) quantize_transposed2_kernel(
+    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
+    const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+    const int quads = chunks / 4;
+    const long long rb = blockIdx.x / quads;
+    const int pair = 2 * static_cast<int>(blockIdx.x - rb * quads) + (threadIdx.x >> 6);
+    const long long row = rb * 128 + 2 * (threadIdx.x & 63);
+    wait_previous();
+    if (row >= rows) return;
+    const TensorScale ts(FORMAT == kNvfp4 ? tensor_scale : nullptr);
+    const int groups = groups_of(cols, FORMAT);
+    uint32_t word[2] = {};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int k0 = pair * 64 + c * 32;
+        uint32_t w[32], m[2] = {};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            w[i] = k0 + i < cols
+                       ? __ldg(reinterpret_cast<const uint32_t*>(X + (k0 + i) * ldx + row)) : 0u;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m[i / 16] = max_halves(m[i / 16], w[i] & 0x7FFF7FFFu);
+        if (FORMAT == kMxfp4) m[0] = m[1] = max_halves(m[0], m[1]);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {         // the low and the high half: two columns of X
+            uint32_t packed[4];
+            Divider<FORMAT> by(0u, ts);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (e % 2 == 0 && (FORMAT == kNvfp4 || e == 0)) {
+                    const uint16_t top = static_cast<uint16_t>(m[e / 2] >> (16 * s));
+                    const uint32_t byte = block_scale<FORMAT>(
+                        __float_as_uint(to_float(*reinterpret_cast<const T*>(&top))), ts);
+                    by = Divider<FORMAT>(byte, ts);
+                    word[s] |= byte << (8 * (FORMAT == kNvfp4 ? 2 * c + e / 2 : c));
+                }
+                Two x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // Neighbours down the column, as a pair.
+                    const uint32_t v =
+                        __byte_perm(w[8 * e + 2 * i], w[8 * e + 2 * i + 1], s ? 0x7632 : 0x5410);
+                    Two t[4];
+                    unpack(make_uint4(v, 0, 0, 0), t, T());
+                    x[i] = t[0];
+                }
+                packed[e] = by.codes(x);
+            }
+            *reinterpret_cast<uint4*>(codes + code_offset(row + s, 2 * pair + c, chunks)) =
+                make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        if (FORMAT == kNvfp4)
+            *reinterpret_cast<uint32_t*>(scales + scale_offset(row + s, 4 * pair, groups)) = word[s];
+        else
+            *reinterpret_cast<uint16_t*>(scales + scale_offset(row + s, 2 * pair, groups)) =
+                static_cast<uint16_t>(word[s]);
+    }
+    launch_next();
+}
+
 // One warp per band of 32 rows (as above) and 128 columns.
 unsigned task_blocks(int rows, int chunks) {
     const long long full = rows / 128, rest = rows % 128;
@@ -255,6 +430,13 @@ cudaError_t quantize_launch(const Mx4Quantize& q, cudaStream_t stream) {
     if (q.trans) {
         const long long blocks = row_blocks(q.rows) * (chunks / 2);
         if (!fits_grid(blocks)) return cudaErrorInvalidConfiguration;
+        if constexpr (sizeof(T) == 2) {
+            if (q.rows % 2 == 0 && q.ldx % 2 == 0 && reinterpret_cast<uintptr_t>(X) % 4 == 0)
+                return launch_dependent(quantize_transposed2_kernel<T, FORMAT>,
+                                        dim3(static_cast<unsigned>(blocks / 2)), 128, 0, stream, X,
+                                        q.ldx, q.rows, q.cols, chunks, q.tensor_scale, q.codes,
+                                        q.scales);
+        }
         return launch_dependent(quantize_transposed_kernel<T, FORMAT>,
                                 dim3(static_cast<unsigned>(blocks)), 128, 0, stream, X, q.ldx,
                                 q.rows, q.cols, chunks, q.tensor_scale, q.codes, q.scales);
@@ -262,10 +444,17 @@ cudaError_t quantize_launch(const Mx4Quantize& q, cudaStream_t stream) {
     if (!fits_grid(row_blocks(q.rows) * (chunks / 4))) return cudaErrorInvalidConfiguration;
     const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && q.cols % 8 == 0 &&
                      (q.rows == 1 || q.ldx * sizeof(T) % 16 == 0);
-    return launch_dependent(vec ? quantize_kernel<T, FORMAT, true>
-                                : quantize_kernel<T, FORMAT, false>,
+    if (FORMAT == kNvfp4) {
+        const long long full = q.rows / 128, rest = q.rows % 128;
+        const long long tasks = (2 * full + (rest > 16 ? 2 : rest > 0 ? 1 : 0)) * (chunks / 2);
+        return launch_dependent(vec ? quantize_nv_kernel<T, true> : quantize_nv_kernel<T, false>,
+                                dim3(static_cast<unsigned>((tasks + kWarps - 1) / kWarps)),
+                                32 * kWarps, 0, stream, X, q.ldx, q.rows, q.cols, chunks,
+                                q.tensor_scale, q.codes, q.scales);
+    }
+    return launch_dependent(vec ? quantize_mx_kernel<T, true> : quantize_mx_kernel<T, false>,
                             dim3(task_blocks(q.rows, chunks)), 32 * kWarps, 0, stream, X, q.ldx,
-                            q.rows, q.cols, chunks, q.tensor_scale, q.codes, q.scales);
+                            q.rows, q.cols, chunks, q.codes, q.scales);
 }
 
 template <typename T, int FORMAT>

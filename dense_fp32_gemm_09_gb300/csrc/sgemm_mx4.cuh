@@ -55,6 +55,56 @@ template <> __device__ __forceinline__ __half from_float<__half>(float v) {
     return __float2half_rn(v);
 }
 
+// Two fp32 numbers in a register pair, and the packed instructions on them: the passes over
+// memory issue about as many instructions as the memory leaves time for, so halving the
+// arithmetic shows.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float lo, float hi) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ Two twice(float v) { return two(v, v); }
+__device__ __forceinline__ float2 parts(Two v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float sum(Two v) {
+    const float2 f = parts(v);
+    return f.x + f.y;
+}
+
+// 16 bytes of a row as pairs.
+template <typename T> constexpr int kPairs = 8 / sizeof(T);
+__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[2], float) {
+    x[0] = two(__uint_as_float(v.x), __uint_as_float(v.y));
+    x[1] = two(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[4], __nv_bfloat16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)      // a bf16 number is the high half of its fp32 one
+        x[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[4], __half) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        x[i] = two(f.x, f.y);
+    }
+}
 // Eight fp32 numbers to eight codes, ties to even, magnitudes above 6 to 6.
 __device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
     uint32_t r;
@@ -174,22 +224,33 @@ struct Divider {
         }
     }
     // Codes of eight numbers; a scale of 0 has codes 0.
-    __device__ __forceinline__ uint32_t codes(const float (&x)[8]) const {
+    __device__ __forceinline__ uint32_t codes(const Two (&x)[4]) const {
         float v[8];
-        if (FORMAT == kMxfp4) {
+        if (FORMAT == kMxfp4 || fast) {
+            // nvfp4: divide() on pairs, of which this arrangement gives the negative.
+            const Two k = twice(FORMAT == kMxfp4 ? r : -r), dd = twice(d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = x[i] * r;
-            return encode8(v);
-        }
-        if (fast) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = divide(x[i], d, r);
-            return encode8(v);
+            for (int i = 0; i < 4; ++i) {
+                Two q = mul(x[i], k);
+                if (FORMAT == kNvfp4) q = fma(fma(q, dd, x[i]), k, q);
+                const float2 f = parts(q);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+            return FORMAT == kMxfp4 ? encode8(v) : encode8(v) ^ 0x88888888u;
         }
         if (d == 0.0f) return 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = quotient(x[i], d);
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = parts(x[i]);
+            v[2 * i] = quotient(f.x, d);
+            v[2 * i + 1] = quotient(f.y, d);
+        }
         return encode8(v);
+    }
+    __device__ __forceinline__ uint32_t codes(const float (&x)[8]) const {
+        const Two t[4] = {two(x[0], x[1]), two(x[2], x[3]), two(x[4], x[5]), two(x[6], x[7])};
+        return codes(t);
     }
 };
 
@@ -201,22 +262,8 @@ __device__ __forceinline__ uint32_t magnitude8(const float (&x)[8]) {
     return m;
 }
 
-// Eight consecutive elements as fp32: 16-byte loads where `vec` says that p is aligned for
-// them, else one by one; those from `left` on are 0.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, int left, float (&x)[8]) {
-    if (vec && left >= 8) {
-        alignas(16) T t[8];
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-            reinterpret_cast<uint4*>(t)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_float(t[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < left ? to_float(__ldg(p + i)) : 0.0f;
-    }
-}
+// Eight numbers to consecutive elements: 16-byte stores where `vec` says that p is aligned for
+// them, else one by one, `left` at most.
 template <typename T>
 __device__ __forceinline__ void store8(T* p, bool vec, int left, const float (&x)[8]) {
     if (vec && left >= 8) {

@@ -41,7 +41,7 @@ constexpr int kGroup = 8;
 
 struct MatmulPlan {
     Mx4Matmul p;
-    int chunks, slabs, stages, split, tmem_cols, tiles_n, tiles_m;
+    int chunks, slabs, stages, split, tmem_cols, tiles_n, tiles_m, c_vec;
     int* status;
 };
 
@@ -159,6 +159,8 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
             const uint64_t p_desc = operand_desc(smem0, 2048);
             const uint64_t q_desc = operand_desc(smem0 + kP, BQ * 16);
             const uint64_t scales_desc = operand_desc(smem0 + kP + kQ, 128);
+            // A's scales come 128 rows at a time, 32 to a column.
+            const uint32_t q_col = static_cast<uint32_t>(m0 & 127) >> 5;
             int stage = 0;
             uint32_t phase = 0;
             for (int s = first; s < last; ++s) {
@@ -183,7 +185,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
                     const uint32_t id = FORMAT == kNvfp4 ? 0u : 2u * (j & 1);
                     mma<FORMAT, 1>(tmem, p_desc + at + j * 256, q_desc + at + j * 2 * BQ,
                                    mx4_idesc<FORMAT>(128, BQ) | id << 4 | id << 29, sfp + 4 * g,
-                                   sfq + 4 * g, s != first || j != 0);
+                                   sfq + 4 * g + q_col, s != first || j != 0);
                 }
                 commit<1>(su32(&empty_bar[stage]));
                 if (++stage == pl.stages) {
@@ -203,7 +205,10 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     if (p.b_ts) f *= __ldg(p.b_ts);
     const long long n = n0 + threadIdx.x;
     const uint32_t mine = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    // Sums go through shared memory: to the cluster, or (where the ring was: every MMA has
+    // read its stage) to whole lines of C.
     float* const part = reinterpret_cast<float*>(smem + pl.stages * kStageBytes<FORMAT, BQ>);
+    float* const staged = reinterpret_cast<float*>(smem);
 #pragma unroll 1
     for (int j = 0; j < BQ && m0 + j < p.M; j += 16) {
         float v[16];
@@ -214,10 +219,9 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<float4*>(part + ((j + i) * 128 + 4 * threadIdx.x)) =
                     make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        } else if (ok && n < p.N) {
+        } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (m0 + j + i < p.M) store_c(p, f, v[i], m0 + j + i, n);
+            for (int i = 0; i < 16; ++i) staged[(j + i) * 128 + threadIdx.x] = f * v[i];
         }
     }
     // Tensor memory goes back before the cluster is waited for: a CTA that holds some
@@ -228,7 +232,14 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
         fence_after();
         tmem_dealloc<1>(tmem, pl.tmem_cols);
     }
-    if (pl.split > 1) {
+    if (pl.split == 1) {
+        if (ok) {
+            if (p.dtype == kF32) store_rows<float>(p, pl.c_vec, staged, BQ, m0, n0, threadIdx.x);
+            else if (p.dtype == kBf16)
+                store_rows<__nv_bfloat16>(p, pl.c_vec, staged, BQ, m0, n0, threadIdx.x);
+            else store_rows<__half>(p, pl.c_vec, staged, BQ, m0, n0, threadIdx.x);
+        }
+    } else {
         cluster_arrive();
         cluster_wait();
         // Rank r sums columns [r, r + 1) * own of the tile, four (or the two that it has) of
@@ -304,8 +315,15 @@ cudaError_t launch_tile(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     if (tiles > 0x7FFFFFFF / kGroup) return cudaErrorInvalidConfiguration;
     pl.tiles_n = static_cast<int>(tiles_n);
     pl.tiles_m = static_cast<int>(tiles_m);
+    // A K range is split while the CTAs still fit the SMs at once and each keeps four slabs.
+    // Two parts of a 64-wide tile, or any of a 128-wide one, cost more to add up than a range
+    // of less than 8192 saves (64 x 4096 x 4096: 1 part 12.6 us, 2 14.2, 4 11.0;
+    // 256 x 1024 x 8192: 1 part 18.3, 2 16.3).
     pl.split = 1;
-    while (pl.split < 8 && tiles * pl.split * 2 <= sms && pl.split * 2 <= pl.slabs) pl.split *= 2;
+    for (int split = 2; BQ <= 64 && split <= 8; split *= 2)
+        if ((BQ < 64 || split > 2 || pl.slabs >= 32) && tiles * split <= sms && pl.slabs >= 4 * split)
+            pl.split = split;
+    pl.c_vec = c_rows_aligned(p);
     constexpr int kMost = 220 * 1024;
     const int red = pl.split > 1 ? BQ * 512 : 0;
     const int per = (pl.slabs + pl.split - 1) / pl.split;
@@ -316,7 +334,7 @@ cudaError_t launch_tile(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     // No more CTAs to an SM, by their shared memory, than find tensor memory there.
     const int resident = 512 / pl.tmem_cols;
     const int least = 228 * 1024 / (resident + 1);
-    const int smem = std::max(pl.stages * kStageBytes<FORMAT, BQ> + red,
+    const int smem = std::max(std::max(pl.stages * kStageBytes<FORMAT, BQ> + red, BQ * 512),
                               resident == 1 ? 116 * 1024 : least);
     pl.status = status_word_ptr();
     auto kernel = mx4_matmul_kernel<FORMAT, BQ>;
@@ -339,13 +357,18 @@ cudaError_t launch_tile(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&c, kernel, pl);
 }
 
+// Few rows of A take the narrowest tile that holds them.  More take 64 columns where such
+// tiles fit the SMs at once, else 128, and the pairs' 256 x 256 where those do not either
+// (512 x 4096 x 4096 in us: 64 wide 22.3, 128 14.2, pairs 15.1; 2048^3: 128 20.2, pairs
+// 13.8).  Pairs would waste half of a tile on an operand of up to 128 rows.
 template <int FORMAT>
 cudaError_t launch_format(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     if (p.M <= 16) return launch_tile<FORMAT, 16>(p, sms, stream);
     if (p.M <= 32) return launch_tile<FORMAT, 32>(p, sms, stream);
-    if (p.M <= 64) return launch_tile<FORMAT, 64>(p, sms, stream);
-    const long long pair_tiles = ((p.N + 255LL) / 256) * ((p.M + 255LL) / 256);
-    if (p.M > 128 && p.N > 128 && pair_tiles * 4 >= sms) return launch_mx4_pair(p, sms, stream);
+    const long long tn = (p.N + 127LL) / 128;
+    if (p.M <= 64 || tn * ((p.M + 63LL) / 64) <= sms) return launch_tile<FORMAT, 64>(p, sms, stream);
+    if (tn * ((p.M + 127LL) / 128) > sms && p.M > 128 && p.N > 128)
+        return launch_mx4_pair(p, sms, stream);
     return launch_tile<FORMAT, 128>(p, sms, stream);
 }
 

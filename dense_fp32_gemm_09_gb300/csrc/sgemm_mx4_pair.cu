@@ -101,42 +101,6 @@ __device__ __forceinline__ void sync_half(int barrier) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(barrier) : "memory");
 }
 
-// 32 rows of C by 128 columns from the sums staged in shared memory (fp32, row by row) by
-// one half's four warps: 16 bytes a thread, whole 128-byte lines of C.
-template <typename T>
-__device__ __forceinline__ void store_rows(const Mx4Matmul& p, bool c_vec, const float* staged,
-                                           long long m0, long long n0, int me) {
-    constexpr int kVec = 16 / sizeof(T), kPerRow = 128 / kVec, kRows = 128 / kPerRow;
-    const int col = me % kPerRow * kVec;
-    const bool vec = c_vec && n0 + col + kVec <= p.N;
-#pragma unroll 2
-    for (int row = me / kPerRow; row < 32 && m0 + row < p.M; row += kRows) {
-        T* c = static_cast<T*>(p.C) + (m0 + row) * p.ldc + n0 + col;
-        float v[kVec];
-#pragma unroll
-        for (int k = 0; k < kVec; k += 4)
-            *reinterpret_cast<float4*>(v + k) =
-                *reinterpret_cast<const float4*>(staged + row * 128 + col + k);
-        if (vec) {
-            alignas(16) T out[kVec];
-            if (p.beta != 0.0f) {
-                *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(c);
-#pragma unroll
-                for (int k = 0; k < kVec; ++k) v[k] = fmaf(p.beta, to_float(out[k]), v[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) out[k] = from_float<T>(v[k]);
-            *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(out);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) {
-                if (n0 + col + k >= p.N) break;
-                c[k] = from_float<T>(p.beta == 0.0f ? v[k] : fmaf(p.beta, to_float(c[k]), v[k]));
-            }
-        }
-    }
-}
-
 template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mx4_pair_kernel(const PairPlan pl) {
@@ -328,10 +292,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     staged[i * 128 + me] = f * v[j / 2][j % 2 * 32 + i];
                 sync_half(1 + half);
                 const long long m = m0 + 32 * j;
-                if (p.dtype == kF32) store_rows<float>(p, pl.c_vec, staged, m, n0, me);
+                if (p.dtype == kF32) store_rows<float>(p, pl.c_vec, staged, 32, m, n0, me);
                 else if (p.dtype == kBf16)
-                    store_rows<__nv_bfloat16>(p, pl.c_vec, staged, m, n0, me);
-                else store_rows<__half>(p, pl.c_vec, staged, m, n0, me);
+                    store_rows<__nv_bfloat16>(p, pl.c_vec, staged, 32, m, n0, me);
+                else store_rows<__half>(p, pl.c_vec, staged, 32, m, n0, me);
             }
         }
     }
@@ -359,8 +323,7 @@ cudaError_t launch_pair(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     pl.tiles_m = static_cast<int>(tm);
     pl.status = status_word_ptr();
     constexpr int smem = kStages * kStageBytes<FORMAT> + kStageC;
-    const int es = p.dtype == kF32 ? 4 : 2;
-    pl.c_vec = reinterpret_cast<uintptr_t>(p.C) % 16 == 0 && p.ldc * es % 16 == 0;
+    pl.c_vec = c_rows_aligned(p);
     auto kernel = mx4_pair_kernel<FORMAT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

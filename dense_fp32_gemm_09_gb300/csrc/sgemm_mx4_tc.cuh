@@ -220,5 +220,48 @@ __device__ __forceinline__ void store_c(const Mx4Matmul& p, float f, float acc, 
 }
 
 
+// Rows [m0, m0 + rows) of C, columns [n0, n0 + 128), from sums in shared memory (fp32, 128 a
+// row), by 128 threads `me`: 16 bytes each and whole 128-byte lines where C's rows are
+// aligned, else side by side.
+template <typename T>
+__device__ __forceinline__ void store_rows(const Mx4Matmul& p, bool c_vec, const float* staged,
+                                           int rows, long long m0, long long n0, int me) {
+    constexpr int kVec = 16 / sizeof(T), kPerRow = 128 / kVec, kRows = 128 / kPerRow;
+    const int end = static_cast<int>(min(static_cast<long long>(rows), p.M - m0));
+    if (!c_vec || n0 + 128 > p.N) {
+        if (n0 + me >= p.N) return;
+        T* c = static_cast<T*>(p.C) + m0 * p.ldc + n0 + me;
+#pragma unroll 4
+        for (int row = 0; row < end; ++row, c += p.ldc) {
+            const float v = staged[row * 128 + me];
+            *c = from_float<T>(p.beta == 0.0f ? v : fmaf(p.beta, to_float(*c), v));
+        }
+        return;
+    }
+    const int col = me % kPerRow * kVec;
+#pragma unroll 2
+    for (int row = me / kPerRow; row < end; row += kRows) {
+        T* c = static_cast<T*>(p.C) + (m0 + row) * p.ldc + n0 + col;
+        float v[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; k += 4)
+            *reinterpret_cast<float4*>(v + k) =
+                *reinterpret_cast<const float4*>(staged + row * 128 + col + k);
+        alignas(16) T out[kVec];
+        if (p.beta != 0.0f) {
+            *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(c);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[k] = fmaf(p.beta, to_float(out[k]), v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) out[k] = from_float<T>(v[k]);
+        *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(out);
+    }
+}
+inline bool c_rows_aligned(const Mx4Matmul& p) {
+    return reinterpret_cast<uintptr_t>(p.C) % 16 == 0 &&
+           (p.M == 1 || p.ldc * (p.dtype == kF32 ? 4 : 2) % 16 == 0);
+}
+
 }  // namespace mx4
 }  // namespace sgemm

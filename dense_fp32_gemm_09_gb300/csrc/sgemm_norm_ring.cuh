@@ -134,56 +134,7 @@ struct BlockSum {
     }
 };
 
-// Two fp32 numbers in a register pair, and the packed instructions on them: the kernels
-// issue about as many instructions as the memory leaves time for, so halving the
-// arithmetic shows.
-using Two = unsigned long long;
-__device__ __forceinline__ Two two(float lo, float hi) {
-    Two r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ Two twice(float v) { return two(v, v); }
-__device__ __forceinline__ float2 parts(Two v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ Two mul(Two a, Two b) {
-    Two r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-    Two r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ float sum(Two v) {
-    const float2 f = parts(v);
-    return f.x + f.y;
-}
-
-// 16 bytes of a row as pairs, and back.
-template <typename T> constexpr int kPairs = 8 / sizeof(T);
-__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[2], float) {
-    x[0] = two(__uint_as_float(v.x), __uint_as_float(v.y));
-    x[1] = two(__uint_as_float(v.z), __uint_as_float(v.w));
-}
-__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[4], __nv_bfloat16) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)      // a bf16 number is the high half of its fp32 one
-        x[i] = two(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-}
-__device__ __forceinline__ void unpack(const uint4& v, Two (&x)[4], __half) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[i] = two(f.x, f.y);
-    }
-}
+// Pairs to 16 bytes of a row.
 __device__ __forceinline__ uint4 pack(const Two (&x)[2], float) {
     const float2 a = parts(x[0]), b = parts(x[1]);
     return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
