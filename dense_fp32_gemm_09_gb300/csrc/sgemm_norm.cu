@@ -253,11 +253,28 @@ struct RingBuilder {
     void also(const void* p, long long ld) {
         if (p != nullptr && !aligned_to(p, rows > 1 ? ld * elem : 0, 16)) whole = false;
     }
+    bool ragged() const { return align < 16 || !whole || ring.row_bytes % 16 != 0; }
+    // The kernels without a ring: `own` columns a thread, up to `most` threads an SM, `extra`
+    // bytes of shared memory a block.
+    RingShape column_shape(int own, int most, long long extra, int sms) const {
+        RingShape s{};
+        s.by_column = s.fits = true;
+        s.ragged = ragged();
+        s.columns = own;
+        s.most = most;
+        s.threads = 64;
+        while (s.threads * own < cols) s.threads *= 2;
+        s.blocks_per_sm = std::min(most / s.threads, 16);
+        while (s.blocks_per_sm > 1 && s.blocks_per_sm * extra > kSharedPerSm) --s.blocks_per_sm;
+        s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * s.blocks_per_sm));
+        s.smem = static_cast<int>(extra);
+        return s;
+    }
     // `columns`: of a thread, 8 (up to 1024 threads of 64 registers) or more (up to 512 of
     // 128); `least`: threads of a block.
     RingShape shape(int columns, int most, int least, long long extra, int sms) {
         RingShape s{};
-        s.ragged = align < 16 || !whole || ring.row_bytes % 16 != 0;
+        s.ragged = ragged();
         ring.mode = align == 16 && ring.row_bytes % 16 == 0 ? kBulk
                     : align >= 4 && ring.row_bytes % 4 == 0 ? kCopy4 : kPlain;
         s.columns = columns;
@@ -303,15 +320,15 @@ RingBuilder ring_of(const NormBackward& p) {
     return b;
 }
 
-// Sixteen columns a thread where the registers hold their sums (1024 threads an SM for the
-// norm before a block, 512 of 128 registers with the norm after it): what a row costs
-// beside its columns, some 300 instructions a thread, weighs half as much as with eight.
-// fp32 rows take eight, which give more loads in flight: 3001 x 2048 49 against 58 us, but
-// bf16 8192 x 8192 235 against 225.  Rows above 8192 columns take sixteen on 1024 threads,
-// whose sums then spill.
+// Up to 512 threads of 128 registers hold a row's numbers and the sums over rows: eight
+// columns a thread of ragged or fp32 rows, sixteen of 2-byte ones (both norms in us, against
+// the ring: 3001 x 2047 fp32 47 and 67, 3001 x 2048 36 and 50, 8192 x 4096 bf16 106 and 127,
+// 8192 x 8192 with a gate 225 and 233).  Wider rows take the ring, with eight columns a
+// thread on 1024 threads of 64 registers, or sixteen, whose sums then spill.
 RingShape backward_shape(const NormBackward& p, RingBuilder& b, int sms) {
-    if (p.block == nullptr || p.cols > 8 * 1024) return b.shape(16, 1024, 64, 0, sms);
-    return p.dtype == kF32 ? b.shape(8, 1024, 64, 0, sms) : b.shape(16, 512, 64, 0, sms);
+    const int own = b.ragged() || p.dtype == kF32 ? 8 : 16;
+    if (p.cols <= own * 512) return b.column_shape(own, 512, 0, sms);
+    return b.shape(p.dtype == kF32 && p.block && p.cols <= 8 * 1024 ? 8 : 16, 1024, 64, 0, sms);
 }
 
 // Blocks of the backward kernel (each keeps a set of column sums).
@@ -339,10 +356,14 @@ cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stre
     b.also(p.y, p.ldy);
     b.also(p.h, p.ldh);
     // Sixteen columns a thread: 121 against 149 us with eight at 8192 x 8192 with a gate.
-    // Few rows take eight, for latency: 6.7 against 7.7 us for one row of 4096.
+    // Few rows take eight, for latency: 6.7 against 7.7 us for one row of 4096.  Ragged rows
+    // take the kernels without a ring (3001 x 2047 fp32 34 against 43).
     const bool few = p.rows <= 2LL * sms && p.cols <= 8 * 1024;
-    const long long extra = p.format >= 0 && p.dtype == kF32 ? 128LL * chunks_of(p.cols) : 0;
-    const RingShape s = b.shape(few ? 8 : 16, 1024, 32, extra, sms);
+    const long long row_fp32 = p.format >= 0 ? 128LL * chunks_of(p.cols) : 0;
+    const RingShape s =
+        b.ragged() && p.cols <= 8 * 1024
+            ? b.column_shape(8, 1024, row_fp32, sms)
+            : b.shape(few ? 8 : 16, 1024, 32, p.dtype == kF32 || b.ragged() ? row_fp32 : 0, sms);
     if (!s.fits) {
         const dim3 grid(static_cast<unsigned>(p.rows));
         if (p.dtype == kF32)

@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(1024, 1)
 // ----------------------------------------------------------------------------
 // Backward: inputs dy, dh, y, block, gate as far as they are there, in this order
 // ----------------------------------------------------------------------------
-template <typename T, bool RAGGED, int COLS, int THREADS, int WHAT, bool SHARED>
-__global__ void __launch_bounds__(THREADS, 1)
+template <typename T, bool RAGGED, int COLS, int WHAT, bool SHARED>
+__global__ void __launch_bounds__(1024, 1)
     norm_backward_ring(const BackwardPlan pl) {
     constexpr bool kAfter = WHAT != kBefore, kNext = WHAT != kAfterOnly;
     constexpr int VEC = 16 / sizeof(T), P = VEC / 2, N = COLS / VEC;
@@ -605,21 +605,17 @@ cudaError_t forward_what(const ForwardPlan& pl, const RingShape& s, cudaStream_t
     if (!pl.p.next) return launch_ring(norm_forward_ring<T, RAGGED, COLS, kAfterOnly>, pl, s, st);
     return launch_ring(norm_forward_ring<T, RAGGED, COLS, kBoth>, pl, s, st);
 }
-template <typename T, bool RAGGED, int COLS, int THREADS>
+template <typename T, bool RAGGED, int COLS>
 cudaError_t backward_what(const BackwardPlan& pl, const RingShape& s, cudaStream_t st) {
     const bool shared = pl.p.dgate && pl.p.ldg == 0;
-    if (!pl.p.block) {
-        if constexpr (COLS == 16 && THREADS == 1024)
-            return launch_ring(norm_backward_ring<T, RAGGED, 16, 1024, kBefore, false>, pl, s, st);
-        return cudaErrorInvalidConfiguration;
-    }
+    if (!pl.p.block)      // always with sixteen columns
+        return launch_ring(norm_backward_ring<T, RAGGED, 16, kBefore, false>, pl, s, st);
     if (!pl.p.dh)
         return shared
-            ? launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kAfterOnly, true>, pl, s, st)
-            : launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kAfterOnly, false>, pl, s, st);
-    return shared
-        ? launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kBoth, true>, pl, s, st)
-        : launch_ring(norm_backward_ring<T, RAGGED, COLS, THREADS, kBoth, false>, pl, s, st);
+            ? launch_ring(norm_backward_ring<T, RAGGED, COLS, kAfterOnly, true>, pl, s, st)
+            : launch_ring(norm_backward_ring<T, RAGGED, COLS, kAfterOnly, false>, pl, s, st);
+    return shared ? launch_ring(norm_backward_ring<T, RAGGED, COLS, kBoth, true>, pl, s, st)
+                  : launch_ring(norm_backward_ring<T, RAGGED, COLS, kBoth, false>, pl, s, st);
 }
 template <typename T, bool RAGGED>
 cudaError_t forward_rows(const ForwardPlan& pl, const RingShape& s, cudaStream_t st) {
@@ -628,13 +624,9 @@ cudaError_t forward_rows(const ForwardPlan& pl, const RingShape& s, cudaStream_t
 }
 template <typename T, bool RAGGED>
 cudaError_t backward_rows(const BackwardPlan& pl, const RingShape& s, cudaStream_t st) {
-    if (s.columns == 8) {
-        if constexpr (sizeof(T) == 4) return backward_what<T, RAGGED, 8, 1024>(pl, s, st);
-        return cudaErrorInvalidConfiguration;
-    }
-    if (s.most == 1024) return backward_what<T, RAGGED, 16, 1024>(pl, s, st);
-    if constexpr (sizeof(T) == 2) return backward_what<T, RAGGED, 16, 512>(pl, s, st);
-    return cudaErrorInvalidConfiguration;
+    if constexpr (sizeof(T) == 4)
+        if (s.columns == 8) return backward_what<T, RAGGED, 8>(pl, s, st);
+    return backward_what<T, RAGGED, 16>(pl, s, st);
 }
 template <typename T>
 cudaError_t forward_ring(const ForwardPlan& pl, const RingShape& s, cudaStream_t st) {

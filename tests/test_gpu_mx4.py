@@ -56,7 +56,7 @@ def check_stored(q, x, fmt, ts=None):
 
 
 SIZES = [(1, 1), (1, 4096), (3, 31), (5, 32), (127, 33), (128, 128), (129, 257), (300, 1000),
-         (2, 4097), (515, 64)]
+         (2, 4097), (515, 64), (34, 130), (130, 2056), (64, 999), (257, 96), (1000, 130)]
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])

@@ -17,7 +17,7 @@ DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
 HALF_ULP = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
 EPS = 1e-5
 SHAPES = [(1, 1), (1, 4096), (3, 7), (5, 64), (33, 257), (130, 1000), (2, 2048), (4, 8200),
-          (2, 40001), (700, 96), (2, 70000)]
+          (2, 40001), (700, 96), (2, 70000), (330, 4096), (3, 5000), (2, 4100), (5, 12000), (2, 16384)]
 
 
 @pytest.fixture()
@@ -204,7 +204,7 @@ def test_gradient_against_differences(sg):
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("rows,cols", [(1, 4096), (3, 17), (130, 200), (5, 1056), (2, 9000), (2, 70000)])
+@pytest.mark.parametrize("rows,cols", [(1, 4096), (3, 17), (130, 200), (5, 1056), (2, 9000), (2, 70000), (3, 9001), (3, 2056), (400, 512)])
 def test_quantized_output(sg, rows, cols, dtype, fmt):
     """Numbers whose 64-bit quotient is not within 1e-4 of a rounding boundary have the
     reference's value; near one either neighbour is right."""
