@@ -143,6 +143,41 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// stored_addresses(codes, scales, rows, cols, format, tensor_scale) -> (address, address, address or None)
+// of a matrix whose buffers have the right types and shapes
+PyObject* stored_addresses(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        at::Tensor codes, scales, ts;
+        if (n != 6 || !tensor(a[0], &codes) || !tensor(a[1], &scales) || !tensor(a[5], &ts) ||
+            !codes.defined() || !scales.defined())
+            return not_here();
+        const long long rows = PyLong_AsLongLong(a[2]), cols = PyLong_AsLongLong(a[3]);
+        const int format = static_cast<int>(PyLong_AsLong(a[4]));
+        if (PyErr_Occurred()) return nullptr;
+        const long long rb = (rows + 127) / 128, cb = (cols + 127) / 128;
+        const long long groups = cb * (format == SGEMM_NVFP4 ? 2 : 1);
+        if (rows < 0 || cols < 0 || codes.scalar_type() != at::kByte || codes.dim() != 4 ||
+            codes.size(0) != rb || codes.size(1) != 4 * cb || codes.size(2) != 128 ||
+            codes.size(3) != 16 || !codes.is_contiguous() || scales.scalar_type() != at::kByte ||
+            scales.dim() != 5 || scales.size(0) != rb || scales.size(1) != groups ||
+            scales.size(2) != 32 || scales.size(3) != 4 || scales.size(4) != 4 ||
+            !scales.is_contiguous() || !here(codes) || !here(scales) || !one_float(ts, format))
+            return not_here();
+        PyObject* r = PyTuple_New(3);
+        if (!r) return nullptr;
+        const at::Tensor* all[] = {&codes, &scales, &ts};
+        for (int i = 0; i < 3; ++i) {
+            PyObject* o = all[i]->defined() ? PyLong_FromVoidPtr(all[i]->data_ptr()) : nullptr;
+            if (!o) {
+                Py_INCREF(Py_None);
+                o = Py_None;
+            }
+            PyTuple_SET_ITEM(r, i, o);
+        }
+        return r;
+    });
+}
+
 bool address(PyObject* o, const void** p) {
     *p = o == Py_None ? nullptr : PyLong_AsVoidPtr(o);
     return !PyErr_Occurred();
@@ -303,7 +338,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {METHOD(bind), METHOD(mx4_quantize), METHOD(mx4_dequantize),
+PyMethodDef kMethods[] = {METHOD(bind), METHOD(stored_addresses), METHOD(mx4_quantize), METHOD(mx4_dequantize),
                           METHOD(mx4_matmul), METHOD(norm_forward), METHOD(norm_backward),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fast_calls", nullptr, -1, kMethods,

@@ -37,21 +37,22 @@ class Mx4:
                  "_ptrs")
 
     def __init__(self, codes, scales, rows: int, cols: int, fmt: str, tensor_scale=None):
-        _format(fmt)
-        shapes = mx4_shapes(rows, cols, fmt)
-        for t, name, shape in ((codes, "codes", shapes[0]), (scales, "scales", shapes[1])):
-            _t.cuda_tensor(t, name)
-            if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
-        self.device = codes.device
-        _t.same_device(scales, "scales", self.device)
-        if tensor_scale is not None:
-            if fmt != "nvfp4":
-                raise ValueError("only nvfp4 has a tensor scale")
-            _t.one_float(tensor_scale, "tensor_scale", self.device)
+        ptrs = _t.fast().stored_addresses(codes, scales, rows, cols, _format(fmt), tensor_scale)
+        if ptrs is None:          # another device, or something to refuse
+            for t, name, shape in zip((codes, scales), ("codes", "scales"),
+                                      mx4_shapes(rows, cols, fmt)):
+                _t.cuda_tensor(t, name)
+                if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
+            _t.same_device(scales, "scales", codes.device)
+            if tensor_scale is not None:
+                if fmt != "nvfp4":
+                    raise ValueError("only nvfp4 has a tensor scale")
+                _t.one_float(tensor_scale, "tensor_scale", codes.device)
+            ptrs = codes.data_ptr(), scales.data_ptr(), _t.ptr(tensor_scale)
         self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
-        self._codes, self._scales, self._both = codes, scales, None
-        self._ptrs = (codes.data_ptr(), scales.data_ptr(), _t.ptr(tensor_scale))
+        self.device = codes.device
+        self._codes, self._scales, self._both, self._ptrs = codes, scales, None, ptrs
 
     @classmethod
     def _new(cls, call, rows: int, cols: int, fmt: str, tensor_scale):
