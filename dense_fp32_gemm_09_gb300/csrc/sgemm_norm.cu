@@ -29,8 +29,8 @@
 //
 // Measured (us, of the time the bytes take at 6.79 TB/s): the norm after a
 // block and the next one, 8192 x 8192 bf16 with a gate 123 (0.80); before, 8192 x 4096 bf16 33
-// (0.60); before, 8192 x 8192 to nvfp4 84 (0.30, 33 instructions a number); gradient of the
-// norm before a block, 8192 x 4096 bf16 56 (0.70); of both, 8192 x 8192 bf16 with a gate 226
+// (0.60); before, 8192 x 8192 bf16 to nvfp4 65 (0.39); gradient of the norm before a block,
+// 8192 x 4096 bf16 56 (0.70); of both, 8192 x 8192 bf16 with a gate 226
 // (0.70), 3001 x 2047 fp32 47 (0.46).  Gradients run 16 warps an SM at 122 to 128 registers
 // with issue slots 38 to 54 % used.  Streaming kernels, 4096 x 20000 bf16: before 395 (0.12),
 // its gradient 1055 (0.07).
@@ -371,7 +371,9 @@ cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stre
     // Few rows take eight, for latency: 6.7 against 7.7 us for one row of 4096.  Ragged rows
     // take the kernels without a ring (3001 x 2047 fp32 34 against 43).
     const bool few = p.rows <= 2LL * sms && p.cols <= 8 * 1024;
-    const long long row_fp32 = p.format >= 0 ? 128LL * chunks_of(p.cols) : 0;
+    // A row of fp32 numbers on its way to codes, but not in norm_quantize_ring.
+    const bool whole_blocks = !p.block && !few && !b.ragged();
+    const long long row_fp32 = p.format >= 0 && !whole_blocks ? 128LL * chunks_of(p.cols) : 0;
     const RingShape s =
         b.ragged() && p.cols <= 8 * 1024
             ? b.column_shape(8, 1024, row_fp32, sms)

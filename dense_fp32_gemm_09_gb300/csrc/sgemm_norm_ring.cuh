@@ -282,6 +282,7 @@ template <typename T, bool RAGGED, int COLS, int WHAT>
 __global__ void __launch_bounds__(1024, 1)
     norm_forward_ring(const ForwardPlan pl) {
     constexpr bool kAfter = WHAT != kBefore, kNext = WHAT != kAfterOnly;
+    constexpr bool kCodes = kNext && (kAfter || RAGGED || COLS != 16);   // else norm_quantize_ring
     constexpr int VEC = 16 / sizeof(T), P = VEC / 2, N = COLS / VEC;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kMaxStages];
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(1024, 1)
         async::mbar_fence_init();
     }
     const int chunks = chunks_of(D), groups = p.format >= 0 ? groups_of(D, p.format) : 0;
-    if (VEC != 8 && p.format >= 0)
+    if (kCodes && VEC != 8 && p.format >= 0)
         for (int c = D + threadIdx.x; c < 32 * chunks_of(D); c += NT) hrow[c] = 0.0f;
     ring_clear(ring, smem);
     __syncthreads();
@@ -379,9 +380,9 @@ __global__ void __launch_bounds__(1024, 1)
 #pragma unroll
                     for (int j = 0; j < P; ++j) w[j] = mul(mul(u[i][j], rn2), w[j]);
                 }
-                if (p.format < 0) {
+                if (!kCodes || p.format < 0) {
                     if (c < D) put<T, RAGGED>(static_cast<T*>(p.h) + row * p.ldh, c, D, w);
-                } else if constexpr (VEC == 8) {
+                } else if constexpr (kCodes && VEC == 8) {
                     // A thread's eight columns are a lane's in quantisation; the threads
                     // reach past the padded row.
                     float x[8];
@@ -394,17 +395,121 @@ __global__ void __launch_bounds__(1024, 1)
                     const int v = threadIdx.x + i * NT;
                     if (p.format == kNvfp4) quantize8<kNvfp4>(x, v, chunks, groups, p, row, ts);
                     else quantize8<kMxfp4>(x, v, chunks, groups, p, row, ts);
-                } else if (c < D) {
-                    *reinterpret_cast<uint4*>(hrow + c) = pack(w, 0.0f);     // zeros past D
+                } else if constexpr (kCodes && VEC != 8) {
+                    if (c < D) *reinterpret_cast<uint4*>(hrow + c) = pack(w, 0.0f);   // zeros past D
                 }
             }
-            if (VEC != 8 && p.format >= 0) {
+            if (kCodes && VEC != 8 && p.format >= 0) {
                 __syncthreads();
                 if (p.format == kNvfp4) quantize_row<kNvfp4>(hrow, p, row, ts);
                 else quantize_row<kMxfp4>(hrow, p, row, ts);
                 // The next row's sums have a barrier before anything is written to hrow.
             }
         }
+    }
+    launch_next();
+}
+
+// ----------------------------------------------------------------------------
+// The norm before a block, to 4 bits: sixteen consecutive columns a thread
+// ----------------------------------------------------------------------------
+// Quantisation's instructions bound this form, not memory.  A thread with whole blocks of
+// nvfp4 (half ones of mxfp4) finds a scale and its reciprocal once for sixteen numbers, and
+// keeps its weights in registers.  Lanes read their 16-byte groups in different orders, so
+// that the eight lanes of a shared-memory access touch all banks; codes are put back in
+// order.  Threads reach past the padded row (a power of two of them, at least 32).
+// 8192 x 8192 in us, against eight columns a lane in norm_forward_ring: bf16 to nvfp4 65 and 84,
+// to mxfp4 55 and 75; fp32 67 and 108, 60 and 110 (memory: 25 and 45).
+template <typename T, int FORMAT>
+__global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan pl) {
+    constexpr int VEC = 16 / sizeof(T), P = VEC / 2, N = 16 / VEC;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kMaxStages];
+    __shared__ float part[2][32];
+    __shared__ int abort_s;
+    const NormForward& p = pl.p;
+    const Ring& ring = pl.ring;
+    const int D = p.cols, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ring.stages; ++i) async::mbar_init(su32(&bars[i]), 1);
+        abort_s = 0;
+        async::mbar_fence_init();
+    }
+    const int chunks = chunks_of(D), groups = groups_of(D, FORMAT);
+    __syncthreads();
+    wait_previous();
+    const TensorScale ts(p.tensor_scale);
+    const int order = N == 2 ? lane >> 2 & 1 : lane >> 1 & 3;
+    const auto column = [&](int i) { return static_cast<int>(threadIdx.x) * 16 + (i ^ order) * VEC; };
+    const bool live = static_cast<int>(threadIdx.x) < 2 * chunks;
+    Two w[N][P];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (column(i) < D) {
+            weights<P, false>(p.next_weight, p.weight_dtype, column(i), D, w[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) w[i][j] = twice(0.0f);
+        }
+    }
+    RowLoop loop{ring, smem, bars, &abort_s, blockIdx.x, p.rows};
+    BlockSum block_sum{part};
+    loop.start();
+    for (; loop.row < p.rows; loop.next()) {
+        const T* const x = reinterpret_cast<const T*>(loop.row_ready());
+        const long long row = loop.row;
+        Two u[N][P];
+        Two s = twice(0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (column(i) < D) {
+                get(x + column(i), u[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < P; ++j) u[i][j] = twice(0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < P; ++j) s = fma(u[i][j], u[i][j], s);
+        }
+        const float r = rsqrtf(block_sum(sum(s)) / static_cast<float>(D) + p.eps);
+        loop.refill_this();
+        if (threadIdx.x == 0) p.next_rstd[row] = r;
+        const Two r2 = twice(r);
+        Two h[2][4];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const int k = i * P + j;
+                // Past the row an infinite r must not make a NaN of 0.
+                const Two v = column(i) < D ? mul(mul(u[i][j], r2), w[i][j]) : twice(0.0f);
+                h[k / 4][k % 4] = v;
+                const float2 f = parts(v);
+                amax = max(amax, max(__float_as_uint(f.x) & 0x7FFFFFFFu,
+                                     __float_as_uint(f.y) & 0x7FFFFFFFu));
+            }
+        if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        const uint32_t byte = block_scale<FORMAT>(amax, ts);
+        const Divider<FORMAT> by(byte, ts);
+        uint32_t low = by.codes(h[0]), high = by.codes(h[1]);
+        if (N == 4 && (order & 1)) {
+            low = low << 16 | low >> 16;
+            high = high << 16 | high >> 16;
+        }
+        const bool swap = N == 2 ? order : order & 2;
+        if (live)
+            *reinterpret_cast<uint2*>(p.codes + code_offset(row, threadIdx.x >> 1, chunks) +
+                                      8 * (threadIdx.x & 1)) =
+                swap ? make_uint2(high, low) : make_uint2(low, high);
+        // Four blocks' bytes to each of their lanes.
+        constexpr int kStep = FORMAT == kNvfp4 ? 1 : 2;
+        uint32_t word = byte << (8 * (lane / kStep % 4));
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, kStep);
+        word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * kStep);
+        if (live && lane % (4 * kStep) == 0)
+            *reinterpret_cast<uint32_t*>(
+                p.scales + scale_offset(row, static_cast<int>(threadIdx.x) / kStep, groups)) = word;
     }
     launch_next();
 }
@@ -601,6 +706,12 @@ cudaError_t launch_ring(K kernel, const P& plan, const RingShape& s, cudaStream_
 
 template <typename T, bool RAGGED, int COLS>
 cudaError_t forward_what(const ForwardPlan& pl, const RingShape& s, cudaStream_t st) {
+    if constexpr (!RAGGED && COLS == 16) {
+        if (!pl.p.block && pl.p.format == kNvfp4)
+            return launch_ring(norm_quantize_ring<T, kNvfp4>, pl, s, st);
+        if (!pl.p.block && pl.p.format >= 0)
+            return launch_ring(norm_quantize_ring<T, kMxfp4>, pl, s, st);
+    }
     if (!pl.p.block) return launch_ring(norm_forward_ring<T, RAGGED, COLS, kBefore>, pl, s, st);
     if (!pl.p.next) return launch_ring(norm_forward_ring<T, RAGGED, COLS, kAfterOnly>, pl, s, st);
     return launch_ring(norm_forward_ring<T, RAGGED, COLS, kBoth>, pl, s, st);

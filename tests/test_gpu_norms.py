@@ -233,6 +233,52 @@ def test_quantized_output(sg, rows, cols, dtype, fmt):
     assert hb.shape == (rows, cols) and rb.shape == (rows,)
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols,pad", [(400, 512, 0), (700, 96, 0), (333, 4096, 8), (5, 16384, 0),
+                                           (3, 8200, 0), (400, 264, 16), (1, 4096, 0), (400, 520, 1)])
+def test_before_quantized(sg, rows, cols, pad, dtype, fmt):
+    """Codes and scales against the 64-bit norm; the statistics' fp32 rounding may move a number
+    by 1e-5 of itself, and with it to the next code where it was that near a boundary.  A
+    row of zeros, one with an infinity and one with a NaN among the rows."""
+    g = torch.Generator().manual_seed(rows + cols)
+    x = (torch.randn(rows, cols + pad, generator=g) * 3).to(DTYPES[dtype])[:, :cols]
+    w = torch.randn(cols, generator=g)
+    bad = rows > 8
+    if bad:
+        x[2] = 0
+        x[4, cols // 2] = float("inf")
+        x[6, cols - 1] = float("nan")
+    ts = 0.03 if fmt == "nvfp4" else None
+    t = None if ts is None else torch.tensor([ts], device="cuda")
+    dev = torch.empty(rows, cols + pad, dtype=DTYPES[dtype], device="cuda")[:, :cols]
+    dev.copy_(x)
+    q, r = sg.norm_before(dev, w.cuda(), eps=EPS, quantize=fmt, tensor_scale=t)
+    keep = [i for i in range(rows) if not (bad and i in (4, 6))]
+    x64 = x.double()
+    r64 = 1 / torch.sqrt((x64 * x64).mean(1) + EPS)
+    assert torch.allclose(r.cpu().double()[keep], r64[keep], rtol=1e-5, atol=0)
+    h = (x64 * r64[:, None] * w.double())[keep]
+    lo, hi = ((h * (1 + s * 1e-5)).float().numpy() for s in (-1, 1))
+    v = [ref.values(*ref.quantize(a, fmt, ts), fmt, cols, ts) for a in (lo, hi)]
+    got = q.dequantize().double().cpu()
+    low, high = np.minimum(*v), np.maximum(*v)
+    slack = 1e-6 * np.abs(high) + 1e-30
+    mine = got[keep].numpy()
+    assert ((mine >= low - slack) & (mine <= high + slack)).all()
+    assert (low == high).mean() > 0.9
+    codes = q.codes.transpose(1, 2).reshape(-1, q.codes.shape[1] * 16)[:rows]
+    assert not bool(codes[keep][:, cols // 2:].any())
+    if bad:
+        assert got[6].isnan().all() and not got[2].any()
+        # inf * (1 / inf): its own block is NaN, the others are 0.
+        block = 16 if fmt == "nvfp4" else 32
+        at = cols // 2 // block * block
+        assert got[4, at:at + block].isnan().all()
+        rest = torch.cat([got[4, :at], got[4, at + block:]])
+        assert not rest.any()
+
+
 @pytest.mark.parametrize("wdtype", ["fp32", "same", "none"])
 def test_weight_types(sg, wdtype):
     wd = torch.float32 if wdtype == "fp32" else torch.bfloat16
