@@ -262,6 +262,13 @@ __device__ __forceinline__ uint32_t magnitude8(const float (&x)[8]) {
     return m;
 }
 
+// The largest magnitude of three numbers, or a NaN, whose bits are above infinity's.
+__device__ __forceinline__ float magnitude3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Eight numbers to consecutive elements: 16-byte stores where `vec` says that p is aligned for
 // them, else one by one, `left` at most.
 template <typename T>

@@ -29,7 +29,7 @@
 //
 // Measured (us, of the time the bytes take at 6.79 TB/s): the norm after a
 // block and the next one, 8192 x 8192 bf16 with a gate 123 (0.80); before, 8192 x 4096 bf16 33
-// (0.60); before, 8192 x 8192 bf16 to nvfp4 65 (0.39); gradient of the norm before a block,
+// (0.60); before, 8192 x 8192 bf16 to nvfp4 61 (0.41); gradient of the norm before a block,
 // 8192 x 4096 bf16 56 (0.70); of both, 8192 x 8192 bf16 with a gate 226
 // (0.70), 3001 x 2047 fp32 47 (0.46).  Gradients run 16 warps an SM at 122 to 128 registers
 // with issue slots 38 to 54 % used.  Streaming kernels, 4096 x 20000 bf16: before 395 (0.12),

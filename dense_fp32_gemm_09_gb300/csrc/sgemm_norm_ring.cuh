@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(1024, 1)
 // keeps its weights in registers.  Lanes read their 16-byte groups in different orders, so
 // that the eight lanes of a shared-memory access touch all banks; codes are put back in
 // order.  Threads reach past the padded row (a power of two of them, at least 32).
-// 8192 x 8192 in us, against eight columns a lane in norm_forward_ring: bf16 to nvfp4 65 and 84,
-// to mxfp4 55 and 75; fp32 67 and 108, 60 and 110 (memory: 25 and 45).
+// 8192 x 8192 in us, against eight columns a lane in norm_forward_ring: bf16 to nvfp4 61 and 84,
+// to mxfp4 53 and 75; fp32 63 and 108, 57 and 110 (memory: 25 and 45).
 template <typename T, int FORMAT>
 __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan pl) {
     constexpr int VEC = 16 / sizeof(T), P = VEC / 2, N = 16 / VEC;
@@ -442,6 +442,12 @@ __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan 
     const int order = N == 2 ? lane >> 2 & 1 : lane >> 1 & 3;
     const auto column = [&](int i) { return static_cast<int>(threadIdx.x) * 16 + (i ^ order) * VEC; };
     const bool live = static_cast<int>(threadIdx.x) < 2 * chunks;
+    // Past the row, an infinite or NaN statistic must not make codes: a thread's own numbers
+    // are times 0 there, and where it has both, the codes are masked (the block's numbers in
+    // the row are then infinite or NaN too, and so is its scale).
+    const int left = D - static_cast<int>(threadIdx.x) * 16;
+    const uint32_t in_low = left >= 8 ? ~0u : left > 0 ? ~0u >> (32 - 4 * left) : 0u;
+    const uint32_t in_high = left >= 16 ? ~0u : left > 8 ? ~0u >> (64 - 4 * left) : 0u;
     Two w[N][P];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -474,21 +480,19 @@ __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan 
         const float r = rsqrtf(block_sum(sum(s)) / static_cast<float>(D) + p.eps);
         loop.refill_this();
         if (threadIdx.x == 0) p.next_rstd[row] = r;
-        const Two r2 = twice(r);
+        const Two r2 = twice(left > 0 ? r : 0.0f);
         Two h[2][4];
-        uint32_t amax = 0;
+        float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const int k = i * P + j;
-                // Past the row an infinite r must not make a NaN of 0.
-                const Two v = column(i) < D ? mul(mul(u[i][j], r2), w[i][j]) : twice(0.0f);
-                h[k / 4][k % 4] = v;
-                const float2 f = parts(v);
-                amax = max(amax, max(__float_as_uint(f.x) & 0x7FFFFFFFu,
-                                     __float_as_uint(f.y) & 0x7FFFFFFFu));
+                h[k / 4][k % 4] = mul(mul(u[i][j], r2), w[i][j]);
+                const float2 f = parts(h[k / 4][k % 4]);
+                most = magnitude3(most, f.x, f.y);
             }
+        uint32_t amax = __float_as_uint(most);
         if (FORMAT == kMxfp4) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
         const uint32_t byte = block_scale<FORMAT>(amax, ts);
         const Divider<FORMAT> by(byte, ts);
@@ -497,11 +501,14 @@ __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan 
             low = low << 16 | low >> 16;
             high = high << 16 | high >> 16;
         }
-        const bool swap = N == 2 ? order : order & 2;
+        if (N == 2 ? order : order & 2) {
+            const uint32_t t = low;
+            low = high;
+            high = t;
+        }
         if (live)
             *reinterpret_cast<uint2*>(p.codes + code_offset(row, threadIdx.x >> 1, chunks) +
-                                      8 * (threadIdx.x & 1)) =
-                swap ? make_uint2(high, low) : make_uint2(low, high);
+                                      8 * (threadIdx.x & 1)) = make_uint2(low & in_low, high & in_high);
         // Four blocks' bytes to each of their lanes.
         constexpr int kStep = FORMAT == kNvfp4 ? 1 : 2;
         uint32_t word = byte << (8 * (lane / kStep % 4));

@@ -279,6 +279,29 @@ def test_before_quantized(sg, rows, cols, pad, dtype, fmt):
         assert not rest.any()
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("cols", [8, 24, 264, 520, 4104])
+def test_before_quantized_padding(sg, cols, dtype, fmt):
+    """Codes and scales past the row's end are zeros, whatever the row holds; with no eps a row of
+    zeros has an infinite statistic, and is NaN."""
+    rows = 400
+    x = torch.randn(rows, cols, generator=torch.Generator().manual_seed(cols)).to(DTYPES[dtype])
+    x[1], x[3, 0], x[5, cols - 1] = 0, float("nan"), float("inf")
+    q, r = sg.norm_before(x.cuda(), eps=0.0, quantize=fmt)
+    assert torch.isinf(r[1])
+    v = q.dequantize()
+    assert v[1].isnan().all() and v[3].isnan().all() and v[5, cols - 1].isnan()
+    assert not v[[0, 2, 4]].isnan().any()
+    codes = q.codes.transpose(1, 2).reshape(-1, q.codes.shape[1] * 16)[:rows]
+    assert not bool(codes[:, cols // 2:].any())
+    block = 16 if fmt == "nvfp4" else 32
+    # [rows/128][blocks/4][row % 32][row / 32 % 4][4]
+    s = q.scales.reshape(q.codes.shape[0], -1, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(
+        q.codes.shape[0] * 128, -1)[:rows]
+    assert not bool(s[:, -(-cols // block):].any())
+
+
 @pytest.mark.parametrize("wdtype", ["fp32", "same", "none"])
 def test_weight_types(sg, wdtype):
     wd = torch.float32 if wdtype == "fp32" else torch.bfloat16
