@@ -32,8 +32,8 @@
 // (0.60); before, 8192 x 8192 bf16 to nvfp4 61 (0.41); gradient of the norm before a block,
 // 8192 x 4096 bf16 56 (0.70); of both, 8192 x 8192 bf16 with a gate 226
 // (0.70), 3001 x 2047 fp32 47 (0.46).  Gradients run 16 warps an SM at 122 to 128 registers
-// with issue slots 38 to 54 % used.  Streaming kernels, 4096 x 20000 bf16: before 395 (0.12),
-// its gradient 1055 (0.07).
+// with issue slots 38 to 54 % used.  Streaming kernels: 4096 x 20000 fp32 before 409 (0.24),
+// bf16 gradient of before 1055 (0.07).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -372,12 +372,18 @@ cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stre
     // take the kernels without a ring (3001 x 2047 fp32 34 against 43).
     const bool few = p.rows <= 2LL * sms && p.cols <= 8 * 1024;
     // A row of fp32 numbers on its way to codes, but not in norm_quantize_ring.
-    const bool whole_blocks = !p.block && !few && !b.ragged();
+    // Aligned 2-byte rows of more than 16384 take 32 (4096 x 20000 bf16: before 77 against 395 us
+    // in the streaming kernel).  Ragged ones would have to be copied by elements (4096 x 20001:
+    // before 457 against 397, to nvfp4 389 against 688, the norm after 977 against 651), and
+    // fp32 ones do not fit with the quantised row beside them.
+    const bool wide = p.cols > 16 * 1024 && p.dtype != kF32 && !b.ragged();
+    const int columns = few ? 8 : wide ? 32 : 16;
+    const bool whole_blocks = !p.block && columns == 16 && !b.ragged();
     const long long row_fp32 = p.format >= 0 && !whole_blocks ? 128LL * chunks_of(p.cols) : 0;
     const RingShape s =
         b.ragged() && p.cols <= 8 * 1024
             ? b.column_shape(8, 1024, row_fp32, sms)
-            : b.shape(few ? 8 : 16, 1024, 32, p.dtype == kF32 || b.ragged() ? row_fp32 : 0, sms);
+            : b.shape(columns, 1024, 32, p.dtype == kF32 ? row_fp32 : 0, sms);
     if (!s.fits) {
         const dim3 grid(static_cast<unsigned>(p.rows));
         if (p.dtype == kF32)

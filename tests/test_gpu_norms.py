@@ -435,3 +435,24 @@ def test_refusals(sg):
         sg.norm_after_backward(x, x, w, w)
     with pytest.raises(ValueError, match="overlap"):
         sg.norm_after_backward(x[:1].expand(4, 32), x, w[:4])
+
+
+@pytest.mark.parametrize("gate", ["none", "rows", "shared"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(3, 16392), (160, 20000), (2, 20001), (4, 32768), (2, 32770)])
+def test_forward_of_wide_rows(sg, rows, cols, dtype, gate):
+    test_forward(sg, rows, cols, dtype, gate)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(3, 16392), (2, 20001), (2, 32768)])
+def test_quantized_output_of_wide_rows(sg, rows, cols, dtype, fmt):
+    test_quantized_output(sg, rows, cols, dtype, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(3, 16392), (2, 32768), (320, 20000)])
+def test_before_quantized_of_wide_rows(sg, rows, cols, dtype, fmt):
+    test_before_quantized(sg, rows, cols, 0, dtype, fmt)
