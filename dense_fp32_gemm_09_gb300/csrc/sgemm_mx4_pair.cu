@@ -6,41 +6,40 @@
 // CTA alone would need 12 KB.  (Roles, layout and scales as in sgemm_mx4_matmul.cu.)
 //
 // Persistent: pair i takes the tiles i, i + pairs, ...
-//   warp 0: bulk copies of the CTA's own halves, and of the scales: its own rows of B, all
-//     256 rows of A (the scales of the column operand are needed by both SMs).
+//   warp 0: tensor-map copies of the CTA's own halves, and of the scales: its own rows of B,
+//     all 256 rows of A (the scales of the column operand are needed by both SMs).  Both CTAs'
+//     copies complete on the first one's barrier, which the thread of the MMAs waits on, so
+//     nothing has to be passed on between them.  (A plain bulk copy can only signal a barrier
+//     of its own CTA.  A thread of the second CTA that passes it on has to release what it
+//     saw: at 8192^3 296 us from one warp, 205 from three in turn, 152 this way.)
 //   warp 1 of the first CTA: copies of scales to tensor memory and the MMAs of both CTAs.
 //     Four MMAs take 512 cycles, alone or with their 12 copies of scales, and a wait on a
-//     ready barrier about 100, so it waits on one a stage and asks about the next one under
+//     full barrier about 100, so it waits on one a stage and asks about the next one under
 //     the MMAs.
-//   warp 10: that barrier, once a stage has arrived in its CTA (a bulk copy can only signal
-//     a barrier of its own CTA; tensor-map copies can signal the other's, but bring the
-//     same bytes at 0.6 of the rate: 212 against 129 us for the copies of 8192^3 alone).
 //   warps 2..9: the epilogue, 128 lanes x 2 halves of the columns.  The 256 columns of fp32
 //     sums leave no room for a second set beside the scales, so a warp first moves its
 //     sums to registers, lets the next tile start, and stores them, through shared memory
 //     and as whole lines, under its MMAs.
 //
-// Bound at 8192^3 (nvfp4 to bf16, 157 us with the operands in L2, 7.0 PFLOP/s; measured with
-// parts left out when the whole took 161): 133 us with neither copies nor stores, 133 with
-// both but no MMAs, 139 without copies, 145 without stores.  The tensor cores and the copies
-// (38 KB a slab and SM) are about even, and each of the three costs the others some.
+// 8192^3, nvfp4 to bf16, operands in L2: 151 to 157 us, 7.0 to 7.3 PFLOP/s; the MMAs alone, at 128 cycles
+// each, would take 116.  2048^3 9.8 us, 4096^3 30, 3001 x 2047 x 1999 14.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
 #include "sgemm_mx4_tc.cuh"
+#include "sgemm_tma_host.h"
 
 namespace sgemm {
 namespace {
 
 using namespace mx4;
-using async::mbar_arrive;
 using async::mbar_expect_tx;
 using async::mbar_fence_init;
 using async::mbar_init;
 using async::su32;
 
-constexpr int kThreads = 352, kEpilogueWarps = 8;
+constexpr int kThreads = 320, kEpilogueWarps = 8;
 constexpr int kTile = 256;
 constexpr int kStages = 5;
 constexpr int kGroup = 16;       // tiles of m a raster group
@@ -54,6 +53,14 @@ static_assert(kTile + kStages * kStageCols<kNvfp4> <= kTmemCols, "tensor memory"
 constexpr int kStageC = 2 * 32 * 128 * 4;    // staging of C: 32 rows of each half, fp32
 static_assert(kStages * kStageBytes<kNvfp4> + kStageC <= 226 * 1024, "shared memory");
 
+constexpr int kLine = 128;                   // of a tensor map, bytes
+
+// The stored operands as lines of 128 bytes (with lines of 2048 the copies of 8192^3 alone took
+// 212 us).  A parameter of its own: its address is taken, and if it were the plan's, the
+// plan would be read again after every store (3001 x 2047 x 1999 19 instead of 14 us).
+struct PairMaps {
+    CUtensorMap a_codes, a_scales, b_codes, b_scales;
+};
 struct PairPlan {
     Mx4Matmul p;
     int chunks, slabs, tiles_n, tiles_m;
@@ -72,9 +79,15 @@ struct Ring {
         }
     }
 };
-__device__ __forceinline__ long long slabs_of_pair(const PairPlan& pl, int start, int pairs,
-                                                   int tiles) {
-    return start < tiles ? ((tiles - 1 - start) / pairs + 1) * static_cast<long long>(pl.slabs) : 0;
+
+// Lines [line, line + a box) into this CTA, completing on `bar` of the first CTA.
+__device__ __forceinline__ void load_lines(uint32_t dst, const CUtensorMap* tm, int line,
+                                           uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(0), "r"(line), "r"(bar)
+        : "memory");
 }
 
 struct Tile {
@@ -91,11 +104,11 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
     asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
     return r;
 }
-// Relaxed: what it announces was not written by this thread (bulk copies, which the
-// barrier has already seen complete) or is ordered by the tcgen05 fence before it (reads of
-// tensor memory).  A release would also wait for the thread's copies in flight: 400
-// instead of 183 us for the copies alone at 8192^3.
-__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* tm) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
+// Relaxed: it announces reads of tensor memory, which the tcgen05 fence before it orders.
+__device__ __forceinline__ void arrive_read(uint32_t addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                  : "memory");
 }
@@ -114,9 +127,9 @@ __device__ __forceinline__ void sync_half(int barrier) {
 
 template <int FORMAT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    mx4_pair_kernel(const PairPlan pl) {
+    mx4_pair_kernel(const __grid_constant__ PairMaps maps, const PairPlan pl) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full_bar[kStages], ready_bar[kStages], empty_bar[kStages];
+    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
     __shared__ __align__(8) uint64_t done_bar, free_bar;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
@@ -131,7 +144,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(su32(&full_bar[s]), 1);
-            mbar_init(su32(&ready_bar[s]), 2);
             mbar_init(su32(&empty_bar[s]), 1);
         }
         mbar_init(su32(&done_bar), 1);
@@ -139,6 +151,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         abort_s = 0;
         mbar_fence_init();
     }
+    if (warp == 0 && lane < 4)
+        prefetch_map(lane == 0 ? &maps.b_codes : lane == 1 ? &maps.a_codes
+                     : lane == 2 ? &maps.b_scales : &maps.a_scales);
     if (warp == 1) tmem_alloc<2>(su32(&tmem_base_s), kTmemCols);
     fence_before();
     __syncthreads();
@@ -160,36 +175,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = start; t < tiles && ok; t += pairs) {
                 const Tile at = tile_at(pl, t);
                 // Blocks of 128 rows; one past the end reads the last again (its sums
-                // are never stored).
+                // are never stored).  Boxes are a whole slab: past a row block's last
+                // columns they bring the next one's, or zeros, which nothing multiplies.
                 const long long pb = min((at.n0 >> 7) + rank, row_blocks_n - 1);
                 const long long q0 = at.m0 >> 7, q1 = min(q0 + 1, row_blocks_m - 1);
-                const uint8_t* pc = p.b_codes + pb * pl.chunks * 2048;
-                const uint8_t* ps = p.b_scales + pb * groups * 512;
-                const uint8_t* qc = p.a_codes + (rank ? q1 : q0) * pl.chunks * 2048;
-                const uint8_t* qs0 = p.a_scales + q0 * groups * 512;
-                const uint8_t* qs1 = p.a_scales + q1 * groups * 512;
+                const int pl0 = static_cast<int>(pb * pl.chunks * (2048 / kLine));
+                const int ql0 = static_cast<int>((rank ? q1 : q0) * pl.chunks * (2048 / kLine));
+                const int ps0 = static_cast<int>(pb * groups * (512 / kLine));
+                const int qs0 = static_cast<int>(q0 * groups * (512 / kLine));
+                const int qs1 = static_cast<int>(q1 * groups * (512 / kLine));
                 for (int s = 0; s < pl.slabs; ++s) {
                     if (!pipe_wait(su32(&empty_bar[ring.stage]), ring.phase ^ 1u, abort_flag, pl.status)) {
                         ok = false;
                         break;
                     }
-                    const int c0 = s * kSlabChunks, nc = min(kSlabChunks, pl.chunks - c0);
-                    const int ng = nc / kChunksPerGroup<FORMAT>;
-                    const long long g0 = c0 / kChunksPerGroup<FORMAT>;
-                    const uint32_t fb = su32(&full_bar[ring.stage]);
+                    const uint32_t fb = in_first_cta(su32(&full_bar[ring.stage]));
                     const uint32_t base = smem0 + ring.stage * kStageBytes<FORMAT>;
-                    mbar_expect_tx(fb, 2 * nc * 2048 + 3 * ng * 512);
-                    bulk_load(base, pc + c0 * 2048LL, nc * 2048, fb);
-                    bulk_load(base + kCodes, qc + c0 * 2048LL, nc * 2048, fb);
+                    if (rank == 0) mbar_expect_tx(su32(&full_bar[ring.stage]), 2 * kStageBytes<FORMAT>);
+                    const int cl = s * (kCodes / kLine), sl = s * (kSf<FORMAT> / kLine);
+                    load_lines(base, &maps.b_codes, pl0 + cl, fb);
+                    load_lines(base + kCodes, &maps.a_codes, ql0 + cl, fb);
                     const uint32_t sf = base + 2 * kCodes;
-                    bulk_load(sf, ps + g0 * 512, ng * 512, fb);
-                    bulk_load(sf + kSf<FORMAT>, qs0 + g0 * 512, ng * 512, fb);
-                    bulk_load(sf + 2 * kSf<FORMAT>, qs1 + g0 * 512, ng * 512, fb);
+                    load_lines(sf, &maps.b_scales, ps0 + sl, fb);
+                    load_lines(sf + kSf<FORMAT>, &maps.a_scales, qs0 + sl, fb);
+                    load_lines(sf + 2 * kSf<FORMAT>, &maps.a_scales, qs1 + sl, fb);
                     ++issued;
                     ring.next();
                 }
             }
-            if (!ok) {   // giving up: copies in flight land before the CTA exits
+            // Giving up: copies in flight land before the pair exits.  They signal the first
+            // CTA, so it waits for both; what the second may have asked for beyond that had
+            // the time limit of the wait that gave up.
+            if (!ok && rank == 0) {
                 volatile int no_abort = 0;
                 for (int i = max(0, issued - kStages); i < issued; ++i)
                     pipe_wait(su32(&full_bar[i % kStages]), (i / kStages) & 1, &no_abort, nullptr);
@@ -203,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // A stage has arrived in both CTAs: its scales to tensor memory.
             auto take = [&](const Ring& r, bool ready) {
                 if (!ready &&
-                    !pipe_wait(su32(&ready_bar[r.stage]), r.phase, abort_flag, pl.status))
+                    !pipe_wait<true>(su32(&full_bar[r.stage]), r.phase, abort_flag, pl.status))
                     return false;
                 fence_after();
                 const uint64_t at = scales_desc + r.stage * (kStageBytes<FORMAT> / 16);
@@ -233,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ready = false, ok = true;
             for (int t = start; t < tiles && ok; t += pairs) {
                 // The previous tile's sums have left tensor memory (first: at once).
-                if (!pipe_wait(su32(&free_bar), turn ^ 1u, abort_flag, pl.status)) break;
+                if (!pipe_wait<true>(su32(&free_bar), turn ^ 1u, abort_flag, pl.status)) break;
                 turn ^= 1u;
                 for (int s = 0; s < pl.slabs; ++s) {
                     if (!take(ring, ready)) {
@@ -244,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // thread's own time, 512 cycles a slab, is what it has least of.
                     Ring ahead = ring;
                     ahead.next();
-                    ready = pipe_peek(su32(&ready_bar[ahead.stage]), ahead.phase);
+                    ready = pipe_peek(su32(&full_bar[ahead.stage]), ahead.phase);
                     multiply(ring, 0, s != 0);
                     multiply(ring, 1, true);
                     if (kSlabChunks * (s + 1) <= pl.chunks) {
@@ -255,16 +272,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ring = ahead;
                 }
                 commit<2>(su32(&done_bar));
-            }
-        }
-    } else if (warp == 10) {
-        if (elect_one()) {
-            Ring ring;
-            const long long total = slabs_of_pair(pl, start, pairs, tiles);
-            for (long long i = 0; i < total; ++i, ring.next()) {
-                if (!pipe_wait(su32(&full_bar[ring.stage]), ring.phase, abort_flag, pl.status))
-                    break;
-                arrive_cluster(in_first_cta(su32(&ready_bar[ring.stage])));
             }
         }
     } else {
@@ -291,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_ld64(mine + 64, v[1]);
             fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(in_first_cta(su32(&free_bar)));
+            if (lane == 0) arrive_read(in_first_cta(su32(&free_bar)));
             const long long n0 = at.n0 + 128 * rank, m0 = at.m0 + half * kCols;
             const int me = 32 * quarter + lane;
 #pragma unroll
@@ -322,9 +329,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+// `bytes` bytes (whole lines) in boxes of `box` bytes.
+bool encode_lines(CUtensorMap* tm, const void* base, long long bytes, int box) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {kLine, static_cast<cuuint64_t>(bytes / kLine)};
+    cuuint64_t strides[1] = {kLine};
+    cuuint32_t boxes[2] = {kLine, static_cast<cuuint32_t>(box / kLine)};
+    cuuint32_t steps[2] = {1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, boxes,
+              steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 template <int FORMAT>
 cudaError_t launch_pair(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     PairPlan pl{};
+    PairMaps maps;
     pl.p = p;
     pl.chunks = chunks_of(p.K);
     pl.slabs = (pl.chunks + kSlabChunks - 1) / kSlabChunks;
@@ -333,6 +355,15 @@ cudaError_t launch_pair(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     pl.tiles_n = static_cast<int>(tn);
     pl.tiles_m = static_cast<int>(tm);
     pl.status = status_word_ptr();
+    // At least two row blocks of four chunks each, so no box is larger than its matrix.
+    const long long ca = row_blocks(p.M) * pl.chunks * 2048, cb = row_blocks(p.N) * pl.chunks * 2048;
+    constexpr int per = 2048 * kChunksPerGroup<FORMAT> / 512;      // code bytes a scale byte
+    if (std::max(ca, cb) / kLine > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (!encode_lines(&maps.a_codes, p.a_codes, ca, kCodes) ||
+        !encode_lines(&maps.b_codes, p.b_codes, cb, kCodes) ||
+        !encode_lines(&maps.a_scales, p.a_scales, ca / per, kSf<FORMAT>) ||
+        !encode_lines(&maps.b_scales, p.b_scales, cb / per, kSf<FORMAT>))
+        return cudaErrorInvalidValue;
     constexpr int smem = kStages * kStageBytes<FORMAT> + kStageC;
     pl.c_vec = c_rows_aligned(p);
     auto kernel = mx4_pair_kernel<FORMAT>;
@@ -348,7 +379,7 @@ cudaError_t launch_pair(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     c.stream = stream;
     c.attrs = at;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, pl);
+    return cudaLaunchKernelEx(&c, kernel, maps, pl);
 }
 
 }  // namespace

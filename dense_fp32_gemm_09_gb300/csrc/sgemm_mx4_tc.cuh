@@ -16,35 +16,47 @@ template <int FORMAT> constexpr int kSlabGroups = kSlabChunks / kChunksPerGroup<
 // the phase completes or kSleepNs have passed: polls and reads of the global timer by the
 // waiting warps slow down the two threads that feed the tensor cores.
 constexpr unsigned kSleepNs = 1000000;
+// CLUSTER: other CTAs of the cluster take part in the phase, so the wait acquires at their scope.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool pipe_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSleepNs)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kSleepNs)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.b32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(kSleepNs)
+            : "memory");
     return ok != 0;
 }
-// Whether the phase has completed, without sleeping.
+// Whether the phase has completed, without sleeping (at the cluster's scope).
 __device__ __forceinline__ bool pipe_peek(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool pipe_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                           int* status) {
-    if (pipe_try(bar, parity)) return true;
+    if (pipe_try<CLUSTER>(bar, parity)) return true;
     const unsigned long long t0 = async::gtimer();
     for (unsigned i = 0; i < async::kMaxSpins; ++i) {
-        if (pipe_try(bar, parity)) return true;
+        if (pipe_try<CLUSTER>(bar, parity)) return true;
         if (*abort) return false;
         if (async::gtimer() - t0 > async::kWaitNs) break;
     }
