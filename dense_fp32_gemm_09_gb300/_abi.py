@@ -65,6 +65,9 @@ SIGNATURES = {
                                 _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp]),
     "sgemm_norm_backward": (_i, [_i, _i, _i] + [_vp, _i] * 3 + [_vp, _vp, _vp, _i, _vp, _vp, _i,
                                  _vp, _i, _f] + [_vp, _i] * 3 + [_vp, _vp, _vp]),
+    "sgemm_norm_backward_workspace": (_i, [_i, _i, ctypes.POINTER(_sz)]),
+    "sgemm_norm_backward_ws": (_i, [_i, _i, _i] + [_vp, _i] * 3 + [_vp, _vp, _vp, _i, _vp, _vp, _i,
+                                    _vp, _i, _f] + [_vp, _i] * 3 + [_vp, _vp, _vp, _sz, _vp]),
     "sgemm_device_status": (_i, []),
     "sgemm_selftest_bounded_wait": (_i, [_i]),
     "sgemm_schedule_check": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(SgemmConfig)]),

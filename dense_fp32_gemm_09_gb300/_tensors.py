@@ -114,7 +114,7 @@ def fast():
         loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "sgemm_mx4_quantize", "sgemm_mx4_dequantize", "sgemm_mx4_matmul",
-            "sgemm_norm_forward", "sgemm_norm_backward")))
+            "sgemm_norm_forward", "sgemm_norm_backward_ws", "sgemm_norm_backward_workspace")))
         _fast = module
     return _fast
 

@@ -24,7 +24,8 @@ decltype(&sgemm_mx4_quantize) f_quantize;
 decltype(&sgemm_mx4_dequantize) f_dequantize;
 decltype(&sgemm_mx4_matmul) f_matmul;
 decltype(&sgemm_norm_forward) f_forward;
-decltype(&sgemm_norm_backward) f_backward;
+decltype(&sgemm_norm_backward_ws) f_backward;
+decltype(&sgemm_norm_backward_workspace) f_backward_workspace;
 
 template <typename F>
 PyObject* guarded(F f) {
@@ -310,30 +311,38 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (gate.defined())
                 dgate = ldg ? empty({s.rows, s.cols}, s.type) : empty({s.cols}, at::kFloat);
         }
+        // From torch's allocator, so that a captured graph owns what it uses.
+        at::Tensor ws;
+        size_t ws_bytes = 0;
+        if (dweight.defined() || dnext.defined() || (dgate.defined() && ldg == 0)) {
+            if (const int st = f_backward_workspace(s.rows, s.cols, &ws_bytes)) return status(st);
+            ws = empty({static_cast<int64_t>(ws_bytes)}, at::kByte);
+        }
         const int st = f_backward(
             s.rows, s.cols, dt, ptr(dy), lddy, ptr(dh), lddh, ptr(y), ldy,
             static_cast<const float*>(ptr(next_rstd)), ptr(next_weight), ptr(block), ldb,
             static_cast<const float*>(ptr(rstd)), ptr(weight), wt, ptr(gate), ldg, scale, ptr(dx),
             s.cols, ptr(dblock), s.cols, ptr(dgate), s.cols, static_cast<float*>(ptr(dweight)),
-            static_cast<float*>(ptr(dnext)), stream());
+            static_cast<float*>(ptr(dnext)), ptr(ws), ws_bytes, stream());
         return st ? status(st) : tuple({dx, dblock, dweight, dgate, dnext});
     });
 }
 
-// bind(addresses of the five C functions, in this order)
+// bind(addresses of the six C functions, in this order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
+    if (n != 6) {
+        PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
         return nullptr;
     }
-    void* p[5];
-    for (int i = 0; i < 5; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+    void* p[6];
+    for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
     f_quantize = reinterpret_cast<decltype(f_quantize)>(p[0]);
     f_dequantize = reinterpret_cast<decltype(f_dequantize)>(p[1]);
     f_matmul = reinterpret_cast<decltype(f_matmul)>(p[2]);
     f_forward = reinterpret_cast<decltype(f_forward)>(p[3]);
     f_backward = reinterpret_cast<decltype(f_backward)>(p[4]);
+    f_backward_workspace = reinterpret_cast<decltype(f_backward_workspace)>(p[5]);
     Py_RETURN_NONE;
 }
 

@@ -455,6 +455,8 @@ struct Workspace {
     std::mutex mu;
     void* ptr = nullptr;
     size_t bytes = 0;
+    bool captured = false;         // a graph may hold ptr: it stays until shutdown
+    std::vector<void*> kept;       // outgrown buffers that graphs may hold
 };
 std::mutex g_ws_mu;   // guards the map itself; entries are stable until shutdown
 std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
@@ -474,28 +476,51 @@ int library_workspace(cudaStream_t stream, size_t need, void** out,
     }
     std::unique_lock<std::mutex> wl(wp->mu);
     Workspace& w = *wp;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) {
+        cudaGetLastError();          // the default stream while another one is captured
+        capture = cudaStreamCaptureStatusNone;
+    }
+    const bool capturing = capture == cudaStreamCaptureStatusActive;
     if (w.bytes >= need) {
+        w.captured |= capturing;
         *out = w.ptr;
         *hold = std::move(wl);
         return SGEMM_OK;
     }
     if (w.ptr) {
-        e = cudaFreeAsync(w.ptr, stream);
+        void* const old = w.ptr;
+        const bool keep = w.captured || capturing;
         w.ptr = nullptr;
         w.bytes = 0;
-        if (e != cudaSuccess) {
+        w.captured = false;
+        if (keep) {
+            w.kept.push_back(old);
+        } else if ((e = cudaFreeAsync(old, stream)) != cudaSuccess) {
             set_error("cudaFreeAsync", e);
             return SGEMM_ERR_WORKSPACE;
         }
     }
     const size_t bytes = std::max(need, static_cast<size_t>(1) << 20);
-    e = cudaMallocAsync(&w.ptr, bytes, stream);
+    if (capturing) {
+        // Not cudaMallocAsync: the buffer would belong to the graph, and later calls use it.
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        e = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e == cudaSuccess) {
+            e = cudaMalloc(&w.ptr, bytes);
+            cudaThreadExchangeStreamCaptureMode(&mode);
+        }
+    } else {
+        e = cudaMallocAsync(&w.ptr, bytes, stream);
+    }
     if (e != cudaSuccess) {
         w.ptr = nullptr;
-        set_error("cudaMallocAsync", e);
+        set_error("workspace allocation", e);
+        cudaGetLastError();
         return SGEMM_ERR_WORKSPACE;
     }
     w.bytes = bytes;
+    w.captured = capturing;
     *out = w.ptr;
     *hold = std::move(wl);
     return SGEMM_OK;
@@ -1312,17 +1337,20 @@ int sgemm_shutdown(void) {
     std::lock_guard<std::mutex> lk(g_ws_mu);
     int rc = SGEMM_OK;
     for (auto& kv : g_ws) {
-        if (kv.second.ptr) {
-            int prev = 0;
-            cudaGetDevice(&prev);
-            cudaSetDevice(kv.first.first);
-            const cudaError_t e = cudaFree(kv.second.ptr);
-            cudaSetDevice(prev);
+        std::vector<void*> all = kv.second.kept;
+        if (kv.second.ptr) all.push_back(kv.second.ptr);
+        if (all.empty()) continue;
+        int prev = 0;
+        cudaGetDevice(&prev);
+        cudaSetDevice(kv.first.first);
+        for (void* p : all) {
+            const cudaError_t e = cudaFree(p);
             if (e != cudaSuccess) {
                 set_error("cudaFree", e);
                 rc = SGEMM_ERR_LAUNCH;
             }
         }
+        cudaSetDevice(prev);
     }
     g_ws.clear();
     shutdown_host_pipes();

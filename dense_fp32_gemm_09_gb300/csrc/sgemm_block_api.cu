@@ -127,6 +127,101 @@ Mat scales_mat(const char* n, const void* p, int rows, int cols, int format) {
         if (st_ != SGEMM_OK) return st_;       \
     } while (0)
 
+// own_ws: in the caller's workspace, else in the library's of the stream.
+int norm_backward(int rows, int cols, int dtype, const void* dy, int lddy, const void* dh,
+                  int lddh, const void* y, int ldy, const float* next_rstd,
+                  const void* next_weight, const void* block, int ldb, const float* rstd,
+                  const void* weight, int weight_dtype, const void* gate, int ldg,
+                  float scale, void* dx, int lddx, void* dblock, int lddb, void* dgate,
+                  int lddg, float* dweight, float* dnext_weight,
+                  bool own_ws, void* ws_given, size_t ws_bytes, sgemm_stream_t stream) {
+    return guarded([&]() -> int {
+        SGEMM_TRY(check_dtype(dtype));
+        SGEMM_TRY(check_dtype(weight_dtype));
+        SGEMM_TRY(check_extent("sgemm_norm_backward", rows, cols));
+        if (cols == 0) return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: rows of no columns");
+        if (!std::isfinite(scale))
+            return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: scale is not finite");
+        const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        const int es = elem_size(dtype), ws = elem_size(weight_dtype);
+        const bool shared = gate != nullptr && ldg == 0;
+        if (dgate && !gate)
+            return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: dgate without a gate");
+        if (rows > 0) {
+            if (block == nullptr && dh == nullptr)
+                return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: neither block nor dh");
+            if (dh == nullptr && dy == nullptr)
+                return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: neither dy nor dh");
+            if (dh != nullptr && (y == nullptr || next_rstd == nullptr || dx == nullptr))
+                return refuse(SGEMM_ERR_INVALID_ARG,
+                              "sgemm_norm_backward: dh needs y, next_rstd and dx");
+            if (dh == nullptr && (next_weight || dnext_weight))
+                return refuse(SGEMM_ERR_INVALID_ARG,
+                              "sgemm_norm_backward: next_weight or its gradient without dh");
+            if (block != nullptr && (rstd == nullptr || dblock == nullptr))
+                return refuse(SGEMM_ERR_INVALID_ARG,
+                              "sgemm_norm_backward: a block needs rstd and dblock");
+            if (block == nullptr && (weight || gate || dweight || dblock))
+                return refuse(SGEMM_ERR_INVALID_ARG,
+                              "sgemm_norm_backward: weight, gate or their gradients without a block");
+        }
+        const Mat in[] = {{"dy", dy, dy ? rows : 0, cols, lddy, es},
+                          {"dh", dh, dh ? rows : 0, cols, lddh, es},
+                          {"y", y, dh ? rows : 0, cols, ldy, es},
+                          {"next_rstd", next_rstd, dh ? 1 : 0, rows, rows, 4},
+                          {"next_weight", next_weight, next_weight ? 1 : 0, cols, cols, ws},
+                          {"block", block, block ? rows : 0, cols, ldb, es},
+                          {"rstd", rstd, block ? 1 : 0, rows, rows, 4},
+                          {"weight", weight, weight ? 1 : 0, cols, cols, ws},
+                          {"gate", gate, gate ? (ldg ? rows : 1) : 0, cols, ldg, es}};
+        const Mat out[] = {{"dx", dx, dx ? rows : 0, cols, lddx, es},
+                           {"dblock", dblock, dblock ? rows : 0, cols, lddb, es},
+                           {"dgate", dgate, dgate ? (shared ? 1 : rows) : 0, cols,
+                            shared ? cols : lddg, shared ? 4 : es},
+                           {"dweight", dweight, dweight ? 1 : 0, cols, cols, 4},
+                           {"dnext_weight", dnext_weight, dnext_weight ? 1 : 0, cols, cols, 4}};
+        for (const Mat& m : in) SGEMM_TRY(check_mat(m));
+        for (const Mat& m : out) SGEMM_TRY(check_mat(m));
+        SGEMM_TRY(check_apart(out, in));
+        int sms = 0;
+        SGEMM_TRY(current_device_sms(&sms));
+        if (rows == 0) {   // sums over no rows
+            float* sums[] = {dweight, shared ? static_cast<float*>(dgate) : nullptr, dnext_weight};
+            for (float* p : sums) {
+                if (p == nullptr) continue;
+                const cudaError_t e = cudaMemsetAsync(p, 0, sizeof(float) * cols, s);
+                if (e != cudaSuccess) {
+                    set_cuda_error("sgemm_norm_backward", e);
+                    return SGEMM_ERR_LAUNCH;
+                }
+            }
+            return SGEMM_OK;
+        }
+        NormBackward p{rows, cols, dtype, weight_dtype, dy, dh, y, block, gate, weight, next_weight,
+                       rstd, next_rstd, lddy, lddh, ldy, ldb, ldg, lddx, lddb, lddg, scale,
+                       dx, dblock, dgate, dweight, dnext_weight, nullptr};
+        std::unique_lock<std::mutex> hold;
+        if (const size_t need = norm_backward_workspace(p, sms)) {
+            void* ws_ptr = ws_given;
+            if (!own_ws) {
+                SGEMM_TRY(stream_workspace(s, need, &ws_ptr, &hold));
+            } else {
+                if (ws_ptr == nullptr || ws_bytes < need || !aligned(ws_ptr, 16))
+                    return refuse(SGEMM_ERR_WORKSPACE,
+                                  "sgemm_norm_backward_ws: workspace of %zu bytes needed, aligned "
+                                  "to 16 (got %zu)", need, ws_bytes);
+                const Mat ws_mat[] = {{"workspace", ws_ptr, 1, static_cast<long long>(need), 1, 1}};
+                SGEMM_TRY(check_apart(ws_mat, in));
+                SGEMM_TRY(check_apart(ws_mat, out));
+            }
+            p.partial = static_cast<float*>(ws_ptr);
+        }
+        int n = 0;
+        const cudaError_t e = launch_norm_backward(p, sms, s, &n);
+        return launched(e, "sgemm_norm_backward", n);
+    });
+}
+
 }  // namespace
 }  // namespace sgemm
 
@@ -308,81 +403,33 @@ int sgemm_norm_backward(int rows, int cols, int dtype, const void* dy, int lddy,
                         const void* weight, int weight_dtype, const void* gate, int ldg,
                         float scale, void* dx, int lddx, void* dblock, int lddb, void* dgate,
                         int lddg, float* dweight, float* dnext_weight, sgemm_stream_t stream) {
+    return norm_backward(rows, cols, dtype, dy, lddy, dh, lddh, y, ldy, next_rstd, next_weight, block,
+                         ldb, rstd, weight, weight_dtype, gate, ldg, scale, dx, lddx, dblock, lddb,
+                         dgate, lddg, dweight, dnext_weight, false, nullptr, 0, stream);
+}
+
+int sgemm_norm_backward_workspace(int rows, int cols, size_t* bytes) {
     return guarded([&]() -> int {
-        SGEMM_TRY(check_dtype(dtype));
-        SGEMM_TRY(check_dtype(weight_dtype));
-        SGEMM_TRY(check_extent("sgemm_norm_backward", rows, cols));
-        if (cols == 0) return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: rows of no columns");
-        if (!std::isfinite(scale))
-            return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: scale is not finite");
-        const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-        const int es = elem_size(dtype), ws = elem_size(weight_dtype);
-        const bool shared = gate != nullptr && ldg == 0;
-        if (dgate && !gate)
-            return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: dgate without a gate");
-        if (rows > 0) {
-            if (block == nullptr && dh == nullptr)
-                return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: neither block nor dh");
-            if (dh == nullptr && dy == nullptr)
-                return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward: neither dy nor dh");
-            if (dh != nullptr && (y == nullptr || next_rstd == nullptr || dx == nullptr))
-                return refuse(SGEMM_ERR_INVALID_ARG,
-                              "sgemm_norm_backward: dh needs y, next_rstd and dx");
-            if (dh == nullptr && (next_weight || dnext_weight))
-                return refuse(SGEMM_ERR_INVALID_ARG,
-                              "sgemm_norm_backward: next_weight or its gradient without dh");
-            if (block != nullptr && (rstd == nullptr || dblock == nullptr))
-                return refuse(SGEMM_ERR_INVALID_ARG,
-                              "sgemm_norm_backward: a block needs rstd and dblock");
-            if (block == nullptr && (weight || gate || dweight || dblock))
-                return refuse(SGEMM_ERR_INVALID_ARG,
-                              "sgemm_norm_backward: weight, gate or their gradients without a block");
-        }
-        const Mat in[] = {{"dy", dy, dy ? rows : 0, cols, lddy, es},
-                          {"dh", dh, dh ? rows : 0, cols, lddh, es},
-                          {"y", y, dh ? rows : 0, cols, ldy, es},
-                          {"next_rstd", next_rstd, dh ? 1 : 0, rows, rows, 4},
-                          {"next_weight", next_weight, next_weight ? 1 : 0, cols, cols, ws},
-                          {"block", block, block ? rows : 0, cols, ldb, es},
-                          {"rstd", rstd, block ? 1 : 0, rows, rows, 4},
-                          {"weight", weight, weight ? 1 : 0, cols, cols, ws},
-                          {"gate", gate, gate ? (ldg ? rows : 1) : 0, cols, ldg, es}};
-        const Mat out[] = {{"dx", dx, dx ? rows : 0, cols, lddx, es},
-                           {"dblock", dblock, dblock ? rows : 0, cols, lddb, es},
-                           {"dgate", dgate, dgate ? (shared ? 1 : rows) : 0, cols,
-                            shared ? cols : lddg, shared ? 4 : es},
-                           {"dweight", dweight, dweight ? 1 : 0, cols, cols, 4},
-                           {"dnext_weight", dnext_weight, dnext_weight ? 1 : 0, cols, cols, 4}};
-        for (const Mat& m : in) SGEMM_TRY(check_mat(m));
-        for (const Mat& m : out) SGEMM_TRY(check_mat(m));
-        SGEMM_TRY(check_apart(out, in));
+        SGEMM_TRY(check_extent("sgemm_norm_backward_workspace", rows, cols));
+        if (bytes == nullptr)
+            return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_norm_backward_workspace: null output");
         int sms = 0;
         SGEMM_TRY(current_device_sms(&sms));
-        if (rows == 0) {   // sums over no rows
-            float* sums[] = {dweight, shared ? static_cast<float*>(dgate) : nullptr, dnext_weight};
-            for (float* p : sums) {
-                if (p == nullptr) continue;
-                const cudaError_t e = cudaMemsetAsync(p, 0, sizeof(float) * cols, s);
-                if (e != cudaSuccess) {
-                    set_cuda_error("sgemm_norm_backward", e);
-                    return SGEMM_ERR_LAUNCH;
-                }
-            }
-            return SGEMM_OK;
-        }
-        NormBackward p{rows, cols, dtype, weight_dtype, dy, dh, y, block, gate, weight, next_weight,
-                       rstd, next_rstd, lddy, lddh, ldy, ldb, ldg, lddx, lddb, lddg, scale,
-                       dx, dblock, dgate, dweight, dnext_weight, nullptr};
-        std::unique_lock<std::mutex> hold;
-        if (const size_t need = norm_backward_workspace(p, sms)) {
-            void* ws_ptr = nullptr;
-            SGEMM_TRY(stream_workspace(s, need, &ws_ptr, &hold));
-            p.partial = static_cast<float*>(ws_ptr);
-        }
-        int n = 0;
-        const cudaError_t e = launch_norm_backward(p, sms, s, &n);
-        return launched(e, "sgemm_norm_backward", n);
+        *bytes = rows > 0 && cols > 0 ? norm_backward_workspace_most(rows, cols, sms) : 0;
+        return SGEMM_OK;
     });
+}
+
+int sgemm_norm_backward_ws(int rows, int cols, int dtype, const void* dy, int lddy, const void* dh,
+                        int lddh, const void* y, int ldy, const float* next_rstd,
+                        const void* next_weight, const void* block, int ldb, const float* rstd,
+                        const void* weight, int weight_dtype, const void* gate, int ldg,
+                        float scale, void* dx, int lddx, void* dblock, int lddb, void* dgate,
+                        int lddg, float* dweight, float* dnext_weight, void* ws,
+                        size_t ws_bytes, sgemm_stream_t stream) {
+    return norm_backward(rows, cols, dtype, dy, lddy, dh, lddh, y, ldy, next_rstd, next_weight, block,
+                         ldb, rstd, weight, weight_dtype, gate, ldg, scale, dx, lddx, dblock, lddb,
+                         dgate, lddg, dweight, dnext_weight, true, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -133,6 +133,8 @@ cudaError_t launch_mx4_matmul(const Mx4Matmul& p, int sms, cudaStream_t stream);
 cudaError_t launch_mx4_pair(const Mx4Matmul& p, int sms, cudaStream_t stream);
 cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stream);
 size_t norm_backward_workspace(const NormBackward& p, int sms);
+// At least that, for any types, strides and alignment of this size.
+size_t norm_backward_workspace_most(int rows, int cols, int sms);
 cudaError_t launch_norm_backward(const NormBackward& p, int sms, cudaStream_t stream,
                                  int* launches);
 

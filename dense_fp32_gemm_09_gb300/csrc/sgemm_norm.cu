@@ -357,6 +357,18 @@ size_t norm_backward_workspace(const NormBackward& p, int sms) {
     return static_cast<size_t>(backward_grid(p, s, sms)) * 3 * p.cols * sizeof(float);
 }
 
+size_t norm_backward_workspace_most(int rows, int cols, int sms) {
+    // Blocks of an SM: those of the kernels without a ring (backward_shape), else two (a ring
+    // of 512 threads or more, or the streaming kernel).
+    const auto blocks = [&](int own) {
+        return cols <= own * 512 ? RingBuilder(kF32, rows, cols).column_shape(own, 512, 0, sms).blocks_per_sm
+                                 : 2;
+    };
+    const long long grid =
+        std::min<long long>(rows, static_cast<long long>(sms) * std::max({blocks(8), blocks(16), 2}));
+    return static_cast<size_t>(grid) * 3 * cols * sizeof(float);
+}
+
 cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stream) {
     RingBuilder b(p.dtype, p.rows, p.cols);
     b.add(p.residual, p.ldr);

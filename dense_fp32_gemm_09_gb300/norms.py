@@ -10,6 +10,8 @@ pass.  ``h`` may leave the pass as a 4-bit matrix (``mx4.Mx4``).  All sums are f
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _tensors as _t
@@ -132,7 +134,7 @@ def _backward(stream, ref, dy, dh, y, next_rstd, next_weight, block, rstd, weigh
         out = _t.fast().norm_backward(ref, dy, dh, y, next_rstd, next_weight, block, rstd, weight,
                                       gate, scale)
         if out is not None:
-            _t.checked(out, "sgemm_norm_backward")
+            _t.checked(out, "sgemm_norm_backward_ws")
             return out
     call = _t.Call(_t.cuda_tensor(ref, "dy" if dy is not None else "dh").device, stream)
     rows, cols, dt, _ = _rows(ref, "dy" if dy is not None else "dh")
@@ -155,10 +157,19 @@ def _backward(stream, ref, dy, dh, y, next_rstd, next_weight, block, rstd, weigh
         if gate is not None:
             dgate = call.empty((rows, cols), ref.dtype) if ldg else \
                 call.empty((cols,), torch.float32)
-    call.run("sgemm_norm_backward", rows, cols, dt, _t.ptr(dy), lddy, _t.ptr(dh), lddh, _t.ptr(y),
+    # From torch's allocator, so that a captured graph owns what it uses.
+    ws = None
+    if dweight is not None or dnext is not None or (dgate is not None and not ldg):
+        size = ctypes.c_size_t(0)
+        with torch.cuda.device(ref.device):
+            _t.check(_t.function("sgemm_norm_backward_workspace")(rows, cols, ctypes.byref(size)),
+                     "sgemm_norm_backward_workspace")
+        ws = call.empty((size.value,), torch.uint8)
+    call.run("sgemm_norm_backward_ws", rows, cols, dt, _t.ptr(dy), lddy, _t.ptr(dh), lddh, _t.ptr(y),
              ldy, _t.ptr(next_rstd), _t.ptr(next_weight), _t.ptr(block), ldb, _t.ptr(rstd),
              _t.ptr(weight), wt, _t.ptr(gate), ldg, scale, _t.ptr(dx), cols, _t.ptr(dblock), cols,
-             _t.ptr(dgate), cols, _t.ptr(dweight), _t.ptr(dnext))
+             _t.ptr(dgate), cols, _t.ptr(dweight), _t.ptr(dnext), _t.ptr(ws),
+             0 if ws is None else ws.numel())
     return dx, dblock, dweight, dgate, dnext
 
 

@@ -113,8 +113,13 @@ typedef struct {
  * so they run on the 16-byte / TMA kernels (the copy moves values, not sums: the
  * results are those of the aligned kernels on aligned operands; they can differ
  * from the 4-byte-load kernels' in rounding, as any two tilings can, and stay
- * within the same bound).  The first call that needs a workspace must not be
- * made while the stream is being captured into a CUDA graph.  One workspace is
+ * within the same bound).  A call made while the stream is being captured into a
+ * CUDA graph leaves the workspace's address in the graph: from then on that buffer
+ * stays where it is until sgemm_shutdown, also when a larger one replaces it for
+ * later calls (and an allocation during a capture is not the graph's).  Graphs
+ * captured on one stream share its workspace, so they must not be replayed at the
+ * same time, nor beside calls on that stream; the _ws forms have no such limit.
+ * One workspace is
  * kept for every (device, stream handle) that needed one, until sgemm_shutdown;
  * a program that cycles through many short-lived streams is better served by
  * sgemm_run_ws or sgemm_run_noalloc.  The product kernel is launched as a
@@ -401,7 +406,8 @@ SGEMM_API int sgemm_norm_forward(int rows, int cols, int dtype, const void* bloc
  * dx is the gradient of `residual` (it may be NULL without dh: it is dy).  Without
  * `block` only dx and dnext_weight are computed.  dgate, dweight and dnext_weight may be
  * NULL.  The sums over rows are deterministic (a fixed order, no atomics) and use the
- * library's workspace of the stream.  rows == 0 writes zeros to them. */
+ * library's workspace of the stream (see sgemm_run, also on CUDA graphs).  rows == 0
+ * writes zeros to them. */
 SGEMM_API int sgemm_norm_backward(int rows, int cols, int dtype, const void* dy, int lddy,
                                   const void* dh, int lddh, const void* y, int ldy,
                                   const float* next_rstd, const void* next_weight,
@@ -410,6 +416,22 @@ SGEMM_API int sgemm_norm_backward(int rows, int cols, int dtype, const void* dy,
                                   float scale, void* dx, int lddx, void* dblock, int lddb,
                                   void* dgate, int lddg, float* dweight, float* dnext_weight,
                                   sgemm_stream_t stream);
+
+/* The same in a caller-owned device workspace: 16-byte aligned, at least as many bytes as
+ * sgemm_norm_backward_workspace gives for these sizes on the current device (for
+ * any types and strides); it may be NULL where none of dweight, dnext_weight and a shared
+ * gate's dgate is asked for.  It needs no initialisation and must stay untouched by
+ * other work while the call runs.  SGEMM_ERR_WORKSPACE if it is missing or too small. */
+SGEMM_API int sgemm_norm_backward_workspace(int rows, int cols, size_t* bytes);
+SGEMM_API int sgemm_norm_backward_ws(int rows, int cols, int dtype, const void* dy, int lddy,
+                                     const void* dh, int lddh, const void* y, int ldy,
+                                     const float* next_rstd, const void* next_weight,
+                                     const void* block, int ldb, const float* rstd,
+                                     const void* weight, int weight_dtype, const void* gate,
+                                     int ldg, float scale, void* dx, int lddx, void* dblock,
+                                     int lddb, void* dgate, int lddg, float* dweight,
+                                     float* dnext_weight, void* ws, size_t ws_bytes,
+                                     sgemm_stream_t stream);
 
 /* Synchronous: reads and clears the device flag that a bounded wait in a
  * tensor-core kernel sets when it gives up; returns SGEMM_ERR_TIMEOUT if it was
