@@ -199,6 +199,8 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax, const TensorScale
         const float a = __uint_as_float(amax);
         // Above 448 every quotient gives 448, so one past 512 may as well be 512.
         if (t.usual) return e4m3_encode(divide(fminf(a, t.cap), t.six, t.r));
+        // Zeros whatever the tensor's scale, and nothing but zeros where that is 0.
+        if (a == 0.0f || t.six == 0.0f) return 0u;
         return e4m3_encode(quotient(a, t.six));
     }
     const uint32_t e = amax >> 23;

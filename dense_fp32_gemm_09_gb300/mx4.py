@@ -103,8 +103,9 @@ class Mx4:
 def mx4_quantize(x, fmt: str = "nvfp4", *, tensor_scale=None, stream=None) -> Mx4:
     """Quantises the rows of a 2-D float32, bfloat16 or float16 CUDA view.  A view with
     unit row stride (``x.t()``) is read as the transpose that it is, without a copy.
-    ``tensor_scale`` (nvfp4 only) is one positive float32 on the device: usually
-    amax(x) / (6 * 448), which puts the largest block scale at the top of e4m3."""
+    ``tensor_scale`` (nvfp4 only) is one float32 >= 0 on the device: usually amax(x) / (6 * 448),
+    which puts the largest block scale at the top of e4m3.  Where that is 0, as for a matrix
+    of zeros, every number held is 0."""
     code = _format(fmt)
     if stream is None:
         both = _t.fast().mx4_quantize(x, code, tensor_scale)

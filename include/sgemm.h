@@ -325,7 +325,8 @@ SGEMM_API int sgemm_tf32x3_multiply(int M, int N, int K, float alpha, float beta
  *                matrix (a device float; NULL means 1): value = code * s * ts.
  *                s = amax / (6 ts) rounded to e4m3, at most 448; codes are x / (s ts)
  *                rounded to the nearest e2m1 value (ties to even, at most 6).  A
- *                block whose scale rounds to 0 has codes 0.
+ *                block whose scale rounds to 0 has codes 0.  With ts = 0 (what amax / 2688 is of
+ *                a matrix of zeros) every scale and code is 0.
  *   SGEMM_MXFP4  blocks of 32, scale 2^e with e = floor(log2 amax) - 2, at least -127:
  *                value = code * 2^e; codes are x / 2^e rounded the same way.
  *

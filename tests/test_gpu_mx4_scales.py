@@ -1,0 +1,69 @@
+"""Tensor scales at the ends of their range."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_mx4 import DTYPES, sample, sg  # noqa: F401  (sg: fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def held(q):
+    return q.dequantize().double().cpu()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 40), (130, 200), (64, 1024)])
+def test_zeros_with_their_own_scale(sg, rows, cols, dtype):  # noqa: F811
+    """amax(x) / 2688 of zeros is 0: zeros are held, and products with them are 0."""
+    x = torch.zeros(rows, cols, dtype=DTYPES[dtype], device="cuda")
+    ts = (x.abs().amax().float() / (6 * 448)).view(1)
+    w = sg.mx4_quantize(sample(70, cols, "bf16", 3).cuda())
+    for q in (sg.mx4_quantize(x, tensor_scale=ts),
+              sg.mx4_quantize(x.t().contiguous().t(), tensor_scale=ts)):
+        assert not bool(held(q).any())
+        rows_of = lambda b, order, n: b.permute(order).reshape(-1, n)[:rows]
+        assert not bool(rows_of(q.codes, (0, 2, 1, 3), q.codes.shape[1] * 16).any())
+        assert not bool(rows_of(q.scales, (0, 3, 2, 1, 4), q.scales.shape[1] * 4).any())
+        c = sg.mx4_matmul(q, w)
+        assert c.shape == (rows, 70) and not bool(c.any())
+        assert not bool(sg.mx4_matmul(w, q).any())
+
+
+@pytest.mark.parametrize("ts", [0.0, -0.0])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_scale_of_zero_holds_zeros(sg, dtype, ts):  # noqa: F811
+    """Whatever the numbers; a block with a NaN or an infinity is NaN as always."""
+    x = sample(70, 200, dtype, 5)
+    x[3, 20], x[5, 199] = float("nan"), float("inf")
+    t = torch.tensor([ts], device="cuda")
+    for v in (x.cuda(), x.t().contiguous().cuda().t()):
+        got = held(sg.mx4_quantize(v, tensor_scale=t))
+        want = torch.zeros(70, 200, dtype=torch.float64)
+        want[3, 16:32], want[5, 192:] = float("nan"), float("nan")
+        assert torch.equal(got.isnan(), want.isnan()) and not bool(got.nan_to_num().any())
+
+
+@pytest.mark.parametrize("ts", [0.0, 3e-39, 1e-45, float("inf")])
+def test_zero_blocks_stay_zero(sg, ts):  # noqa: F811
+    """Blocks of zeros have scale 0 under any tensor scale."""
+    x = torch.zeros(40, 96)
+    x[::2, 32:48] = torch.randn(20, 16) * 1e-37
+    q = sg.mx4_quantize(x.cuda(), tensor_scale=torch.tensor([ts], device="cuda"))
+    s = q.scales.permute(0, 3, 2, 1, 4).reshape(-1, q.scales.shape[1] * 4)[:40].cpu()
+    assert not bool(s[:, [0, 1, 3, 4, 5, 6, 7]].any()) and not bool(s[1::2].any())
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(5, 512), (400, 512), (400, 264), (6, 9001), (3, 20001), (400, 77)])
+def test_norms_of_zero_scale(sg, rows, cols, dtype):  # noqa: F811
+    """The norms quantise by the same rule in each of their kernels."""
+    x = torch.randn(rows, cols).to(DTYPES[dtype]).cuda()
+    x[1] = 0
+    t = torch.zeros(1, device="cuda")
+    h, _ = sg.norm_before(x, quantize="nvfp4", tensor_scale=t)
+    _, _, h2, _ = sg.norm_after(x, torch.zeros_like(x), quantize="nvfp4", tensor_scale=t)
+    for q in (h, h2):
+        assert not bool(held(q).any())
+    y = sg.mx4_matmul(h, sg.mx4_quantize(torch.ones(33, cols, device="cuda")))
+    assert np.array_equal(y.cpu().numpy(), np.zeros((rows, 33)))
