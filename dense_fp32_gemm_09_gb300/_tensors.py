@@ -125,10 +125,6 @@ def checked(result, name: str) -> None:
         check(result, name)
 
 
-def current(device) -> bool:
-    return _current_device() == device.index
-
-
 _functions = {}
 
 

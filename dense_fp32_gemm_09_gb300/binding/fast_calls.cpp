@@ -115,9 +115,12 @@ int gate_ld(const at::Tensor& g, const Shape& s) {
 long long code_bytes(long long rows, long long cols) {
     return (rows + 127) / 128 * ((cols + 127) / 128) * 8192;
 }
-at::Tensor stored(long long rows, long long cols, int format) {
+long long stored_bytes(long long rows, long long cols, int format) {
     const long long codes = code_bytes(rows, cols);
-    return empty({codes + codes / (format == SGEMM_NVFP4 ? 8 : 16)}, at::kByte);
+    return codes + codes / (format == SGEMM_NVFP4 ? 8 : 16);
+}
+at::Tensor stored(long long rows, long long cols, int format) {
+    return empty({stored_bytes(rows, cols, format)}, at::kByte);
 }
 PyObject* status(int st) { return PyLong_FromLong(st); }
 
@@ -144,59 +147,59 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// stored_addresses(codes, scales, rows, cols, format, tensor_scale) -> (address, address, address or None)
-// of a matrix whose buffers have the right types and shapes
-PyObject* stored_addresses(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// Whether these buffers hold a rows x cols matrix: codes and scales, or both in one (no scales).
+bool holds(const at::Tensor& codes, const at::Tensor& scales, const at::Tensor& ts, long long rows,
+           long long cols, int format) {
+    if (!codes.defined() || rows < 0 || cols < 0 || codes.scalar_type() != at::kByte ||
+        !codes.is_contiguous() || !here(codes) || !one_float(ts, format))
+        return false;
+    if (!scales.defined()) return codes.dim() == 1 && codes.size(0) == stored_bytes(rows, cols, format);
+    const long long rb = (rows + 127) / 128, cb = (cols + 127) / 128;
+    const long long groups = cb * (format == SGEMM_NVFP4 ? 2 : 1);
+    return codes.dim() == 4 && codes.size(0) == rb && codes.size(1) == 4 * cb &&
+           codes.size(2) == 128 && codes.size(3) == 16 && scales.scalar_type() == at::kByte &&
+           scales.dim() == 5 && scales.size(0) == rb && scales.size(1) == groups &&
+           scales.size(2) == 32 && scales.size(3) == 4 && scales.size(4) == 4 &&
+           scales.is_contiguous() && here(scales);
+}
+// Addresses of a matrix given as (codes, scales, tensor_scale), looked up in each call: a
+// tensor's memory may be another one by the next.
+bool stored_at(PyObject* t, long long rows, long long cols, int format, const void* (&p)[3]) {
+    at::Tensor codes, scales, ts;
+    if (!PyTuple_Check(t) || PyTuple_GET_SIZE(t) != 3 || !tensor(PyTuple_GET_ITEM(t, 0), &codes) ||
+        !tensor(PyTuple_GET_ITEM(t, 1), &scales) || !tensor(PyTuple_GET_ITEM(t, 2), &ts) ||
+        !holds(codes, scales, ts, rows, cols, format))
+        return false;
+    p[0] = codes.data_ptr();
+    p[1] = scales.defined() ? scales.data_ptr()
+                            : static_cast<uint8_t*>(codes.data_ptr()) + code_bytes(rows, cols);
+    p[2] = ptr(ts);
+    return true;
+}
+
+// mx4_holds((codes, scales, tensor_scale), rows, cols, format) -> True or None
+PyObject* mx4_holds(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        at::Tensor codes, scales, ts;
-        if (n != 6 || !tensor(a[0], &codes) || !tensor(a[1], &scales) || !tensor(a[5], &ts) ||
-            !codes.defined() || !scales.defined())
-            return not_here();
-        const long long rows = PyLong_AsLongLong(a[2]), cols = PyLong_AsLongLong(a[3]);
-        const int format = static_cast<int>(PyLong_AsLong(a[4]));
+        if (n != 4) return not_here();
+        const long long rows = PyLong_AsLongLong(a[1]), cols = PyLong_AsLongLong(a[2]);
+        const int format = static_cast<int>(PyLong_AsLong(a[3]));
         if (PyErr_Occurred()) return nullptr;
-        const long long rb = (rows + 127) / 128, cb = (cols + 127) / 128;
-        const long long groups = cb * (format == SGEMM_NVFP4 ? 2 : 1);
-        if (rows < 0 || cols < 0 || codes.scalar_type() != at::kByte || codes.dim() != 4 ||
-            codes.size(0) != rb || codes.size(1) != 4 * cb || codes.size(2) != 128 ||
-            codes.size(3) != 16 || !codes.is_contiguous() || scales.scalar_type() != at::kByte ||
-            scales.dim() != 5 || scales.size(0) != rb || scales.size(1) != groups ||
-            scales.size(2) != 32 || scales.size(3) != 4 || scales.size(4) != 4 ||
-            !scales.is_contiguous() || !here(codes) || !here(scales) || !one_float(ts, format))
-            return not_here();
-        PyObject* r = PyTuple_New(3);
-        if (!r) return nullptr;
-        const at::Tensor* all[] = {&codes, &scales, &ts};
-        for (int i = 0; i < 3; ++i) {
-            PyObject* o = all[i]->defined() ? PyLong_FromVoidPtr(all[i]->data_ptr()) : nullptr;
-            if (!o) {
-                Py_INCREF(Py_None);
-                o = Py_None;
-            }
-            PyTuple_SET_ITEM(r, i, o);
-        }
-        return r;
+        const void* p[3];
+        if (!stored_at(a[0], rows, cols, format, p)) return not_here();
+        Py_RETURN_TRUE;
     });
 }
 
-bool address(PyObject* o, const void** p) {
-    *p = o == Py_None ? nullptr : PyLong_AsVoidPtr(o);
-    return !PyErr_Occurred();
-}
-bool addresses(PyObject* t, const void* (&p)[3]) {
-    return PyTuple_Check(t) && PyTuple_GET_SIZE(t) == 3 &&
-           address(PyTuple_GET_ITEM(t, 0), &p[0]) && address(PyTuple_GET_ITEM(t, 1), &p[1]) &&
-           address(PyTuple_GET_ITEM(t, 2), &p[2]);
-}
-
-// mx4_dequantize(addresses, rows, cols, format, dtype code) -> tensor
+// mx4_dequantize(stored, rows, cols, format, dtype code) -> tensor
 PyObject* mx4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        const void* p[3];
-        if (n != 5 || !addresses(a[0], p)) return PyErr_Occurred() ? nullptr : not_here();
+        if (n != 5) return not_here();
         const long rows = PyLong_AsLong(a[1]), cols = PyLong_AsLong(a[2]);
         const int format = static_cast<int>(PyLong_AsLong(a[3]));
         const int dt = static_cast<int>(PyLong_AsLong(a[4]));
+        if (PyErr_Occurred()) return nullptr;
+        const void* p[3];
+        if (!stored_at(a[0], rows, cols, format, p)) return not_here();
         at::Tensor y = empty({rows, cols}, dtype_of(dt));
         const int st = f_dequantize(rows, cols, format, p[0], p[1], static_cast<const float*>(p[2]),
                                     dt, y.data_ptr(), std::max(cols, 1L), stream());
@@ -204,17 +207,18 @@ PyObject* mx4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// mx4_matmul(a addresses, b addresses, M, N, K, format, alpha, dtype code) -> tensor
+// mx4_matmul(stored a, stored b, M, N, K, format, alpha, dtype code) -> tensor
 PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded([&]() -> PyObject* {
-        const void *p[3], *q[3];
-        if (n != 8 || !addresses(a[0], p) || !addresses(a[1], q))
-            return PyErr_Occurred() ? nullptr : not_here();
+        if (n != 8) return not_here();
         const long M = PyLong_AsLong(a[2]), N = PyLong_AsLong(a[3]), K = PyLong_AsLong(a[4]);
         const int format = static_cast<int>(PyLong_AsLong(a[5]));
         const float alpha = static_cast<float>(PyFloat_AsDouble(a[6]));
         const int dt = static_cast<int>(PyLong_AsLong(a[7]));
         if (PyErr_Occurred()) return nullptr;
+        const void *p[3], *q[3];
+        if (!stored_at(a[0], M, K, format, p) || !stored_at(a[1], N, K, format, q))
+            return not_here();
         at::Tensor c = empty({M, N}, dtype_of(dt));
         const int st = f_matmul(M, N, K, format, alpha, p[0], p[1],
                                 static_cast<const float*>(p[2]), q[0], q[1],
@@ -347,7 +351,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {METHOD(bind), METHOD(stored_addresses), METHOD(mx4_quantize), METHOD(mx4_dequantize),
+PyMethodDef kMethods[] = {METHOD(bind), METHOD(mx4_holds), METHOD(mx4_quantize), METHOD(mx4_dequantize),
                           METHOD(mx4_matmul), METHOD(norm_forward), METHOD(norm_backward),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fast_calls", nullptr, -1, kMethods,

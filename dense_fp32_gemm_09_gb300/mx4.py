@@ -31,28 +31,17 @@ def _format(fmt) -> int:
 
 class Mx4:
     """A quantised rows x cols matrix: its two buffers, its format and, for nvfp4, the
-    scale of the whole tensor (one float32 on the device, None for 1)."""
+    scale of the whole tensor (one float32 on the device, None for 1).  Its shape, format and
+    buffers stay; ``tensor_scale`` may be set, which scales the numbers held."""
 
-    __slots__ = ("rows", "cols", "fmt", "tensor_scale", "device", "_codes", "_scales", "_both",
-                 "_ptrs")
+    __slots__ = ("_rows", "_cols", "_fmt", "_ts", "_codes", "_scales", "_both")
 
     def __init__(self, codes, scales, rows: int, cols: int, fmt: str, tensor_scale=None):
-        ptrs = _t.fast().stored_addresses(codes, scales, rows, cols, _format(fmt), tensor_scale)
-        if ptrs is None:          # another device, or something to refuse
-            for t, name, shape in zip((codes, scales), ("codes", "scales"),
-                                      mx4_shapes(rows, cols, fmt)):
-                _t.cuda_tensor(t, name)
-                if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
-                    raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
-            _t.same_device(scales, "scales", codes.device)
-            if tensor_scale is not None:
-                if fmt != "nvfp4":
-                    raise ValueError("only nvfp4 has a tensor scale")
-                _t.one_float(tensor_scale, "tensor_scale", codes.device)
-            ptrs = codes.data_ptr(), scales.data_ptr(), _t.ptr(tensor_scale)
-        self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
-        self.device = codes.device
-        self._codes, self._scales, self._both, self._ptrs = codes, scales, None, ptrs
+        code = _format(fmt)
+        self._rows, self._cols, self._fmt, self._ts = rows, cols, fmt, tensor_scale
+        self._codes, self._scales, self._both = codes, scales, None
+        if scales is None or _t.fast().mx4_holds(self._stored(), rows, cols, code) is None:
+            self._addresses()          # on another device, or something to refuse
 
     @classmethod
     def _new(cls, call, rows: int, cols: int, fmt: str, tensor_scale):
@@ -65,33 +54,80 @@ class Mx4:
     def _of(cls, both, rows: int, cols: int, fmt: str, tensor_scale):
         """The matrix in one buffer, codes first."""
         q = cls.__new__(cls)
-        at = both.data_ptr()
-        q.rows, q.cols, q.fmt, q.tensor_scale, q.device = rows, cols, fmt, tensor_scale, both.device
+        q._rows, q._cols, q._fmt, q._ts = rows, cols, fmt, tensor_scale
         q._codes, q._scales, q._both = None, None, both
-        q._ptrs = (at, at + -(-rows // 128) * -(-cols // 128) * 8192,
-                   None if tensor_scale is None else tensor_scale.data_ptr())
         return q
 
+    def _stored(self):
+        """The tensors as the binding takes them: (codes, scales, tensor scale), or both
+        buffers in one and no scales."""
+        if self._both is not None:
+            return self._both, None, self._ts
+        return self._codes, self._scales, self._ts
+
+    def _addresses(self):
+        """(codes, scales, tensor scale) as the library takes them, of buffers that fit."""
+        shapes = mx4_shapes(self._rows, self._cols, self._fmt)
+        if self._both is not None:
+            sizes = [math.prod(shape) for shape in shapes]
+            if self._both.dtype != torch.uint8 or self._both.shape != (sum(sizes),):
+                raise ValueError("the matrix's buffer is not the one it was made with")
+            at = self._both.data_ptr()
+            return at, at + sizes[0], _t.ptr(self._scale_of(self._ts))
+        for t, name, shape in zip((self._codes, self._scales), ("codes", "scales"), shapes):
+            _t.cuda_tensor(t, name)
+            if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}")
+        _t.same_device(self._scales, "scales", self._codes.device)
+        return self._codes.data_ptr(), self._scales.data_ptr(), _t.ptr(self._scale_of(self._ts))
+
+    def _scale_of(self, t):
+        if t is not None and self._fmt != "nvfp4":
+            raise ValueError("only nvfp4 has a tensor scale")
+        return _t.one_float(t, "tensor_scale", self.device)
+
+    @property
+    def rows(self):
+        return self._rows
+
+    @property
+    def cols(self):
+        return self._cols
+
+    @property
+    def fmt(self):
+        return self._fmt
+
+    @property
+    def device(self):
+        return (self._codes if self._both is None else self._both).device
+
+    @property
+    def tensor_scale(self):
+        return self._ts
+
+    @tensor_scale.setter
+    def tensor_scale(self, t):
+        self._ts = self._scale_of(t)
+
     def _views(self):
-        if self._codes is None:
-            codes, scales = mx4_shapes(self.rows, self.cols, self.fmt)
-            n = math.prod(codes)
-            self._codes = self._both[:n].view(codes)
-            self._scales = self._both[n:].view(scales)
+        if self._both is None:
+            return self._codes, self._scales
+        codes, scales = mx4_shapes(self._rows, self._cols, self._fmt)
+        n = math.prod(codes)
+        return self._both[:n].view(codes), self._both[n:].view(scales)
 
     @property
     def codes(self):
-        self._views()
-        return self._codes
+        return self._views()[0]
 
     @property
     def scales(self):
-        self._views()
-        return self._scales
+        return self._views()[1]
 
     @property
     def shape(self):
-        return self.rows, self.cols
+        return self._rows, self._cols
 
     def dequantize(self, dtype=torch.float32, *, stream=None):
         return mx4_dequantize(self, dtype, stream=stream)
@@ -126,7 +162,7 @@ def mx4_quantize(x, fmt: str = "nvfp4", *, tensor_scale=None, stream=None) -> Mx
         _t.one_float(tensor_scale, "tensor_scale", device)
     call = _t.Call(device, stream)
     q = Mx4._new(call, rows, cols, fmt, tensor_scale)
-    codes, scales, ts = q._ptrs
+    codes, scales, ts = q._addresses()
     call.run("sgemm_mx4_quantize", trans, rows, cols, dt, x.data_ptr(), ld, code, ts, codes, scales)
     return q
 
@@ -135,11 +171,12 @@ def mx4_dequantize(q: Mx4, dtype=torch.float32, out=None, *, stream=None):
     """The rows x cols numbers that `q` holds, rounded once to `dtype` (or into ``out``)."""
     if not isinstance(q, Mx4):
         raise TypeError("q must be an Mx4")
-    if stream is None and out is None and _t.current(q.device):
-        out = _t.fast().mx4_dequantize(q._ptrs, q.rows, q.cols, FORMATS[q.fmt],
+    if stream is None and out is None:
+        out = _t.fast().mx4_dequantize(q._stored(), q._rows, q._cols, FORMATS[q._fmt],
                                        _t.dtype_code(dtype, "dtype"))
-        _t.checked(out, "sgemm_mx4_dequantize")
-        return out
+        if out is not None:
+            _t.checked(out, "sgemm_mx4_dequantize")
+            return out
     call = _t.Call(q.device, stream)
     if out is None:
         dt, ld = _t.dtype_code(dtype, "dtype"), max(q.cols, 1)
@@ -147,7 +184,7 @@ def mx4_dequantize(q: Mx4, dtype=torch.float32, out=None, *, stream=None):
     else:
         ld = _t.matrix(out, "out", q.shape, None, q.device)
         dt = _t.dtype_code(out.dtype, "out")
-    codes, scales, ts = q._ptrs
+    codes, scales, ts = q._addresses()
     call.run("sgemm_mx4_dequantize", q.rows, q.cols, FORMATS[q.fmt], codes, scales, ts, dt,
              out.data_ptr(), ld)
     return out
@@ -161,18 +198,19 @@ def mx4_matmul(a: Mx4, b: Mx4, out=None, *, dtype=torch.float32, alpha: float = 
     beta == 0 it is only written, otherwise it is the C of the formula."""
     if not isinstance(a, Mx4) or not isinstance(b, Mx4):
         raise TypeError("a and b must be Mx4")
-    if a.cols != b.cols:
+    if a._cols != b._cols:
         raise ValueError(f"inner dimensions differ: a is {a.shape}, b is {b.shape}")
-    if a.fmt != b.fmt:
+    if a._fmt != b._fmt:
         raise ValueError(f"formats differ: a is {a.fmt}, b is {b.fmt}")
+    M, N = a._rows, b._rows
+    if stream is None and out is None and beta == 0.0:
+        out = _t.fast().mx4_matmul(a._stored(), b._stored(), M, N, a._cols, FORMATS[a._fmt], alpha,
+                                   _t.dtype_code(dtype, "dtype"))
+        if out is not None:
+            _t.checked(out, "sgemm_mx4_matmul")
+            return out
     if a.device != b.device:
         raise ValueError(f"a and b must be on one device: {a.device}, {b.device}")
-    M, N = a.rows, b.rows
-    if stream is None and out is None and beta == 0.0 and _t.current(a.device):
-        out = _t.fast().mx4_matmul(a._ptrs, b._ptrs, M, N, a.cols, FORMATS[a.fmt], alpha,
-                                   _t.dtype_code(dtype, "dtype"))
-        _t.checked(out, "sgemm_mx4_matmul")
-        return out
     call = _t.Call(a.device, stream)
     if out is None:
         if beta != 0.0:
@@ -182,8 +220,8 @@ def mx4_matmul(a: Mx4, b: Mx4, out=None, *, dtype=torch.float32, alpha: float = 
     else:
         ld = _t.matrix(out, "out", (M, N), None, a.device)
         dt = _t.dtype_code(out.dtype, "out")
-    a_codes, a_scales, a_ts = a._ptrs
-    b_codes, b_scales, b_ts = b._ptrs
+    a_codes, a_scales, a_ts = a._addresses()
+    b_codes, b_scales, b_ts = b._addresses()
     call.run("sgemm_mx4_matmul", M, N, a.cols, FORMATS[a.fmt], alpha, a_codes, a_scales, a_ts,
              b_codes, b_scales, b_ts, beta, dt, out.data_ptr(), ld)
     return out

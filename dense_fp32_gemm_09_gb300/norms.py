@@ -89,10 +89,11 @@ def _forward(stream, x, block, weight, gate, scale, eps, next_norm, next_weight,
                 raise ValueError("only nvfp4 has a tensor scale")
             ts = _t.one_float(tensor_scale, "tensor_scale", x.device)
             q = _mx4.Mx4._new(call, rows, cols, quantize, ts)
+    codes, scales, _ = (None, None, None) if q is None else q._addresses()
     call.run("sgemm_norm_forward", rows, cols, dt, _t.ptr(block), ldb, x.data_ptr(), ldr,
              _t.ptr(weight), _t.ptr(next_weight), wt, _t.ptr(gate), ldg, scale, eps, _t.ptr(y),
              cols, _t.ptr(rstd), int(next_norm), _t.ptr(h), cols, _t.ptr(next_rstd), fmt,
-             _t.ptr(ts), q and q._ptrs[0], q and q._ptrs[1])
+             _t.ptr(ts), codes, scales)
     return y, rstd, h if q is None else q, next_rstd
 
 
