@@ -164,11 +164,25 @@ __device__ __forceinline__ float reciprocal(float v) {      // within an ulp
 }
 static __device__ __noinline__ float quotient(float x, float d) { return __fdiv_rn(x, d); }
 
-// x / d correctly rounded from r, the reciprocal of d to an ulp: q0 = x r, then
-// q0 - r (q0 d - x), whose remainder an FMA gives exactly (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000", 1990).  Three instructions instead of
-// a division, which alone would take longer than the memory.  x and the quotient must
-// be far from the ends of the range; the signs keep a quotient of -0.
+// x / d from r, the reciprocal of d within an ulp: q0 = x r, then q0 - r (q0 d - x) (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000", 1990).  Three instructions
+// instead of a division, which alone would take longer than the memory.  x and the
+// quotient must be far from the ends of the range; the signs keep a quotient of -0.
+//
+// With such an r the result is not always the rounded quotient, but it falls on the same side
+// of every boundary between codes (or scales), and on it in the same cases, unless d is
+// excluded below.  Before its last rounding it is off by less than 17 / (2 D) ulp, D being the
+// 24-bit significand of d (q0 is within 3 ulp; r's error and the remainder's rounding follow).
+// So it misjudges a boundary m only if x / d lies that near to one of the points half an ulp
+// beside m, (2 Q + 1) / 2 ulp with Q the significand of m: 2^s X = (2 Q + 1) D + j with X the
+// significand of x, s 24 or 25, 0 < |j| < 17.  A boundary between codes has three significant
+// bits, one between e4m3 scales five, so Q is a multiple of 2^21, or 2^19, or (below a power of
+// two) 2^24 - 1, and D is j or -j modulo 2^22, or 2^20.
+constexpr uint32_t kCodeBoundaries = (1u << 22) - 1, kScaleBoundaries = (1u << 20) - 1;
+__device__ __forceinline__ bool judges(float d, uint32_t mask) {
+    const uint32_t low = __float_as_uint(d) & mask;
+    return low == 0 || ((low + 32) & mask) > 64;
+}
 __device__ __forceinline__ float divide(float x, float d, float r) {
     const float q = x * r;
     return fmaf(fmaf(q, d, -x), -r, q);
@@ -181,7 +195,7 @@ struct TensorScale {
     __device__ __forceinline__ explicit TensorScale(const float* p) {
         ts = p ? __ldg(p) : 1.0f;
         six = 6.0f * ts;
-        usual = six > 0x1p-90f && six < 0x1p90f;
+        usual = six > 0x1p-90f && six < 0x1p90f && judges(six, kScaleBoundaries);
         r = reciprocal(six);
         cap = 512.0f * six;
     }
@@ -207,9 +221,10 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax, const TensorScale
     return e == 255 ? 255u : e < 2 ? 0u : e - 2;
 }
 
-// How numbers of a block are divided by its scale d = value of `byte` (* ts), correctly
-// rounded.  mxfp4: times 2^-e, exact.  nvfp4: divide() where the remainder stays in the
-// normal range and the quotient finite (a scale below the top of e4m3), else a division.
+// How numbers of a block are divided by its scale d = value of `byte` (* ts); codes are those
+// of the correctly rounded quotient.  mxfp4: times 2^-e, exact.  nvfp4: divide() where it judges
+// rightly, the remainder stays in the normal range and the quotient is finite (a scale below
+// the top of e4m3), else a division.
 template <int FORMAT>
 struct Divider {
     float d, r;
@@ -218,7 +233,7 @@ struct Divider {
         if (FORMAT == kNvfp4) {
             d = e4m3_decode(byte) * t.ts;
             r = reciprocal(d);
-            fast = d > 0x1p-90f && d < 0x1p90f && byte < 0x7Eu;
+            fast = d > 0x1p-90f && d < 0x1p90f && byte < 0x7Eu && judges(d, kCodeBoundaries);
         } else {
             d = 0.0f;
             r = __uint_as_float((254u - byte) << 23);

@@ -1,9 +1,10 @@
-"""Tensor scales at the ends of their range."""
+"""Tensor scales at the ends of their range, and those whose quotients are hardest."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_mx4 import DTYPES, sample, sg  # noqa: F401  (sg: fixture)
+import mx4_reference as ref
+from test_gpu_mx4 import DTYPES, check_stored, sample, sg  # noqa: F401  (sg: fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,42 @@ def test_norms_of_zero_scale(sg, rows, cols, dtype):  # noqa: F811
         assert not bool(held(q).any())
     y = sg.mx4_matmul(h, sg.mx4_quantize(torch.ones(33, cols, device="cuda")))
     assert np.array_equal(y.cpu().numpy(), np.zeros((rows, 33)))
+
+
+def around(v, steps=4):
+    """fp32 numbers next to each of v."""
+    out, lo, hi = [v], v, v
+    for _ in range(steps):
+        lo, hi = np.nextafter(lo, np.float32(0)), np.nextafter(hi, np.float32(1e30))
+        out += [lo, hi]
+    return np.concatenate(out)
+
+
+@pytest.mark.parametrize("base", [1 << 23, 3 << 22, 1 << 24])
+def test_quotients_of_the_hardest_divisors(sg, base):  # noqa: F811
+    """Scales next to the significands where a quotient is nearest to a tie without being one."""
+    mids = ((ref.E2M1[1:] + ref.E2M1[:-1]) / 2).astype(np.float32)
+    for j in [j for j in range(-34, 35) if 1 << 23 <= base + j < 1 << 24]:
+        ts = np.float32((base + j) * 2.0 ** -23)
+        v = around(mids * ts)
+        v = np.concatenate([v, -v, v])[:126 // 15 * 15]
+        x = np.concatenate([np.full((len(v) // 15, 1), 6 * ts, np.float32), v.reshape(-1, 15)], 1)
+        check_stored(sg.mx4_quantize(torch.from_numpy(x).cuda(),
+                                     tensor_scale=torch.tensor([ts], device="cuda")),
+                     torch.from_numpy(x), "nvfp4", ts)
+
+
+@pytest.mark.parametrize("base", [i << 20 for i in range(8, 17)])
+def test_block_scales_of_the_hardest_divisors(sg, base):  # noqa: F811
+    """The same for the block's scale, amax / (6 ts)."""
+    mids = ((ref.E4M3[1:] + ref.E4M3[:-1]) / 2).astype(np.float32)
+    for j in [j for j in range(-34, 35, 3) if 1 << 23 <= base + j < 1 << 24]:
+        six = np.float32((base + j) * 2.0 ** -23)
+        ts = np.float32(six / np.float32(6))
+        for t in (np.nextafter(ts, np.float32(0)), ts, np.nextafter(ts, np.float32(9))):
+            x = np.zeros((len(mids) * 9, 16), np.float32)
+            x[:, 5] = around(mids * (np.float32(6) * t))
+            x[:, 9] = -x[:, 5] / 3
+            check_stored(sg.mx4_quantize(torch.from_numpy(x).cuda(),
+                                         tensor_scale=torch.tensor([t], device="cuda")),
+                         torch.from_numpy(x), "nvfp4", t)
