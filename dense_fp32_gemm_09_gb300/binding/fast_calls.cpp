@@ -58,7 +58,19 @@ bool here(const at::Tensor& t) {
 sgemm_stream_t stream() {
     return reinterpret_cast<sgemm_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
 }
+// Without Python's lock, as torch's own calls and those through ctypes: a launch waits where the
+// queue is full, possibly for something that another thread of the program is to do.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename... P, typename... A>
+int unlocked(int (*f)(P...), A... a) {
+    const Unlocked u;
+    return f(a...);
+}
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type) {
+    const Unlocked u;
     return at::detail::empty_cuda(
         size, type, c10::Device(c10::DeviceType::CUDA, c10::cuda::current_device()), std::nullopt);
 }
@@ -141,7 +153,8 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (ld < width || ld > INT_MAX) return not_here();
         at::Tensor q = stored(rows, cols, format);
         uint8_t* p = static_cast<uint8_t*>(q.data_ptr());
-        const int st = f_quantize(trans, rows, cols, dt, x.data_ptr(), ld, format,
+        const int st = unlocked(
+            f_quantize, trans, rows, cols, dt, x.data_ptr(), ld, format,
                                   static_cast<const float*>(ptr(ts)), p, p + code_bytes(rows, cols),
                                   stream());
         return st ? status(st) : wrap(q);
@@ -202,7 +215,8 @@ PyObject* mx4_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const void* p[3];
         if (!stored_at(a[0], rows, cols, format, p)) return not_here();
         at::Tensor y = empty({rows, cols}, dtype_of(dt));
-        const int st = f_dequantize(rows, cols, format, p[0], p[1], static_cast<const float*>(p[2]),
+        const int st = unlocked(
+            f_dequantize, rows, cols, format, p[0], p[1], static_cast<const float*>(p[2]),
                                     dt, y.data_ptr(), std::max(cols, 1L), stream());
         return st ? status(st) : wrap(y);
     });
@@ -221,7 +235,8 @@ PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!stored_at(a[0], M, K, format, p) || !stored_at(a[1], N, K, format, q))
             return not_here();
         at::Tensor c = empty({M, N}, dtype_of(dt));
-        const int st = f_matmul(M, N, K, format, alpha, p[0], p[1],
+        const int st = unlocked(
+            f_matmul, M, N, K, format, alpha, p[0], p[1],
                                 static_cast<const float*>(p[2]), q[0], q[1],
                                 static_cast<const float*>(q[2]), 0.0f, dt, c.data_ptr(),
                                 std::max(N, 1L), stream());
@@ -274,8 +289,8 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             h = format < 0 ? empty({s.rows, s.cols}, s.type) : stored(s.rows, s.cols, format);
             if (format >= 0) codes = static_cast<uint8_t*>(h.data_ptr());
         }
-        const int st = f_forward(
-            s.rows, s.cols, dt, ptr(block), ldb, x.data_ptr(), ldr, ptr(weight), ptr(next_weight),
+        const int st = unlocked(
+            f_forward, s.rows, s.cols, dt, ptr(block), ldb, x.data_ptr(), ldr, ptr(weight), ptr(next_weight),
             wt, ptr(gate), ldg, scale, eps, ptr(y), s.cols, static_cast<float*>(ptr(rstd)), next,
             codes ? nullptr : ptr(h), s.cols, static_cast<float*>(ptr(next_rstd)), format,
             static_cast<const float*>(ptr(ts)), codes,
@@ -323,8 +338,8 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
             if (const int st = f_backward_workspace(s.rows, s.cols, &ws_bytes)) return status(st);
             ws = empty({static_cast<int64_t>(ws_bytes)}, at::kByte);
         }
-        const int st = f_backward(
-            s.rows, s.cols, dt, ptr(dy), lddy, ptr(dh), lddh, ptr(y), ldy,
+        const int st = unlocked(
+            f_backward, s.rows, s.cols, dt, ptr(dy), lddy, ptr(dh), lddh, ptr(y), ldy,
             static_cast<const float*>(ptr(next_rstd)), ptr(next_weight), ptr(block), ldb,
             static_cast<const float*>(ptr(rstd)), ptr(weight), wt, ptr(gate), ldg, scale, ptr(dx),
             s.cols, ptr(dblock), s.cols, ptr(dgate), s.cols, static_cast<float*>(ptr(dweight)),

@@ -45,3 +45,39 @@ def test_out_of_memory_is_torch_s(sg, name, compiled):
     held.clear()
     call(s)
     torch.cuda.synchronize()
+
+
+def test_other_threads_run_during_a_call(sg):
+    """A call that has to wait in the library does not keep Python's lock.  The library's
+    dequantisation is replaced by libc's usleep, whose argument is then the number of rows."""
+    import ctypes
+    import threading
+    import time
+
+    from dense_fp32_gemm_09_gb300 import _tensors
+    names = ["sgemm_mx4_quantize", "sgemm_mx4_dequantize", "sgemm_mx4_matmul", "sgemm_norm_forward",
+             "sgemm_norm_backward_ws", "sgemm_norm_backward_workspace"]
+    entries = [ctypes.cast(getattr(sg.load(), n), ctypes.c_void_p).value for n in names]
+    usleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    q = sg.mx4_quantize(torch.ones(400000, 4, device="cuda"))
+    want = q.dequantize()
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.005)
+    other = threading.Thread(target=tick)
+    other.start()
+    try:
+        _tensors.fast().bind(entries[0], usleep, *entries[2:])
+        start = time.perf_counter()
+        q.dequantize()
+        end = time.perf_counter()
+    finally:
+        _tensors.fast().bind(*entries)
+        stop.set()
+        other.join()
+    assert end - start >= 0.39
+    assert sum(start + 0.05 < t < end - 0.05 for t in ticks) >= 5
+    assert torch.equal(q.dequantize(), want)
