@@ -105,10 +105,11 @@ def fast():
 
         from . import build
         lib = load()
-        if not os.path.exists(build.FAST_PATH):
-            raise RuntimeError(f"{build.FAST_PATH} is missing: build the library first "
+        path = build.fast_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the library for this torch first "
                                "(python -m dense_fp32_gemm_09_gb300.build)")
-        loader = importlib.machinery.ExtensionFileLoader("_fast_calls", build.FAST_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("_fast_calls", path)
         module = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_fast_calls", loader))
         loader.exec_module(module)

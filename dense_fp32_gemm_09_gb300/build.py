@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -22,7 +23,6 @@ OBJ_DIR = os.path.join(OUT_DIR, "obj")
 LIB_NAME = "libsgemm_gb300.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
 FAST_SRC = os.path.join(PKG_DIR, "binding", "fast_calls.cpp")
-FAST_PATH = os.path.join(OUT_DIR, "_fast_calls.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -59,11 +59,21 @@ def _newer(path: str, files) -> bool:
                                         for f in files)
 
 
+def fast_path() -> str:
+    """The binding for this Python and this torch: it fits no other."""
+    import sysconfig
+
+    import torch
+    return os.path.join(OUT_DIR, f"_fast_calls-torch{torch.__version__}-"
+                                 f"{sysconfig.get_config_var('SOABI')}.so")
+
+
 def build_binding(force: bool = False) -> str:
     """Compile the binding of the usual calls (host code only, against the installed torch)."""
+    path = fast_path()
     inputs = [FAST_SRC, os.path.join(INCLUDE, "sgemm.h"), os.path.abspath(__file__)]
-    if not force and _newer(FAST_PATH, inputs):
-        return FAST_PATH
+    if not force and _newer(path, inputs):
+        return path
     import sysconfig
 
     import torch
@@ -72,7 +82,7 @@ def build_binding(force: bool = False) -> str:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     include = [INCLUDE, sysconfig.get_paths()["include"], cuda, *cpp_extension.include_paths()]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = FAST_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-isystem{d}" for d in include[1:]), f"-I{INCLUDE}", FAST_SRC, "-o", tmp,
@@ -80,8 +90,17 @@ def build_binding(force: bool = False) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for {FAST_SRC}:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, FAST_PATH)
-    return FAST_PATH
+    os.replace(tmp, path)
+    return path
+
+
+def _try_binding(force: bool) -> None:
+    """The library is whole without the binding, which needs torch, Python's headers and a C++
+    compiler; the operators that use it say that it is missing when they are called."""
+    try:
+        build_binding(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        warnings.warn(f"the binding of the 4-bit and norm operators was not built: {e}")
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -100,14 +119,13 @@ def _compile(src: str, verbose: bool) -> str:
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if needed) and return the path of the shared library."""
     if not force and up_to_date():
-        build_binding()
+        _try_binding(False)
         return LIB_PATH
     os.makedirs(OBJ_DIR, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(build_binding, force)
+        ex.submit(_try_binding, force)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
