@@ -10,6 +10,8 @@ of a gated residual block with their gradients (``norms``).
 from __future__ import annotations
 
 import ctypes
+import importlib
+import importlib.util
 
 from ._abi import (SGEMM_ERR_INVALID_ARG, SGEMM_ERR_LAUNCH, SGEMM_ERR_UNSUPPORTED,  # noqa: F401
                    SGEMM_ERR_WORKSPACE, SGEMM_OK, SgemmConfig, SgemmError, check, load)
@@ -17,20 +19,19 @@ from ._abi import (SGEMM_ERR_INVALID_ARG, SGEMM_ERR_LAUNCH, SGEMM_ERR_UNSUPPORTE
 __all__ = ["sgemm", "sgemm_run", "sgemm_run_ws", "sgemm_run_with", "sgemm_run_host",
            "sgemm_run_noalloc", "sgemm_run_ex", "sgemm_run_op",
            "sgemm_query_config", "sgemm_workspace_size", "kernel_table", "launch_count",
-           "SgemmError", "load",
-           "Mx4", "mx4_quantize", "mx4_dequantize", "mx4_matmul",
-           "norm_before", "norm_before_backward", "norm_after", "norm_after_backward"]
+           "SgemmError", "load"]
 
 _BLOCK_OPS = {name: module for module, names in (
     ("mx4", ("Mx4", "mx4_quantize", "mx4_dequantize", "mx4_matmul")),
     ("norms", ("norm_before", "norm_before_backward", "norm_after", "norm_after_backward")),
 ) for name in names}
+if importlib.util.find_spec("torch") is not None:      # "import *" looks each of them up
+    __all__ += list(_BLOCK_OPS)
 
 
 def __getattr__(name):
     # These modules need torch, which the rest of the package imports only when called.
     if name in _BLOCK_OPS:
-        import importlib
         value = getattr(importlib.import_module(f".{_BLOCK_OPS[name]}", __name__), name)
         globals()[name] = value
         return value

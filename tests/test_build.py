@@ -43,3 +43,14 @@ def test_the_binding_is_that_of_the_installed_torch(lib):
     name = os.path.basename(build.fast_path())
     assert torch.__version__ in name and f"cpython-{sys.version_info[0]}{sys.version_info[1]}" in name
     assert os.path.exists(build.fast_path())
+
+
+def test_everything_can_be_imported_without_torch():
+    r = run("from dense_fp32_gemm_09_gb300 import *\nassert callable(sgemm_query_config)\n"
+            "import dense_fp32_gemm_09_gb300 as sg\n"
+            "assert 'sgemm' in sg.__all__ and 'mx4_matmul' not in sg.__all__\n")
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([sys.executable, "-c", "import sys; sys.path.insert(0, sys.argv[1])\n"
+                        "from dense_fp32_gemm_09_gb300 import *\nassert mx4_matmul and norm_after\n",
+                        REPO], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
