@@ -251,13 +251,12 @@ __global__ void __launch_bounds__(512, 1) norm_backward_columns(const NormBackwa
                 s = fma(w[j], dn, s);
             }
             const float mn = block_sum(sum(s)) * rn * inv;
-            const Two k = twice(-rn * rn * mn);
+            const Two k = twice(-rn * mn);       // (rn^2 would overflow where rn and t do not)
             s = twice(0.0f);
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                t[j] = mul(mul(w[j], dh.pair(j)), rn2);
-                if (p.dy) t[j] = fma(mul(w[j], dh.pair(j)), rn2, dy.pair(j));
-                t[j] = fma(y.pair(j), k, t[j]);
+                const Two e = fma(y.pair(j), k, mul(w[j], dh.pair(j)));
+                t[j] = p.dy ? fma(e, rn2, dy.pair(j)) : mul(e, rn2);
             }
         } else {
 #pragma unroll
@@ -286,10 +285,10 @@ __global__ void __launch_bounds__(512, 1) norm_backward_columns(const NormBackwa
             }
             if (!SHARED && gate_rows && p.dgate)
                 own.store(static_cast<T*>(p.dgate) + row * p.lddg, dg);
-            const float m = block_sum(sum(s)) * (p.scale * r) * inv;
-            const Two k = twice(-r * r * m);
+            const float m = block_sum(sum(s)) * r * inv;       // without the scale
+            const Two k = twice(-r * m);
 #pragma unroll
-            for (int j = 0; j < P; ++j) w[j] = fma(t[j], sr, mul(blk.pair(j), k));
+            for (int j = 0; j < P; ++j) w[j] = mul(fma(blk.pair(j), k, t[j]), sr);
             if (more) load_after(row + gridDim.x);
             own.store(static_cast<T*>(p.dblock) + row * p.lddb, w);
         }

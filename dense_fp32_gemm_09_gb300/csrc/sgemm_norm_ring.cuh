@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(1024, 1)
             }
             const float mn = block_sum(sum(s)) * rn * inv;
             loop.refill_previous();
-            const Two k = twice(-rn * rn * mn);
+            const Two k = twice(-rn * mn);       // (rn^2 would overflow where rn and t do not)
             s = twice(0.0f);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -603,6 +603,9 @@ __global__ void __launch_bounds__(1024, 1)
                 get(dh + c, d);
 #pragma unroll
                 for (int j = 0; j < P; ++j) w[j] = mul(w[j], d[j]);
+                get(y + c, d);
+#pragma unroll
+                for (int j = 0; j < P; ++j) w[j] = fma(d[j], k, w[j]);
                 if (p.dy) {
                     get(dy + c, t[i]);
 #pragma unroll
@@ -611,9 +614,6 @@ __global__ void __launch_bounds__(1024, 1)
 #pragma unroll
                     for (int j = 0; j < P; ++j) t[i][j] = mul(w[j], rn2);
                 }
-                get(y + c, d);
-#pragma unroll
-                for (int j = 0; j < P; ++j) t[i][j] = fma(d[j], k, t[i][j]);
                 put<T, RAGGED>(static_cast<T*>(p.dx) + row * p.lddx, c, D, t[i]);
             }
         } else {
@@ -664,9 +664,9 @@ __global__ void __launch_bounds__(1024, 1)
                     t[i][j] = mul(t[i][j], w[j]);
                 }
             }
-            const float m = block_sum(sum(s)) * (p.scale * r) * inv;
+            const float m = block_sum(sum(s)) * r * inv;       // without the scale
             if constexpr (!kNext) loop.refill_previous();
-            const Two k = twice(-r * r * m);
+            const Two k = twice(-r * m);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = (threadIdx.x + i * NT) * VEC;
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(1024, 1)
                 Two n[P];
                 get(blk + c, n);
 #pragma unroll
-                for (int j = 0; j < P; ++j) n[j] = fma(t[i][j], sr, mul(n[j], k));
+                for (int j = 0; j < P; ++j) n[j] = mul(fma(n[j], k, t[i][j]), sr);
                 put<T, RAGGED>(static_cast<T*>(p.dblock) + row * p.lddb, c, D, n);
             }
         }
