@@ -237,13 +237,13 @@ struct Divider {
         } else {
             d = 0.0f;
             r = __uint_as_float((254u - byte) << 23);
-            fast = true;
+            fast = byte != 255u;
         }
     }
-    // Codes of eight numbers; a scale of 0 has codes 0.
+    // Codes of eight numbers; a scale of 0 or NaN has codes 0 (zeros past a row's end too).
     __device__ __forceinline__ uint32_t codes(const Two (&x)[4]) const {
         float v[8];
-        if (FORMAT == kMxfp4 || fast) {
+        if (fast) {
             // nvfp4: divide() on pairs, of which this arrangement gives the negative.
             const Two k = twice(FORMAT == kMxfp4 ? r : -r), dd = twice(d);
 #pragma unroll
@@ -256,7 +256,7 @@ struct Divider {
             }
             return FORMAT == kMxfp4 ? encode8(v) : encode8(v) ^ 0x88888888u;
         }
-        if (d == 0.0f) return 0u;
+        if (FORMAT == kMxfp4 || !(fabsf(d) > 0.0f)) return 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = parts(x[i]);

@@ -442,12 +442,9 @@ __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan 
     const int order = N == 2 ? lane >> 2 & 1 : lane >> 1 & 3;
     const auto column = [&](int i) { return static_cast<int>(threadIdx.x) * 16 + (i ^ order) * VEC; };
     const bool live = static_cast<int>(threadIdx.x) < 2 * chunks;
-    // Past the row, an infinite or NaN statistic must not make codes: a thread's own numbers
-    // are times 0 there, and where it has both, the codes are masked (the block's numbers in
-    // the row are then infinite or NaN too, and so is its scale).
+    // An infinite or NaN statistic must not make scales of the padding: it is 0 for threads past
+    // the row.  (A block with columns of both is then infinite or NaN in the row too: codes 0.)
     const int left = D - static_cast<int>(threadIdx.x) * 16;
-    const uint32_t in_low = left >= 8 ? ~0u : left > 0 ? ~0u >> (32 - 4 * left) : 0u;
-    const uint32_t in_high = left >= 16 ? ~0u : left > 8 ? ~0u >> (64 - 4 * left) : 0u;
     Two w[N][P];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -508,7 +505,7 @@ __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan 
         }
         if (live)
             *reinterpret_cast<uint2*>(p.codes + code_offset(row, threadIdx.x >> 1, chunks) +
-                                      8 * (threadIdx.x & 1)) = make_uint2(low & in_low, high & in_high);
+                                      8 * (threadIdx.x & 1)) = make_uint2(low, high);
         // Four blocks' bytes to each of their lanes.
         constexpr int kStep = FORMAT == kNvfp4 ? 1 : 2;
         uint32_t word = byte << (8 * (lane / kStep % 4));

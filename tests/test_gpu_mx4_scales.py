@@ -107,3 +107,24 @@ def test_block_scales_of_the_hardest_divisors(sg, base):  # noqa: F811
             check_stored(sg.mx4_quantize(torch.from_numpy(x).cuda(),
                                          tensor_scale=torch.tensor([t], device="cuda")),
                          torch.from_numpy(x), "nvfp4", t)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(1, 1), (5, 77), (130, 200), (64, 1025), (34, 130)])
+def test_padding_after_what_is_not_a_number(sg, rows, cols, dtype, fmt):  # noqa: F811
+    """Codes past the row's end are zeros also in a block whose scale is NaN, and that block
+    makes its row of a product NaN."""
+    x = sample(rows, cols, dtype, 2)
+    x[0, cols - 1] = float("nan")
+    x[rows - 1, cols - 1] = float("inf")
+    for v in (x.cuda(), x.t().contiguous().cuda().t()):
+        q = sg.mx4_quantize(v, fmt)
+        check_stored(q, x, fmt)
+        byte = q.codes.transpose(1, 2).reshape(-1, q.codes.shape[1] * 16)[:rows]
+        code = torch.stack((byte & 15, byte >> 4), 2).view(rows, -1)
+        assert not bool(code[:, cols:].any())
+        c = sg.mx4_matmul(q, sg.mx4_quantize(torch.ones(20, cols, device="cuda"), fmt))
+        bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        bad[0] = bad[rows - 1] = True
+        assert torch.equal(c.isnan(), bad[:, None].expand(rows, 20))

@@ -59,3 +59,25 @@ def test_after(sg, rows, cols, dtype, both, gate):  # noqa: F811
     n = f64(c.block) * f64(r)[:, None]
     near(got[2], (g * t * n).sum(0), 2 * (c.ec + 24 * 2.0 ** -24) * (g.abs() * tm * n.abs()).sum(0) + 1e-6,
          "dweight")
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("after", [True, False])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("rows,cols", [(7, 77), (400, 264), (7, 8201), (7, 9001), (7, 9005),
+                                       (7, 16383), (7, 20001)])
+def test_padding_of_rows_that_are_not_numbers(sg, rows, cols, dtype, after, fmt):  # noqa: F811
+    """Codes and scales past the row's end are zeros, whatever the row holds."""
+    x = Case(rows, cols, dtype, "none").block
+    x[1], x[3, 0], x[5, cols - 1] = 0, float("nan"), float("inf")
+    if after:
+        q = sg.norm_after(torch.ones_like(x).cuda(), x.cuda(), scale=0.0, eps=0.0, quantize=fmt)[2]
+    else:
+        q, _ = sg.norm_before(x.cuda(), eps=0.0, quantize=fmt)
+    byte = q.codes.transpose(1, 2).reshape(-1, q.codes.shape[1] * 16)[:rows]
+    code = torch.stack((byte & 15, byte >> 4), 2).view(rows, -1)
+    assert not bool(code[:, cols:].any())
+    s = q.scales.permute(0, 3, 2, 1, 4).reshape(-1, q.scales.shape[1] * 4)[:rows]
+    assert not bool(s[:, -(-cols // (16 if fmt == "nvfp4" else 32)):].any())
+    v = q.dequantize()
+    assert bool(v[3].isnan().all()) and not bool(v[[0, 2, 4]].isnan().any())
