@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar;
     __shared__ uint32_t tmem_base_s;
-    __shared__ int abort_s;
+    __shared__ int abort_s, issued_s;
     const Mx4Matmul& p = pl.p;
     const int warp = warp_index();
     const int rank = static_cast<int>(blockIdx.x) % pl.split;
@@ -124,13 +124,9 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
             const uint8_t* qs = p.a_scales + (m0 >> 7) * groups * 512;
             int stage = 0;
             uint32_t phase = 0;
-            bool ok = true;
             int issued = 0;
             for (int s = first; s < last; ++s) {
-                if (!pipe_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) {
-                    ok = false;
-                    break;
-                }
+                if (!pipe_wait(su32(&empty_bar[stage]), phase ^ 1u, abort_flag, pl.status)) break;
                 const int c0 = s * kSlabChunks, nc = min(kSlabChunks, pl.chunks - c0);
                 const int ng = nc / kChunksPerGroup<FORMAT>, g0 = c0 / kChunksPerGroup<FORMAT>;
                 const uint32_t fb = su32(&full_bar[stage]);
@@ -151,12 +147,7 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
                     phase ^= 1u;
                 }
             }
-            if (!ok) {   // giving up: copies in flight land before the CTA exits
-                volatile int no_abort = 0;
-                for (int i = max(0, issued - pl.stages); i < issued; ++i)
-                    pipe_wait(su32(&full_bar[i % pl.stages]), (i / pl.stages) & 1, &no_abort,
-                              nullptr);
-            }
+            issued_s = issued;
         }
     } else if (warp == 1) {
         if (elect_one()) {
@@ -201,8 +192,16 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
         }
     }
     __syncwarp();
+    // (Sums that a wait gave up on are committed as well, but not stored.)
     const bool ok = __all_sync(0xFFFFFFFFu,
-                               pipe_wait(su32(&done_bar), 0, abort_flag, pl.status));
+                               pipe_wait(su32(&done_bar), 0, abort_flag, pl.status) && !*abort_flag);
+    if (!ok && warp == 0 && elect_one()) {
+        // Copies in flight land before the CTA exits, whichever of its waits gave up.
+        volatile int no_abort = 0;
+        for (int i = max(0, issued_s - pl.stages); i < issued_s; ++i)
+            pipe_wait(su32(&full_bar[i % pl.stages]), (i / pl.stages) & 1, &no_abort, nullptr);
+    }
+    __syncwarp();
     fence_after();
     float f = p.alpha;
     if (p.a_ts) f *= __ldg(p.a_ts);

@@ -203,10 +203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ring.next();
                 }
             }
-            // Giving up: copies in flight land before the pair exits.  They signal the first
-            // CTA, so it waits for both; what the second may have asked for beyond that had
-            // the time limit of the wait that gave up.
-            if (!ok && rank == 0) {
+            // Copies in flight land before the pair exits, whichever wait gave up.  They signal
+            // the first CTA, so it waits for both; what the second may have asked for beyond
+            // that had the time limit of the wait that gave up.
+            if (rank == 0) {
                 volatile int no_abort = 0;
                 for (int i = max(0, issued - kStages); i < issued; ++i)
                     pipe_wait(su32(&full_bar[i % kStages]), (i / kStages) & 1, &no_abort, nullptr);
@@ -271,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     commit<2>(su32(&empty_bar[ring.stage]));
                     ring = ahead;
                 }
-                commit<2>(su32(&done_bar));
+                if (ok) commit<2>(su32(&done_bar));      // else both epilogues give up
             }
         }
     } else {
@@ -286,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int t = start; t < tiles; t += pairs) {
             // All four warps of this half go on, or none.
             const bool ok = all_of_half(
-                1 + half, pipe_wait(su32(&done_bar), turn, abort_flag, pl.status));
+                1 + half, pipe_wait(su32(&done_bar), turn, abort_flag, pl.status) && !*abort_flag);
             if (!ok) break;
             turn ^= 1u;
             fence_after();

@@ -21,9 +21,9 @@ using async::su32;
 // Rows in a ring of shared-memory stages
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void ring_fill(const Ring& g, uint8_t* stage, uint64_t* bar,
-                                          long long row) {
+                                          long long row, bool copying) {
     if (g.mode == kBulk) {
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && copying) {
             async::mbar_expect_tx(su32(bar), g.n * g.row_bytes);
             for (int i = 0; i < g.n; ++i)
                 bulk_load(su32(stage + i * g.pitch), g.p[i] + row * g.ld[i], g.row_bytes, su32(bar));
@@ -45,10 +45,21 @@ __device__ __forceinline__ void ring_fill(const Ring& g, uint8_t* stage, uint64_
     }
 }
 
+// After a wait that gave up: until no stage has copies in flight.  One of a barrier's parities is
+// the phase that was filled last; the other has completed, or runs into the time limit.
+static __device__ __noinline__ void ring_drain(uint32_t bars, int stages) {
+    volatile int no_abort = 0;
+    for (int s = 0; s < stages; ++s)
+        for (uint32_t parity = 0; parity < 2; ++parity)
+            pipe_wait(bars + 8 * s, parity, &no_abort, nullptr);
+}
+
 // Rows blockIdx.x, + gridDim.x, ... in turn.  `start` fills the ring; `row_ready` waits for
 // the current row's stage.  Once a row, after a block-wide barrier that follows the last
 // read of a stage, that stage is filled again: the previous row's (refill_previous) or,
 // where the current row's inputs are read no more, its own (refill_this, a row earlier).
+// A bulk copy that does not arrive in time ends the copying, not the loop (whose barriers all
+// threads have to meet): the status word says that what was written since is not to be used.
 struct RowLoop {
     const Ring& g;
     uint8_t* smem;
@@ -58,11 +69,16 @@ struct RowLoop {
     int k = 0;                       // rows done
     int stage = 0;                   // k % stages
     uint32_t phase = 0;              // k / stages % 2
+    bool ok = true;                  // copies have arrived in time
     __device__ __forceinline__ void fill(int ahead) {
         int s = stage + ahead;
         if (s >= g.stages) s -= g.stages;
         const long long r = row + ahead * static_cast<long long>(gridDim.x);
-        if (r < rows) ring_fill(g, smem + s * (g.n * g.pitch), bars + s, r);
+        if (r < rows) ring_fill(g, smem + s * (g.n * g.pitch), bars + s, r, ok);
+    }
+    // Copies in flight land before the block exits.
+    __device__ __forceinline__ void finish() {
+        if (threadIdx.x == 0 && !ok) ring_drain(su32(bars), g.stages);
     }
     __device__ __forceinline__ void commit() {
         if (g.mode == kCopy4) asm volatile("cp.async.commit_group;" ::: "memory");
@@ -81,7 +97,7 @@ struct RowLoop {
             commit();
         }
         if (g.mode == kBulk) {
-            pipe_wait(su32(bars + stage), phase, abort, g.status);
+            ok &= pipe_wait(su32(bars + stage), phase, abort, g.status);
         } else {
             // One group a row, and with refill_previous an empty one at first: all but
             // stages - 2 of the newest have arrived.
@@ -407,6 +423,7 @@ __global__ void __launch_bounds__(1024, 1)
             }
         }
     }
+    loop.finish();
     launch_next();
 }
 
@@ -515,6 +532,7 @@ __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan 
             *reinterpret_cast<uint32_t*>(
                 p.scales + scale_offset(row, static_cast<int>(threadIdx.x) / kStep, groups)) = word;
     }
+    loop.finish();
     launch_next();
 }
 
@@ -676,6 +694,7 @@ __global__ void __launch_bounds__(1024, 1)
             }
         }
     }
+    loop.finish();
     if (p.partial) {
         float* const pw = p.partial + blockIdx.x * 3LL * D;
 #pragma unroll
