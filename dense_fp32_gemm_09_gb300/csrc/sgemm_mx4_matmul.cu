@@ -379,7 +379,6 @@ cudaError_t launch_format(const Mx4Matmul& p, int sms, cudaStream_t stream) {
 
 cudaError_t launch_mx4_matmul(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     if (p.K == 0) {
-        if (p.beta == 1.0f) return cudaSuccess;
         const long long blocks = (static_cast<long long>(p.M) * p.N + 255) / 256;
         mx4_scale_kernel<<<static_cast<unsigned>(std::min<long long>(blocks, 8LL * sms)), 256, 0,
                            stream>>>(p);

@@ -72,3 +72,23 @@ def test_emptied_buffer_is_refused(sg):  # noqa: F811
     q.codes.untyped_storage().resize_(0)
     with pytest.raises(sg.SgemmError, match="null"):
         q.dequantize()
+
+
+def test_launches_are_counted(sg):  # noqa: F811
+    """sgemm_launch_count counts kernels: one a call, none where C only stays as it is."""
+    def count(call):
+        before = sg.launch_count()
+        call()
+        return sg.launch_count() - before
+    q, w, c = made(sg), made(sg, rows=30, seed=2), torch.ones(40, 30, device="cuda")
+    empty = sg.mx4_quantize(torch.ones(40, 0, device="cuda"))
+    none = sg.mx4_quantize(torch.ones(30, 0, device="cuda"))
+    assert count(lambda: sg.mx4_matmul(q, w)) == 1 and count(q.dequantize) == 1
+    assert count(lambda: sg.mx4_matmul(empty, none, c, beta=1.0)) == 0
+    assert count(lambda: sg.mx4_matmul(q, w, c, alpha=0.0, beta=1.0)) == 0
+    assert bool((c == 1).all())
+    assert count(lambda: sg.mx4_matmul(q, w, c, alpha=0.0, beta=2.0)) == 1
+    x, one = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    _, r = sg.norm_before(x)
+    assert count(lambda: sg.norm_before_backward(x, x, r)) == 1
+    assert count(lambda: sg.norm_before_backward(x, x, r, one)) == 2
