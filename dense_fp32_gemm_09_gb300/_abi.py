@@ -61,6 +61,7 @@ SIGNATURES = {
     "sgemm_mx4_quantize": (_i, [_i, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp]),
     "sgemm_mx4_dequantize": (_i, [_i, _i, _i, _vp, _vp, _vp, _i, _vp, _i, _vp]),
     "sgemm_mx4_matmul": (_i, [_i, _i, _i, _i, _f] + [_vp] * 6 + [_f, _i, _vp, _i, _vp]),
+    "sgemm_mx4_choose_check": (_i, [_i, _i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)]),
     "sgemm_norm_forward": (_i, [_i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _i, _vp, _i, _f, _f,
                                 _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp]),
     "sgemm_norm_backward": (_i, [_i, _i, _i] + [_vp, _i] * 3 + [_vp, _vp, _vp, _i, _vp, _vp, _i,

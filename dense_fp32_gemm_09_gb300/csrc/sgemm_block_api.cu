@@ -334,6 +334,17 @@ int sgemm_mx4_matmul(int M, int N, int K, int format, float alpha, const void* a
     });
 }
 
+int sgemm_mx4_choose_check(int M, int N, int K, int sms, int* tile, int* split) {
+    if (M < 1 || N < 1 || K < 1 || sms < 2 || tile == nullptr || split == nullptr)
+        return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_mx4_choose_check: bad argument");
+    SGEMM_TRY(check_extent("sgemm_mx4_choose_check", M, K));
+    SGEMM_TRY(check_extent("sgemm_mx4_choose_check", N, K));
+    const Mx4Choice c = choose_mx4(M, N, K, sms);
+    *tile = c.tile;
+    *split = c.split;
+    return SGEMM_OK;
+}
+
 int sgemm_norm_forward(int rows, int cols, int dtype, const void* block, int ldb,
                        const void* residual, int ldr, const void* weight, const void* next_weight,
                        int weight_dtype, const void* gate, int ldg, float scale, float eps,

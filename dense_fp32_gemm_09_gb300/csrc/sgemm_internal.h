@@ -127,6 +127,11 @@ struct NormBackward {
     float *dweight, *dnext_weight;
     float* partial;           // the blocks' column sums
 };
+struct Mx4Choice {
+    int tile;                 // rows of A a tile; 256: pairs of CTAs
+    int split;                // parts of a tile's K range
+};
+Mx4Choice choose_mx4(int M, int N, int K, int sms);
 cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t stream);
 cudaError_t launch_mx4_dequantize(const Mx4Dequantize& q, cudaStream_t stream);
 cudaError_t launch_mx4_matmul(const Mx4Matmul& p, int sms, cudaStream_t stream);

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(256) mx4_scale_kernel(const Mx4Matmul p) {
 }
 
 template <int FORMAT, int BQ>
-cudaError_t launch_tile(const Mx4Matmul& p, int sms, cudaStream_t stream) {
+cudaError_t launch_tile(const Mx4Matmul& p, int split, cudaStream_t stream) {
     MatmulPlan pl{};
     pl.p = p;
     pl.chunks = chunks_of(p.K);
@@ -318,14 +318,7 @@ cudaError_t launch_tile(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     if (tiles > 0x7FFFFFFF / kGroup) return cudaErrorInvalidConfiguration;
     pl.tiles_n = static_cast<int>(tiles_n);
     pl.tiles_m = static_cast<int>(tiles_m);
-    // A K range is split while the CTAs still fit the SMs at once and each keeps four slabs.
-    // Two parts of a 64-wide tile, or any of a 128-wide one, cost more to add up than a range
-    // of less than 8192 saves (64 x 4096 x 4096: 1 part 12.6 us, 2 14.2, 4 11.0;
-    // 256 x 1024 x 8192: 1 part 18.3, 2 16.3).
-    pl.split = 1;
-    for (int split = 2; BQ <= 64 && split <= 8; split *= 2)
-        if ((BQ < 64 || split > 2 || pl.slabs >= 32) && tiles * split <= sms && pl.slabs >= 4 * split)
-            pl.split = split;
+    pl.split = split;
     pl.c_vec = c_rows_aligned(p);
     constexpr int kMost = 220 * 1024;
     const int red = pl.split > 1 ? BQ * 512 : 0;
@@ -360,22 +353,44 @@ cudaError_t launch_tile(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     return cudaLaunchKernelEx(&c, kernel, pl);
 }
 
+template <int FORMAT>
+cudaError_t launch_format(const Mx4Matmul& p, int sms, cudaStream_t stream) {
+    const Mx4Choice c = choose_mx4(p.M, p.N, p.K, sms);
+    switch (c.tile) {
+        case 16: return launch_tile<FORMAT, 16>(p, c.split, stream);
+        case 32: return launch_tile<FORMAT, 32>(p, c.split, stream);
+        case 64: return launch_tile<FORMAT, 64>(p, c.split, stream);
+        case 128: return launch_tile<FORMAT, 128>(p, c.split, stream);
+        default: return launch_mx4_pair(p, sms, stream);
+    }
+}
+
+}  // namespace
+
 // Few rows of A take the narrowest tile that holds them.  More take 64 columns where such
 // tiles fit the SMs at once, else 128, and the pairs' 256 x 256 where those do not either
 // (512 x 4096 x 4096 in us: 64 wide 22.3, 128 14.2, pairs 15.1; 2048^3: 128 20.2, pairs
 // 13.8).  Pairs would waste half of a tile on an operand of up to 128 rows.
-template <int FORMAT>
-cudaError_t launch_format(const Mx4Matmul& p, int sms, cudaStream_t stream) {
-    if (p.M <= 16) return launch_tile<FORMAT, 16>(p, sms, stream);
-    if (p.M <= 32) return launch_tile<FORMAT, 32>(p, sms, stream);
-    const long long tn = (p.N + 127LL) / 128;
-    if (p.M <= 64 || tn * ((p.M + 63LL) / 64) <= sms) return launch_tile<FORMAT, 64>(p, sms, stream);
-    if (tn * ((p.M + 127LL) / 128) > sms && p.M > 128 && p.N > 128)
-        return launch_mx4_pair(p, sms, stream);
-    return launch_tile<FORMAT, 128>(p, sms, stream);
+//
+// A K range is split while the CTAs still fit the SMs at once and each keeps four slabs.
+// Two parts of a 64-wide tile, or any of a 128-wide one, cost more to add up than a range
+// of less than 8192 saves (64 x 4096 x 4096: 1 part 12.6 us, 2 14.2, 4 11.0;
+// 256 x 1024 x 8192: 1 part 18.3, 2 16.3).
+Mx4Choice choose_mx4(int M, int N, int K, int sms) {
+    const long long tn = (N + 127LL) / 128;
+    const int slabs = (chunks_of(K) + kSlabChunks - 1) / kSlabChunks;
+    Mx4Choice c{128, 1};
+    if (M <= 16) c.tile = 16;
+    else if (M <= 32) c.tile = 32;
+    else if (M <= 64 || tn * ((M + 63LL) / 64) <= sms) c.tile = 64;
+    else if (tn * ((M + 127LL) / 128) > sms && M > 128 && N > 128) c.tile = 256;
+    if (c.tile > 64) return c;
+    const long long tiles = tn * ((M + c.tile - 1LL) / c.tile);
+    for (int split = 2; split <= 8; split *= 2)
+        if ((c.tile < 64 || split > 2 || slabs >= 32) && tiles * split <= sms && slabs >= 4 * split)
+            c.split = split;
+    return c;
 }
-
-}  // namespace
 
 cudaError_t launch_mx4_matmul(const Mx4Matmul& p, int sms, cudaStream_t stream) {
     if (p.K == 0) {

@@ -369,6 +369,10 @@ SGEMM_API int sgemm_mx4_matmul(int M, int N, int K, int format, float alpha, con
                                const float* b_tensor_scale, float beta, int dtype, void* C, int ldc,
                                sgemm_stream_t stream);
 
+/* What sgemm_mx4_matmul chooses for these sizes on a GPU with `sms` SMs (host only): rows of
+ * A in a tile (256: tiles of 256 x 256 on pairs of SMs) and parts of a tile's K range. */
+SGEMM_API int sgemm_mx4_choose_check(int M, int N, int K, int sms, int* tile, int* split);
+
 /* ---------------------------------------------------------------------------
  * Norms around a residual block, over rows of `cols` numbers of `dtype`:
  *
