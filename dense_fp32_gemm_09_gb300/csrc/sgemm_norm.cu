@@ -273,24 +273,22 @@ struct RingBuilder {
         s.by_column = s.fits = true;
         s.ragged = ragged();
         s.columns = own;
-        s.most = most;
         s.threads = 64;
         while (s.threads * own < cols) s.threads *= 2;
-        s.blocks_per_sm = std::min(most / s.threads, 16);
-        while (s.blocks_per_sm > 1 && s.blocks_per_sm * extra > kSharedPerSm) --s.blocks_per_sm;
-        s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * s.blocks_per_sm));
+        int per = std::min(most / s.threads, 16);
+        while (per > 1 && per * extra > kSharedPerSm) --per;
+        s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * per));
         s.smem = static_cast<int>(extra);
         return s;
     }
-    // `columns`: of a thread, 8 (up to 1024 threads of 64 registers) or more (up to 512 of
-    // 128); `least`: threads of a block.
+    // The kernels with a ring: `columns` a thread, blocks of `least` to `most` threads and at most
+    // `most` of them an SM, `extra` bytes of shared memory a block beside the stages.
     RingShape shape(int columns, int most, int least, long long extra, int sms) {
         RingShape s{};
         s.ragged = ragged();
         ring.mode = align == 16 && ring.row_bytes % 16 == 0 ? kBulk
                     : align >= 4 && ring.row_bytes % 4 == 0 ? kCopy4 : kPlain;
         s.columns = columns;
-        s.most = most;
         s.threads = least;
         while (s.threads < most && s.threads * columns < cols) s.threads *= 2;
         const long long stage = static_cast<long long>(ring.n) * ring.pitch;
@@ -299,7 +297,6 @@ struct RingBuilder {
         // As many as the registers hold; two stages each at least, if they fit at all.
         int per = std::min(most / s.threads, 32);
         while (per > 1 && per * (2 * stage + extra) > kSharedPerSm) --per;
-        s.blocks_per_sm = per;
         s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * per));
         // No more stages than rows a block has.
         const long long fit = (kSharedPerSm / per - extra) / stage;
@@ -360,12 +357,11 @@ size_t norm_backward_workspace(const NormBackward& p, int sms) {
 size_t norm_backward_workspace_most(int rows, int cols, int sms) {
     // Blocks of an SM: those of the kernels without a ring (backward_shape), else two (a ring
     // of 512 threads or more, or the streaming kernel).
-    const auto blocks = [&](int own) {
-        return cols <= own * 512 ? RingBuilder(kF32, rows, cols).column_shape(own, 512, 0, sms).blocks_per_sm
-                                 : 2;
-    };
-    const long long grid =
-        std::min<long long>(rows, static_cast<long long>(sms) * std::max({blocks(8), blocks(16), 2}));
+    long long grid = std::min<long long>(rows, 2LL * sms);
+    for (int own : {8, 16})
+        if (cols <= own * 512)
+            grid = std::max<long long>(
+                grid, RingBuilder(kF32, rows, cols).column_shape(own, 512, 0, sms).grid);
     return static_cast<size_t>(grid) * 3 * cols * sizeof(float);
 }
 

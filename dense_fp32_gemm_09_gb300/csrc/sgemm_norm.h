@@ -31,8 +31,7 @@ struct BackwardPlan {
 
 struct RingShape {
     int threads, grid, smem;
-    int columns, most; // a thread's; threads that the kernel's registers allow on an SM
-    int blocks_per_sm;
+    int columns;       // of a thread
     bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
     bool by_column;    // the kernels for single columns, without a ring
     bool fits;

@@ -190,7 +190,6 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_columns(const NormForwar
                 if (p.format == kNvfp4) quantize_row<kNvfp4>(hrow, p, row, ts);
                 else quantize_row<kMxfp4>(hrow, p, row, ts);
                 // The next row's sums have a barrier before anything is written to hrow.
-                if constexpr (!kAfter) __syncthreads();
             }
         }
     }

@@ -755,8 +755,9 @@ template <typename T, bool RAGGED>
 cudaError_t forward_rows(const ForwardPlan& pl, const RingShape& s, cudaStream_t st) {
     if constexpr (sizeof(T) == 2 && !RAGGED)
         if (s.columns == 32) return forward_what<T, RAGGED, 32>(pl, s, st);
-    return s.columns == 8 ? forward_what<T, RAGGED, 8>(pl, s, st)
-                          : forward_what<T, RAGGED, 16>(pl, s, st);
+    if constexpr (!RAGGED)      // (few rows: ragged ones of that width have no ring)
+        if (s.columns == 8) return forward_what<T, RAGGED, 8>(pl, s, st);
+    return forward_what<T, RAGGED, 16>(pl, s, st);
 }
 template <typename T, bool RAGGED>
 cudaError_t backward_rows(const BackwardPlan& pl, const RingShape& s, cudaStream_t st) {
