@@ -8,9 +8,11 @@
 // The transpose needs no exchange: a thread takes a column of X (two of a 2-byte type) down
 // 64 rows, so that a warp's loads run along X's rows and its stores are contiguous.
 //
-// Measured (us, of the time the bytes take at 6.79 TB/s), 16384 x 8192 bf16: to nvfp4 56
-// (0.90), to mxfp4 51.5 (0.97), back 52 (0.97); 8192 x 4096 bf16 transposed to nvfp4 20 (0.62),
-// to mxfp4 16 (0.80).
+// Measured (us, the kernel alone; of the memory's 6.79 TB/s), 16384 x 8192 bf16: to nvfp4 57
+// (0.89), to mxfp4 51.6 (0.97), back 52 (0.97); 8192 x 4096 bf16 transposed to nvfp4 20.4 (0.62),
+// to mxfp4 15.5 (0.81).  Other alignments load or store one number at a time: 8192 x 4097 bf16 to
+// nvfp4 34.7 (0.36), back 16.7 (0.76); 3001 x 1999 fp32 to mxfp4 7.8 (0.51), from its transpose 6.2
+// (0.65), back to bf16 5.1 (0.44).
 #include <cuda_runtime.h>
 
 #include "sgemm_internal.h"

@@ -21,9 +21,10 @@
 // Every wait is bounded; one that gives up sets the device status word and the CTA
 // drains, meets its cluster's barriers and exits.
 //
-// Few rows of A are bound by the weight's bytes where it is large (nvfp4 to bf16, 1 x 16384 x
-// 16384: 25.4 us, 5.9 TB/s) and by latency where it is small (1 x 4096 x 4096: 5.2 us, whose
-// 9.4 MB would take 1.4; one CTA an SM, issue slots 6 % used).  512 x 4096 x 4096 takes 9.2 us.
+// Few rows of A are bound by the weight's bytes where it is large (nvfp4 to bf16, the kernel
+// alone, 1 x 16384 x 16384: 24.4 us, 6.2 TB/s) and by latency where it is small (1 x 4096 x 4096:
+// 5.3 us, whose 9.4 MB would take 1.4; one CTA an SM, issue slots 6 % used; 16 x 8192 x 4096 7.1).
+// 512 x 4096 x 4096 takes 8.8 us, 16384 x 64 x 4096 (mxfp4 to fp32) 7.8 to 8.9.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -369,13 +370,13 @@ cudaError_t launch_format(const Mx4Matmul& p, int sms, cudaStream_t stream) {
 
 // Few rows of A take the narrowest tile that holds them.  More take 64 columns where such
 // tiles fit the SMs at once, else 128, and the pairs' 256 x 256 where those do not either
-// (512 x 4096 x 4096 in us: 64 wide 22.3, 128 14.2, pairs 15.1; 2048^3: 128 20.2, pairs
-// 13.8).  Pairs would waste half of a tile on an operand of up to 128 rows.
+// (us, the kernel alone, 512 x 4096 x 4096: 64 wide 16.5, 128 8.8, pairs 11.0; 2048^3: 64 wide
+// 22.8, 128 13.1, pairs 9.3).  Pairs would waste half of a tile on an operand of up to 128 rows.
 //
 // A K range is split while the CTAs still fit the SMs at once and each keeps four slabs.
 // Two parts of a 64-wide tile, or any of a 128-wide one, cost more to add up than a range
-// of less than 8192 saves (64 x 4096 x 4096: 1 part 12.6 us, 2 14.2, 4 11.0;
-// 256 x 1024 x 8192: 1 part 18.3, 2 16.3).
+// of less than 8192 saves (64 x 4096 x 4096: 1 part 8.3 us, 2 9.6, 4 7.5;
+// 256 x 1024 x 8192: 1 part 13.0, 2 11.9, 4 8.9).
 Mx4Choice choose_mx4(int M, int N, int K, int sms) {
     const long long tn = (N + 127LL) / 128;
     const int slabs = (chunks_of(K) + kSlabChunks - 1) / kSlabChunks;

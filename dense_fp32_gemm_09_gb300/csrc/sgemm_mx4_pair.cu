@@ -22,7 +22,7 @@
 //     and as whole lines, under its MMAs.
 //
 // 8192^3, nvfp4 to bf16, operands in L2: 151 to 157 us, 7.0 to 7.3 PFLOP/s; the MMAs alone, at 128 cycles
-// each, would take 116.  2048^3 9.8 us, 4096^3 30, 3001 x 2047 x 1999 14.
+// each, would take 116.  2048^3 9.3 us, 4096^3 28, 3001 x 2047 x 1999 14.
 #include <cuda_runtime.h>
 
 #include <algorithm>

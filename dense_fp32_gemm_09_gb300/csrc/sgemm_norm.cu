@@ -27,13 +27,16 @@
 // Sums over rows (gradients of weights and of a shared gate) stay in a thread's registers
 // until its block writes them out once; a second kernel adds the blocks' sums in their order.
 //
-// Measured (us, of the time the bytes take at 6.79 TB/s): the norm after a
-// block and the next one, 8192 x 8192 bf16 with a gate 123 (0.80); before, 8192 x 4096 bf16 33
-// (0.60); before, 8192 x 8192 bf16 to nvfp4 61 (0.41); gradient of the norm before a block,
-// 8192 x 4096 bf16 56 (0.70); of both, 8192 x 8192 bf16 with a gate 226
-// (0.70), 3001 x 2047 fp32 47 (0.46).  Gradients run 16 warps an SM at 122 to 128 registers
-// with issue slots 38 to 54 % used.  Streaming kernels: 4096 x 20000 fp32 before 409 (0.24),
-// bf16 gradient of before 1055 (0.07).
+// Measured (us, kernels alone; of the memory's 6.79 TB/s).  8192 x 8192 bf16 with a gate a row:
+// after a block and the next norm 111 (0.89), the norm after alone 81 (0.97), both with h to nvfp4
+// 138 (0.61).  Before a block: 8192 x 8192 bf16 50 (0.78), to nvfp4 57.5 (0.44), 8192 x 4096 bf16
+// 27.4 (0.72).  Both, 3001 x 2047 fp32 25.8 (0.56).
+// Gradients: of the norm before, 8192 x 4096 bf16 53.6 (0.74); of both, 8192 x 8192 bf16 with a
+// gate a row 208 (0.76), 3001 x 2047 fp32 44.1 (0.49), 3001 x 2048 fp32 31.5 (0.69); of the norm
+// after, 8192 x 8192 bf16 with a gate a row 122 (0.81).  They run 16 warps an SM at 122 to 128
+// registers with issue slots 38 to 54 % used; 2-byte rows of both norms spill 48 to 64 bytes.
+// Streaming kernels: 4096 x 20000 fp32 before 394 (0.24), to nvfp4 821 (0.07); gradient of before,
+// 4096 x 20000 bf16 1305 (0.06); of both, 4096 x 11268 fp32 with a gate a row 2285 (0.10).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -329,11 +332,13 @@ RingBuilder ring_of(const NormBackward& p) {
     return b;
 }
 
-// Up to 512 threads of 128 registers hold a row's numbers and the sums over rows: eight
-// columns a thread of ragged or fp32 rows, sixteen of 2-byte ones (both norms in us, against
-// the ring: 3001 x 2047 fp32 47 and 67, 3001 x 2048 36 and 50, 8192 x 4096 bf16 106 and 127,
-// 8192 x 8192 with a gate 225 and 233).  Wider rows take the ring, with eight columns a
-// thread on 1024 threads of 64 registers, or sixteen, whose sums then spill.
+// Up to 512 threads of 128 registers hold a row's numbers and the sums over rows (2-byte rows of
+// both norms with 48 to 64 bytes of spills): eight columns a thread of ragged or fp32 rows, sixteen
+// of 2-byte ones (both norms in us, against the ring: 3001 x 2047 fp32 44 and 63, 3001 x 2048 31.5
+// and 44.5, 8192 x 4096 bf16 86.5 and 130, 8192 x 8192 with a gate 208 and 297).  Wider rows take
+// the ring, with eight columns a thread on 1024 threads of 64 registers, or sixteen, whose sums
+// then spill, as far as one stage of all inputs fits: up to 16384 columns, but fp32 rows of both
+// norms only to 11264 with a gate a row and 14080 without.
 RingShape backward_shape(const NormBackward& p, RingBuilder& b, int sms) {
     const int own = b.ragged() || p.dtype == kF32 ? 8 : 16;
     if (p.cols <= own * 512) return b.column_shape(own, 512, 0, sms);
@@ -375,14 +380,14 @@ cudaError_t launch_norm_forward(const NormForward& p, int sms, cudaStream_t stre
     b.also(p.next_weight, 0);
     b.also(p.y, p.ldy);
     b.also(p.h, p.ldh);
-    // Sixteen columns a thread: 121 against 149 us with eight at 8192 x 8192 with a gate.
-    // Few rows take eight, for latency: 6.7 against 7.7 us for one row of 4096.  Ragged rows
-    // take the kernels without a ring (3001 x 2047 fp32 34 against 43).
+    // Sixteen columns a thread: 111 against 141 us with eight at 8192 x 8192 with a gate.
+    // Few rows take eight, for latency: 3.0 against 3.3 us for one row of 4096.  Ragged rows
+    // take the kernels without a ring (3001 x 2047 fp32 25.8 against 30.5).
     const bool few = p.rows <= 2LL * sms && p.cols <= 8 * 1024;
     // A row of fp32 numbers on its way to codes, but not in norm_quantize_ring.
-    // Aligned 2-byte rows of more than 16384 take 32 (4096 x 20000 bf16: before 77 against 395 us
-    // in the streaming kernel).  Ragged ones would have to be copied by elements (4096 x 20001:
-    // before 457 against 397, to nvfp4 389 against 688, the norm after 977 against 651), and
+    // Aligned 2-byte rows of more than 16384 take 32 (4096 x 20000 bf16: before 76 against 395 us
+    // in the streaming kernel).  Ragged ones would have to be copied by elements (tried, 4096 x
+    // 20001: before 457 against 397, to nvfp4 389 against 688, the norm after 977 against 651), and
     // fp32 ones do not fit with the quantised row beside them.
     const bool wide = p.cols > 16 * 1024 && p.dtype != kF32 && !b.ragged();
     const int columns = few ? 8 : wide ? 32 : 16;

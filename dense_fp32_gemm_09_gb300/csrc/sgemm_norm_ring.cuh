@@ -435,8 +435,8 @@ __global__ void __launch_bounds__(1024, 1)
 // keeps its weights in registers.  Lanes read their 16-byte groups in different orders, so
 // that the eight lanes of a shared-memory access touch all banks; codes are put back in
 // order.  Threads reach past the padded row (a power of two of them, at least 32).
-// 8192 x 8192 in us, against eight columns a lane in norm_forward_ring: bf16 to nvfp4 61 and 84,
-// to mxfp4 53 and 75; fp32 63 and 108, 57 and 110 (memory: 25 and 45).
+// 8192 x 8192 in us, against eight columns a thread in norm_forward_ring: bf16 to nvfp4 57.5 and
+// 102, to mxfp4 51 and 93.5; fp32 59.5 and 142, 53 and 133 (memory: 25 and 45).
 template <typename T, int FORMAT>
 __global__ void __launch_bounds__(1024, 1) norm_quantize_ring(const ForwardPlan pl) {
     constexpr int VEC = 16 / sizeof(T), P = VEC / 2, N = 16 / VEC;

@@ -3,6 +3,11 @@
 A matrix is held as e2m1 codes with one 8-bit scale per block of 16 (``"nvfp4"``: e4m3
 scales and an optional float32 scale for the whole tensor) or 32 (``"mxfp4"``: powers of
 two) consecutive columns.  ``include/sgemm.h`` states the formats and their layout.
+
+Results are outside torch's graph, also of inputs that require a gradient: quantisation has none, and
+a product's is two more products (``examples/gated_residual_block.py``).  With ``stream`` a
+call runs on that stream, in no order with the current one; as everywhere in torch, inputs
+made on another stream must be kept until it is done with them.
 """
 from __future__ import annotations
 

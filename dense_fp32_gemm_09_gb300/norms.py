@@ -7,6 +7,10 @@
 
 ``norm_before`` is the second line on its own, ``norm_after`` the first, or both in one
 pass.  ``h`` may leave the pass as a 4-bit matrix (``mx4.Mx4``).  All sums are float32.
+
+Results are outside torch's graph, also of inputs that require a gradient: the ``_backward``
+functions are the gradients, to be called by hand or from a ``torch.autograd.Function``.
+``stream`` as in ``mx4``.
 """
 from __future__ import annotations
 
