@@ -4,8 +4,9 @@ Thin Python face of the C ABI in ``include/sgemm.h``.  PyTorch supplies device
 memory and streams; every step of the product runs in the library's kernels.
 The library is loaded on first use and its absence is an error.
 
-Around the product: 4-bit operands and their tensor-core product (``mx4``), and the norms
-of a gated residual block with their gradients (``norms``).
+Around the product: 4-bit operands and their tensor-core product (``mx4``), the norms of a
+gated residual block with their gradients (``norms``), layer norm (``layer_norms``), the gated
+feed-forward block (``gated``) and 8-bit activation checkpoints (``act8``).
 """
 from __future__ import annotations
 
@@ -24,6 +25,9 @@ __all__ = ["sgemm", "sgemm_run", "sgemm_run_ws", "sgemm_run_with", "sgemm_run_ho
 _BLOCK_OPS = {name: module for module, names in (
     ("mx4", ("Mx4", "mx4_quantize", "mx4_dequantize", "mx4_matmul")),
     ("norms", ("norm_before", "norm_before_backward", "norm_after", "norm_after_backward")),
+    ("act8", ("Act8", "act8_quantize", "act8_dequantize")),
+    ("layer_norms", ("layer_norm", "layer_norm_backward")),
+    ("gated", ("gated_ff", "gated_ff_backward")),
 ) for name in names}
 if importlib.util.find_spec("torch") is not None:      # "import *" looks each of them up
     __all__ += list(_BLOCK_OPS)

@@ -69,6 +69,18 @@ SIGNATURES = {
     "sgemm_norm_backward_workspace": (_i, [_i, _i, ctypes.POINTER(_sz)]),
     "sgemm_norm_backward_ws": (_i, [_i, _i, _i] + [_vp, _i] * 3 + [_vp, _vp, _vp, _i, _vp, _vp, _i,
                                     _vp, _i, _f] + [_vp, _i] * 3 + [_vp, _vp, _vp, _sz, _vp]),
+    "sgemm_act8_sizes": (_i, [_i, _i, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+    "sgemm_act8_quantize": (_i, [_i, _i, _i, _vp, _i, _vp, _vp, _vp]),
+    "sgemm_act8_dequantize": (_i, [_i, _i, _vp, _vp, _i, _vp, _i, _vp]),
+    "sgemm_layer_norm_forward": (_i, [_i, _i, _i, _vp, _i, _vp, _vp, _i, _f, _vp, _i] + [_vp] * 5),
+    "sgemm_layer_norm_backward_workspace": (_i, [_i, _i, ctypes.POINTER(_sz)]),
+    "sgemm_layer_norm_backward": (_i, [_i, _i, _i] + [_vp, _i] * 3 + [_vp] * 5 + [_i, _vp, _i]
+                                  + [_vp] * 3 + [_sz, _vp]),
+    "sgemm_gated_ff_workspace": (_i, [_i] * 5 + [ctypes.POINTER(_sz)]),
+    "sgemm_gated_ff_forward": (_i, [_i] * 5 + [_vp, _i] * 4 + [_i, _vp, _vp, _i, _vp, _vp, _vp, _sz,
+                                    _vp]),
+    "sgemm_gated_ff_backward": (_i, [_i] * 5 + [_vp, _i] * 2 + [_vp, _vp] + [_vp, _i] * 2
+                                + [_i, _vp, _vp, _i, _vp, _vp] + [_vp, _i] * 4 + [_vp, _sz, _vp]),
     "sgemm_device_status": (_i, []),
     "sgemm_selftest_bounded_wait": (_i, [_i]),
     "sgemm_schedule_check": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(SgemmConfig)]),

@@ -2,101 +2,16 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
-#include <exception>
 
-#include "sgemm_internal.h"
+#include "sgemm_checks.h"
 #include "sgemm_mx4.cuh"
 
 namespace sgemm {
 namespace {
 
-constexpr int kMaxDim = 1 << 30;
-
-int refuse(int status, const char* fmt, ...) {
-    char msg[256];
-    va_list ap;
-    va_start(ap, fmt);
-    std::vsnprintf(msg, sizeof(msg), fmt, ap);
-    va_end(ap);
-    set_last_error_message(msg);
-    return status;
-}
-
-// No C++ exception leaves a C entry point.
-template <typename F>
-int guarded(F f) {
-    try {
-        return f();
-    } catch (const std::exception& e) {
-        return refuse(SGEMM_ERR_LAUNCH, "exception: %s", e.what());
-    } catch (...) {
-        return refuse(SGEMM_ERR_LAUNCH, "unknown exception");
-    }
-}
-
-int launched(cudaError_t e, const char* what, int n = 1) {
-    if (e == cudaSuccess) {
-        count_launches(n);
-        return SGEMM_OK;
-    }
-    set_cuda_error(what, e);
-    return SGEMM_ERR_LAUNCH;
-}
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-int elem_size(int dtype) { return dtype == SGEMM_F32 ? 4 : 2; }
-
-int check_dtype(int dtype) {
-    if (dtype == SGEMM_F32 || dtype == SGEMM_BF16 || dtype == SGEMM_F16) return SGEMM_OK;
-    return refuse(SGEMM_ERR_INVALID_ARG, "unknown element type %d", dtype);
-}
 int check_format(int format) {
     if (format == SGEMM_NVFP4 || format == SGEMM_MXFP4) return SGEMM_OK;
     return refuse(SGEMM_ERR_INVALID_ARG, "unknown 4-bit format %d", format);
-}
-int check_extent(const char* what, int rows, int cols) {
-    if (rows < 0 || cols < 0)
-        return refuse(SGEMM_ERR_INVALID_ARG, "%s: negative size %d x %d", what, rows, cols);
-    if (rows > kMaxDim || cols > kMaxDim)
-        return refuse(SGEMM_ERR_UNSUPPORTED, "%s: dimension above 2^30: %d x %d", what, rows, cols);
-    return SGEMM_OK;
-}
-
-// A strided matrix argument: name, address, rows, width and leading dimension.
-struct Mat {
-    const char* name;
-    const void* p;
-    long long rows, cols, ld;
-    int elem;
-    long long bytes() const {
-        return rows <= 0 || cols <= 0 ? 0 : ((rows - 1) * ld + cols) * elem;
-    }
-};
-int check_mat(const Mat& m) {
-    if (m.ld < (m.cols > 1 ? m.cols : 1) && m.rows > 1)
-        return refuse(SGEMM_ERR_INVALID_ARG, "%s: leading dimension %lld below row width %lld",
-                      m.name, m.ld, m.cols);
-    if (m.rows > 0 && m.cols > 0 && m.p == nullptr)
-        return refuse(SGEMM_ERR_INVALID_ARG, "%s: null pointer with non-empty extent", m.name);
-    if (!aligned(m.p, m.elem))
-        return refuse(SGEMM_ERR_INVALID_ARG, "%s: not aligned to its %d-byte elements", m.name,
-                      m.elem);
-    return SGEMM_OK;
-}
-// Every output apart from every input and from every other output.
-template <int NO, int NI>
-int check_apart(const Mat (&out)[NO], const Mat (&in)[NI]) {
-    for (int o = 0; o < NO; ++o) {
-        for (int i = 0; i < NI; ++i)
-            if (byte_ranges_overlap(out[o].p, out[o].bytes(), in[i].p, in[i].bytes()))
-                return refuse(SGEMM_ERR_INVALID_ARG, "%s overlaps %s", out[o].name, in[i].name);
-        for (int i = 0; i < o; ++i)
-            if (byte_ranges_overlap(out[o].p, out[o].bytes(), out[i].p, out[i].bytes()))
-                return refuse(SGEMM_ERR_INVALID_ARG, "%s overlaps %s", out[o].name, out[i].name);
-    }
-    return SGEMM_OK;
 }
 
 long long code_bytes(int rows, int cols) { return mx4::row_blocks(rows) * mx4::chunks_of(cols) * 2048; }
@@ -122,12 +37,6 @@ Mat codes_mat(const char* n, const void* p, int rows, int cols) {
 Mat scales_mat(const char* n, const void* p, int rows, int cols, int format) {
     return Mat{n, p, 1, scale_bytes(rows, cols, format), 1, 1};
 }
-
-#define SGEMM_TRY(expr)                        \
-    do {                                       \
-        const int st_ = (expr);                \
-        if (st_ != SGEMM_OK) return st_;       \
-    } while (0)
 
 // own_ws: in the caller's workspace, else in the library's of the stream.
 int norm_backward(int rows, int cols, int dtype, const void* dy, int lddy, const void* dh,

@@ -438,6 +438,117 @@ SGEMM_API int sgemm_norm_backward_ws(int rows, int cols, int dtype, const void* 
                                      float* dnext_weight, void* ws, size_t ws_bytes,
                                      sgemm_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit activation checkpoints.  A rows x cols matrix is held as int8 codes and one fp32
+ * scale per 64 consecutive columns of a row; value = code * scale.  With amax the largest
+ * magnitude of a block, in fp32:
+ *
+ *   scale = amax / 127      code = x * (127 / amax), rounded to the nearest integer
+ *                                                    (ties to even)
+ *
+ * (scale at most the largest number whose product with 127 is finite).  A block whose amax is
+ * below 2^-100 has scale 0 and codes 0; one with an infinity or a NaN
+ * has scale NaN and codes 0: all of it is NaN.
+ *
+ * Layout: codes [rows][cols padded to 64], scales [rows][cols padded to 64 / 64], both 16-byte
+ * aligned device memory of sgemm_act8_sizes() bytes.  Codes of padded columns are 0.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of the two buffers of a rows x cols matrix (host only). */
+SGEMM_API int sgemm_act8_sizes(int rows, int cols, size_t* codes, size_t* scales);
+
+/* X (rows x cols of `dtype`, leading dimension ldx) to codes and scales, and back: Y = code *
+ * scale in fp32, rounded once.  Any alignment of X and Y to their elements.  Asynchronous on
+ * `stream`; one launch, no workspace.  rows == 0 or cols == 0 is a no-op. */
+SGEMM_API int sgemm_act8_quantize(int rows, int cols, int dtype, const void* X, int ldx,
+                                  void* codes, float* scales, sgemm_stream_t stream);
+SGEMM_API int sgemm_act8_dequantize(int rows, int cols, const void* codes, const float* scales,
+                                    int dtype, void* Y, int ldy, sgemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm over rows of `cols` numbers of `dtype`, all arithmetic in fp32:
+ *
+ *   m = mean(x)    r = (mean((x - m)^2) + eps)^-1/2    y = (x - m) * r * weight + bias
+ *
+ * weight and bias are of `weight_dtype`, NULL for ones and zeros; m and r go to mean and rstd,
+ * one per row.  With codes and scales (both or neither), x is also stored as an 8-bit
+ * checkpoint.  Outputs must not overlap inputs.  Leading dimensions count elements; any
+ * alignment to the element.  cols == 0 is SGEMM_ERR_INVALID_ARG, rows == 0 a no-op. */
+SGEMM_API int sgemm_layer_norm_forward(int rows, int cols, int dtype, const void* x, int ldx,
+                                       const void* weight, const void* bias, int weight_dtype,
+                                       float eps, void* y, int ldy, float* mean, float* rstd,
+                                       void* codes, float* scales, sgemm_stream_t stream);
+
+/* Its gradient from dh (of y), the saved mean and rstd, and x or an 8-bit checkpoint of it
+ * (codes and scales; x NULL).  With n = (x - m) * r and g = weight * dh:
+ *
+ *   dx = dy + r * (g - mean(g) - n * mean(g * n))        dy: NULL for zeros
+ *   dweight = sum over rows of dh * n      dbias = sum over rows of dh     (fp32, or NULL)
+ *
+ * The sums over rows are deterministic (a fixed order, no atomics) and go through the caller's
+ * device workspace: 128-byte aligned, at least as many bytes as the query gives for these sizes
+ * on the current device; it needs no initialisation, must stay untouched by other work while
+ * the call runs, and may be NULL without dweight and dbias.  SGEMM_ERR_WORKSPACE if it is
+ * missing or too small.  rows == 0 writes zeros to the sums. */
+SGEMM_API int sgemm_layer_norm_backward_workspace(int rows, int cols, size_t* bytes);
+SGEMM_API int sgemm_layer_norm_backward(int rows, int cols, int dtype, const void* dh, int lddh,
+                                        const void* dy, int lddy, const void* x, int ldx,
+                                        const void* codes, const float* scales, const float* mean,
+                                        const float* rstd, const void* weight, int weight_dtype,
+                                        void* dx, int lddx, float* dweight, float* dbias, void* ws,
+                                        size_t ws_bytes, sgemm_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward block, of SGEMM_BF16 or SGEMM_F16 numbers:
+ *
+ *   g = x . w_gate^T      u = x . w_up^T      h = act(g) * u
+ *
+ * x is M x K, the weights are N x K (one row per output), h is M x N.  Sums are held in fp32; h
+ * is made from them before they are rounded.  act is t / (1 + e^-t) (SGEMM_SILU) or
+ * t (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3))) / 2 (SGEMM_GELU_TANH).
+ *
+ * `keep` says what is kept of g and u for the gradient: nothing (gate and up NULL); M x N
+ * matrices of `dtype`, both with leading dimension ldk; or 8-bit checkpoints (gate and up are the
+ * codes, with gate_scales and up_scales), made from the fp32 sums.
+ *
+ * A matrix is read in place if its address and (with more than one row) its row stride are
+ * multiples of 16 bytes, and otherwise copied into the workspace first.  `ws` is the caller's
+ * device memory: 128-byte aligned, at least as many bytes as sgemm_gated_ff_workspace gives for
+ * these sizes (`backward` 0 or 1; `packed`: 1 for an x, 2 for a w_gate, 4 for a w_up that is
+ * copied, or for an x given in 8 bits); it needs no initialisation and must stay untouched by
+ * other work while the call runs; NULL where 0 bytes are needed.  Outputs must not overlap
+ * inputs.  Any alignment to the element.  N == 0 or K == 0 is SGEMM_ERR_INVALID_ARG, M == 0 a
+ * no-op. */
+typedef enum { SGEMM_SILU = 0, SGEMM_GELU_TANH = 1 } sgemm_activation;
+typedef enum { SGEMM_KEEP_NONE = 0, SGEMM_KEEP_FULL = 1, SGEMM_KEEP_8BIT = 2 } sgemm_keep;
+
+SGEMM_API int sgemm_gated_ff_workspace(int M, int N, int K, int backward, int packed,
+                                       size_t* bytes);
+SGEMM_API int sgemm_gated_ff_forward(int M, int N, int K, int dtype, int activation, const void* x,
+                                     int ldx, const void* w_gate, int ldg, const void* w_up,
+                                     int ldu, void* h, int ldh, int keep, void* gate, void* up,
+                                     int ldk, float* gate_scales, float* up_scales, void* ws,
+                                     size_t ws_bytes, sgemm_stream_t stream);
+
+/* Its gradient from dh (of h), x or an 8-bit checkpoint of it (x_codes and x_scales; x NULL),
+ * and what was kept of g and u (`keep` full or 8-bit):
+ *
+ *   dg = dh * u * act'(g)     du = dh * act(g)                     rounded to `dtype`
+ *   dx = dg . w_gate + du . w_up     dw_gate = dg^T . x     dw_up = du^T . x
+ *
+ * from fp32 sums in a fixed order, rounded once to `dtype`.  h, unless NULL, is made again from
+ * what was kept.  An x in 8 bits is rounded to `dtype` for the products.  M == 0 writes zeros to
+ * the weights' gradients. */
+SGEMM_API int sgemm_gated_ff_backward(int M, int N, int K, int dtype, int activation,
+                                      const void* dh, int lddh, const void* x, int ldx,
+                                      const void* x_codes, const float* x_scales,
+                                      const void* w_gate, int ldg, const void* w_up, int ldu,
+                                      int keep, const void* gate, const void* up, int ldk,
+                                      const float* gate_scales, const float* up_scales, void* dx,
+                                      int lddx, void* dw_gate, int lddwg, void* dw_up, int lddwu,
+                                      void* h, int ldh, void* ws, size_t ws_bytes,
+                                      sgemm_stream_t stream);
+
 /* Synchronous: reads and clears the device flag that a bounded wait in a
  * tensor-core kernel sets when it gives up; returns SGEMM_ERR_TIMEOUT if it was
  * set, SGEMM_OK otherwise.  Call after synchronising the work in question. */
