@@ -11,8 +11,10 @@
 
 #include <algorithm>
 
+#include "sgemm_ff_plan.h"
 #include "sgemm_gated_ff.cuh"
 #include "sgemm_launch.cuh"
+#include "sgemm_tma_host.h"
 
 namespace sgemm {
 namespace {
@@ -21,177 +23,386 @@ using namespace ff;
 
 constexpr int kThreads = 256;
 
-// An operand P(i, k) with steps si and sk between elements.
-struct Operand {
-    const void* p;
-    long long si, sk;
-};
-// C(i, j) = sum over both pairs and k of a(i, k) b(j, k); with GATED, C = act(first) second.
-struct Product {
-    int M, N, K;
-    Operand a[2], b[2];
-    int pairs;
-    void* c;
-    long long ldc;
-    FfKept kept;
-};
+// Eight 2-byte numbers at p, of which `n` are inside; vec: p is on 16 bytes.
 template <typename T>
-__device__ __forceinline__ float at(const Operand& o, long long i, long long k) {
-    return to_float(static_cast<const T*>(o.p)[i * o.si + k * o.sk]);
-}
-
-template <typename T, bool GATED, int ACT>
-__global__ void __launch_bounds__(kThreads) ff_product(const Product p) {
-    __shared__ float as[32][33], bs[2][32][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    wait_previous();
-    const long long tiles_j = (p.N + 31) / 32, tiles = tiles_j * ((p.M + 31) / 32);
-    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const long long i0 = tile / tiles_j * 32, j0 = tile % tiles_j * 32;
-        float acc[2][4] = {};
-        for (int pair = 0; pair < (GATED ? 1 : p.pairs); ++pair)
-            for (int k0 = 0; k0 < p.K; k0 += 32) {
-                __syncthreads();
-                for (int r = ty; r < 32; r += 8) {
-                    const bool ka = k0 + tx < p.K;
-                    as[r][tx] = ka && i0 + r < p.M ? at<T>(p.a[pair], i0 + r, k0 + tx) : 0.0f;
-                    bs[0][r][tx] = ka && j0 + r < p.N ? at<T>(p.b[pair], j0 + r, k0 + tx) : 0.0f;
-                    if (GATED)
-                        bs[1][r][tx] = ka && j0 + r < p.N ? at<T>(p.b[1], j0 + r, k0 + tx) : 0.0f;
-                }
-                __syncthreads();
-                for (int k = 0; k < 32; ++k)
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
+    if (vec && n >= 8) {
+        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));
+        const T* t = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        acc[0][r] = fmaf(as[ty + 8 * r][k], bs[0][tx][k], acc[0][r]);
-                        if (GATED) acc[1][r] = fmaf(as[ty + 8 * r][k], bs[1][tx][k], acc[1][r]);
-                    }
-            }
+        for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
+    } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const long long i = i0 + ty + 8 * r, j = j0 + tx;
-            if (i >= p.M || j >= p.N) continue;
-            float v = acc[0][r];
-            if (GATED) {
-                if (p.kept.keep == kKeep8) {       // fp32, for the quantisation that follows
-                    static_cast<float*>(p.kept.gate)[i * p.kept.ld + j] = v;
-                    static_cast<float*>(p.kept.up)[i * p.kept.ld + j] = acc[1][r];
-                } else if (p.kept.keep == kKeepFull) {
-                    static_cast<T*>(p.kept.gate)[i * p.kept.ld + j] = from_float<T>(v);
-                    static_cast<T*>(p.kept.up)[i * p.kept.ld + j] = from_float<T>(acc[1][r]);
-                }
-                v = act<ACT>(v) * acc[1][r];
-            }
-            static_cast<T*>(p.c)[i * p.ldc + j] = from_float<T>(v);
-        }
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_float(p[i]) : 0.0f;
     }
-    launch_next();
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&v)[8]) {
+    if (vec && n >= 8) {
+        alignas(16) T t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = from_float<T>(v[i]);
+        *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = from_float<T>(v[i]);
+    }
 }
 
-// dg, du (rows of `pitch`), and h again, from dh and what was kept.
-template <typename T, int ACT>
+struct Aligned {
+    bool dh, kept, h;
+};
+// dg, du (rows of `pitch`, a multiple of 64), and h again, from dh and what was kept: eight columns
+// a thread.
+template <typename T, int ACT, bool KEPT8>
 __global__ void __launch_bounds__(kThreads)
-    ff_gradient(const GatedFfBackward p, T* dg, T* du, long long pitch) {
-    const long long all = p.M * static_cast<long long>(p.N);
+    ff_gradient(const GatedFfBackward p, T* dg, T* du, long long pitch, const Aligned on) {
+    const int groups = (p.N + 7) / 8;
+    const long long all = p.M * static_cast<long long>(groups);
     const long long codes = act8_pitch(p.N);
     wait_previous();
     for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < all;
          i += static_cast<long long>(gridDim.x) * kThreads) {
-        const long long row = i / p.N, c = i - row * p.N;
-        float g, u;
-        if (p.kept.keep == kKeep8) {
+        const long long row = i / groups;
+        const int c = static_cast<int>(i - row * groups) * 8, n = p.N - c;
+        float g[8], u[8], dh[8];
+        load8(static_cast<const T*>(p.dh) + row * p.lddh + c, n, on.dh, dh);
+        if constexpr (KEPT8) {
             const long long k = row * codes + c;
-            g = act8::value(static_cast<const int8_t*>(p.kept.gate)[k], p.kept.gate_scales[k / 64]);
-            u = act8::value(static_cast<const int8_t*>(p.kept.up)[k], p.kept.up_scales[k / 64]);
+            const auto held = [&](const void* from, const float* scales, float (&v)[8]) {
+                const uint2 w =
+                    __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(from) + k));
+                const float s = __ldg(scales + k / kAct8Block);
+                act8::values4(w.x, s, reinterpret_cast<float(&)[4]>(v[0]));
+                act8::values4(w.y, s, reinterpret_cast<float(&)[4]>(v[4]));
+            };
+            held(p.kept.gate, p.kept.gate_scales, g);
+            held(p.kept.up, p.kept.up_scales, u);
         } else {
-            g = to_float(static_cast<const T*>(p.kept.gate)[row * p.kept.ld + c]);
-            u = to_float(static_cast<const T*>(p.kept.up)[row * p.kept.ld + c]);
+            load8(static_cast<const T*>(p.kept.gate) + row * p.kept.ld + c, n, on.kept, g);
+            load8(static_cast<const T*>(p.kept.up) + row * p.kept.ld + c, n, on.kept, u);
         }
-        const float dh = to_float(static_cast<const T*>(p.dh)[row * p.lddh + c]);
-        const Act a = Act::of<ACT>(g);
-        du[row * pitch + c] = from_float<T>(dh * a.value());
-        dg[row * pitch + c] = from_float<T>(dh * u * a.slope());
-        if (p.h) static_cast<T*>(p.h)[row * p.ldh + c] = from_float<T>(a.value() * u);
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const Act a = Act::of<ACT>(g[j]);
+            const float v = a.value();
+            h[j] = v * u[j];
+            g[j] = dh[j] * u[j] * a.slope();
+            u[j] = dh[j] * v;
+        }
+        store8(dg + row * pitch + c, 8, true, g);
+        store8(du + row * pitch + c, 8, true, u);
+        if (p.h) store8(static_cast<T*>(p.h) + row * p.ldh + c, n, on.h, h);
     }
     launch_next();
 }
 
-long long up64(long long n) { return (n + 63) / 64 * 64; }
-size_t matrix_bytes(long long rows, long long cols) {
-    return static_cast<size_t>(rows * up64(cols) * 2);
-}
-
-template <typename T, int ACT>
-cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* launches) {
-    Product q{p.M, p.N, p.K, {{p.x, p.ldx, 1}, {p.x, p.ldx, 1}},
-              {{p.w_gate, p.ldg, 1}, {p.w_up, p.ldu, 1}}, 2, p.h, p.ldh, p.kept};
-    float* full = nullptr;
-    if (p.kept.keep == kKeep8) {
-        full = reinterpret_cast<float*>(p.ws);
-        q.kept.gate = full;
-        q.kept.up = full + p.M * up64(p.N);
-        q.kept.ld = up64(p.N);
+// Matrices of 2-byte numbers into rows of `pitch`, eight columns a thread; blockIdx.y: which.
+struct Copies {
+    const uint16_t* from[3];
+    uint16_t* to[3];
+    long long ld[3], rows[3];
+    int cols;
+    long long pitch;
+};
+__global__ void __launch_bounds__(kThreads) ff_copy_rows(const Copies q) {
+    const int which = blockIdx.y, groups = (q.cols + 7) / 8;
+    const long long all = q.rows[which] * groups;
+    wait_previous();
+    for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < all;
+         i += static_cast<long long>(gridDim.x) * kThreads) {
+        const long long row = i / groups;
+        const int c = static_cast<int>(i - row * groups) * 8, n = q.cols - c;
+        const uint16_t* x = q.from[which] + row * q.ld[which] + c;
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) w[j / 2] |= static_cast<uint32_t>(__ldg(x + j)) << (j % 2 * 16);
+        *reinterpret_cast<uint4*>(q.to[which] + row * q.pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *launches = 1;
-    cudaError_t e = launch_dependent(ff_product<T, true, ACT>, dim3(sms * 8), kThreads, 0, st, q);
-    if (e != cudaSuccess || !full) return e;
-    *launches = 3;
-    e = launch_act8_quantize(Act8Quantize{p.M, p.N, mx4::kF32, q.kept.gate, q.kept.ld,
-                                          static_cast<int8_t*>(p.kept.gate), p.kept.gate_scales},
-                             sms, st);
+    launch_next();
+}
+
+// dx = the parts' sums, added in their order; four columns a thread.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ff_add_parts(const float* partial, long long ld, int split, int rows, int cols, T* dx,
+                 long long lddx) {
+    const int groups = (cols + 3) / 4;
+    const long long all = rows * static_cast<long long>(groups);
+    wait_previous();
+    for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < all;
+         i += static_cast<long long>(gridDim.x) * kThreads) {
+        const long long row = i / groups;
+        const int c = static_cast<int>(i - row * groups) * 4;
+        float4 s = make_float4(0, 0, 0, 0);
+        for (int k = 0; k < split; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(
+                partial + (k * static_cast<long long>(rows) + row) * ld + c);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c + j < cols) dx[row * lddx + c + j] = from_float<T>(v[j]);
+    }
+    launch_next();
+}
+
+// ----------------------------------------------------------------------------
+// Plans
+// ----------------------------------------------------------------------------
+long long up64(long long n) { return (n + 63) / 64 * 64; }
+long long matrix_bytes(long long rows, long long cols) { return rows * up64(cols) * 2; }
+long long up_to(long long n, int m) { return (n + m - 1) / m; }
+
+struct Choice {
+    int bn, split;
+};
+constexpr int kPairsOfGpu = 76;      // 152 SMs
+// Clocks of a stage: four MMAs of 128 for 256 columns; narrower ones wait for shared memory.
+int stage_clocks(int bn) { return bn == 256 ? 512 : bn == 128 ? 320 : 224; }
+
+Choice choose_forward(int M, int N, int K, int keep) {
+    Choice best{256, 1};
+    double least = 0;
+    for (int bn : {256, 128, 64}) {
+        if (bn == 64 && keep == kKeep8) continue;       // a block of 64 in two tiles
+        const long long rounds = up_to(up_to(M, kTileRows) * up_to(N, bn / 2), kPairsOfGpu);
+        const double t = static_cast<double>(rounds) * up_to(K, 64) * stage_clocks(bn) + 12.0 * bn;
+        if (least == 0 || t < least) best.bn = bn, least = t;
+    }
+    return best;
+}
+Choice choose_weights(int M, int N, int K) {
+    Choice best{256, 1};
+    double least = 0;
+    for (int bn : {256, 128}) {
+        const long long rounds = up_to(2 * up_to(N, kTileRows) * up_to(K, bn), kPairsOfGpu);
+        const double t = static_cast<double>(rounds) * (up_to(M, 64) * stage_clocks(bn) + 6.0 * bn);
+        if (least == 0 || t < least) best.bn = bn, least = t;
+    }
+    return best;
+}
+// Few tiles share a contraction between up to sixteen pairs, eight stages each at least; their
+// sums take another pass over M x K.
+Choice choose_input(int M, int N, int K) {
+    Choice best{256, 1};
+    double least = 0;
+    const long long stages = 2 * up_to(N, 64);
+    for (int bn : {256, 128}) {
+        const long long tiles = up_to(M, kTileRows) * up_to(K, bn);
+        for (int split = 1; split <= 16 && (split == 1 || stages / split >= 8); ++split) {
+            const double rounds = static_cast<double>(up_to(tiles * split, kPairsOfGpu));
+            double t = rounds * (up_to(stages, split) * stage_clocks(bn) + 12.0 * bn);
+            if (split > 1) t += 5000 + 8.0 * M * K * split / 2500;
+            if (least == 0 || t < least) best = {bn, split}, least = t;
+        }
+    }
+    return best;
+}
+
+// A matrix of 2-byte numbers, boxes of 64 columns by `box` rows, zeros outside.
+bool encode(CUtensorMap* tm, const void* base, long long rows, long long cols, long long ld, int box) {
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    // One row has no stride to speak of.
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? ld : up64(cols)) * 2};
+    cuuint32_t boxes[2] = {64, static_cast<cuuint32_t>(box)};
+    cuuint32_t steps[2] = {1, 1};
+    return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, boxes,
+              steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool on16(const void* p, long long rows, long long ld, int elem = 2) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld * elem % 16 == 0);
+}
+
+// What of a call's operands is copied into the workspace first, and where.
+struct Operands {
+    const void *x, *w_gate, *w_up;
+    long long ldx, ldg, ldu;
+    Copies copies{};
+    int n = 0;
+    uint8_t* at;
+    Operands(int M, int N, int K, const void* x_, long long ldx_, const void* g, long long ldg_,
+             const void* u, long long ldu_, uint8_t* ws)
+        : x(x_), w_gate(g), w_up(u), ldx(ldx_), ldg(ldg_), ldu(ldu_), at(ws) {
+        copies.cols = K;
+        copies.pitch = up64(K);
+        if (x) place(x, ldx, M);
+        place(w_gate, ldg, N);
+        place(w_up, ldu, N);
+    }
+    void place(const void*& p, long long& ld, long long rows) {
+        if (on16(p, rows, ld)) return;
+        copies.from[n] = static_cast<const uint16_t*>(p);
+        copies.to[n] = reinterpret_cast<uint16_t*>(at);
+        copies.ld[n] = ld;
+        copies.rows[n++] = rows;
+        p = at;
+        ld = copies.pitch;
+        at += matrix_bytes(rows, copies.cols);
+    }
+    cudaError_t copy(int sms, cudaStream_t st, int* launches) const {
+        if (n == 0) return cudaSuccess;
+        const long long most = std::max({copies.rows[0], copies.rows[1], copies.rows[2]});
+        const long long blocks = up_to(most * up_to(copies.cols, 8), kThreads);
+        ++*launches;
+        return launch_dependent(ff_copy_rows,
+                                dim3(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL)), n),
+                                kThreads, 0, st, copies);
+    }
+};
+
+template <typename T>
+cudaError_t pair(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int act, int sms,
+                 cudaStream_t st) {
+    return std::is_same<T, __half>::value ? pair_f16(maps, pl, mode, bn, act, sms, st)
+                                          : pair_bf16(maps, pl, mode, bn, act, sms, st);
+}
+
+template <typename T>
+cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* launches) {
+    const Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, p.ws);
+    cudaError_t e = in.copy(sms, st, launches);
     if (e != cudaSuccess) return e;
-    return launch_act8_quantize(Act8Quantize{p.M, p.N, mx4::kF32, q.kept.up, q.kept.ld,
-                                             static_cast<int8_t*>(p.kept.up), p.kept.up_scales},
-                                sms, st);
+    const Choice c = choose_forward(p.M, p.N, p.K, p.kept.keep);
+    PairMaps maps;
+    if (!encode(&maps.a[0], in.x, p.M, p.K, in.ldx, 128) ||
+        !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, c.bn / 2) ||
+        !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, c.bn / 2))
+        return cudaErrorInvalidValue;
+    maps.a[1] = maps.a[0];
+    PairPlan pl{};
+    pl.rows = p.M;
+    pl.cols = p.N;
+    pl.tiles_m = static_cast<int>(up_to(p.M, kTileRows));
+    pl.tiles_n = static_cast<int>(up_to(p.N, c.bn / 2));
+    pl.stages = static_cast<int>(up_to(p.K, 64));
+    pl.split = 1;
+    pl.c[0] = p.h;
+    pl.ldc[0] = p.ldh;
+    pl.c_vec = on16(p.h, p.M, p.ldh);
+    pl.kept = p.kept;
+    pl.kept_vec = on16(p.kept.gate, p.M, p.kept.ld) && on16(p.kept.up, p.M, p.kept.ld);
+    pl.status = status_word_ptr();
+    ++*launches;
+    return pair<T>(maps, pl, kForward, c.bn, p.activation, sms, st);
 }
 
 template <typename T, int ACT>
+cudaError_t gradient(const GatedFfBackward& p, T* dg, T* du, long long pitch, int sms,
+                     cudaStream_t st) {
+    const Aligned on{on16(p.dh, p.M, p.lddh),
+                     on16(p.kept.gate, p.M, p.kept.ld) && on16(p.kept.up, p.M, p.kept.ld),
+                     on16(p.h, p.M, p.ldh)};
+    const long long blocks = up_to(p.M * up_to(p.N, 8), kThreads);
+    const dim3 grid(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL)));
+    return p.kept.keep == kKeep8
+               ? launch_dependent(ff_gradient<T, ACT, true>, grid, kThreads, 0, st, p, dg, du, pitch, on)
+               : launch_dependent(ff_gradient<T, ACT, false>, grid, kThreads, 0, st, p, dg, du, pitch, on);
+}
+
+template <typename T>
 cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* launches) {
     const long long pitch = up64(p.N);
-    T* dg = reinterpret_cast<T*>(p.ws);
-    T* du = dg + p.M * pitch;
-    const void* x = p.x;
-    long long ldx = p.ldx;
-    cudaError_t e;
-    *launches = 0;
-    if (p.x_codes) {
-        ldx = up64(p.K);
-        x = du + p.M * pitch;
-        e = launch_act8_dequantize(Act8Dequantize{p.M, p.K, p.dtype, p.x_codes, p.x_scales,
-                                                  const_cast<void*>(x), ldx}, sms, st);
+    T* const dg = reinterpret_cast<T*>(p.ws);
+    T* const du = dg + p.M * pitch;
+    uint8_t* at = reinterpret_cast<uint8_t*>(du + p.M * pitch);
+    Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, at);
+    if (p.x_codes) {       // rounded to the operands' type
+        in.x = in.at;
+        in.ldx = up64(p.K);
+        in.at += matrix_bytes(p.M, p.K);
+        const cudaError_t e = launch_act8_dequantize(
+            Act8Dequantize{p.M, p.K, p.dtype, p.x_codes, p.x_scales, const_cast<void*>(in.x), in.ldx},
+            sms, st);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
-    e = launch_dependent(ff_gradient<T, ACT>, dim3(sms * 8), kThreads, 0, st, p, dg, du, pitch);
+    cudaError_t e = in.copy(sms, st, launches);
     if (e != cudaSuccess) return e;
-    const Product dx{p.M, p.K, p.N, {{dg, pitch, 1}, {du, pitch, 1}},
-                     {{p.w_gate, 1, p.ldg}, {p.w_up, 1, p.ldu}}, 2, p.dx, p.lddx, {}};
-    e = launch_dependent(ff_product<T, false, ACT>, dim3(sms * 8), kThreads, 0, st, dx);
+    e = p.activation == kSilu ? gradient<T, kSilu>(p, dg, du, pitch, sms, st)
+                              : gradient<T, kGeluTanh>(p, dg, du, pitch, sms, st);
     if (e != cudaSuccess) return e;
-    const Product dwg{p.N, p.K, p.M, {{dg, 1, pitch}, {}}, {{x, 1, ldx}, {}}, 1, p.dw_gate, p.lddwg, {}};
-    e = launch_dependent(ff_product<T, false, ACT>, dim3(sms * 8), kThreads, 0, st, dwg);
+    ++*launches;
+
+    PairMaps maps;
+    PairPlan pl{};
+    pl.status = status_word_ptr();
+    // dx, from dg and Wg, then du and Wu.
+    const Choice ci = choose_input(p.M, p.N, p.K);
+    if (!encode(&maps.a[0], dg, p.M, p.N, pitch, 128) || !encode(&maps.a[1], du, p.M, p.N, pitch, 128) ||
+        !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, 64) ||
+        !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, 64))
+        return cudaErrorInvalidValue;
+    pl.rows = p.M;
+    pl.cols = p.K;
+    pl.tiles_m = static_cast<int>(up_to(p.M, kTileRows));
+    pl.tiles_n = static_cast<int>(up_to(p.K, ci.bn));
+    pl.stages = static_cast<int>(2 * up_to(p.N, 64));
+    pl.split = ci.split;
+    pl.c[0] = p.dx;
+    pl.ldc[0] = p.lddx;
+    pl.c_vec = on16(p.dx, p.M, p.lddx);
+    pl.partial = ci.split > 1 ? reinterpret_cast<float*>(in.at) : nullptr;
+    pl.partial_ld = up64(p.K);
+    e = pair<T>(maps, pl, kInput, ci.bn, p.activation, sms, st);
     if (e != cudaSuccess) return e;
-    const Product dwu{p.N, p.K, p.M, {{du, 1, pitch}, {}}, {{x, 1, ldx}, {}}, 1, p.dw_up, p.lddwu, {}};
-    *launches += 4;
-    return launch_dependent(ff_product<T, false, ACT>, dim3(sms * 8), kThreads, 0, st, dwu);
+    ++*launches;
+    if (pl.partial) {
+        const long long blocks = up_to(p.M * up_to(p.K, 4), kThreads);
+        e = launch_dependent(ff_add_parts<T>,
+                             dim3(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL))),
+                             kThreads, 0, st, pl.partial, pl.partial_ld, pl.split, p.M, p.K,
+                             static_cast<T*>(p.dx), p.lddx);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    // dWg, then dWu.
+    const Choice cw = choose_weights(p.M, p.N, p.K);
+    if (!encode(&maps.a[0], dg, p.M, p.N, pitch, 64) || !encode(&maps.a[1], du, p.M, p.N, pitch, 64) ||
+        !encode(&maps.b[0], in.x, p.M, p.K, in.ldx, 64))
+        return cudaErrorInvalidValue;
+    maps.b[1] = maps.b[0];
+    pl.rows = p.N;
+    pl.tiles_m = static_cast<int>(2 * up_to(p.N, kTileRows));
+    pl.tiles_n = static_cast<int>(up_to(p.K, cw.bn));
+    pl.stages = static_cast<int>(up_to(p.M, 64));
+    pl.split = 1;
+    pl.partial = nullptr;
+    pl.c[0] = p.dw_gate;
+    pl.c[1] = p.dw_up;
+    pl.ldc[0] = p.lddwg;
+    pl.ldc[1] = p.lddwu;
+    pl.c_vec = on16(p.dw_gate, p.N, p.lddwg) && on16(p.dw_up, p.N, p.lddwu);
+    ++*launches;
+    return pair<T>(maps, pl, kWeights, cw.bn, p.activation, sms, st);
+}
+
+// Copies of the operands that are not read in place.
+size_t copied_bytes(int M, int N, int K, int packed) {
+    return static_cast<size_t>((packed & 1 ? matrix_bytes(M, K) : 0) +
+                               (packed & 2 ? matrix_bytes(N, K) : 0) +
+                               (packed & 4 ? matrix_bytes(N, K) : 0));
+}
+int packed_bit(int bit, const void* p, long long rows, long long ld) {
+    return on16(p, rows, ld) ? 0 : bit;
 }
 
 }  // namespace
 
-// Copies of the operands that are not read in place.
-size_t copied_bytes(int M, int N, int K, int packed) {
-    return (packed & 1 ? matrix_bytes(M, K) : 0) + (packed & 2 ? matrix_bytes(N, K) : 0) +
-           (packed & 4 ? matrix_bytes(N, K) : 0);
-}
-int packed_bit(int bit, const void* p, long long rows, long long ld) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld % 8 == 0) ? 0 : bit;
-}
-
 size_t gated_ff_forward_workspace(int M, int N, int K, int packed) {
-    return 4 * matrix_bytes(M, N) + copied_bytes(M, N, K, packed);
+    return copied_bytes(M, N, K, packed);
 }
 size_t gated_ff_backward_workspace(int M, int N, int K, int packed) {
-    return 2 * matrix_bytes(M, N) + copied_bytes(M, N, K, packed);
+    const Choice c = choose_input(M, N, K);
+    const size_t parts = c.split > 1 ? static_cast<size_t>(c.split) * 2 * matrix_bytes(M, K) : 0;
+    return 2 * static_cast<size_t>(matrix_bytes(M, N)) + copied_bytes(M, N, K, packed) + parts;
 }
 int gated_ff_packed(const GatedFfForward& p) {
     return packed_bit(1, p.x, p.M, p.ldx) | packed_bit(2, p.w_gate, p.N, p.ldg) |
@@ -204,21 +415,15 @@ int gated_ff_packed(const GatedFfBackward& p) {
 
 cudaError_t launch_gated_ff_forward(const GatedFfForward& p, int sms, cudaStream_t stream,
                                     int* launches) {
-    const bool silu = p.activation == kSilu;
-    if (p.dtype == kBf16)
-        return silu ? forward<__nv_bfloat16, kSilu>(p, sms, stream, launches)
-                    : forward<__nv_bfloat16, kGeluTanh>(p, sms, stream, launches);
-    return silu ? forward<__half, kSilu>(p, sms, stream, launches)
-                : forward<__half, kGeluTanh>(p, sms, stream, launches);
+    *launches = 0;
+    return p.dtype == kBf16 ? forward<__nv_bfloat16>(p, sms, stream, launches)
+                            : forward<__half>(p, sms, stream, launches);
 }
 cudaError_t launch_gated_ff_backward(const GatedFfBackward& p, int sms, cudaStream_t stream,
                                      int* launches) {
-    const bool silu = p.activation == kSilu;
-    if (p.dtype == kBf16)
-        return silu ? backward<__nv_bfloat16, kSilu>(p, sms, stream, launches)
-                    : backward<__nv_bfloat16, kGeluTanh>(p, sms, stream, launches);
-    return silu ? backward<__half, kSilu>(p, sms, stream, launches)
-                : backward<__half, kGeluTanh>(p, sms, stream, launches);
+    *launches = 0;
+    return p.dtype == kBf16 ? backward<__nv_bfloat16>(p, sms, stream, launches)
+                            : backward<__half>(p, sms, stream, launches);
 }
 
 }  // namespace sgemm
