@@ -67,5 +67,39 @@ __device__ __forceinline__ float value(int8_t code, float scale) {
     return static_cast<float>(code) * scale;
 }
 
+// 16 bytes that are read once: not into the L1 cache.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+// One 16-byte group of a row to the codes at `c` and, from the first of the lanes of a block of
+// 64, its scale.  Whole warps.
+template <typename T>
+__device__ __forceinline__ void keep_group(const uint4& raw, int8_t* codes, float* scales, int c,
+                                           bool live) {
+    constexpr int VEC = 16 / sizeof(T), LANES = kAct8Block / VEC;
+    Two x[VEC / 2];
+    mx4::unpack(raw, x, T());
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+        const float2 f = mx4::parts(x[j]);
+        amax = max(amax, max(magnitude(f.x), magnitude(f.y)));
+    }
+    const BlockScale s(block_amax<LANES>(amax));
+    if (!live) return;
+    uint32_t w[VEC / 4];
+#pragma unroll
+    for (int j = 0; j < VEC / 4; ++j) {
+        const float2 f = mx4::parts(x[2 * j]), g = mx4::parts(x[2 * j + 1]);
+        w[j] = s.codes4(f.x, f.y, g.x, g.y);
+    }
+    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(codes + c) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(codes + c) = w[0];
+    if (c % kAct8Block == 0) scales[c / kAct8Block] = s.scale;
+}
+
 }  // namespace act8
 }  // namespace sgemm

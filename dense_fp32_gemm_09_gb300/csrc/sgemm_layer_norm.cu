@@ -15,6 +15,7 @@
 
 #include "sgemm_act8.cuh"
 #include "sgemm_launch.cuh"
+#include "sgemm_layer_norm.h"
 
 namespace sgemm {
 namespace {
@@ -147,50 +148,136 @@ __global__ void __launch_bounds__(1024) layer_norm_columns(const LayerNormBackwa
     launch_next();
 }
 
-// Blocks of the backward kernel (each keeps a set of column sums).
-int backward_grid(int rows, int sms) {
-    return static_cast<int>(std::min<long long>(rows, 2LL * sms));
+// ----------------------------------------------------------------------------
+// Choice of kernel
+// ----------------------------------------------------------------------------
+using layer_norm::kByBlock;
+using layer_norm::kByWarp;
+using layer_norm::kWide;
+using layer_norm::Shape;
+
+// Whether every row (one a call has no stride to speak of) and vector is on 16 bytes.
+struct Alignment {
+    bool whole = true;
+    long long rows;
+    int elem;
+    Alignment(int dtype, long long r, int cols) : rows(r), elem(dtype == kF32 ? 4 : 2) {
+        whole = static_cast<long long>(cols) * elem % 16 == 0;
+    }
+    void add(const void* p, long long ld) {
+        if (p == nullptr) return;
+        whole &= reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld * elem % 16 == 0);
+    }
+};
+// A block a row, `own` columns a thread; up to `most` threads an SM.
+Shape by_block(long long rows, int cols, int own, int most, bool ragged, int sms) {
+    Shape s{};
+    s.kind = kByBlock;
+    s.ragged = ragged;
+    s.columns = own;
+    s.threads = 64;
+    while (s.threads * own < cols) s.threads *= 2;
+    const int per = std::min(most / s.threads, 16);
+    s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * per));
+    return s;
+}
+
+Shape forward_shape(const LayerNormForward& p, int sms) {
+    Alignment on(p.dtype, p.rows, p.cols);
+    on.add(p.x, p.ldx);
+    on.add(p.y, p.ldy);
+    on.add(p.weight, 0);
+    on.add(p.bias, 0);
+    if (!on.whole) {
+        if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, true, sms);
+        return Shape{kWide};
+    }
+    const int vec = 16 / on.elem;
+    if (p.rows > 2LL * sms && p.cols <= 32 * 32 * vec) {
+        Shape s{};
+        s.kind = kByWarp;
+        s.groups = 1;
+        while (s.groups * 32 * vec < p.cols) s.groups *= 2;
+        s.grid = (p.rows + 3) / 4;
+        return s;
+    }
+    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, false, sms);
+    if (p.cols <= 16 * 1024) return by_block(p.rows, p.cols, 16, 1024, false, sms);
+    return Shape{kWide};
+}
+
+// Up to 512 threads hold a row's numbers and the sums over rows: eight columns a thread of
+// ragged or fp32 rows, sixteen of 2-byte ones.
+Shape backward_shape(const LayerNormBackward& p, int sms) {
+    Alignment on(p.dtype, p.rows, p.cols);
+    on.add(p.dh, p.lddh);
+    on.add(p.dy, p.lddy);
+    on.add(p.x, p.ldx);
+    on.add(p.dx, p.lddx);
+    on.add(p.weight, 0);
+    const int own = !on.whole || p.dtype == kF32 ? 8 : 16;
+    if (p.cols <= own * 512) return by_block(p.rows, p.cols, own, 512, !on.whole, sms);
+    Shape s{kWide};
+    s.grid = static_cast<int>(std::min<long long>(p.rows, 2LL * sms));
+    return s;
 }
 
 }  // namespace
 
 size_t layer_norm_backward_workspace(int rows, int cols, int sms) {
-    return static_cast<size_t>(backward_grid(rows, sms)) * 2 * cols * sizeof(float);
+    long long grid = std::min<long long>(rows, 2LL * sms);
+    for (int own : {8, 16})
+        if (cols <= own * 512)
+            grid = std::max<long long>(grid, by_block(rows, cols, own, 512, false, sms).grid);
+    return static_cast<size_t>(grid) * 2 * cols * sizeof(float);
 }
 
 cudaError_t launch_layer_norm_forward(const LayerNormForward& p, int sms, cudaStream_t stream,
                                       int* launches) {
     *launches = 1;
-    const dim3 grid(static_cast<unsigned>(p.rows));
+    const Shape s = forward_shape(p, sms);
     cudaError_t e;
-    if (p.dtype == kF32)
-        e = launch_dependent(layer_norm_forward_wide<float>, grid, kThreads, 0, stream, p);
-    else if (p.dtype == kBf16)
-        e = launch_dependent(layer_norm_forward_wide<__nv_bfloat16>, grid, kThreads, 0, stream, p);
-    else
-        e = launch_dependent(layer_norm_forward_wide<__half>, grid, kThreads, 0, stream, p);
-    if (e != cudaSuccess || p.codes == nullptr) return e;
-    *launches = 2;
+    if (s.kind == kWide) {
+        const dim3 grid(static_cast<unsigned>(p.rows));
+        if (p.dtype == kF32)
+            e = launch_dependent(layer_norm_forward_wide<float>, grid, kThreads, 0, stream, p);
+        else if (p.dtype == kBf16)
+            e = launch_dependent(layer_norm_forward_wide<__nv_bfloat16>, grid, kThreads, 0, stream, p);
+        else
+            e = launch_dependent(layer_norm_forward_wide<__half>, grid, kThreads, 0, stream, p);
+    } else {
+        e = p.dtype == kF32    ? layer_norm::forward_f32(p, s, stream)
+            : p.dtype == kBf16 ? layer_norm::forward_bf16(p, s, stream)
+                               : layer_norm::forward_f16(p, s, stream);
+    }
+    if (e != cudaSuccess || p.codes == nullptr || (s.kind != kWide && !s.ragged)) return e;
+    *launches = 2;         // a pass of its own over rows that are read by elements
     return launch_act8_quantize(
         Act8Quantize{p.rows, p.cols, p.dtype, p.x, p.ldx, p.codes, p.scales}, sms, stream);
 }
 
 cudaError_t launch_layer_norm_backward(const LayerNormBackward& p, int sms, cudaStream_t stream,
                                        int* launches) {
-    const int blocks = backward_grid(p.rows, sms);
-    const dim3 grid(static_cast<unsigned>(blocks));
+    const Shape s = backward_shape(p, sms);
     *launches = 1;
     cudaError_t e;
-    if (p.dtype == kF32)
-        e = launch_dependent(layer_norm_backward_wide<float>, grid, kThreads, 0, stream, p);
-    else if (p.dtype == kBf16)
-        e = launch_dependent(layer_norm_backward_wide<__nv_bfloat16>, grid, kThreads, 0, stream, p);
-    else
-        e = launch_dependent(layer_norm_backward_wide<__half>, grid, kThreads, 0, stream, p);
+    if (s.kind == kWide) {
+        const dim3 grid(s.grid);
+        if (p.dtype == kF32)
+            e = launch_dependent(layer_norm_backward_wide<float>, grid, kThreads, 0, stream, p);
+        else if (p.dtype == kBf16)
+            e = launch_dependent(layer_norm_backward_wide<__nv_bfloat16>, grid, kThreads, 0, stream, p);
+        else
+            e = launch_dependent(layer_norm_backward_wide<__half>, grid, kThreads, 0, stream, p);
+    } else {
+        e = p.dtype == kF32    ? layer_norm::backward_f32(p, s, stream)
+            : p.dtype == kBf16 ? layer_norm::backward_bf16(p, s, stream)
+                               : layer_norm::backward_f16(p, s, stream);
+    }
     if (e != cudaSuccess || (!p.dweight && !p.dbias)) return e;
     *launches = 2;
     return launch_dependent(layer_norm_columns, dim3((p.cols + 31) / 32, 2), 1024, 0, stream, p,
-                            blocks);
+                            s.grid);
 }
 
 }  // namespace sgemm

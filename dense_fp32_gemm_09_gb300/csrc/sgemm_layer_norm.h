@@ -1,0 +1,27 @@
+// Launch shapes of the layer norm kernels that keep a row in registers, and their launchers, one
+// translation unit for each element type.
+#pragma once
+
+#include "sgemm_block_train.h"
+
+namespace sgemm {
+namespace layer_norm {
+
+enum : int { kByBlock = 0, kByWarp = 1, kWide = 2 };
+struct Shape {
+    int kind;
+    int threads, grid;
+    int columns;       // of a thread, by block
+    int groups;        // of 16 bytes a lane, by warp
+    bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
+};
+
+cudaError_t forward_f32(const LayerNormForward& p, const Shape& s, cudaStream_t st);
+cudaError_t forward_bf16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
+cudaError_t forward_f16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
+cudaError_t backward_f32(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
+cudaError_t backward_bf16(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
+cudaError_t backward_f16(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
+
+}  // namespace layer_norm
+}  // namespace sgemm

@@ -252,8 +252,9 @@ def test_long_offsets(sg):
     x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
     x[-64:] = cuda(c.x)
     y, mean, rstd = sg.layer_norm(x, cuda(c.w), cuda(c.b))
-    want = sg.layer_norm(x[-64:].clone(), cuda(c.w), cuda(c.b))
-    assert torch.equal(y[-64:], want[0]) and torch.equal(mean[-64:], want[1])
+    # (A call of 64 rows may sum a row in another order.)
+    for got, want, rel in zip((y, mean, rstd), check_forward(sg, c), (2 * c.u, 2 * c.e, 2 * c.e)):
+        assert torch.allclose(got[-64:].float(), want.float(), rtol=rel, atol=4 * c.e)
     assert torch.equal(y[0].float(), cuda(c.b).bfloat16().float())
 
 
