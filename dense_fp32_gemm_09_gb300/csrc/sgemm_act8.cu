@@ -19,7 +19,29 @@ using namespace act8;
 using mx4::from_float;
 using mx4::to_float;
 
-constexpr int kThreads = 256, kAhead = 4;
+constexpr int kThreads = 256, kAhead = 2;
+
+// 32 bytes of a row, at any 16.
+__device__ __forceinline__ void load_pair(const void* p, bool on32, uint4 (&v)[2]) {
+    if (on32) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
+                       "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w) : "l"(p));
+    } else {
+        v[0] = __ldg(static_cast<const uint4*>(p));
+        v[1] = __ldg(static_cast<const uint4*>(p) + 1);
+    }
+}
+__device__ __forceinline__ void store_pair(void* p, bool on32, const uint4 (&v)[2]) {
+    if (on32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0].x),
+                     "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z),
+                     "r"(v[1].w) : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = v[0];
+        static_cast<uint4*>(p)[1] = v[1];
+    }
+}
 
 // Walks the groups `i`, `i + step`, ... of rows of `groups` without a division a step.
 struct Walk {
@@ -41,34 +63,37 @@ struct Walk {
     }
 };
 
-// A thread takes 16 bytes of a row, four such groups in flight.
+// A thread takes 32 bytes of a row, kAhead such pieces in flight.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantize q) {
-    constexpr int VEC = 16 / sizeof(T);
+__global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantize q, const bool on32) {
+    constexpr int COLS = 32 / sizeof(T);
     const long long pitch = act8_pitch(q.cols);
     const long long step = static_cast<long long>(gridDim.x) * kThreads;
     Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x, step,
-            static_cast<int>(pitch / VEC));
+            static_cast<int>(pitch / COLS));
     wait_previous();
     // Whole warps: a block's lanes are in one row, and all there.
     long long first = __shfl_sync(0xFFFFFFFFu, at.row, 0);
     while (first < q.rows) {
-        uint4 raw[kAhead];
+        uint4 raw[kAhead][2];
         long long row[kAhead];
         int col[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             row[i] = at.row;
-            col[i] = at.col * VEC;
-            raw[i] = at.row < q.rows && col[i] < q.cols
-                         ? load_once(static_cast<const T*>(q.X) + at.row * q.ldx + col[i])
-                         : make_uint4(0, 0, 0, 0);
+            col[i] = at.col * COLS;
+            raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+            const T* x = static_cast<const T*>(q.X) + at.row * q.ldx + col[i];
+            if (at.row < q.rows) {
+                if (col[i] + COLS <= q.cols) load_pair(x, on32, raw[i]);
+                else if (col[i] < q.cols) raw[i][0] = __ldg(reinterpret_cast<const uint4*>(x));
+            }
             at.next();
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            keep_group<T>(raw[i], q.codes + row[i] * pitch, q.scales + row[i] * (pitch / kAct8Block),
-                          col[i], row[i] < q.rows);
+            keep_groups<T, 2>(raw[i], q.codes + row[i] * pitch,
+                              q.scales + row[i] * (pitch / kAct8Block), col[i], row[i] < q.rows);
         first = __shfl_sync(0xFFFFFFFFu, at.row, 0);
     }
     launch_next();
@@ -105,45 +130,56 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quant
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequantize q) {
-    constexpr int VEC = 16 / sizeof(T);
+__global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequantize q,
+                                                                 const bool on32) {
+    constexpr int VEC = 16 / sizeof(T), COLS = 2 * VEC;
     const long long pitch = act8_pitch(q.cols);
     const long long step = static_cast<long long>(gridDim.x) * kThreads;
-    Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x, step, q.cols / VEC);
+    Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x, step,
+            (q.cols + COLS - 1) / COLS);
     wait_previous();
     while (at.row < q.rows) {
-        uint32_t codes[kAhead][VEC / 4];
+        uint32_t codes[kAhead][COLS / 4];
         float scale[kAhead];
         T* to[kAhead];
+        bool both[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             to[i] = nullptr;
             if (at.row < q.rows) {
-                const long long k = at.row * pitch + at.col * VEC;
-                if constexpr (VEC == 8) {
+                const long long k = at.row * pitch + at.col * COLS;
+                if constexpr (COLS == 16) {
+                    const uint4 w = load_once(q.codes + k);
+                    codes[i][0] = w.x;
+                    codes[i][1] = w.y;
+                    codes[i][2] = w.z;
+                    codes[i][3] = w.w;
+                } else {
                     const uint2 w = __ldg(reinterpret_cast<const uint2*>(q.codes + k));
                     codes[i][0] = w.x;
                     codes[i][1] = w.y;
-                } else {
-                    codes[i][0] = __ldg(reinterpret_cast<const uint32_t*>(q.codes + k));
                 }
                 scale[i] = __ldg(q.scales + k / kAct8Block);
-                to[i] = static_cast<T*>(q.Y) + at.row * q.ldy + at.col * VEC;
+                to[i] = static_cast<T*>(q.Y) + at.row * q.ldy + at.col * COLS;
+                both[i] = at.col * COLS + COLS <= q.cols;
             }
             at.next();
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (to[i] == nullptr) break;
-            alignas(16) T out[VEC];
+            uint4 out[2];
 #pragma unroll
-            for (int j = 0; j < VEC / 4; ++j) {
-                float v[4];
-                values4(codes[i][j], scale[i], v);
+            for (int g = 0; g < 2; ++g) {
+                Two v[VEC / 2];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) out[4 * j + k] = from_float<T>(v[k]);
+                for (int j = 0; j < VEC / 4; ++j)
+                    values4(codes[i][g * VEC / 4 + j], scale[i],
+                            reinterpret_cast<Two(&)[2]>(v[2 * j]));
+                out[g] = mx4::pack(v, T());
             }
-            *reinterpret_cast<uint4*>(to[i]) = *reinterpret_cast<const uint4*>(out);
+            if (both[i]) store_pair(to[i], on32, out);
+            else *reinterpret_cast<uint4*>(to[i]) = out[0];
         }
     }
     launch_next();
@@ -185,24 +221,28 @@ dim3 grid_of(long long units, int each, int sms) {
     return dim3(static_cast<unsigned>(std::max(1LL, std::min<long long>(blocks, sms * 8LL))));
 }
 
+// Whether they start on 32 bytes.
+bool on_32(const void* p, long long rows, long long ld, int elem) {
+    return reinterpret_cast<uintptr_t>(p) % 32 == 0 && (rows <= 1 || ld * elem % 32 == 0);
+}
 template <typename T>
 cudaError_t quantize(const Act8Quantize& q, int sms, cudaStream_t st) {
     const long long pitch = act8_pitch(q.cols);
     if (whole(q.X, q.rows, q.cols, q.ldx, sizeof(T)))
         return launch_dependent(act8_quantize_rows<T>,
-                                grid_of(q.rows * (pitch * sizeof(T) / 16), kThreads, sms), kThreads, 0,
-                                st, q);
+                                grid_of(q.rows * (pitch * sizeof(T) / 32), kThreads, sms), kThreads, 0,
+                                st, q, on_32(q.X, q.rows, q.ldx, sizeof(T)));
     return launch_dependent(act8_quantize_ragged<T>,
                             grid_of(q.rows * ((pitch + 255) / 256), kThreads / 32, sms), kThreads, 0, st,
                             q);
 }
 template <typename T>
 cudaError_t dequantize(const Act8Dequantize& q, int sms, cudaStream_t st) {
+    constexpr int COLS = 32 / sizeof(T);
     if (whole(q.Y, q.rows, q.cols, q.ldy, sizeof(T)))
-        return launch_dependent(
-            act8_dequantize_rows<T>,
-            grid_of(q.rows * (static_cast<long long>(q.cols) * sizeof(T) / 16), kThreads, sms), kThreads,
-            0, st, q);
+        return launch_dependent(act8_dequantize_rows<T>,
+                                grid_of(q.rows * ((q.cols + COLS - 1LL) / COLS), kThreads, sms),
+                                kThreads, 0, st, q, on_32(q.Y, q.rows, q.ldy, sizeof(T)));
     return launch_dependent(act8_dequantize_ragged<T>,
                             grid_of(q.rows * ((act8_pitch(q.cols) + 255) / 256), kThreads / 32, sms),
                             kThreads, 0, st, q);

@@ -74,8 +74,15 @@ __global__ void __launch_bounds__(kThreads)
                 const uint2 w =
                     __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(from) + k));
                 const float s = __ldg(scales + k / kAct8Block);
-                act8::values4(w.x, s, reinterpret_cast<float(&)[4]>(v[0]));
-                act8::values4(w.y, s, reinterpret_cast<float(&)[4]>(v[4]));
+                mx4::Two t[4];
+                act8::values4(w.x, s, reinterpret_cast<mx4::Two(&)[2]>(t[0]));
+                act8::values4(w.y, s, reinterpret_cast<mx4::Two(&)[2]>(t[2]));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = mx4::parts(t[j]);
+                    v[2 * j] = f.x;
+                    v[2 * j + 1] = f.y;
+                }
             };
             held(p.kept.gate, p.kept.gate_scales, g);
             held(p.kept.up, p.kept.up_scales, u);

@@ -175,7 +175,7 @@ Shape by_block(long long rows, int cols, int own, int most, bool ragged, int sms
     s.kind = kByBlock;
     s.ragged = ragged;
     s.columns = own;
-    s.threads = 64;
+    s.threads = 32;
     while (s.threads * own < cols) s.threads *= 2;
     const int per = std::min(most / s.threads, 16);
     s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * per));
@@ -192,17 +192,18 @@ Shape forward_shape(const LayerNormForward& p, int sms) {
         if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, true, sms);
         return Shape{kWide};
     }
-    const int vec = 16 / on.elem;
-    if (p.rows > 2LL * sms && p.cols <= 32 * 32 * vec) {
+    if (p.rows <= 2LL * sms && p.cols <= 8 * 1024)
+        return by_block(p.rows, p.cols, 8, 1024, false, sms);
+    if (p.cols <= 256) {
         Shape s{};
         s.kind = kByWarp;
-        s.groups = 1;
-        while (s.groups * 32 * vec < p.cols) s.groups *= 2;
-        s.grid = (p.rows + 3) / 4;
+        s.groups = p.cols * on.elem <= 512 ? 1 : 2;
+        s.grid = static_cast<int>((p.rows + 3LL) / 4);
         return s;
     }
-    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, false, sms);
-    if (p.cols <= 16 * 1024) return by_block(p.rows, p.cols, 16, 1024, false, sms);
+    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 16, 512, false, sms);
+    // Wider 2-byte rows, as far as weight and bias fit beside them in shared memory.
+    if (p.cols <= 16 * 1024 && on.elem == 2) return by_block(p.rows, p.cols, 16, 1024, false, sms);
     return Shape{kWide};
 }
 

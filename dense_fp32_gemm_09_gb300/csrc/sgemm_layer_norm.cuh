@@ -14,7 +14,8 @@
 namespace sgemm {
 namespace layer_norm {
 
-using act8::keep_group;
+using act8::add;
+using act8::keep_groups;
 using act8::load_once;
 using mx4::from_float;
 using mx4::parts;
@@ -27,11 +28,6 @@ using norm::BlockSum;
 using norm::kPairs;
 using norm::Own;
 
-__device__ __forceinline__ Two add(Two a, Two b) {
-    Two r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -113,11 +109,11 @@ __global__ void __launch_bounds__(kWarpThreads) forward_warp(const LayerNormForw
 #pragma unroll
                 for (int j = 0; j < P; ++j)
                     v[j] = mx4::fma(mx4::mul(add(v[j], less), r2), w[j], b[j]);
-                *reinterpret_cast<uint4*>(y + c) = norm::pack(v, T());
+                *reinterpret_cast<uint4*>(y + c) = mx4::pack(v, T());
             }
             if constexpr (KEEP)
                 if (32 * i * VEC < pitch)
-                    keep_group<T>(raw[i], p.codes + row * pitch, p.scales + row * (pitch / kAct8Block),
+                    keep_groups<T, 1>({raw[i]}, p.codes + row * pitch, p.scales + row * (pitch / kAct8Block),
                                   c, c < pitch);
         }
     }
@@ -125,68 +121,200 @@ __global__ void __launch_bounds__(kWarpThreads) forward_warp(const LayerNormForw
 }
 
 // ----------------------------------------------------------------------------
-// Forward, one block a row: OWN columns a thread (see Own), the next row loaded while this one
-// is reduced
+// Forward, a block takes ROWS rows at a time: OWN columns a thread (see Own)
 // ----------------------------------------------------------------------------
-template <typename T, bool VEC, int OWN, bool KEEP>
-__global__ void __launch_bounds__(1024, 1) forward_block(const LayerNormForward p) {
+// Sums of two numbers over the warp: to every lane, with one exchange for the two of them (the
+// upper half of the warp goes on with the second).
+__device__ __forceinline__ float2 warp_sums(float a, float b) {
+    const bool upper = threadIdx.x & 16;
+    float v = upper ? b : a;
+    v += __shfl_xor_sync(0xFFFFFFFFu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    const float w = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+    return upper ? make_float2(w, v) : make_float2(v, w);
+}
+template <int ROWS>
+__device__ __forceinline__ void warp_sums(float (&v)[ROWS]) {
+    if constexpr (ROWS == 1) {
+        v[0] = warp_sum(v[0]);
+    } else {
+        const float2 s = warp_sums(v[0], v[1]);
+        v[0] = s.x;
+        v[1] = s.y;
+    }
+}
+
+// A row's mean and variance with one barrier: a warp's mean and its sum of squares about that,
+// then, from every warp's pair, M2 = sum_w (M2_w + n_w (mean_w - mean)^2).  Nothing is a
+// difference of large squares.
+//
+// Weight and bias stay in a thread's registers.  WIDE: in shared memory, as fp32; a thread reads its
+// groups' first and second four columns from two arrays, so that a warp's reads meet no bank
+// twice.
+template <typename T, bool VEC, int OWN, bool KEEP, int ROWS, bool WIDE>
+__global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
+    forward_block(const LayerNormForward p) {
     using O = Own<T, VEC, OWN>;
     constexpr int P = OWN / 2;
-    __shared__ float part[2][32];
-    const int D = p.cols;
+    constexpr int kSets = ROWS == 1 ? 2 : 1;       // row sets ahead
+    __shared__ float2 part[2][ROWS][32];
+    extern __shared__ __align__(16) float held[];
+    const int D = p.cols, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float inv = 1.0f / static_cast<float>(D);
     const long long pitch = act8_pitch(D);
     const O own(D);
+    // Columns of this thread's warp, and of warp `lane`.
+    float mine = 0.0f;
+#pragma unroll
+    for (int i = 0; i < O::kGroups; ++i) mine += own.c[i] < D ? static_cast<float>(O::kWidth) : 0.0f;
+    mine = warp_sum(mine);
+    if (lane == 0) part[0][0][warp].x = mine;
+    __syncthreads();
+    const bool there = lane < static_cast<int>(blockDim.x >> 5);
+    const float theirs = there ? part[0][0][lane].x : 0.0f;
+    const float my_inv = mine > 0.0f ? 1.0f / mine : 0.0f;
+    const float their_inv = theirs > 0.0f ? 1.0f / theirs : 0.0f;
+    __syncthreads();
     wait_previous();
-    BlockSum block_sum{part};
     const T* const x_at = static_cast<const T*>(p.x);
-    typename O::Row x;
-    if (blockIdx.x < p.rows) own.load(x_at + blockIdx.x * p.ldx, x);
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        Two v[P];
-        Two s = twice(0.0f);
+    // Row set i: the rows ROWS i, ...; past the last one a row is read again and not stored.
+    typename O::Row x[kSets][ROWS];
+    const long long all = (static_cast<long long>(p.rows) + ROWS - 1) / ROWS;
+    auto load = [&](typename O::Row (&to)[ROWS], long long i) {
+        if (i >= all) return;
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            v[j] = x.pair(j);
-            s = add(s, v[j]);
-        }
-        const float m = block_sum(sum(s)) * inv;
-        if constexpr (KEEP)
+        for (int k = 0; k < ROWS; ++k)
+            own.load(x_at + min(i * ROWS + k, p.rows - 1LL) * p.ldx, to[k]);
+    };
 #pragma unroll
-            for (int i = 0; i < O::kGroups; ++i)
-                if (i * blockDim.x * O::kWidth < pitch)
-                    keep_group<T>(x.raw[i], p.codes + row * pitch,
-                                  p.scales + row * (pitch / kAct8Block), own.c[i], own.c[i] < pitch);
-        if (row + gridDim.x < p.rows) own.load(x_at + (row + gridDim.x) * p.ldx, x);
-        const Two less = twice(-m);
-        s = twice(0.0f);
+    for (int k = 0; k < kSets; ++k) load(x[k], blockIdx.x + k * static_cast<long long>(gridDim.x));
+    Two w[WIDE ? 1 : P], b[WIDE ? 1 : P];
+    const int half = (D + 7) / 8 * 4;              // (WIDE: groups of eight columns)
+    if constexpr (WIDE) {
+        float* const to[2] = {held, held + 2 * half};
+        const void* const from[2] = {p.weight, p.bias};
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-            v[j] = add(v[j], less);
-            if constexpr (VEC) {
-                if (own.c[2 * j / O::kWidth] < D) s = mx4::fma(v[j], v[j], s);
-            } else {
-                const float2 f = parts(v[j]);
-                const Two in = two(own.c[2 * j] < D ? f.x : 0.0f, own.c[2 * j + 1] < D ? f.y : 0.0f);
-                s = mx4::fma(in, in, s);
+        for (int v = 0; v < 2; ++v) {
+            Two t[P];
+            if (from[v]) own.weights(from[v], p.weight_dtype, t);
+#pragma unroll
+            for (int i = 0; i < P / 4; ++i) {
+                if (own.c[i] >= D) continue;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 f = parts(t[4 * i + 2 * j]), g = parts(t[4 * i + 2 * j + 1]);
+                    const float none = v == 0 ? 1.0f : 0.0f;
+                    *reinterpret_cast<float4*>(to[v] + j * half + own.c[i] / 2) =
+                        from[v] ? make_float4(f.x, f.y, g.x, g.y) : make_float4(none, none, none, none);
+                }
             }
         }
-        const float r = rsqrtf(block_sum(sum(s)) * inv + p.eps);
-        if (threadIdx.x == 0) {
-            p.mean[row] = m;
-            p.rstd[row] = r;
-        }
-        const Two r2 = twice(r);
-        Two w[P];
+    } else {
         own.weights(p.weight, p.weight_dtype, w);
+        if (p.bias) own.weights(p.bias, p.weight_dtype, b);
+        else
 #pragma unroll
-        for (int j = 0; j < P; ++j) v[j] = mx4::mul(mx4::mul(v[j], r2), w[j]);
-        if (p.bias) {
-            own.weights(p.bias, p.weight_dtype, w);
+            for (int j = 0; j < P; ++j) b[j] = twice(0.0f);
+    }
+    int turn = 0;
+    auto set = [&](typename O::Row (&x)[ROWS], long long i) {
+        const int rows = static_cast<int>(min(static_cast<long long>(ROWS), p.rows - i * ROWS));
+        Two v[ROWS][P];
+        float s[ROWS], q[ROWS];
 #pragma unroll
-            for (int j = 0; j < P; ++j) v[j] = add(v[j], w[j]);
+        for (int k = 0; k < ROWS; ++k) {
+            Two t = twice(0.0f);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                v[k][j] = x[k].pair(j);
+                t = add(t, v[k][j]);
+            }
+            s[k] = sum(t);
+            if constexpr (KEEP) {
+                const long long row = i * ROWS + k;
+#pragma unroll
+                for (int g = 0; g < O::kGroups; ++g)
+                    if (g * blockDim.x * O::kWidth < pitch)
+                        keep_groups<T, 1>({x[k].raw[g]}, p.codes + row * pitch,
+                                      p.scales + row * (pitch / kAct8Block), own.c[g],
+                                      k < rows && own.c[g] < pitch);
+            }
         }
-        own.store(static_cast<T*>(p.y) + row * p.ldy, v);
+        load(x, i + kSets * static_cast<long long>(gridDim.x));
+        warp_sums<ROWS>(s);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const Two less = twice(-s[k] * my_inv);
+            Two t = twice(0.0f);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const Two d = add(v[k][j], less);
+                if constexpr (VEC) {
+                    if (own.c[2 * j / O::kWidth] < D) t = mx4::fma(d, d, t);
+                } else {
+                    const float2 f = parts(d);
+                    const Two in =
+                        two(own.c[2 * j] < D ? f.x : 0.0f, own.c[2 * j + 1] < D ? f.y : 0.0f);
+                    t = mx4::fma(in, in, t);
+                }
+            }
+            q[k] = sum(t);
+        }
+        warp_sums<ROWS>(q);
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) part[turn][k][warp] = make_float2(s[k], q[k]);
+        __syncthreads();
+        float m[ROWS], sw[ROWS];
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const float2 t = there ? part[turn][k][lane] : make_float2(0.0f, 0.0f);
+            m[k] = sw[k] = t.x;
+            q[k] = t.y;
+        }
+        turn ^= 1;
+        warp_sums<ROWS>(m);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            m[k] *= inv;
+            const float d = sw[k] * their_inv - m[k];
+            if (theirs > 0.0f) q[k] = fmaf(theirs * d, d, q[k]);
+        }
+        warp_sums<ROWS>(q);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const long long row = i * ROWS + k;
+            const float r = rsqrtf(fmaf(q[k], inv, p.eps));
+            if (k >= rows) break;
+            if (threadIdx.x == 0) {
+                p.mean[row] = m[k];
+                p.rstd[row] = r;
+            }
+            const Two less = twice(-m[k]), r2 = twice(r);
+            if constexpr (WIDE) {
+#pragma unroll
+                for (int g = 0; g < P / 2; ++g) {          // four columns
+                    const int at = g % 2 * half + own.c[g / 2] / 2;
+                    if (own.c[g / 2] >= D) continue;
+                    const float4 wv = *reinterpret_cast<const float4*>(held + at);
+                    const float4 bv = *reinterpret_cast<const float4*>(held + 2 * half + at);
+                    v[k][2 * g] = mx4::fma(mx4::mul(add(v[k][2 * g], less), r2), two(wv.x, wv.y),
+                                           two(bv.x, bv.y));
+                    v[k][2 * g + 1] = mx4::fma(mx4::mul(add(v[k][2 * g + 1], less), r2),
+                                               two(wv.z, wv.w), two(bv.z, bv.w));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    v[k][j] = mx4::fma(mx4::mul(add(v[k][j], less), r2), w[j], b[j]);
+            }
+            own.store(static_cast<T*>(p.y) + row * p.ldy, v[k]);
+        }
+    };
+    for (long long i = blockIdx.x; i < all; i += kSets * static_cast<long long>(gridDim.x)) {
+        set(x[0], i);
+        if (kSets == 2 && i + gridDim.x < all) set(x[kSets - 1], i + gridDim.x);
     }
     launch_next();
 }
@@ -224,10 +352,7 @@ struct KeptRow {
         if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < OWN / 4; ++i) {
-                float v[4];
-                act8::values4(codes[i], scale[4 * i / kW], v);
-                x[2 * i] = two(v[0], v[1]);
-                x[2 * i + 1] = two(v[2], v[3]);
+                act8::values4(codes[i], scale[4 * i / kW], reinterpret_cast<Two(&)[2]>(x[2 * i]));
             }
         } else {
 #pragma unroll
@@ -339,26 +464,29 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
 // ----------------------------------------------------------------------------
 template <typename T, bool KEEP>
 cudaError_t forward_rows_of(const LayerNormForward& p, const Shape& s, cudaStream_t st) {
-    const auto run = [&](auto kernel, int threads) {
-        return launch_dependent(kernel, dim3(s.grid), threads, 0, st, p);
-    };
-    if (s.kind == kByWarp) {
-        switch (s.groups) {
-            case 1: return run(forward_warp<T, 1, KEEP>, kWarpThreads);
-            case 2: return run(forward_warp<T, 2, KEEP>, kWarpThreads);
-            case 4: return run(forward_warp<T, 4, KEEP>, kWarpThreads);
-            case 8: return run(forward_warp<T, 8, KEEP>, kWarpThreads);
-            case 16: return run(forward_warp<T, 16, KEEP>, kWarpThreads);
-            default: return run(forward_warp<T, 32, KEEP>, kWarpThreads);
+    const auto run = [&](auto kernel, int threads, int smem = 0) {
+        if (smem) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
         }
-    }
-    if (s.columns == 8) return run(forward_block<T, true, 8, KEEP>, s.threads);
-    return run(forward_block<T, true, 16, KEEP>, s.threads);
+        return launch_dependent(kernel, dim3(s.grid), threads, smem, st, p);
+    };
+    if (s.kind == kByWarp)
+        return s.groups == 1 ? run(forward_warp<T, 1, KEEP>, kWarpThreads)
+                             : run(forward_warp<T, 2, KEEP>, kWarpThreads);
+    if (s.columns == 8) return run(forward_block<T, true, 8, KEEP, 1, false>, s.threads);
+    if (s.threads <= 512)
+        return run(forward_block<T, true, 16, KEEP, sizeof(T) == 4 ? 1 : 2, false>, s.threads);
+    if constexpr (sizeof(T) == 2)
+        return run(forward_block<T, true, 16, KEEP, 1, true>, s.threads, (p.cols + 7) / 8 * 64);
+    return cudaErrorInvalidConfiguration;
 }
 template <typename T>
 cudaError_t forward(const LayerNormForward& p, const Shape& s, cudaStream_t st) {
     if (s.ragged)
-        return launch_dependent(forward_block<T, false, 8, false>, dim3(s.grid), s.threads, 0, st, p);
+        return launch_dependent(forward_block<T, false, 8, false, 1, false>, dim3(s.grid), s.threads, 0,
+                                st, p);
     return p.codes ? forward_rows_of<T, true>(p, s, st) : forward_rows_of<T, false>(p, s, st);
 }
 template <typename T>

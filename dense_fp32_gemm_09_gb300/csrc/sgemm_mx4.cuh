@@ -105,6 +105,32 @@ __device__ __forceinline__ void unpack(const uint4& v, Two (&x)[4], __half) {
         x[i] = two(f.x, f.y);
     }
 }
+// Pairs to 16 bytes of a row.
+__device__ __forceinline__ uint4 pack(const Two (&x)[2], float) {
+    const float2 a = parts(x[0]), b = parts(x[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                      __float_as_uint(b.y));
+}
+__device__ __forceinline__ uint4 pack(const Two (&x)[4], __nv_bfloat16) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts(x[i]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const Two (&x)[4], __half) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts(x[i]);
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // Eight fp32 numbers to eight codes, ties to even, magnitudes above 6 to 6.
 __device__ __forceinline__ uint32_t encode8(const float (&v)[8]) {
     uint32_t r;
