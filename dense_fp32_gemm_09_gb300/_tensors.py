@@ -1,4 +1,4 @@
-"""Argument checks and allocation shared by the 4-bit and norm entry points."""
+"""Argument checks and allocation shared by the entry points around the product."""
 from __future__ import annotations
 
 import torch
@@ -113,9 +113,14 @@ def fast():
         module = importlib.util.module_from_spec(
             importlib.util.spec_from_loader("_fast_calls", loader))
         loader.exec_module(module)
-        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        at = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+        module.bind(*map(at, (
             "sgemm_mx4_quantize", "sgemm_mx4_dequantize", "sgemm_mx4_matmul",
             "sgemm_norm_forward", "sgemm_norm_backward_ws", "sgemm_norm_backward_workspace")))
+        module.bind_train(*map(at, (
+            "sgemm_act8_quantize", "sgemm_act8_dequantize", "sgemm_layer_norm_forward",
+            "sgemm_layer_norm_backward", "sgemm_layer_norm_backward_workspace",
+            "sgemm_gated_ff_forward", "sgemm_gated_ff_backward", "sgemm_gated_ff_workspace")))
         _fast = module
     return _fast
 

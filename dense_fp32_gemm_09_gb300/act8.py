@@ -41,9 +41,13 @@ class Act8:
     def _new(cls, call, rows: int, cols: int):
         """An unwritten matrix."""
         codes, scales = act8_shapes(rows, cols)
+        return cls._of(call.empty(codes, torch.int8), call.empty(scales, torch.float32), rows, cols)
+
+    @classmethod
+    def _of(cls, codes, scales, rows: int, cols: int):
+        """The matrix in buffers that fit."""
         q = cls.__new__(cls)
-        q._rows, q._cols = rows, cols
-        q._codes, q._scales = call.empty(codes, torch.int8), call.empty(scales, torch.float32)
+        q._rows, q._cols, q._codes, q._scales = rows, cols, codes, scales
         return q
 
     def _addresses(self):
@@ -100,6 +104,11 @@ def act8_quantize(x, *, stream=None) -> Act8:
     """The rows of a 2-D float32, bfloat16 or float16 CUDA view with unit column stride, in 8
     bits.  A block of 64 columns with an infinity or a NaN is NaN; one whose largest magnitude
     is below 2^-100 is zeros."""
+    if stream is None:
+        out = _t.fast().act8_quantize(x)
+        if out is not None:
+            _t.checked(out, "sgemm_act8_quantize")
+            return Act8._of(*out, *x.shape)
     call = _t.Call(_t.cuda_tensor(x, "x").device, stream)
     dt, ld = _t.dtype_code(x.dtype, "x"), _t.row_ld(x, "x")
     rows, cols = x.shape
@@ -112,6 +121,12 @@ def act8_dequantize(q: Act8, dtype=torch.float32, out=None, *, stream=None):
     """The rows x cols numbers that `q` holds, rounded once to `dtype` (or into ``out``)."""
     if not isinstance(q, Act8):
         raise TypeError("q must be an Act8")
+    if stream is None and out is None:
+        out = _t.fast().act8_dequantize(q._codes, q._scales, q._rows, q._cols,
+                                        _t.dtype_code(dtype, "dtype"))
+        if out is not None:
+            _t.checked(out, "sgemm_act8_dequantize")
+            return out
     call = _t.Call(q.device, stream)
     if out is None:
         dt, ld = _t.dtype_code(dtype, "dtype"), max(q.cols, 1)

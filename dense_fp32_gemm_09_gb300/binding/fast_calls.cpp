@@ -1,7 +1,7 @@
-// The usual form of the 4-bit and norm calls, from Python to the C ABI in one step: CUDA
+// The usual form of the calls around the product, from Python to the C ABI in one step: CUDA
 // tensors of the current device with ordinary strides on the current stream.  Each function
-// returns None for anything else, and the Python code (mx4.py, norms.py), which states the
-// checks and their messages, takes the call.  Nothing is computed here: outputs are
+// returns None for anything else, and the Python code (mx4.py, norms.py, act8.py, layer_norms.py,
+// gated.py), which states the checks and their messages, takes the call.  Nothing is computed here: outputs are
 // allocated and sgemm_* functions called.  (A call of the Python code costs 7 to 24
 // microseconds on the host where the kernels take 1 to 5.)
 #define PY_SSIZE_T_CLEAN
@@ -27,6 +27,14 @@ decltype(&sgemm_mx4_matmul) f_matmul;
 decltype(&sgemm_norm_forward) f_forward;
 decltype(&sgemm_norm_backward_ws) f_backward;
 decltype(&sgemm_norm_backward_workspace) f_backward_workspace;
+decltype(&sgemm_act8_quantize) f_act8_quantize;
+decltype(&sgemm_act8_dequantize) f_act8_dequantize;
+decltype(&sgemm_layer_norm_forward) f_layer_norm;
+decltype(&sgemm_layer_norm_backward) f_layer_norm_backward;
+decltype(&sgemm_layer_norm_backward_workspace) f_layer_norm_workspace;
+decltype(&sgemm_gated_ff_forward) f_gated_ff;
+decltype(&sgemm_gated_ff_backward) f_gated_ff_backward;
+decltype(&sgemm_gated_ff_workspace) f_gated_ff_workspace;
 
 template <typename F>
 PyObject* guarded(F f) {
@@ -348,27 +356,270 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// bind(addresses of the six C functions, in this order)
-PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
+// ----------------------------------------------------------------------------
+// 8-bit checkpoints, layer norm, the gated feed-forward block
+// ----------------------------------------------------------------------------
+long long act8_blocks(long long cols) { return (cols + 63) / 64; }
+// An unwritten checkpoint's buffers.
+struct Kept {
+    at::Tensor codes, scales;
+    static Kept make(long long rows, long long cols) {
+        return {empty({rows, 64 * act8_blocks(cols)}, at::kChar),
+                empty({rows, act8_blocks(cols)}, at::kFloat)};
+    }
+    // Whether these hold a rows x cols matrix.
+    bool holds(long long rows, long long cols) const {
+        return codes.defined() && scales.defined() && codes.scalar_type() == at::kChar &&
+               scales.scalar_type() == at::kFloat && codes.dim() == 2 && scales.dim() == 2 &&
+               codes.size(0) == rows && scales.size(0) == rows &&
+               codes.size(1) == 64 * act8_blocks(cols) && scales.size(1) == act8_blocks(cols) &&
+               codes.is_contiguous() && scales.is_contiguous() && here(codes) && here(scales);
+    }
+};
+float* floats(const at::Tensor& t) { return static_cast<float*>(ptr(t)); }
+// Shape, type and leading dimension of a matrix that a call goes by; false if it is not usual.
+bool leading(const at::Tensor& t, Shape* s, int* dt, int* ld) {
+    if (!t.defined() || t.dim() != 2) return false;
+    *s = Shape{t.size(0), t.size(1), t.scalar_type()};
+    *dt = dtype_code(t);
+    if (*dt < 0 || s->cols < 1 || s->cols > INT_MAX) return false;
+    *ld = matrix(t, *s);
+    return *ld >= 0;
+}
+
+// act8_quantize(x) -> (codes, scales)
+PyObject* act8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        at::Tensor x;
+        Shape s;
+        int dt, ld;
+        if (n != 1 || !tensor(a[0], &x) || !leading(x, &s, &dt, &ld)) return not_here();
+        const Kept q = Kept::make(s.rows, s.cols);
+        const int st = unlocked(f_act8_quantize, s.rows, s.cols, dt, x.data_ptr(), ld, ptr(q.codes),
+                                floats(q.scales), stream());
+        return st ? status(st) : tuple({q.codes, q.scales});
+    });
+}
+
+// act8_dequantize(codes, scales, rows, cols, dtype code) -> tensor
+PyObject* act8_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        Kept q;
+        if (n != 5 || !tensor(a[0], &q.codes) || !tensor(a[1], &q.scales)) return not_here();
+        const long rows = PyLong_AsLong(a[2]), cols = PyLong_AsLong(a[3]);
+        const int dt = static_cast<int>(PyLong_AsLong(a[4]));
+        if (PyErr_Occurred()) return nullptr;
+        if (!q.holds(rows, cols)) return not_here();
+        at::Tensor y = empty({rows, cols}, dtype_of(dt));
+        const int st = unlocked(f_act8_dequantize, rows, cols, ptr(q.codes), floats(q.scales), dt,
+                                y.data_ptr(), std::max(cols, 1L), stream());
+        return st ? status(st) : wrap(y);
+    });
+}
+
+// layer_norm(x, weight, bias, eps, keep) -> (y, mean, rstd, codes, scales)
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        at::Tensor x, weight, bias;
+        Shape s;
+        int dt, ld;
+        if (n != 5 || !tensor(a[0], &x) || !tensor(a[1], &weight) || !tensor(a[2], &bias) ||
+            !leading(x, &s, &dt, &ld))
+            return not_here();
+        const float eps = static_cast<float>(PyFloat_AsDouble(a[3]));
+        const int keep = PyObject_IsTrue(a[4]);
+        if (PyErr_Occurred()) return nullptr;
+        const int wt = weights(weight, bias, s);
+        if (wt < 0) return not_here();
+        at::Tensor y = empty({s.rows, s.cols}, s.type), mean = empty({s.rows}, at::kFloat),
+                   rstd = empty({s.rows}, at::kFloat);
+        Kept q;
+        if (keep) q = Kept::make(s.rows, s.cols);
+        const int st = unlocked(f_layer_norm, s.rows, s.cols, dt, x.data_ptr(), ld, ptr(weight),
+                                ptr(bias), wt, eps, y.data_ptr(), s.cols, floats(mean), floats(rstd),
+                                ptr(q.codes), floats(q.scales), stream());
+        return st ? status(st) : tuple({y, mean, rstd, q.codes, q.scales});
+    });
+}
+
+// layer_norm_backward(dh, x, codes, scales, mean, rstd, weight, dy) -> (dx, dweight, dbias)
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        at::Tensor dh, x, mean, rstd, weight, dy;
+        Kept q;
+        at::Tensor* to[] = {&dh, &x, &q.codes, &q.scales, &mean, &rstd, &weight, &dy};
+        if (n != 8) return not_here();
+        for (int i = 0; i < 8; ++i)
+            if (!tensor(a[i], to[i])) return not_here();
+        Shape s;
+        int dt, lddh;
+        if (!leading(dh, &s, &dt, &lddh)) return not_here();
+        const int ldx = matrix(x, s), lddy = matrix(dy, s), wt = weights(weight, at::Tensor(), s);
+        if (ldx < 0 || lddy < 0 || wt < 0 || x.defined() == q.codes.defined() || !mean.defined() ||
+            !rstd.defined() || !vector(mean, s.rows, at::kFloat) ||
+            !vector(rstd, s.rows, at::kFloat) || (!x.defined() && !q.holds(s.rows, s.cols)))
+            return not_here();
+        at::Tensor dx = empty({s.rows, s.cols}, s.type), dweight, dbias = empty({s.cols}, at::kFloat);
+        if (weight.defined()) dweight = empty({s.cols}, at::kFloat);
+        // From torch's allocator, so that a captured graph owns what it uses.
+        size_t ws_bytes = 0;
+        if (const int st = f_layer_norm_workspace(s.rows, s.cols, &ws_bytes)) return status(st);
+        at::Tensor ws = empty({static_cast<int64_t>(ws_bytes)}, at::kByte);
+        const int st = unlocked(f_layer_norm_backward, s.rows, s.cols, dt, dh.data_ptr(), lddh, ptr(dy),
+                                lddy, ptr(x), x.defined() ? ldx : static_cast<int>(s.cols),
+                                ptr(q.codes), floats(q.scales), floats(mean), floats(rstd),
+                                ptr(weight), wt, dx.data_ptr(), s.cols, floats(dweight),
+                                floats(dbias), ws.data_ptr(), ws_bytes, stream());
+        return st ? status(st) : tuple({dx, dweight, dbias});
+    });
+}
+
+// Whether a block reads a copy of these rows (include/sgemm.h).
+int packed(int bit, const at::Tensor& t, int ld) {
+    return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 && (t.size(0) <= 1 || ld % 8 == 0) ? 0
+                                                                                                  : bit;
+}
+// The two weights of a block whose tokens are of type `type`.
+struct Layer {
+    long long N = 0, K = 0;
+    int ldg = -1, ldu = -1;
+    bool usual(const at::Tensor& wg, const at::Tensor& wu, at::ScalarType type) {
+        if (!wg.defined() || !wu.defined() || wg.dim() != 2) return false;
+        N = wg.size(0);
+        K = wg.size(1);
+        if (N < 1 || K < 1 || K > INT_MAX) return false;
+        const Shape s{N, K, type};
+        ldg = matrix(wg, s);
+        ldu = matrix(wu, s);
+        return ldg >= 0 && ldu >= 0;
+    }
+};
+at::Tensor workspace(size_t bytes) {
+    return bytes ? empty({static_cast<int64_t>(bytes)}, at::kByte) : at::Tensor();
+}
+
+// gated_ff(x, w_gate, w_up, activation, keep) -> (h, gate, up, gate_scales, up_scales)
+PyObject* gated_ff(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        at::Tensor x, wg, wu;
+        Shape s;
+        int dt, ldx;
+        Layer w;
+        if (n != 5 || !tensor(a[0], &x) || !tensor(a[1], &wg) || !tensor(a[2], &wu) ||
+            !leading(x, &s, &dt, &ldx) || dt == SGEMM_F32 || !w.usual(wg, wu, s.type) || w.K != s.cols)
+            return not_here();
+        const int act = static_cast<int>(PyLong_AsLong(a[3]));
+        const int keep = static_cast<int>(PyLong_AsLong(a[4]));
+        if (PyErr_Occurred()) return nullptr;
+        const long long M = s.rows;
+        at::Tensor h = empty({M, w.N}, s.type);
+        Kept gate, up;
+        const long long ldk = keep == SGEMM_KEEP_FULL ? (w.N + 7) / 8 * 8 : w.N;
+        if (keep == SGEMM_KEEP_FULL) {
+            for (at::Tensor* t : {&gate.codes, &up.codes}) {
+                *t = empty({M, ldk}, s.type);
+                if (ldk != w.N) *t = t->narrow(1, 0, w.N);
+            }
+        } else if (keep == SGEMM_KEEP_8BIT) {
+            gate = Kept::make(M, w.N);
+            up = Kept::make(M, w.N);
+        }
+        size_t bytes = 0;
+        const int pack = packed(1, x, ldx) | packed(2, wg, w.ldg) | packed(4, wu, w.ldu);
+        if (pack)
+            if (const int st = f_gated_ff_workspace(M, w.N, w.K, 0, pack, &bytes)) return status(st);
+        const at::Tensor ws = workspace(bytes);
+        const int st = unlocked(f_gated_ff, M, w.N, w.K, dt, act, x.data_ptr(), ldx, wg.data_ptr(),
+                                w.ldg, wu.data_ptr(), w.ldu, h.data_ptr(), w.N, keep, ptr(gate.codes),
+                                ptr(up.codes), ldk, floats(gate.scales), floats(up.scales), ptr(ws),
+                                bytes, stream());
+        return st ? status(st) : tuple({h, gate.codes, up.codes, gate.scales, up.scales});
+    });
+}
+
+// gated_ff_backward(dh, x, x_codes, x_scales, w_gate, w_up, gate, up, gate_scales, up_scales,
+// activation, return_h) -> (dx, dw_gate, dw_up, h)
+PyObject* gated_ff_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject* {
+        at::Tensor dh, x, wg, wu;
+        Kept kx, gate, up;
+        at::Tensor* to[] = {&dh, &x, &kx.codes, &kx.scales, &wg, &wu,
+                            &gate.codes, &up.codes, &gate.scales, &up.scales};
+        if (n != 12) return not_here();
+        for (int i = 0; i < 10; ++i)
+            if (!tensor(a[i], to[i])) return not_here();
+        const int act = static_cast<int>(PyLong_AsLong(a[10])), again = PyObject_IsTrue(a[11]);
+        if (PyErr_Occurred()) return nullptr;
+        Shape s;
+        int dt, lddh;
+        Layer w;
+        if (!leading(dh, &s, &dt, &lddh) || dt == SGEMM_F32 || !w.usual(wg, wu, s.type) || w.N != s.cols)
+            return not_here();
+        const long long M = s.rows;
+        const int ldx = matrix(x, Shape{M, w.K, s.type});
+        if (ldx < 0 || x.defined() == kx.codes.defined() || (!x.defined() && !kx.holds(M, w.K)) ||
+            !gate.codes.defined() || !up.codes.defined())
+            return not_here();
+        int keep = SGEMM_KEEP_8BIT, ldk = static_cast<int>(w.N);
+        if (!gate.scales.defined() && !up.scales.defined()) {
+            keep = SGEMM_KEEP_FULL;
+            ldk = matrix(gate.codes, s);
+            if (ldk < 0 || matrix(up.codes, s) != ldk) return not_here();
+        } else if (!gate.holds(M, w.N) || !up.holds(M, w.N)) {
+            return not_here();
+        }
+        at::Tensor dx = empty({M, w.K}, s.type), dwg = empty({w.N, w.K}, s.type),
+                   dwu = empty({w.N, w.K}, s.type), h;
+        if (again) h = empty({M, w.N}, s.type);
+        const int pack = (x.defined() ? packed(1, x, ldx) : 1) | packed(2, wg, w.ldg) |
+                         packed(4, wu, w.ldu);
+        size_t bytes = 0;
+        if (const int st = f_gated_ff_workspace(M, w.N, w.K, 1, pack, &bytes)) return status(st);
+        const at::Tensor ws = workspace(bytes);
+        const int st = unlocked(
+            f_gated_ff_backward, M, w.N, w.K, dt, act, dh.data_ptr(), lddh, ptr(x),
+            x.defined() ? ldx : static_cast<int>(w.K), ptr(kx.codes), floats(kx.scales), wg.data_ptr(),
+            w.ldg, wu.data_ptr(), w.ldu, keep, ptr(gate.codes), ptr(up.codes), ldk,
+            floats(gate.scales), floats(up.scales), dx.data_ptr(), w.K, dwg.data_ptr(), w.K,
+            dwu.data_ptr(), w.K, ptr(h), w.N, ptr(ws), bytes, stream());
+        return st ? status(st) : tuple({dx, dwg, dwu, h});
+    });
+}
+
+// The C functions' addresses, in the order given.
+template <size_t COUNT>
+PyObject* take(PyObject* const* a, Py_ssize_t n, const char* name, void** const (&to)[COUNT]) {
+    if (n != static_cast<Py_ssize_t>(COUNT)) {
+        PyErr_Format(PyExc_TypeError, "%s takes %zu addresses", name, COUNT);
         return nullptr;
     }
-    void* p[6];
-    for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+    void* p[COUNT];
+    for (size_t i = 0; i < COUNT; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
-    f_quantize = reinterpret_cast<decltype(f_quantize)>(p[0]);
-    f_dequantize = reinterpret_cast<decltype(f_dequantize)>(p[1]);
-    f_matmul = reinterpret_cast<decltype(f_matmul)>(p[2]);
-    f_forward = reinterpret_cast<decltype(f_forward)>(p[3]);
-    f_backward = reinterpret_cast<decltype(f_backward)>(p[4]);
-    f_backward_workspace = reinterpret_cast<decltype(f_backward_workspace)>(p[5]);
+    for (size_t i = 0; i < COUNT; ++i) *to[i] = p[i];
     Py_RETURN_NONE;
+}
+template <typename F>
+void** slot(F& f) { return reinterpret_cast<void**>(&f); }
+// bind(those of the 4-bit operands and the norms)
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    void** const to[] = {slot(f_quantize), slot(f_dequantize), slot(f_matmul),
+                         slot(f_forward), slot(f_backward), slot(f_backward_workspace)};
+    return take(a, n, "bind", to);
+}
+// bind_train(those of the checkpoints, layer norm and the feed-forward block)
+PyObject* bind_train(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    void** const to[] = {slot(f_act8_quantize), slot(f_act8_dequantize), slot(f_layer_norm),
+                         slot(f_layer_norm_backward), slot(f_layer_norm_workspace),
+                         slot(f_gated_ff), slot(f_gated_ff_backward), slot(f_gated_ff_workspace)};
+    return take(a, n, "bind_train", to);
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
-PyMethodDef kMethods[] = {METHOD(bind), METHOD(mx4_holds), METHOD(mx4_quantize), METHOD(mx4_dequantize),
+PyMethodDef kMethods[] = {METHOD(bind), METHOD(bind_train), METHOD(mx4_holds), METHOD(mx4_quantize), METHOD(mx4_dequantize),
                           METHOD(mx4_matmul), METHOD(norm_forward), METHOD(norm_backward),
+                          METHOD(act8_quantize), METHOD(act8_dequantize), METHOD(layer_norm),
+                          METHOD(layer_norm_backward), METHOD(gated_ff), METHOD(gated_ff_backward),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fast_calls", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -72,6 +72,14 @@ def gated_ff(x, w_gate, w_up, *, activation: str = "silu", keep: str | None = No
     act = _activation(activation)
     if keep not in KEEP:
         raise ValueError(f"keep must be None, 'full' or '8bit', got {keep!r}")
+    if stream is None:
+        out = _t.fast().gated_ff(x, w_gate, w_up, act, KEEP[keep])
+        if out is not None:
+            _t.checked(out, "sgemm_gated_ff_forward")
+            h, gate, up, gs, us = out
+            if keep == "8bit":
+                gate, up = Act8._of(gate, gs, *h.shape), Act8._of(up, us, *h.shape)
+            return h if keep is None else (h, (gate, up))
     call = _t.Call(_t.cuda_tensor(x, "x").device, stream)
     dt, ldx = _dtype(x, "x"), _t.row_ld(x, "x")
     M = x.shape[0]
@@ -101,6 +109,24 @@ def gated_ff_backward(dh, x, w_gate, w_up, kept, *, activation: str = "silu",
     also h, made again from what was kept: (dx, dw_gate, dw_up, h).  Gradients are of dh's type;
     the gradients of the pre-activations, which the products multiply, are rounded to it too."""
     act = _activation(activation)
+    if not isinstance(kept, (tuple, list)) or len(kept) != 2:
+        raise TypeError("kept must be the (gate, up) that gated_ff(..., keep=...) returned")
+    gate, up = kept
+    in8 = isinstance(gate, Act8)
+    if in8 != isinstance(up, Act8):
+        raise TypeError("gate and up must be kept in one form")
+    if stream is None:
+        held_x = (None, x._codes, x._scales) if isinstance(x, Act8) else (x, None, None)
+        held_k = (gate._codes, up._codes, gate._scales, up._scales) if in8 else \
+            (gate, up, None, None)
+        fits = not in8 or gate.shape == up.shape == getattr(dh, "shape", None)
+        if held_x[0] is not x:             # (the library's rows are padded: it sees no width)
+            fits = fits and x.shape[1:] == getattr(w_gate, "shape", ())[1:]
+        out = _t.fast().gated_ff_backward(dh, *held_x, w_gate, w_up, *held_k, act, return_h) \
+            if fits else None
+        if out is not None:
+            _t.checked(out, "sgemm_gated_ff_backward")
+            return out if return_h else out[:3]
     call = _t.Call(_t.cuda_tensor(dh, "dh").device, stream)
     dt, lddh = _dtype(dh, "dh"), _t.row_ld(dh, "dh")
     N, K, ldg, ldu = _layer(dh, "dh", w_gate, w_up)
@@ -117,16 +143,11 @@ def gated_ff_backward(dh, x, w_gate, w_up, kept, *, activation: str = "silu",
         ldx = _t.matrix(x, "x", (M, K), dh.dtype, dh.device)
         x_at = x.data_ptr()
         packed |= _packed(_X, x, ldx)
-    if not isinstance(kept, (tuple, list)) or len(kept) != 2:
-        raise TypeError("kept must be the (gate, up) that gated_ff(..., keep=...) returned")
-    gate, up = kept
     ldk, gs, us = N, None, None
-    if isinstance(gate, Act8) and isinstance(up, Act8):
+    if in8:
         form = KEEP["8bit"]
         (g_at, gs), (u_at, us) = (held(q, n, (M, N), dh.device) for q, n in
                                   ((gate, "gate"), (up, "up")))
-    elif isinstance(gate, Act8) or isinstance(up, Act8):
-        raise TypeError("gate and up must be kept in one form")
     else:
         form = KEEP["full"]
         ldk = _t.matrix(gate, "gate", (M, N), dh.dtype, dh.device)

@@ -25,6 +25,11 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, keep: str | None
     (y, mean, rstd, kept)."""
     if keep not in (None, "8bit"):
         raise ValueError(f"keep must be None or '8bit', got {keep!r}")
+    if stream is None:
+        out = _t.fast().layer_norm(x, weight, bias, eps, keep is not None)
+        if out is not None:
+            _t.checked(out, "sgemm_layer_norm_forward")
+            return out[:3] if keep is None else (*out[:3], Act8._of(*out[3:], *x.shape))
     call = _t.Call(_t.cuda_tensor(x, "x").device, stream)
     rows, cols, dt, ld = _norms._rows(x, "x")
     wt = _norms._weights(cols, x, ("weight", weight), ("bias", bias))
@@ -43,6 +48,13 @@ def layer_norm_backward(dh, x, mean, rstd, weight=None, *, dy=None, stream=None)
     the norm's input or an ``Act8`` of it; ``dy``, the gradient that reaches x past the norm, is
     added to dx in the same pass.  dweight (None without a weight) and dbias are float32 sums
     over the rows, in a fixed order."""
+    if stream is None:
+        held_x = (None, x._codes, x._scales) if isinstance(x, Act8) else (x, None, None)
+        fits = held_x[0] is x or x.shape == getattr(dh, "shape", None)
+        out = _t.fast().layer_norm_backward(dh, *held_x, mean, rstd, weight, dy) if fits else None
+        if out is not None:
+            _t.checked(out, "sgemm_layer_norm_backward")
+            return out
     call = _t.Call(_t.cuda_tensor(dh, "dh").device, stream)
     rows, cols, dt, lddh = _norms._rows(dh, "dh")
     codes = scales = x_at = None

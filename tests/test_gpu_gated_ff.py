@@ -361,3 +361,8 @@ def test_refusals(sg):
                  (dh, x, wg, wu, (kept[0], kept[1].clone(memory_format=torch.contiguous_format)[:7]))):
         with pytest.raises((TypeError, ValueError)):
             sg.gated_ff_backward(*args)
+    # Checkpoints of another width whose padded rows are the same.
+    wide = sg.act8_quantize(torch.zeros(8, 41, device="cuda"))
+    for args in ((dh, wide, wg, wu, kept), (dh, x, wg, wu, (wide, wide))):
+        with pytest.raises(ValueError):
+            sg.gated_ff_backward(*args)

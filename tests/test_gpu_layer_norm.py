@@ -273,7 +273,7 @@ def test_refusals(sg):
     q = sg.act8_quantize(x)
     for args in ((x, x[:7], mean, rstd, w), (x, x.bfloat16(), mean, rstd, w), (x, x, mean[:7], rstd, w),
                  (x, x, mean, rstd.double(), w), (x, x, mean, rstd, w[:5]), (x.t(), x, mean, rstd, w),
-                 (x[:7], q, mean[:7], rstd[:7], w), (x, x, mean.cpu(), rstd, w), (x, None, mean, rstd, w)):
+                 (x[:7], q, mean[:7], rstd[:7], w), (x, sg.act8_quantize(x[:, :63]), mean, rstd, w), (x, x, mean.cpu(), rstd, w), (x, None, mean, rstd, w)):
         with pytest.raises((TypeError, ValueError)):
             sg.layer_norm_backward(*args)
     with pytest.raises(ValueError):
