@@ -35,6 +35,8 @@ cudaError_t pair_bf16(const PairMaps& maps, const PairPlan& pl, int mode, int bn
                       int sms, cudaStream_t stream);
 cudaError_t pair_f16(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int activation,
                      int sms, cudaStream_t stream);
+// Forward of up to 16 tokens, without 8-bit checkpoints (sgemm_ff_token.cu); operands on 16 bytes, on32: on 32.
+cudaError_t launch_token(const GatedFfForward& p, bool on32, int sms, cudaStream_t stream);
 
 }  // namespace ff
 }  // namespace sgemm

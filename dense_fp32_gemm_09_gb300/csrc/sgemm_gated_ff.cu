@@ -168,6 +168,7 @@ long long up_to(long long n, int m) { return (n + m - 1) / m; }
 struct Choice {
     int bn, split;
 };
+constexpr int kTokens = 16;          // up to here sgemm_ff_token.cu
 constexpr int kPairsOfGpu = 76;      // 152 SMs
 // Clocks of a stage: four MMAs of 128 for 256 columns; narrower ones wait for shared memory.
 int stage_clocks(int bn) { return bn == 256 ? 512 : bn == 128 ? 320 : 224; }
@@ -224,9 +225,10 @@ bool encode(CUtensorMap* tm, const void* base, long long rows, long long cols, l
               steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool on16(const void* p, long long rows, long long ld, int elem = 2) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld * elem % 16 == 0);
+bool rows_on(int bytes, const void* p, long long rows, long long ld) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (rows <= 1 || ld * 2 % bytes == 0);
 }
+bool on16(const void* p, long long rows, long long ld) { return rows_on(16, p, rows, ld); }
 
 // What of a call's operands is copied into the workspace first, and where.
 struct Operands {
@@ -277,6 +279,18 @@ cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* laun
     const Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, p.ws);
     cudaError_t e = in.copy(sms, st, launches);
     if (e != cudaSuccess) return e;
+    if (p.M <= kTokens && p.kept.keep != kKeep8) {
+        GatedFfForward q = p;
+        q.x = in.x;
+        q.w_gate = in.w_gate;
+        q.w_up = in.w_up;
+        q.ldx = in.ldx;
+        q.ldg = in.ldg;
+        q.ldu = in.ldu;
+        ++*launches;
+        return launch_token(q, rows_on(32, in.x, p.M, in.ldx) && rows_on(32, in.w_gate, p.N, in.ldg) &&
+                                   rows_on(32, in.w_up, p.N, in.ldu), sms, st);
+    }
     const Choice c = choose_forward(p.M, p.N, p.K, p.kept.keep);
     PairMaps maps;
     if (!encode(&maps.a[0], in.x, p.M, p.K, in.ldx, 128) ||

@@ -75,12 +75,14 @@ def check_forward(sg, c, name, **views):
     h = sg.gated_ff(x, wg, wu, activation=name)
     near(h, want, tol, "h")
     h1, (gate, up) = sg.gated_ff(x, wg, wu, activation=name, keep="full")
-    assert torch.equal(h1, h) or c.M <= 16
+    assert torch.equal(h1, h)
     near(h1, want, tol, "h beside what is kept")
     near(gate, g, eg + c.u * 1.01 * (g.abs() + eg) + c.t, "gate")
     near(up, u, eu + c.u * 1.01 * (u.abs() + eu) + c.t, "up")
     h2, kept = sg.gated_ff(x, wg, wu, activation=name, keep="8bit")
-    assert torch.equal(h2, h1)
+    # (Up to 16 tokens, checkpoints in 8 bits take another kernel, which sums in another order.)
+    assert torch.equal(h2, h1) or c.M <= 16
+    near(h2, want, tol, "h beside what is kept in 8 bits")
     for q, v, ev in zip(kept, (g, u), (eg, eu)):
         # Half a step of the block's largest magnitude, and the fp32 roundings of the definition.
         top = torch.nn.functional.pad(v.abs() + ev, (0, -c.N % 64)).view(c.M, -1, 64).amax(2)
