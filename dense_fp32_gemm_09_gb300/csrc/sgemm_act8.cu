@@ -43,26 +43,6 @@ __device__ __forceinline__ void store_pair(void* p, bool on32, const uint4 (&v)[
     }
 }
 
-// Walks the groups `i`, `i + step`, ... of rows of `groups` without a division a step.
-struct Walk {
-    long long row;
-    int col, drow, dcol, groups;
-    __device__ __forceinline__ Walk(long long i, long long step, int n) : groups(n) {
-        row = i / n;
-        col = static_cast<int>(i - row * n);
-        drow = static_cast<int>(step / n);
-        dcol = static_cast<int>(step - static_cast<long long>(drow) * n);
-    }
-    __device__ __forceinline__ void next() {
-        row += drow;
-        col += dcol;
-        if (col >= groups) {
-            col -= groups;
-            ++row;
-        }
-    }
-};
-
 // A thread takes 32 bytes of a row, kAhead such pieces in flight.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantize q, const bool on32) {
@@ -71,7 +51,7 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantiz
     const long long step = static_cast<long long>(gridDim.x) * kThreads;
     Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x, step,
             static_cast<int>(pitch / COLS));
-    wait_previous();
+    start_dependent();
     // Whole warps: a block's lanes are in one row, and all there.
     long long first = __shfl_sync(0xFFFFFFFFu, at.row, 0);
     while (first < q.rows) {
@@ -96,7 +76,6 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantiz
                               q.scales + row[i] * (pitch / kAct8Block), col[i], row[i] < q.rows);
         first = __shfl_sync(0xFFFFFFFFu, at.row, 0);
     }
-    launch_next();
 }
 
 // A warp takes 256 columns of a row, lane l the columns l, l + 32, ...
@@ -107,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quant
     const long long step = static_cast<long long>(gridDim.x) * (kThreads / 32);
     Walk at(blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32, step,
             static_cast<int>((pitch + 255) / 256));
-    wait_previous();
+    start_dependent();
     for (; at.row < q.rows; at.next()) {
         const T* x = static_cast<const T*>(q.X) + at.row * q.ldx;
         int8_t* codes = q.codes + at.row * pitch;
@@ -126,7 +105,6 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quant
             if (lane == 0) q.scales[(at.row * pitch + c) / kAct8Block] = s.scale;
         }
     }
-    launch_next();
 }
 
 template <typename T>
@@ -137,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequa
     const long long step = static_cast<long long>(gridDim.x) * kThreads;
     Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x, step,
             (q.cols + COLS - 1) / COLS);
-    wait_previous();
+    start_dependent();
     while (at.row < q.rows) {
         uint32_t codes[kAhead][COLS / 4];
         float scale[kAhead];
@@ -182,7 +160,6 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequa
             else *reinterpret_cast<uint4*>(to[i]) = out[0];
         }
     }
-    launch_next();
 }
 
 template <typename T>
@@ -192,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_ragged(const Act8Deq
     const long long step = static_cast<long long>(gridDim.x) * (kThreads / 32);
     Walk at(blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32, step,
             static_cast<int>((pitch + 255) / 256));
-    wait_previous();
+    start_dependent();
     for (; at.row < q.rows; at.next()) {
         T* y = static_cast<T*>(q.Y) + at.row * q.ldy;
         const int8_t* codes = q.codes + at.row * pitch;
@@ -208,7 +185,6 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_ragged(const Act8Deq
         for (int i = 0; i < 8; ++i)
             if (c0 + 32 * i < q.cols) y[c0 + 32 * i] = from_float<T>(v[i]);
     }
-    launch_next();
 }
 
 // Whether rows are whole, aligned 16-byte groups.

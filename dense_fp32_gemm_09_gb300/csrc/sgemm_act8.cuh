@@ -101,6 +101,26 @@ __device__ __forceinline__ float value(int8_t code, float scale) {
     return static_cast<float>(code) * scale;
 }
 
+// Walks the groups `i`, `i + step`, ... of rows of `groups` without a division a step.
+struct Walk {
+    long long row;
+    int col, drow, dcol, groups;
+    __device__ __forceinline__ Walk(long long i, long long step, int n) : groups(n) {
+        row = i / n;
+        col = static_cast<int>(i - row * n);
+        drow = static_cast<int>(step / n);
+        dcol = static_cast<int>(step - static_cast<long long>(drow) * n);
+    }
+    __device__ __forceinline__ void next() {
+        row += drow;
+        col += dcol;
+        if (col >= groups) {
+            col -= groups;
+            ++row;
+        }
+    }
+};
+
 // 16 bytes that are read once: not into the L1 cache.
 __device__ __forceinline__ uint4 load_once(const void* p) {
     uint4 v;

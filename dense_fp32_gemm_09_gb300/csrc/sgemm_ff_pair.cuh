@@ -18,10 +18,10 @@
 // Persistent: pair i takes the work items i, i + pairs, ...
 //   warp 0: copies of the CTA's own halves; both CTAs' complete on the first one's barrier;
 //   warp 1 of the first CTA: the MMAs of both CTAs, four a stage;
-//   warps 2..5 and 6..9: the epilogues of even and odd items.  Tensor memory holds two sets of
-//     sums, so that one item's epilogue runs under the next one's MMAs.  A warp has 32 tokens,
-//     one a lane, and passes 64 columns at a time through its own 4 KB of shared memory, to
-//     store whole 128-byte lines.
+//   warps 2..5 and 6..9: the epilogue, 128 rows x each half of the columns.  Tensor memory holds
+//     two sets of sums, so that one item's epilogue runs under the next one's MMAs.  A warp has
+//     32 rows, one a lane, and passes up to 64 columns at a time through its own 4 KB of shared
+//     memory, to store whole 128-byte lines.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -159,12 +159,12 @@ __device__ __forceinline__ Item item_at(const PairPlan& pl, int i) {
 }
 
 // A warp's 32 rows of CHUNKS 16-byte chunks: staged one row a lane, stored in whole lines.
-// Chunk c of row r lies at chunk c ^ (r mod 8) (mod 4 with four chunks, two rows a line), so that
-// neither side meets a bank twice.
+// The chunks of the rows that share a 128-byte line are permuted, so that neither side meets a
+// bank twice.
 template <int CHUNKS>
 __device__ __forceinline__ uint32_t staged_at(int row, int chunk) {
-    return CHUNKS == 8 ? row * 128 + ((chunk ^ (row & 7)) << 4)
-                       : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+    constexpr int kPerLine = 8 / CHUNKS;
+    return row * (16 * CHUNKS) + ((chunk ^ (row / kPerLine & (CHUNKS - 1))) << 4);
 }
 __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
@@ -188,36 +188,45 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Staged rows to `to`, rows `ld` elements of E bytes apart, of which `rows` and `cols` are inside
-// the result.  vec: rows start on 16 bytes.
-template <int CHUNKS, int E>
+__device__ __forceinline__ uint32_t ld_shared_word(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+// Staged rows to `to`, `ld` bytes apart, of which `rows` rows and `bytes` bytes each are inside the
+// result.  vec: rows start on 16 bytes; otherwise a warp stores a row at a time, two 2-byte
+// numbers a lane.
+template <int CHUNKS>
 __device__ __forceinline__ void store_staged(uint32_t staged, uint8_t* to, long long ld, int rows,
-                                             int cols, bool vec, int lane) {
+                                             int bytes, bool vec, int lane) {
     constexpr int kPer = 32 / CHUNKS;              // rows a step
-    const int chunk = lane % CHUNKS, c = chunk * (16 / E);
     __syncwarp();
+    if (vec && bytes >= 16 * CHUNKS) {
+        const int chunk = lane % CHUNKS;
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += kPer) {
-        const int r = r0 + lane / CHUNKS;
-        if (r >= rows || c >= cols) continue;
-        const uint4 v = ld_shared(staged + staged_at<CHUNKS>(r, chunk));
-        uint8_t* at = to + (r * ld + c) * E;
-        if (vec && c + 16 / E <= cols) {
-            *reinterpret_cast<uint4*>(at) = v;
-        } else {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 16 / E; ++i)
-                if (c + i < cols) {
-                    if (E == 4) reinterpret_cast<uint32_t*>(at)[i] = w[i];
-                    else reinterpret_cast<uint16_t*>(at)[i] =
-                             static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
-                }
+        for (int r0 = 0; r0 < 32; r0 += kPer) {
+            const int r = r0 + lane / CHUNKS;
+            if (r >= rows) break;
+            *reinterpret_cast<uint4*>(to + r * ld + 16 * chunk) =
+                ld_shared(staged + staged_at<CHUNKS>(r, chunk));
+        }
+    } else if (lane < 4 * CHUNKS && 4 * lane < bytes) {
+        const bool both = 4 * lane + 4 <= bytes;
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+            const uint32_t v = ld_shared_word(staged + staged_at<CHUNKS>(r, lane >> 2) + (lane & 3) * 4);
+            uint8_t* const at = to + r * ld + 4 * lane;
+            if (both && (reinterpret_cast<uintptr_t>(at) & 3) == 0) {
+                *reinterpret_cast<uint32_t*>(at) = v;
+            } else {
+                *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(v);
+                if (both) reinterpret_cast<uint16_t*>(at)[1] = static_cast<uint16_t>(v >> 16);
+            }
         }
     }
     __syncwarp();
 }
-// 64 numbers a lane as 2-byte rows.
+// COLS numbers a lane as 2-byte rows.
 template <typename T, int COLS>
 __device__ __forceinline__ void put_rows(uint32_t staged, const float (&v)[COLS], uint8_t* to,
                                          long long ld, int rows, int cols, bool vec, int lane) {
@@ -226,7 +235,7 @@ __device__ __forceinline__ void put_rows(uint32_t staged, const float (&v)[COLS]
         st_shared(staged + staged_at<COLS / 8>(lane, i / 8),
                   make_uint4(pack2<T>(v[i], v[i + 1]), pack2<T>(v[i + 2], v[i + 3]),
                              pack2<T>(v[i + 4], v[i + 5]), pack2<T>(v[i + 6], v[i + 7])));
-    store_staged<COLS / 8, 2>(staged, to, ld, rows, cols, vec, lane);
+    store_staged<COLS / 8>(staged, to, 2 * ld, rows, 2 * min(cols, COLS), vec, lane);
 }
 // 64 numbers a lane, one block of an 8-bit checkpoint (columns past the end are zeros).
 __device__ __forceinline__ void put_codes(uint32_t staged, const float (&v)[64], int8_t* codes,
@@ -244,17 +253,17 @@ __device__ __forceinline__ void put_codes(uint32_t staged, const float (&v)[64],
                              s.codes4(v[i + 4], v[i + 5], v[i + 6], v[i + 7]),
                              s.codes4(v[i + 8], v[i + 9], v[i + 10], v[i + 11]),
                              s.codes4(v[i + 12], v[i + 13], v[i + 14], v[i + 15])));
-    store_staged<4, 4>(staged, reinterpret_cast<uint8_t*>(codes + row * pitch + col), pitch / 4,
-                       rows, 16, true, lane);
+    store_staged<4>(staged, reinterpret_cast<uint8_t*>(codes + row * pitch + col), pitch, rows, 64, true,
+                    lane);
 }
 template <int COLS>
 __device__ __forceinline__ void tmem_get(uint32_t at, float (&v)[COLS]) {
     if constexpr (COLS == 64) {
         mx4::tmem_ld64(at, v);
     } else {
-        static_assert(COLS == 32, "columns");
-        mx4::tmem_ld16(at, reinterpret_cast<float(&)[16]>(v[0]));
-        mx4::tmem_ld16(at + 16, reinterpret_cast<float(&)[16]>(v[16]));
+#pragma unroll
+        for (int i = 0; i < COLS; i += 16)
+            mx4::tmem_ld16(at + i, reinterpret_cast<float(&)[16]>(v[i]));
     }
 }
 
@@ -284,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(su32(&done_bar[i]), 1);
-            mbar_init(su32(&free_bar[i]), kEpilogueWarps);     // four warps of each CTA
+            mbar_init(su32(&free_bar[i]), 2 * kEpilogueWarps);
         }
         abort_s = 0;
         mbar_fence_init();
@@ -300,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_wait();
     fence_after();
     const uint32_t tmem = tmem_base_s;
-    wait_previous();
+    start_dependent();
 
     if (warp == 0) {
         if (elect_one()) {
@@ -395,35 +404,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
-        const int quarter = warp & 3, mine = (warp - 2) >> 2;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t staged = smem0 + N_STAGES * kStage<BN> + (warp - 2) * kStaged;
-        int n = mine;
-        for (int i = start + mine * pairs; i < items; i += 2 * pairs, n += 2) {
-            // All four warps of this group go on, or none.
+        int n = 0;
+        for (int i = start; i < items; i += pairs, ++n) {
+            // All four warps of this half go on, or none.
             const bool ok = all_of_group(
-                1 + mine, pipe_wait(su32(&done_bar[mine]), (n >> 1) & 1, abort_flag, pl.status) &&
+                1 + half, pipe_wait(su32(&done_bar[n & 1]), (n >> 1) & 1, abort_flag, pl.status) &&
                               !*abort_flag);
             if (!ok) break;
             fence_after();
             const Item t = item_at<MODE, BN>(pl, i);
-            const uint32_t sums = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + mine * BN;
+            const uint32_t sums = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + (n & 1) * BN;
             const long long row = t.row + rank * (kRows / 2) + 32 * quarter;
             const int rows = static_cast<int>(max(0LL, min(32LL, pl.rows - row)));
             auto done_reading = [&] {
                 fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_read(in_first_cta(su32(&free_bar[mine])));
+                if (lane == 0) arrive_read(in_first_cta(su32(&free_bar[n & 1])));
             };
             if constexpr (MODE == kForward) {
-                constexpr int kCols = BN >= 128 ? 64 : 32;     // at a time
+                constexpr int kCols = BN / 4;                  // outputs of a half
                 const FfKept& kept = pl.kept;
-#pragma unroll 1
-                for (int c = 0; c < BN / 2; c += kCols) {
+                {
                     float g[kCols], u[kCols];
-                    tmem_get<kCols>(sums + c, g);
-                    tmem_get<kCols>(sums + BN / 2 + c, u);
-                    if (c + kCols == BN / 2) done_reading();
-                    const int col = t.col + c, cols = pl.cols - col;
+                    tmem_get<kCols>(sums + half * kCols, g);
+                    tmem_get<kCols>(sums + BN / 2 + half * kCols, u);
+                    done_reading();
+                    const int col = t.col + half * kCols, cols = pl.cols - col;
                     if (rows == 0 || cols <= 0) continue;
                     if (kept.keep == kKeepFull) {
                         put_rows<T, kCols>(staged, g, static_cast<uint8_t*>(kept.gate) +
@@ -450,10 +458,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             } else {
 #pragma unroll 1
-                for (int c = 0; c < BN; c += 64) {
+                for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 64) {
                     float v[64];
                     tmem_get<64>(sums + c, v);
-                    if (c + 64 == BN) done_reading();
+                    if (c + 64 == (half + 1) * (BN / 2)) done_reading();
                     const int col = t.col + c, cols = pl.cols - col;
                     if (rows == 0 || cols <= 0) continue;
                     if (MODE == kInput && pl.partial) {
@@ -469,8 +477,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                                      __float_as_uint(v[half + j + 1]),
                                                      __float_as_uint(v[half + j + 2]),
                                                      __float_as_uint(v[half + j + 3])));
-                            store_staged<8, 4>(staged, reinterpret_cast<uint8_t*>(to + half),
-                                               pl.partial_ld, rows, 32, true, lane);
+                            store_staged<8>(staged, reinterpret_cast<uint8_t*>(to + half),
+                                            4 * pl.partial_ld, rows, 128, true, lane);
                         }
                         continue;
                     }
@@ -488,7 +496,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncthreads();
     cluster_arrive();       // the other CTA is done with this one's memory and barriers
     cluster_wait();
-    launch_next();
     if (warp == 1) {
         fence_after();
         mx4::tmem_dealloc<2>(tmem, kTmemCols);

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
             from += gridDim.x;
         }
     };
-    wait_previous();
+    start_dependent();
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load(a[i]);
     float acc[NT][4] = {};
@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
             group += gridDim.x;
         }
     }
-    launch_next();
 }
 
 template <typename T, int ACT>

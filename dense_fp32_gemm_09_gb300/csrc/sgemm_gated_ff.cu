@@ -58,14 +58,13 @@ struct Aligned {
 template <typename T, int ACT, bool KEPT8>
 __global__ void __launch_bounds__(kThreads)
     ff_gradient(const GatedFfBackward p, T* dg, T* du, long long pitch, const Aligned on) {
-    const int groups = (p.N + 7) / 8;
-    const long long all = p.M * static_cast<long long>(groups);
     const long long codes = act8_pitch(p.N);
-    wait_previous();
-    for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < all;
-         i += static_cast<long long>(gridDim.x) * kThreads) {
-        const long long row = i / groups;
-        const int c = static_cast<int>(i - row * groups) * 8, n = p.N - c;
+    act8::Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x,
+                  static_cast<long long>(gridDim.x) * kThreads, (p.N + 7) / 8);
+    start_dependent();
+    for (; at.row < p.M; at.next()) {
+        const long long row = at.row;
+        const int c = at.col * 8, n = p.N - c;
         float g[8], u[8], dh[8];
         load8(static_cast<const T*>(p.dh) + row * p.lddh + c, n, on.dh, dh);
         if constexpr (KEPT8) {
@@ -103,10 +102,11 @@ __global__ void __launch_bounds__(kThreads)
         store8(du + row * pitch + c, 8, true, u);
         if (p.h) store8(static_cast<T*>(p.h) + row * p.ldh + c, n, on.h, h);
     }
-    launch_next();
 }
 
-// Matrices of 2-byte numbers into rows of `pitch`, eight columns a thread; blockIdx.y: which.
+// Matrices of 2-byte numbers into rows of `pitch`, a warp a row, two numbers a lane; blockIdx.y:
+// which.  Rows that start between two words are read in whole words all the same, and a word
+// of the copy is made of the second number of the lane before and the first of its own.
 struct Copies {
     const uint16_t* from[3];
     uint16_t* to[3];
@@ -115,21 +115,38 @@ struct Copies {
     long long pitch;
 };
 __global__ void __launch_bounds__(kThreads) ff_copy_rows(const Copies q) {
-    const int which = blockIdx.y, groups = (q.cols + 7) / 8;
-    const long long all = q.rows[which] * groups;
-    wait_previous();
-    for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < all;
-         i += static_cast<long long>(gridDim.x) * kThreads) {
-        const long long row = i / groups;
-        const int c = static_cast<int>(i - row * groups) * 8, n = q.cols - c;
-        const uint16_t* x = q.from[which] + row * q.ld[which] + c;
-        uint32_t w[4] = {};
+    constexpr int kWords = 8;            // of a lane on their way
+    const int which = blockIdx.y, lane = threadIdx.x & 31;
+    const long long warps = static_cast<long long>(gridDim.x) * (kThreads / 32);
+    start_dependent();
+    for (long long row = blockIdx.x * (kThreads / 32LL) + threadIdx.x / 32; row < q.rows[which];
+         row += warps) {
+        const uint16_t* const x = q.from[which] + row * q.ld[which];
+        uint16_t* const y = q.to[which] + row * q.pitch;
+        const int off = reinterpret_cast<uintptr_t>(x) & 2 ? 1 : 0;
+        for (int start = 0; start < q.cols; start += 64 * kWords) {
+            uint32_t w[kWords];
+            uint32_t before[kWords];     // (lane 0, off: the number before its word)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) w[j / 2] |= static_cast<uint32_t>(__ldg(x + j)) << (j % 2 * 16);
-        *reinterpret_cast<uint4*>(q.to[which] + row * q.pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < kWords; ++j) {
+                const int c = start + 64 * j + 2 * lane + off;     // of the word read
+                w[j] = before[j] = 0;
+                if (c + 1 < q.cols) w[j] = __ldg(reinterpret_cast<const uint32_t*>(x + c));
+                else if (c < q.cols) w[j] = __ldg(x + c);
+                if (off && lane == 0 && c <= q.cols) before[j] = __ldg(x + c - 1);
+            }
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) {
+                const int c = start + 64 * j + 2 * lane;           // of the word written
+                uint32_t v = w[j];
+                if (off) {
+                    const uint32_t last = __shfl_up_sync(0xFFFFFFFFu, w[j] >> 16, 1);
+                    v = (lane == 0 ? before[j] : last) | w[j] << 16;
+                }
+                if (c < q.cols) *reinterpret_cast<uint32_t*>(y + c) = v;
+            }
+        }
     }
-    launch_next();
 }
 
 // dx = the parts' sums, added in their order; four columns a thread.
@@ -137,13 +154,12 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads)
     ff_add_parts(const float* partial, long long ld, int split, int rows, int cols, T* dx,
                  long long lddx) {
-    const int groups = (cols + 3) / 4;
-    const long long all = rows * static_cast<long long>(groups);
-    wait_previous();
-    for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < all;
-         i += static_cast<long long>(gridDim.x) * kThreads) {
-        const long long row = i / groups;
-        const int c = static_cast<int>(i - row * groups) * 4;
+    act8::Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x,
+                  static_cast<long long>(gridDim.x) * kThreads, (cols + 3) / 4);
+    start_dependent();
+    for (; at.row < rows; at.next()) {
+        const long long row = at.row;
+        const int c = at.col * 4;
         float4 s = make_float4(0, 0, 0, 0);
         for (int k = 0; k < split; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(
@@ -155,7 +171,6 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < 4; ++j)
             if (c + j < cols) dx[row * lddx + c + j] = from_float<T>(v[j]);
     }
-    launch_next();
 }
 
 // ----------------------------------------------------------------------------
@@ -177,7 +192,7 @@ Choice choose_forward(int M, int N, int K, int keep) {
     Choice best{256, 1};
     double least = 0;
     for (int bn : {256, 128, 64}) {
-        if (bn == 64 && keep == kKeep8) continue;       // a block of 64 in two tiles
+        if (bn != 256 && keep == kKeep8) continue;      // a warp holds blocks of 64 whole
         const long long rounds = up_to(up_to(M, kTileRows) * up_to(N, bn / 2), kPairsOfGpu);
         const double t = static_cast<double>(rounds) * up_to(K, 64) * stage_clocks(bn) + 12.0 * bn;
         if (least == 0 || t < least) best.bn = bn, least = t;
@@ -259,7 +274,7 @@ struct Operands {
     cudaError_t copy(int sms, cudaStream_t st, int* launches) const {
         if (n == 0) return cudaSuccess;
         const long long most = std::max({copies.rows[0], copies.rows[1], copies.rows[2]});
-        const long long blocks = up_to(most * up_to(copies.cols, 8), kThreads);
+        const long long blocks = up_to(most, kThreads / 32);
         ++*launches;
         return launch_dependent(ff_copy_rows,
                                 dim3(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL)), n),

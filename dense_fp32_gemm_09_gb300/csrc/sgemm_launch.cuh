@@ -12,6 +12,12 @@ __device__ __forceinline__ void wait_previous() {
 __device__ __forceinline__ void launch_next() {
     asm volatile("griddepcontrol.launch_dependents;");
 }
+// Both at once, for kernels of calls of several launches: the next kernel is set up on SMs that
+// this one leaves free, and still waits for all of it.
+__device__ __forceinline__ void start_dependent() {
+    launch_next();
+    wait_previous();
+}
 
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,

@@ -53,7 +53,7 @@ __device__ __forceinline__ float shared_at(const void* w, int wtype, int c, floa
 template <typename T>
 __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerNormForward p) {
     const int D = p.cols;
-    wait_previous();
+    start_dependent();
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(p.x) + row * p.ldx;
         T* y = static_cast<T*>(p.y) + row * p.ldy;
@@ -76,7 +76,6 @@ __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerN
                                       shared_at(p.bias, p.weight_dtype, c, 0.0f)));
         }
     }
-    launch_next();
 }
 
 // A block takes the rows blockIdx.x, blockIdx.x + gridDim.x, ...; its sums over them go to
@@ -86,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) layer_norm_backward_wide(const Layer
     const int D = p.cols;
     const float inv = 1.0f / static_cast<float>(D);
     const long long pitch = act8_pitch(D);
-    wait_previous();
+    start_dependent();
     float* const pw = p.partial + blockIdx.x * 2LL * D;
     float* const pb = pw + D;
     bool first = true;
@@ -120,7 +119,6 @@ __global__ void __launch_bounds__(kThreads) layer_norm_backward_wide(const Layer
         }
         first = false;
     }
-    launch_next();
 }
 
 // out[c] = sum over the blocks' partial sums; blockIdx.y: dw, db.  A warp takes every 32nd
@@ -130,7 +128,7 @@ __global__ void __launch_bounds__(1024) layer_norm_columns(const LayerNormBackwa
     __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    wait_previous();
+    start_dependent();
     if (out == nullptr) return;
     float s = 0.0f;
     if (c < p.cols) {
@@ -145,7 +143,6 @@ __global__ void __launch_bounds__(1024) layer_norm_columns(const LayerNormBackwa
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
     const int mine = blockIdx.x * 32 + slice;
     if (lane == 0 && mine < p.cols) out[mine] = s;
-    launch_next();
 }
 
 // ----------------------------------------------------------------------------

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kWarpThreads) forward_warp(const LayerNormForw
     const float inv = 1.0f / static_cast<float>(D);
     const long long pitch = act8_pitch(D);
     const long long row = blockIdx.x * static_cast<long long>(kWarpThreads / 32) + threadIdx.x / 32;
-    wait_previous();
+    start_dependent();
     if (row < p.rows) {
         const T* x = static_cast<const T*>(p.x) + row * p.ldx;
         uint4 raw[NV];
@@ -117,7 +117,6 @@ __global__ void __launch_bounds__(kWarpThreads) forward_warp(const LayerNormForw
                                   c, c < pitch);
         }
     }
-    launch_next();
 }
 
 // ----------------------------------------------------------------------------
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
     const float my_inv = mine > 0.0f ? 1.0f / mine : 0.0f;
     const float their_inv = theirs > 0.0f ? 1.0f / theirs : 0.0f;
     __syncthreads();
-    wait_previous();
+    start_dependent();
     const T* const x_at = static_cast<const T*>(p.x);
     // Row set i: the rows ROWS i, ...; past the last one a row is read again and not stored.
     typename O::Row x[kSets][ROWS];
@@ -316,7 +315,6 @@ __global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
         set(x[0], i);
         if (kSets == 2 && i + gridDim.x < all) set(x[kSets - 1], i + gridDim.x);
     }
-    launch_next();
 }
 
 // ----------------------------------------------------------------------------
@@ -397,7 +395,7 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
     const float inv = 1.0f / static_cast<float>(D);
     const long long pitch = act8_pitch(D);
     const O own(D);
-    wait_previous();
+    start_dependent();
     BlockSum2 block_sum{part};
     const T* const dh_at = static_cast<const T*>(p.dh);
     const T* const dy_at = static_cast<const T*>(p.dy);
@@ -456,7 +454,6 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
         if (p.dweight) own.store(pw, sw);
         if (p.dbias) own.store(pw + D, sb);
     }
-    launch_next();
 }
 
 // ----------------------------------------------------------------------------
