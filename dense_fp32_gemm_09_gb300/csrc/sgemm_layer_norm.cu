@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(1024) layer_norm_columns(const LayerNormBackwa
     float s = 0.0f;
     if (c < p.cols) {
         const float* from = p.partial + static_cast<long long>(blockIdx.y) * p.cols + c;
-#pragma unroll 4
+#pragma unroll 10
         for (int i = slice; i < blocks; i += 32) s += from[i * 2LL * p.cols];
     }
     part[slice][lane] = s;

@@ -27,6 +27,7 @@ using mx4::two;
 using norm::BlockSum;
 using norm::kPairs;
 using norm::Own;
+using async::su32;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -318,46 +319,25 @@ __global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
 }
 
 // ----------------------------------------------------------------------------
-// Backward: OWN columns a thread, the row in registers, each input loaded a row ahead
+// Backward of ragged rows: single columns a thread, the row in registers, each input loaded a row
+// ahead
 // ----------------------------------------------------------------------------
 // A row of an 8-bit checkpoint, as Own's rows: codes and the scales of their blocks.
-template <typename T, bool VEC, int OWN>
+template <typename O, int OWN>
 struct KeptRow {
-    using O = Own<T, VEC, OWN>;
-    static constexpr int kW = O::kWidth;
-    uint32_t codes[VEC ? OWN / 4 : 1];
-    int8_t code[VEC ? 1 : OWN];
-    float scale[VEC ? O::kGroups : OWN];
+    int8_t code[OWN];
+    float scale[OWN];
     __device__ __forceinline__ void load(const O& own, const int8_t* row, const float* scales) {
 #pragma unroll
-        for (int i = 0; i < O::kGroups; ++i) {
+        for (int i = 0; i < OWN; ++i) {
             const int c = own.c[i];
             const bool in = c < own.D;
             scale[i] = in ? __ldg(scales + c / kAct8Block) : 0.0f;
-            if constexpr (!VEC) {
-                code[i] = in ? __ldg(row + c) : int8_t(0);
-            } else if constexpr (kW == 8) {
-                const uint2 w = in ? __ldg(reinterpret_cast<const uint2*>(row + c)) : make_uint2(0, 0);
-                codes[2 * i] = w.x;
-                codes[2 * i + 1] = w.y;
-            } else {
-                codes[i] = in ? __ldg(reinterpret_cast<const uint32_t*>(row + c)) : 0u;
-            }
+            code[i] = in ? __ldg(row + c) : int8_t(0);
         }
     }
-    // All of the thread's numbers.
-    __device__ __forceinline__ void pairs(Two (&x)[OWN / 2]) const {
-        if constexpr (VEC) {
-#pragma unroll
-            for (int i = 0; i < OWN / 4; ++i) {
-                act8::values4(codes[i], scale[4 * i / kW], reinterpret_cast<Two(&)[2]>(x[2 * i]));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < OWN / 2; ++j)
-                x[j] = two(act8::value(code[2 * j], scale[2 * j]),
-                           act8::value(code[2 * j + 1], scale[2 * j + 1]));
-        }
+    __device__ __forceinline__ Two pair(int j) const {
+        return two(act8::value(code[2 * j], scale[2 * j]), act8::value(code[2 * j + 1], scale[2 * j + 1]));
     }
 };
 
@@ -366,29 +346,20 @@ struct BlockSum2 {
     float2 (*part)[32];
     int turn = 0;
     __device__ __forceinline__ float2 operator()(float a, float b) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-            b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-        }
+        const float2 mine = warp_sums(a, b);
         float2* p = part[turn];
         turn ^= 1;
         const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0) p[threadIdx.x >> 5] = make_float2(a, b);
+        if (lane == 0) p[threadIdx.x >> 5] = mine;
         __syncthreads();
-        float2 v = lane < warps ? p[lane] : make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
-        }
-        return v;
+        const float2 v = lane < warps ? p[lane] : make_float2(0.0f, 0.0f);
+        return warp_sums(v.x, v.y);
     }
 };
 
-template <typename T, bool VEC, int OWN, bool KEPT>
+template <typename T, int OWN, bool KEPT>
 __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward p) {
-    using O = Own<T, VEC, OWN>;
+    using O = Own<T, false, OWN>;
     constexpr int P = OWN / 2;
     __shared__ float2 part[2][32];
     const int D = p.cols;
@@ -401,7 +372,7 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
     const T* const dy_at = static_cast<const T*>(p.dy);
     const T* const x_at = static_cast<const T*>(p.x);
     typename O::Row dh, dy, x;
-    KeptRow<T, VEC, OWN> kept;
+    KeptRow<O, OWN> kept;
     float m = 0.0f, r = 0.0f;
     auto load = [&](long long row) {
         own.load(dh_at + row * p.lddh, dh);
@@ -419,10 +390,11 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const bool more = row + gridDim.x < p.rows;
         Two n[P], g[P];
-        if constexpr (KEPT) kept.pairs(n);
-        else
 #pragma unroll
-            for (int j = 0; j < P; ++j) n[j] = x.pair(j);
+        for (int j = 0; j < P; ++j) {
+            if constexpr (KEPT) n[j] = kept.pair(j);
+            else n[j] = x.pair(j);
+        }
         own.weights(p.weight, p.weight_dtype, g);
         const Two less = twice(-m), r2 = twice(r);
         Two s1 = twice(0.0f), s2 = twice(0.0f);
@@ -449,6 +421,142 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
         if (p.dy && more) own.load(dy_at + (row + gridDim.x) * p.lddy, dy);
         own.store(static_cast<T*>(p.dx) + row * p.lddx, g);
     }
+    if (p.partial) {
+        float* const pw = p.partial + blockIdx.x * 2LL * D;
+        if (p.dweight) own.store(pw, sw);
+        if (p.dbias) own.store(pw + D, sb);
+    }
+}
+
+// ----------------------------------------------------------------------------
+// Backward of aligned rows: a ring of shared-memory stages holds the rows ahead
+// ----------------------------------------------------------------------------
+// Registers hold the sums over rows and one row's numbers; a second row's in flight
+// (backward_block) is not enough to cover the memory's latency: 8192 x 4096 bf16 58 us so, whether
+// x comes in 16 or in 8 bits.
+//
+// After the barrier of a row every thread is done with the row before, whose stage is filled
+// again then.  A copy that does not arrive in time ends the copying, not the loop (whose barriers
+// all threads have to meet): the status word says that what was written since is not to be used.
+template <typename T, int OWN, bool KEPT>
+__global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward p, const Ring ring) {
+    using O = Own<T, true, OWN>;
+    constexpr int P = OWN / 2, VEC = O::kWidth;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kMaxStages];
+    __shared__ float2 part[2][32];
+    __shared__ int abort_s;
+    const int D = p.cols;
+    const float inv = 1.0f / static_cast<float>(D);
+    const long long pitch = act8_pitch(D);
+    const O own(D);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ring.stages; ++i) async::mbar_init(su32(&bars[i]), 1);
+        abort_s = 0;
+        async::mbar_fence_init();
+    }
+    __syncthreads();
+    start_dependent();
+    BlockSum2 block_sum{part};
+    const int row_bytes = D * static_cast<int>(sizeof(T));
+    const int x_bytes = KEPT ? static_cast<int>(pitch) : row_bytes;
+    // A stage: dh, x or its codes, dy.
+    auto fill = [&](int stage, long long row) {
+        const uint32_t bar = su32(&bars[stage]), to = su32(smem + stage * ring.stage_bytes);
+        async::mbar_expect_tx(bar, row_bytes + x_bytes + (p.dy ? row_bytes : 0));
+        mx4::bulk_load(to, static_cast<const T*>(p.dh) + row * p.lddh, row_bytes, bar);
+        if (KEPT) mx4::bulk_load(to + row_bytes, p.codes + row * pitch, x_bytes, bar);
+        else mx4::bulk_load(to + row_bytes, static_cast<const T*>(p.x) + row * p.ldx, x_bytes, bar);
+        if (p.dy)
+            mx4::bulk_load(to + row_bytes + x_bytes, static_cast<const T*>(p.dy) + row * p.lddy,
+                           row_bytes, bar);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < ring.stages; ++i) {
+            const long long row = blockIdx.x + i * static_cast<long long>(gridDim.x);
+            if (row < p.rows) fill(i, row);
+        }
+    float scale[O::kGroups];
+    float m = 0.0f, r = 0.0f;
+    auto load = [&](long long row) {       // what is not in the ring
+        m = __ldg(p.mean + row);
+        r = __ldg(p.rstd + row);
+        if constexpr (KEPT)
+#pragma unroll
+            for (int i = 0; i < O::kGroups; ++i)
+                scale[i] = own.c[i] < D ? __ldg(p.scales + (row * pitch + own.c[i]) / kAct8Block) : 0.0f;
+    };
+    if (blockIdx.x < p.rows) load(blockIdx.x);
+    Two w[P];
+    own.weights(p.weight, p.weight_dtype, w);
+    Two sw[P] = {}, sb[P] = {};
+    int stage = 0, before = 0;
+    uint32_t phase = 0;
+    bool ok = true, first = true;
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const uint8_t* const at = smem + stage * ring.stage_bytes;
+        ok &= mx4::pipe_wait(su32(&bars[stage]), phase, &abort_s, ring.status);
+        Two n[P], g[P];
+        const Two less = twice(-m), r2 = twice(r);
+        Two s1 = twice(0.0f), s2 = twice(0.0f);
+#pragma unroll
+        for (int i = 0; i < O::kGroups; ++i) {
+            const int c = own.c[i], j0 = i * VEC / 2;
+            if (c < D) {
+                mx4::unpack(*reinterpret_cast<const uint4*>(at + c * sizeof(T)),
+                            reinterpret_cast<Two(&)[VEC / 2]>(g[j0]), T());
+                if constexpr (KEPT) {
+#pragma unroll
+                    for (int j = 0; j < VEC / 4; ++j)
+                        act8::values4(*reinterpret_cast<const uint32_t*>(at + row_bytes + c + 4 * j),
+                                      scale[i], reinterpret_cast<Two(&)[2]>(n[j0 + 2 * j]));
+                } else {
+                    mx4::unpack(*reinterpret_cast<const uint4*>(at + row_bytes + c * sizeof(T)),
+                                reinterpret_cast<Two(&)[VEC / 2]>(n[j0]), T());
+                }
+            } else {
+#pragma unroll
+                for (int j = j0; j < j0 + VEC / 2; ++j) g[j] = n[j] = twice(0.0f);
+            }
+#pragma unroll
+            for (int j = j0; j < j0 + VEC / 2; ++j) {
+                n[j] = mx4::mul(add(n[j], less), r2);
+                sb[j] = add(sb[j], g[j]);
+                sw[j] = mx4::fma(g[j], n[j], sw[j]);
+                g[j] = mx4::mul(w[j], g[j]);
+                s1 = add(s1, g[j]);
+                s2 = mx4::fma(g[j], n[j], s2);
+            }
+        }
+        const float2 sums = block_sum(sum(s1), sum(s2));
+        const long long refill = row + (ring.stages - 1) * static_cast<long long>(gridDim.x);
+        if (threadIdx.x == 0 && !first && ok && refill < p.rows) fill(before, refill);
+        if (row + gridDim.x < p.rows) load(row + gridDim.x);
+        const Two mg = twice(-sums.x * inv), mn = twice(-sums.y * inv);
+        T* const dx = static_cast<T*>(p.dx) + row * p.lddx;
+#pragma unroll
+        for (int i = 0; i < O::kGroups; ++i) {
+            const int c = own.c[i], j0 = i * VEC / 2;
+            if (c >= D) continue;
+            Two t[VEC / 2];
+            if (p.dy)
+                mx4::unpack(*reinterpret_cast<const uint4*>(at + row_bytes + x_bytes + c * sizeof(T)), t,
+                            T());
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+                const Two v = mx4::fma(n[j0 + j], mn, add(g[j0 + j], mg));
+                t[j] = p.dy ? mx4::fma(v, r2, t[j]) : mx4::mul(v, r2);
+            }
+            *reinterpret_cast<uint4*>(dx + c) = mx4::pack(t, T());
+        }
+        first = false;
+        before = stage;
+        if (++stage == ring.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (threadIdx.x == 0 && !ok) norm::ring_drain(su32(bars), ring.stages);
     if (p.partial) {
         float* const pw = p.partial + blockIdx.x * 2LL * D;
         if (p.dweight) own.store(pw, sw);
@@ -492,9 +600,22 @@ cudaError_t backward(const LayerNormBackward& p, const Shape& s, cudaStream_t st
     const auto run = [&](auto kernel) {
         return launch_dependent(kernel, dim3(s.grid), s.threads, 0, st, p);
     };
-    if (s.ragged)
-        return p.codes ? run(backward_block<T, false, 8, true>) : run(backward_block<T, false, 8, false>);
-    return p.codes ? run(backward_block<T, true, OWN, true>) : run(backward_block<T, true, OWN, false>);
+    if (s.ragged) return p.codes ? run(backward_block<T, 8, true>) : run(backward_block<T, 8, false>);
+    const int row = p.cols * static_cast<int>(sizeof(T));
+    const int stage = (p.dy ? 2 : 1) * row + (p.codes ? static_cast<int>(act8_pitch(p.cols)) : row);
+    const int per = std::max(1, std::min(512 / s.threads, 16));
+    const long long own = (p.rows + s.grid - 1LL) / s.grid;
+    const Ring ring{stage, static_cast<int>(std::min<long long>(
+                               {kMaxStages, norm::kSharedPerSm / per / stage, std::max(2LL, own)})),
+                    status_word_ptr()};
+    const auto run_ring = [&](auto kernel) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, norm::kSharedPerSm);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(kernel, dim3(s.grid), s.threads, ring.stages * ring.stage_bytes, st, p,
+                                ring);
+    };
+    return p.codes ? run_ring(backward_ring<T, OWN, true>) : run_ring(backward_ring<T, OWN, false>);
 }
 
 }  // namespace layer_norm

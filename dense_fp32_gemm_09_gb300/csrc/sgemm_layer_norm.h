@@ -16,6 +16,13 @@ struct Shape {
     bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
 };
 
+// The backward pass's rows ahead in shared memory.
+constexpr int kMaxStages = 4;
+struct Ring {
+    int stage_bytes, stages;
+    int* status;
+};
+
 cudaError_t forward_f32(const LayerNormForward& p, const Shape& s, cudaStream_t st);
 cudaError_t forward_bf16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
 cudaError_t forward_f16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
