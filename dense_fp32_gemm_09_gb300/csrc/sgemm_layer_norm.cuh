@@ -341,33 +341,79 @@ struct KeptRow {
     }
 };
 
-// Sums of two numbers over the block, one barrier.  Calls alternate between two buffers.
-struct BlockSum2 {
-    float2 (*part)[32];
+// The threads that share a row: a block is one or several such teams, which meet only at its end.
+struct Team {
+    int threads, id, tid;
+    __device__ __forceinline__ explicit Team(int n) : threads(n) {
+        id = threadIdx.x / n;
+        tid = threadIdx.x - id * n;
+    }
+    // (Barrier 0 is the whole block's.)
+    __device__ __forceinline__ void sync() const {
+        if (threads == 32) __syncwarp();
+        else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + id), "r"(threads) : "memory");
+    }
+};
+// Sums of two numbers over a team, one barrier.  Calls alternate between two buffers.
+struct TeamSum {
+    const Team& team;
+    float2 (*part)[16];              // [2][16]
     int turn = 0;
     __device__ __forceinline__ float2 operator()(float a, float b) {
         const float2 mine = warp_sums(a, b);
+        if (team.threads == 32) {
+            team.sync();             // (as every row has a barrier)
+            return mine;
+        }
         float2* p = part[turn];
         turn ^= 1;
-        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0) p[threadIdx.x >> 5] = mine;
-        __syncthreads();
+        const int lane = threadIdx.x & 31, warps = team.threads >> 5;
+        if (lane == 0) p[team.tid >> 5] = mine;
+        team.sync();
         const float2 v = lane < warps ? p[lane] : make_float2(0.0f, 0.0f);
         return warp_sums(v.x, v.y);
     }
 };
+// The teams' sums over rows, added in the teams' order, to the block's part of the workspace.
+template <typename O, int P>
+__device__ __forceinline__ void store_sums(const LayerNormBackward& p, const O& own, const Team& team,
+                                           float* held, const Two (&sw)[P], const Two (&sb)[P]) {
+    if (!p.partial) return;
+    const int D = p.cols, teams = blockDim.x / team.threads;
+    float* const to = p.partial + blockIdx.x * 2LL * D;
+    if (teams == 1) {
+        own.store(to, sw);
+        own.store(to + D, sb);
+        return;
+    }
+    const int width = (D + 3) / 4 * 4;              // (16-byte stores of aligned columns)
+    __syncthreads();                                // the ring is read no more
+    own.store(held + team.id * 2 * width, sw);
+    own.store(held + (team.id * 2 + 1) * width, sb);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+        const int at = i < D ? i : i - D + width;
+        float v = 0.0f;
+        for (int k = 0; k < teams; ++k) v += held[k * 2 * width + at];
+        to[i] = v;
+    }
+}
 
 template <typename T, int OWN, bool KEPT>
-__global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward p) {
+__global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward p, int team_threads) {
     using O = Own<T, false, OWN>;
     constexpr int P = OWN / 2;
-    __shared__ float2 part[2][32];
-    const int D = p.cols;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float2 part[16][2][16];
+    const Team team(team_threads);
+    const int D = p.cols, teams = blockDim.x / team_threads;
     const float inv = 1.0f / static_cast<float>(D);
     const long long pitch = act8_pitch(D);
-    const O own(D);
+    const O own(D, team.tid, team_threads);
     start_dependent();
-    BlockSum2 block_sum{part};
+    TeamSum team_sum{team, part[team.id]};
+    const long long first_row = blockIdx.x * static_cast<long long>(teams) + team.id;
+    const long long step = static_cast<long long>(gridDim.x) * teams;
     const T* const dh_at = static_cast<const T*>(p.dh);
     const T* const dy_at = static_cast<const T*>(p.dy);
     const T* const x_at = static_cast<const T*>(p.x);
@@ -382,13 +428,13 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
         m = __ldg(p.mean + row);
         r = __ldg(p.rstd + row);
     };
-    if (blockIdx.x < p.rows) {
-        load(blockIdx.x);
-        if (p.dy) own.load(dy_at + blockIdx.x * p.lddy, dy);
+    if (first_row < p.rows) {
+        load(first_row);
+        if (p.dy) own.load(dy_at + first_row * p.lddy, dy);
     }
     Two sw[P] = {}, sb[P] = {};
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const bool more = row + gridDim.x < p.rows;
+    for (long long row = first_row; row < p.rows; row += step) {
+        const bool more = row + step < p.rows;
         Two n[P], g[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) {
@@ -410,22 +456,18 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
             s2 = mx4::fma(g[j], n[j], s2);
         }
         const float rr = r;
-        if (more) load(row + gridDim.x);
-        const float2 sums = block_sum(sum(s1), sum(s2));
+        if (more) load(row + step);
+        const float2 sums = team_sum(sum(s1), sum(s2));
         const Two mg = twice(-sums.x * inv), mn = twice(-sums.y * inv), rr2 = twice(rr);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             const Two t = mx4::fma(n[j], mn, add(g[j], mg));
             g[j] = p.dy ? mx4::fma(t, rr2, dy.pair(j)) : mx4::mul(t, rr2);
         }
-        if (p.dy && more) own.load(dy_at + (row + gridDim.x) * p.lddy, dy);
+        if (p.dy && more) own.load(dy_at + (row + step) * p.lddy, dy);
         own.store(static_cast<T*>(p.dx) + row * p.lddx, g);
     }
-    if (p.partial) {
-        float* const pw = p.partial + blockIdx.x * 2LL * D;
-        if (p.dweight) own.store(pw, sw);
-        if (p.dbias) own.store(pw + D, sb);
-    }
+    store_sums(p, own, team, reinterpret_cast<float*>(smem), sw, sb);
 }
 
 // ----------------------------------------------------------------------------
@@ -442,22 +484,28 @@ template <typename T, int OWN, bool KEPT>
 __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward p, const Ring ring) {
     using O = Own<T, true, OWN>;
     constexpr int P = OWN / 2, VEC = O::kWidth;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[kMaxStages];
-    __shared__ float2 part[2][32];
+    extern __shared__ __align__(128) uint8_t smem_all[];
+    __shared__ __align__(8) uint64_t all_bars[16][kMaxStages];
+    __shared__ float2 part[16][2][16];
     __shared__ int abort_s;
-    const int D = p.cols;
+    const Team team(ring.team);
+    const int D = p.cols, teams = blockDim.x / ring.team;
+    uint8_t* const smem = smem_all + team.id * ring.stages * ring.stage_bytes;
+    uint64_t* const bars = all_bars[team.id];
+    const bool leader = team.tid == 0;
+    const long long first_row = blockIdx.x * static_cast<long long>(teams) + team.id;
+    const long long step = static_cast<long long>(gridDim.x) * teams;
     const float inv = 1.0f / static_cast<float>(D);
     const long long pitch = act8_pitch(D);
-    const O own(D);
-    if (threadIdx.x == 0) {
+    const O own(D, team.tid, ring.team);
+    if (threadIdx.x == 0) abort_s = 0;
+    if (leader) {
         for (int i = 0; i < ring.stages; ++i) async::mbar_init(su32(&bars[i]), 1);
-        abort_s = 0;
         async::mbar_fence_init();
     }
     __syncthreads();
     start_dependent();
-    BlockSum2 block_sum{part};
+    TeamSum team_sum{team, part[team.id]};
     const int row_bytes = D * static_cast<int>(sizeof(T));
     const int x_bytes = KEPT ? static_cast<int>(pitch) : row_bytes;
     // A stage: dh, x or its codes, dy.
@@ -471,11 +519,9 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
             mx4::bulk_load(to + row_bytes + x_bytes, static_cast<const T*>(p.dy) + row * p.lddy,
                            row_bytes, bar);
     };
-    if (threadIdx.x == 0)
-        for (int i = 0; i < ring.stages; ++i) {
-            const long long row = blockIdx.x + i * static_cast<long long>(gridDim.x);
-            if (row < p.rows) fill(i, row);
-        }
+    if (leader)
+        for (int i = 0; i < ring.stages; ++i)
+            if (first_row + i * step < p.rows) fill(i, first_row + i * step);
     float scale[O::kGroups];
     float m = 0.0f, r = 0.0f;
     auto load = [&](long long row) {       // what is not in the ring
@@ -486,14 +532,14 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
             for (int i = 0; i < O::kGroups; ++i)
                 scale[i] = own.c[i] < D ? __ldg(p.scales + (row * pitch + own.c[i]) / kAct8Block) : 0.0f;
     };
-    if (blockIdx.x < p.rows) load(blockIdx.x);
+    if (first_row < p.rows) load(first_row);
     Two w[P];
     own.weights(p.weight, p.weight_dtype, w);
     Two sw[P] = {}, sb[P] = {};
     int stage = 0, before = 0;
     uint32_t phase = 0;
     bool ok = true, first = true;
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    for (long long row = first_row; row < p.rows; row += step) {
         const uint8_t* const at = smem + stage * ring.stage_bytes;
         ok &= mx4::pipe_wait(su32(&bars[stage]), phase, &abort_s, ring.status);
         Two n[P], g[P];
@@ -528,10 +574,10 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
                 s2 = mx4::fma(g[j], n[j], s2);
             }
         }
-        const float2 sums = block_sum(sum(s1), sum(s2));
-        const long long refill = row + (ring.stages - 1) * static_cast<long long>(gridDim.x);
-        if (threadIdx.x == 0 && !first && ok && refill < p.rows) fill(before, refill);
-        if (row + gridDim.x < p.rows) load(row + gridDim.x);
+        const float2 sums = team_sum(sum(s1), sum(s2));
+        const long long refill = row + (ring.stages - 1) * step;
+        if (leader && !first && ok && refill < p.rows) fill(before, refill);
+        if (row + step < p.rows) load(row + step);
         const Two mg = twice(-sums.x * inv), mn = twice(-sums.y * inv);
         T* const dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
@@ -556,12 +602,8 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
             phase ^= 1u;
         }
     }
-    if (threadIdx.x == 0 && !ok) norm::ring_drain(su32(bars), ring.stages);
-    if (p.partial) {
-        float* const pw = p.partial + blockIdx.x * 2LL * D;
-        if (p.dweight) own.store(pw, sw);
-        if (p.dbias) own.store(pw + D, sb);
-    }
+    if (leader && !ok) norm::ring_drain(su32(bars), ring.stages);
+    store_sums(p, own, team, reinterpret_cast<float*>(smem_all), sw, sb);
 }
 
 // ----------------------------------------------------------------------------
@@ -597,25 +639,27 @@ cudaError_t forward(const LayerNormForward& p, const Shape& s, cudaStream_t st) 
 template <typename T>
 cudaError_t backward(const LayerNormBackward& p, const Shape& s, cudaStream_t st) {
     constexpr int OWN = sizeof(T) == 4 ? 8 : 16;
-    const auto run = [&](auto kernel) {
-        return launch_dependent(kernel, dim3(s.grid), s.threads, 0, st, p);
-    };
-    if (s.ragged) return p.codes ? run(backward_block<T, 8, true>) : run(backward_block<T, 8, false>);
-    const int row = p.cols * static_cast<int>(sizeof(T));
-    const int stage = (p.dy ? 2 : 1) * row + (p.codes ? static_cast<int>(act8_pitch(p.cols)) : row);
-    const int per = std::max(1, std::min(512 / s.threads, 16));
-    const long long own = (p.rows + s.grid - 1LL) / s.grid;
-    const Ring ring{stage, static_cast<int>(std::min<long long>(
-                               {kMaxStages, norm::kSharedPerSm / per / stage, std::max(2LL, own)})),
-                    status_word_ptr()};
-    const auto run_ring = [&](auto kernel) {
+    const int teams = s.threads / s.team;
+    // The teams' sums at the end.
+    const int held = teams > 1 ? teams * 2 * ((p.cols + 3) / 4 * 4) * static_cast<int>(sizeof(float)) : 0;
+    const auto run = [&](auto kernel, int smem, const auto& more) {
         const cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, norm::kSharedPerSm);
         if (e != cudaSuccess) return e;
-        return launch_dependent(kernel, dim3(s.grid), s.threads, ring.stages * ring.stage_bytes, st, p,
-                                ring);
+        return launch_dependent(kernel, dim3(s.grid), s.threads, std::max(smem, held), st, p, more);
     };
-    return p.codes ? run_ring(backward_ring<T, OWN, true>) : run_ring(backward_ring<T, OWN, false>);
+    if (s.ragged)
+        return p.codes ? run(backward_block<T, 8, true>, 0, s.team)
+                       : run(backward_block<T, 8, false>, 0, s.team);
+    const int row = p.cols * static_cast<int>(sizeof(T));
+    const int stage = (p.dy ? 2 : 1) * row + (p.codes ? static_cast<int>(act8_pitch(p.cols)) : row);
+    const long long own = (p.rows + static_cast<long long>(s.grid) * teams - 1) / (s.grid * teams);
+    const int rows_at_once = s.team <= 128 ? teams : 512 / s.team;       // of an SM
+    const int stages = static_cast<int>(
+        std::min<long long>({kMaxStages, norm::kSharedPerSm / rows_at_once / stage, std::max(2LL, own)}));
+    const Ring ring{s.team, stage, stages, status_word_ptr()};
+    return p.codes ? run(backward_ring<T, OWN, true>, teams * stages * stage, ring)
+                   : run(backward_ring<T, OWN, false>, teams * stages * stage, ring);
 }
 
 }  // namespace layer_norm

@@ -11,6 +11,7 @@ enum : int { kByBlock = 0, kByWarp = 1, kWide = 2 };
 struct Shape {
     int kind;
     int threads, grid;
+    int team;          // backward: threads that share a row
     int columns;       // of a thread, by block
     int groups;        // of 16 bytes a lane, by warp
     bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
@@ -19,6 +20,7 @@ struct Shape {
 // The backward pass's rows ahead in shared memory.
 constexpr int kMaxStages = 4;
 struct Ring {
+    int team;              // threads that share a row
     int stage_bytes, stages;
     int* status;
 };

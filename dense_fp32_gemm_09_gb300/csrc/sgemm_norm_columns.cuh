@@ -23,9 +23,11 @@ struct Own {
     static constexpr int kWidth = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;
     static constexpr int kGroups = OWN / kWidth, kPairs2 = OWN / 2;
     int c[kGroups], D;
-    __device__ __forceinline__ explicit Own(int d) : D(d) {
+    __device__ __forceinline__ explicit Own(int d) : Own(d, threadIdx.x, blockDim.x) {}
+    // Thread `tid` of `threads` that share a row.
+    __device__ __forceinline__ Own(int d, int tid, int threads) : D(d) {
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) c[i] = (threadIdx.x + i * blockDim.x) * kWidth;
+        for (int i = 0; i < kGroups; ++i) c[i] = (tid + i * threads) * kWidth;
     }
     // A row's numbers as they are stored; zeros past its end.
     struct Row {
