@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantiz
     }
 }
 
-// A warp takes 256 columns of a row, lane l the columns l, l + 32, ...
+// A warp takes 256 columns of a row, lane l the columns l, l + 32, ...: four blocks, whose scales
+// a quarter of the lanes each computes (by every lane for its own two numbers 49 instructions a
+// number).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quantize q) {
     const long long pitch = act8_pitch(q.cols);
@@ -88,21 +90,36 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quant
             static_cast<int>((pitch + 255) / 256));
     start_dependent();
     for (; at.row < q.rows; at.next()) {
-        const T* x = static_cast<const T*>(q.X) + at.row * q.ldx;
-        int8_t* codes = q.codes + at.row * pitch;
         const int c0 = at.col * 256 + lane;
+        const T* const x = static_cast<const T*>(q.X) + at.row * q.ldx + c0;
+        int8_t* const codes = q.codes + at.row * pitch + c0;
+        const int left = q.cols - c0, kept = static_cast<int>(pitch) - at.col * 256;
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c0 + 32 * i < q.cols ? to_float(__ldg(x + c0 + 32 * i)) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = 32 * i < left ? to_float(__ldg(x + 32 * i)) : 0.0f;
+        // The four blocks' amax: after two exchanges a lane goes on with one of them.
+        uint32_t m[4];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const int c = c0 + 32 * i;
-            const BlockScale s(block_amax<32>(max(magnitude(v[i]), magnitude(v[i + 1]))));
-            if (c >= pitch) continue;         // (the block's lanes agree)
-            const uint32_t w = s.codes4(v[i], v[i + 1], 0.0f, 0.0f);
-            codes[c] = static_cast<int8_t>(w);
-            codes[c + 32] = static_cast<int8_t>(w >> 8);
-            if (lane == 0) q.scales[(at.row * pitch + c) / kAct8Block] = s.scale;
+        for (int b = 0; b < 4; ++b) m[b] = max(magnitude(v[2 * b]), magnitude(v[2 * b + 1]));
+        const bool upper = lane & 16, high = lane & 8;
+        uint32_t p0 = upper ? m[2] : m[0], p1 = upper ? m[3] : m[1];
+        p0 = max(p0, __shfl_xor_sync(0xFFFFFFFFu, upper ? m[0] : m[2], 16));
+        p1 = max(p1, __shfl_xor_sync(0xFFFFFFFFu, upper ? m[1] : m[3], 16));
+        uint32_t amax = high ? p1 : p0;
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, high ? p0 : p1, 8));
+        const BlockScale own(block_amax<8>(amax));       // of block lane / 8
+        if ((lane & 7) == 0 && 64 * (lane >> 3) < kept)
+            q.scales[at.row * (pitch / kAct8Block) + at.col * 4 + (lane >> 3)] = own.scale;
+        const float mine = own.finite ? own.inv : __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            BlockScale s = own;
+            s.inv = __shfl_sync(0xFFFFFFFFu, mine, 8 * b);
+            s.finite = s.inv == s.inv;
+            if (64 * b >= kept) break;
+            const uint32_t w = s.codes4(v[2 * b], v[2 * b + 1], 0.0f, 0.0f);
+            codes[64 * b] = static_cast<int8_t>(w);
+            codes[64 * b + 32] = static_cast<int8_t>(w >> 8);
         }
     }
 }
@@ -171,19 +188,20 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_ragged(const Act8Deq
             static_cast<int>((pitch + 255) / 256));
     start_dependent();
     for (; at.row < q.rows; at.next()) {
-        T* y = static_cast<T*>(q.Y) + at.row * q.ldy;
-        const int8_t* codes = q.codes + at.row * pitch;
-        const float* scales = q.scales + at.row * (pitch / kAct8Block);
         const int c0 = at.col * 256 + lane;
-        float v[8];
+        T* const y = static_cast<T*>(q.Y) + at.row * q.ldy + c0;
+        const int8_t* const codes = q.codes + at.row * pitch + c0;
+        const float* const scales = q.scales + at.row * (pitch / kAct8Block) + at.col * 4;
+        const int left = q.cols - c0, kept = static_cast<int>(pitch) - at.col * 256;
+        int8_t code[8];
+        float scale[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = c0 + 32 * i;
-            v[i] = c < q.cols ? value(__ldg(codes + c), __ldg(scales + c / kAct8Block)) : 0.0f;
-        }
+        for (int i = 0; i < 8; ++i) code[i] = 32 * i < kept ? __ldg(codes + 32 * i) : int8_t(0);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) scale[b] = 64 * b < kept ? __ldg(scales + b) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (c0 + 32 * i < q.cols) y[c0 + 32 * i] = from_float<T>(v[i]);
+            if (32 * i < left) y[32 * i] = from_float<T>(value(code[i], scale[i / 2]));
     }
 }
 

@@ -78,47 +78,99 @@ __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerN
     }
 }
 
-// A block takes the rows blockIdx.x, blockIdx.x + gridDim.x, ...; its sums over them go to
-// partial[blockIdx.x][2][D] (dw, db), each column kept by one thread.
+// n of a row's column, from x or from its checkpoint.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) layer_norm_backward_wide(const LayerNormBackward p) {
-    const int D = p.cols;
-    const float inv = 1.0f / static_cast<float>(D);
-    const long long pitch = act8_pitch(D);
-    start_dependent();
-    float* const pw = p.partial + blockIdx.x * 2LL * D;
-    float* const pb = pw + D;
-    bool first = true;
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const T* dh = static_cast<const T*>(p.dh) + row * p.lddh;
-        const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-        const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-        T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-        const float m = __ldg(p.mean + row), r = __ldg(p.rstd + row);
-        auto n_at = [&](int c) {
-            const float v = p.codes ? value(p.codes[row * pitch + c],
-                                            p.scales[(row * pitch + c) / kAct8Block])
-                                    : to_float(x[c]);
-            return (v - m) * r;
-        };
-        float sg = 0.0f, sn = 0.0f;
-        for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(dh[c]);
-            sg += g;
-            sn = fmaf(g, n_at(c), sn);
-        }
-        const float mg = block_sum(sg) * inv, mn = block_sum(sn) * inv;
-        for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float h = to_float(dh[c]), n = n_at(c);
-            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * h;
-            float t = r * (g - mg - n * mn);
-            if (p.dy) t += to_float(dy[c]);
-            dx[c] = from_float<T>(t);
-            if (p.dweight) pw[c] = first ? h * n : pw[c] + h * n;
-            if (p.dbias) pb[c] = first ? h : pb[c] + h;
-        }
-        first = false;
+struct Normed {
+    const T* x;
+    const int8_t* codes;
+    const float* scales;
+    float m, r;
+    __device__ __forceinline__ Normed(const LayerNormBackward& p, long long row)
+        : x(static_cast<const T*>(p.x) + row * p.ldx),
+          codes(p.codes ? p.codes + row * act8_pitch(p.cols) : nullptr),
+          scales(p.codes ? p.scales + row * (act8_pitch(p.cols) / kAct8Block) : nullptr),
+          m(__ldg(p.mean + row)), r(__ldg(p.rstd + row)) {}
+    __device__ __forceinline__ float at(int c) const {
+        const float v = codes ? value(__ldg(codes + c), __ldg(scales + c / kAct8Block))
+                              : to_float(__ldg(x + c));
+        return (v - m) * r;
     }
+};
+// dx of rows too wide for registers: one row a block, read twice.
+constexpr int kWideThreads = 512;
+template <typename T>
+__global__ void __launch_bounds__(kWideThreads) layer_norm_backward_wide(const LayerNormBackward p) {
+    __shared__ float2 part[kWideThreads / 32];
+    const int D = p.cols, lane = threadIdx.x & 31;
+    const float inv = 1.0f / static_cast<float>(D);
+    start_dependent();
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const T* const dh = static_cast<const T*>(p.dh) + row * p.lddh;
+        const T* const dy = static_cast<const T*>(p.dy) + row * p.lddy;
+        T* const dx = static_cast<T*>(p.dx) + row * p.lddx;
+        const Normed<T> n(p, row);
+        float sg = 0.0f, sn = 0.0f;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < D; c += kWideThreads) {
+            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(__ldg(dh + c));
+            sg += g;
+            sn = fmaf(g, n.at(c), sn);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            sg += __shfl_xor_sync(0xFFFFFFFFu, sg, o);
+            sn += __shfl_xor_sync(0xFFFFFFFFu, sn, o);
+        }
+        __syncthreads();
+        if (lane == 0) part[threadIdx.x >> 5] = make_float2(sg, sn);
+        __syncthreads();
+        sg = sn = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWideThreads / 32; ++i) {
+            sg += part[i].x;
+            sn += part[i].y;
+        }
+        const float mg = sg * inv, mn = sn * inv;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < D; c += kWideThreads) {
+            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(__ldg(dh + c));
+            float t = n.r * (g - mg - n.at(c) * mn);
+            if (p.dy) t += to_float(__ldg(dy + c));
+            dx[c] = from_float<T>(t);
+        }
+    }
+}
+// Sums over a strip of rows (blockIdx.y) of 32 columns a warp, to partial[blockIdx.y][2][D]; the
+// warps take every eighth row and are added in their order.
+constexpr int kStripWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(32 * kStripWarps)
+    layer_norm_strips(const LayerNormBackward p, long long rows_each) {
+    __shared__ float2 part[kStripWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    const long long first = blockIdx.y * rows_each, end = min(first + rows_each, p.rows + 0LL);
+    start_dependent();
+    float sw = 0.0f, sb = 0.0f;
+    if (c < p.cols) {
+#pragma unroll 4
+        for (long long row = first + warp; row < end; row += kStripWarps) {
+            const float h = to_float(__ldg(static_cast<const T*>(p.dh) + row * p.lddh + c));
+            sb += h;
+            sw = fmaf(h, Normed<T>(p, row).at(c), sw);
+        }
+    }
+    part[warp][lane] = make_float2(sw, sb);
+    __syncthreads();
+    if (warp > 0 || c >= p.cols) return;
+#pragma unroll
+    for (int i = 1; i < kStripWarps; ++i) {
+        sw += part[i][lane].x;
+        sb += part[i][lane].y;
+    }
+    float* const to = p.partial + blockIdx.y * 2LL * p.cols + c;
+    to[0] = sw;
+    to[p.cols] = sb;
 }
 
 // out[c] = sum over the blocks' partial sums; blockIdx.y: dw, db.  A warp takes every 32nd
@@ -231,9 +283,23 @@ Shape backward_shape(const LayerNormBackward& p, int sms) {
     on.add(p.weight, 0);
     const int own = !on.whole || p.dtype == kF32 ? 8 : 16;
     if (p.cols <= own * 512) return backward_shape(p.rows, p.cols, own, !on.whole, sms);
+    // Strips of rows, for eight blocks an SM and no more strips than the workspace holds.
     Shape s{kWide};
-    s.grid = static_cast<int>(std::min<long long>(p.rows, 2LL * sms));
+    const long long tiles = (p.cols + 31) / 32;
+    s.grid = static_cast<int>(std::max(1LL, std::min({8LL * sms / tiles, 2LL * sms, p.rows / 16LL})));
     return s;
+}
+
+template <typename T>
+cudaError_t backward_wide(const LayerNormBackward& p, const Shape& s, int sms, cudaStream_t st,
+                          int* launches) {
+    const dim3 grid(static_cast<unsigned>(std::min<long long>(p.rows, 4LL * sms)));
+    const cudaError_t e =
+        launch_dependent(layer_norm_backward_wide<T>, grid, kWideThreads, 0, st, p);
+    if (e != cudaSuccess || (!p.dweight && !p.dbias)) return e;
+    ++*launches;
+    return launch_dependent(layer_norm_strips<T>, dim3((p.cols + 31) / 32, s.grid), 32 * kStripWarps, 0,
+                            st, p, (static_cast<long long>(p.rows) + s.grid - 1) / s.grid);
 }
 
 }  // namespace
@@ -272,20 +338,16 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackward& p, int sms, cuda
     *launches = 1;
     cudaError_t e;
     if (s.kind == kWide) {
-        const dim3 grid(s.grid);
-        if (p.dtype == kF32)
-            e = launch_dependent(layer_norm_backward_wide<float>, grid, kThreads, 0, stream, p);
-        else if (p.dtype == kBf16)
-            e = launch_dependent(layer_norm_backward_wide<__nv_bfloat16>, grid, kThreads, 0, stream, p);
-        else
-            e = launch_dependent(layer_norm_backward_wide<__half>, grid, kThreads, 0, stream, p);
+        e = p.dtype == kF32    ? backward_wide<float>(p, s, sms, stream, launches)
+            : p.dtype == kBf16 ? backward_wide<__nv_bfloat16>(p, s, sms, stream, launches)
+                               : backward_wide<__half>(p, s, sms, stream, launches);
     } else {
         e = p.dtype == kF32    ? layer_norm::backward_f32(p, s, stream)
             : p.dtype == kBf16 ? layer_norm::backward_bf16(p, s, stream)
                                : layer_norm::backward_f16(p, s, stream);
     }
     if (e != cudaSuccess || (!p.dweight && !p.dbias)) return e;
-    *launches = 2;
+    ++*launches;
     return launch_dependent(layer_norm_columns, dim3((p.cols + 31) / 32, 2), 1024, 0, stream, p,
                             s.grid);
 }
