@@ -272,6 +272,7 @@ Shape backward_shape(long long rows, int cols, int own, bool ragged, int sms) {
     s.threads = teams * s.team;
     const long long per = std::min(512 / static_cast<long long>(room * s.team), 2LL);
     s.grid = static_cast<int>(std::min((rows + teams - 1) / teams, sms * per));
+    s.blocks = 1;
     return s;
 }
 Shape backward_shape(const LayerNormBackward& p, int sms) {
@@ -283,6 +284,19 @@ Shape backward_shape(const LayerNormBackward& p, int sms) {
     on.add(p.weight, 0);
     const int own = !on.whole || p.dtype == kF32 ? 8 : 16;
     if (p.cols <= own * 512) return backward_shape(p.rows, p.cols, own, !on.whole, sms);
+    if (p.cols <= 8 * (own * 512 - 64)) {      // up to eight blocks a row, whole blocks of 64 each
+        Shape c{};
+        c.kind = kByBlock;
+        c.ragged = !on.whole;
+        c.columns = own;
+        c.team = c.threads = 512;
+        for (c.blocks = 2;; c.blocks *= 2) {
+            c.each = static_cast<int>(act8_pitch((p.cols + c.blocks - 1) / c.blocks));
+            if (c.each <= own * 512) break;
+        }
+        c.grid = static_cast<int>(std::min<long long>(p.rows, sms / c.blocks)) * c.blocks;
+        return c;
+    }
     // Strips of rows, for eight blocks an SM and no more strips than the workspace holds.
     Shape s{kWide};
     const long long tiles = (p.cols + 31) / 32;
@@ -334,7 +348,7 @@ cudaError_t launch_layer_norm_forward(const LayerNormForward& p, int sms, cudaSt
 
 cudaError_t launch_layer_norm_backward(const LayerNormBackward& p, int sms, cudaStream_t stream,
                                        int* launches) {
-    const Shape s = backward_shape(p, sms);
+    Shape s = backward_shape(p, sms);
     *launches = 1;
     cudaError_t e;
     if (s.kind == kWide) {
@@ -349,7 +363,7 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackward& p, int sms, cuda
     if (e != cudaSuccess || (!p.dweight && !p.dbias)) return e;
     ++*launches;
     return launch_dependent(layer_norm_columns, dim3((p.cols + 31) / 32, 2), 1024, 0, stream, p,
-                            s.grid);
+                            s.kind == kWide ? s.grid : s.grid / s.blocks);
 }
 
 }  // namespace sgemm

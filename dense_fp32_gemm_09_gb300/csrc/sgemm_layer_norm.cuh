@@ -354,6 +354,41 @@ struct Team {
         else asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + id), "r"(threads) : "memory");
     }
 };
+__device__ __forceinline__ const void* at_column(const void* w, int type, int c) {
+    if (w == nullptr) return w;
+    return static_cast<const uint8_t*>(w) + static_cast<long long>(c) * (type == mx4::kF32 ? 4 : 2);
+}
+// SPLIT: rows too wide for one block.  A cluster of `count` blocks takes a row, each `each` of its
+// columns.
+template <bool SPLIT>
+struct Slice {
+    int count, rank, first, cols;
+    __device__ __forceinline__ Slice(int n, int each, int D) {
+        count = SPLIT ? n : 1;
+        rank = SPLIT ? static_cast<int>(blockIdx.x) % n : 0;
+        first = SPLIT ? rank * each : 0;
+        cols = SPLIT ? min(each, D - first) : D;
+    }
+};
+// The blocks' sums of a slice's row, added in their order: every block writes its own to all, and one
+// barrier of the cluster later they are there.  Two sets, which rows take in turn: a set is written
+// again after the next row's barrier, which all reads of it precede.
+__device__ __forceinline__ float2 cluster_sums(const Slice<true>& slice, float2 (*all)[8], int turn, float2 v) {
+    if (static_cast<int>(threadIdx.x) < slice.count) {
+        uint32_t to;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;"
+            : "=r"(to) : "r"(su32(&all[turn][slice.rank])), "r"(threadIdx.x));
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y) : "memory");
+    }
+    mx4::cluster_arrive();
+    mx4::cluster_wait();
+    float2 s = all[turn][0];
+    for (int i = 1; i < slice.count; ++i) {
+        s.x += all[turn][i].x;
+        s.y += all[turn][i].y;
+    }
+    return s;
+}
 // Sums of two numbers over a team, one barrier.  Calls alternate between two buffers.
 struct TeamSum {
     const Team& team;
@@ -375,12 +410,13 @@ struct TeamSum {
     }
 };
 // The teams' sums over rows, added in the teams' order, to the block's part of the workspace.
-template <typename O, int P>
+template <typename O, int P, bool SPLIT>
 __device__ __forceinline__ void store_sums(const LayerNormBackward& p, const O& own, const Team& team,
-                                           float* held, const Two (&sw)[P], const Two (&sb)[P]) {
+                                           const Slice<SPLIT>& slice, float* held, const Two (&sw)[P],
+                                           const Two (&sb)[P]) {
     if (!p.partial) return;
     const int D = p.cols, teams = blockDim.x / team.threads;
-    float* const to = p.partial + blockIdx.x * 2LL * D;
+    float* const to = p.partial + blockIdx.x / slice.count * 2LL * D + slice.first;
     if (teams == 1) {
         own.store(to, sw);
         own.store(to + D, sb);
@@ -399,31 +435,38 @@ __device__ __forceinline__ void store_sums(const LayerNormBackward& p, const O& 
     }
 }
 
-template <typename T, int OWN, bool KEPT>
-__global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward p, int team_threads) {
+template <typename T, int OWN, bool KEPT, bool SPLIT>
+__global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward p, int team_threads, int blocks, int each) {
     using O = Own<T, false, OWN>;
     constexpr int P = OWN / 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 part[16][2][16];
+    __shared__ float2 of_blocks[2][8];
     const Team team(team_threads);
-    const int D = p.cols, teams = blockDim.x / team_threads;
-    const float inv = 1.0f / static_cast<float>(D);
-    const long long pitch = act8_pitch(D);
-    const O own(D, team.tid, team_threads);
+    const Slice<SPLIT> slice(blocks, each, p.cols);
+    const int teams = blockDim.x / team_threads;
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    const long long pitch = act8_pitch(p.cols);
+    const O own(slice.cols, team.tid, team_threads);
+    if constexpr (SPLIT) {     // the other blocks' shared memory is there
+        mx4::cluster_arrive();
+        mx4::cluster_wait();
+    }
     start_dependent();
     TeamSum team_sum{team, part[team.id]};
-    const long long first_row = blockIdx.x * static_cast<long long>(teams) + team.id;
-    const long long step = static_cast<long long>(gridDim.x) * teams;
-    const T* const dh_at = static_cast<const T*>(p.dh);
-    const T* const dy_at = static_cast<const T*>(p.dy);
-    const T* const x_at = static_cast<const T*>(p.x);
+    const long long first_row = blockIdx.x / slice.count * static_cast<long long>(teams) + team.id;
+    const long long step = static_cast<long long>(gridDim.x / slice.count) * teams;
+    const T* const dh_at = static_cast<const T*>(p.dh) + slice.first;
+    const T* const dy_at = static_cast<const T*>(p.dy) + slice.first;
+    const T* const x_at = static_cast<const T*>(p.x) + slice.first;
     typename O::Row dh, dy, x;
     KeptRow<O, OWN> kept;
     float m = 0.0f, r = 0.0f;
     auto load = [&](long long row) {
         own.load(dh_at + row * p.lddh, dh);
         if constexpr (KEPT)
-            kept.load(own, p.codes + row * pitch, p.scales + row * (pitch / kAct8Block));
+            kept.load(own, p.codes + row * pitch + slice.first,
+                      p.scales + (row * pitch + slice.first) / kAct8Block);
         else own.load(x_at + row * p.ldx, x);
         m = __ldg(p.mean + row);
         r = __ldg(p.rstd + row);
@@ -433,6 +476,7 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
         if (p.dy) own.load(dy_at + first_row * p.lddy, dy);
     }
     Two sw[P] = {}, sb[P] = {};
+    int turn = 0;
     for (long long row = first_row; row < p.rows; row += step) {
         const bool more = row + step < p.rows;
         Two n[P], g[P];
@@ -441,7 +485,7 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
             if constexpr (KEPT) n[j] = kept.pair(j);
             else n[j] = x.pair(j);
         }
-        own.weights(p.weight, p.weight_dtype, g);
+        own.weights(at_column(p.weight, p.weight_dtype, slice.first), p.weight_dtype, g);
         const Two less = twice(-m), r2 = twice(r);
         Two s1 = twice(0.0f), s2 = twice(0.0f);
         // dh is 0 past the row's end, and so is what it multiplies into the sums.
@@ -457,7 +501,11 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
         }
         const float rr = r;
         if (more) load(row + step);
-        const float2 sums = team_sum(sum(s1), sum(s2));
+        float2 sums = team_sum(sum(s1), sum(s2));
+        if constexpr (SPLIT) {
+            sums = cluster_sums(slice, of_blocks, turn, sums);
+            turn ^= 1;
+        }
         const Two mg = twice(-sums.x * inv), mn = twice(-sums.y * inv), rr2 = twice(rr);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
@@ -465,9 +513,9 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
             g[j] = p.dy ? mx4::fma(t, rr2, dy.pair(j)) : mx4::mul(t, rr2);
         }
         if (p.dy && more) own.load(dy_at + (row + step) * p.lddy, dy);
-        own.store(static_cast<T*>(p.dx) + row * p.lddx, g);
+        own.store(static_cast<T*>(p.dx) + row * p.lddx + slice.first, g);
     }
-    store_sums(p, own, team, reinterpret_cast<float*>(smem), sw, sb);
+    store_sums(p, own, team, slice, reinterpret_cast<float*>(smem), sw, sb);
 }
 
 // ----------------------------------------------------------------------------
@@ -480,23 +528,25 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
 // After the barrier of a row every thread is done with the row before, whose stage is filled
 // again then.  A copy that does not arrive in time ends the copying, not the loop (whose barriers
 // all threads have to meet): the status word says that what was written since is not to be used.
-template <typename T, int OWN, bool KEPT>
+template <typename T, int OWN, bool KEPT, bool SPLIT>
 __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward p, const Ring ring) {
     using O = Own<T, true, OWN>;
     constexpr int P = OWN / 2, VEC = O::kWidth;
     extern __shared__ __align__(128) uint8_t smem_all[];
     __shared__ __align__(8) uint64_t all_bars[16][kMaxStages];
     __shared__ float2 part[16][2][16];
+    __shared__ float2 of_blocks[2][8];
     __shared__ int abort_s;
     const Team team(ring.team);
-    const int D = p.cols, teams = blockDim.x / ring.team;
+    const Slice<SPLIT> slice(ring.blocks, ring.each, p.cols);
+    const int D = slice.cols, teams = blockDim.x / ring.team;
     uint8_t* const smem = smem_all + team.id * ring.stages * ring.stage_bytes;
     uint64_t* const bars = all_bars[team.id];
     const bool leader = team.tid == 0;
-    const long long first_row = blockIdx.x * static_cast<long long>(teams) + team.id;
-    const long long step = static_cast<long long>(gridDim.x) * teams;
-    const float inv = 1.0f / static_cast<float>(D);
-    const long long pitch = act8_pitch(D);
+    const long long first_row = blockIdx.x / slice.count * static_cast<long long>(teams) + team.id;
+    const long long step = static_cast<long long>(gridDim.x / slice.count) * teams;
+    const float inv = 1.0f / static_cast<float>(p.cols);
+    const long long pitch = act8_pitch(p.cols);
     const O own(D, team.tid, ring.team);
     if (threadIdx.x == 0) abort_s = 0;
     if (leader) {
@@ -504,20 +554,26 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
         async::mbar_fence_init();
     }
     __syncthreads();
+    if constexpr (SPLIT) {     // the other blocks' shared memory is there
+        mx4::cluster_arrive();
+        mx4::cluster_wait();
+    }
     start_dependent();
     TeamSum team_sum{team, part[team.id]};
     const int row_bytes = D * static_cast<int>(sizeof(T));
-    const int x_bytes = KEPT ? static_cast<int>(pitch) : row_bytes;
+    const int x_bytes = KEPT ? static_cast<int>(act8_pitch(D)) : row_bytes;
     // A stage: dh, x or its codes, dy.
     auto fill = [&](int stage, long long row) {
         const uint32_t bar = su32(&bars[stage]), to = su32(smem + stage * ring.stage_bytes);
         async::mbar_expect_tx(bar, row_bytes + x_bytes + (p.dy ? row_bytes : 0));
-        mx4::bulk_load(to, static_cast<const T*>(p.dh) + row * p.lddh, row_bytes, bar);
-        if (KEPT) mx4::bulk_load(to + row_bytes, p.codes + row * pitch, x_bytes, bar);
-        else mx4::bulk_load(to + row_bytes, static_cast<const T*>(p.x) + row * p.ldx, x_bytes, bar);
+        mx4::bulk_load(to, static_cast<const T*>(p.dh) + row * p.lddh + slice.first, row_bytes, bar);
+        if (KEPT) mx4::bulk_load(to + row_bytes, p.codes + row * pitch + slice.first, x_bytes, bar);
+        else
+            mx4::bulk_load(to + row_bytes, static_cast<const T*>(p.x) + row * p.ldx + slice.first, x_bytes,
+                           bar);
         if (p.dy)
-            mx4::bulk_load(to + row_bytes + x_bytes, static_cast<const T*>(p.dy) + row * p.lddy,
-                           row_bytes, bar);
+            mx4::bulk_load(to + row_bytes + x_bytes,
+                           static_cast<const T*>(p.dy) + row * p.lddy + slice.first, row_bytes, bar);
     };
     if (leader)
         for (int i = 0; i < ring.stages; ++i)
@@ -530,13 +586,13 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
         if constexpr (KEPT)
 #pragma unroll
             for (int i = 0; i < O::kGroups; ++i)
-                scale[i] = own.c[i] < D ? __ldg(p.scales + (row * pitch + own.c[i]) / kAct8Block) : 0.0f;
+                scale[i] = own.c[i] < D ? __ldg(p.scales + (row * pitch + slice.first + own.c[i]) / kAct8Block) : 0.0f;
     };
     if (first_row < p.rows) load(first_row);
     Two w[P];
-    own.weights(p.weight, p.weight_dtype, w);
+    own.weights(at_column(p.weight, p.weight_dtype, slice.first), p.weight_dtype, w);
     Two sw[P] = {}, sb[P] = {};
-    int stage = 0, before = 0;
+    int stage = 0, before = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true, first = true;
     for (long long row = first_row; row < p.rows; row += step) {
@@ -574,12 +630,16 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
                 s2 = mx4::fma(g[j], n[j], s2);
             }
         }
-        const float2 sums = team_sum(sum(s1), sum(s2));
+        float2 sums = team_sum(sum(s1), sum(s2));
+        if constexpr (SPLIT) {
+            sums = cluster_sums(slice, of_blocks, turn, sums);
+            turn ^= 1;
+        }
         const long long refill = row + (ring.stages - 1) * step;
         if (leader && !first && ok && refill < p.rows) fill(before, refill);
         if (row + step < p.rows) load(row + step);
         const Two mg = twice(-sums.x * inv), mn = twice(-sums.y * inv);
-        T* const dx = static_cast<T*>(p.dx) + row * p.lddx;
+        T* const dx = static_cast<T*>(p.dx) + row * p.lddx + slice.first;
 #pragma unroll
         for (int i = 0; i < O::kGroups; ++i) {
             const int c = own.c[i], j0 = i * VEC / 2;
@@ -603,7 +663,7 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
         }
     }
     if (leader && !ok) norm::ring_drain(su32(bars), ring.stages);
-    store_sums(p, own, team, reinterpret_cast<float*>(smem_all), sw, sb);
+    store_sums(p, own, team, slice, reinterpret_cast<float*>(smem_all), sw, sb);
 }
 
 // ----------------------------------------------------------------------------
@@ -636,30 +696,68 @@ cudaError_t forward(const LayerNormForward& p, const Shape& s, cudaStream_t st) 
                                 st, p);
     return p.codes ? forward_rows_of<T, true>(p, s, st) : forward_rows_of<T, false>(p, s, st);
 }
+// No more clusters of `blocks` than run at once, `grid` blocks at most.  (One that waits for its SMs
+// would come to its rows when the others are done.)
+template <typename K, typename... A>
+cudaError_t launch_clusters(K kernel, int blocks, int* grid, int threads, int smem, cudaStream_t st,
+                            const A&... args) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(static_cast<unsigned>(*grid));
+    c.blockDim = dim3(static_cast<unsigned>(threads));
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    c.attrs = at;
+    c.numAttrs = 1;
+    int most = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &c);
+    if (e != cudaSuccess) return e;
+    if (most < 1) return cudaErrorInvalidConfiguration;
+    *grid = std::min(*grid, most * blocks);
+    c.gridDim = dim3(static_cast<unsigned>(*grid));
+    c.numAttrs = 2;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
 template <typename T>
-cudaError_t backward(const LayerNormBackward& p, const Shape& s, cudaStream_t st) {
+cudaError_t backward(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
     constexpr int OWN = sizeof(T) == 4 ? 8 : 16;
     const int teams = s.threads / s.team;
     // The teams' sums at the end.
     const int held = teams > 1 ? teams * 2 * ((p.cols + 3) / 4 * 4) * static_cast<int>(sizeof(float)) : 0;
-    const auto run = [&](auto kernel, int smem, const auto& more) {
+    const auto run = [&](auto kernel, int smem, const auto&... more) {
+        smem = std::max(smem, held);
         const cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, norm::kSharedPerSm);
         if (e != cudaSuccess) return e;
-        return launch_dependent(kernel, dim3(s.grid), s.threads, std::max(smem, held), st, p, more);
+        if (s.blocks == 1) return launch_dependent(kernel, dim3(s.grid), s.threads, smem, st, p, more...);
+        return launch_clusters(kernel, s.blocks, &s.grid, s.threads, smem, st, p, more...);
+    };
+    const auto choose = [&](auto one, auto split, int smem, const auto&... more) {
+        return s.blocks == 1 ? run(one, smem, more...) : run(split, smem, more...);
     };
     if (s.ragged)
-        return p.codes ? run(backward_block<T, 8, true>, 0, s.team)
-                       : run(backward_block<T, 8, false>, 0, s.team);
-    const int row = p.cols * static_cast<int>(sizeof(T));
-    const int stage = (p.dy ? 2 : 1) * row + (p.codes ? static_cast<int>(act8_pitch(p.cols)) : row);
-    const long long own = (p.rows + static_cast<long long>(s.grid) * teams - 1) / (s.grid * teams);
+        return p.codes ? choose(backward_block<T, 8, true, false>, backward_block<T, 8, true, true>, 0,
+                                s.team, s.blocks, s.each)
+                       : choose(backward_block<T, 8, false, false>, backward_block<T, 8, false, true>, 0,
+                                s.team, s.blocks, s.each);
+    const int cols = s.blocks == 1 ? p.cols : s.each;
+    const int row = cols * static_cast<int>(sizeof(T));
+    const int stage = (p.dy ? 2 : 1) * row + (p.codes ? static_cast<int>(act8_pitch(cols)) : row);
+    const long long sets = static_cast<long long>(s.grid / s.blocks) * teams;
+    const long long own = (p.rows + sets - 1) / sets;
     const int rows_at_once = s.team <= 128 ? teams : 512 / s.team;       // of an SM
     const int stages = static_cast<int>(
         std::min<long long>({kMaxStages, norm::kSharedPerSm / rows_at_once / stage, std::max(2LL, own)}));
-    const Ring ring{s.team, stage, stages, status_word_ptr()};
-    return p.codes ? run(backward_ring<T, OWN, true>, teams * stages * stage, ring)
-                   : run(backward_ring<T, OWN, false>, teams * stages * stage, ring);
+    const Ring ring{s.team, s.blocks, s.each, stage, stages, status_word_ptr()};
+    const int smem = teams * stages * stage;
+    return p.codes ? choose(backward_ring<T, OWN, true, false>, backward_ring<T, OWN, true, true>, smem, ring)
+                   : choose(backward_ring<T, OWN, false, false>, backward_ring<T, OWN, false, true>, smem,
+                            ring);
 }
 
 }  // namespace layer_norm

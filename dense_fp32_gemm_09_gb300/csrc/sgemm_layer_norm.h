@@ -11,7 +11,8 @@ enum : int { kByBlock = 0, kByWarp = 1, kWide = 2 };
 struct Shape {
     int kind;
     int threads, grid;
-    int team;          // backward: threads that share a row
+    int team;          // backward: threads of a block that share a row,
+    int blocks, each;  // blocks that share one (clusters of them), and their columns each
     int columns;       // of a thread, by block
     int groups;        // of 16 bytes a lane, by warp
     bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
@@ -21,6 +22,7 @@ struct Shape {
 constexpr int kMaxStages = 4;
 struct Ring {
     int team;              // threads that share a row
+    int blocks, each;      // a row's blocks, and their columns
     int stage_bytes, stages;
     int* status;
 };
@@ -28,9 +30,10 @@ struct Ring {
 cudaError_t forward_f32(const LayerNormForward& p, const Shape& s, cudaStream_t st);
 cudaError_t forward_bf16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
 cudaError_t forward_f16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
-cudaError_t backward_f32(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
-cudaError_t backward_bf16(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
-cudaError_t backward_f16(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
+// (With clusters, the grid becomes as many as run at once.)
+cudaError_t backward_f32(const LayerNormBackward& p, Shape& s, cudaStream_t st);
+cudaError_t backward_bf16(const LayerNormBackward& p, Shape& s, cudaStream_t st);
+cudaError_t backward_f16(const LayerNormBackward& p, Shape& s, cudaStream_t st);
 
 }  // namespace layer_norm
 }  // namespace sgemm

@@ -7,7 +7,7 @@ namespace layer_norm {
 cudaError_t forward_f16(const LayerNormForward& p, const Shape& s, cudaStream_t st) {
     return forward<__half>(p, s, st);
 }
-cudaError_t backward_f16(const LayerNormBackward& p, const Shape& s, cudaStream_t st) {
+cudaError_t backward_f16(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
     return backward<__half>(p, s, st);
 }
 

@@ -7,7 +7,7 @@ namespace layer_norm {
 cudaError_t forward_f32(const LayerNormForward& p, const Shape& s, cudaStream_t st) {
     return forward<float>(p, s, st);
 }
-cudaError_t backward_f32(const LayerNormBackward& p, const Shape& s, cudaStream_t st) {
+cudaError_t backward_f32(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
     return backward<float>(p, s, st);
 }
 
