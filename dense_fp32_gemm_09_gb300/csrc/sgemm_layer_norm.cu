@@ -290,6 +290,8 @@ Shape backward_shape(const LayerNormBackward& p, int sms) {
         c.ragged = !on.whole;
         c.columns = own;
         c.team = c.threads = 512;
+        // (Clusters of three blocks of 256 threads, two to an SM, 11279 x 9208 bf16: 463 us, of two of
+        // 512 threads 313.)
         for (c.blocks = 2;; c.blocks *= 2) {
             c.each = static_cast<int>(act8_pitch((p.cols + c.blocks - 1) / c.blocks));
             if (c.each <= own * 512) break;
