@@ -78,9 +78,7 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantiz
     }
 }
 
-// A warp takes 256 columns of a row, lane l the columns l, l + 32, ...: four blocks, whose scales
-// a quarter of the lanes each computes (by every lane for its own two numbers 49 instructions a
-// number).
+// A warp takes 256 columns of a row, lane l the columns l, l + 32, ...
 template <typename T>
 __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quantize q) {
     const long long pitch = act8_pitch(q.cols);
@@ -97,30 +95,7 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quant
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 32 * i < left ? to_float(__ldg(x + 32 * i)) : 0.0f;
-        // The four blocks' amax: after two exchanges a lane goes on with one of them.
-        uint32_t m[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) m[b] = max(magnitude(v[2 * b]), magnitude(v[2 * b + 1]));
-        const bool upper = lane & 16, high = lane & 8;
-        uint32_t p0 = upper ? m[2] : m[0], p1 = upper ? m[3] : m[1];
-        p0 = max(p0, __shfl_xor_sync(0xFFFFFFFFu, upper ? m[0] : m[2], 16));
-        p1 = max(p1, __shfl_xor_sync(0xFFFFFFFFu, upper ? m[1] : m[3], 16));
-        uint32_t amax = high ? p1 : p0;
-        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, high ? p0 : p1, 8));
-        const BlockScale own(block_amax<8>(amax));       // of block lane / 8
-        if ((lane & 7) == 0 && 64 * (lane >> 3) < kept)
-            q.scales[at.row * (pitch / kAct8Block) + at.col * 4 + (lane >> 3)] = own.scale;
-        const float mine = own.finite ? own.inv : __uint_as_float(0x7FC00000u);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            BlockScale s = own;
-            s.inv = __shfl_sync(0xFFFFFFFFu, mine, 8 * b);
-            s.finite = s.inv == s.inv;
-            if (64 * b >= kept) break;
-            const uint32_t w = s.codes4(v[2 * b], v[2 * b + 1], 0.0f, 0.0f);
-            codes[64 * b] = static_cast<int8_t>(w);
-            codes[64 * b + 32] = static_cast<int8_t>(w >> 8);
-        }
+        keep_singles(v, codes, q.scales + at.row * (pitch / kAct8Block) + at.col * 4, kept);
     }
 }
 

@@ -219,8 +219,9 @@ struct Alignment {
     }
 };
 // A block a row, `own` columns a thread; up to `most` threads an SM.
-Shape by_block(long long rows, int cols, int own, int most, bool ragged, int sms) {
+Shape by_block(long long rows, int cols, int own, int most, bool ragged, int sms, bool keeps = false) {
     Shape s{};
+    s.keeps = keeps;
     s.kind = kByBlock;
     s.ragged = ragged;
     s.columns = own;
@@ -238,21 +239,25 @@ Shape forward_shape(const LayerNormForward& p, int sms) {
     on.add(p.weight, 0);
     on.add(p.bias, 0);
     if (!on.whole) {
+        // (The checkpoint takes registers that only blocks of up to 512 threads have.)
+        if (p.codes && p.cols <= 8 * 512) return by_block(p.rows, p.cols, 8, 512, true, sms, true);
         if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, true, sms);
         return Shape{kWide};
     }
+    const bool keep = p.codes != nullptr;
     if (p.rows <= 2LL * sms && p.cols <= 8 * 1024)
-        return by_block(p.rows, p.cols, 8, 1024, false, sms);
+        return by_block(p.rows, p.cols, 8, 1024, false, sms, keep);
     if (p.cols <= 256) {
         Shape s{};
+        s.keeps = keep;
         s.kind = kByWarp;
         s.groups = p.cols * on.elem <= 512 ? 1 : 2;
         s.grid = static_cast<int>((p.rows + 3LL) / 4);
         return s;
     }
-    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 16, 512, false, sms);
+    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 16, 512, false, sms, keep);
     // Wider 2-byte rows, as far as weight and bias fit beside them in shared memory.
-    if (p.cols <= 16 * 1024 && on.elem == 2) return by_block(p.rows, p.cols, 16, 1024, false, sms);
+    if (p.cols <= 16 * 1024 && on.elem == 2) return by_block(p.rows, p.cols, 16, 1024, false, sms, keep);
     return Shape{kWide};
 }
 
@@ -342,8 +347,8 @@ cudaError_t launch_layer_norm_forward(const LayerNormForward& p, int sms, cudaSt
             : p.dtype == kBf16 ? layer_norm::forward_bf16(p, s, stream)
                                : layer_norm::forward_f16(p, s, stream);
     }
-    if (e != cudaSuccess || p.codes == nullptr || (s.kind != kWide && !s.ragged)) return e;
-    *launches = 2;         // a pass of its own over rows that are read by elements
+    if (e != cudaSuccess || p.codes == nullptr || s.keeps) return e;
+    *launches = 2;         // a pass of its own
     return launch_act8_quantize(
         Act8Quantize{p.rows, p.cols, p.dtype, p.x, p.ldx, p.codes, p.scales}, sms, stream);
 }

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sgemm_act8.cuh"
 #include "sgemm_launch.cuh"
@@ -49,6 +50,72 @@ __device__ __forceinline__ void shared_pairs(const void* w, int type, int c, flo
         norm::get_shared<__half, P, false>(static_cast<const __half*>(w), c, 0, x);
     }
 }
+// Columns of a thread where rows are not whole, aligned 16-byte groups: a warp has 32 OWN of them side
+// by side, a lane every 32nd, so that a load or store of a warp is contiguous at any alignment
+// and every one of them is at a fixed distance from the thread's first.  (With the block's threads
+// side by side instead, 3001 x 2047 fp32 took 65 instructions a number forward.)
+template <typename T, int OWN>
+struct Single {
+    static constexpr int kWidth = 1, kGroups = OWN, kPairs2 = OWN / 2;
+    int first, left;                 // the thread's first column, and how many there are from it
+    __device__ __forceinline__ explicit Single(int d) : Single(d, threadIdx.x, 0) {}
+    __device__ __forceinline__ Single(int d, int tid, int) {
+        first = (tid >> 5) * (32 * OWN) + (tid & 31);
+        left = d - first;
+    }
+    __device__ __forceinline__ bool in(int i) const { return 32 * i < left; }
+    struct Row {
+        T v[OWN];
+        __device__ __forceinline__ Two pair(int j) const {
+            return two(to_float(v[2 * j]), to_float(v[2 * j + 1]));
+        }
+    };
+    __device__ __forceinline__ void load(const T* row, Row& to) const {
+        row += first;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) to.v[i] = in(i) ? __ldg(row + 32 * i) : T(0.0f);
+    }
+    template <typename S>
+    __device__ __forceinline__ void store(S* row, const Two (&x)[kPairs2]) const {
+        row += first;
+#pragma unroll
+        for (int j = 0; j < kPairs2; ++j) {
+            const float2 f = parts(x[j]);
+            if (in(2 * j)) row[64 * j] = from_float<S>(f.x);
+            if (in(2 * j + 1)) row[64 * j + 32] = from_float<S>(f.y);
+        }
+    }
+    template <typename W>
+    __device__ __forceinline__ void shared(const W* w, Two (&x)[kPairs2]) const {
+        w += first;
+#pragma unroll
+        for (int j = 0; j < kPairs2; ++j)
+            x[j] = two(in(2 * j) ? to_float(__ldg(w + 64 * j)) : 0.0f,
+                       in(2 * j + 1) ? to_float(__ldg(w + 64 * j + 32)) : 0.0f);
+    }
+    // Weights; ones where there are none.
+    __device__ __forceinline__ void weights(const void* w, int type, Two (&x)[kPairs2]) const {
+        if (w == nullptr) {
+#pragma unroll
+            for (int j = 0; j < kPairs2; ++j) x[j] = twice(1.0f);
+        } else if (type == mx4::kF32) {
+            shared(static_cast<const float*>(w), x);
+        } else if (type == mx4::kBf16) {
+            shared(static_cast<const __nv_bfloat16*>(w), x);
+        } else {
+            shared(static_cast<const __half*>(w), x);
+        }
+    }
+};
+template <typename T, bool VEC, int OWN>
+using Columns = std::conditional_t<VEC, Own<T, true, OWN>, Single<T, OWN>>;
+template <typename T, int OWN>
+__device__ __forceinline__ bool inside(const Own<T, true, OWN>& own, int group) {
+    return own.c[group] < own.D;
+}
+template <typename T, int OWN>
+__device__ __forceinline__ bool inside(const Single<T, OWN>& own, int group) { return own.in(group); }
+
 // ----------------------------------------------------------------------------
 // Forward, one warp a row: NV 16-byte groups a lane, no barriers
 // ----------------------------------------------------------------------------
@@ -153,9 +220,9 @@ __device__ __forceinline__ void warp_sums(float (&v)[ROWS]) {
 // groups' first and second four columns from two arrays, so that a warp's reads meet no bank
 // twice.
 template <typename T, bool VEC, int OWN, bool KEEP, int ROWS, bool WIDE>
-__global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
+__global__ void __launch_bounds__((OWN == 16 && !WIDE) || (!VEC && KEEP) ? 512 : 1024, 1)
     forward_block(const LayerNormForward p) {
-    using O = Own<T, VEC, OWN>;
+    using O = Columns<T, VEC, OWN>;
     constexpr int P = OWN / 2;
     constexpr int kSets = ROWS == 1 ? 2 : 1;       // row sets ahead
     __shared__ float2 part[2][ROWS][32];
@@ -167,7 +234,7 @@ __global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
     // Columns of this thread's warp, and of warp `lane`.
     float mine = 0.0f;
 #pragma unroll
-    for (int i = 0; i < O::kGroups; ++i) mine += own.c[i] < D ? static_cast<float>(O::kWidth) : 0.0f;
+    for (int i = 0; i < O::kGroups; ++i) mine += inside(own, i) ? static_cast<float>(O::kWidth) : 0.0f;
     mine = warp_sum(mine);
     if (lane == 0) part[0][0][warp].x = mine;
     __syncthreads();
@@ -233,12 +300,23 @@ __global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
             s[k] = sum(t);
             if constexpr (KEEP) {
                 const long long row = i * ROWS + k;
+                int8_t* const codes = p.codes + row * pitch;
+                float* const scales = p.scales + row * (pitch / kAct8Block);
+                if constexpr (VEC) {
 #pragma unroll
-                for (int g = 0; g < O::kGroups; ++g)
-                    if (g * blockDim.x * O::kWidth < pitch)
-                        keep_groups<T, 1>({x[k].raw[g]}, p.codes + row * pitch,
-                                      p.scales + row * (pitch / kAct8Block), own.c[g],
-                                      k < rows && own.c[g] < pitch);
+                    for (int g = 0; g < O::kGroups; ++g)
+                        if (g * blockDim.x * O::kWidth < pitch)
+                            keep_groups<T, 1>({x[k].raw[g]}, codes, scales, own.c[g],
+                                              k < rows && own.c[g] < pitch);
+                } else {
+                    static_assert(ROWS == 1, "rows");
+                    float t[OWN];
+#pragma unroll
+                    for (int j = 0; j < OWN; ++j) t[j] = to_float(x[k].v[j]);
+                    const int from = warp * 32 * OWN;
+                    act8::keep_singles(t, codes + own.first, scales + from / kAct8Block,
+                                       static_cast<int>(pitch) - from);
+                }
             }
         }
         load(x, i + kSets * static_cast<long long>(gridDim.x));
@@ -251,11 +329,11 @@ __global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
             for (int j = 0; j < P; ++j) {
                 const Two d = add(v[k][j], less);
                 if constexpr (VEC) {
-                    if (own.c[2 * j / O::kWidth] < D) t = mx4::fma(d, d, t);
+                    if (inside(own, 2 * j / O::kWidth)) t = mx4::fma(d, d, t);
                 } else {
                     const float2 f = parts(d);
                     const Two in =
-                        two(own.c[2 * j] < D ? f.x : 0.0f, own.c[2 * j + 1] < D ? f.y : 0.0f);
+                        two(own.in(2 * j) ? f.x : 0.0f, own.in(2 * j + 1) ? f.y : 0.0f);
                     t = mx4::fma(in, in, t);
                 }
             }
@@ -323,21 +401,20 @@ __global__ void __launch_bounds__(OWN == 16 && !WIDE ? 512 : 1024, 1)
 // ahead
 // ----------------------------------------------------------------------------
 // A row of an 8-bit checkpoint, as Own's rows: codes and the scales of their blocks.
-template <typename O, int OWN>
+template <typename T, int OWN>
 struct KeptRow {
     int8_t code[OWN];
-    float scale[OWN];
-    __device__ __forceinline__ void load(const O& own, const int8_t* row, const float* scales) {
+    float scale[OWN / 2];
+    __device__ __forceinline__ void load(const Single<T, OWN>& own, const int8_t* row, const float* scales) {
+        row += own.first;
+        scales += own.first / kAct8Block;
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) {
-            const int c = own.c[i];
-            const bool in = c < own.D;
-            scale[i] = in ? __ldg(scales + c / kAct8Block) : 0.0f;
-            code[i] = in ? __ldg(row + c) : int8_t(0);
-        }
+        for (int i = 0; i < OWN; ++i) code[i] = own.in(i) ? __ldg(row + 32 * i) : int8_t(0);
+#pragma unroll
+        for (int i = 0; i < OWN / 2; ++i) scale[i] = own.in(2 * i) ? __ldg(scales + i) : 0.0f;
     }
     __device__ __forceinline__ Two pair(int j) const {
-        return two(act8::value(code[2 * j], scale[2 * j]), act8::value(code[2 * j + 1], scale[2 * j + 1]));
+        return two(act8::value(code[2 * j], scale[j]), act8::value(code[2 * j + 1], scale[j]));
     }
 };
 
@@ -437,7 +514,7 @@ __device__ __forceinline__ void store_sums(const LayerNormBackward& p, const O& 
 
 template <typename T, int OWN, bool KEPT, bool SPLIT>
 __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward p, int team_threads, int blocks, int each) {
-    using O = Own<T, false, OWN>;
+    using O = Single<T, OWN>;
     constexpr int P = OWN / 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float2 part[16][2][16];
@@ -460,7 +537,7 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
     const T* const dy_at = static_cast<const T*>(p.dy) + slice.first;
     const T* const x_at = static_cast<const T*>(p.x) + slice.first;
     typename O::Row dh, dy, x;
-    KeptRow<O, OWN> kept;
+    KeptRow<T, OWN> kept;
     float m = 0.0f, r = 0.0f;
     auto load = [&](long long row) {
         own.load(dh_at + row * p.lddh, dh);
@@ -475,6 +552,8 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
         load(first_row);
         if (p.dy) own.load(dy_at + first_row * p.lddy, dy);
     }
+    Two w[P];
+    own.weights(at_column(p.weight, p.weight_dtype, slice.first), p.weight_dtype, w);
     Two sw[P] = {}, sb[P] = {};
     int turn = 0;
     for (long long row = first_row; row < p.rows; row += step) {
@@ -485,7 +564,6 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
             if constexpr (KEPT) n[j] = kept.pair(j);
             else n[j] = x.pair(j);
         }
-        own.weights(at_column(p.weight, p.weight_dtype, slice.first), p.weight_dtype, g);
         const Two less = twice(-m), r2 = twice(r);
         Two s1 = twice(0.0f), s2 = twice(0.0f);
         // dh is 0 past the row's end, and so is what it multiplies into the sums.
@@ -495,7 +573,7 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
             n[j] = mx4::mul(add(n[j], less), r2);
             sb[j] = add(sb[j], h);
             sw[j] = mx4::fma(h, n[j], sw[j]);
-            g[j] = mx4::mul(g[j], h);
+            g[j] = mx4::mul(w[j], h);
             s1 = add(s1, g[j]);
             s2 = mx4::fma(g[j], n[j], s2);
         }
@@ -692,9 +770,10 @@ cudaError_t forward_rows_of(const LayerNormForward& p, const Shape& s, cudaStrea
 template <typename T>
 cudaError_t forward(const LayerNormForward& p, const Shape& s, cudaStream_t st) {
     if (s.ragged)
-        return launch_dependent(forward_block<T, false, 8, false, 1, false>, dim3(s.grid), s.threads, 0,
-                                st, p);
-    return p.codes ? forward_rows_of<T, true>(p, s, st) : forward_rows_of<T, false>(p, s, st);
+        return launch_dependent(s.keeps ? forward_block<T, false, 8, true, 1, false>
+                                        : forward_block<T, false, 8, false, 1, false>,
+                                dim3(s.grid), s.threads, 0, st, p);
+    return s.keeps ? forward_rows_of<T, true>(p, s, st) : forward_rows_of<T, false>(p, s, st);
 }
 // No more clusters of `blocks` than run at once, `grid` blocks at most.  (One that waits for its SMs
 // would come to its rows when the others are done.)

@@ -15,6 +15,7 @@ struct Shape {
     int blocks, each;  // blocks that share one (clusters of them), and their columns each
     int columns;       // of a thread, by block
     int groups;        // of 16 bytes a lane, by warp
+    bool keeps;        // forward: the checkpoint is written in the same pass
     bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
 };
 
