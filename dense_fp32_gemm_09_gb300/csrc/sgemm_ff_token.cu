@@ -6,7 +6,7 @@
 // thread's sums are g and u of the same output and tokens.  A sum does not depend on the order of
 // its terms, so a thread feeds the MMAs 32 consecutive bytes of a row of W and of x as they
 // come: nothing passes through shared memory, and a warp's loads are whole 128-byte lines, 4 KB
-// of them in flight.  (The 256-row tiles of sgemm_ff_pair.cuh spend 16 times as many MMAs on
+// of them in flight, or 2 KB from nine tokens on.  (The 256-row tiles of sgemm_ff_pair.cuh spend 16 times as many MMAs on
 // one token and fill as many SMs as there are tiles.)  The warps' sums are added
 // through shared memory in their order.
 #include <cuda_runtime.h>
@@ -24,7 +24,6 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kPiece = 64;               // of the contraction, 16 a lane
-constexpr int kAhead = 2;                // pieces of a warp on their way
 
 template <typename T>
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -89,13 +88,23 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
     const uint16_t* const x = static_cast<const uint16_t*>(p.x) + g * p.ldx;
     const uint16_t* const w_gate = static_cast<const uint16_t*>(p.w_gate);
     const uint16_t* const w_up = static_cast<const uint16_t*>(p.w_up);
-    // A piece is loaded as soon as the one four before it has been multiplied, across groups.
-    Piece a[kAhead][2];
+    // A piece is loaded as soon as the one kAhead before it has been multiplied, across groups.
+    // With sixteen tokens that of x too, and one piece is as much as the registers of 32 warps hold
+    // (16 tokens, 16384 x 4096: two pieces ahead without x 53 us, one 43.4, with x 42.4).
+    constexpr int kAhead = NT == 1 ? 2 : 1;
+    constexpr bool kTokensAhead = NT == 2;
+    Piece a[kAhead][2], b[kTokensAhead ? kAhead : 1][NT];
+    auto load_tokens = [&](Piece (&to)[NT], int k) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            to[n] = load_piece<false>(x + 8 * n * p.ldx + k, 8 * n + g < p.M ? p.K - k : 0, on32);
+    };
     int from = blockIdx.x, next = 0;
     const uint16_t* wg = nullptr;
     const uint16_t* wu = nullptr;
-    auto load = [&](Piece (&to)[2]) {
+    auto load = [&](int i) {
         if (from >= groups) return;
+        Piece (&to)[2] = a[i];
         if (next == 0) {                 // past the last output: its row again, not stored
             const long long row = min(8LL * from + g, p.N - 1LL);
             wg = w_gate + row * p.ldg;
@@ -104,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
         const int k = mine + next * (kWarps * kPiece);
         to[0] = load_piece<true>(wg + k, p.K - k, on32);
         to[1] = load_piece<true>(wu + k, p.K - k, on32);
+        if constexpr (kTokensAhead) load_tokens(b[i], k);
         if (++next == pieces) {
             next = 0;
             from += gridDim.x;
@@ -111,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
     };
     start_dependent();
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(a[i]);
+    for (int i = 0; i < kAhead; ++i) load(i);
     float acc[NT][4] = {};
     int piece = 0, turn = 0;
     for (int group = blockIdx.x; group < groups;) {
@@ -119,16 +129,16 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
         for (int i = 0; i < kAhead; ++i) {
             if (group >= groups) break;
             const int k = mine + piece * (kWarps * kPiece);
+            if constexpr (!kTokensAhead) load_tokens(b[0], k);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const Piece b = load_piece<false>(x + 8 * n * p.ldx + k,
-                                                  8 * n + g < p.M ? p.K - k : 0, on32);
+                const Piece& of = b[kTokensAhead ? i : 0][n];
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
                     mma16<T>(acc[n], a[i][0].w[2 * s], a[i][1].w[2 * s], a[i][0].w[2 * s + 1],
-                             a[i][1].w[2 * s + 1], b.w[2 * s], b.w[2 * s + 1]);
+                             a[i][1].w[2 * s + 1], of.w[2 * s], of.w[2 * s + 1]);
             }
-            load(a[i]);
+            load(i);
             if (++piece < pieces) continue;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
