@@ -98,6 +98,13 @@ size_t gated_ff_backward_workspace(int M, int N, int K, int packed);
 // Which of x, w_gate and w_up (bits 1, 2, 4) the kernels cannot read in place.
 int gated_ff_packed(const GatedFfForward& p);
 int gated_ff_packed(const GatedFfBackward& p);
+// What a product takes: tile columns (of the operand: twice the outputs forward; 0: the kernel for
+// few tokens) and parts of the contraction.
+enum : int { kProductForward = 0, kProductInput = 1, kProductWeights = 2 };
+struct FfChoice {
+    int bn, split;
+};
+FfChoice choose_gated_ff(int product, int M, int N, int K, int keep);
 cudaError_t launch_gated_ff_forward(const GatedFfForward& p, int sms, cudaStream_t stream,
                                     int* launches);
 cudaError_t launch_gated_ff_backward(const GatedFfBackward& p, int sms, cudaStream_t stream,

@@ -464,10 +464,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (c + 64 == (half + 1) * (BN / 2)) done_reading();
                     const int col = t.col + c, cols = pl.cols - col;
                     if (rows == 0 || cols <= 0) continue;
-                    if (MODE == kInput && pl.partial) {
+                    if (pl.partial) {
                         // One part's fp32 sums, 32 columns at a time.
-                        float* to = pl.partial +
-                                    (t.part * static_cast<long long>(pl.rows) + row) * pl.partial_ld + col;
+                        const long long set = MODE == kWeights ? 2 * t.part + t.matrix : t.part;
+                        float* to = pl.partial + (set * pl.rows + row) * pl.partial_ld + col;
 #pragma unroll
                         for (int half = 0; half < 64; half += 32) {
 #pragma unroll
@@ -518,12 +518,10 @@ cudaError_t launch_pair_of(const PairMaps& maps, const PairPlan& pl, int mode, i
                            int sms, cudaStream_t st) {
     if (mode == kForward) {
         if (activation == kSilu)
-            return bn == 256   ? launch_pair<T, kForward, 256, kSilu>(maps, pl, sms, st)
-                   : bn == 128 ? launch_pair<T, kForward, 128, kSilu>(maps, pl, sms, st)
-                               : launch_pair<T, kForward, 64, kSilu>(maps, pl, sms, st);
-        return bn == 256   ? launch_pair<T, kForward, 256, kGeluTanh>(maps, pl, sms, st)
-               : bn == 128 ? launch_pair<T, kForward, 128, kGeluTanh>(maps, pl, sms, st)
-                           : launch_pair<T, kForward, 64, kGeluTanh>(maps, pl, sms, st);
+            return bn == 256 ? launch_pair<T, kForward, 256, kSilu>(maps, pl, sms, st)
+                             : launch_pair<T, kForward, 128, kSilu>(maps, pl, sms, st);
+        return bn == 256 ? launch_pair<T, kForward, 256, kGeluTanh>(maps, pl, sms, st)
+                         : launch_pair<T, kForward, 128, kGeluTanh>(maps, pl, sms, st);
     }
     if (mode == kInput)
         return bn == 256 ? launch_pair<T, kInput, 256, kSilu>(maps, pl, sms, st)

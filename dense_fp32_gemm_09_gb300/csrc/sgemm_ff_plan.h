@@ -26,7 +26,7 @@ struct PairPlan {
     long long ldc[2];
     int c_vec, kept_vec;       // 1: rows start on 16 bytes
     FfKept kept;
-    float* partial;            // split > 1: [part][rows][partial_ld]
+    float* partial;            // split > 1: [part][matrix of the result][rows][partial_ld]
     long long partial_ld;
     int* status;
 };

@@ -149,27 +149,35 @@ __global__ void __launch_bounds__(kThreads) ff_copy_rows(const Copies q) {
     }
 }
 
-// dx = the parts' sums, added in their order; four columns a thread.
+// A product's parts, added in their order; four columns a thread, blockIdx.y: the matrix of the
+// result.
+struct Parts {
+    const float* partial;            // [part][matrix][rows][ld]
+    long long ld;
+    int split, matrices, rows, cols;
+    void* to[2];
+    long long ldto[2];
+};
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    ff_add_parts(const float* partial, long long ld, int split, int rows, int cols, T* dx,
-                 long long lddx) {
+__global__ void __launch_bounds__(kThreads) ff_add_parts(const Parts q) {
+    const int m = blockIdx.y;
     act8::Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x,
-                  static_cast<long long>(gridDim.x) * kThreads, (cols + 3) / 4);
+                  static_cast<long long>(gridDim.x) * kThreads, (q.cols + 3) / 4);
     start_dependent();
-    for (; at.row < rows; at.next()) {
-        const long long row = at.row;
+    for (; at.row < q.rows; at.next()) {
         const int c = at.col * 4;
         float4 s = make_float4(0, 0, 0, 0);
-        for (int k = 0; k < split; ++k) {
+#pragma unroll 4
+        for (int k = 0; k < q.split; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(
-                partial + (k * static_cast<long long>(rows) + row) * ld + c);
+                q.partial + ((k * static_cast<long long>(q.matrices) + m) * q.rows + at.row) * q.ld + c);
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
         const float v[4] = {s.x, s.y, s.z, s.w};
+        T* const to = static_cast<T*>(q.to[m]) + at.row * q.ldto[m] + c;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c + j < cols) dx[row * lddx + c + j] = from_float<T>(v[j]);
+            if (c + j < q.cols) to[j] = from_float<T>(v[j]);
     }
 }
 
@@ -180,18 +188,19 @@ long long up64(long long n) { return (n + 63) / 64 * 64; }
 long long matrix_bytes(long long rows, long long cols) { return rows * up64(cols) * 2; }
 long long up_to(long long n, int m) { return (n + m - 1) / m; }
 
-struct Choice {
-    int bn, split;
-};
 constexpr int kTokens = 16;          // up to here sgemm_ff_token.cu
 constexpr int kPairsOfGpu = 76;      // 152 SMs
-// Clocks of a stage: four MMAs of 128 for 256 columns; narrower ones wait for shared memory.
-int stage_clocks(int bn) { return bn == 256 ? 512 : bn == 128 ? 320 : 224; }
+// Clocks of a stage: four MMAs of 128 for 256 columns; narrower tiles wait for shared memory.  (Tiles
+// of 64 took 8.8 us where 128 took 7.0, 256x4096x1024, and at best 3 % less, 300x300x4096.)
+int stage_clocks(int bn) { return bn == 256 ? 512 : 320; }
 
-Choice choose_forward(int M, int N, int K, int keep) {
-    Choice best{256, 1};
+// Rounds of tiles, each as long as its stages and, forward with three results, its epilogue.  The
+// model's choice was the fastest of all, or within 3 % of it, on 14 shapes from 17 to 16384 tokens.
+FfChoice choose_forward(int M, int N, int K, int keep) {
+    if (M <= kTokens && keep != kKeep8) return FfChoice{0, 1};
+    FfChoice best{256, 1};
     double least = 0;
-    for (int bn : {256, 128, 64}) {
+    for (int bn : {256, 128}) {
         if (bn != 256 && keep == kKeep8) continue;      // a warp holds blocks of 64 whole
         const long long rounds = up_to(up_to(M, kTileRows) * up_to(N, bn / 2), kPairsOfGpu);
         const double t = static_cast<double>(rounds) * up_to(K, 64) * stage_clocks(bn) + 12.0 * bn;
@@ -199,32 +208,27 @@ Choice choose_forward(int M, int N, int K, int keep) {
     }
     return best;
 }
-Choice choose_weights(int M, int N, int K) {
-    Choice best{256, 1};
+// Few tiles share a contraction between up to sixteen pairs, eight stages each at least; their sums
+// take another pass over the result.
+FfChoice choose_split(long long tiles_of_rows, long long results, int cols, long long stages) {
+    FfChoice best{256, 1};
     double least = 0;
     for (int bn : {256, 128}) {
-        const long long rounds = up_to(2 * up_to(N, kTileRows) * up_to(K, bn), kPairsOfGpu);
-        const double t = static_cast<double>(rounds) * (up_to(M, 64) * stage_clocks(bn) + 6.0 * bn);
-        if (least == 0 || t < least) best.bn = bn, least = t;
-    }
-    return best;
-}
-// Few tiles share a contraction between up to sixteen pairs, eight stages each at least; their
-// sums take another pass over M x K.
-Choice choose_input(int M, int N, int K) {
-    Choice best{256, 1};
-    double least = 0;
-    const long long stages = 2 * up_to(N, 64);
-    for (int bn : {256, 128}) {
-        const long long tiles = up_to(M, kTileRows) * up_to(K, bn);
+        const long long tiles = tiles_of_rows * up_to(cols, bn);
         for (int split = 1; split <= 16 && (split == 1 || stages / split >= 8); ++split) {
             const double rounds = static_cast<double>(up_to(tiles * split, kPairsOfGpu));
             double t = rounds * (up_to(stages, split) * stage_clocks(bn) + 12.0 * bn);
-            if (split > 1) t += 5000 + 8.0 * M * K * split / 2500;
+            if (split > 1) t += 5000 + 8.0 * results * split / 2500;
             if (least == 0 || t < least) best = {bn, split}, least = t;
         }
     }
     return best;
+}
+FfChoice choose_input(int M, int N, int K) {
+    return choose_split(up_to(M, kTileRows), static_cast<long long>(M) * K, K, 2 * up_to(N, 64));
+}
+FfChoice choose_weights(int M, int N, int K) {
+    return choose_split(2 * up_to(N, kTileRows), 2LL * N * K, K, up_to(M, 64));
 }
 
 // A matrix of 2-byte numbers, boxes of 64 columns by `box` rows, zeros outside.
@@ -294,7 +298,8 @@ cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* laun
     const Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, p.ws);
     cudaError_t e = in.copy(sms, st, launches);
     if (e != cudaSuccess) return e;
-    if (p.M <= kTokens && p.kept.keep != kKeep8) {
+    const FfChoice c = choose_forward(p.M, p.N, p.K, p.kept.keep);
+    if (c.bn == 0) {
         GatedFfForward q = p;
         q.x = in.x;
         q.w_gate = in.w_gate;
@@ -306,7 +311,6 @@ cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* laun
         return launch_token(q, rows_on(32, in.x, p.M, in.ldx) && rows_on(32, in.w_gate, p.N, in.ldg) &&
                                    rows_on(32, in.w_up, p.N, in.ldu), sms, st);
     }
-    const Choice c = choose_forward(p.M, p.N, p.K, p.kept.keep);
     PairMaps maps;
     if (!encode(&maps.a[0], in.x, p.M, p.K, in.ldx, 128) ||
         !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, c.bn / 2) ||
@@ -343,6 +347,19 @@ cudaError_t gradient(const GatedFfBackward& p, T* dg, T* du, long long pitch, in
                : launch_dependent(ff_gradient<T, ACT, false>, grid, kThreads, 0, st, p, dg, du, pitch, on);
 }
 
+// The second half of a product whose tiles were split.
+template <typename T>
+cudaError_t add_parts(const PairPlan& pl, int matrices, int sms, cudaStream_t st, int* launches) {
+    if (!pl.partial) return cudaSuccess;
+    const Parts q{pl.partial, pl.partial_ld, pl.split, matrices, pl.rows, pl.cols,
+                  {pl.c[0], pl.c[1]}, {pl.ldc[0], pl.ldc[1]}};
+    const long long blocks = up_to(pl.rows * up_to(pl.cols, 4), kThreads);
+    ++*launches;
+    return launch_dependent(ff_add_parts<T>,
+                            dim3(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL)), matrices),
+                            kThreads, 0, st, q);
+}
+
 template <typename T>
 cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* launches) {
     const long long pitch = up64(p.N);
@@ -371,7 +388,7 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
     PairPlan pl{};
     pl.status = status_word_ptr();
     // dx, from dg and Wg, then du and Wu.
-    const Choice ci = choose_input(p.M, p.N, p.K);
+    const FfChoice ci = choose_input(p.M, p.N, p.K);
     if (!encode(&maps.a[0], dg, p.M, p.N, pitch, 128) || !encode(&maps.a[1], du, p.M, p.N, pitch, 128) ||
         !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, 64) ||
         !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, 64))
@@ -390,17 +407,10 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
     e = pair<T>(maps, pl, kInput, ci.bn, p.activation, sms, st);
     if (e != cudaSuccess) return e;
     ++*launches;
-    if (pl.partial) {
-        const long long blocks = up_to(p.M * up_to(p.K, 4), kThreads);
-        e = launch_dependent(ff_add_parts<T>,
-                             dim3(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL))),
-                             kThreads, 0, st, pl.partial, pl.partial_ld, pl.split, p.M, p.K,
-                             static_cast<T*>(p.dx), p.lddx);
-        if (e != cudaSuccess) return e;
-        ++*launches;
-    }
+    e = add_parts<T>(pl, 1, sms, st, launches);
+    if (e != cudaSuccess) return e;
     // dWg, then dWu.
-    const Choice cw = choose_weights(p.M, p.N, p.K);
+    const FfChoice cw = choose_weights(p.M, p.N, p.K);
     if (!encode(&maps.a[0], dg, p.M, p.N, pitch, 64) || !encode(&maps.a[1], du, p.M, p.N, pitch, 64) ||
         !encode(&maps.b[0], in.x, p.M, p.K, in.ldx, 64))
         return cudaErrorInvalidValue;
@@ -409,15 +419,17 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
     pl.tiles_m = static_cast<int>(2 * up_to(p.N, kTileRows));
     pl.tiles_n = static_cast<int>(up_to(p.K, cw.bn));
     pl.stages = static_cast<int>(up_to(p.M, 64));
-    pl.split = 1;
-    pl.partial = nullptr;
+    pl.split = cw.split;
+    pl.partial = cw.split > 1 ? reinterpret_cast<float*>(in.at) : nullptr;     // (dx's are used up)
     pl.c[0] = p.dw_gate;
     pl.c[1] = p.dw_up;
     pl.ldc[0] = p.lddwg;
     pl.ldc[1] = p.lddwu;
     pl.c_vec = on16(p.dw_gate, p.N, p.lddwg) && on16(p.dw_up, p.N, p.lddwu);
+    e = pair<T>(maps, pl, kWeights, cw.bn, p.activation, sms, st);
+    if (e != cudaSuccess) return e;
     ++*launches;
-    return pair<T>(maps, pl, kWeights, cw.bn, p.activation, sms, st);
+    return add_parts<T>(pl, 2, sms, st, launches);
 }
 
 // Copies of the operands that are not read in place.
@@ -432,13 +444,18 @@ int packed_bit(int bit, const void* p, long long rows, long long ld) {
 
 }  // namespace
 
+FfChoice choose_gated_ff(int product, int M, int N, int K, int keep) {
+    return product == kProductForward ? choose_forward(M, N, K, keep)
+           : product == kProductInput ? choose_input(M, N, K) : choose_weights(M, N, K);
+}
 size_t gated_ff_forward_workspace(int M, int N, int K, int packed) {
     return copied_bytes(M, N, K, packed);
 }
 size_t gated_ff_backward_workspace(int M, int N, int K, int packed) {
-    const Choice c = choose_input(M, N, K);
-    const size_t parts = c.split > 1 ? static_cast<size_t>(c.split) * 2 * matrix_bytes(M, K) : 0;
-    return 2 * static_cast<size_t>(matrix_bytes(M, N)) + copied_bytes(M, N, K, packed) + parts;
+    const auto parts = [](const FfChoice& c, size_t result) { return c.split > 1 ? c.split * result : 0; };
+    const size_t dx = parts(choose_input(M, N, K), 2 * matrix_bytes(M, K));          // fp32
+    const size_t dw = parts(choose_weights(M, N, K), 4 * matrix_bytes(N, K));
+    return 2 * static_cast<size_t>(matrix_bytes(M, N)) + copied_bytes(M, N, K, packed) + std::max(dx, dw);
 }
 int gated_ff_packed(const GatedFfForward& p) {
     return packed_bit(1, p.x, p.M, p.ldx) | packed_bit(2, p.w_gate, p.N, p.ldg) |

@@ -248,6 +248,19 @@ int sgemm_gated_ff_workspace(int M, int N, int K, int backward, int packed, size
     });
 }
 
+int sgemm_gated_ff_choose_check(int M, int N, int K, int keep, int product, int* columns, int* parts) {
+    return guarded([&]() -> int {
+        const char* const what = "sgemm_gated_ff_choose_check";
+        SGEMM_TRY(check_ff(what, M, N, K, SGEMM_BF16, SGEMM_SILU, keep, false));
+        if (M == 0 || product < 0 || product > 2 || columns == nullptr || parts == nullptr)
+            return refuse(SGEMM_ERR_INVALID_ARG, "%s: bad argument", what);
+        const FfChoice c = choose_gated_ff(product, M, N, K, keep);
+        *columns = c.bn;
+        *parts = c.split;
+        return SGEMM_OK;
+    });
+}
+
 int sgemm_gated_ff_forward(int M, int N, int K, int dtype, int activation, const void* x, int ldx,
                            const void* w_gate, int ldg, const void* w_up, int ldu, void* h,
                            int ldh, int keep, void* gate, void* up, int ldk, float* gate_scales,

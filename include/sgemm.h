@@ -530,6 +530,12 @@ SGEMM_API int sgemm_gated_ff_forward(int M, int N, int K, int dtype, int activat
                                      int ldk, float* gate_scales, float* up_scales, void* ws,
                                      size_t ws_bytes, sgemm_stream_t stream);
 
+/* What a product takes for these sizes (host only): `product` 0 for the forward pass (with `keep`),
+ * 1 for dx, 2 for the weights' gradients; in *columns its tile's columns (forward half of them of
+ * each weight; 0 for the kernel of up to 16 tokens), in *parts those of a tile's contraction. */
+SGEMM_API int sgemm_gated_ff_choose_check(int M, int N, int K, int keep, int product, int* columns,
+                                          int* parts);
+
 /* Its gradient from dh (of h), x or an 8-bit checkpoint of it (x_codes and x_scales; x NULL),
  * and what was kept of g and u (`keep` full or 8-bit):
  *
