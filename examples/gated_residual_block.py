@@ -43,9 +43,13 @@ class Linear:
 
     def backward(self, dy, x):
         """(gradient of x, gradient of W) from the gradient of y."""
-        dx = sg.mx4_matmul(quantize(dy, self.fmt), self.backward_weight, dtype=torch.bfloat16)
-        dw = sg.mx4_matmul(quantize(dy.t(), self.fmt), quantize(x.t(), self.fmt))
-        return dx, dw
+        return self.backward_input(dy), self.backward_weight_of(dy, x)
+
+    def backward_input(self, dy):
+        return sg.mx4_matmul(quantize(dy, self.fmt), self.backward_weight, dtype=torch.bfloat16)
+
+    def backward_weight_of(self, dy, x):
+        return sg.mx4_matmul(quantize(dy.t(), self.fmt), quantize(x.t(), self.fmt))
 
 
 def quantize(x, fmt: str):

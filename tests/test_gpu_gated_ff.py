@@ -21,6 +21,10 @@ SHAPES = [(1, 1, 1), (1, 8, 16), (3, 5, 7), (1, 1000, 200), (8, 333, 257), (16, 
           (1, 2048, 4096), (5, 100, 8), (33, 64, 72), (128, 128, 64), (129, 257, 65), (256, 256, 256),
           (300, 520, 136), (257, 1000, 2047), (1000, 640, 1024), (64, 4096, 512), (700, 96, 1000),
           (2000, 300, 64), (9, 2050, 1030), (513, 129, 320)]
+# Several rounds of tiles, every tile and split (test_gated_ff_choice.py).
+MANY = [(2600, 2100, 200), (4700, 2600, 72), (1000, 4100, 520), (900, 100, 6000), (9000, 64, 300),
+        (40, 3000, 520), (3000, 40, 520), (20000, 260, 250), (12000, 500, 1000),
+        (30000, 512, 512)]
 
 
 @pytest.fixture()
@@ -116,7 +120,7 @@ def whole(c, seed=1):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + MANY)
 def test_forward_of_integers_is_exact(sg, M, N, K, dtype):
     c = whole(Case(M, N, K, dtype))
     x, wg, wu = c.x.double(), c.wg.double(), c.wu.double()
@@ -174,7 +178,7 @@ def test_backward(sg, M, N, K, dtype, name):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("M,N,K", SHAPES + [(40, 3000, 520), (3000, 40, 520)])
+@pytest.mark.parametrize("M,N,K", SHAPES + MANY)
 def test_backward_of_integers_is_exact(sg, M, N, K, dtype):
     c = whole(Case(M, N, K, dtype))
     x, wg, wu, dh = (t.double() for t in (c.x, c.wg, c.wu, c.dh))

@@ -93,6 +93,31 @@ def test_graphs_beside_each_other(sg):
         assert same(got, ref)
 
 
+@pytest.mark.parametrize("cols", [64, 2047, 8192, 9000, 16384, 20001])
+def test_norms_of_every_width_in_graphs(sg, cols):
+    """Every kernel of the norm (one warp, one block, a cluster of blocks a row) is captured."""
+    g = torch.Generator("cuda").manual_seed(cols)
+    x, dh, dy = (torch.randn((50, cols), generator=g, device="cuda").bfloat16() for _ in range(3))
+    w = torch.randn((cols,), generator=g, device="cuda")
+
+    def call():
+        y, mean, rstd, kept = sg.layer_norm(x, w, w, keep="8bit")
+        return (y, mean, rstd, *sg.layer_norm_backward(dh, kept, mean, rstd, w, dy=dy),
+                *sg.layer_norm_backward(dh, x, mean, rstd, w))
+
+    want = call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, want)
+
+
 def test_threads(sg):
     data = [inputs(100 + 50 * i, 136 + 8 * i, 72 + i, seed=i) for i in range(4)]
     want = [block(sg, t) for t in data]
