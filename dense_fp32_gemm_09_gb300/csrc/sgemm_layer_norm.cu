@@ -26,7 +26,7 @@ using mx4::kBf16;
 using mx4::kF32;
 using mx4::to_float;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 
 // Sum over the block, in an order fixed by the thread numbers.
 __device__ __forceinline__ float block_sum(float v) {
@@ -58,11 +58,13 @@ __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerN
         const T* x = static_cast<const T*>(p.x) + row * p.ldx;
         T* y = static_cast<T*>(p.y) + row * p.ldy;
         float s = 0.0f;
-        for (int c = threadIdx.x; c < D; c += kThreads) s += to_float(x[c]);
+#pragma unroll 8
+        for (int c = threadIdx.x; c < D; c += kThreads) s += to_float(__ldg(x + c));
         const float m = block_sum(s) / static_cast<float>(D);
         s = 0.0f;
+#pragma unroll 8
         for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float d = to_float(x[c]) - m;
+            const float d = to_float(__ldg(x + c)) - m;
             s = fmaf(d, d, s);
         }
         const float r = rsqrtf(block_sum(s) / static_cast<float>(D) + p.eps);
@@ -70,8 +72,9 @@ __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerN
             p.mean[row] = m;
             p.rstd[row] = r;
         }
+#pragma unroll 8
         for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float n = (to_float(x[c]) - m) * r;
+            const float n = (to_float(__ldg(x + c)) - m) * r;
             y[c] = from_float<T>(fmaf(n, shared_at(p.weight, p.weight_dtype, c, 1.0f),
                                       shared_at(p.bias, p.weight_dtype, c, 0.0f)));
         }
@@ -97,10 +100,9 @@ struct Normed {
     }
 };
 // dx of rows too wide for registers: one row a block, read twice.
-constexpr int kWideThreads = 512;
 template <typename T>
-__global__ void __launch_bounds__(kWideThreads) layer_norm_backward_wide(const LayerNormBackward p) {
-    __shared__ float2 part[kWideThreads / 32];
+__global__ void __launch_bounds__(kThreads) layer_norm_backward_wide(const LayerNormBackward p) {
+    __shared__ float2 part[kThreads / 32];
     const int D = p.cols, lane = threadIdx.x & 31;
     const float inv = 1.0f / static_cast<float>(D);
     start_dependent();
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kWideThreads) layer_norm_backward_wide(const L
         const Normed<T> n(p, row);
         float sg = 0.0f, sn = 0.0f;
 #pragma unroll 4
-        for (int c = threadIdx.x; c < D; c += kWideThreads) {
+        for (int c = threadIdx.x; c < D; c += kThreads) {
             const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(__ldg(dh + c));
             sg += g;
             sn = fmaf(g, n.at(c), sn);
@@ -126,13 +128,13 @@ __global__ void __launch_bounds__(kWideThreads) layer_norm_backward_wide(const L
         __syncthreads();
         sg = sn = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kWideThreads / 32; ++i) {
+        for (int i = 0; i < kThreads / 32; ++i) {
             sg += part[i].x;
             sn += part[i].y;
         }
         const float mg = sg * inv, mn = sn * inv;
 #pragma unroll 4
-        for (int c = threadIdx.x; c < D; c += kWideThreads) {
+        for (int c = threadIdx.x; c < D; c += kThreads) {
             const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(__ldg(dh + c));
             float t = n.r * (g - mg - n.at(c) * mn);
             if (p.dy) t += to_float(__ldg(dy + c));
@@ -316,7 +318,7 @@ cudaError_t backward_wide(const LayerNormBackward& p, const Shape& s, int sms, c
                           int* launches) {
     const dim3 grid(static_cast<unsigned>(std::min<long long>(p.rows, 4LL * sms)));
     const cudaError_t e =
-        launch_dependent(layer_norm_backward_wide<T>, grid, kWideThreads, 0, st, p);
+        launch_dependent(layer_norm_backward_wide<T>, grid, kThreads, 0, st, p);
     if (e != cudaSuccess || (!p.dweight && !p.dbias)) return e;
     ++*launches;
     return launch_dependent(layer_norm_strips<T>, dim3((p.cols + 31) / 32, s.grid), 32 * kStripWarps, 0,
