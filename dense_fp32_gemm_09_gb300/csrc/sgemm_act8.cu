@@ -1,10 +1,15 @@
 // 8-bit activation checkpoints: rows to codes and scales, and back (sgemm_act8.cuh).
 //
 // Both directions are bound by memory: 5 bytes a number for fp32, 3 for 2-byte types, and a
-// sixteenth for the scales.  Aligned rows move 16 bytes of numbers at a time, so that a warp's
-// accesses are whole lines on both sides; a block of 64 columns is 8 or 16 neighbouring lanes.
+// sixteenth for the scales.  Aligned rows move 32 bytes of numbers a thread, so that a warp's
+// accesses are whole lines on both sides; a block of 64 columns is 4 or 8 neighbouring lanes.
 // Ragged rows (odd widths, strides or addresses) move single numbers, neighbouring lanes
 // neighbouring columns, a warp 256 columns at a time.
+//
+// Measured (us, kernels alone; of the memory's 6.79 TB/s): 16384 x 8192 bf16 to 8 bits 63.7 (0.95),
+// back 64.4 to 67.9 (0.94 to 0.89); 8192 x 8192 fp32 53.6 (0.93) and 57.5 (0.87); 3001 x 1999 fp32
+// 8.3 (0.54) and 6.7 (0.67).  With 16 bytes a thread and two divisions a block by every lane the
+// first two took 83 and 69.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -22,6 +22,12 @@
 //     two sets of sums, so that one item's epilogue runs under the next one's MMAs.  A warp has
 //     32 rows, one a lane, and passes up to 64 columns at a time through its own 4 KB of shared
 //     memory, to store whole 128-byte lines.
+//
+// Four MMAs of a stage take 512 clocks, so a tile of 256 x 256 x 2048 takes 8.5 us at 1.93 GHz; measured
+// are 10.2 to 12 with its share of the start and the end.  The tensor pipes are active 87 to 90 % of the
+// time (4096 x 2048 x 4096); at full size the card's power limit holds the clock lower.  Tiles of
+// 256 x 128 fill more pairs where there are few.  What is left is the last round: 3001 x 2047 x 1999
+// has 192 tiles for 76 pairs, 2.5 rounds that take 3.
 #pragma once
 
 #include <cuda_runtime.h>

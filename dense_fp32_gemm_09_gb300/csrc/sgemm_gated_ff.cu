@@ -6,7 +6,19 @@
 //     du = dh act(g)     dg = dh u act'(g)                 element by element, to the workspace
 //     dx = dg Wg + du Wu      dWg = dg^T x      dWu = du^T x
 // dg and du are rounded to the type of x, the tensor cores' operand type, so that a gradient
-// is off by the rounding of its terms (half an ulp each, at random) beside its own.
+// is off by the rounding of its terms (half an ulp each, at random) beside its own; so are the
+// numbers of an x that comes in 8 bits, whose own steps are 2^-8 of their block's largest.  In
+// norm, bf16: dx and the weights' gradients 2.3e-3 of 64 bits' where the rounding of the result
+// alone is 1.7e-3, the weights' gradients of an x in 8 bits 2.8e-3.
+//
+// The products: sgemm_ff_pair.cuh, and sgemm_ff_token.cu for up to 16 tokens.  Rows that are not on
+// 16 bytes cannot be read by tensor maps and are copied into the workspace first (3001 x 2047 and
+// 1999 x 2047 twice: 12 us beside a product of 36).
+//
+// Measured (us, kernels alone): forward 8192 x 4096 x 8192 bf16 527 to 550 (2.0 to 2.1 PFLOP/s; the
+// measured rate of a library product is 1.9, sustained 1.7), with g and u kept in 8 bits 546; the
+// gradient 1330 to 1350, of it 122 for ff_gradient (0.8 of the memory).  500 x 1024 x 4096 11.9 and
+// 28, 16384 x 256 x 64 backward 18 to 23.
 #include <cuda_runtime.h>
 
 #include <algorithm>
