@@ -54,7 +54,7 @@ struct LayerNormBackward {
     void* dx;
     long long lddx;
     float *dweight, *dbias;        // null: not asked for
-    float* partial;                // the blocks' column sums: [block][weight, bias][cols]
+    float* partial;                // the blocks' column sums: [block][weight, bias][cols]; null: none
 };
 cudaError_t launch_layer_norm_forward(const LayerNormForward& p, int sms, cudaStream_t stream,
                                       int* launches);

@@ -219,7 +219,8 @@ int sgemm_layer_norm_backward(int rows, int cols, int dtype, const void* dh, int
             }
             return SGEMM_OK;
         }
-        if (dweight || dbias) {
+        const bool sums = dweight || dbias;        // otherwise ws was not looked at, and is not used
+        if (sums) {
             const size_t need = layer_norm_backward_workspace(rows, cols, sms);
             SGEMM_TRY(check_ws("sgemm_layer_norm_backward", ws, ws_bytes, need));
             const Mat mat[] = {{"workspace", ws, 1, static_cast<long long>(need), 1, 1}};
@@ -229,7 +230,7 @@ int sgemm_layer_norm_backward(int rows, int cols, int dtype, const void* dh, int
         const LayerNormBackward p{rows, cols, dtype, weight_dtype, dh, dy, codes ? nullptr : x,
                                   lddh, lddy, ldx, static_cast<const int8_t*>(codes), scales,
                                   mean, rstd, weight, dx, lddx, dweight, dbias,
-                                  static_cast<float*>(ws)};
+                                  sums ? static_cast<float*>(ws) : nullptr};
         int n = 0;
         const cudaError_t e = launch_layer_norm_backward(p, sms, s, &n);
         return launched(e, "sgemm_layer_norm_backward", n);

@@ -278,3 +278,22 @@ def test_refusals(sg):
             sg.layer_norm_backward(*args)
     with pytest.raises(ValueError):
         sg.layer_norm_backward(x, x, mean, rstd, w, dy=x[:, :63])
+
+
+@pytest.mark.parametrize("cols", [64, 1000, 2047, 4096, 9000, 20001])
+def test_without_sums_the_workspace_stays(sg, cols):
+    """The C entry without dweight and dbias takes any workspace, of no bytes too, and leaves it."""
+    import ctypes
+    c, lib, s = Case(37, cols, "fp32"), sg.load(), torch.cuda.current_stream().cuda_stream
+    x, dh, w = cuda(c.x), cuda(c.dh), cuda(c.w)
+    _, mean, rstd = sg.layer_norm(x, w)
+    want = sg.layer_norm_backward(dh, x, mean, rstd, w)[0]
+    n = ctypes.c_size_t(0)
+    assert lib.sgemm_layer_norm_backward_workspace(37, cols, ctypes.byref(n)) == 0
+    ws = torch.full((n.value,), 9, dtype=torch.uint8, device="cuda")
+    dx = torch.zeros_like(x)
+    assert lib.sgemm_layer_norm_backward(
+        37, cols, 0, dh.data_ptr(), cols, None, 0, x.data_ptr(), cols, None, None, mean.data_ptr(),
+        rstd.data_ptr(), w.data_ptr(), 0, dx.data_ptr(), cols, None, None, ws.data_ptr(), 0, s) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(dx, want) and bool((ws == 9).all())
