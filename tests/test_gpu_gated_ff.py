@@ -372,3 +372,38 @@ def test_refusals(sg):
     for args in ((dh, wide, wg, wu, kept), (dh, x, wg, wu, (wide, wide))):
         with pytest.raises(ValueError):
             sg.gated_ff_backward(*args)
+
+
+@pytest.mark.parametrize("M,N,K", [(140000, 16384, 64), (270000, 64, 8191)])
+def test_long_offsets(sg, M, N, K):
+    """More than 2^31 numbers in h, dh and what is kept, or in an x and a dx of unaligned rows: the
+    last rows are their own.  Integers, so that every sum is exact in any order up to the result."""
+    c = whole(Case(64, N, K, "bf16"))
+    x, dh = torch.zeros(M, K, dtype=c.dt, device="cuda"), torch.zeros(M, N, dtype=c.dt, device="cuda")
+    x[-64:], dh[-64:] = c.x, c.dh
+    for keep in ("full", "8bit"):
+        h, kept = sg.gated_ff(x, c.wg, c.wu, keep=keep)
+        h0, kept0 = sg.gated_ff(c.x, c.wg, c.wu, keep=keep)
+        assert torch.equal(h[-64:], h0) and not bool(h[:-64].any())
+        for a, b in zip(kept, kept0):
+            if keep == "full":
+                assert torch.equal(a[-64:], b) and not bool(a[:-64].any())
+            else:
+                assert torch.equal(a.codes[-64:], b.codes) and torch.equal(a.scales[-64:], b.scales)
+        del h
+        got = sg.gated_ff_backward(dh, x, c.wg, c.wu, kept, return_h=True)
+        want = sg.gated_ff_backward(c.dh, c.x, c.wg, c.wu, kept0, return_h=True)
+        assert torch.equal(got[3][-64:], want[3]) and not bool(got[0][:-64].any())
+        # (What is not an integer, slopes and numbers of 8 bits, makes sums that depend on their order:
+        # both sides are within depth() of the magnitudes, and rounded once.)
+        g, u = (q.dequantize().double() if keep == "8bit" else q.double() for q in kept0)
+        a, slope = act(g, "silu")
+        dg, du = (c.dh.double() * u * slope).abs() * 1.01, (c.dh.double() * a).abs() * 1.01
+        bounds = ((got[0][-64:], want[0], depth(2 * N) * (dg @ c.wg.double().abs() + du @ c.wu.double().abs())),
+                  (got[1], want[1], depth(M) * (dg.t() @ c.x.double().abs())),
+                  (got[2], want[2], depth(M) * (du.t() @ c.x.double().abs())))
+        for a, b, sum_off in bounds:
+            b = b.double()
+            tol = 2 * sum_off + 2 * c.u * 1.01 * (b.abs() + 2 * sum_off) + c.t
+            assert bool(((a.double() - b).abs() <= tol).all())
+        del kept, got

@@ -297,3 +297,23 @@ def test_without_sums_the_workspace_stays(sg, cols):
         rstd.data_ptr(), w.data_ptr(), 0, dx.data_ptr(), cols, None, None, ws.data_ptr(), 0, s) == 0
     torch.cuda.synchronize()
     assert torch.equal(dx, want) and bool((ws == 9).all())
+
+
+@pytest.mark.parametrize("cols", [8192, 8191])
+def test_gradient_of_long_offsets(sg, cols):
+    """More than 2^31 elements, from a matrix and from a checkpoint: the last rows are their own."""
+    rows = 270000
+    c = Case(64, cols, "bf16")
+    x, dh, dy = (torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for big, small in ((x, c.x), (dh, c.dh), (dy, c.dy)):
+        big[-64:] = cuda(small)
+    _, mean, rstd, kept = sg.layer_norm(x, cuda(c.w), cuda(c.b), keep="8bit")
+    for of, rows_of in ((x, cuda(c.x)), (kept, sg.act8_quantize(cuda(c.x)))):
+        got = sg.layer_norm_backward(dh, of, mean, rstd, cuda(c.w), dy=dy)
+        want = sg.layer_norm_backward(cuda(c.dh), rows_of, mean[-64:], rstd[-64:], cuda(c.w), dy=cuda(c.dy))
+        # The same kernel and the same statistics: the same rows.  The other rows' dh are 0, but sums are
+        # added in another order: 64 terms of fp32, twice, of at most 64 times the largest |dh| |n|.
+        assert torch.equal(got[0][-64:], want[0]) and not bool(got[0][:-64].any())
+        most = 64 * float(c.dh.abs().max()) * max(1.0, float(((c.x.float() - 0.7) / 2).abs().max()) * 1.5)
+        for a, b in zip(got[1:], want[1:]):
+            assert bool(((a - b).abs() <= 2 * 64 * E24 * most).all())
