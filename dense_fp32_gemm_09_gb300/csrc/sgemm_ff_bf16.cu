@@ -5,8 +5,8 @@ namespace sgemm {
 namespace ff {
 
 cudaError_t pair_bf16(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int activation,
-                      int sms, cudaStream_t stream) {
-    return launch_pair_of<__nv_bfloat16>(maps, pl, mode, bn, activation, sms, stream);
+                      cudaStream_t stream) {
+    return launch_pair_of<__nv_bfloat16>(maps, pl, mode, bn, activation, stream);
 }
 
 }  // namespace ff

@@ -5,8 +5,8 @@ namespace sgemm {
 namespace ff {
 
 cudaError_t pair_f16(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int activation,
-                      int sms, cudaStream_t stream) {
-    return launch_pair_of<__half>(maps, pl, mode, bn, activation, sms, stream);
+                      cudaStream_t stream) {
+    return launch_pair_of<__half>(maps, pl, mode, bn, activation, stream);
 }
 
 }  // namespace ff

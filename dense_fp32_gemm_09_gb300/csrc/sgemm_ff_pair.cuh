@@ -1,9 +1,9 @@
 // Products of the gated feed-forward block on the tensor cores: tiles of 256 x BN, each by a
 // pair of CTAs (tcgen05, cta_group::2, 2-byte operands, fp32 sums).
 //
-//     forward   act(x Wg^T) (x Wu^T)    both operands with the contraction along their rows
-//     input     dg Wg + du Wu           the weights' contraction across their rows
-//     weights   dg^T x, du^T x          both operands' contraction across their rows
+//     forward     act(x Wg^T) (x Wu^T)    both operands with the contraction along their rows
+//     backward    dg Wg + du Wu           the weights' contraction across their rows, and in the same
+//                 dg^T x, du^T x          launch, both operands' contraction across their rows
 //
 // The two CTAs hold 128 of a tile's rows each and half of its BN columns' operand; the MMA reads the
 // other half from the other SM.  Forward, one CTA's half are rows of Wg and the other's the same
@@ -15,7 +15,7 @@
 // [64 of the contraction][64 columns].  What lies outside a matrix arrives as zeros, so no size
 // needs padding.
 //
-// Persistent: pair i takes the work items i, i + pairs, ...
+// Persistent: a pair takes its share of the work items, one after the other.
 //   warp 0: copies of the CTA's own halves; both CTAs' complete on the first one's barrier;
 //   warp 1 of the first CTA: the MMAs of both CTAs, four a stage;
 //   warps 2..5 and 6..9: the epilogue, 128 rows x each half of the columns.  Tensor memory holds
@@ -140,29 +140,58 @@ struct Ring {
 
 // One work item: a tile, and a range of its stages.
 struct Item {
-    int matrix;            // gradient of weights: 0 dWg, 1 dWu
+    int result;            // PairPlan::to
     int row, col;          // its first row and column of the result
     int first, last;       // stages
     int part;
 };
 template <int MODE, int BN>
-__device__ __forceinline__ Item item_at(const PairPlan& pl, int i) {
+__device__ __forceinline__ Item item_of(const Product& p, int i, bool weights) {
     Item t{};
-    const int tile = i / pl.split;
-    t.part = i - tile * pl.split;
-    const int group = tile / (kGroup * pl.tiles_n), in = tile - group * kGroup * pl.tiles_n;
-    const int high = min(kGroup, pl.tiles_m - group * kGroup);
+    const int tile = i / p.split;
+    t.part = i - tile * p.split;
+    const int group = tile / (kGroup * p.tiles_n), in = tile - group * kGroup * p.tiles_n;
+    const int high = min(kGroup, p.tiles_m - group * kGroup);
     int m = group * kGroup + in % high;
-    if (MODE == kWeights && m >= pl.tiles_m / 2) {
-        m -= pl.tiles_m / 2;
-        t.matrix = 1;
+    if (weights) {
+        const int half = p.tiles_m / 2;
+        t.result = m >= half ? 2 : 1;
+        if (m >= half) m -= half;
     }
     t.row = m * kRows;
     t.col = in / high * (MODE == kForward ? BN / 2 : BN);
-    t.first = static_cast<int>(static_cast<long long>(pl.stages) * t.part / pl.split);
-    t.last = static_cast<int>(static_cast<long long>(pl.stages) * (t.part + 1) / pl.split);
+    t.first = static_cast<int>(static_cast<long long>(p.stages) * t.part / p.split);
+    t.last = static_cast<int>(static_cast<long long>(p.stages) * (t.part + 1) / p.split);
     return t;
 }
+// A pair's items.  Those of the first product go round the pairs; where they do not come out even, the
+// `few` pairs with one less take pl.extra each of the second product's next, and what is left of
+// it goes round, from these pairs on.
+template <int MODE, int BN>
+struct Share {
+    int pair, pairs, ones, lead, few, slot, count;
+    __device__ __forceinline__ Share(const PairPlan& pl) {
+        pair = static_cast<int>(blockIdx.x) >> 1;
+        pairs = static_cast<int>(gridDim.x) >> 1;
+        const int n = pl.of[0].tiles_m * pl.of[0].tiles_n * pl.of[0].split;
+        ones = count = (n - pair + pairs - 1) / pairs;
+        lead = few = slot = 0;
+        if constexpr (MODE == kBackward) {
+            const int m = pl.of[1].tiles_m * pl.of[1].tiles_n * pl.of[1].split;
+            const int more = n % pairs;                // pairs 0 .. more - 1 have one more
+            few = more ? pairs - more : 0;
+            lead = few && pair >= more ? pl.extra : 0;
+            slot = pair >= more ? pair - more : pair + few;
+            count += lead + (m - few * pl.extra - slot + pairs - 1) / pairs;
+        }
+    }
+    __device__ __forceinline__ Item at(const PairPlan& pl, int i) const {
+        if (MODE == kForward || i < ones) return item_of<MODE, BN>(pl.of[0], pair + i * pairs, false);
+        i -= ones;
+        return item_of<MODE, BN>(pl.of[1], i < lead ? slot + i * few
+                                                    : few * pl.extra + slot + (i - lead) * pairs, true);
+    }
+};
 
 // A warp's 32 rows of CHUNKS 16-byte chunks: staged one row a lane, stored in whole lines.
 // The chunks of the rows that share a 128-byte line are permuted, so that neither side meets a
@@ -276,7 +305,6 @@ __device__ __forceinline__ void tmem_get(uint32_t at, float (&v)[COLS]) {
 template <typename T, int MODE, int BN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     ff_pair_kernel(const __grid_constant__ PairMaps maps, const PairPlan pl) {
-    constexpr bool kAcrossA = MODE == kWeights, kAcrossB = MODE != kForward;
     constexpr int kTmemCols = 2 * BN;
     constexpr int N_STAGES = kStages<BN>;
     extern __shared__ uint8_t smem_raw[];
@@ -286,9 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __shared__ int abort_s;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x) & 1;
-    const int pairs = static_cast<int>(gridDim.x) >> 1;
-    const int start = static_cast<int>(blockIdx.x) >> 1;
-    const int items = pl.tiles_m * pl.tiles_n * pl.split;
+    const Share<MODE, BN> share(pl);
     volatile int* abort_flag = &abort_s;
     const uint32_t smem0 = (su32(smem_raw) + 1023u) & ~1023u;
 
@@ -304,8 +330,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         abort_s = 0;
         mbar_fence_init();
     }
-    if (warp == 0 && lane < 4) {
-        const CUtensorMap* tm = lane < 2 ? &maps.a[lane] : &maps.b[lane - 2];
+    if (warp == 0 && lane < (MODE == kForward ? 3 : 7)) {
+        const CUtensorMap* tm = MODE == kForward ? (lane < 1 ? &maps.a[0] : &maps.b[lane - 1])
+                                                 : (lane < 4 ? &maps.a[lane] : &maps.b[lane - 4]);
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
     }
     if (warp == 1) mx4::tmem_alloc<2>(su32(&tmem_base_s), kTmemCols);
@@ -322,8 +349,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             Ring<N_STAGES> ring;
             int issued = 0;
             bool ok = true;
-            for (int i = start; i < items && ok; i += pairs) {
-                const Item t = item_at<MODE, BN>(pl, i);
+            for (int i = 0; i < share.count && ok; ++i) {
+                const Item t = share.at(pl, i);
                 const int row = t.row + rank * (kRows / 2);
                 const int col = MODE == kForward ? t.col : t.col + rank * (BN / 2);
                 for (int s = t.first; s < t.last; ++s) {
@@ -335,23 +362,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t fb = in_first_cta(su32(&full_bar[ring.stage]));
                     const uint32_t a = smem0 + ring.stage * kStage<BN>, b = a + kHalfA<BN>;
                     if (rank == 0) mbar_expect_tx(su32(&full_bar[ring.stage]), 2 * kStage<BN>);
-                    // Two pairs of operands one after the other (gradient of the input).
-                    const int second = MODE == kInput && s >= pl.stages / 2;
-                    const int k = (s - second * (pl.stages / 2)) * kDeep;
-                    const CUtensorMap* am = &maps.a[MODE == kWeights ? t.matrix : second];
-                    const CUtensorMap* bm = &maps.b[MODE == kForward ? rank : second];
-                    if (kAcrossA) {
-                        load_box(a, am, row, k, fb);
-                        load_box(a + kDeep * kLineBytes, am, row + 64, k, fb);
+                    if constexpr (MODE == kForward) {
+                        load_box(a, &maps.a[0], s * kDeep, row, fb);
+                        load_box(b, &maps.b[rank], s * kDeep, col, fb);
                     } else {
-                        load_box(a, am, k, row, fb);
-                    }
-                    if (kAcrossB) {
+                        int k = s * kDeep;
+                        const CUtensorMap* bm = &maps.b[2];
+                        if (t.result == 0) {       // dg and Wg, then du and Wu
+                            const int half = pl.of[0].stages / 2, second = s >= half;
+                            k -= second * half * kDeep;
+                            bm = &maps.b[second];
+                            load_box(a, &maps.a[second], k, row, fb);
+                        } else {
+                            const CUtensorMap* am = &maps.a[1 + t.result];
+                            load_box(a, am, row, k, fb);
+                            load_box(a + kDeep * kLineBytes, am, row + 64, k, fb);
+                        }
 #pragma unroll
                         for (int c = 0; c < BN / 2; c += 64)
                             load_box(b + c / 64 * (kDeep * kLineBytes), bm, col + c, k, fb);
-                    } else {
-                        load_box(b, bm, k, col, fb);
                     }
                     ++issued;
                     ring.next();
@@ -370,17 +399,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (rank == 0 && elect_one()) {
             constexpr uint32_t kLead = kDeep * kLineBytes;
             // Sixteen of the contraction: 32 bytes of a line, or 16 lines.
-            constexpr uint32_t kStepA = (kAcrossA ? 16 * kLineBytes : 32) / 16;
-            constexpr uint32_t kStepB = (kAcrossB ? 16 * kLineBytes : 32) / 16;
-            const uint64_t a_desc = line_desc(smem0, kAcrossA ? kLead : 0);
-            const uint64_t b_desc = line_desc(smem0 + kHalfA<BN>, kAcrossB ? kLead : 0);
+            constexpr uint32_t kAlong = 32 / 16, kAcross = 16 * kLineBytes / 16;
+            constexpr uint32_t kStepB = MODE == kForward ? kAlong : kAcross;
+            const uint64_t a_along = line_desc(smem0, 0), a_across = line_desc(smem0, kLead);
+            const uint64_t b_desc = line_desc(smem0 + kHalfA<BN>, MODE == kForward ? 0 : kLead);
             constexpr bool kIsBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
-            constexpr uint32_t idesc = ff_idesc(kIsBf16, BN, kAcrossA, kAcrossB);
             Ring<N_STAGES> ring;
-            int n = 0;
             bool ready = false, ok = true;
-            for (int i = start; i < items && ok; i += pairs, ++n) {
-                const Item t = item_at<MODE, BN>(pl, i);
+            for (int n = 0; n < share.count && ok; ++n) {
+                const Item t = share.at(pl, n);
+                const bool across = t.result > 0;          // the contraction runs across dg's rows
+                const uint64_t a_desc = across ? a_across : a_along;
+                const uint32_t step_a = across ? kAcross : kAlong;
+                const uint32_t idesc = across ? ff_idesc(kIsBf16, BN, true, true)
+                                              : ff_idesc(kIsBf16, BN, false, MODE != kForward);
                 const uint32_t sums = tmem + (n & 1) * BN;
                 // The item before the last one has left this set of sums (first: at once).
                 if (!pipe_wait<true>(su32(&free_bar[n & 1]), ((n >> 1) & 1) ^ 1u, abort_flag,
@@ -401,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     const uint32_t at = ring.stage * (kStage<BN> / 16);
 #pragma unroll
                     for (int k = 0; k < kDeep / 16; ++k)
-                        ff_mma(sums, a_desc + at + k * kStepA, b_desc + at + k * kStepB, idesc,
+                        ff_mma(sums, a_desc + at + k * step_a, b_desc + at + k * kStepB, idesc,
                                s != t.first || k != 0);
                     commit<2>(su32(&empty_bar[ring.stage]));
                     ring = ahead;
@@ -412,18 +444,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t staged = smem0 + N_STAGES * kStage<BN> + (warp - 2) * kStaged;
-        int n = 0;
-        for (int i = start; i < items; i += pairs, ++n) {
+        for (int n = 0; n < share.count; ++n) {
             // All four warps of this half go on, or none.
             const bool ok = all_of_group(
                 1 + half, pipe_wait(su32(&done_bar[n & 1]), (n >> 1) & 1, abort_flag, pl.status) &&
                               !*abort_flag);
             if (!ok) break;
             fence_after();
-            const Item t = item_at<MODE, BN>(pl, i);
+            const Item t = share.at(pl, n);
+            const Result& to = pl.to[MODE == kForward ? 0 : t.result];
+            const Product& of = pl.of[MODE == kForward ? 0 : t.result > 0];
             const uint32_t sums = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + (n & 1) * BN;
             const long long row = t.row + rank * (kRows / 2) + 32 * quarter;
-            const int rows = static_cast<int>(max(0LL, min(32LL, pl.rows - row)));
+            const int rows = static_cast<int>(max(0LL, min(32LL, of.rows - row)));
             auto done_reading = [&] {
                 fence_before();
                 __syncwarp();
@@ -437,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     tmem_get<kCols>(sums + half * kCols, g);
                     tmem_get<kCols>(sums + BN / 2 + half * kCols, u);
                     done_reading();
-                    const int col = t.col + half * kCols, cols = pl.cols - col;
+                    const int col = t.col + half * kCols, cols = of.cols - col;
                     if (rows == 0 || cols <= 0) continue;
                     if (kept.keep == kKeepFull) {
                         put_rows<T, kCols>(staged, g, static_cast<uint8_t*>(kept.gate) +
@@ -449,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     }
                     if constexpr (kCols == 64) {
                         if (kept.keep == kKeep8) {
-                            const long long pitch = act8_pitch(pl.cols);
+                            const long long pitch = act8_pitch(of.cols);
                             put_codes(staged, g, static_cast<int8_t*>(kept.gate), kept.gate_scales,
                                       pitch, row, col, rows, lane);
                             put_codes(staged, u, static_cast<int8_t*>(kept.up), kept.up_scales,
@@ -459,8 +492,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) g[j] = act<ACT>(g[j]) * u[j];
                     put_rows<T, kCols>(staged, g,
-                                       static_cast<uint8_t*>(pl.c[0]) + (row * pl.ldc[0] + col) * 2,
-                                       pl.ldc[0], rows, cols, pl.c_vec, lane);
+                                       static_cast<uint8_t*>(to.c) + (row * to.ld + col) * 2, to.ld,
+                                       rows, cols, to.vec, lane);
                 }
             } else {
 #pragma unroll 1
@@ -468,12 +501,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     float v[64];
                     tmem_get<64>(sums + c, v);
                     if (c + 64 == (half + 1) * (BN / 2)) done_reading();
-                    const int col = t.col + c, cols = pl.cols - col;
+                    const int col = t.col + c, cols = of.cols - col;
                     if (rows == 0 || cols <= 0) continue;
-                    if (pl.partial) {
+                    if (to.partial) {
                         // One part's fp32 sums, 32 columns at a time.
-                        const long long set = MODE == kWeights ? 2 * t.part + t.matrix : t.part;
-                        float* to = pl.partial + (set * pl.rows + row) * pl.partial_ld + col;
+                        float* at = to.partial +
+                                    (static_cast<long long>(t.part) * of.rows + row) * pl.partial_ld + col;
 #pragma unroll
                         for (int half = 0; half < 64; half += 32) {
 #pragma unroll
@@ -483,16 +516,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                                      __float_as_uint(v[half + j + 1]),
                                                      __float_as_uint(v[half + j + 2]),
                                                      __float_as_uint(v[half + j + 3])));
-                            store_staged<8>(staged, reinterpret_cast<uint8_t*>(to + half),
+                            store_staged<8>(staged, reinterpret_cast<uint8_t*>(at + half),
                                             4 * pl.partial_ld, rows, 128, true, lane);
                         }
                         continue;
                     }
-                    const long long ld = pl.ldc[MODE == kWeights ? t.matrix : 0];
-                    put_rows<T, 64>(staged, v,
-                                    static_cast<uint8_t*>(pl.c[MODE == kWeights ? t.matrix : 0]) +
-                                        (row * ld + col) * 2,
-                                    ld, rows, cols, pl.c_vec, lane);
+                    put_rows<T, 64>(staged, v, static_cast<uint8_t*>(to.c) + (row * to.ld + col) * 2, to.ld,
+                                    rows, cols, to.vec, lane);
                 }
             }
         }
@@ -509,31 +539,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 template <typename T, int MODE, int BN, int ACT>
-cudaError_t launch_pair(const PairMaps& maps, const PairPlan& pl, int sms, cudaStream_t stream) {
+cudaError_t launch_pair(const PairMaps& maps, const PairPlan& pl, cudaStream_t stream) {
     auto kernel = ff_pair_kernel<T, MODE, BN, ACT>;
     const cudaError_t e = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem<BN>);
     if (e != cudaSuccess) return e;
-    const long long items = static_cast<long long>(pl.tiles_m) * pl.tiles_n * pl.split;
-    if (items > 0x7FFFFFFF / kGroup) return cudaErrorInvalidConfiguration;
-    const unsigned grid = 2 * static_cast<unsigned>(std::min<long long>(sms / 2, items));
-    return launch_dependent(kernel, dim3(grid), kPairThreads, kPairSmem<BN>, stream, maps, pl);
+    return launch_dependent(kernel, dim3(2 * pl.pairs), kPairThreads, kPairSmem<BN>, stream, maps, pl);
 }
 template <typename T>
 cudaError_t launch_pair_of(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int activation,
-                           int sms, cudaStream_t st) {
+                           cudaStream_t st) {
+    // Items are counted in 32 bits.
+    if (pl.of[0].items() + pl.of[1].items() > 0x7FFFFFFF / kGroup) return cudaErrorInvalidConfiguration;
     if (mode == kForward) {
         if (activation == kSilu)
-            return bn == 256 ? launch_pair<T, kForward, 256, kSilu>(maps, pl, sms, st)
-                             : launch_pair<T, kForward, 128, kSilu>(maps, pl, sms, st);
-        return bn == 256 ? launch_pair<T, kForward, 256, kGeluTanh>(maps, pl, sms, st)
-                         : launch_pair<T, kForward, 128, kGeluTanh>(maps, pl, sms, st);
+            return bn == 256 ? launch_pair<T, kForward, 256, kSilu>(maps, pl, st)
+                             : launch_pair<T, kForward, 128, kSilu>(maps, pl, st);
+        return bn == 256 ? launch_pair<T, kForward, 256, kGeluTanh>(maps, pl, st)
+                         : launch_pair<T, kForward, 128, kGeluTanh>(maps, pl, st);
     }
-    if (mode == kInput)
-        return bn == 256 ? launch_pair<T, kInput, 256, kSilu>(maps, pl, sms, st)
-                         : launch_pair<T, kInput, 128, kSilu>(maps, pl, sms, st);
-    return bn == 256 ? launch_pair<T, kWeights, 256, kSilu>(maps, pl, sms, st)
-                     : launch_pair<T, kWeights, 128, kSilu>(maps, pl, sms, st);
+    return bn == 256 ? launch_pair<T, kBackward, 256, kSilu>(maps, pl, st)
+                     : launch_pair<T, kBackward, 128, kSilu>(maps, pl, st);
 }
 
 }  // namespace ff

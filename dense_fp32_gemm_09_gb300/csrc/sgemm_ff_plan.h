@@ -9,32 +9,44 @@
 namespace sgemm {
 namespace ff {
 
-enum : int { kForward = 0, kInput = 1, kWeights = 2 };
+enum : int { kForward = 0, kBackward = 1 };
 constexpr int kTileRows = 256;
 
-// A parameter of its own: its address is taken, and if it were the plan's, the plan would be
-// read again after every store.
+// Forward: a[0] x, b[0] Wg, b[1] Wu.  Backward: a[0], a[1] dg, du read along their rows, a[2], a[3]
+// across them, b[0] Wg, b[1] Wu, b[2] x.  A parameter of its own: its address is taken, and if it
+// were the plan's, the plan would be read again after every store.
 struct PairMaps {
-    CUtensorMap a[2], b[2];
+    CUtensorMap a[4], b[3];
 };
-struct PairPlan {
-    int rows, cols;            // of the result
-    int tiles_m, tiles_n;      // (gradient of weights: dWg's tiles of rows, then dWu's)
+// Forward: h.  Backward: dx; and dWg with dWu, one product whose tiles of rows follow each other.
+struct Product {
+    int rows, cols;            // of a result
+    int tiles_m, tiles_n;
     int stages;                // of a tile's contraction, 64 each (both halves of dx's)
     int split;                 // parts of a tile's contraction
-    void* c[2];
-    long long ldc[2];
-    int c_vec, kept_vec;       // 1: rows start on 16 bytes
-    FfKept kept;
-    float* partial;            // split > 1: [part][matrix of the result][rows][partial_ld]
+    long long items() const { return static_cast<long long>(tiles_m) * tiles_n * split; }
+};
+struct Result {
+    void* c;
+    long long ld;
+    int vec;                   // 1: rows start on 16 bytes
+    float* partial;            // split > 1: [part][rows][partial_ld]
+};
+struct PairPlan {
+    Product of[2];
+    Result to[3];              // h; or dx, dWg, dWu
     long long partial_ld;
+    int pairs;                 // that share the items
+    int extra;                 // items of the second product by which pairs with fewer of the first lead
+    FfKept kept;
+    int kept_vec;              // 1: rows start on 16 bytes
     int* status;
 };
 
 cudaError_t pair_bf16(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int activation,
-                      int sms, cudaStream_t stream);
+                      cudaStream_t stream);
 cudaError_t pair_f16(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int activation,
-                     int sms, cudaStream_t stream);
+                     cudaStream_t stream);
 // Forward of up to 16 tokens, without 8-bit checkpoints (sgemm_ff_token.cu); operands on 16 bytes, on32: on 32.
 cudaError_t launch_token(const GatedFfForward& p, bool on32, int sms, cudaStream_t stream);
 

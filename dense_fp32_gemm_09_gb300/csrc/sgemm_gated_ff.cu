@@ -17,8 +17,8 @@
 //
 // Measured (us, kernels alone): forward 8192 x 4096 x 8192 bf16 527 to 550 (2.0 to 2.1 PFLOP/s; the
 // measured rate of a library product is 1.9, sustained 1.7), with g and u kept in 8 bits 546; the
-// gradient 1330 to 1350, of it 122 for ff_gradient (0.8 of the memory).  500 x 1024 x 4096 11.9 and
-// 28, 16384 x 256 x 64 backward 18 to 23.
+// gradient 1223 to 1249, of it 122 for ff_gradient (0.8 of the memory).  500 x 1024 x 4096 12.1 and
+// 25.2, 16384 x 256 x 64 backward 16.2.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -161,32 +161,35 @@ __global__ void __launch_bounds__(kThreads) ff_copy_rows(const Copies q) {
     }
 }
 
-// A product's parts, added in their order; four columns a thread, blockIdx.y: the matrix of the
-// result.
+// The parts of split products, added in their order; four columns a thread, blockIdx.y: which of
+// the results.
 struct Parts {
-    const float* partial;            // [part][matrix][rows][ld]
+    struct One {
+        const float* partial;        // [part][rows][ld]
+        int split, rows;
+        void* to;
+        long long ldto;
+    } of[3];
     long long ld;
-    int split, matrices, rows, cols;
-    void* to[2];
-    long long ldto[2];
+    int cols;
 };
 template <typename T>
 __global__ void __launch_bounds__(kThreads) ff_add_parts(const Parts q) {
-    const int m = blockIdx.y;
+    const Parts::One& one = q.of[blockIdx.y];
     act8::Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x,
                   static_cast<long long>(gridDim.x) * kThreads, (q.cols + 3) / 4);
     start_dependent();
-    for (; at.row < q.rows; at.next()) {
+    for (; at.row < one.rows; at.next()) {
         const int c = at.col * 4;
         float4 s = make_float4(0, 0, 0, 0);
 #pragma unroll 4
-        for (int k = 0; k < q.split; ++k) {
+        for (int k = 0; k < one.split; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(
-                q.partial + ((k * static_cast<long long>(q.matrices) + m) * q.rows + at.row) * q.ld + c);
+                one.partial + (static_cast<long long>(k) * one.rows + at.row) * q.ld + c);
             s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
         }
         const float v[4] = {s.x, s.y, s.z, s.w};
-        T* const to = static_cast<T*>(q.to[m]) + at.row * q.ldto[m] + c;
+        T* const to = static_cast<T*>(one.to) + at.row * one.ldto + c;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (c + j < q.cols) to[j] = from_float<T>(v[j]);
@@ -220,27 +223,57 @@ FfChoice choose_forward(int M, int N, int K, int keep) {
     }
     return best;
 }
-// Few tiles share a contraction between up to sixteen pairs, eight stages each at least; their sums
-// take another pass over the result.
-FfChoice choose_split(long long tiles_of_rows, long long results, int cols, long long stages) {
-    FfChoice best{256, 1};
-    double least = 0;
-    for (int bn : {256, 128}) {
-        const long long tiles = tiles_of_rows * up_to(cols, bn);
-        for (int split = 1; split <= 16 && (split == 1 || stages / split >= 8); ++split) {
-            const double rounds = static_cast<double>(up_to(tiles * split, kPairsOfGpu));
-            double t = rounds * (up_to(stages, split) * stage_clocks(bn) + 12.0 * bn);
-            if (split > 1) t += 5000 + 8.0 * results * split / 2500;
-            if (least == 0 || t < least) best = {bn, split}, least = t;
-        }
+double item_clocks(long long stages, int bn) { return static_cast<double>(stages) * stage_clocks(bn) + 12.0 * bn; }
+// n items of `one` clocks each and m of `two` on `pairs` pairs (Share in sgemm_ff_pair.cuh): how many of
+// the second kind pairs with fewer of the first lead by, and how long all take.
+struct Spread {
+    int extra;
+    double clocks;
+};
+Spread spread(long long n, long long m, double one, double two, long long pairs) {
+    const long long more = n % pairs, few = more ? pairs - more : 0;
+    const double whole = static_cast<double>(n / pairs) * one;
+    Spread best{0, -1.0};
+    const long long least = few ? std::min(static_cast<long long>(one / two), m / few) : 0;
+    for (long long e = least; e <= least + 1 && e * few <= m; ++e) {
+        const long long rounds = (m - e * few) / pairs, left = (m - e * few) % pairs;
+        double t = whole + (e + rounds + (left > 0)) * two;
+        if (few) t = std::max(t, whole + one + (rounds + (left > few)) * two);
+        if (best.clocks < 0 || t < best.clocks) best = {static_cast<int>(e), t};
+        if (!few) break;
     }
     return best;
 }
-FfChoice choose_input(int M, int N, int K) {
-    return choose_split(up_to(M, kTileRows), static_cast<long long>(M) * K, K, 2 * up_to(N, 64));
-}
-FfChoice choose_weights(int M, int N, int K) {
-    return choose_split(2 * up_to(N, kTileRows), 2LL * N * K, K, up_to(M, 64));
+// Gradient: one launch for dx and the weights' gradients, so that few tiles of one leave pairs for
+// the other.  Few tiles share a contraction between up to sixteen pairs, eight stages each at
+// least and no more than two rounds of them; their sums take another pass over the results.
+// Measured (us, tokens x outputs x inputs, two launches and one): 500 x 4096 x 1024 28.7, 25.2;
+// 1000 x 1024 x 1024 19.0, 13.9; 2000 x 2048 x 512 29.3, 22.0; 8192 x 8192 x 4096 1330, 1249.  Of all
+// tiles and parts the model's choice was the fastest, or within 5 % of it, on 21 of 22 shapes
+// (one token, 4096 x 4096: 47.0, where four parts of dx and tiles of 256 take 38.6).
+struct Gradients {
+    int bn, split_x, split_w;
+};
+Gradients choose_gradients(int M, int N, int K) {
+    Gradients best{256, 1, 1};
+    double least = 0;
+    const long long deep_x = 2 * up_to(N, 64), deep_w = up_to(M, 64);
+    for (int bn : {256, 128}) {
+        const long long x = up_to(M, kTileRows) * up_to(K, bn), w = 2 * up_to(N, kTileRows) * up_to(K, bn);
+        const auto parts = [](int split, long long tiles, long long stages) {
+            return split == 1 || (split <= 16 && stages / split >= 8 && tiles * split <= 2 * kPairsOfGpu);
+        };
+        for (int i = 1; parts(i, x, deep_x); ++i) {
+            for (int j = 1; parts(j, w, deep_w); ++j) {
+                double t = spread(x * i, w * j, item_clocks(up_to(deep_x, i), bn),
+                                  item_clocks(up_to(deep_w, j), bn), kPairsOfGpu).clocks;
+                const double added = (i > 1 ? 1.0 * i * M : 0) + (j > 1 ? 2.0 * j * N : 0);
+                if (added > 0) t += 5000 + 8 * added * K / 2500;
+                if (least == 0 || t < least) best = {bn, i, j}, least = t;
+            }
+        }
+    }
+    return best;
 }
 
 // A matrix of 2-byte numbers, boxes of 64 columns by `box` rows, zeros outside.
@@ -299,10 +332,9 @@ struct Operands {
 };
 
 template <typename T>
-cudaError_t pair(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int act, int sms,
-                 cudaStream_t st) {
-    return std::is_same<T, __half>::value ? pair_f16(maps, pl, mode, bn, act, sms, st)
-                                          : pair_bf16(maps, pl, mode, bn, act, sms, st);
+cudaError_t pair(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int act, cudaStream_t st) {
+    return std::is_same<T, __half>::value ? pair_f16(maps, pl, mode, bn, act, st)
+                                          : pair_bf16(maps, pl, mode, bn, act, st);
 }
 
 template <typename T>
@@ -328,22 +360,16 @@ cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* laun
         !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, c.bn / 2) ||
         !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, c.bn / 2))
         return cudaErrorInvalidValue;
-    maps.a[1] = maps.a[0];
     PairPlan pl{};
-    pl.rows = p.M;
-    pl.cols = p.N;
-    pl.tiles_m = static_cast<int>(up_to(p.M, kTileRows));
-    pl.tiles_n = static_cast<int>(up_to(p.N, c.bn / 2));
-    pl.stages = static_cast<int>(up_to(p.K, 64));
-    pl.split = 1;
-    pl.c[0] = p.h;
-    pl.ldc[0] = p.ldh;
-    pl.c_vec = on16(p.h, p.M, p.ldh);
+    pl.of[0] = {p.M, p.N, static_cast<int>(up_to(p.M, kTileRows)), static_cast<int>(up_to(p.N, c.bn / 2)),
+                static_cast<int>(up_to(p.K, 64)), 1};
+    pl.pairs = static_cast<int>(std::min<long long>(sms / 2, pl.of[0].items()));
+    pl.to[0] = {p.h, p.ldh, on16(p.h, p.M, p.ldh), nullptr};
     pl.kept = p.kept;
     pl.kept_vec = on16(p.kept.gate, p.M, p.kept.ld) && on16(p.kept.up, p.M, p.kept.ld);
     pl.status = status_word_ptr();
     ++*launches;
-    return pair<T>(maps, pl, kForward, c.bn, p.activation, sms, st);
+    return pair<T>(maps, pl, kForward, c.bn, p.activation, st);
 }
 
 template <typename T, int ACT>
@@ -359,16 +385,24 @@ cudaError_t gradient(const GatedFfBackward& p, T* dg, T* du, long long pitch, in
                : launch_dependent(ff_gradient<T, ACT, false>, grid, kThreads, 0, st, p, dg, du, pitch, on);
 }
 
-// The second half of a product whose tiles were split.
+// The second half of products whose tiles were split.
 template <typename T>
-cudaError_t add_parts(const PairPlan& pl, int matrices, int sms, cudaStream_t st, int* launches) {
-    if (!pl.partial) return cudaSuccess;
-    const Parts q{pl.partial, pl.partial_ld, pl.split, matrices, pl.rows, pl.cols,
-                  {pl.c[0], pl.c[1]}, {pl.ldc[0], pl.ldc[1]}};
-    const long long blocks = up_to(pl.rows * up_to(pl.cols, 4), kThreads);
+cudaError_t add_parts(const PairPlan& pl, int sms, cudaStream_t st, int* launches) {
+    Parts q{};
+    int n = 0, rows = 0;
+    for (int i = 0; i < 3; ++i) {
+        const Product& of = pl.of[i > 0];
+        if (!pl.to[i].partial) continue;
+        q.of[n++] = {pl.to[i].partial, of.split, of.rows, pl.to[i].c, pl.to[i].ld};
+        rows = std::max(rows, of.rows);
+    }
+    if (n == 0) return cudaSuccess;
+    q.ld = pl.partial_ld;
+    q.cols = pl.of[0].cols;
+    const long long blocks = up_to(rows * up_to(q.cols, 4), kThreads);
     ++*launches;
     return launch_dependent(ff_add_parts<T>,
-                            dim3(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL)), matrices),
+                            dim3(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL)), n),
                             kThreads, 0, st, q);
 }
 
@@ -399,49 +433,37 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
     PairMaps maps;
     PairPlan pl{};
     pl.status = status_word_ptr();
-    // dx, from dg and Wg, then du and Wu.
-    const FfChoice ci = choose_input(p.M, p.N, p.K);
+    // dx, from dg and Wg, then du and Wu; dWg and dWu.
+    const Gradients c = choose_gradients(p.M, p.N, p.K);
     if (!encode(&maps.a[0], dg, p.M, p.N, pitch, 128) || !encode(&maps.a[1], du, p.M, p.N, pitch, 128) ||
+        !encode(&maps.a[2], dg, p.M, p.N, pitch, 64) || !encode(&maps.a[3], du, p.M, p.N, pitch, 64) ||
         !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, 64) ||
-        !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, 64))
+        !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, 64) ||
+        !encode(&maps.b[2], in.x, p.M, p.K, in.ldx, 64))
         return cudaErrorInvalidValue;
-    pl.rows = p.M;
-    pl.cols = p.K;
-    pl.tiles_m = static_cast<int>(up_to(p.M, kTileRows));
-    pl.tiles_n = static_cast<int>(up_to(p.K, ci.bn));
-    pl.stages = static_cast<int>(2 * up_to(p.N, 64));
-    pl.split = ci.split;
-    pl.c[0] = p.dx;
-    pl.ldc[0] = p.lddx;
-    pl.c_vec = on16(p.dx, p.M, p.lddx);
-    pl.partial = ci.split > 1 ? reinterpret_cast<float*>(in.at) : nullptr;
+    const int tiles_n = static_cast<int>(up_to(p.K, c.bn));
+    pl.of[0] = {p.M, p.K, static_cast<int>(up_to(p.M, kTileRows)), tiles_n,
+                static_cast<int>(2 * up_to(p.N, 64)), c.split_x};
+    pl.of[1] = {p.N, p.K, static_cast<int>(2 * up_to(p.N, kTileRows)), tiles_n,
+                static_cast<int>(up_to(p.M, 64)), c.split_w};
+    pl.pairs = static_cast<int>(std::min<long long>(sms / 2, pl.of[0].items() + pl.of[1].items()));
+    pl.extra = spread(pl.of[0].items(), pl.of[1].items(), item_clocks(up_to(pl.of[0].stages, c.split_x), c.bn),
+                      item_clocks(up_to(pl.of[1].stages, c.split_w), c.bn), pl.pairs).extra;
+    pl.to[0] = {p.dx, p.lddx, on16(p.dx, p.M, p.lddx), nullptr};
+    pl.to[1] = {p.dw_gate, p.lddwg, on16(p.dw_gate, p.N, p.lddwg), nullptr};
+    pl.to[2] = {p.dw_up, p.lddwu, on16(p.dw_up, p.N, p.lddwu), nullptr};
     pl.partial_ld = up64(p.K);
-    e = pair<T>(maps, pl, kInput, ci.bn, p.activation, sms, st);
+    float* partial = reinterpret_cast<float*>(in.at);
+    for (int i = 0; i < 3; ++i) {
+        const Product& of = pl.of[i > 0];
+        if (of.split == 1) continue;
+        pl.to[i].partial = partial;
+        partial += of.split * (of.rows * pl.partial_ld);
+    }
+    e = pair<T>(maps, pl, kBackward, c.bn, p.activation, st);
     if (e != cudaSuccess) return e;
     ++*launches;
-    e = add_parts<T>(pl, 1, sms, st, launches);
-    if (e != cudaSuccess) return e;
-    // dWg, then dWu.
-    const FfChoice cw = choose_weights(p.M, p.N, p.K);
-    if (!encode(&maps.a[0], dg, p.M, p.N, pitch, 64) || !encode(&maps.a[1], du, p.M, p.N, pitch, 64) ||
-        !encode(&maps.b[0], in.x, p.M, p.K, in.ldx, 64))
-        return cudaErrorInvalidValue;
-    maps.b[1] = maps.b[0];
-    pl.rows = p.N;
-    pl.tiles_m = static_cast<int>(2 * up_to(p.N, kTileRows));
-    pl.tiles_n = static_cast<int>(up_to(p.K, cw.bn));
-    pl.stages = static_cast<int>(up_to(p.M, 64));
-    pl.split = cw.split;
-    pl.partial = cw.split > 1 ? reinterpret_cast<float*>(in.at) : nullptr;     // (dx's are used up)
-    pl.c[0] = p.dw_gate;
-    pl.c[1] = p.dw_up;
-    pl.ldc[0] = p.lddwg;
-    pl.ldc[1] = p.lddwu;
-    pl.c_vec = on16(p.dw_gate, p.N, p.lddwg) && on16(p.dw_up, p.N, p.lddwu);
-    e = pair<T>(maps, pl, kWeights, cw.bn, p.activation, sms, st);
-    if (e != cudaSuccess) return e;
-    ++*launches;
-    return add_parts<T>(pl, 2, sms, st, launches);
+    return add_parts<T>(pl, sms, st, launches);
 }
 
 // Copies of the operands that are not read in place.
@@ -457,17 +479,18 @@ int packed_bit(int bit, const void* p, long long rows, long long ld) {
 }  // namespace
 
 FfChoice choose_gated_ff(int product, int M, int N, int K, int keep) {
-    return product == kProductForward ? choose_forward(M, N, K, keep)
-           : product == kProductInput ? choose_input(M, N, K) : choose_weights(M, N, K);
+    if (product == kProductForward) return choose_forward(M, N, K, keep);
+    const Gradients c = choose_gradients(M, N, K);
+    return FfChoice{c.bn, product == kProductInput ? c.split_x : c.split_w};
 }
 size_t gated_ff_forward_workspace(int M, int N, int K, int packed) {
     return copied_bytes(M, N, K, packed);
 }
 size_t gated_ff_backward_workspace(int M, int N, int K, int packed) {
-    const auto parts = [](const FfChoice& c, size_t result) { return c.split > 1 ? c.split * result : 0; };
-    const size_t dx = parts(choose_input(M, N, K), 2 * matrix_bytes(M, K));          // fp32
-    const size_t dw = parts(choose_weights(M, N, K), 4 * matrix_bytes(N, K));
-    return 2 * static_cast<size_t>(matrix_bytes(M, N)) + copied_bytes(M, N, K, packed) + std::max(dx, dw);
+    const Gradients c = choose_gradients(M, N, K);
+    const long long parts = (c.split_x > 1 ? 1LL * c.split_x * M : 0) + (c.split_w > 1 ? 2LL * c.split_w * N : 0);
+    return 2 * static_cast<size_t>(matrix_bytes(M, N)) + copied_bytes(M, N, K, packed) +
+           static_cast<size_t>(parts * up64(K)) * sizeof(float);
 }
 int gated_ff_packed(const GatedFfForward& p) {
     return packed_bit(1, p.x, p.M, p.ldx) | packed_bit(2, p.w_gate, p.N, p.ldg) |

@@ -28,15 +28,15 @@ def test_choices_fit(lib):
                     columns, parts = choice(lib, M, N, K, keep, FORWARD)
                     assert parts == 1
                     assert columns == 256 if keep == EIGHT else (columns == 0) == (M <= 16)
-                most = 0
+                sums = 0
                 for product, stages, result in ((INPUT, 2 * -(-N // 64), M * -(-K // 64) * 64),
                                                 (WEIGHTS, -(-M // 64), 2 * N * -(-K // 64) * 64)):
                     columns, parts = choice(lib, M, N, K, FULL, product)
                     assert columns in (128, 256) and 1 <= parts <= 16
                     assert parts == 1 or stages // parts >= 8
-                    most = max(most, parts * 4 * result if parts > 1 else 0)
+                    sums += parts * 4 * result if parts > 1 else 0
                 assert lib.sgemm_gated_ff_workspace(M, N, K, 1, 0, ctypes.byref(need)) == 0
-                assert need.value == 4 * M * -(-N // 64) * 64 + most
+                assert need.value == 4 * M * -(-N // 64) * 64 + sums
 
 
 def test_every_kind_is_run_by_the_gpu_tests(lib):

@@ -24,7 +24,7 @@ SHAPES = [(1, 1, 1), (1, 8, 16), (3, 5, 7), (1, 1000, 200), (8, 333, 257), (16, 
 # Several rounds of tiles, every tile and split (test_gated_ff_choice.py).
 MANY = [(2600, 2100, 200), (4700, 2600, 72), (1000, 4100, 520), (900, 100, 6000), (9000, 64, 300),
         (40, 3000, 520), (3000, 40, 520), (20000, 260, 250), (12000, 500, 1000),
-        (30000, 512, 512)]
+        (30000, 512, 512), (700, 8192, 700), (30, 8200, 4100)]
 
 
 @pytest.fixture()
