@@ -89,13 +89,17 @@ __device__ __forceinline__ uint32_t block_amax(uint32_t amax) {
     for (int o = 1; o < LANES; o *= 2) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     return amax;
 }
-// Four codes to two pairs: 2^23 + (code + 128) has the code's bits in its last byte.
-__device__ __forceinline__ void values4(uint32_t codes, float scale, Two (&v)[2]) {
+// The first (which = 0) or second two of four codes, each times its scale: 2^23 + (code + 128) has
+// the code's bits in its last byte.
+__device__ __forceinline__ Two values2(uint32_t codes, int which, Two by) {
     const uint32_t u = codes ^ 0x80808080u;
-    const Two less = mx4::twice(-8388736.0f), by = mx4::twice(scale);
     const auto whole = [&](int i) { return __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + i)); };
-    v[0] = mx4::mul(add(mx4::two(whole(0), whole(1)), less), by);
-    v[1] = mx4::mul(add(mx4::two(whole(2), whole(3)), less), by);
+    return mx4::mul(add(mx4::two(whole(2 * which), whole(2 * which + 1)), mx4::twice(-8388736.0f)), by);
+}
+__device__ __forceinline__ void values4(uint32_t codes, float scale, Two (&v)[2]) {
+    const Two by = mx4::twice(scale);
+    v[0] = values2(codes, 0, by);
+    v[1] = values2(codes, 1, by);
 }
 __device__ __forceinline__ float value(int8_t code, float scale) {
     return static_cast<float>(code) * scale;

@@ -15,6 +15,8 @@
 //     a ring of shared-memory stages, ragged ones (widths, strides or addresses that are not whole
 //     16-byte groups) into registers, one row ahead; rows too wide for a team are split over a
 //     cluster of two to eight blocks;
+//   * both: many wide rows of 2-byte numbers that are ragged alike, by blocks that take rows which
+//     begin at one place of a 16-byte group, in whole groups of the memory;
 //   * below, for rows too wide for either: streaming kernels, and the sums over rows in strips.
 // Sums over rows: a block adds its rows' in their order, and a second kernel adds the blocks' in
 // theirs, so two runs give the same bits.  (The order of a row's sums depends on the kernel.)
@@ -24,7 +26,8 @@
 // input kept in 8 bits too 8192 x 8192 bf16 73 (0.68), 3001 x 2047 fp32 14 (0.58); streaming, 4096 x 16384
 // fp32 123 (0.64).  Gradient, with dy: 8192 x 8192 bf16 92 (0.86), 8192 x 4096 bf16 51.5 (0.77) and fp32
 // 84 (0.94), 8192 x 1024 bf16 19.5 (0.51), 4096 x 16384 bf16 136 (0.58), 3001 x 2047 fp32 22.3 (0.65);
-// from a checkpoint 8192 x 4096 bf16 57 (0.61), 3001 x 2047 fp32 20.9 (0.57).  The gradient of 2-byte
+// from a checkpoint 8192 x 4096 bf16 57 (0.61), 3001 x 2047 fp32 20.9 (0.57); ragged 3001 x 5001 bf16
+// forward 19.9 (0.44), gradient 49 (0.36).  The gradient of 2-byte
 // rows holds 16 warps an SM at 128 registers with issue slots half used: neither memory nor issue
 // is full, which reads as latency.  A first pass over the next row between a row's two (its
 // numbers read from the ring twice, none kept in registers over the barrier) was slower: 8192 x 4096
@@ -225,32 +228,58 @@ __global__ void __launch_bounds__(1024) layer_norm_columns(const LayerNormBackwa
 using layer_norm::kByBlock;
 using layer_norm::kByWarp;
 using layer_norm::kWide;
+using layer_norm::kShifted;
+using layer_norm::kSingle;
+using layer_norm::kWhole;
 using layer_norm::Shape;
+using layer_norm::whole_steps;
 
-// Whether every row (one a call has no stride to speak of) and vector is on 16 bytes.
+// Where the rows of a call's matrices begin in 16-byte groups of memory (one row a call has no stride
+// to speak of): all at the start of one, with vectors that do too; or every row of all of them
+// at the same place; or neither.
 struct Alignment {
-    bool whole = true;
+    bool whole, same = true, any = false;
     long long rows;
-    int elem;
+    int elem, base = 0, step = 0;
     Alignment(int dtype, long long r, int cols) : rows(r), elem(dtype == kF32 ? 4 : 2) {
         whole = static_cast<long long>(cols) * elem % 16 == 0;
     }
     void add(const void* p, long long ld) {
         if (p == nullptr) return;
-        whole &= reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld * elem % 16 == 0);
+        const int at = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16);
+        const int by = rows > 1 ? static_cast<int>(ld * elem % 16) : 0;
+        whole &= at == 0 && by == 0;
+        same &= !any || (at == base && by == step);
+        any = true;
+        base = at;
+        step = by;
+    }
+    void add_vector(const void* p) { whole &= reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+    // Shifted: 2-byte rows of more than 4096 numbers, more than two an SM.  In us, bf16, against single
+    // columns: 3001 x 5001 forward 19.9, 30.8, gradient 49.0, 84.3; 16000 x 8191 110, 171 and 314, 448;
+    // but 3001 x 2047 gradient 22.0, 19.3; 300 x 8001 forward 5.9, 5.3; 10 x 8001 gradient 8.8, 6.6.
+    int access(int cols, int sms) const {
+        return whole ? kWhole : same && elem == 2 && cols > 8 * 512 && rows > 2LL * sms ? kShifted : kSingle;
+    }
+    int period() const {
+        int n = 1;
+        while (step * n % 16) n *= 2;
+        return n;
     }
 };
 // A block a row, `own` columns a thread; up to `most` threads an SM.
-Shape by_block(long long rows, int cols, int own, int most, bool ragged, int sms, bool keeps = false) {
+Shape by_block(long long rows, int cols, int own, int most, int access, int period, int sms,
+               bool keeps = false) {
     Shape s{};
     s.keeps = keeps;
     s.kind = kByBlock;
-    s.ragged = ragged;
+    s.access = access;
+    s.period = period;
     s.columns = own;
     s.threads = 32;
     while (s.threads * own < cols) s.threads *= 2;
     const int per = std::min(most / s.threads, 16);
-    s.grid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * per));
+    s.grid = whole_steps(static_cast<int>(std::min<long long>(rows, static_cast<long long>(sms) * per)), period, rows);
     return s;
 }
 
@@ -258,17 +287,19 @@ Shape forward_shape(const LayerNormForward& p, int sms) {
     Alignment on(p.dtype, p.rows, p.cols);
     on.add(p.x, p.ldx);
     on.add(p.y, p.ldy);
-    on.add(p.weight, 0);
-    on.add(p.bias, 0);
+    on.add_vector(p.weight);
+    on.add_vector(p.bias);
     if (!on.whole) {
+        if (on.access(p.cols, sms) == kShifted && p.cols <= 16 * 512)
+            return by_block(p.rows, p.cols, 16, 512, kShifted, on.period(), sms);
         // (The checkpoint takes registers that only blocks of up to 512 threads have.)
-        if (p.codes && p.cols <= 8 * 512) return by_block(p.rows, p.cols, 8, 512, true, sms, true);
-        if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, true, sms);
+        if (p.codes && p.cols <= 8 * 512) return by_block(p.rows, p.cols, 8, 512, kSingle, 1, sms, true);
+        if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, kSingle, 1, sms);
         return Shape{kWide};
     }
     const bool keep = p.codes != nullptr;
     if (p.rows <= 2LL * sms && p.cols <= 8 * 1024)
-        return by_block(p.rows, p.cols, 8, 1024, false, sms, keep);
+        return by_block(p.rows, p.cols, 8, 1024, kWhole, 1, sms, keep);
     if (p.cols <= 256) {
         Shape s{};
         s.keeps = keep;
@@ -277,9 +308,9 @@ Shape forward_shape(const LayerNormForward& p, int sms) {
         s.grid = static_cast<int>((p.rows + 3LL) / 4);
         return s;
     }
-    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 16, 512, false, sms, keep);
+    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 16, 512, kWhole, 1, sms, keep);
     // Wider 2-byte rows, as far as weight and bias fit beside them in shared memory.
-    if (p.cols <= 16 * 1024 && on.elem == 2) return by_block(p.rows, p.cols, 16, 1024, false, sms, keep);
+    if (p.cols <= 16 * 1024 && on.elem == 2) return by_block(p.rows, p.cols, 16, 1024, kWhole, 1, sms, keep);
     return Shape{kWide};
 }
 
@@ -287,47 +318,43 @@ Shape forward_shape(const LayerNormForward& p, int sms) {
 // ragged or fp32 rows, sixteen of 2-byte ones.  Teams of up to 128 share a block an SM, so that
 // fewer sums are left to add up (16384 x 256 bf16 13.7 against 16.9 us, 8192 x 1024 19.4 against
 // 21.2); for wider rows the blocks' own pace counts more (8192 x 4096 52.4 against 50.1).
-Shape backward_shape(long long rows, int cols, int own, bool ragged, int sms) {
-    Shape s{};
-    s.kind = kByBlock;
-    s.ragged = ragged;
-    s.columns = own;
-    s.team = 32;
-    while (s.team * own < cols) s.team *= 2;
-    const long long room = s.team <= 128 ? 512 / s.team : 1;
-    const int teams = static_cast<int>(std::max(1LL, std::min(room, (rows + sms - 1) / sms)));
-    s.threads = teams * s.team;
-    const long long per = std::min(512 / static_cast<long long>(room * s.team), 2LL);
-    s.grid = static_cast<int>(std::min((rows + teams - 1) / teams, sms * per));
-    s.blocks = 1;
-    return s;
-}
 Shape backward_shape(const LayerNormBackward& p, int sms) {
     Alignment on(p.dtype, p.rows, p.cols);
     on.add(p.dh, p.lddh);
     on.add(p.dy, p.lddy);
     on.add(p.x, p.ldx);
     on.add(p.dx, p.lddx);
-    on.add(p.weight, 0);
-    const int own = !on.whole || p.dtype == kF32 ? 8 : 16;
-    if (p.cols <= own * 512) return backward_shape(p.rows, p.cols, own, !on.whole, sms);
-    if (p.cols <= 8 * (own * 512 - 64)) {      // up to eight blocks a row, whole blocks of 64 each
-        Shape c{};
-        c.kind = kByBlock;
-        c.ragged = !on.whole;
-        c.columns = own;
-        c.team = c.threads = 512;
+    on.add_vector(p.weight);
+    Shape s{};
+    s.kind = kByBlock;
+    s.access = on.access(p.cols, sms);
+    s.period = s.access == kShifted ? on.period() : 1;
+    s.columns = s.access == kSingle || p.dtype == kF32 ? 8 : 16;
+    if (p.cols <= s.columns * 512) {
+        s.team = 32;
+        while (s.team * s.columns < p.cols) s.team *= 2;
+        const long long room = s.team <= 128 ? 512 / s.team : 1;
+        const int teams = static_cast<int>(std::max(1LL, std::min(room, (p.rows + 0LL + sms - 1) / sms)));
+        s.threads = teams * s.team;
+        const long long per = std::min(512 / static_cast<long long>(room * s.team), 2LL);
+        s.grid = whole_steps(static_cast<int>(std::min((p.rows + 0LL + teams - 1) / teams, sms * per)), s.period,
+                             (p.rows + 0LL + teams - 1) / teams);
+        s.blocks = 1;
+        return s;
+    }
+    if (p.cols <= 8 * (s.columns * 512 - 64)) {    // up to eight blocks a row, whole blocks of 64 each
+        s.team = s.threads = 512;
         // (Clusters of three blocks of 256 threads, two to an SM, 11279 x 9208 bf16: 463 us, of two of
         // 512 threads 313.)
-        for (c.blocks = 2;; c.blocks *= 2) {
-            c.each = static_cast<int>(act8_pitch((p.cols + c.blocks - 1) / c.blocks));
-            if (c.each <= own * 512) break;
+        for (s.blocks = 2;; s.blocks *= 2) {
+            s.each = static_cast<int>(act8_pitch((p.cols + s.blocks - 1) / s.blocks));
+            if (s.each <= s.columns * 512) break;
         }
-        c.grid = static_cast<int>(std::min<long long>(p.rows, sms / c.blocks)) * c.blocks;
-        return c;
+        s.grid = static_cast<int>(std::min<long long>(p.rows, sms / s.blocks)) * s.blocks;
+        return s;
     }
     // Strips of rows, for eight blocks an SM and no more strips than the workspace holds.
-    Shape s{kWide};
+    s = Shape{kWide};
     const long long tiles = (p.cols + 31) / 32;
     s.grid = static_cast<int>(std::max(1LL, std::min({8LL * sms / tiles, 2LL * sms, p.rows / 16LL})));
     return s;

@@ -107,14 +107,105 @@ struct Single {
         }
     }
 };
-template <typename T, bool VEC, int OWN>
-using Columns = std::conditional_t<VEC, Own<T, true, OWN>, Single<T, OWN>>;
+// Columns of a thread where rows begin anywhere in a 16-byte group of memory, all rows of the thread (in
+// every matrix of the call) at the same place: those of OWN / width whole groups, and, of the few before
+// the first group and after the last, one a thread, in a pair of its own (whose second number is
+// 0).  Rows of an odd width begin at the same place every eighth row; the launch steps by multiples of
+// that.  (For 2-byte rows; fp32 ones gain nothing, 3001 x 2047 forward 11.0 us, single columns 10.1.
+// With the first and last group masked instead of set apart that row took 331 instructions a thread,
+// single columns 325.)
+template <typename T, int OWN>
+struct Shifted {
+    using Body = Own<T, true, OWN>;
+    static constexpr int kWidth = Body::kWidth, kGroups = Body::kGroups, kPairs2 = OWN / 2 + 1;
+    int head, D;                     // columns before the first group, all columns
+    int single;                      // the thread's column outside the groups, -1: none
+    Body body;
+    // place: numbers of a group before the row's first.
+    __device__ __forceinline__ Shifted(int d, int tid, int threads, int place)
+        : head(min((kWidth - place) % kWidth, d)), D(d), body((d - head) / kWidth * kWidth, tid, threads) {
+        single = tid < head ? tid : body.D + tid < d ? body.D + tid : -1;
+    }
+    __device__ __forceinline__ bool in(int group) const { return body.c[group] < body.D; }
+    struct Row {
+        typename Body::Row body;
+        T single;
+        __device__ __forceinline__ Two pair(int j) const {
+            return j < OWN / 2 ? body.pair(j) : two(to_float(single), 0.0f);
+        }
+    };
+    __device__ __forceinline__ void load(const T* row, Row& to) const {
+        body.load(row + head, to.body);
+        to.single = single >= 0 ? __ldg(row + single) : T(0.0f);
+    }
+    __device__ __forceinline__ void store(T* row, const Two (&x)[kPairs2]) const {
+        body.store(row + head, reinterpret_cast<const Two(&)[OWN / 2]>(x));
+        if (single >= 0) row[single] = from_float<T>(parts(x[OWN / 2]).x);
+    }
+    // fp32 numbers to shared memory, column c at to[pad() + c], so that the groups are on 16 bytes.
+    __device__ __forceinline__ int pad() const { return -head & 3; }
+    __device__ __forceinline__ void hold(float* to, const Two (&x)[kPairs2]) const {
+        to += pad();
+        body.store(to + head, reinterpret_cast<const Two(&)[OWN / 2]>(x));
+        if (single >= 0) to[single] = parts(x[OWN / 2]).x;
+    }
+    template <typename W>
+    __device__ __forceinline__ void shared(const W* w, Two (&x)[kPairs2]) const {
+#pragma unroll
+        for (int j = 0; j < OWN / 2; ++j) {
+            const int i = 2 * j / kWidth, at = head + body.c[i] + 2 * j % kWidth;
+            x[j] = in(i) ? two(to_float(__ldg(w + at)), to_float(__ldg(w + at + 1))) : twice(0.0f);
+        }
+        x[OWN / 2] = two(single >= 0 ? to_float(__ldg(w + single)) : 0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void weights(const void* w, int type, Two (&x)[kPairs2]) const {
+        if (w == nullptr) {
+#pragma unroll
+            for (int j = 0; j < kPairs2; ++j) x[j] = twice(1.0f);
+        } else if (type == mx4::kF32) {
+            shared(static_cast<const float*>(w), x);
+        } else if (type == mx4::kBf16) {
+            shared(static_cast<const __nv_bfloat16*>(w), x);
+        } else {
+            shared(static_cast<const __half*>(w), x);
+        }
+    }
+};
+template <typename T, int ACCESS, int OWN>
+using Columns = std::conditional_t<ACCESS == kWhole, Own<T, true, OWN>,
+                                   std::conditional_t<ACCESS == kShifted, Shifted<T, OWN>, Single<T, OWN>>>;
+// The place in its group at which a row begins.
+template <typename T>
+__device__ __forceinline__ int place(const void* matrix, long long elements) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(static_cast<const T*>(matrix) + elements) & 15) /
+           static_cast<int>(sizeof(T));
+}
+template <typename T, int ACCESS, int OWN>
+__device__ __forceinline__ Columns<T, ACCESS, OWN> columns(int d, int tid, int threads, int off) {
+    if constexpr (ACCESS == kShifted) return Columns<T, ACCESS, OWN>(d, tid, threads, off);
+    else return Columns<T, ACCESS, OWN>(d, tid, threads);
+}
 template <typename T, int OWN>
 __device__ __forceinline__ bool inside(const Own<T, true, OWN>& own, int group) {
     return own.c[group] < own.D;
 }
 template <typename T, int OWN>
+__device__ __forceinline__ bool inside(const Shifted<T, OWN>& own, int group) { return own.in(group); }
+template <typename T, int OWN>
 __device__ __forceinline__ bool inside(const Single<T, OWN>& own, int group) { return own.in(group); }
+// The groups, the columns before them, and the thread's column outside them (-1: none).
+template <typename T, int OWN>
+__device__ __forceinline__ const Own<T, true, OWN>& groups_of(const Own<T, true, OWN>& own) { return own; }
+template <typename T, int OWN>
+__device__ __forceinline__ const Own<T, true, OWN>& groups_of(const Shifted<T, OWN>& own) { return own.body; }
+template <typename T, int OWN>
+__device__ __forceinline__ int head_of(const Own<T, true, OWN>&) { return 0; }
+template <typename T, int OWN>
+__device__ __forceinline__ int head_of(const Shifted<T, OWN>& own) { return own.head; }
+template <typename T, int OWN>
+__device__ __forceinline__ int outside_of(const Own<T, true, OWN>&) { return -1; }
+template <typename T, int OWN>
+__device__ __forceinline__ int outside_of(const Shifted<T, OWN>& own) { return own.single; }
 
 // ----------------------------------------------------------------------------
 // Forward, one warp a row: NV 16-byte groups a lane, no barriers
@@ -219,22 +310,24 @@ __device__ __forceinline__ void warp_sums(float (&v)[ROWS]) {
 // Weight and bias stay in a thread's registers.  WIDE: in shared memory, as fp32; a thread reads its
 // groups' first and second four columns from two arrays, so that a warp's reads meet no bank
 // twice.
-template <typename T, bool VEC, int OWN, bool KEEP, int ROWS, bool WIDE>
-__global__ void __launch_bounds__((OWN == 16 && !WIDE) || (!VEC && KEEP) ? 512 : 1024, 1)
+template <typename T, int ACCESS, int OWN, bool KEEP, int ROWS, bool WIDE>
+__global__ void __launch_bounds__((OWN == 16 && !WIDE) || (ACCESS == kSingle && KEEP) ? 512 : 1024, 1)
     forward_block(const LayerNormForward p) {
-    using O = Columns<T, VEC, OWN>;
-    constexpr int P = OWN / 2;
+    using O = Columns<T, ACCESS, OWN>;
+    static_assert(ACCESS != kShifted || !KEEP, "blocks of 64 columns are not a thread's groups");
+    constexpr int P = O::kPairs2;
     constexpr int kSets = ROWS == 1 ? 2 : 1;       // row sets ahead
     __shared__ float2 part[2][ROWS][32];
     extern __shared__ __align__(16) float held[];
     const int D = p.cols, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float inv = 1.0f / static_cast<float>(D);
     const long long pitch = act8_pitch(D);
-    const O own(D);
+    const O own = columns<T, ACCESS, OWN>(D, threadIdx.x, blockDim.x, place<T>(p.x, blockIdx.x * p.ldx));
     // Columns of this thread's warp, and of warp `lane`.
     float mine = 0.0f;
 #pragma unroll
     for (int i = 0; i < O::kGroups; ++i) mine += inside(own, i) ? static_cast<float>(O::kWidth) : 0.0f;
+    if constexpr (ACCESS == kShifted) mine += own.single >= 0 ? 1.0f : 0.0f;
     mine = warp_sum(mine);
     if (lane == 0) part[0][0][warp].x = mine;
     __syncthreads();
@@ -302,7 +395,7 @@ __global__ void __launch_bounds__((OWN == 16 && !WIDE) || (!VEC && KEEP) ? 512 :
                 const long long row = i * ROWS + k;
                 int8_t* const codes = p.codes + row * pitch;
                 float* const scales = p.scales + row * (pitch / kAct8Block);
-                if constexpr (VEC) {
+                if constexpr (ACCESS == kWhole) {
 #pragma unroll
                     for (int g = 0; g < O::kGroups; ++g)
                         if (g * blockDim.x * O::kWidth < pitch)
@@ -328,13 +421,18 @@ __global__ void __launch_bounds__((OWN == 16 && !WIDE) || (!VEC && KEEP) ? 512 :
 #pragma unroll
             for (int j = 0; j < P; ++j) {
                 const Two d = add(v[k][j], less);
-                if constexpr (VEC) {
-                    if (inside(own, 2 * j / O::kWidth)) t = mx4::fma(d, d, t);
-                } else {
+                if constexpr (ACCESS == kSingle) {
                     const float2 f = parts(d);
                     const Two in =
                         two(own.in(2 * j) ? f.x : 0.0f, own.in(2 * j + 1) ? f.y : 0.0f);
                     t = mx4::fma(in, in, t);
+                } else if (ACCESS == kShifted && j == OWN / 2) {
+                    if constexpr (ACCESS == kShifted) {
+                        const Two in = two(own.single >= 0 ? parts(d).x : 0.0f, 0.0f);
+                        t = mx4::fma(in, in, t);
+                    }
+                } else if (inside(own, 2 * j / O::kWidth)) {
+                    t = mx4::fma(d, d, t);
                 }
             }
             q[k] = sum(t);
@@ -486,6 +584,8 @@ struct TeamSum {
         return warp_sums(v.x, v.y);
     }
 };
+// Of a row of sums in shared memory: whole 16-byte groups, and what a shifted row's begin after.
+__host__ __device__ constexpr int held_width(int cols) { return (cols + 3) / 4 * 4 + 4; }
 // The teams' sums over rows, added in the teams' order, to the block's part of the workspace.
 template <typename O, int P, bool SPLIT>
 __device__ __forceinline__ void store_sums(const LayerNormBackward& p, const O& own, const Team& team,
@@ -499,7 +599,7 @@ __device__ __forceinline__ void store_sums(const LayerNormBackward& p, const O& 
         own.store(to + D, sb);
         return;
     }
-    const int width = (D + 3) / 4 * 4;              // (16-byte stores of aligned columns)
+    const int width = held_width(D);
     __syncthreads();                                // the ring is read no more
     own.store(held + team.id * 2 * width, sw);
     own.store(held + (team.id * 2 + 1) * width, sb);
@@ -509,6 +609,26 @@ __device__ __forceinline__ void store_sums(const LayerNormBackward& p, const O& 
         float v = 0.0f;
         for (int k = 0; k < teams; ++k) v += held[k * 2 * width + at];
         to[i] = v;
+    }
+}
+// Shifted (one team of 512 threads a block): through shared memory, to be written in order, as a
+// thread's groups are no whole groups of the workspace's memory.
+template <typename T, int OWN, int P, bool SPLIT>
+__device__ __forceinline__ void store_sums(const LayerNormBackward& p, const Shifted<T, OWN>& own, const Team&,
+                                           const Slice<SPLIT>& slice, float* held, const Two (&sw)[P],
+                                           const Two (&sb)[P]) {
+    if (!p.partial) return;
+    const int width = held_width(slice.cols);
+    float* const to = p.partial + blockIdx.x / slice.count * 2LL * p.cols + slice.first;
+    __syncthreads();                                // the ring is read no more
+    own.hold(held, sw);
+    own.hold(held + width, sb);
+    __syncthreads();
+    held += own.pad();
+#pragma unroll 4
+    for (int i = threadIdx.x; i < slice.cols; i += 512) {
+        to[i] = held[i];
+        to[p.cols + i] = held[width + i];
     }
 }
 
@@ -597,7 +717,7 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
 }
 
 // ----------------------------------------------------------------------------
-// Backward of aligned rows: a ring of shared-memory stages holds the rows ahead
+// Backward of aligned and shifted rows: a ring of shared-memory stages holds the rows ahead
 // ----------------------------------------------------------------------------
 // Registers hold the sums over rows and one row's numbers; a second row's in flight
 // (backward_block) is not enough to cover the memory's latency: 8192 x 4096 bf16 58 us so, whether
@@ -606,10 +726,12 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
 // After the barrier of a row every thread is done with the row before, whose stage is filled
 // again then.  A copy that does not arrive in time ends the copying, not the loop (whose barriers
 // all threads have to meet): the status word says that what was written since is not to be used.
-template <typename T, int OWN, bool KEPT, bool SPLIT>
+// Shifted rows: their whole groups go through the ring, the numbers outside them through registers.
+template <typename T, int ACCESS, int OWN, bool KEPT, bool SPLIT>
 __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward p, const Ring ring) {
-    using O = Own<T, true, OWN>;
+    using O = Columns<T, ACCESS, OWN>;
     constexpr int P = OWN / 2, VEC = O::kWidth;
+    constexpr bool kOutside = ACCESS == kShifted;
     extern __shared__ __align__(128) uint8_t smem_all[];
     __shared__ __align__(8) uint64_t all_bars[16][kMaxStages];
     __shared__ float2 part[16][2][16];
@@ -617,7 +739,7 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
     __shared__ int abort_s;
     const Team team(ring.team);
     const Slice<SPLIT> slice(ring.blocks, ring.each, p.cols);
-    const int D = slice.cols, teams = blockDim.x / ring.team;
+    const int teams = blockDim.x / ring.team;
     uint8_t* const smem = smem_all + team.id * ring.stages * ring.stage_bytes;
     uint64_t* const bars = all_bars[team.id];
     const bool leader = team.tid == 0;
@@ -625,7 +747,10 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
     const long long step = static_cast<long long>(gridDim.x / slice.count) * teams;
     const float inv = 1.0f / static_cast<float>(p.cols);
     const long long pitch = act8_pitch(p.cols);
-    const O own(D, team.tid, ring.team);
+    // (A slice begins at a multiple of 64 columns: at its row's place in a group.)
+    const O all = columns<T, ACCESS, OWN>(slice.cols, team.tid, ring.team, place<T>(p.dh, first_row * p.lddh));
+    const auto& own = groups_of(all);
+    const int D = own.D, head = head_of(all), outside = outside_of(all);
     if (threadIdx.x == 0) abort_s = 0;
     if (leader) {
         for (int i = 0; i < ring.stages; ++i) async::mbar_init(su32(&bars[i]), 1);
@@ -639,37 +764,57 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
     start_dependent();
     TeamSum team_sum{team, part[team.id]};
     const int row_bytes = D * static_cast<int>(sizeof(T));
-    const int x_bytes = KEPT ? static_cast<int>(act8_pitch(D)) : row_bytes;
+    const int x_bytes = KEPT ? static_cast<int>(act8_pitch(slice.cols)) : row_bytes;
     // A stage: dh, x or its codes, dy.
     auto fill = [&](int stage, long long row) {
         const uint32_t bar = su32(&bars[stage]), to = su32(smem + stage * ring.stage_bytes);
         async::mbar_expect_tx(bar, row_bytes + x_bytes + (p.dy ? row_bytes : 0));
-        mx4::bulk_load(to, static_cast<const T*>(p.dh) + row * p.lddh + slice.first, row_bytes, bar);
+        const int first = slice.first + head;
+        mx4::bulk_load(to, static_cast<const T*>(p.dh) + row * p.lddh + first, row_bytes, bar);
         if (KEPT) mx4::bulk_load(to + row_bytes, p.codes + row * pitch + slice.first, x_bytes, bar);
         else
-            mx4::bulk_load(to + row_bytes, static_cast<const T*>(p.x) + row * p.ldx + slice.first, x_bytes,
-                           bar);
+            mx4::bulk_load(to + row_bytes, static_cast<const T*>(p.x) + row * p.ldx + first, x_bytes, bar);
         if (p.dy)
-            mx4::bulk_load(to + row_bytes + x_bytes,
-                           static_cast<const T*>(p.dy) + row * p.lddy + slice.first, row_bytes, bar);
+            mx4::bulk_load(to + row_bytes + x_bytes, static_cast<const T*>(p.dy) + row * p.lddy + first,
+                           row_bytes, bar);
     };
     if (leader)
         for (int i = 0; i < ring.stages; ++i)
             if (first_row + i * step < p.rows) fill(i, first_row + i * step);
-    float scale[O::kGroups];
+    // Shifted, a group's eight codes may lie in two blocks: two scales.
+    constexpr int kScales = kOutside ? 2 : 1;
+    float scale[O::kGroups][kScales];
     float m = 0.0f, r = 0.0f;
+    T dh_1 = T(0.0f), x_1 = T(0.0f), dy_1 = T(0.0f);   // the numbers outside the groups, as they are stored
+    int8_t code_1 = 0;
+    float scale_1 = 0.0f, sw_1 = 0.0f, sb_1 = 0.0f;
     auto load = [&](long long row) {       // what is not in the ring
         m = __ldg(p.mean + row);
         r = __ldg(p.rstd + row);
         if constexpr (KEPT)
 #pragma unroll
             for (int i = 0; i < O::kGroups; ++i)
-                scale[i] = own.c[i] < D ? __ldg(p.scales + (row * pitch + slice.first + own.c[i]) / kAct8Block) : 0.0f;
+#pragma unroll
+                for (int j = 0; j < kScales; ++j)
+                    scale[i][j] = own.c[i] < D ? __ldg(p.scales + (row * pitch + slice.first + head + own.c[i] +
+                                                                   j * (VEC - 1)) / kAct8Block) : 0.0f;
+        if (kOutside && outside >= 0) {
+            const int c = slice.first + outside;
+            dh_1 = __ldg(static_cast<const T*>(p.dh) + row * p.lddh + c);
+            if constexpr (KEPT) {
+                code_1 = __ldg(p.codes + row * pitch + c);
+                scale_1 = __ldg(p.scales + (row * pitch + c) / kAct8Block);
+            } else {
+                x_1 = __ldg(static_cast<const T*>(p.x) + row * p.ldx + c);
+            }
+            if (p.dy) dy_1 = __ldg(static_cast<const T*>(p.dy) + row * p.lddy + c);
+        }
     };
     if (first_row < p.rows) load(first_row);
-    Two w[P];
-    own.weights(at_column(p.weight, p.weight_dtype, slice.first), p.weight_dtype, w);
-    Two sw[P] = {}, sb[P] = {};
+    Two w[O::kPairs2];
+    all.weights(at_column(p.weight, p.weight_dtype, slice.first), p.weight_dtype, w);
+    const float w_1 = kOutside ? parts(w[O::kPairs2 - 1]).x : 0.0f;
+    Two sw[O::kPairs2] = {}, sb[O::kPairs2] = {};
     int stage = 0, before = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true, first = true;
@@ -685,11 +830,29 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
             if (c < D) {
                 mx4::unpack(*reinterpret_cast<const uint4*>(at + c * sizeof(T)),
                             reinterpret_cast<Two(&)[VEC / 2]>(g[j0]), T());
-                if constexpr (KEPT) {
+                if constexpr (KEPT && kOutside) {
+                    // The words that hold the group's codes (one past them lies in the stage too).
+                    const int byte = head + c, cut = kAct8Block - byte % kAct8Block;
+                    const uint8_t* const codes = at + row_bytes + (byte & ~3);
+                    uint32_t lo = *reinterpret_cast<const uint32_t*>(codes);
+#pragma unroll
+                    for (int j = 0; j < VEC / 4; ++j) {
+                        const uint32_t hi = *reinterpret_cast<const uint32_t*>(codes + 4 * j + 4);
+                        const uint32_t four = __funnelshift_r(lo, hi, 8 * (byte & 3));
+                        lo = hi;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int e = 4 * j + 2 * k;
+                            n[j0 + 2 * j + k] = act8::values2(
+                                four, k, two(e < cut ? scale[i][0] : scale[i][kScales - 1],
+                                             e + 1 < cut ? scale[i][0] : scale[i][kScales - 1]));
+                        }
+                    }
+                } else if constexpr (KEPT) {
 #pragma unroll
                     for (int j = 0; j < VEC / 4; ++j)
                         act8::values4(*reinterpret_cast<const uint32_t*>(at + row_bytes + c + 4 * j),
-                                      scale[i], reinterpret_cast<Two(&)[2]>(n[j0 + 2 * j]));
+                                      scale[i][0], reinterpret_cast<Two(&)[2]>(n[j0 + 2 * j]));
                 } else {
                     mx4::unpack(*reinterpret_cast<const uint4*>(at + row_bytes + c * sizeof(T)),
                                 reinterpret_cast<Two(&)[VEC / 2]>(n[j0]), T());
@@ -708,7 +871,18 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
                 s2 = mx4::fma(g[j], n[j], s2);
             }
         }
-        float2 sums = team_sum(sum(s1), sum(s2));
+        float n_1 = 0.0f, g_1 = 0.0f, dy_now = 0.0f, of_g = sum(s1), of_gn = sum(s2);
+        if (kOutside && outside >= 0) {
+            const float h = to_float(dh_1);
+            n_1 = ((KEPT ? act8::value(code_1, scale_1) : to_float(x_1)) - m) * r;
+            dy_now = to_float(dy_1);
+            sb_1 += h;
+            sw_1 = fmaf(h, n_1, sw_1);
+            g_1 = w_1 * h;
+            of_g += g_1;
+            of_gn = fmaf(g_1, n_1, of_gn);
+        }
+        float2 sums = team_sum(of_g, of_gn);
         if constexpr (SPLIT) {
             sums = cluster_sums(slice, of_blocks, turn, sums);
             turn ^= 1;
@@ -717,7 +891,10 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
         if (leader && !first && ok && refill < p.rows) fill(before, refill);
         if (row + step < p.rows) load(row + step);
         const Two mg = twice(-sums.x * inv), mn = twice(-sums.y * inv);
-        T* const dx = static_cast<T*>(p.dx) + row * p.lddx + slice.first;
+        T* const dx = static_cast<T*>(p.dx) + row * p.lddx + slice.first + head;
+        if (kOutside && outside >= 0)
+            dx[outside - head] = from_float<T>(
+                fmaf(fmaf(n_1, -sums.y * inv, g_1 - sums.x * inv), parts(r2).x, dy_now));
 #pragma unroll
         for (int i = 0; i < O::kGroups; ++i) {
             const int c = own.c[i], j0 = i * VEC / 2;
@@ -741,7 +918,11 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
         }
     }
     if (leader && !ok) norm::ring_drain(su32(bars), ring.stages);
-    store_sums(p, own, team, slice, reinterpret_cast<float*>(smem_all), sw, sb);
+    if constexpr (kOutside) {
+        sw[O::kPairs2 - 1] = two(sw_1, 0.0f);
+        sb[O::kPairs2 - 1] = two(sb_1, 0.0f);
+    }
+    store_sums(p, all, team, slice, reinterpret_cast<float*>(smem_all), sw, sb);
 }
 
 // ----------------------------------------------------------------------------
@@ -760,35 +941,39 @@ cudaError_t forward_rows_of(const LayerNormForward& p, const Shape& s, cudaStrea
     if (s.kind == kByWarp)
         return s.groups == 1 ? run(forward_warp<T, 1, KEEP>, kWarpThreads)
                              : run(forward_warp<T, 2, KEEP>, kWarpThreads);
-    if (s.columns == 8) return run(forward_block<T, true, 8, KEEP, 1, false>, s.threads);
+    if (s.columns == 8) return run(forward_block<T, kWhole, 8, KEEP, 1, false>, s.threads);
     if (s.threads <= 512)
-        return run(forward_block<T, true, 16, KEEP, sizeof(T) == 4 ? 1 : 2, false>, s.threads);
+        return run(forward_block<T, kWhole, 16, KEEP, sizeof(T) == 4 ? 1 : 2, false>, s.threads);
     if constexpr (sizeof(T) == 2)
-        return run(forward_block<T, true, 16, KEEP, 1, true>, s.threads, (p.cols + 7) / 8 * 64);
+        return run(forward_block<T, kWhole, 16, KEEP, 1, true>, s.threads, (p.cols + 7) / 8 * 64);
     return cudaErrorInvalidConfiguration;
 }
 template <typename T>
 cudaError_t forward(const LayerNormForward& p, const Shape& s, cudaStream_t st) {
-    if (s.ragged)
-        return launch_dependent(s.keeps ? forward_block<T, false, 8, true, 1, false>
-                                        : forward_block<T, false, 8, false, 1, false>,
+    if (s.access == kSingle)
+        return launch_dependent(s.keeps ? forward_block<T, kSingle, 8, true, 1, false>
+                                        : forward_block<T, kSingle, 8, false, 1, false>,
                                 dim3(s.grid), s.threads, 0, st, p);
+    if constexpr (sizeof(T) == 2)
+        if (s.access == kShifted)
+            return launch_dependent(forward_block<T, kShifted, 16, false, 1, false>, dim3(s.grid), s.threads,
+                                    0, st, p);
     return s.keeps ? forward_rows_of<T, true>(p, s, st) : forward_rows_of<T, false>(p, s, st);
 }
-// No more clusters of `blocks` than run at once, `grid` blocks at most.  (One that waits for its SMs
+// No more clusters of `blocks` than run at once, s.grid blocks at most.  (One that waits for its SMs
 // would come to its rows when the others are done.)
 template <typename K, typename... A>
-cudaError_t launch_clusters(K kernel, int blocks, int* grid, int threads, int smem, cudaStream_t st,
+cudaError_t launch_clusters(K kernel, Shape& s, int smem, cudaStream_t st, const LayerNormBackward& p,
                             const A&... args) {
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.x = s.blocks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3(static_cast<unsigned>(*grid));
-    c.blockDim = dim3(static_cast<unsigned>(threads));
+    c.gridDim = dim3(static_cast<unsigned>(s.grid));
+    c.blockDim = dim3(static_cast<unsigned>(s.threads));
     c.dynamicSmemBytes = smem;
     c.stream = st;
     c.attrs = at;
@@ -796,37 +981,40 @@ cudaError_t launch_clusters(K kernel, int blocks, int* grid, int threads, int sm
     int most = 0;
     const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &c);
     if (e != cudaSuccess) return e;
-    if (most < 1) return cudaErrorInvalidConfiguration;
-    *grid = std::min(*grid, most * blocks);
-    c.gridDim = dim3(static_cast<unsigned>(*grid));
+    if (most < s.period) return cudaErrorInvalidConfiguration;     // (a small part of a GPU)
+    s.grid = whole_steps(std::min(s.grid / s.blocks, most), s.period, p.rows) * s.blocks;
+    c.gridDim = dim3(static_cast<unsigned>(s.grid));
     c.numAttrs = 2;
-    return cudaLaunchKernelEx(&c, kernel, args...);
+    return cudaLaunchKernelEx(&c, kernel, p, args...);
 }
 template <typename T>
 cudaError_t backward(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
     constexpr int OWN = sizeof(T) == 4 ? 8 : 16;
     const int teams = s.threads / s.team;
     // The teams' sums at the end.
-    const int held = teams > 1 ? teams * 2 * ((p.cols + 3) / 4 * 4) * static_cast<int>(sizeof(float)) : 0;
+    const int held = teams > 1 || s.access == kShifted
+                         ? teams * 2 * held_width(s.blocks == 1 ? p.cols : s.each) * static_cast<int>(sizeof(float)) : 0;
     const auto run = [&](auto kernel, int smem, const auto&... more) {
         smem = std::max(smem, held);
         const cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, norm::kSharedPerSm);
         if (e != cudaSuccess) return e;
         if (s.blocks == 1) return launch_dependent(kernel, dim3(s.grid), s.threads, smem, st, p, more...);
-        return launch_clusters(kernel, s.blocks, &s.grid, s.threads, smem, st, p, more...);
+        return launch_clusters(kernel, s, smem, st, p, more...);
     };
     const auto choose = [&](auto one, auto split, int smem, const auto&... more) {
         return s.blocks == 1 ? run(one, smem, more...) : run(split, smem, more...);
     };
-    if (s.ragged)
+    if (s.access == kSingle)
         return p.codes ? choose(backward_block<T, 8, true, false>, backward_block<T, 8, true, true>, 0,
                                 s.team, s.blocks, s.each)
                        : choose(backward_block<T, 8, false, false>, backward_block<T, 8, false, true>, 0,
                                 s.team, s.blocks, s.each);
     const int cols = s.blocks == 1 ? p.cols : s.each;
-    const int row = cols * static_cast<int>(sizeof(T));
-    const int stage = (p.dy ? 2 : 1) * row + (p.codes ? static_cast<int>(act8_pitch(cols)) : row);
+    // (Shifted, at most the whole groups of a row, and a word past its codes.)
+    const int row = cols * static_cast<int>(sizeof(T)) / 16 * 16;
+    const int stage = (p.dy ? 2 : 1) * row +
+                      (p.codes ? static_cast<int>(act8_pitch(cols)) + (s.access == kShifted ? 16 : 0) : row);
     const long long sets = static_cast<long long>(s.grid / s.blocks) * teams;
     const long long own = (p.rows + sets - 1) / sets;
     const int rows_at_once = s.team <= 128 ? teams : 512 / s.team;       // of an SM
@@ -834,9 +1022,16 @@ cudaError_t backward(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
         std::min<long long>({kMaxStages, norm::kSharedPerSm / rows_at_once / stage, std::max(2LL, own)}));
     const Ring ring{s.team, s.blocks, s.each, stage, stages, status_word_ptr()};
     const int smem = teams * stages * stage;
-    return p.codes ? choose(backward_ring<T, OWN, true, false>, backward_ring<T, OWN, true, true>, smem, ring)
-                   : choose(backward_ring<T, OWN, false, false>, backward_ring<T, OWN, false, true>, smem,
-                            ring);
+    if constexpr (sizeof(T) == 2)
+        if (s.access == kShifted)
+            return p.codes ? choose(backward_ring<T, kShifted, OWN, true, false>,
+                                    backward_ring<T, kShifted, OWN, true, true>, smem, ring)
+                           : choose(backward_ring<T, kShifted, OWN, false, false>,
+                                    backward_ring<T, kShifted, OWN, false, true>, smem, ring);
+    return p.codes ? choose(backward_ring<T, kWhole, OWN, true, false>,
+                            backward_ring<T, kWhole, OWN, true, true>, smem, ring)
+                   : choose(backward_ring<T, kWhole, OWN, false, false>,
+                            backward_ring<T, kWhole, OWN, false, true>, smem, ring);
 }
 
 }  // namespace layer_norm

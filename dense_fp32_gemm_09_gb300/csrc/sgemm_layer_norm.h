@@ -8,6 +8,9 @@ namespace sgemm {
 namespace layer_norm {
 
 enum : int { kByBlock = 0, kByWarp = 1, kWide = 2 };
+// Rows in global memory: whole, aligned 16-byte groups; of 2-byte numbers, beginning anywhere in a
+// group, in every matrix of the call at the same place; or anything else.
+enum : int { kWhole = 0, kShifted = 1, kSingle = 2 };
 struct Shape {
     int kind;
     int threads, grid;
@@ -16,8 +19,14 @@ struct Shape {
     int columns;       // of a thread, by block
     int groups;        // of 16 bytes a lane, by warp
     bool keeps;        // forward: the checkpoint is written in the same pass
-    bool ragged;       // rows in global memory are not whole, aligned 16-byte groups
+    int access;        // kWhole, kShifted or kSingle
+    int period;        // kShifted: rows from one to the next that begins at the same place of a group
 };
+
+// Sets of rows of which each takes every `sets`-th: a multiple of the period, unless none has a second.
+inline int whole_steps(int sets, int period, long long rows) {
+    return rows <= sets ? sets : sets - sets % period;
+}
 
 // The backward pass's rows ahead in shared memory.
 constexpr int kMaxStages = 4;

@@ -219,6 +219,93 @@ def test_strides_and_alignment(sg, dtype, offset, pad):
     check_backward(sg, c, strided(c.x), f64(c.x), views=(strided(c.dh), strided(c.dy)))
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_rows_at_different_places(sg, rows, cols, dtype):
+    """Matrices that begin at different places of a 16-byte group, and all at the same one past its
+    start: as contiguous ones."""
+    c = Case(rows, cols, dtype)
+
+    def at(t, offset):
+        flat = torch.full((t.numel() + 16,), float("nan"), dtype=t.dtype, device="cuda")
+        view = flat[offset:offset + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view
+
+    x = cuda(c.x)
+    want = sg.layer_norm(x, cuda(c.w), cuda(c.b), keep="8bit")
+    for offset in (1, 3):
+        got = check_forward(sg, c, at(c.x, offset))
+        kept = sg.layer_norm(at(c.x, offset), cuda(c.w), cuda(c.b), keep="8bit")[3]
+        assert torch.equal(kept.codes, want[3].codes) and torch.equal(kept.scales, want[3].scales)
+        check_backward(sg, c, at(c.x, offset), f64(c.x), views=(at(c.dh, 2 * offset), at(c.dy, 1)))
+        check_backward(sg, c, kept, f64(kept.dequantize()), views=(at(c.dh, offset), at(c.dy, 2)))
+
+
+@pytest.mark.parametrize("rows,cols,pad", [(700, 2047, 0), (700, 2047, 2), (41, 1001, 7), (700, 1022, 0), (9, 6, 0),
+                                           (310, 4097, 0), (1000, 5001, 0), (400, 4100, 1), (320, 8185, 2),
+                                           (500, 8191, 0), (400, 9001, 0), (350, 20003, 0), (310, 33000, 1)])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_rows_at_one_place(sg, rows, cols, pad, dtype):
+    """Every matrix of the C call begins at the same place of a 16-byte group, which is not its start,
+    and nothing outside the outputs is written."""
+    import ctypes
+    c, lib, s = Case(rows, cols, dtype), sg.load(), torch.cuda.current_stream().cuda_stream
+    ld, code = cols + pad, {"fp32": 0, "bf16": 1, "fp16": 2}[dtype]
+
+    def buffer(t=None):
+        flat = torch.full((1 + rows * ld + 16,), 7.0, dtype=DTYPES[dtype], device="cuda")
+        view = flat[1:1 + rows * ld].view(rows, ld)[:, :cols]
+        if t is not None:
+            view.copy_(t)
+        return flat, view
+
+    (_, x), (_, dh), (_, dy), (y_all, y), (dx_all, dx) = buffer(c.x), buffer(c.dh), buffer(c.dy), buffer(), buffer()
+    w, b = cuda(c.w), cuda(c.b)
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    assert lib.sgemm_layer_norm_forward(rows, cols, code, x.data_ptr(), ld, w.data_ptr(), b.data_ptr(), 0, EPS,
+                                        y.data_ptr(), ld, mean.data_ptr(), rstd.data_ptr(), None, None, s) == 0
+    m, r, em, er = moments(c)
+    near(mean, m, em, "mean")
+    near(rstd, r, er * r, "rstd")
+    n = (f64(c.x) - m[:, None]) * r[:, None]
+    want = n * f64(c.w) + f64(c.b)
+    near(y, want, (em * r)[:, None] * f64(c.w).abs() * 1.01 + (n * f64(c.w)).abs() * (er[:, None] + 4 * E24) +
+         E24 * (want.abs() + f64(c.b).abs()) + c.u * want.abs() * 1.01 + 1e-7, "y")
+    q = sg.act8_quantize(cuda(c.x))
+    size = ctypes.c_size_t(0)
+    assert lib.sgemm_layer_norm_backward_workspace(rows, cols, ctypes.byref(size)) == 0
+    ws = torch.full((size.value + 256,), 9, dtype=torch.uint8, device="cuda")
+    for kept in (False, True):
+        dw, db = torch.full((cols,), 7.0, device="cuda"), torch.full((cols,), 7.0, device="cuda")
+        of = (None, 0, q.codes.data_ptr(), q.scales.data_ptr()) if kept else (x.data_ptr(), ld, None, None)
+        assert lib.sgemm_layer_norm_backward(
+            rows, cols, code, dh.data_ptr(), ld, dy.data_ptr(), ld, *of, mean.data_ptr(), rstd.data_ptr(),
+            w.data_ptr(), 0, dx.data_ptr(), ld, dw.data_ptr(), db.data_ptr(), ws.data_ptr(), size.value, s) == 0
+        # Against the call on matrices at their groups' starts, of padded rows: the terms are the same,
+        # their sums' orders are not.  c.e and c.ec bound one side's sums of magnitudes.
+        width = -(-cols // 8) * 8
+
+        def padded(t):
+            return torch.zeros(rows, width, dtype=DTYPES[dtype], device="cuda")[:, :cols].copy_(t)
+
+        ref = sg.layer_norm_backward(padded(c.dh), q if kept else padded(c.x), mean, rstd, w, dy=padded(c.dy))
+        v = f64(q.dequantize()) if kept else f64(c.x)
+        n, dh64 = (v - f64(mean)[:, None]) * f64(rstd)[:, None], f64(c.dh)
+        g, r64 = dh64 * f64(c.w), f64(rstd)[:, None]
+        ga, na = g.abs().mean(1, keepdim=True), (g * n).abs().mean(1, keepdim=True)
+        off = 2 * r64 * (c.e * ga + n.abs() * c.e * na + 6 * E24 * (g.abs() + ga + n.abs() * na)) + \
+            4 * E24 * f64(c.dy).abs()
+        near(dx, f64(ref[0]), off + 2 * c.u * 1.01 * (f64(ref[0]).abs() + off), "dx")
+        near(dw, f64(ref[1]), 2 * (c.ec + 4 * E24) * (dh64 * n).abs().sum(0) + 1e-30, "dweight")
+        near(db, f64(ref[2]), 2 * (c.ec + 4 * E24) * dh64.abs().sum(0) + 1e-30, "dbias")
+        assert bool((ws[size.value:] == 9).all())
+    for flat, view in ((y_all, y), (dx_all, dx)):
+        rest = flat.clone()
+        rest[1:1 + rows * ld].view(rows, ld)[:, :cols] = 7.0
+        assert bool((rest == 7.0).all())
+
+
 @pytest.mark.parametrize("cols", [64, 1000, 4096, 8192, 40001])
 def test_odd_numbers_stay_in_their_row(sg, cols):
     """Infinities and NaN make their own row NaN and no other; the columns' sums get them."""
@@ -302,18 +389,19 @@ def test_without_sums_the_workspace_stays(sg, cols):
 @pytest.mark.parametrize("cols", [8192, 8191])
 def test_gradient_of_long_offsets(sg, cols):
     """More than 2^31 elements, from a matrix and from a checkpoint: the last rows are their own."""
-    rows = 270000
+    rows, few = 270000, 400
     c = Case(64, cols, "bf16")
     x, dh, dy = (torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(3))
     for big, small in ((x, c.x), (dh, c.dh), (dy, c.dy)):
         big[-64:] = cuda(small)
     _, mean, rstd, kept = sg.layer_norm(x, cuda(c.w), cuda(c.b), keep="8bit")
-    for of, rows_of in ((x, cuda(c.x)), (kept, sg.act8_quantize(cuda(c.x)))):
+    x_few, dh_few, dy_few = (t[-few:].clone() for t in (x, dh, dy))
+    for of, rows_of in ((x, x_few), (kept, sg.act8_quantize(x_few))):
         got = sg.layer_norm_backward(dh, of, mean, rstd, cuda(c.w), dy=dy)
-        want = sg.layer_norm_backward(cuda(c.dh), rows_of, mean[-64:], rstd[-64:], cuda(c.w), dy=cuda(c.dy))
+        want = sg.layer_norm_backward(dh_few, rows_of, mean[-few:], rstd[-few:], cuda(c.w), dy=dy_few)
         # The same kernel and the same statistics: the same rows.  The other rows' dh are 0, but sums are
         # added in another order: 64 terms of fp32, twice, of at most 64 times the largest |dh| |n|.
-        assert torch.equal(got[0][-64:], want[0]) and not bool(got[0][:-64].any())
+        assert torch.equal(got[0][-few:], want[0]) and not bool(got[0][:-64].any())
         most = 64 * float(c.dh.abs().max()) * max(1.0, float(((c.x.float() - 0.7) / 2).abs().max()) * 1.5)
         for a, b in zip(got[1:], want[1:]):
             assert bool(((a - b).abs() <= 2 * 64 * E24 * most).all())
