@@ -26,8 +26,9 @@
 // Four MMAs of a stage take 512 clocks, so a tile of 256 x 256 x 2048 takes 8.5 us at 1.93 GHz; measured
 // are 10.2 to 12 with its share of the start and the end.  The tensor pipes are active 87 to 90 % of the
 // time (4096 x 2048 x 4096); at full size the card's power limit holds the clock lower.  Tiles of
-// 256 x 128 fill more pairs where there are few.  What is left is the last round: 3001 x 2047 x 1999
-// has 192 tiles for 76 pairs, 2.5 rounds that take 3.
+// 256 x 128 fill more pairs where there are few, and forward tiles of 224 and 160 columns the last round
+// better: 3001 x 2047 x 1999 has 192 tiles of 256 for 76 pairs, 2.5 rounds that take 3, and takes 47.6 us
+// by them, by 216 tiles of 224 44.9 (copies of the operands included).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -67,9 +68,10 @@ constexpr int kStaged = 4096;                  // bytes of a warp's staging
 template <int BN> constexpr int kHalfA = kRows / 2 * kLineBytes;
 template <int BN> constexpr int kHalfB = BN / 2 * kLineBytes;
 template <int BN> constexpr int kStage = kHalfA<BN> + kHalfB<BN>;
-template <int BN> constexpr int kStages = BN == 256 ? 6 : 8;
+template <int BN> constexpr int kStages = BN >= 224 ? 6 : BN == 160 ? 7 : 8;
 template <int BN> constexpr int kPairSmem = kStages<BN> * kStage<BN> + kEpilogueWarps * kStaged + 1024;
-static_assert(kPairSmem<256> <= 226 * 1024 && kPairSmem<128> <= 226 * 1024, "shared memory");
+static_assert(kPairSmem<256> <= 226 * 1024 && kPairSmem<224> <= 226 * 1024 &&
+                  kPairSmem<160> <= 226 * 1024 && kPairSmem<128> <= 226 * 1024, "shared memory");
 
 // Shared-memory operand in 128-byte lines with the 128-byte swizzle; eight lines (1024 bytes)
 // are a pattern.  Contraction along the lines: `lead` is not used.  Across them: eight of
@@ -228,24 +230,24 @@ __device__ __forceinline__ uint32_t ld_shared_word(uint32_t addr) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
-// Staged rows to `to`, `ld` bytes apart, of which `rows` rows and `bytes` bytes each are inside the
-// result.  vec: rows start on 16 bytes; otherwise a warp stores a row at a time, two 2-byte
-// numbers a lane.
-template <int CHUNKS>
+// Staged rows of USED chunks to `to`, `ld` bytes apart, of which `rows` rows and `bytes` bytes each are
+// inside the result.  vec: rows start on 16 bytes; otherwise a warp stores a row at a time, two
+// 2-byte numbers a lane.
+template <int CHUNKS, int USED = CHUNKS>
 __device__ __forceinline__ void store_staged(uint32_t staged, uint8_t* to, long long ld, int rows,
                                              int bytes, bool vec, int lane) {
     constexpr int kPer = 32 / CHUNKS;              // rows a step
     __syncwarp();
-    if (vec && bytes >= 16 * CHUNKS) {
+    if (vec && bytes >= 16 * USED) {
         const int chunk = lane % CHUNKS;
 #pragma unroll
         for (int r0 = 0; r0 < 32; r0 += kPer) {
             const int r = r0 + lane / CHUNKS;
-            if (r >= rows) break;
+            if (r >= rows || chunk >= USED) break;
             *reinterpret_cast<uint4*>(to + r * ld + 16 * chunk) =
                 ld_shared(staged + staged_at<CHUNKS>(r, chunk));
         }
-    } else if (lane < 4 * CHUNKS && 4 * lane < bytes) {
+    } else if (lane < 4 * USED && 4 * lane < bytes) {
         const bool both = 4 * lane + 4 <= bytes;
 #pragma unroll 4
         for (int r = 0; r < rows; ++r) {
@@ -262,15 +264,16 @@ __device__ __forceinline__ void store_staged(uint32_t staged, uint8_t* to, long 
     __syncwarp();
 }
 // COLS numbers a lane as 2-byte rows.
-template <typename T, int COLS>
-__device__ __forceinline__ void put_rows(uint32_t staged, const float (&v)[COLS], uint8_t* to,
+template <typename T, int COLS, int N>
+__device__ __forceinline__ void put_rows(uint32_t staged, const float (&v)[N], uint8_t* to,
                                          long long ld, int rows, int cols, bool vec, int lane) {
+    constexpr int kChunks = COLS > 32 ? 8 : 4;
 #pragma unroll
     for (int i = 0; i < COLS; i += 8)
-        st_shared(staged + staged_at<COLS / 8>(lane, i / 8),
+        st_shared(staged + staged_at<kChunks>(lane, i / 8),
                   make_uint4(pack2<T>(v[i], v[i + 1]), pack2<T>(v[i + 2], v[i + 3]),
                              pack2<T>(v[i + 4], v[i + 5]), pack2<T>(v[i + 6], v[i + 7])));
-    store_staged<COLS / 8>(staged, to, 2 * ld, rows, 2 * min(cols, COLS), vec, lane);
+    store_staged<kChunks, COLS / 8>(staged, to, 2 * ld, rows, 2 * min(cols, COLS), vec, lane);
 }
 // 64 numbers a lane, one block of an 8-bit checkpoint (columns past the end are zeros).
 __device__ __forceinline__ void put_codes(uint32_t staged, const float (&v)[64], int8_t* codes,
@@ -305,7 +308,8 @@ __device__ __forceinline__ void tmem_get(uint32_t at, float (&v)[COLS]) {
 template <typename T, int MODE, int BN, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     ff_pair_kernel(const __grid_constant__ PairMaps maps, const PairPlan pl) {
-    constexpr int kTmemCols = 2 * BN;
+    constexpr int kSums = BN > 128 ? 256 : 128;        // columns of tensor memory from one set to the other
+    constexpr int kTmemCols = 2 * kSums;
     constexpr int N_STAGES = kStages<BN>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full_bar[N_STAGES], empty_bar[N_STAGES];
@@ -413,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const uint32_t step_a = across ? kAcross : kAlong;
                 const uint32_t idesc = across ? ff_idesc(kIsBf16, BN, true, true)
                                               : ff_idesc(kIsBf16, BN, false, MODE != kForward);
-                const uint32_t sums = tmem + (n & 1) * BN;
+                const uint32_t sums = tmem + (n & 1) * kSums;
                 // The item before the last one has left this set of sums (first: at once).
                 if (!pipe_wait<true>(su32(&free_bar[n & 1]), ((n >> 1) & 1) ^ 1u, abort_flag,
                                      pl.status))
@@ -454,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const Item t = share.at(pl, n);
             const Result& to = pl.to[MODE == kForward ? 0 : t.result];
             const Product& of = pl.of[MODE == kForward ? 0 : t.result > 0];
-            const uint32_t sums = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + (n & 1) * BN;
+            const uint32_t sums = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + (n & 1) * kSums;
             const long long row = t.row + rank * (kRows / 2) + 32 * quarter;
             const int rows = static_cast<int>(max(0LL, min(32LL, of.rows - row)));
             auto done_reading = [&] {
@@ -464,11 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             };
             if constexpr (MODE == kForward) {
                 constexpr int kCols = BN / 4;                  // outputs of a half
+                constexpr int kRead = kCols > 32 ? 64 : 32;    // (those past a half's are not used)
                 const FfKept& kept = pl.kept;
                 {
-                    float g[kCols], u[kCols];
-                    tmem_get<kCols>(sums + half * kCols, g);
-                    tmem_get<kCols>(sums + BN / 2 + half * kCols, u);
+                    float g[kRead], u[kRead];
+                    tmem_get<kRead>(sums + half * kCols, g);
+                    tmem_get<kRead>(sums + BN / 2 + half * kCols, u);
                     done_reading();
                     const int col = t.col + half * kCols, cols = of.cols - col;
                     if (rows == 0 || cols <= 0) continue;
@@ -551,13 +556,18 @@ cudaError_t launch_pair_of(const PairMaps& maps, const PairPlan& pl, int mode, i
                            cudaStream_t st) {
     // Items are counted in 32 bits.
     if (pl.of[0].items() + pl.of[1].items() > 0x7FFFFFFF / kGroup) return cudaErrorInvalidConfiguration;
-    if (mode == kForward) {
-        if (activation == kSilu)
-            return bn == 256 ? launch_pair<T, kForward, 256, kSilu>(maps, pl, st)
-                             : launch_pair<T, kForward, 128, kSilu>(maps, pl, st);
-        return bn == 256 ? launch_pair<T, kForward, 256, kGeluTanh>(maps, pl, st)
-                         : launch_pair<T, kForward, 128, kGeluTanh>(maps, pl, st);
-    }
+    const auto forward = [&](auto width) {
+        constexpr int BN = decltype(width)::value;
+        return activation == kSilu ? launch_pair<T, kForward, BN, kSilu>(maps, pl, st)
+                                   : launch_pair<T, kForward, BN, kGeluTanh>(maps, pl, st);
+    };
+    if (mode == kForward)
+        switch (bn) {
+            case 256: return forward(std::integral_constant<int, 256>());
+            case 224: return forward(std::integral_constant<int, 224>());
+            case 160: return forward(std::integral_constant<int, 160>());
+            default: return forward(std::integral_constant<int, 128>());
+        }
     return bn == 256 ? launch_pair<T, kBackward, 256, kSilu>(maps, pl, st)
                      : launch_pair<T, kBackward, 128, kSilu>(maps, pl, st);
 }

@@ -13,7 +13,7 @@
 //
 // The products: sgemm_ff_pair.cuh, and sgemm_ff_token.cu for up to 16 tokens.  Rows that are not on
 // 16 bytes cannot be read by tensor maps and are copied into the workspace first (3001 x 2047 and
-// 1999 x 2047 twice: 12 us beside a product of 36).
+// 1999 x 2047 twice: 12 us beside a product of 34).
 //
 // Measured (us, kernels alone): forward 8192 x 4096 x 8192 bf16 527 to 550 (2.0 to 2.1 PFLOP/s; the
 // measured rate of a library product is 1.9, sustained 1.7), with g and u kept in 8 bits 546; the
@@ -205,20 +205,24 @@ long long up_to(long long n, int m) { return (n + m - 1) / m; }
 
 constexpr int kTokens = 16;          // up to here sgemm_ff_token.cu
 constexpr int kPairsOfGpu = 76;      // 152 SMs
-// Clocks of a stage: four MMAs of 128 for 256 columns; narrower tiles wait for shared memory.  (Tiles
-// of 64 took 8.8 us where 128 took 7.0, 256x4096x1024, and at best 3 % less, 300x300x4096.)
-int stage_clocks(int bn) { return bn == 256 ? 512 : 320; }
+// Clocks of a stage: four MMAs of 128 for 256 columns; narrow tiles wait for shared memory.  (Tiles
+// of 64 took 8.8 us where 128 took 7.0, 256x4096x1024, and at best 3 % less, 300x300x4096; of 192, 400
+// clocks a stage, never the least.)
+int stage_clocks(int bn) { return bn == 160 ? 360 : std::max(2 * bn, 320); }
 
-// Rounds of tiles, each as long as its stages and, forward with three results, its epilogue.  The
-// model's choice was the fastest of all, or within 3 % of it, on 14 shapes from 17 to 16384 tokens.
+// Rounds of tiles, each as long as its stages.  The model's choice was the fastest of all, or
+// within 2 % of it, on 21 shapes from 17 to 12000 tokens.  Tiles of 224 and 160 columns are for h alone:
+// they fill the last round better (2048x2048x2048 22.9 us, by 256 24.2; 64x8192x4096 26.5, 30.7; 400x2500x5000
+// 30.7, 33.9), but store no whole 128-byte lines, which shows with three results (2000x2048x512,
+// gate and up kept: 256 12.8, 224 14.1).  A checkpoint's blocks of 64 are whole in a warp of 256 only.
 FfChoice choose_forward(int M, int N, int K, int keep) {
     if (M <= kTokens && keep != kKeep8) return FfChoice{0, 1};
     FfChoice best{256, 1};
     double least = 0;
-    for (int bn : {256, 128}) {
-        if (bn != 256 && keep == kKeep8) continue;      // a warp holds blocks of 64 whole
+    for (int bn : {256, 224, 160, 128}) {
+        if (bn != 256 && (keep == kKeep8 || (keep != kKeepNone && bn != 128))) continue;
         const long long rounds = up_to(up_to(M, kTileRows) * up_to(N, bn / 2), kPairsOfGpu);
-        const double t = static_cast<double>(rounds) * up_to(K, 64) * stage_clocks(bn) + 12.0 * bn;
+        const double t = static_cast<double>(rounds) * up_to(K, 64) * stage_clocks(bn) + 6.0 * bn;
         if (least == 0 || t < least) best.bn = bn, least = t;
     }
     return best;

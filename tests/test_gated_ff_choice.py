@@ -47,7 +47,7 @@ def test_every_kind_is_run_by_the_gpu_tests(lib):
         for product in (INPUT, WEIGHTS):
             columns, parts = choice(lib, *s, FULL, product)
             kinds[product].add((columns, parts > 1))
-    assert kinds[FORWARD] == {0, 128, 256}
+    assert kinds[FORWARD] == {0, 128, 160, 224, 256}
     assert kinds[INPUT] == kinds[WEIGHTS] == {(c, p) for c in (128, 256) for p in (False, True)}
 
 

@@ -20,7 +20,8 @@ T = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25}
 SHAPES = [(1, 1, 1), (1, 8, 16), (3, 5, 7), (1, 1000, 200), (8, 333, 257), (16, 64, 64), (17, 130, 100),
           (1, 2048, 4096), (5, 100, 8), (33, 64, 72), (128, 128, 64), (129, 257, 65), (256, 256, 256),
           (300, 520, 136), (257, 1000, 2047), (1000, 640, 1024), (64, 4096, 512), (700, 96, 1000),
-          (2000, 300, 64), (9, 2050, 1030), (513, 129, 320)]
+          (2000, 300, 64), (9, 2050, 1030), (513, 129, 320), (64, 8100, 250), (64, 8192, 256), (400, 2501, 200),
+          (400, 2504, 200), (2500, 1000, 64)]
 # Several rounds of tiles, every tile and split (test_gated_ff_choice.py).
 MANY = [(2600, 2100, 200), (4700, 2600, 72), (1000, 4100, 520), (900, 100, 6000), (9000, 64, 300),
         (40, 3000, 520), (3000, 40, 520), (20000, 260, 250), (12000, 500, 1000),
@@ -407,3 +408,21 @@ def test_long_offsets(sg, M, N, K):
             tol = 2 * sum_off + 2 * c.u * 1.01 * (b.abs() + 2 * sum_off) + c.t
             assert bool(((a.double() - b).abs() <= tol).all())
         del kept, got
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 200, 136), (64, 8100, 72), (64, 8200, 72), (400, 2501, 72), (400, 2496, 72),
+                                   (70, 7168, 64), (1300, 2560, 64), (7, 333, 72)])
+def test_forward_alone_writes_its_result_only(sg, M, N, K):
+    """h in a larger buffer through the C entry: tiles of every width, at the row's end and short of it."""
+    lib, s = sg.load(), torch.cuda.current_stream().cuda_stream
+    c = whole(Case(M, N, K, "bf16"))
+    g, u = c.x.double() @ c.wg.double().t(), c.x.double() @ c.wu.double().t()
+    for off, pad in ((0, 0), (0, 8), (1, 5)):
+        flat = torch.full((off + M * (N + pad) + 64,), 7.0, dtype=c.dt, device="cuda")
+        view = flat[off:off + M * (N + pad)].view(M, N + pad)[:, :N]
+        assert lib.sgemm_gated_ff_forward(M, N, K, 1, 0, c.x.data_ptr(), K, c.wg.data_ptr(), K, c.wu.data_ptr(), K,
+                                          view.data_ptr(), N + pad, 0, None, None, N, None, None, None, 0, s) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(view, (g * u).to(c.dt))
+        view.fill_(7.0)
+        assert bool((flat == 7.0).all())
