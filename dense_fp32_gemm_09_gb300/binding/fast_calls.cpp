@@ -525,7 +525,9 @@ PyObject* gated_ff(PyObject*, PyObject* const* a, Py_ssize_t n) {
             up = Kept::make(M, w.N);
         }
         size_t bytes = 0;
-        const int pack = packed(1, x, ldx) | packed(2, wg, w.ldg) | packed(4, wu, w.ldu);
+        const bool in_place = M <= 16 && keep != SGEMM_KEEP_8BIT;       // (include/sgemm.h)
+        const int pack =
+            in_place ? 0 : packed(1, x, ldx) | packed(2, wg, w.ldg) | packed(4, wu, w.ldu);
         if (pack)
             if (const int st = f_gated_ff_workspace(M, w.N, w.K, 0, pack, &bytes)) return status(st);
         const at::Tensor ws = workspace(bytes);

@@ -47,8 +47,9 @@ cudaError_t pair_bf16(const PairMaps& maps, const PairPlan& pl, int mode, int bn
                       cudaStream_t stream);
 cudaError_t pair_f16(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int activation,
                      cudaStream_t stream);
-// Forward of up to 16 tokens, without 8-bit checkpoints (sgemm_ff_token.cu); operands on 16 bytes, on32: on 32.
-cudaError_t launch_token(const GatedFfForward& p, bool on32, int sms, cudaStream_t stream);
+// Forward of up to 16 tokens, without 8-bit checkpoints (sgemm_ff_token.cu).  on: rows of the operands
+// are on so many bytes, 32, 16 or fewer.
+cudaError_t launch_token(const GatedFfForward& p, int on, int sms, cudaStream_t stream);
 
 }  // namespace ff
 }  // namespace sgemm

@@ -81,10 +81,85 @@ __device__ __forceinline__ Piece load_piece(const uint16_t* p, int n, bool on32)
     return r;
 }
 
+// The first and the end of a matrix in memory.
+struct Extent {
+    const uint8_t *first, *end;
+    __device__ __forceinline__ Extent(const void* p, long long rows, int cols, long long ld)
+        : first(static_cast<const uint8_t*>(p)), end(first + 2 * ((rows - 1) * ld + cols)) {}
+};
+// The same of a row that begins anywhere: the 16-byte groups that hold the numbers, as they are in
+// memory, and where the first number begins.  Groups that are partly outside the matrix are left for
+// later, so that what is on its way meets no branch.
+struct Groups {
+    uint4 v[3];
+    const uint8_t* at;
+    int skip, n;                 // bytes before the first number; numbers inside
+    int left;                    // bit j: group j is still to be read
+};
+__device__ __forceinline__ uint4 load_if(const uint8_t* p, bool yes) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(static_cast<uint32_t>(yes)));
+    return v;
+}
+__device__ __forceinline__ Groups load_groups(const uint16_t* p, int n, const Extent& m) {
+    Groups r;
+    r.skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    r.at = reinterpret_cast<const uint8_t*>(p) - r.skip;
+    r.n = n;
+    r.left = 0;
+    const int bytes = n > 0 ? r.skip + 2 * min(n, 16) : 0;   // needed from `at` on
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const uint8_t* const q = r.at + 16 * j;
+        const bool need = 16 * j < bytes, in = q >= m.first && q + 16 <= m.end;
+        r.v[j] = load_if(q, need && in);
+        r.left |= (need && !in) << j;
+    }
+    return r;
+}
+__device__ __forceinline__ uint4 load_part(const uint8_t* p, const Extent& m) {
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        h[i] = p + 2 * i >= m.first && p + 2 * i < m.end ? __ldg(reinterpret_cast<const uint16_t*>(p + 2 * i)) : 0u;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+// The numbers, cut out of the groups; zeros past the row's end.
+__device__ __forceinline__ Piece cut(Groups& g, const Extent& m) {
+    if (g.left) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (g.left >> j & 1) g.v[j] = load_part(g.at + 16 * j, m);
+    }
+    uint32_t w[12] = {g.v[0].x, g.v[0].y, g.v[0].z, g.v[0].w, g.v[1].x, g.v[1].y,
+                      g.v[1].z, g.v[1].w, g.v[2].x, g.v[2].y, g.v[2].z, g.v[2].w};
+#pragma unroll
+    for (int i = 0; i < 10; ++i) w[i] = g.skip & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) w[i] = g.skip & 4 ? w[i + 1] : w[i];
+    Piece r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (g.skip & 2));
+    if (g.n < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (2 * i + 1 >= g.n) r.w[i] = 2 * i < g.n ? r.w[i] & 0xFFFFu : 0u;
+    }
+    return r;
+}
+__device__ __forceinline__ const Piece& cut(const Piece& p, const Extent&) { return p; }
+
 // Persistent: a block takes the groups blockIdx.x, + gridDim.x, ... of eight outputs.
-// NT: groups of eight tokens.
-template <typename T, int ACT, int NT>
-__global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForward p, const bool on32) {
+// NT: groups of eight tokens.  ANY: rows that begin anywhere, with more registers for what is on its
+// way.  (Copied first to rows on 16 bytes, as the larger tiles need it, one token 8191 x 4095 took 83.4 us,
+// now 44.7, sixteen 88 and 55, one 1000 x 777 7.1 and 3.1.  Rows on 16 bytes take 23 and 25: here a third
+// load and 40 instructions to cut 16 numbers out, half the warps.)
+template <typename T, int ACT, int NT, bool ANY>
+__global__ void __launch_bounds__(kThreads, ANY ? 1 : 2) ff_token_kernel(const GatedFfForward p, const bool on32) {
     __shared__ float sums[2][kWarps][2][8][8 * NT];       // gate, up: [output][token]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -98,26 +173,36 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
     // (16 tokens, 16384 x 4096: two pieces ahead without x 53 us, one 43.4, with x 42.4).
     constexpr int kAhead = NT == 1 ? 2 : 1;
     constexpr bool kTokensAhead = NT == 2;
-    Piece a[kAhead][2], b[kTokensAhead ? kAhead : 1][NT];
-    auto load_tokens = [&](Piece (&to)[NT], int k) {
+    using Loaded = std::conditional_t<ANY, Groups, Piece>;
+    Loaded a[kAhead][2], b[kTokensAhead ? kAhead : 1][NT];
+    const Extent of_x(p.x, p.M, p.K, p.ldx), of_gate(w_gate, p.N, p.K, p.ldg), of_up(w_up, p.N, p.K, p.ldu);
+    auto load_tokens = [&](Loaded (&to)[NT], int k) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            to[n] = load_piece<false>(x + 8 * n * p.ldx + k, 8 * n + g < p.M ? p.K - k : 0, on32);
+        for (int n = 0; n < NT; ++n) {
+            const int left = 8 * n + g < p.M ? p.K - k : 0;
+            if constexpr (ANY) to[n] = load_groups(x + 8 * n * p.ldx + k, left, of_x);
+            else to[n] = load_piece<false>(x + 8 * n * p.ldx + k, left, on32);
+        }
     };
     int from = blockIdx.x, next = 0;
     const uint16_t* wg = nullptr;
     const uint16_t* wu = nullptr;
     auto load = [&](int i) {
         if (from >= groups) return;
-        Piece (&to)[2] = a[i];
+        Loaded (&to)[2] = a[i];
         if (next == 0) {                 // past the last output: its row again, not stored
             const long long row = min(8LL * from + g, p.N - 1LL);
             wg = w_gate + row * p.ldg;
             wu = w_up + row * p.ldu;
         }
         const int k = mine + next * (kWarps * kPiece);
-        to[0] = load_piece<true>(wg + k, p.K - k, on32);
-        to[1] = load_piece<true>(wu + k, p.K - k, on32);
+        if constexpr (ANY) {
+            to[0] = load_groups(wg + k, p.K - k, of_gate);
+            to[1] = load_groups(wu + k, p.K - k, of_up);
+        } else {
+            to[0] = load_piece<true>(wg + k, p.K - k, on32);
+            to[1] = load_piece<true>(wu + k, p.K - k, on32);
+        }
         if constexpr (kTokensAhead) load_tokens(b[i], k);
         if (++next == pieces) {
             next = 0;
@@ -135,13 +220,16 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
             if (group >= groups) break;
             const int k = mine + piece * (kWarps * kPiece);
             if constexpr (!kTokensAhead) load_tokens(b[0], k);
+            {
+                const Piece gate = cut(a[i][0], of_gate), up = cut(a[i][1], of_up);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const Piece& of = b[kTokensAhead ? i : 0][n];
+                for (int n = 0; n < NT; ++n) {
+                    const Piece of = cut(b[kTokensAhead ? i : 0][n], of_x);
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    mma16<T>(acc[n], a[i][0].w[2 * s], a[i][1].w[2 * s], a[i][0].w[2 * s + 1],
-                             a[i][1].w[2 * s + 1], of.w[2 * s], of.w[2 * s + 1]);
+                    for (int s = 0; s < 4; ++s)
+                        mma16<T>(acc[n], gate.w[2 * s], up.w[2 * s], gate.w[2 * s + 1], up.w[2 * s + 1],
+                                 of.w[2 * s], of.w[2 * s + 1]);
+                }
             }
             load(i);
             if (++piece < pieces) continue;
@@ -178,22 +266,24 @@ __global__ void __launch_bounds__(kThreads, 2) ff_token_kernel(const GatedFfForw
 }
 
 template <typename T, int ACT>
-cudaError_t launch(const GatedFfForward& p, bool on32, int sms, cudaStream_t st) {
+cudaError_t launch(const GatedFfForward& p, int on, int sms, cudaStream_t st) {
     const int groups = (p.N + 7) / 8;
-    const auto run = [&](auto kernel) {
-        return launch_dependent(kernel, dim3(std::min(groups, 2 * sms)), kThreads, 0, st, p, on32);
+    const auto run = [&](auto kernel, int blocks) {
+        return launch_dependent(kernel, dim3(std::min(groups, blocks * sms)), kThreads, 0, st, p, on == 32);
     };
-    return p.M <= 8 ? run(ff_token_kernel<T, ACT, 1>) : run(ff_token_kernel<T, ACT, 2>);
+    if (on < 16)
+        return p.M <= 8 ? run(ff_token_kernel<T, ACT, 1, true>, 1) : run(ff_token_kernel<T, ACT, 2, true>, 1);
+    return p.M <= 8 ? run(ff_token_kernel<T, ACT, 1, false>, 2) : run(ff_token_kernel<T, ACT, 2, false>, 2);
 }
 
 }  // namespace
 
-cudaError_t launch_token(const GatedFfForward& p, bool on32, int sms, cudaStream_t st) {
+cudaError_t launch_token(const GatedFfForward& p, int on, int sms, cudaStream_t st) {
     const bool silu = p.activation == kSilu;
     if (p.dtype == kBf16)
-        return silu ? launch<__nv_bfloat16, kSilu>(p, on32, sms, st)
-                    : launch<__nv_bfloat16, kGeluTanh>(p, on32, sms, st);
-    return silu ? launch<__half, kSilu>(p, on32, sms, st) : launch<__half, kGeluTanh>(p, on32, sms, st);
+        return silu ? launch<__nv_bfloat16, kSilu>(p, on, sms, st)
+                    : launch<__nv_bfloat16, kGeluTanh>(p, on, sms, st);
+    return silu ? launch<__half, kSilu>(p, on, sms, st) : launch<__half, kGeluTanh>(p, on, sms, st);
 }
 
 }  // namespace ff

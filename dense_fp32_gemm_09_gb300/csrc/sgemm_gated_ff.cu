@@ -12,7 +12,7 @@
 // alone is 1.7e-3, the weights' gradients of an x in 8 bits 2.8e-3.
 //
 // The products: sgemm_ff_pair.cuh, and sgemm_ff_token.cu for up to 16 tokens.  Rows that are not on
-// 16 bytes cannot be read by tensor maps and are copied into the workspace first (3001 x 2047 and
+// 16 bytes cannot be read by tensor maps and, for these, are copied into the workspace first (3001 x 2047 and
 // 1999 x 2047 twice: 12 us beside a product of 34).
 //
 // Measured (us, kernels alone): forward 8192 x 4096 x 8192 bf16 527 to 550 (2.0 to 2.1 PFLOP/s; the
@@ -343,22 +343,18 @@ cudaError_t pair(const PairMaps& maps, const PairPlan& pl, int mode, int bn, int
 
 template <typename T>
 cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* launches) {
-    const Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, p.ws);
-    cudaError_t e = in.copy(sms, st, launches);
-    if (e != cudaSuccess) return e;
     const FfChoice c = choose_forward(p.M, p.N, p.K, p.kept.keep);
     if (c.bn == 0) {
-        GatedFfForward q = p;
-        q.x = in.x;
-        q.w_gate = in.w_gate;
-        q.w_up = in.w_up;
-        q.ldx = in.ldx;
-        q.ldg = in.ldg;
-        q.ldu = in.ldu;
+        const auto all_on = [&](int bytes) {
+            return rows_on(bytes, p.x, p.M, p.ldx) && rows_on(bytes, p.w_gate, p.N, p.ldg) &&
+                   rows_on(bytes, p.w_up, p.N, p.ldu);
+        };
         ++*launches;
-        return launch_token(q, rows_on(32, in.x, p.M, in.ldx) && rows_on(32, in.w_gate, p.N, in.ldg) &&
-                                   rows_on(32, in.w_up, p.N, in.ldu), sms, st);
+        return launch_token(p, all_on(32) ? 32 : all_on(16) ? 16 : 2, sms, st);
     }
+    const Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, p.ws);
+    const cudaError_t e = in.copy(sms, st, launches);
+    if (e != cudaSuccess) return e;
     PairMaps maps;
     if (!encode(&maps.a[0], in.x, p.M, p.K, in.ldx, 128) ||
         !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, c.bn / 2) ||
@@ -497,6 +493,7 @@ size_t gated_ff_backward_workspace(int M, int N, int K, int packed) {
            static_cast<size_t>(parts * up64(K)) * sizeof(float);
 }
 int gated_ff_packed(const GatedFfForward& p) {
+    if (choose_forward(p.M, p.N, p.K, p.kept.keep).bn == 0) return 0;
     return packed_bit(1, p.x, p.M, p.ldx) | packed_bit(2, p.w_gate, p.N, p.ldg) |
            packed_bit(4, p.w_up, p.N, p.ldu);
 }

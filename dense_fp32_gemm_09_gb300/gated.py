@@ -48,6 +48,10 @@ def _layer(ref, name: str, w_gate, w_up, inputs=None):
     return N, K, ldg, ldu
 
 
+# Forward calls of up to so many tokens read every matrix in place, unless they keep 8-bit checkpoints.
+_FEW_TOKENS = 16
+
+
 def _packed(bit: int, t, ld: int) -> int:
     """`bit` where the kernels read a copy of a matrix: its rows are not 16-byte aligned."""
     aligned = t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or ld % 8 == 0)
@@ -95,6 +99,8 @@ def gated_ff(x, w_gate, w_up, *, activation: str = "silu", keep: str | None = No
         (gate, gs), (up, us) = (q._addresses() for q in kept)
         at = (gate, up, gs, us)
     packed = _packed(_X, x, ldx) | _packed(_GATE, w_gate, ldg) | _packed(_UP, w_up, ldu)
+    if M <= _FEW_TOKENS and keep != "8bit":
+        packed = 0
     ws, size = _workspace(call, M, N, K, 0, packed)
     call.run("sgemm_gated_ff_forward", M, N, K, dt, act, x.data_ptr(), ldx, w_gate.data_ptr(), ldg,
              w_up.data_ptr(), ldu, h.data_ptr(), N, KEEP[keep], at[0], at[1], ldk, at[2], at[3],

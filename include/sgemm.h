@@ -512,7 +512,8 @@ SGEMM_API int sgemm_layer_norm_backward(int rows, int cols, int dtype, const voi
  * codes, with gate_scales and up_scales), made from the fp32 sums.
  *
  * A matrix is read in place if its address and (with more than one row) its row stride are
- * multiples of 16 bytes, and otherwise copied into the workspace first.  `ws` is the caller's
+ * multiples of 16 bytes, or in a forward call of up to 16 tokens that keeps no 8-bit
+ * checkpoints, and otherwise copied into the workspace first.  `ws` is the caller's
  * device memory: 128-byte aligned, at least as many bytes as sgemm_gated_ff_workspace gives for
  * these sizes (`backward` 0 or 1; `packed`: 1 for an x, 2 for a w_gate, 4 for a w_up that is
  * copied, or for an x given in 8 bits); it needs no initialisation and must stay untouched by

@@ -269,7 +269,8 @@ def test_nothing_outside_the_outputs_is_written(sg, M, N, K, keep):
             qs = [sg.act8_quantize(torch.zeros(M, N, device="cuda")) for _ in range(2)]
             k_at = (qs[0].codes.data_ptr(), qs[1].codes.data_ptr(), 0, qs[0].scales.data_ptr(),
                     qs[1].scales.data_ptr())
-        w, n = ws(0, packed)
+        # (Up to 16 tokens without 8-bit checkpoints: every matrix is read in place.)
+        w, n = ws(0, 0 if M <= 16 and keep == 1 else packed)
         args = (M, N, K, 1, 0, c.x.data_ptr(), K, c.wg.data_ptr(), K, c.wu.data_ptr(), K, h.data_ptr(), N + pad,
                 keep, *k_at)
         if n:
