@@ -24,11 +24,12 @@
 //     memory, to store whole 128-byte lines.
 //
 // Four MMAs of a stage take 512 clocks, so a tile of 256 x 256 x 2048 takes 8.5 us at 1.93 GHz; measured
-// are 10.2 to 12 with its share of the start and the end.  The tensor pipes are active 87 to 90 % of the
-// time (4096 x 2048 x 4096); at full size the card's power limit holds the clock lower.  Tiles of
-// 256 x 128 fill more pairs where there are few, and forward tiles of 224 and 160 columns the last round
-// better: 3001 x 2047 x 1999 has 192 tiles of 256 for 76 pairs, 2.5 rounds that take 3, and takes 47.6 us
-// by them, by 216 tiles of 224 44.9 (copies of the operands included).
+// are 10.2 to 12 with its share of the start and the end.  The tensor pipes are active 84 (forward, g
+// and u to 8 bits) and 93 % of the time (gradient), 4096 x 2048 x 4096; at full size the card's power
+// limit holds the clock lower.  Tiles of 256 x 128 fill more pairs where there are few, and forward tiles
+// of 224 and 160 columns the last round better: 3001 x 2047 x 1999 has 192 tiles of 256 for 76 pairs, 2.5
+// rounds that take 3, and takes 47.6 us by them, by 216 tiles of 224 44.9 (copies of the operands
+// included).
 #pragma once
 
 #include <cuda_runtime.h>
