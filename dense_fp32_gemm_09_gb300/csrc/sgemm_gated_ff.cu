@@ -13,7 +13,7 @@
 //
 // The products: sgemm_ff_pair.cuh, and sgemm_ff_token.cu for up to 16 tokens.  Rows that are not on
 // 16 bytes cannot be read by tensor maps and, for these, are copied into the workspace first (3001 x 2047 and
-// 1999 x 2047 twice: 12 us beside a product of 34).
+// 1999 x 2047 twice: 10 us beside a product of 34).
 //
 // Measured (us, kernels alone): forward 8192 x 4096 x 8192 bf16 527 to 550 (2.0 to 2.1 PFLOP/s; the
 // measured rate of a library product is 1.9, sustained 1.7), with g and u kept in 8 bits 546; the
@@ -116,9 +116,7 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// Matrices of 2-byte numbers into rows of `pitch`, a warp a row, two numbers a lane; blockIdx.y:
-// which.  Rows that start between two words are read in whole words all the same, and a word
-// of the copy is made of the second number of the lane before and the first of its own.
+// Matrices of 2-byte numbers into rows of `pitch`, a warp a row; blockIdx.y: which.
 struct Copies {
     const uint16_t* from[3];
     uint16_t* to[3];
@@ -126,6 +124,43 @@ struct Copies {
     int cols;
     long long pitch;
 };
+// One row, eight numbers a lane: the row's 16-byte groups of memory, cut at the place where it begins.
+// All of the groups are inside the matrix.  (Numbers past the row's end may be written: the copy's
+// rows are padded.)
+__device__ __forceinline__ void copy_groups(const uint16_t* x, uint16_t* y, int cols) {
+    constexpr int kEach = 4;             // of a lane on their way
+    const int lane = threadIdx.x & 31, skip = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15);
+    const uint4* const at = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(x) - skip);
+    const int groups = (skip + 2 * cols + 15) / 16, out = (cols + 7) / 8;
+    const auto get = [&](int i) { return i < groups ? __ldg(at + i) : make_uint4(0, 0, 0, 0); };
+    for (int start = lane; start - lane < out; start += 32 * kEach) {
+        uint4 own[kEach], last[kEach];   // (lane 31: the next lane's)
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            own[j] = get(start + 32 * j);
+            if (lane == 31) last[j] = get(start + 32 * j + 1);
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            uint32_t w[8] = {own[j].x, own[j].y, own[j].z, own[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
+            if (lane == 31) w[4] = last[j].x, w[5] = last[j].y, w[6] = last[j].z, w[7] = last[j].w;
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = skip & 8 ? w[i + 2] : w[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = skip & 4 ? w[i + 1] : w[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (skip & 2));
+            if (start + 32 * j < out)
+                reinterpret_cast<uint4*>(y)[start + 32 * j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+// Rows near the matrix's ends, whose first or last group is partly outside: two numbers a lane.  Rows
+// that start between two words are read in whole words all the same, and a word of the copy is
+// made of the second number of the lane before and the first of its own.  (All rows so: 3001 x 2047
+// x 1999 forward 46.5 us, now 44.4; 100 x 4001 x 4001 52.4 and 47.3.)
 __global__ void __launch_bounds__(kThreads) ff_copy_rows(const Copies q) {
     constexpr int kWords = 8;            // of a lane on their way
     const int which = blockIdx.y, lane = threadIdx.x & 31;
@@ -135,6 +170,11 @@ __global__ void __launch_bounds__(kThreads) ff_copy_rows(const Copies q) {
          row += warps) {
         const uint16_t* const x = q.from[which] + row * q.ld[which];
         uint16_t* const y = q.to[which] + row * q.pitch;
+        // (Seven numbers of a group may lie before the row, and as many after it.)
+        if (row * q.ld[which] >= 8 && (q.rows[which] - 1 - row) * q.ld[which] >= 8) {
+            copy_groups(x, y, q.cols);
+            continue;
+        }
         const int off = reinterpret_cast<uintptr_t>(x) & 2 ? 1 : 0;
         for (int start = 0; start < q.cols; start += 64 * kWords) {
             uint32_t w[kWords];
