@@ -19,16 +19,17 @@ constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
 struct Act {
-    float s, slope_z, g;
+    float s, slope_z, g, near;
     template <int ACT>
     __device__ __forceinline__ static Act of(float g) {
         Act a;
-        a.g = g;
+        a.g = a.near = g;
         float z = g;
         a.slope_z = 1.0f;
         if (ACT == kGeluTanh) {
-            // From |g| = 30 on s is 0 or 1, and beyond 10^19 g^2 would overflow.
-            const float c = fminf(fmaxf(g, -30.0f), 30.0f), q = c * c;
+            // From |g| = 30 on s is 0 or 1, and beyond 10^19 g^2 would overflow.  (A NaN stays one.)
+            const float c = fabsf(g) > 30.0f ? copysignf(30.0f, g) : g, q = c * c;
+            a.near = c;
             z = kGeluC * c * fmaf(kGeluCube, q, 1.0f);
             a.slope_z = kGeluC * fmaf(3.0f * kGeluCube, q, 1.0f);
         }
@@ -36,7 +37,8 @@ struct Act {
         return a;
     }
     __device__ __forceinline__ float value() const { return g * s; }
-    __device__ __forceinline__ float slope() const { return s * fmaf(g * (1.0f - s), slope_z, 1.0f); }
+    // (With g itself, g slope_z is infinite from -1.8e36 down, and 0 times that NaN.)
+    __device__ __forceinline__ float slope() const { return s * fmaf(near * (1.0f - s), slope_z, 1.0f); }
 };
 template <int ACT>
 __device__ __forceinline__ float act(float g) { return Act::of<ACT>(g).value(); }
