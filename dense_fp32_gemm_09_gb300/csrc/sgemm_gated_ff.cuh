@@ -12,9 +12,14 @@ using mx4::kBf16;
 using mx4::to_float;
 
 // act(g) = g s with s = 1 / (1 + e^-z): z = g for silu; for the tanh form of gelu,
-// g (1 + tanh t) / 2 with t = c (g + 0.044715 g^3), c = sqrt(2 / pi), it is z = 2 t.  The
-// approximate exponential and reciprocal are off by a few 2^-22 of s, far below the 2-byte
-// rounding of what is made of it.
+// g (1 + tanh t) / 2 with t = c (g + 0.044715 g^3), c = sqrt(2 / pi), it is z = 2 t.
+//
+// With e = e^-|z|, s = 1 / (1 + e) or, where z < 0, e / (1 + e): e is at most 1, so that no
+// z leaves fp32 before s does.  (1 / (1 + e^-z) by the fast reciprocal was 0 from z = -87.4 down, where
+// s is 1e-38, and bf16's g s u an ordinary number if u is large.)  The fast exponential is off by up to
+// 2 + 1.173 |z| units of 2^-23 (CUDA's bound), so s by about 2^-20 of itself at z = -3, 2^-18 at -20 and
+// 2^-16 at -80, and less where z > 0: e is then the smaller part of 1 + e.  h and what the products
+// take are rounded to 2^-8 or 2^-11 afterwards.
 constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
@@ -33,7 +38,8 @@ struct Act {
             z = kGeluC * c * fmaf(kGeluCube, q, 1.0f);
             a.slope_z = kGeluC * fmaf(3.0f * kGeluCube, q, 1.0f);
         }
-        a.s = __fdividef(1.0f, 1.0f + __expf(-z));
+        const float e = __expf(-fabsf(z)), r = __fdividef(1.0f, 1.0f + e);
+        a.s = z < 0.0f ? e * r : r;
         return a;
     }
     __device__ __forceinline__ float value() const { return g * s; }
