@@ -131,7 +131,8 @@ __device__ __forceinline__ void copy_groups(const uint16_t* x, uint16_t* y, int 
     constexpr int kEach = 4;             // of a lane on their way
     const int lane = threadIdx.x & 31, skip = static_cast<int>(reinterpret_cast<uintptr_t>(x) & 15);
     const uint4* const at = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(x) - skip);
-    const int groups = (skip + 2 * cols + 15) / 16, out = (cols + 7) / 8;
+    // (Counted in numbers: in bytes, rows of 2^30 columns would pass 2^31.)
+    const int groups = (skip / 2 + cols + 7) / 8, out = (cols + 7) / 8;
     const auto get = [&](int i) { return i < groups ? __ldg(at + i) : make_uint4(0, 0, 0, 0); };
     for (int start = lane; start - lane < out; start += 32 * kEach) {
         uint4 own[kEach], last[kEach];   // (lane 31: the next lane's)
