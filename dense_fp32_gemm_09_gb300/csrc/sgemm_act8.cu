@@ -29,12 +29,12 @@ constexpr int kThreads = 256, kAhead = 2;
 // 32 bytes of a row, at any 16.
 __device__ __forceinline__ void load_pair(const void* p, bool on32, uint4 (&v)[2]) {
     if (on32) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
                        "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w) : "l"(p));
     } else {
-        v[0] = __ldg(static_cast<const uint4*>(p));
-        v[1] = __ldg(static_cast<const uint4*>(p) + 1);
+        v[0] = fetch(static_cast<const uint4*>(p));
+        v[1] = fetch(static_cast<const uint4*>(p) + 1);
     }
 }
 __device__ __forceinline__ void store_pair(void* p, bool on32, const uint4 (&v)[2]) {
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_rows(const Act8Quantiz
             const T* x = static_cast<const T*>(q.X) + at.row * q.ldx + col[i];
             if (at.row < q.rows) {
                 if (col[i] + COLS <= q.cols) load_pair(x, on32, raw[i]);
-                else if (col[i] < q.cols) raw[i][0] = __ldg(reinterpret_cast<const uint4*>(x));
+                else if (col[i] < q.cols) raw[i][0] = fetch(reinterpret_cast<const uint4*>(x));
             }
             at.next();
         }
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quant
         const int left = q.cols - c0, kept = static_cast<int>(pitch) - at.col * 256;
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 32 * i < left ? to_float(__ldg(x + 32 * i)) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = 32 * i < left ? to_float(fetch(x + 32 * i)) : 0.0f;
         keep_singles(v, codes, q.scales + at.row * (pitch / kAct8Block) + at.col * 4, kept);
     }
 }
@@ -130,11 +130,11 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequa
                     codes[i][2] = w.z;
                     codes[i][3] = w.w;
                 } else {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(q.codes + k));
+                    const uint2 w = fetch(reinterpret_cast<const uint2*>(q.codes + k));
                     codes[i][0] = w.x;
                     codes[i][1] = w.y;
                 }
-                scale[i] = __ldg(q.scales + k / kAct8Block);
+                scale[i] = fetch(q.scales + k / kAct8Block);
                 to[i] = static_cast<T*>(q.Y) + at.row * q.ldy + at.col * COLS;
                 both[i] = at.col * COLS + COLS <= q.cols;
             }
@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_ragged(const Act8Deq
         int8_t code[8];
         float scale[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) code[i] = 32 * i < kept ? __ldg(codes + 32 * i) : int8_t(0);
+        for (int i = 0; i < 8; ++i) code[i] = 32 * i < kept ? fetch(codes + 32 * i) : int8_t(0);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) scale[b] = 64 * b < kept ? __ldg(scales + b) : 0.0f;
+        for (int b = 0; b < 4; ++b) scale[b] = 64 * b < kept ? fetch(scales + b) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (32 * i < left) y[32 * i] = from_float<T>(value(code[i], scale[i / 2]));

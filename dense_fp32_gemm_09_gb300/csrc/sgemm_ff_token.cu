@@ -57,16 +57,16 @@ __device__ __forceinline__ Piece load_piece(const uint16_t* p, int n, bool on32)
         if (on32) {
             if (ONCE)
                 asm volatile(
-                    "ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                    "ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
                       "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7]) : "l"(p));
             else
-                asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                              : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
                                "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7]) : "l"(p));
         } else {
-            const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p));
-            const uint4 hi = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+            const uint4 lo = fetch_here(reinterpret_cast<const uint4*>(p));
+            const uint4 hi = fetch_here(reinterpret_cast<const uint4*>(p) + 1);
             r.w[0] = lo.x; r.w[1] = lo.y; r.w[2] = lo.z; r.w[3] = lo.w;
             r.w[4] = hi.x; r.w[5] = hi.y; r.w[6] = hi.z; r.w[7] = hi.w;
         }
@@ -75,8 +75,8 @@ __device__ __forceinline__ Piece load_piece(const uint16_t* p, int n, bool on32)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         r.w[i] = 0;
-        if (2 * i < n) r.w[i] = __ldg(p + 2 * i);
-        if (2 * i + 1 < n) r.w[i] |= static_cast<uint32_t>(__ldg(p + 2 * i + 1)) << 16;
+        if (2 * i < n) r.w[i] = fetch_here(p + 2 * i);
+        if (2 * i + 1 < n) r.w[i] |= static_cast<uint32_t>(fetch_here(p + 2 * i + 1)) << 16;
     }
     return r;
 }
@@ -96,15 +96,6 @@ struct Groups {
     int skip, n;                 // bytes before the first number; numbers inside
     int left;                    // bit j: group j is still to be read
 };
-__device__ __forceinline__ uint4 load_if(const uint8_t* p, bool yes) {
-    uint4 v;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
-        "@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(static_cast<uint32_t>(yes)));
-    return v;
-}
 __device__ __forceinline__ Groups load_groups(const uint16_t* p, int n, const Extent& m) {
     Groups r;
     r.skip = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
@@ -116,7 +107,7 @@ __device__ __forceinline__ Groups load_groups(const uint16_t* p, int n, const Ex
     for (int j = 0; j < 3; ++j) {
         const uint8_t* const q = r.at + 16 * j;
         const bool need = 16 * j < bytes, in = q >= m.first && q + 16 <= m.end;
-        r.v[j] = load_if(q, need && in);
+        r.v[j] = fetch_if(q, need && in);
         r.left |= (need && !in) << j;
     }
     return r;
@@ -125,7 +116,7 @@ __device__ __forceinline__ uint4 load_part(const uint8_t* p, const Extent& m) {
     uint32_t h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        h[i] = p + 2 * i >= m.first && p + 2 * i < m.end ? __ldg(reinterpret_cast<const uint16_t*>(p + 2 * i)) : 0u;
+        h[i] = p + 2 * i >= m.first && p + 2 * i < m.end ? fetch_here(reinterpret_cast<const uint16_t*>(p + 2 * i)) : 0u;
     return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
 }
 // The numbers, cut out of the groups; zeros past the row's end.

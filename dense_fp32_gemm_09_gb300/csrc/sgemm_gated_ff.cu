@@ -39,7 +39,7 @@ constexpr int kThreads = 256;
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
     if (vec && n >= 8) {
-        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 raw = fetch_here(reinterpret_cast<const uint4*>(p));
         const T* t = reinterpret_cast<const T*>(&raw);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kThreads)
             const long long k = row * codes + c;
             const auto held = [&](const void* from, const float* scales, float (&v)[8]) {
                 const uint2 w =
-                    __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(from) + k));
-                const float s = __ldg(scales + k / kAct8Block);
+                    fetch_here(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(from) + k));
+                const float s = fetch_here(scales + k / kAct8Block);
                 mx4::Two t[4];
                 act8::values4(w.x, s, reinterpret_cast<mx4::Two(&)[2]>(t[0]));
                 act8::values4(w.y, s, reinterpret_cast<mx4::Two(&)[2]>(t[2]));
@@ -133,7 +133,7 @@ __device__ __forceinline__ void copy_groups(const uint16_t* x, uint16_t* y, int 
     const uint4* const at = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(x) - skip);
     // (Counted in numbers: in bytes, rows of 2^30 columns would pass 2^31.)
     const int groups = (skip / 2 + cols + 7) / 8, out = (cols + 7) / 8;
-    const auto get = [&](int i) { return i < groups ? __ldg(at + i) : make_uint4(0, 0, 0, 0); };
+    const auto get = [&](int i) { return i < groups ? fetch_here(at + i) : make_uint4(0, 0, 0, 0); };
     for (int start = lane; start - lane < out; start += 32 * kEach) {
         uint4 own[kEach], last[kEach];   // (lane 31: the next lane's)
 #pragma unroll
@@ -184,9 +184,9 @@ __global__ void __launch_bounds__(kThreads) ff_copy_rows(const Copies q) {
             for (int j = 0; j < kWords; ++j) {
                 const int c = start + 64 * j + 2 * lane + off;     // of the word read
                 w[j] = before[j] = 0;
-                if (c + 1 < q.cols) w[j] = __ldg(reinterpret_cast<const uint32_t*>(x + c));
-                else if (c < q.cols) w[j] = __ldg(x + c);
-                if (off && lane == 0 && c <= q.cols) before[j] = __ldg(x + c - 1);
+                if (c + 1 < q.cols) w[j] = fetch_here(reinterpret_cast<const uint32_t*>(x + c));
+                else if (c < q.cols) w[j] = fetch_here(x + c);
+                if (off && lane == 0 && c <= q.cols) before[j] = fetch_here(x + c - 1);
             }
 #pragma unroll
             for (int j = 0; j < kWords; ++j) {

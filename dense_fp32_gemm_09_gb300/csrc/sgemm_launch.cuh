@@ -3,6 +3,9 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
 
 namespace sgemm {
 
@@ -17,6 +20,47 @@ __device__ __forceinline__ void launch_next() {
 __device__ __forceinline__ void start_dependent() {
     launch_next();
     wait_previous();
+}
+
+// A read of global memory after the wait.  A load of data that stays as it is for the whole kernel
+// (__ldg, ld.global.nc, the compiler's own choice for const pointers that are __restrict__) may be moved
+// to before the wait, where the previous kernel still writes: the assembler does, whatever the
+// source's order.  So kernels that are launched as dependents use none.
+template <typename T>
+__device__ __forceinline__ T fetch(const T* p) {
+    __builtin_assume(__isGlobal(p));
+    return *p;
+}
+// The same, issued where it stands in the source, for loads among branches and stores.  (Feed-forward block
+// 16 x 4096 x 16384 43.3 us, with fetch 44.2; but layer norm of 9001 x 10883 fp16, forward and gradient,
+// 696 with this, 661 with fetch.)
+template <typename T>
+__device__ __forceinline__ T fetch_here(const T* p) {
+    static_assert(std::is_trivially_copyable<T>::value, "a number or a vector of them");
+    union {
+        T value;
+        uint32_t w[sizeof(T) < 4 ? 1 : sizeof(T) / 4];
+    } r;
+    if constexpr (sizeof(T) == 16)
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "l"(p));
+    else if constexpr (sizeof(T) == 8)
+        asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p));
+    else if constexpr (sizeof(T) == 4) asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+    else if constexpr (sizeof(T) == 2) asm volatile("ld.global.u16 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+    else asm volatile("ld.global.u8 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+    return r.value;
+}
+
+// 16 bytes so, or zeros.
+__device__ __forceinline__ uint4 fetch_if(const void* p, bool yes) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+        "@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(static_cast<uint32_t>(yes)));
+    return v;
 }
 
 template <typename... P, typename... A>

@@ -67,12 +67,13 @@ __device__ __forceinline__ float block_sum(float v) {
 
 __device__ __forceinline__ float shared_at(const void* w, int wtype, int c, float none) {
     if (w == nullptr) return none;
-    if (wtype == kF32) return __ldg(static_cast<const float*>(w) + c);
-    if (wtype == kBf16) return to_float(__ldg(static_cast<const __nv_bfloat16*>(w) + c));
-    return to_float(__ldg(static_cast<const __half*>(w) + c));
+    if (wtype == kF32) return fetch(static_cast<const float*>(w) + c);
+    if (wtype == kBf16) return to_float(fetch(static_cast<const __nv_bfloat16*>(w) + c));
+    return to_float(fetch(static_cast<const __half*>(w) + c));
 }
 
-// One row per block, read once for each pass.
+// One row per block, read once for each pass; kBatch numbers of a thread are loaded before one is stored.
+constexpr int kBatch = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerNormForward p) {
     const int D = p.cols;
@@ -82,12 +83,12 @@ __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerN
         T* y = static_cast<T*>(p.y) + row * p.ldy;
         float s = 0.0f;
 #pragma unroll 8
-        for (int c = threadIdx.x; c < D; c += kThreads) s += to_float(__ldg(x + c));
+        for (int c = threadIdx.x; c < D; c += kThreads) s += to_float(fetch(x + c));
         const float m = block_sum(s) / static_cast<float>(D);
         s = 0.0f;
 #pragma unroll 8
         for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float d = to_float(__ldg(x + c)) - m;
+            const float d = to_float(fetch(x + c)) - m;
             s = fmaf(d, d, s);
         }
         const float r = rsqrtf(block_sum(s) / static_cast<float>(D) + p.eps);
@@ -95,12 +96,20 @@ __global__ void __launch_bounds__(kThreads) layer_norm_forward_wide(const LayerN
             p.mean[row] = m;
             p.rstd[row] = r;
         }
-#pragma unroll 8
-        for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float n = (to_float(__ldg(x + c)) - m) * r;
-            y[c] = from_float<T>(fmaf(n, shared_at(p.weight, p.weight_dtype, c, 1.0f),
+        const auto result = [&](int c) {
+            const float n = (to_float(fetch(x + c)) - m) * r;
+            return from_float<T>(fmaf(n, shared_at(p.weight, p.weight_dtype, c, 1.0f),
                                       shared_at(p.bias, p.weight_dtype, c, 0.0f)));
+        };
+        int c = threadIdx.x;
+        for (; c + (kBatch - 1) * kThreads < D; c += kBatch * kThreads) {
+            T v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) v[i] = result(c + i * kThreads);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) y[c + i * kThreads] = v[i];
         }
+        for (; c < D; c += kThreads) y[c] = result(c);
     }
 }
 
@@ -115,10 +124,10 @@ struct Normed {
         : x(static_cast<const T*>(p.x) + row * p.ldx),
           codes(p.codes ? p.codes + row * act8_pitch(p.cols) : nullptr),
           scales(p.codes ? p.scales + row * (act8_pitch(p.cols) / kAct8Block) : nullptr),
-          m(__ldg(p.mean + row)), r(__ldg(p.rstd + row)) {}
+          m(fetch(p.mean + row)), r(fetch(p.rstd + row)) {}
     __device__ __forceinline__ float at(int c) const {
-        const float v = codes ? value(__ldg(codes + c), __ldg(scales + c / kAct8Block))
-                              : to_float(__ldg(x + c));
+        const float v = codes ? value(fetch(codes + c), fetch(scales + c / kAct8Block))
+                              : to_float(fetch(x + c));
         return (v - m) * r;
     }
 };
@@ -137,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) layer_norm_backward_wide(const Layer
         float sg = 0.0f, sn = 0.0f;
 #pragma unroll 4
         for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(__ldg(dh + c));
+            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(fetch(dh + c));
             sg += g;
             sn = fmaf(g, n.at(c), sn);
         }
@@ -158,9 +167,9 @@ __global__ void __launch_bounds__(kThreads) layer_norm_backward_wide(const Layer
         const float mg = sg * inv, mn = sn * inv;
 #pragma unroll 4
         for (int c = threadIdx.x; c < D; c += kThreads) {
-            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(__ldg(dh + c));
+            const float g = shared_at(p.weight, p.weight_dtype, c, 1.0f) * to_float(fetch(dh + c));
             float t = n.r * (g - mg - n.at(c) * mn);
-            if (p.dy) t += to_float(__ldg(dy + c));
+            if (p.dy) t += to_float(fetch(dy + c));
             dx[c] = from_float<T>(t);
         }
     }
@@ -180,7 +189,7 @@ __global__ void __launch_bounds__(32 * kStripWarps)
     if (c < p.cols) {
 #pragma unroll 4
         for (long long row = first + warp; row < end; row += kStripWarps) {
-            const float h = to_float(__ldg(static_cast<const T*>(p.dh) + row * p.lddh + c));
+            const float h = to_float(fetch(static_cast<const T*>(p.dh) + row * p.lddh + c));
             sb += h;
             sw = fmaf(h, Normed<T>(p, row).at(c), sw);
         }

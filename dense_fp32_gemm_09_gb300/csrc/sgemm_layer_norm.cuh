@@ -73,7 +73,7 @@ struct Single {
     __device__ __forceinline__ void load(const T* row, Row& to) const {
         row += first;
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) to.v[i] = in(i) ? __ldg(row + 32 * i) : T(0.0f);
+        for (int i = 0; i < OWN; ++i) to.v[i] = in(i) ? fetch(row + 32 * i) : T(0.0f);
     }
     template <typename S>
     __device__ __forceinline__ void store(S* row, const Two (&x)[kPairs2]) const {
@@ -90,8 +90,8 @@ struct Single {
         w += first;
 #pragma unroll
         for (int j = 0; j < kPairs2; ++j)
-            x[j] = two(in(2 * j) ? to_float(__ldg(w + 64 * j)) : 0.0f,
-                       in(2 * j + 1) ? to_float(__ldg(w + 64 * j + 32)) : 0.0f);
+            x[j] = two(in(2 * j) ? to_float(fetch(w + 64 * j)) : 0.0f,
+                       in(2 * j + 1) ? to_float(fetch(w + 64 * j + 32)) : 0.0f);
     }
     // Weights; ones where there are none.
     __device__ __forceinline__ void weights(const void* w, int type, Two (&x)[kPairs2]) const {
@@ -136,7 +136,7 @@ struct Shifted {
     };
     __device__ __forceinline__ void load(const T* row, Row& to) const {
         body.load(row + head, to.body);
-        to.single = single >= 0 ? __ldg(row + single) : T(0.0f);
+        to.single = single >= 0 ? fetch(row + single) : T(0.0f);
     }
     __device__ __forceinline__ void store(T* row, const Two (&x)[kPairs2]) const {
         body.store(row + head, reinterpret_cast<const Two(&)[OWN / 2]>(x));
@@ -154,9 +154,9 @@ struct Shifted {
 #pragma unroll
         for (int j = 0; j < OWN / 2; ++j) {
             const int i = 2 * j / kWidth, at = head + body.c[i] + 2 * j % kWidth;
-            x[j] = in(i) ? two(to_float(__ldg(w + at)), to_float(__ldg(w + at + 1))) : twice(0.0f);
+            x[j] = in(i) ? two(to_float(fetch(w + at)), to_float(fetch(w + at + 1))) : twice(0.0f);
         }
-        x[OWN / 2] = two(single >= 0 ? to_float(__ldg(w + single)) : 0.0f, 0.0f);
+        x[OWN / 2] = two(single >= 0 ? to_float(fetch(w + single)) : 0.0f, 0.0f);
     }
     __device__ __forceinline__ void weights(const void* w, int type, Two (&x)[kPairs2]) const {
         if (w == nullptr) {
@@ -507,9 +507,9 @@ struct KeptRow {
         row += own.first;
         scales += own.first / kAct8Block;
 #pragma unroll
-        for (int i = 0; i < OWN; ++i) code[i] = own.in(i) ? __ldg(row + 32 * i) : int8_t(0);
+        for (int i = 0; i < OWN; ++i) code[i] = own.in(i) ? fetch(row + 32 * i) : int8_t(0);
 #pragma unroll
-        for (int i = 0; i < OWN / 2; ++i) scale[i] = own.in(2 * i) ? __ldg(scales + i) : 0.0f;
+        for (int i = 0; i < OWN / 2; ++i) scale[i] = own.in(2 * i) ? fetch(scales + i) : 0.0f;
     }
     __device__ __forceinline__ Two pair(int j) const {
         return two(act8::value(code[2 * j], scale[j]), act8::value(code[2 * j + 1], scale[j]));
@@ -665,8 +665,8 @@ __global__ void __launch_bounds__(512, 1) backward_block(const LayerNormBackward
             kept.load(own, p.codes + row * pitch + slice.first,
                       p.scales + (row * pitch + slice.first) / kAct8Block);
         else own.load(x_at + row * p.ldx, x);
-        m = __ldg(p.mean + row);
-        r = __ldg(p.rstd + row);
+        m = fetch(p.mean + row);
+        r = fetch(p.rstd + row);
     };
     if (first_row < p.rows) {
         load(first_row);
@@ -789,25 +789,25 @@ __global__ void __launch_bounds__(512, 1) backward_ring(const LayerNormBackward 
     int8_t code_1 = 0;
     float scale_1 = 0.0f, sw_1 = 0.0f, sb_1 = 0.0f;
     auto load = [&](long long row) {       // what is not in the ring
-        m = __ldg(p.mean + row);
-        r = __ldg(p.rstd + row);
+        m = fetch(p.mean + row);
+        r = fetch(p.rstd + row);
         if constexpr (KEPT)
 #pragma unroll
             for (int i = 0; i < O::kGroups; ++i)
 #pragma unroll
                 for (int j = 0; j < kScales; ++j)
-                    scale[i][j] = own.c[i] < D ? __ldg(p.scales + (row * pitch + slice.first + head + own.c[i] +
+                    scale[i][j] = own.c[i] < D ? fetch(p.scales + (row * pitch + slice.first + head + own.c[i] +
                                                                    j * (VEC - 1)) / kAct8Block) : 0.0f;
         if (kOutside && outside >= 0) {
             const int c = slice.first + outside;
-            dh_1 = __ldg(static_cast<const T*>(p.dh) + row * p.lddh + c);
+            dh_1 = fetch(static_cast<const T*>(p.dh) + row * p.lddh + c);
             if constexpr (KEPT) {
-                code_1 = __ldg(p.codes + row * pitch + c);
-                scale_1 = __ldg(p.scales + (row * pitch + c) / kAct8Block);
+                code_1 = fetch(p.codes + row * pitch + c);
+                scale_1 = fetch(p.scales + (row * pitch + c) / kAct8Block);
             } else {
-                x_1 = __ldg(static_cast<const T*>(p.x) + row * p.ldx + c);
+                x_1 = fetch(static_cast<const T*>(p.x) + row * p.ldx + c);
             }
-            if (p.dy) dy_1 = __ldg(static_cast<const T*>(p.dy) + row * p.lddy + c);
+            if (p.dy) dy_1 = fetch(static_cast<const T*>(p.dy) + row * p.lddy + c);
         }
     };
     if (first_row < p.rows) load(first_row);

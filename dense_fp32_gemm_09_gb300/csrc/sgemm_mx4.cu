@@ -52,12 +52,11 @@ struct Eight {
         if (VEC) {
 #pragma unroll
             for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-                raw[i] = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p) + i)
-                                  : make_uint4(0, 0, 0, 0);
+                raw[i] = fetch_if(reinterpret_cast<const uint4*>(p) + i, left > 0);
         } else {
             alignas(16) T t[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[i] = i < left ? __ldg(p + i) : T(0.0f);
+            for (int i = 0; i < 8; ++i) t[i] = i < left ? fetch(p + i) : T(0.0f);
 #pragma unroll
             for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
                 raw[i] = reinterpret_cast<const uint4*>(t)[i];
@@ -108,9 +107,9 @@ __device__ __forceinline__ uint32_t magnitude(const uint4 (&raw)[N]) {
 // two lanes to 32 columns of a row.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) quantize_nv_kernel(
-    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
-    const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
-    uint8_t* __restrict__ scales) {
+    const T* X, long long ldx, int rows, int cols, int chunks,
+    const float* tensor_scale, uint8_t* codes,
+    uint8_t* scales) {
     const int groups = chunks / 2, lane = threadIdx.x & 31, q = lane & 1;
     const long long id = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const long long band = id / groups;              // 2 a block of 128 rows
@@ -172,8 +171,8 @@ __global__ void __launch_bounds__(32 * kWarps) quantize_nv_kernel(
 // mxfp4: four lanes take a row's 32 columns, eight each, a warp 32 rows of 128 columns.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) quantize_mx_kernel(
-    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
-    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+    const T* X, long long ldx, int rows, int cols, int chunks,
+    uint8_t* codes, uint8_t* scales) {
     Task t;
     const bool any = task_of(rows, chunks / 4, &t);
     wait_previous();
@@ -251,21 +250,21 @@ __device__ __forceinline__ void store_whole(T* p, const float (&v)[8], bool live
 // store of eight scattered pieces a lane took 30 us, this 5.5).
 template <typename T, int FORMAT, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
-    const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-    const float* __restrict__ tensor_scale, int rows, int cols, int chunks, T* __restrict__ Y,
+    const uint8_t* codes, const uint8_t* scales,
+    const float* tensor_scale, int rows, int cols, int chunks, T* Y,
     long long ldy) {
     __shared__ __align__(16) T staged[VEC ? 1 : kWarps][8][VEC ? 8 : 136];
     Task t;
     const bool any = task_of(rows, chunks / 4, &t);
     wait_previous();
     if (!any) return;
-    const float ts = FORMAT == kNvfp4 && tensor_scale ? __ldg(tensor_scale) : 1.0f;
+    const float ts = FORMAT == kNvfp4 && tensor_scale ? fetch(tensor_scale) : 1.0f;
     const int groups = groups_of(cols, FORMAT);
     constexpr int kGroups = FORMAT == kNvfp4 ? 2 : 1;
     uint4 words[kGroups];
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
-        words[g] = __ldg(reinterpret_cast<const uint4*>(
+        words[g] = fetch(reinterpret_cast<const uint4*>(
             scales + scale_offset(t.row, 4 * (t.quad * kGroups + g), groups)));
     const int lane = threadIdx.x & 31, r8 = lane >> 2;
     const long long r0 = t.row - r8;
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
         uint32_t packed[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            packed[c] = __ldg(reinterpret_cast<const uint32_t*>(
+            packed[c] = fetch(reinterpret_cast<const uint32_t*>(
                 codes + code_offset(row, 4 * t.quad + c, chunks) + 4 * t.q));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -310,9 +309,9 @@ __global__ void __launch_bounds__(32 * kWarps) dequantize_kernel(
 // X stored cols x rows: a thread takes column `row` of X, 64 of its rows.
 template <typename T, int FORMAT>
 __global__ void __launch_bounds__(128) quantize_transposed_kernel(
-    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
-    const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
-    uint8_t* __restrict__ scales) {
+    const T* X, long long ldx, int rows, int cols, int chunks,
+    const float* tensor_scale, uint8_t* codes,
+    uint8_t* scales) {
     const int pairs = chunks / 2;
     const long long rb = blockIdx.x / pairs;
     const int pair = static_cast<int>(blockIdx.x - rb * pairs);
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(128) quantize_transposed_kernel(
         const int k0 = pair * 64 + c * 32;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            x[i / 8][i % 8] = k0 + i < cols ? to_float(__ldg(X + (k0 + i) * ldx + row)) : 0.0f;
+            x[i / 8][i % 8] = k0 + i < cols ? to_float(fetch(X + (k0 + i) * ldx + row)) : 0.0f;
         uint32_t m[4], packed[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) m[i] = magnitude8(x[i]);
@@ -358,9 +357,9 @@ __global__ void __launch_bounds__(128) quantize_transposed_kernel(
 // allow 4-byte loads: 64 threads take 128 columns, so a warp loads 128 bytes of a row of X.
 template <typename T, int FORMAT>
 __global__ void __launch_bounds__(128) quantize_transposed2_kernel(
-    const T* __restrict__ X, long long ldx, int rows, int cols, int chunks,
-    const float* __restrict__ tensor_scale, uint8_t* __restrict__ codes,
-    uint8_t* __restrict__ scales) {
+    const T* X, long long ldx, int rows, int cols, int chunks,
+    const float* tensor_scale, uint8_t* codes,
+    uint8_t* scales) {
     const int quads = chunks / 4;
     const long long rb = blockIdx.x / quads;
     const int pair = 2 * static_cast<int>(blockIdx.x - rb * quads) + (threadIdx.x >> 6);
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(128) quantize_transposed2_kernel(
 #pragma unroll
         for (int i = 0; i < 32; ++i)
             w[i] = k0 + i < cols
-                       ? __ldg(reinterpret_cast<const uint32_t*>(X + (k0 + i) * ldx + row)) : 0u;
+                       ? fetch(reinterpret_cast<const uint32_t*>(X + (k0 + i) * ldx + row)) : 0u;
 #pragma unroll
         for (int i = 0; i < 32; ++i) m[i / 16] = max_halves(m[i / 16], w[i] & 0x7FFF7FFFu);
         if (FORMAT == kMxfp4) m[0] = m[1] = max_halves(m[0], m[1]);

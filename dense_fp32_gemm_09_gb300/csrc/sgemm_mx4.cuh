@@ -19,6 +19,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "sgemm_launch.cuh"
+
 namespace sgemm {
 namespace mx4 {
 
@@ -219,7 +221,7 @@ struct TensorScale {
     float ts, six, r, cap;
     bool usual;
     __device__ __forceinline__ explicit TensorScale(const float* p) {
-        ts = p ? __ldg(p) : 1.0f;
+        ts = p ? fetch(p) : 1.0f;
         six = 6.0f * ts;
         usual = six > 0x1p-90f && six < 0x1p90f && judges(six, kScaleBoundaries);
         r = reciprocal(six);

@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(128) mx4_matmul_kernel(const MatmulPlan pl) {
     __syncwarp();
     fence_after();
     float f = p.alpha;
-    if (p.a_ts) f *= __ldg(p.a_ts);
-    if (p.b_ts) f *= __ldg(p.b_ts);
+    if (p.a_ts) f *= fetch(p.a_ts);
+    if (p.b_ts) f *= fetch(p.b_ts);
     const long long n = n0 + threadIdx.x;
     const uint32_t mine = tmem + (static_cast<uint32_t>(32 * warp) << 16);
     // Sums go through shared memory: to the cluster, or (where the ring was: every MMA has

@@ -278,8 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         constexpr int kCols = kTile / 2;
         float f = p.alpha;
-        if (p.a_ts) f *= __ldg(p.a_ts);
-        if (p.b_ts) f *= __ldg(p.b_ts);
+        if (p.a_ts) f *= fetch(p.a_ts);
+        if (p.b_ts) f *= fetch(p.b_ts);
         float* const staged = reinterpret_cast<float*>(smem + kStages * kStageBytes<FORMAT> +
                                                        half * (kStageC / 2));
         uint32_t turn = 0;

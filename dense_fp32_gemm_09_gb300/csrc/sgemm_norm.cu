@@ -73,9 +73,9 @@ __device__ __forceinline__ float block_sum(float v) {
 
 __device__ __forceinline__ float weight_at(const void* w, int wtype, int c) {
     if (w == nullptr) return 1.0f;
-    if (wtype == kF32) return __ldg(static_cast<const float*>(w) + c);
-    if (wtype == kBf16) return to_float(__ldg(static_cast<const __nv_bfloat16*>(w) + c));
-    return to_float(__ldg(static_cast<const __half*>(w) + c));
+    if (wtype == kF32) return fetch(static_cast<const float*>(w) + c);
+    if (wtype == kBf16) return to_float(fetch(static_cast<const __nv_bfloat16*>(w) + c));
+    return to_float(fetch(static_cast<const __half*>(w) + c));
 }
 
 // One row per block.
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_wide(const NormBackwar
         const T* gate = static_cast<const T*>(p.gate) + row * p.ldg;
         float rn = 0.0f, mn = 0.0f, r = 0.0f, m = 0.0f;
         if (p.dh) {
-            rn = __ldg(p.next_rstd + row);
+            rn = fetch(p.next_rstd + row);
             float s = 0.0f;
             for (int c = threadIdx.x; c < D; c += kThreads)
                 s += weight_at(p.next_weight, p.weight_dtype, c) * to_float(dh[c]) *
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) norm_backward_wide(const NormBackwar
         };
         auto g = [&](int c) { return p.gate ? p.scale * to_float(gate[c]) : p.scale; };
         if (p.block) {
-            r = __ldg(p.rstd + row);
+            r = fetch(p.rstd + row);
             float s = 0.0f;
             for (int c = threadIdx.x; c < D; c += kThreads)
                 s += weight_at(p.weight, p.weight_dtype, c) * g(c) * t(c) * (to_float(b[c]) * r);

@@ -47,9 +47,9 @@ struct Own {
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
             if constexpr (VEC)
-                to.raw[i] = c[i] < D ? __ldg(reinterpret_cast<const uint4*>(row + c[i]))
+                to.raw[i] = c[i] < D ? fetch(reinterpret_cast<const uint4*>(row + c[i]))
                                      : make_uint4(0, 0, 0, 0);
-            else to.v[i] = c[i] < D ? __ldg(row + c[i]) : T(0.0f);
+            else to.v[i] = c[i] < D ? fetch(row + c[i]) : T(0.0f);
         }
     }
     template <typename S>
@@ -99,8 +99,8 @@ struct Own {
         } else {
 #pragma unroll
             for (int j = 0; j < kPairs2; ++j)
-                x[j] = two(c[2 * j] < D ? to_float(__ldg(w + c[2 * j])) : 0.0f,
-                           c[2 * j + 1] < D ? to_float(__ldg(w + c[2 * j + 1])) : 0.0f);
+                x[j] = two(c[2 * j] < D ? to_float(fetch(w + c[2 * j])) : 0.0f,
+                           c[2 * j + 1] < D ? to_float(fetch(w + c[2 * j + 1])) : 0.0f);
         }
     }
     // Weights; ones where there are none.
@@ -222,14 +222,14 @@ __global__ void __launch_bounds__(512, 1) norm_backward_columns(const NormBackwa
         if constexpr (kNext) {
             own.load(dh_at + row * p.lddh, dh);
             own.load(y_at + row * p.ldy, y);
-            rn = __ldg(p.next_rstd + row);
+            rn = fetch(p.next_rstd + row);
         }
     };
     auto load_after = [&](long long row) {     // what the norm after the block reads
         if constexpr (kAfter) {
             own.load(blk_at + row * p.ldb, blk);
             if (gate_rows) own.load(gate_at + row * p.ldg, gate);
-            r = __ldg(p.rstd + row);
+            r = fetch(p.rstd + row);
         }
     };
     if (kAfter && p.gate && !gate_rows) own.load(gate_at, gate);

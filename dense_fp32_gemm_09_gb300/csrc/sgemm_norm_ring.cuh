@@ -40,7 +40,7 @@ __device__ __forceinline__ void ring_fill(const Ring& g, uint8_t* stage, uint64_
             const uint8_t* from = g.p[i] + row * g.ld[i];
             for (int c = 2 * threadIdx.x; c < g.row_bytes; c += 2 * blockDim.x)
                 *reinterpret_cast<uint16_t*>(stage + i * g.pitch + c) =
-                    __ldg(reinterpret_cast<const uint16_t*>(from + c));
+                    fetch(reinterpret_cast<const uint16_t*>(from + c));
         }
     }
 }
@@ -177,11 +177,11 @@ __device__ __forceinline__ void get_shared(const W* p, int c, int D, Two (&x)[P]
     if constexpr (RAGGED) {
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            x[j] = two(c + 2 * j < D ? to_float(__ldg(p + c + 2 * j)) : 0.0f,
-                       c + 2 * j + 1 < D ? to_float(__ldg(p + c + 2 * j + 1)) : 0.0f);
+            x[j] = two(c + 2 * j < D ? to_float(fetch(p + c + 2 * j)) : 0.0f,
+                       c + 2 * j + 1 < D ? to_float(fetch(p + c + 2 * j + 1)) : 0.0f);
     } else if constexpr (2 * P * sizeof(W) == 8) {
         // Four 2-byte weights with a vector of four fp32 numbers.
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + c));
+        const uint2 v = fetch(reinterpret_cast<const uint2*>(p + c));
         Two t[4];
         unpack(make_uint4(v.x, v.y, 0, 0), t, W());
 #pragma unroll
@@ -191,7 +191,7 @@ __device__ __forceinline__ void get_shared(const W* p, int c, int D, Two (&x)[P]
 #pragma unroll
         for (int i = 0; i < P / kEach; ++i) {
             Two t[kEach];
-            unpack(__ldg(reinterpret_cast<const uint4*>(p + c) + i), t, W());
+            unpack(fetch(reinterpret_cast<const uint4*>(p + c) + i), t, W());
 #pragma unroll
             for (int j = 0; j < kEach; ++j) x[i * kEach + j] = t[j];
         }
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(1024, 1)
     Two sw[N][P] = {}, sg[SHARED ? N : 1][P] = {}, sn[N][P] = {};
     loop.start();
     // A row's statistics are loaded a row ahead: nothing else hides that latency.
-    auto stat = [&](const float* v, long long row) { return row < p.rows ? __ldg(v + row) : 0.0f; };
+    auto stat = [&](const float* v, long long row) { return row < p.rows ? fetch(v + row) : 0.0f; };
     float rn_ahead = kNext ? stat(p.next_rstd, loop.row) : 0.0f;
     float r_ahead = kAfter ? stat(p.rstd, loop.row) : 0.0f;
     for (; loop.row < p.rows; loop.next()) {
