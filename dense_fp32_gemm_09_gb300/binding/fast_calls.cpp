@@ -574,7 +574,7 @@ PyObject* gated_ff_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    dwu = empty({w.N, w.K}, s.type), h;
         if (again) h = empty({M, w.N}, s.type);
         const int pack = (x.defined() ? packed(1, x, ldx) : 1) | packed(2, wg, w.ldg) |
-                         packed(4, wu, w.ldu);
+                         packed(4, wu, w.ldu) | (dt == SGEMM_F16 ? 8 : 0);
         size_t bytes = 0;
         if (const int st = f_gated_ff_workspace(M, w.N, w.K, 1, pack, &bytes)) return status(st);
         const at::Tensor ws = workspace(bytes);

@@ -95,7 +95,8 @@ struct GatedFfBackward {
 };
 size_t gated_ff_forward_workspace(int M, int N, int K, int packed);
 size_t gated_ff_backward_workspace(int M, int N, int K, int packed);
-// Which of x, w_gate and w_up (bits 1, 2, 4) the kernels cannot read in place.
+// Which of x, w_gate and w_up (bits 1, 2, 4) the kernels cannot read in place; backward, kPackedFp16 too.
+constexpr int kPackedFp16 = 8;
 int gated_ff_packed(const GatedFfForward& p);
 int gated_ff_packed(const GatedFfBackward& p);
 // What a product takes: tile columns (of the operand: twice the outputs forward; 0: the kernel for

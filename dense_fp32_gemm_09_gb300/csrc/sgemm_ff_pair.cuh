@@ -502,6 +502,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                        rows, cols, to.vec, lane);
                 }
             } else {
+                constexpr bool kScaled = std::is_same<T, __half>::value;
+                float by = 1.0f;
+                if constexpr (kScaled)
+                    if (lane < rows) by = scale_back(fetch_here(to.largest + row + lane));
 #pragma unroll 1
                 for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 64) {
                     float v[64];
@@ -509,6 +513,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (c + 64 == (half + 1) * (BN / 2)) done_reading();
                     const int col = t.col + c, cols = of.cols - col;
                     if (rows == 0 || cols <= 0) continue;
+                    if constexpr (kScaled)
+#pragma unroll
+                        for (int j = 0; j < 64; ++j) v[j] *= by;
                     if (to.partial) {
                         // One part's fp32 sums, 32 columns at a time.
                         float* at = to.partial +

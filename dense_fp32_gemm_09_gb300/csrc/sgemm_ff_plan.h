@@ -13,7 +13,7 @@ enum : int { kForward = 0, kBackward = 1 };
 constexpr int kTileRows = 256;
 
 // Forward: a[0] x, b[0] Wg, b[1] Wu.  Backward: a[0], a[1] dg, du read along their rows, a[2], a[3]
-// across them, b[0] Wg, b[1] Wu, b[2] x.  A parameter of its own: its address is taken, and if it
+// across them (fp16: matrices of their own, see scale_up), b[0] Wg, b[1] Wu, b[2] x.  A parameter of its own: its address is taken, and if it
 // were the plan's, the plan would be read again after every store.
 struct PairMaps {
     CUtensorMap a[4], b[3];
@@ -31,6 +31,7 @@ struct Result {
     long long ld;
     int vec;                   // 1: rows start on 16 bytes
     float* partial;            // split > 1: [part][rows][partial_ld]
+    const uint32_t* largest;   // fp16 backward: of the operands, for each row of the result
 };
 struct PairPlan {
     Product of[2];

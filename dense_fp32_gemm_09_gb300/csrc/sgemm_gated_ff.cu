@@ -9,7 +9,8 @@
 // is off by the rounding of its terms (half an ulp each, at random) beside its own; so are the
 // numbers of an x that comes in 8 bits, whose own steps are 2^-8 of their block's largest.  In
 // norm, bf16: dx and the weights' gradients 2.3e-3 of 64 bits' where the rounding of the result
-// alone is 1.7e-3, the weights' gradients of an x in 8 bits 2.8e-3.
+// alone is 1.7e-3, the weights' gradients of an x in 8 bits 2.8e-3.  fp16 has too few exponents for dg and
+// du and takes them by powers of two for each row and column (ff_gradient_fp16).
 //
 // The products: sgemm_ff_pair.cuh, and sgemm_ff_token.cu for up to 16 tokens.  Rows that are not on
 // 16 bytes cannot be read by tensor maps and, for these, are copied into the workspace first (3001 x 2047 and
@@ -35,18 +36,20 @@ using namespace ff;
 
 constexpr int kThreads = 256;
 
-// Eight 2-byte numbers at p, of which `n` are inside; vec: p is on 16 bytes.
+// Eight 2-byte numbers at p as they are stored, zeros for those from the n-th on; vec: p is on 16 bytes.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        const uint4 raw = fetch_here(reinterpret_cast<const uint4*>(p));
-        const T* t = reinterpret_cast<const T*>(&raw);
+__device__ __forceinline__ uint4 load8(const T* p, int n, bool vec) {
+    if (vec && n >= 8) return fetch_here(reinterpret_cast<const uint4*>(p));
+    alignas(16) T t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
-    } else {
+    for (int i = 0; i < 8; ++i) t[i] = i < n ? fetch_here(p + i) : T(0.0f);
+    return *reinterpret_cast<const uint4*>(t);
+}
+template <typename T>
+__device__ __forceinline__ void numbers8(const uint4& raw, float (&v)[8]) {
+    const T* t = reinterpret_cast<const T*>(&raw);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_float(p[i]) : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&v)[8]) {
@@ -65,54 +68,175 @@ __device__ __forceinline__ void store8(T* p, int n, bool vec, const float (&v)[8
 struct Aligned {
     bool dh, kept, h;
 };
-// dg, du (rows of `pitch`, a multiple of 64), and h again, from dh and what was kept: eight columns
+// What dg, du and h again are made of: dh and what was kept of eight columns of a row from c on, of which n > 0
+// are inside (the others are 0).  All loads come before the first number is used.
+template <typename T, bool KEPT8>
+struct Inputs8 {
+    uint4 dh, gate, up;              // KEPT8: eight codes, and the scale's bits
+    __device__ __forceinline__ void load(const GatedFfBackward& p, long long row, int c, int n, const Aligned& on) {
+        dh = load8(static_cast<const T*>(p.dh) + row * p.lddh + c, n, on.dh);
+        if constexpr (KEPT8) {
+            const long long k = row * act8_pitch(p.N) + c;
+            const auto held = [&](const void* from, const float* scales) {
+                const uint2 w = fetch_here(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(from) + k));
+                return make_uint4(w.x, w.y, __float_as_uint(fetch_here(scales + k / kAct8Block)), 0);
+            };
+            gate = held(p.kept.gate, p.kept.gate_scales);
+            up = held(p.kept.up, p.kept.up_scales);
+        } else {
+            gate = load8(static_cast<const T*>(p.kept.gate) + row * p.kept.ld + c, n, on.kept);
+            up = load8(static_cast<const T*>(p.kept.up) + row * p.kept.ld + c, n, on.kept);
+        }
+    }
+    __device__ __forceinline__ static void kept(const uint4& raw, float (&v)[8]) {
+        if constexpr (KEPT8) {
+            const float s = __uint_as_float(raw.z);
+            mx4::Two t[4];
+            act8::values4(raw.x, s, reinterpret_cast<mx4::Two(&)[2]>(t[0]));
+            act8::values4(raw.y, s, reinterpret_cast<mx4::Two(&)[2]>(t[2]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = mx4::parts(t[j]);
+                v[2 * j] = f.x;
+                v[2 * j + 1] = f.y;
+            }
+        } else {
+            numbers8<T>(raw, v);
+        }
+    }
+    template <int ACT>
+    __device__ __forceinline__ void gradients(float (&dg)[8], float (&du)[8], float (&h)[8]) const {
+        float (&g)[8] = dg, (&u)[8] = du, d[8];
+        numbers8<T>(dh, d);
+        kept(gate, g);
+        kept(up, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const Act a = Act::of<ACT>(g[j]);
+            const float v = a.value();
+            h[j] = v * u[j];
+            g[j] = d[j] * u[j] * a.slope();
+            u[j] = d[j] * v;
+        }
+    }
+};
+// bf16: dg, du (rows of `pitch`, a multiple of 64), and h again, from dh and what was kept: eight columns
 // a thread.
 template <typename T, int ACT, bool KEPT8>
 __global__ void __launch_bounds__(kThreads)
     ff_gradient(const GatedFfBackward p, T* dg, T* du, long long pitch, const Aligned on) {
-    const long long codes = act8_pitch(p.N);
     act8::Walk at(blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x,
                   static_cast<long long>(gridDim.x) * kThreads, (p.N + 7) / 8);
     start_dependent();
     for (; at.row < p.M; at.next()) {
         const long long row = at.row;
         const int c = at.col * 8, n = p.N - c;
-        float g[8], u[8], dh[8];
-        load8(static_cast<const T*>(p.dh) + row * p.lddh + c, n, on.dh, dh);
-        if constexpr (KEPT8) {
-            const long long k = row * codes + c;
-            const auto held = [&](const void* from, const float* scales, float (&v)[8]) {
-                const uint2 w =
-                    fetch_here(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(from) + k));
-                const float s = fetch_here(scales + k / kAct8Block);
-                mx4::Two t[4];
-                act8::values4(w.x, s, reinterpret_cast<mx4::Two(&)[2]>(t[0]));
-                act8::values4(w.y, s, reinterpret_cast<mx4::Two(&)[2]>(t[2]));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = mx4::parts(t[j]);
-                    v[2 * j] = f.x;
-                    v[2 * j + 1] = f.y;
-                }
-            };
-            held(p.kept.gate, p.kept.gate_scales, g);
-            held(p.kept.up, p.kept.up_scales, u);
-        } else {
-            load8(static_cast<const T*>(p.kept.gate) + row * p.kept.ld + c, n, on.kept, g);
-            load8(static_cast<const T*>(p.kept.up) + row * p.kept.ld + c, n, on.kept, u);
-        }
-        float h[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const Act a = Act::of<ACT>(g[j]);
-            const float v = a.value();
-            h[j] = v * u[j];
-            g[j] = dh[j] * u[j] * a.slope();
-            u[j] = dh[j] * v;
-        }
+        float g[8], u[8], h[8];
+        Inputs8<T, KEPT8> in;
+        in.load(p, row, c, n, on);
+        in.template gradients<ACT>(g, u, h);
         store8(dg + row * pitch + c, 8, true, g);
         store8(du + row * pitch + c, 8, true, u);
         if (p.h) store8(static_cast<T*>(p.h) + row * p.ldh + c, n, on.h, h);
+    }
+}
+
+// fp16: the same in two passes (scale_up in sgemm_gated_ff.cuh).  The first finds the largest finite
+// magnitudes of each row and column; maxima do not depend on the order of the atomics.  The second
+// makes dg and du again and stores them twice, by the rows' powers of two for dx and by the columns'
+// for the weights' gradients.  (One power for the whole matrix would need no second copy, but one large
+// token would take the precision of all others.)  A block has 256 columns, a warp a row of them at a
+// time, so that a thread's columns stay and so do their maxima and powers.  Against one unscaled copy in one
+// pass the gradient of 500 x 4096 x 1024 (tokens x outputs x inputs) takes 35.4 us and took 26.0, of
+// 8192 x 8192 x 4096 1485 and 1373 (96 of it the first pass).
+struct Scaled {
+    __half *dg_rows, *du_rows, *dg_cols, *du_cols;     // rows of `pitch`
+    uint32_t *rows, *of_dg, *of_du;                    // fp32 bits: [M], [N], [N]
+    long long pitch;
+};
+constexpr int kTileCols = 256, kRowsAhead = 2;
+__global__ void __launch_bounds__(kThreads) ff_clear(uint32_t* p, long long n) {
+    start_dependent();
+    for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * kThreads)
+        p[i] = 0;
+}
+__device__ __forceinline__ uint32_t finite_magnitude(float v) {
+    const uint32_t m = act8::magnitude(v);
+    return m < kInfinite ? m : 0u;
+}
+template <int ACT, bool KEPT8, bool STORE>
+__global__ void __launch_bounds__(kThreads)
+    ff_gradient_fp16(const GatedFfBackward p, const Scaled q, const Aligned on) {
+    constexpr int kWarps = kThreads / 32;
+    __shared__ uint32_t part[STORE ? 1 : kWarps][2][STORE ? 1 : kTileCols];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = blockIdx.x * kTileCols, c = first + 8 * lane, n = p.N - c;
+    start_dependent();
+    uint32_t mg[8] = {}, mu[8] = {};                   // STORE: unused
+    float fg[8], fu[8];
+    if constexpr (STORE)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            fg[j] = j < n ? scale_up(fetch_here(q.of_dg + c + j)) : 0.0f;
+            fu[j] = j < n ? scale_up(fetch_here(q.of_du + c + j)) : 0.0f;
+        }
+    const long long step = static_cast<long long>(gridDim.y) * kWarps;
+    for (long long first_row = blockIdx.y * static_cast<long long>(kWarps) + warp; first_row < p.M;
+         first_row += kRowsAhead * step) {
+        Inputs8<__half, KEPT8> in[kRowsAhead] = {};
+#pragma unroll
+        for (int i = 0; i < kRowsAhead; ++i)
+            if (n > 0 && first_row + i * step < p.M) in[i].load(p, first_row + i * step, c, n, on);
+#pragma unroll
+        for (int i = 0; i < kRowsAhead; ++i) {
+            const long long row = first_row + i * step;
+            if (row >= p.M) break;
+            float g[8], u[8], h[8];
+            in[i].template gradients<ACT>(g, u, h);
+            if constexpr (STORE) {
+                if (n <= 0) continue;
+                const float by = scale_up(fetch_here(q.rows + row));
+                const long long to = row * q.pitch + c;
+                float v[8];
+                const auto put = [&](__half* at, const float (&x)[8], auto factor) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = x[j] * factor(j);
+                    store8(at + to, 8, true, v);
+                };
+                put(q.dg_rows, g, [&](int) { return by; });
+                put(q.du_rows, u, [&](int) { return by; });
+                put(q.dg_cols, g, [&](int j) { return fg[j]; });
+                put(q.du_cols, u, [&](int j) { return fu[j]; });
+                if (p.h) store8(static_cast<__half*>(p.h) + row * p.ldh + c, n, on.h, h);
+            } else {
+                uint32_t most = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t a = finite_magnitude(g[j]), b = finite_magnitude(u[j]);
+                    mg[j] = max(mg[j], a);
+                    mu[j] = max(mu[j], b);
+                    most = max(most, max(a, b));
+                }
+                most = __reduce_max_sync(0xFFFFFFFFu, most);
+                if (lane == 0 && most) atomicMax(q.rows + row, most);
+            }
+        }
+    }
+    if constexpr (!STORE) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            part[warp][0][8 * lane + j] = mg[j];
+            part[warp][1][8 * lane + j] = mu[j];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * kTileCols; i += kThreads) {
+            const int which = i / kTileCols, col = i % kTileCols;
+            uint32_t most = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) most = max(most, part[w][which][col]);
+            if (most && first + col < p.N) atomicMax((which ? q.of_du : q.of_dg) + first + col, most);
+        }
     }
 }
 
@@ -242,6 +366,7 @@ __global__ void __launch_bounds__(kThreads) ff_add_parts(const Parts q) {
 // ----------------------------------------------------------------------------
 long long up64(long long n) { return (n + 63) / 64 * 64; }
 long long matrix_bytes(long long rows, long long cols) { return rows * up64(cols) * 2; }
+long long largest_bytes(long long M, long long N) { return up64(M + 2 * N) * 4; }     // Scaled's
 long long up_to(long long n, int m) { return (n + m - 1) / m; }
 
 constexpr int kTokens = 16;          // up to here sgemm_ff_token.cu
@@ -405,7 +530,7 @@ cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* laun
     pl.of[0] = {p.M, p.N, static_cast<int>(up_to(p.M, kTileRows)), static_cast<int>(up_to(p.N, c.bn / 2)),
                 static_cast<int>(up_to(p.K, 64)), 1};
     pl.pairs = static_cast<int>(std::min<long long>(sms / 2, pl.of[0].items()));
-    pl.to[0] = {p.h, p.ldh, on16(p.h, p.M, p.ldh), nullptr};
+    pl.to[0] = {p.h, p.ldh, on16(p.h, p.M, p.ldh), nullptr, nullptr};
     pl.kept = p.kept;
     pl.kept_vec = on16(p.kept.gate, p.M, p.kept.ld) && on16(p.kept.up, p.M, p.kept.ld);
     pl.status = status_word_ptr();
@@ -413,17 +538,39 @@ cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* laun
     return pair<T>(maps, pl, kForward, c.bn, p.activation, st);
 }
 
+// dg and du to `q` (bf16: of it dg_rows and du_rows, read both ways).
 template <typename T, int ACT>
-cudaError_t gradient(const GatedFfBackward& p, T* dg, T* du, long long pitch, int sms,
-                     cudaStream_t st) {
+cudaError_t gradient(const GatedFfBackward& p, const Scaled& q, int sms, cudaStream_t st, int* launches) {
     const Aligned on{on16(p.dh, p.M, p.lddh),
                      on16(p.kept.gate, p.M, p.kept.ld) && on16(p.kept.up, p.M, p.kept.ld),
                      on16(p.h, p.M, p.ldh)};
-    const long long blocks = up_to(p.M * up_to(p.N, 8), kThreads);
-    const dim3 grid(static_cast<unsigned>(std::min<long long>(blocks, sms * 8LL)));
-    return p.kept.keep == kKeep8
-               ? launch_dependent(ff_gradient<T, ACT, true>, grid, kThreads, 0, st, p, dg, du, pitch, on)
-               : launch_dependent(ff_gradient<T, ACT, false>, grid, kThreads, 0, st, p, dg, du, pitch, on);
+    const bool in8 = p.kept.keep == kKeep8;
+    const auto blocks_of = [&](long long units) {
+        return static_cast<unsigned>(std::max(1LL, std::min<long long>(units, sms * 8LL)));
+    };
+    if constexpr (std::is_same<T, __half>::value) {
+        constexpr long long kBlocksAnSm = 3;
+        const long long words = p.M + 2LL * p.N, tiles = up_to(p.N, kTileCols);
+        cudaError_t e = launch_dependent(ff_clear, dim3(blocks_of(up_to(words, kThreads))), kThreads, 0, st,
+                                         q.rows, words);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        const dim3 grid(static_cast<unsigned>(tiles),
+                        static_cast<unsigned>(std::max(1LL, std::min(up_to(p.M, kThreads / 32), sms * kBlocksAnSm / tiles))));
+        e = launch_dependent(in8 ? ff_gradient_fp16<ACT, true, false> : ff_gradient_fp16<ACT, false, false>, grid,
+                             kThreads, 0, st, p, q, on);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        e = launch_dependent(in8 ? ff_gradient_fp16<ACT, true, true> : ff_gradient_fp16<ACT, false, true>, grid,
+                             kThreads, 0, st, p, q, on);
+        ++*launches;
+        return e;
+    } else {
+        ++*launches;
+        return launch_dependent(in8 ? ff_gradient<T, ACT, true> : ff_gradient<T, ACT, false>,
+                                dim3(blocks_of(up_to(p.M * up_to(p.N, 8), kThreads))), kThreads, 0, st, p,
+                                reinterpret_cast<T*>(q.dg_rows), reinterpret_cast<T*>(q.du_rows), q.pitch, on);
+    }
 }
 
 // The second half of products whose tiles were split.
@@ -449,10 +596,25 @@ cudaError_t add_parts(const PairPlan& pl, int sms, cudaStream_t st, int* launche
 
 template <typename T>
 cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* launches) {
-    const long long pitch = up64(p.N);
-    T* const dg = reinterpret_cast<T*>(p.ws);
-    T* const du = dg + p.M * pitch;
-    uint8_t* at = reinterpret_cast<uint8_t*>(du + p.M * pitch);
+    constexpr bool kScaled = std::is_same<T, __half>::value;
+    uint8_t* at = p.ws;
+    const auto take = [&](long long bytes) {
+        uint8_t* const from = at;
+        at += bytes;
+        return from;
+    };
+    const auto matrix = [&] { return reinterpret_cast<__half*>(take(matrix_bytes(p.M, p.N))); };
+    Scaled q{};
+    q.pitch = up64(p.N);
+    q.dg_rows = q.dg_cols = matrix();
+    q.du_rows = q.du_cols = matrix();
+    if (kScaled) {
+        q.dg_cols = matrix();
+        q.du_cols = matrix();
+        q.rows = reinterpret_cast<uint32_t*>(take(largest_bytes(p.M, p.N)));
+        q.of_dg = q.rows + p.M;
+        q.of_du = q.of_dg + p.N;
+    }
     Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, at);
     if (p.x_codes) {       // rounded to the operands' type
         in.x = in.at;
@@ -466,18 +628,19 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
     }
     cudaError_t e = in.copy(sms, st, launches);
     if (e != cudaSuccess) return e;
-    e = p.activation == kSilu ? gradient<T, kSilu>(p, dg, du, pitch, sms, st)
-                              : gradient<T, kGeluTanh>(p, dg, du, pitch, sms, st);
+    e = p.activation == kSilu ? gradient<T, kSilu>(p, q, sms, st, launches)
+                              : gradient<T, kGeluTanh>(p, q, sms, st, launches);
     if (e != cudaSuccess) return e;
-    ++*launches;
 
     PairMaps maps;
     PairPlan pl{};
     pl.status = status_word_ptr();
     // dx, from dg and Wg, then du and Wu; dWg and dWu.
     const Gradients c = choose_gradients(p.M, p.N, p.K);
-    if (!encode(&maps.a[0], dg, p.M, p.N, pitch, 128) || !encode(&maps.a[1], du, p.M, p.N, pitch, 128) ||
-        !encode(&maps.a[2], dg, p.M, p.N, pitch, 64) || !encode(&maps.a[3], du, p.M, p.N, pitch, 64) ||
+    if (!encode(&maps.a[0], q.dg_rows, p.M, p.N, q.pitch, 128) ||
+        !encode(&maps.a[1], q.du_rows, p.M, p.N, q.pitch, 128) ||
+        !encode(&maps.a[2], q.dg_cols, p.M, p.N, q.pitch, 64) ||
+        !encode(&maps.a[3], q.du_cols, p.M, p.N, q.pitch, 64) ||
         !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, 64) ||
         !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, 64) ||
         !encode(&maps.b[2], in.x, p.M, p.K, in.ldx, 64))
@@ -490,9 +653,9 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
     pl.pairs = static_cast<int>(std::min<long long>(sms / 2, pl.of[0].items() + pl.of[1].items()));
     pl.extra = spread(pl.of[0].items(), pl.of[1].items(), item_clocks(up_to(pl.of[0].stages, c.split_x), c.bn),
                       item_clocks(up_to(pl.of[1].stages, c.split_w), c.bn), pl.pairs).extra;
-    pl.to[0] = {p.dx, p.lddx, on16(p.dx, p.M, p.lddx), nullptr};
-    pl.to[1] = {p.dw_gate, p.lddwg, on16(p.dw_gate, p.N, p.lddwg), nullptr};
-    pl.to[2] = {p.dw_up, p.lddwu, on16(p.dw_up, p.N, p.lddwu), nullptr};
+    pl.to[0] = {p.dx, p.lddx, on16(p.dx, p.M, p.lddx), nullptr, q.rows};
+    pl.to[1] = {p.dw_gate, p.lddwg, on16(p.dw_gate, p.N, p.lddwg), nullptr, q.of_dg};
+    pl.to[2] = {p.dw_up, p.lddwu, on16(p.dw_up, p.N, p.lddwu), nullptr, q.of_du};
     pl.partial_ld = up64(p.K);
     float* partial = reinterpret_cast<float*>(in.at);
     for (int i = 0; i < 3; ++i) {
@@ -530,7 +693,8 @@ size_t gated_ff_forward_workspace(int M, int N, int K, int packed) {
 size_t gated_ff_backward_workspace(int M, int N, int K, int packed) {
     const Gradients c = choose_gradients(M, N, K);
     const long long parts = (c.split_x > 1 ? 1LL * c.split_x * M : 0) + (c.split_w > 1 ? 2LL * c.split_w * N : 0);
-    return 2 * static_cast<size_t>(matrix_bytes(M, N)) + copied_bytes(M, N, K, packed) +
+    const long long scaled = packed & kPackedFp16 ? 2 * matrix_bytes(M, N) + largest_bytes(M, N) : 0;
+    return static_cast<size_t>(2 * matrix_bytes(M, N) + scaled) + copied_bytes(M, N, K, packed) +
            static_cast<size_t>(parts * up64(K)) * sizeof(float);
 }
 int gated_ff_packed(const GatedFfForward& p) {
@@ -540,7 +704,8 @@ int gated_ff_packed(const GatedFfForward& p) {
 }
 int gated_ff_packed(const GatedFfBackward& p) {
     return (p.x_codes ? 1 : packed_bit(1, p.x, p.M, p.ldx)) |
-           packed_bit(2, p.w_gate, p.N, p.ldg) | packed_bit(4, p.w_up, p.N, p.ldu);
+           packed_bit(2, p.w_gate, p.N, p.ldg) | packed_bit(4, p.w_up, p.N, p.ldu) |
+           (p.dtype == mx4::kF16 ? kPackedFp16 : 0);
 }
 
 cudaError_t launch_gated_ff_forward(const GatedFfForward& p, int sms, cudaStream_t stream,

@@ -49,5 +49,20 @@ struct Act {
 template <int ACT>
 __device__ __forceinline__ float act(float g) { return Act::of<ACT>(g).value(); }
 
+// fp16 holds 2^-24 to 65504, dg and du have the range of fp32.  What the products take is dg and du
+// times 2^e, and a product's rows are times 2^-e at the end: for dx one e for each row of (dg, du), for
+// the weights' gradients one for each column of dg and of du, the results' rows.  2^e brings the largest
+// finite magnitude (its bits are kept) to at least 2^14 and below 2^15.
+constexpr uint32_t kInfinite = 0x7F800000u;
+__device__ __forceinline__ uint32_t power_of(uint32_t largest) {       // e + 127, at most 253
+    return min(268u - (largest >> 23), 253u);
+}
+__device__ __forceinline__ float scale_up(uint32_t largest) {
+    return __uint_as_float(power_of(largest) << 23);
+}
+__device__ __forceinline__ float scale_back(uint32_t largest) {
+    return __uint_as_float((254u - power_of(largest)) << 23);
+}
+
 }  // namespace ff
 }  // namespace sgemm

@@ -241,7 +241,8 @@ int sgemm_gated_ff_workspace(int M, int N, int K, int backward, int packed, size
     return guarded([&]() -> int {
         SGEMM_TRY(check_ff("sgemm_gated_ff_workspace", M, N, K, SGEMM_BF16, SGEMM_SILU,
                            SGEMM_KEEP_FULL, false));
-        if (bytes == nullptr || packed < 0 || packed > 7 || backward < 0 || backward > 1)
+        if (bytes == nullptr || backward < 0 || backward > 1 || packed < 0 ||
+            packed > (backward ? 7 + kPackedFp16 : 7))
             return refuse(SGEMM_ERR_INVALID_ARG, "sgemm_gated_ff_workspace: bad argument");
         *bytes = M == 0 ? 0 : backward ? gated_ff_backward_workspace(M, N, K, packed)
                                        : gated_ff_forward_workspace(M, N, K, packed);

@@ -20,7 +20,7 @@ from .act8 import Act8, held
 
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 KEEP = {None: 0, "full": 1, "8bit": 2}
-_X, _GATE, _UP = 1, 2, 4
+_X, _GATE, _UP, _FP16 = 1, 2, 4, 8       # (`packed` of include/sgemm.h)
 
 
 def _activation(name) -> int:
@@ -112,8 +112,9 @@ def gated_ff_backward(dh, x, w_gate, w_up, kept, *, activation: str = "silu",
                       return_h: bool = False, stream=None):
     """(dx, dw_gate, dw_up) of ``gated_ff`` from the gradient of h.  ``x`` is the block's input
     or an ``Act8`` of it, ``kept`` what ``gated_ff(..., keep=...)`` returned.  With ``return_h``
-    also h, made again from what was kept: (dx, dw_gate, dw_up, h).  Gradients are of dh's type;
-    the gradients of the pre-activations, which the products multiply, are rounded to it too."""
+    also h, made again from what was kept: (dx, dw_gate, dw_up, h).  Gradients are of dh's type; what
+    the products multiply, the gradients of the pre-activations and an x in 8 bits, is rounded to it
+    too, float16 with powers of two that keep float32's range (``include/sgemm.h``)."""
     act = _activation(activation)
     if not isinstance(kept, (tuple, list)) or len(kept) != 2:
         raise TypeError("kept must be the (gate, up) that gated_ff(..., keep=...) returned")
@@ -142,6 +143,8 @@ def gated_ff_backward(dh, x, w_gate, w_up, kept, *, activation: str = "silu",
     x_codes = x_scales = x_at = None
     ldx = K
     packed = _packed(_GATE, w_gate, ldg) | _packed(_UP, w_up, ldu)
+    if dh.dtype == torch.float16:
+        packed |= _FP16
     if isinstance(x, Act8):
         x_codes, x_scales = held(x, "x", (M, K), dh.device)
         packed |= _X
