@@ -16,12 +16,32 @@ using mx4::to_float;
 //
 // With e = e^-|z|, s = 1 / (1 + e) or, where z < 0, e / (1 + e): e is at most 1, so that no
 // z leaves fp32 before s does.  (1 / (1 + e^-z) by the fast reciprocal was 0 from z = -87.4 down, where
-// s is 1e-38, and bf16's g s u an ordinary number if u is large.)  The fast exponential is off by up to
-// 2 + 1.173 |z| units of 2^-23 (CUDA's bound), so s by about 2^-20 of itself at z = -3, 2^-18 at -20 and
-// 2^-16 at -80, and less where z > 0: e is then the smaller part of 1 + e.  h and what the products
-// take are rounded to 2^-8 or 2^-11 afterwards.
+// s is 1e-38, and bf16's g s u an ordinary number if u is large.)  e is the square of 2^(-|z| log2(e) / 2),
+// whose smallest numbers are normal ones where e's are not, as the hardware's exponential wants them.
+// The exponent's two roundings make e off by |z| 2^-23 of itself, the exponential and the reciprocal by a
+// few 2^-23: s by about 2^-20 at z = -3, 2^-18.5 at -20 and 2^-16.5 at -80, and less where z > 0, as e is
+// the smaller part of 1 + e then.  h and what the products take are rounded to 2^-8 or 2^-11 afterwards.
 constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
+constexpr float kHalfLog2E = 0.72134752f;
+
+__device__ __forceinline__ float exp2_fast(float x) {        // 0 where 2^x is below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float reciprocal_fast(float x) {  // of 1 to 2
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// -bound to bound; a NaN stays one.
+__device__ __forceinline__ float held_to(float x, float bound) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(-bound));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(bound));
+    return r;
+}
 
 struct Act {
     float s, slope_z, g, near;
@@ -32,13 +52,13 @@ struct Act {
         float z = g;
         a.slope_z = 1.0f;
         if (ACT == kGeluTanh) {
-            // From |g| = 30 on s is 0 or 1, and beyond 10^19 g^2 would overflow.  (A NaN stays one.)
-            const float c = fabsf(g) > 30.0f ? copysignf(30.0f, g) : g, q = c * c;
+            // From |g| = 30 on s is 0 or 1, and beyond 10^19 g^2 would overflow.
+            const float c = held_to(g, 30.0f), q = c * c;
             a.near = c;
             z = kGeluC * c * fmaf(kGeluCube, q, 1.0f);
             a.slope_z = kGeluC * fmaf(3.0f * kGeluCube, q, 1.0f);
         }
-        const float e = __expf(-fabsf(z)), r = __fdividef(1.0f, 1.0f + e);
+        const float root = exp2_fast(-kHalfLog2E * fabsf(z)), e = root * root, r = reciprocal_fast(1.0f + e);
         a.s = z < 0.0f ? e * r : r;
         return a;
     }
