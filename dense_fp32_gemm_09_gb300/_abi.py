@@ -76,6 +76,7 @@ SIGNATURES = {
     "sgemm_layer_norm_backward_workspace": (_i, [_i, _i, ctypes.POINTER(_sz)]),
     "sgemm_layer_norm_backward": (_i, [_i, _i, _i] + [_vp, _i] * 3 + [_vp] * 5 + [_i, _vp, _i]
                                   + [_vp] * 3 + [_sz, _vp]),
+    "sgemm_layer_norm_choose_check": (_i, [_i] * 9 + [ctypes.POINTER(_i)] * 4),
     "sgemm_gated_ff_workspace": (_i, [_i] * 5 + [ctypes.POINTER(_sz)]),
     "sgemm_gated_ff_choose_check": (_i, [_i] * 5 + [ctypes.POINTER(_i), ctypes.POINTER(_i)]),
     "sgemm_gated_ff_forward": (_i, [_i] * 5 + [_vp, _i] * 4 + [_i, _vp, _vp, _i, _vp, _vp, _vp, _sz,

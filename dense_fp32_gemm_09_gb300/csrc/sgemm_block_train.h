@@ -62,6 +62,15 @@ cudaError_t launch_layer_norm_forward(const LayerNormForward& p, int sms, cudaSt
 size_t layer_norm_backward_workspace(int rows, int cols, int sms);
 cudaError_t launch_layer_norm_backward(const LayerNormBackward& p, int sms, cudaStream_t stream,
                                        int* launches);
+// What the norm takes for matrices whose rows all begin `begin` bytes past 16 and are ld apart, on `sms` SMs
+// with room for `clusters` clusters of blocks: how rows are accessed (0 whole 16-byte groups, 1 shifted ones,
+// 2 single columns, 3 streaming), the places where they begin, a row's blocks, and how many such sets of blocks
+// share the rows.
+struct LayerNormChoice {
+    int access, places, blocks, sets;
+};
+LayerNormChoice choose_layer_norm(int rows, int cols, int dtype, bool backward, bool keep, int begin, long long ld,
+                                  int sms, int clusters);
 
 enum : int { kSilu = 0, kGeluTanh = 1 };
 enum : int { kKeepNone = 0, kKeepFull = 1, kKeep8 = 2 };

@@ -254,8 +254,9 @@ struct Alignment {
         whole = static_cast<long long>(cols) * elem % 16 == 0;
     }
     void add(const void* p, long long ld) {
-        if (p == nullptr) return;
-        const int at = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16);
+        if (p != nullptr) add_at(static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16), ld);
+    }
+    void add_at(int at, long long ld) {
         const int by = rows > 1 ? static_cast<int>(ld * elem % 16) : 0;
         whole &= at == 0 && by == 0;
         same &= !any || (at == base && by == step);
@@ -276,7 +277,8 @@ struct Alignment {
         return n;
     }
 };
-// A block a row, `own` columns a thread; up to `most` threads an SM.
+// A block a row, `own` columns a thread; up to `most` threads an SM.  (A grid of 0: on a small part of a GPU
+// there may be fewer blocks than places where rows begin.)
 Shape by_block(long long rows, int cols, int own, int most, int access, int period, int sms,
                bool keeps = false) {
     Shape s{};
@@ -292,34 +294,30 @@ Shape by_block(long long rows, int cols, int own, int most, int access, int peri
     return s;
 }
 
-Shape forward_shape(const LayerNormForward& p, int sms) {
-    Alignment on(p.dtype, p.rows, p.cols);
-    on.add(p.x, p.ldx);
-    on.add(p.y, p.ldy);
-    on.add_vector(p.weight);
-    on.add_vector(p.bias);
+Shape forward_shape(const Alignment& on, int cols, bool keep, int sms) {
+    const long long rows = on.rows;
     if (!on.whole) {
-        if (on.access(p.cols, sms) == kShifted && p.cols <= 16 * 512)
-            return by_block(p.rows, p.cols, 16, 512, kShifted, on.period(), sms);
+        if (on.access(cols, sms) == kShifted && cols <= 16 * 512) {
+            const Shape s = by_block(rows, cols, 16, 512, kShifted, on.period(), sms);
+            if (s.grid > 0) return s;
+        }
         // (The checkpoint takes registers that only blocks of up to 512 threads have.)
-        if (p.codes && p.cols <= 8 * 512) return by_block(p.rows, p.cols, 8, 512, kSingle, 1, sms, true);
-        if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 8, 1024, kSingle, 1, sms);
+        if (keep && cols <= 8 * 512) return by_block(rows, cols, 8, 512, kSingle, 1, sms, true);
+        if (cols <= 8 * 1024) return by_block(rows, cols, 8, 1024, kSingle, 1, sms);
         return Shape{kWide};
     }
-    const bool keep = p.codes != nullptr;
-    if (p.rows <= 2LL * sms && p.cols <= 8 * 1024)
-        return by_block(p.rows, p.cols, 8, 1024, kWhole, 1, sms, keep);
-    if (p.cols <= 256) {
+    if (rows <= 2LL * sms && cols <= 8 * 1024) return by_block(rows, cols, 8, 1024, kWhole, 1, sms, keep);
+    if (cols <= 256) {
         Shape s{};
         s.keeps = keep;
         s.kind = kByWarp;
-        s.groups = p.cols * on.elem <= 512 ? 1 : 2;
-        s.grid = static_cast<int>((p.rows + 3LL) / 4);
+        s.groups = cols * on.elem <= 512 ? 1 : 2;
+        s.grid = static_cast<int>((rows + 3LL) / 4);
         return s;
     }
-    if (p.cols <= 8 * 1024) return by_block(p.rows, p.cols, 16, 512, kWhole, 1, sms, keep);
+    if (cols <= 8 * 1024) return by_block(rows, cols, 16, 512, kWhole, 1, sms, keep);
     // Wider 2-byte rows, as far as weight and bias fit beside them in shared memory.
-    if (p.cols <= 16 * 1024 && on.elem == 2) return by_block(p.rows, p.cols, 16, 1024, kWhole, 1, sms, keep);
+    if (cols <= 16 * 1024 && on.elem == 2) return by_block(rows, cols, 16, 1024, kWhole, 1, sms, keep);
     return Shape{kWide};
 }
 
@@ -327,45 +325,50 @@ Shape forward_shape(const LayerNormForward& p, int sms) {
 // ragged or fp32 rows, sixteen of 2-byte ones.  Teams of up to 128 share a block an SM, so that
 // fewer sums are left to add up (16384 x 256 bf16 13.7 against 16.9 us, 8192 x 1024 19.4 against
 // 21.2); for wider rows the blocks' own pace counts more (8192 x 4096 52.4 against 50.1).
-Shape backward_shape(const LayerNormBackward& p, int sms) {
-    Alignment on(p.dtype, p.rows, p.cols);
-    on.add(p.dh, p.lddh);
-    on.add(p.dy, p.lddy);
-    on.add(p.x, p.ldx);
-    on.add(p.dx, p.lddx);
-    on.add_vector(p.weight);
+// clusters(shape): how many of its clusters run at once.  A part of a GPU may have room for fewer than
+// there are places where shifted rows begin, which are single columns then, or for none: streaming.
+template <typename Clusters>
+Shape backward_shape(const Alignment& on, int cols, int sms, Clusters clusters) {
+    const long long rows = on.rows;
     Shape s{};
     s.kind = kByBlock;
-    s.access = on.access(p.cols, sms);
-    s.period = s.access == kShifted ? on.period() : 1;
-    s.columns = s.access == kSingle || p.dtype == kF32 ? 8 : 16;
-    if (p.cols <= s.columns * 512) {
-        s.team = 32;
-        while (s.team * s.columns < p.cols) s.team *= 2;
-        const long long room = s.team <= 128 ? 512 / s.team : 1;
-        const int teams = static_cast<int>(std::max(1LL, std::min(room, (p.rows + 0LL + sms - 1) / sms)));
-        s.threads = teams * s.team;
-        const long long per = std::min(512 / static_cast<long long>(room * s.team), 2LL);
-        s.grid = whole_steps(static_cast<int>(std::min((p.rows + 0LL + teams - 1) / teams, sms * per)), s.period,
-                             (p.rows + 0LL + teams - 1) / teams);
-        s.blocks = 1;
-        return s;
-    }
-    if (p.cols <= 8 * (s.columns * 512 - 64)) {    // up to eight blocks a row, whole blocks of 64 each
-        s.team = s.threads = 512;
-        // (Clusters of three blocks of 256 threads, two to an SM, 11279 x 9208 bf16: 463 us, of two of
-        // 512 threads 313.)
-        for (s.blocks = 2;; s.blocks *= 2) {
-            s.each = static_cast<int>(act8_pitch((p.cols + s.blocks - 1) / s.blocks));
-            if (s.each <= s.columns * 512) break;
+    for (int access = on.access(cols, sms);; access = kSingle) {
+        s.access = access;
+        s.period = access == kShifted ? on.period() : 1;
+        s.columns = access == kSingle || on.elem == 4 ? 8 : 16;
+        if (cols <= s.columns * 512) {
+            s.team = 32;
+            while (s.team * s.columns < cols) s.team *= 2;
+            const long long room = s.team <= 128 ? 512 / s.team : 1;
+            const int teams = static_cast<int>(std::max(1LL, std::min(room, (rows + sms - 1) / sms)));
+            s.threads = teams * s.team;
+            const long long per = std::min(512 / static_cast<long long>(room * s.team), 2LL);
+            const long long all = (rows + teams - 1) / teams;
+            s.grid = whole_steps(static_cast<int>(std::min(all, sms * per)), s.period, all);
+            s.blocks = 1;
+        } else if (cols <= 8 * (s.columns * 512 - 64)) {    // up to eight blocks a row, whole blocks of 64 each
+            s.team = s.threads = 512;
+            // (Clusters of three blocks of 256 threads, two to an SM, 11279 x 9208 bf16: 463 us, of two of
+            // 512 threads 313.)
+            for (s.blocks = 2;; s.blocks *= 2) {
+                s.each = static_cast<int>(act8_pitch((cols + s.blocks - 1) / s.blocks));
+                if (s.each <= s.columns * 512) break;
+            }
+            // (No more than run at once: one that waits for its SMs would come to its rows when the others
+            // are done.)
+            s.grid = static_cast<int>(std::min<long long>(rows, sms / s.blocks)) * s.blocks;
+            const int most = s.grid ? clusters(s) : 0;
+            s.grid = whole_steps(std::min(s.grid / s.blocks, most), s.period, rows) * s.blocks;
+        } else {
+            s.grid = 0;
         }
-        s.grid = static_cast<int>(std::min<long long>(p.rows, sms / s.blocks)) * s.blocks;
-        return s;
+        if (s.grid > 0) return s;
+        if (access != kShifted) break;
     }
     // Strips of rows, for eight blocks an SM and no more strips than the workspace holds.
     s = Shape{kWide};
-    const long long tiles = (p.cols + 31) / 32;
-    s.grid = static_cast<int>(std::max(1LL, std::min({8LL * sms / tiles, 2LL * sms, p.rows / 16LL})));
+    const long long tiles = (cols + 31) / 32;
+    s.grid = static_cast<int>(std::max(1LL, std::min({8LL * sms / tiles, 2LL * sms, rows / 16LL})));
     return s;
 }
 
@@ -390,7 +393,12 @@ size_t layer_norm_backward_workspace(int rows, int cols, int sms) {
 cudaError_t launch_layer_norm_forward(const LayerNormForward& p, int sms, cudaStream_t stream,
                                       int* launches) {
     *launches = 1;
-    const Shape s = forward_shape(p, sms);
+    Alignment on(p.dtype, p.rows, p.cols);
+    on.add(p.x, p.ldx);
+    on.add(p.y, p.ldy);
+    on.add_vector(p.weight);
+    on.add_vector(p.bias);
+    const Shape s = forward_shape(on, p.cols, p.codes != nullptr, sms);
     cudaError_t e;
     if (s.kind == kWide) {
         const dim3 grid(static_cast<unsigned>(p.rows));
@@ -413,9 +421,23 @@ cudaError_t launch_layer_norm_forward(const LayerNormForward& p, int sms, cudaSt
 
 cudaError_t launch_layer_norm_backward(const LayerNormBackward& p, int sms, cudaStream_t stream,
                                        int* launches) {
-    Shape s = backward_shape(p, sms);
     *launches = 1;
-    cudaError_t e;
+    Alignment on(p.dtype, p.rows, p.cols);
+    on.add(p.dh, p.lddh);
+    on.add(p.dy, p.lddy);
+    on.add(p.x, p.ldx);
+    on.add(p.dx, p.lddx);
+    on.add_vector(p.weight);
+    cudaError_t e = cudaSuccess;
+    const Shape s = backward_shape(on, p.cols, sms, [&](const Shape& of) {
+        int most = 0;
+        const cudaError_t asked = p.dtype == kF32    ? layer_norm::clusters_f32(p, of, &most)
+                                  : p.dtype == kBf16 ? layer_norm::clusters_bf16(p, of, &most)
+                                                     : layer_norm::clusters_f16(p, of, &most);
+        if (asked != cudaSuccess) e = asked;
+        return most;
+    });
+    if (e != cudaSuccess) return e;
     if (s.kind == kWide) {
         e = p.dtype == kF32    ? backward_wide<float>(p, s, sms, stream, launches)
             : p.dtype == kBf16 ? backward_wide<__nv_bfloat16>(p, s, sms, stream, launches)
@@ -429,6 +451,18 @@ cudaError_t launch_layer_norm_backward(const LayerNormBackward& p, int sms, cuda
     ++*launches;
     return launch_dependent(layer_norm_columns, dim3((p.cols + 31) / 32, 2), 1024, 0, stream, p,
                             s.kind == kWide ? s.grid : s.grid / s.blocks);
+}
+
+LayerNormChoice choose_layer_norm(int rows, int cols, int dtype, bool backward, bool keep, int begin, long long ld,
+                                  int sms, int clusters) {
+    Alignment on(dtype, rows, cols);
+    on.add_at(begin, ld);
+    const Shape s = backward ? backward_shape(on, cols, sms, [&](const Shape&) { return clusters; })
+                             : forward_shape(on, cols, keep, sms);
+    if (s.kind == kWide) return {3, 1, 1, backward ? s.grid : rows};
+    if (s.kind == kByWarp) return {kWhole, 1, 1, s.grid};
+    const int blocks = backward ? s.blocks : 1;
+    return {s.access, s.access == kShifted ? s.period : 1, blocks, s.grid / blocks};
 }
 
 }  // namespace sgemm

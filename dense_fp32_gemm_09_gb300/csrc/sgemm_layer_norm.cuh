@@ -960,12 +960,8 @@ cudaError_t forward(const LayerNormForward& p, const Shape& s, cudaStream_t st) 
                                     0, st, p);
     return s.keeps ? forward_rows_of<T, true>(p, s, st) : forward_rows_of<T, false>(p, s, st);
 }
-// No more clusters of `blocks` than run at once, s.grid blocks at most.  (One that waits for its SMs
-// would come to its rows when the others are done.)
-template <typename K, typename... A>
-cudaError_t launch_clusters(K kernel, Shape& s, int smem, cudaStream_t st, const LayerNormBackward& p,
-                            const A&... args) {
-    cudaLaunchAttribute at[2];
+// Of a launch of s.grid blocks, in clusters of s.blocks; with the attributes of `at`, the first the cluster's.
+inline cudaLaunchConfig_t cluster_launch(const Shape& s, int smem, cudaStream_t st, cudaLaunchAttribute (&at)[2]) {
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = s.blocks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -977,30 +973,21 @@ cudaError_t launch_clusters(K kernel, Shape& s, int smem, cudaStream_t st, const
     c.dynamicSmemBytes = smem;
     c.stream = st;
     c.attrs = at;
-    c.numAttrs = 1;
-    int most = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&most, kernel, &c);
-    if (e != cudaSuccess) return e;
-    if (most < s.period) return cudaErrorInvalidConfiguration;     // (a small part of a GPU)
-    s.grid = whole_steps(std::min(s.grid / s.blocks, most), s.period, p.rows) * s.blocks;
-    c.gridDim = dim3(static_cast<unsigned>(s.grid));
     c.numAttrs = 2;
-    return cudaLaunchKernelEx(&c, kernel, p, args...);
+    return c;
 }
-template <typename T>
-cudaError_t backward(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
+// use(kernel, shared memory, its arguments after p) for the kernel that takes a shape.
+template <typename T, typename F>
+cudaError_t with_backward(const LayerNormBackward& p, const Shape& s, F use) {
     constexpr int OWN = sizeof(T) == 4 ? 8 : 16;
     const int teams = s.threads / s.team;
     // The teams' sums at the end.
     const int held = teams > 1 || s.access == kShifted
                          ? teams * 2 * held_width(s.blocks == 1 ? p.cols : s.each) * static_cast<int>(sizeof(float)) : 0;
     const auto run = [&](auto kernel, int smem, const auto&... more) {
-        smem = std::max(smem, held);
         const cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, norm::kSharedPerSm);
-        if (e != cudaSuccess) return e;
-        if (s.blocks == 1) return launch_dependent(kernel, dim3(s.grid), s.threads, smem, st, p, more...);
-        return launch_clusters(kernel, s, smem, st, p, more...);
+        return e != cudaSuccess ? e : use(kernel, std::max(smem, held), more...);
     };
     const auto choose = [&](auto one, auto split, int smem, const auto&... more) {
         return s.blocks == 1 ? run(one, smem, more...) : run(split, smem, more...);
@@ -1032,6 +1019,24 @@ cudaError_t backward(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
                             backward_ring<T, kWhole, OWN, true, true>, smem, ring)
                    : choose(backward_ring<T, kWhole, OWN, false, false>,
                             backward_ring<T, kWhole, OWN, false, true>, smem, ring);
+}
+template <typename T>
+cudaError_t backward(const LayerNormBackward& p, const Shape& s, cudaStream_t st) {
+    return with_backward<T>(p, s, [&](auto kernel, int smem, const auto&... more) {
+        if (s.blocks == 1) return launch_dependent(kernel, dim3(s.grid), s.threads, smem, st, p, more...);
+        cudaLaunchAttribute at[2];
+        const cudaLaunchConfig_t c = cluster_launch(s, smem, st, at);
+        return cudaLaunchKernelEx(&c, kernel, p, more...);
+    });
+}
+template <typename T>
+cudaError_t clusters(const LayerNormBackward& p, const Shape& s, int* most) {
+    return with_backward<T>(p, s, [&](auto kernel, int smem, const auto&...) {
+        cudaLaunchAttribute at[2];
+        cudaLaunchConfig_t c = cluster_launch(s, smem, nullptr, at);
+        c.numAttrs = 1;
+        return cudaOccupancyMaxActiveClusters(most, kernel, &c);
+    });
 }
 
 }  // namespace layer_norm

@@ -23,7 +23,8 @@ struct Shape {
     int period;        // kShifted: rows from one to the next that begins at the same place of a group
 };
 
-// Sets of rows of which each takes every `sets`-th: a multiple of the period, unless none has a second.
+// Sets of rows of which each takes every `sets`-th: a multiple of the period, unless none has a second; 0 where
+// there are fewer than that.
 inline int whole_steps(int sets, int period, long long rows) {
     return rows <= sets ? sets : sets - sets % period;
 }
@@ -40,10 +41,13 @@ struct Ring {
 cudaError_t forward_f32(const LayerNormForward& p, const Shape& s, cudaStream_t st);
 cudaError_t forward_bf16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
 cudaError_t forward_f16(const LayerNormForward& p, const Shape& s, cudaStream_t st);
-// (With clusters, the grid becomes as many as run at once.)
-cudaError_t backward_f32(const LayerNormBackward& p, Shape& s, cudaStream_t st);
-cudaError_t backward_bf16(const LayerNormBackward& p, Shape& s, cudaStream_t st);
-cudaError_t backward_f16(const LayerNormBackward& p, Shape& s, cudaStream_t st);
+cudaError_t backward_f32(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
+cudaError_t backward_bf16(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
+cudaError_t backward_f16(const LayerNormBackward& p, const Shape& s, cudaStream_t st);
+// How many clusters of a shape run at once.
+cudaError_t clusters_f32(const LayerNormBackward& p, const Shape& s, int* most);
+cudaError_t clusters_bf16(const LayerNormBackward& p, const Shape& s, int* most);
+cudaError_t clusters_f16(const LayerNormBackward& p, const Shape& s, int* most);
 
 }  // namespace layer_norm
 }  // namespace sgemm

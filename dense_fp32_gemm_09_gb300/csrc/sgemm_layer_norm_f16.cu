@@ -7,8 +7,11 @@ namespace layer_norm {
 cudaError_t forward_f16(const LayerNormForward& p, const Shape& s, cudaStream_t st) {
     return forward<__half>(p, s, st);
 }
-cudaError_t backward_f16(const LayerNormBackward& p, Shape& s, cudaStream_t st) {
+cudaError_t backward_f16(const LayerNormBackward& p, const Shape& s, cudaStream_t st) {
     return backward<__half>(p, s, st);
+}
+cudaError_t clusters_f16(const LayerNormBackward& p, const Shape& s, int* most) {
+    return clusters<__half>(p, s, most);
 }
 
 }  // namespace layer_norm

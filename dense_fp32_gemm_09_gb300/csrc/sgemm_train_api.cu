@@ -237,6 +237,25 @@ int sgemm_layer_norm_backward(int rows, int cols, int dtype, const void* dh, int
     });
 }
 
+int sgemm_layer_norm_choose_check(int rows, int cols, int dtype, int backward, int keep, int begin, int ld, int sms,
+                                  int clusters, int* access, int* places, int* blocks, int* sets) {
+    return guarded([&]() -> int {
+        const char* const what = "sgemm_layer_norm_choose_check";
+        SGEMM_TRY(check_dtype(dtype));
+        SGEMM_TRY(check_extent(what, rows, cols));
+        if (rows == 0 || cols == 0 || begin < 0 || begin > 15 || begin % elem_size(dtype) || ld < cols || sms < 1 ||
+            clusters < 0 || !access || !places || !blocks || !sets)
+            return refuse(SGEMM_ERR_INVALID_ARG, "%s: bad argument", what);
+        const LayerNormChoice c =
+            choose_layer_norm(rows, cols, dtype, backward != 0, keep != 0, begin, ld, sms, clusters);
+        *access = c.access;
+        *places = c.places;
+        *blocks = c.blocks;
+        *sets = c.sets;
+        return SGEMM_OK;
+    });
+}
+
 int sgemm_gated_ff_workspace(int M, int N, int K, int backward, int packed, size_t* bytes) {
     return guarded([&]() -> int {
         SGEMM_TRY(check_ff("sgemm_gated_ff_workspace", M, N, K, SGEMM_BF16, SGEMM_SILU,

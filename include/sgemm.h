@@ -498,6 +498,14 @@ SGEMM_API int sgemm_layer_norm_backward(int rows, int cols, int dtype, const voi
                                         void* dx, int lddx, float* dweight, float* dbias, void* ws,
                                         size_t ws_bytes, sgemm_stream_t stream);
 
+/* What layer norm (`backward` 0, with `keep` with a checkpoint, or 1) takes on a GPU, or a part of one, of `sms` SMs
+ * where `clusters` clusters of blocks run at once, for matrices whose rows all begin `begin` bytes past a multiple
+ * of 16 and are ld apart (host only): in *access 0 for rows of whole 16-byte groups, 1 for rows that begin at
+ * *places places of one, 2 for single columns, 3 for the kernels that stream rows of any width; in *blocks those
+ * that share a row, in *sets the sets of them that share the rows. */
+SGEMM_API int sgemm_layer_norm_choose_check(int rows, int cols, int dtype, int backward, int keep, int begin, int ld,
+                                            int sms, int clusters, int* access, int* places, int* blocks, int* sets);
+
 /* ---------------------------------------------------------------------------
  * Gated feed-forward block, of SGEMM_BF16 or SGEMM_F16 numbers:
  *
