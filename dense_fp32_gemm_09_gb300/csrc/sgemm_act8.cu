@@ -104,7 +104,12 @@ __global__ void __launch_bounds__(kThreads) act8_quantize_ragged(const Act8Quant
     }
 }
 
-template <typename T>
+// What rounding v to a number r leaves; nothing of an infinity.
+__device__ __forceinline__ float rest_of(float v, float r) {
+    return act8::magnitude(r) == 0x7F800000u ? 0.0f : v - r;
+}
+// REST: the rests too.
+template <typename T, bool REST>
 __global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequantize q,
                                                                  const bool on32) {
     constexpr int VEC = 16 / sizeof(T), COLS = 2 * VEC;
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequa
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (to[i] == nullptr) break;
-            uint4 out[2];
+            uint4 out[2], rest[2];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 Two v[VEC / 2];
@@ -152,14 +157,28 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_rows(const Act8Dequa
                     values4(codes[i][g * VEC / 4 + j], scale[i],
                             reinterpret_cast<Two(&)[2]>(v[2 * j]));
                 out[g] = mx4::pack(v, T());
+                if constexpr (REST) {
+                    Two r[VEC / 2];
+                    mx4::unpack(out[g], r, T());
+#pragma unroll
+                    for (int j = 0; j < VEC / 2; ++j) {
+                        const float2 a = mx4::parts(v[j]), b = mx4::parts(r[j]);
+                        v[j] = mx4::two(rest_of(a.x, b.x), rest_of(a.y, b.y));
+                    }
+                    rest[g] = mx4::pack(v, T());
+                }
             }
-            if (both[i]) store_pair(to[i], on32, out);
-            else *reinterpret_cast<uint4*>(to[i]) = out[0];
+            const auto put = [&](T* at, const uint4 (&w)[2]) {
+                if (both[i]) store_pair(at, on32, w);
+                else *reinterpret_cast<uint4*>(at) = w[0];
+            };
+            put(to[i], out);
+            if constexpr (REST) put(static_cast<T*>(q.rest) + (to[i] - static_cast<T*>(q.Y)), rest);
         }
     }
 }
 
-template <typename T>
+template <typename T, bool REST>
 __global__ void __launch_bounds__(kThreads) act8_dequantize_ragged(const Act8Dequantize q) {
     const long long pitch = act8_pitch(q.cols);
     const int lane = threadIdx.x & 31;
@@ -169,7 +188,8 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_ragged(const Act8Deq
     start_dependent();
     for (; at.row < q.rows; at.next()) {
         const int c0 = at.col * 256 + lane;
-        T* const y = static_cast<T*>(q.Y) + at.row * q.ldy + c0;
+        const long long to = at.row * q.ldy + c0;
+        T* const y = static_cast<T*>(q.Y) + to;
         const int8_t* const codes = q.codes + at.row * pitch + c0;
         const float* const scales = q.scales + at.row * (pitch / kAct8Block) + at.col * 4;
         const int left = q.cols - c0, kept = static_cast<int>(pitch) - at.col * 256;
@@ -181,7 +201,13 @@ __global__ void __launch_bounds__(kThreads) act8_dequantize_ragged(const Act8Deq
         for (int b = 0; b < 4; ++b) scale[b] = 64 * b < kept ? fetch(scales + b) : 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (32 * i < left) y[32 * i] = from_float<T>(value(code[i], scale[i / 2]));
+            if (32 * i < left) {
+                const float v = value(code[i], scale[i / 2]);
+                const T r = from_float<T>(v);
+                y[32 * i] = r;
+                if constexpr (REST)
+                    static_cast<T*>(q.rest)[to + 32 * i] = from_float<T>(rest_of(v, to_float(r)));
+            }
     }
 }
 
@@ -210,16 +236,21 @@ cudaError_t quantize(const Act8Quantize& q, int sms, cudaStream_t st) {
                             grid_of(q.rows * ((pitch + 255) / 256), kThreads / 32, sms), kThreads, 0, st,
                             q);
 }
-template <typename T>
+template <typename T, bool REST>
 cudaError_t dequantize(const Act8Dequantize& q, int sms, cudaStream_t st) {
     constexpr int COLS = 32 / sizeof(T);
-    if (whole(q.Y, q.rows, q.cols, q.ldy, sizeof(T)))
-        return launch_dependent(act8_dequantize_rows<T>,
+    if (whole(q.Y, q.rows, q.cols, q.ldy, sizeof(T)) && whole(q.rest, q.rows, q.cols, q.ldy, sizeof(T)))
+        return launch_dependent(act8_dequantize_rows<T, REST>,
                                 grid_of(q.rows * ((q.cols + COLS - 1LL) / COLS), kThreads, sms),
-                                kThreads, 0, st, q, on_32(q.Y, q.rows, q.ldy, sizeof(T)));
-    return launch_dependent(act8_dequantize_ragged<T>,
+                                kThreads, 0, st, q,
+                                on_32(q.Y, q.rows, q.ldy, sizeof(T)) && on_32(q.rest, q.rows, q.ldy, sizeof(T)));
+    return launch_dependent(act8_dequantize_ragged<T, REST>,
                             grid_of(q.rows * ((act8_pitch(q.cols) + 255) / 256), kThreads / 32, sms),
                             kThreads, 0, st, q);
+}
+template <typename T>
+cudaError_t dequantize(const Act8Dequantize& q, int sms, cudaStream_t st) {
+    return q.rest ? dequantize<T, true>(q, sms, st) : dequantize<T, false>(q, sms, st);
 }
 
 }  // namespace
@@ -231,7 +262,7 @@ cudaError_t launch_act8_quantize(const Act8Quantize& q, int sms, cudaStream_t st
 }
 
 cudaError_t launch_act8_dequantize(const Act8Dequantize& q, int sms, cudaStream_t stream) {
-    return q.dtype == mx4::kF32    ? dequantize<float>(q, sms, stream)
+    return q.dtype == mx4::kF32    ? dequantize<float, false>(q, sms, stream)       // (fp32 holds them)
            : q.dtype == mx4::kBf16 ? dequantize<__nv_bfloat16>(q, sms, stream)
                                    : dequantize<__half>(q, sms, stream);
 }

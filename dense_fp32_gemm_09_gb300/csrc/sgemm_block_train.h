@@ -27,6 +27,7 @@ struct Act8Dequantize {
     const float* scales;
     void* Y;
     long long ldy;
+    void* rest;                    // null, or as Y: what the roundings to Y leave, rounded
 };
 cudaError_t launch_act8_quantize(const Act8Quantize& q, int sms, cudaStream_t stream);
 cudaError_t launch_act8_dequantize(const Act8Dequantize& q, int sms, cudaStream_t stream);

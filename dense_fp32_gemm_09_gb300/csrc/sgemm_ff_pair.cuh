@@ -335,7 +335,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         abort_s = 0;
         mbar_fence_init();
     }
-    if (warp == 0 && lane < (MODE == kForward ? 3 : 7)) {
+    if (warp == 0 && lane < (MODE == kForward ? 3 : pl.of[1].half < pl.of[1].stages ? 8 : 7)) {
         const CUtensorMap* tm = MODE == kForward ? (lane < 1 ? &maps.a[0] : &maps.b[lane - 1])
                                                  : (lane < 4 ? &maps.a[lane] : &maps.b[lane - 4]);
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
@@ -371,12 +371,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         load_box(a, &maps.a[0], s * kDeep, row, fb);
                         load_box(b, &maps.b[rank], s * kDeep, col, fb);
                     } else {
-                        int k = s * kDeep;
-                        const CUtensorMap* bm = &maps.b[2];
-                        if (t.result == 0) {       // dg and Wg, then du and Wu
-                            const int half = pl.of[0].stages / 2, second = s >= half;
-                            k -= second * half * kDeep;
-                            bm = &maps.b[second];
+                        // dg and Wg, then du and Wu; x, then its rest.
+                        const int half = pl.of[t.result > 0].half, second = s >= half;
+                        const int k = (s - second * half) * kDeep;
+                        const CUtensorMap* bm = &maps.b[2 * (t.result > 0) + second];
+                        if (t.result == 0) {
                             load_box(a, &maps.a[second], k, row, fb);
                         } else {
                             const CUtensorMap* am = &maps.a[1 + t.result];

@@ -13,16 +13,18 @@ enum : int { kForward = 0, kBackward = 1 };
 constexpr int kTileRows = 256;
 
 // Forward: a[0] x, b[0] Wg, b[1] Wu.  Backward: a[0], a[1] dg, du read along their rows, a[2], a[3]
-// across them (fp16: matrices of their own, see scale_up), b[0] Wg, b[1] Wu, b[2] x.  A parameter of its own: its address is taken, and if it
+// across them (fp16: matrices of their own, see scale_up), b[0] Wg, b[1] Wu, b[2] x, of an x in
+// 8 bits b[3] what the roundings to b[2] leave.  A parameter of its own: its address is taken, and if it
 // were the plan's, the plan would be read again after every store.
 struct PairMaps {
-    CUtensorMap a[4], b[3];
+    CUtensorMap a[4], b[4];
 };
 // Forward: h.  Backward: dx; and dWg with dWu, one product whose tiles of rows follow each other.
 struct Product {
     int rows, cols;            // of a result
     int tiles_m, tiles_n;
-    int stages;                // of a tile's contraction, 64 each (both halves of dx's)
+    int stages;                // of a tile's contraction, 64 each (both halves of dx's, or of an x in two)
+    int half;                  // backward: stages of the first half
     int split;                 // parts of a tile's contraction
     long long items() const { return static_cast<long long>(tiles_m) * tiles_n * split; }
 };

@@ -6,10 +6,10 @@
 //     du = dh act(g)     dg = dh u act'(g)                 element by element, to the workspace
 //     dx = dg Wg + du Wu      dWg = dg^T x      dWu = du^T x
 // dg and du are rounded to the type of x, the tensor cores' operand type, so that a gradient
-// is off by the rounding of its terms (half an ulp each, at random) beside its own; so are the
-// numbers of an x that comes in 8 bits, whose own steps are 2^-8 of their block's largest.  In
-// norm, bf16: dx and the weights' gradients 2.3e-3 of 64 bits' where the rounding of the result
-// alone is 1.7e-3, the weights' gradients of an x in 8 bits 2.8e-3.  fp16 has too few exponents for dg and
+// is off by the rounding of its terms (half an ulp each, at random) beside its own: in norm, bf16,
+// 2.3e-3 of 64 bits' where the rounding of the result alone is 1.7e-3.  The numbers of an x that comes in
+// 8 bits are code times scale, of more bits than the type has: the products take the rounding and the
+// rounding of what is left, as two halves of one contraction (the rounding alone: 2.8e-3).  fp16 has too few exponents for dg and
 // du and takes them by powers of two for each row and column (ff_gradient_fp16).
 //
 // The products: sgemm_ff_pair.cuh, and sgemm_ff_token.cu for up to 16 tokens.  Rows that are not on
@@ -424,10 +424,11 @@ Spread spread(long long n, long long m, double one, double two, long long pairs)
 struct Gradients {
     int bn, split_x, split_w;
 };
-Gradients choose_gradients(int M, int N, int K) {
+// x_parts: 2 for an x in 8 bits.
+Gradients choose_gradients(int M, int N, int K, int x_parts) {
     Gradients best{256, 1, 1};
     double least = 0;
-    const long long deep_x = 2 * up_to(N, 64), deep_w = up_to(M, 64);
+    const long long deep_x = 2 * up_to(N, 64), deep_w = x_parts * up_to(M, 64);
     for (int bn : {256, 128}) {
         const long long x = up_to(M, kTileRows) * up_to(K, bn), w = 2 * up_to(N, kTileRows) * up_to(K, bn);
         const auto parts = [](int split, long long tiles, long long stages) {
@@ -528,7 +529,7 @@ cudaError_t forward(const GatedFfForward& p, int sms, cudaStream_t st, int* laun
         return cudaErrorInvalidValue;
     PairPlan pl{};
     pl.of[0] = {p.M, p.N, static_cast<int>(up_to(p.M, kTileRows)), static_cast<int>(up_to(p.N, c.bn / 2)),
-                static_cast<int>(up_to(p.K, 64)), 1};
+                static_cast<int>(up_to(p.K, 64)), 0, 1};
     pl.pairs = static_cast<int>(std::min<long long>(sms / 2, pl.of[0].items()));
     pl.to[0] = {p.h, p.ldh, on16(p.h, p.M, p.ldh), nullptr, nullptr};
     pl.kept = p.kept;
@@ -616,12 +617,16 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
         q.of_du = q.of_dg + p.N;
     }
     Operands in(p.M, p.N, p.K, p.x, p.ldx, p.w_gate, p.ldg, p.w_up, p.ldu, at);
-    if (p.x_codes) {       // rounded to the operands' type
+    const void* rest = nullptr;
+    if (p.x_codes) {       // the operands' type holds them in two
         in.x = in.at;
         in.ldx = up64(p.K);
         in.at += matrix_bytes(p.M, p.K);
+        rest = in.at;
+        in.at += matrix_bytes(p.M, p.K);
         const cudaError_t e = launch_act8_dequantize(
-            Act8Dequantize{p.M, p.K, p.dtype, p.x_codes, p.x_scales, const_cast<void*>(in.x), in.ldx},
+            Act8Dequantize{p.M, p.K, p.dtype, p.x_codes, p.x_scales, const_cast<void*>(in.x), in.ldx,
+                           const_cast<void*>(rest)},
             sms, st);
         if (e != cudaSuccess) return e;
         ++*launches;
@@ -636,20 +641,22 @@ cudaError_t backward(const GatedFfBackward& p, int sms, cudaStream_t st, int* la
     PairPlan pl{};
     pl.status = status_word_ptr();
     // dx, from dg and Wg, then du and Wu; dWg and dWu.
-    const Gradients c = choose_gradients(p.M, p.N, p.K);
+    const int x_parts = rest ? 2 : 1;
+    const Gradients c = choose_gradients(p.M, p.N, p.K, x_parts);
     if (!encode(&maps.a[0], q.dg_rows, p.M, p.N, q.pitch, 128) ||
         !encode(&maps.a[1], q.du_rows, p.M, p.N, q.pitch, 128) ||
         !encode(&maps.a[2], q.dg_cols, p.M, p.N, q.pitch, 64) ||
         !encode(&maps.a[3], q.du_cols, p.M, p.N, q.pitch, 64) ||
         !encode(&maps.b[0], in.w_gate, p.N, p.K, in.ldg, 64) ||
         !encode(&maps.b[1], in.w_up, p.N, p.K, in.ldu, 64) ||
-        !encode(&maps.b[2], in.x, p.M, p.K, in.ldx, 64))
+        !encode(&maps.b[2], in.x, p.M, p.K, in.ldx, 64) ||
+        (rest && !encode(&maps.b[3], rest, p.M, p.K, in.ldx, 64)))
         return cudaErrorInvalidValue;
     const int tiles_n = static_cast<int>(up_to(p.K, c.bn));
     pl.of[0] = {p.M, p.K, static_cast<int>(up_to(p.M, kTileRows)), tiles_n,
-                static_cast<int>(2 * up_to(p.N, 64)), c.split_x};
+                static_cast<int>(2 * up_to(p.N, 64)), static_cast<int>(up_to(p.N, 64)), c.split_x};
     pl.of[1] = {p.N, p.K, static_cast<int>(2 * up_to(p.N, kTileRows)), tiles_n,
-                static_cast<int>(up_to(p.M, 64)), c.split_w};
+                static_cast<int>(x_parts * up_to(p.M, 64)), static_cast<int>(up_to(p.M, 64)), c.split_w};
     pl.pairs = static_cast<int>(std::min<long long>(sms / 2, pl.of[0].items() + pl.of[1].items()));
     pl.extra = spread(pl.of[0].items(), pl.of[1].items(), item_clocks(up_to(pl.of[0].stages, c.split_x), c.bn),
                       item_clocks(up_to(pl.of[1].stages, c.split_w), c.bn), pl.pairs).extra;
@@ -684,18 +691,23 @@ int packed_bit(int bit, const void* p, long long rows, long long ld) {
 
 FfChoice choose_gated_ff(int product, int M, int N, int K, int keep) {
     if (product == kProductForward) return choose_forward(M, N, K, keep);
-    const Gradients c = choose_gradients(M, N, K);
+    const Gradients c = choose_gradients(M, N, K, 1);
     return FfChoice{c.bn, product == kProductInput ? c.split_x : c.split_w};
 }
 size_t gated_ff_forward_workspace(int M, int N, int K, int packed) {
     return copied_bytes(M, N, K, packed);
 }
 size_t gated_ff_backward_workspace(int M, int N, int K, int packed) {
-    const Gradients c = choose_gradients(M, N, K);
-    const long long parts = (c.split_x > 1 ? 1LL * c.split_x * M : 0) + (c.split_w > 1 ? 2LL * c.split_w * N : 0);
     const long long scaled = packed & kPackedFp16 ? 2 * matrix_bytes(M, N) + largest_bytes(M, N) : 0;
-    return static_cast<size_t>(2 * matrix_bytes(M, N) + scaled) + copied_bytes(M, N, K, packed) +
-           static_cast<size_t>(parts * up64(K)) * sizeof(float);
+    const auto with = [&](int x_parts) {
+        const Gradients c = choose_gradients(M, N, K, x_parts);
+        const long long parts =
+            (c.split_x > 1 ? 1LL * c.split_x * M : 0) + (c.split_w > 1 ? 2LL * c.split_w * N : 0);
+        return static_cast<size_t>(2 * matrix_bytes(M, N) + scaled + (x_parts - 1) * matrix_bytes(M, K)) +
+               copied_bytes(M, N, K, packed) + static_cast<size_t>(parts * up64(K)) * sizeof(float);
+    };
+    // (The same bit stands for an x whose rows are copied and for one in 8 bits.)
+    return packed & 1 ? std::max(with(1), with(2)) : with(1);
 }
 int gated_ff_packed(const GatedFfForward& p) {
     if (choose_forward(p.M, p.N, p.K, p.kept.keep).bn == 0) return 0;

@@ -120,7 +120,8 @@ int sgemm_act8_dequantize(int rows, int cols, const void* codes, const float* sc
         if (rows == 0 || cols == 0) return SGEMM_OK;
         int sms = 0;
         SGEMM_TRY(current_device_sms(&sms));
-        const Act8Dequantize q{rows, cols, dtype, static_cast<const int8_t*>(codes), scales, Y, ldy};
+        const Act8Dequantize q{rows, cols, dtype, static_cast<const int8_t*>(codes), scales, Y, ldy,
+                               nullptr};
         return launched(launch_act8_dequantize(q, sms, stream_of(stream)), "sgemm_act8_dequantize");
     });
 }

@@ -112,9 +112,10 @@ def gated_ff_backward(dh, x, w_gate, w_up, kept, *, activation: str = "silu",
                       return_h: bool = False, stream=None):
     """(dx, dw_gate, dw_up) of ``gated_ff`` from the gradient of h.  ``x`` is the block's input
     or an ``Act8`` of it, ``kept`` what ``gated_ff(..., keep=...)`` returned.  With ``return_h``
-    also h, made again from what was kept: (dx, dw_gate, dw_up, h).  Gradients are of dh's type; what
-    the products multiply, the gradients of the pre-activations and an x in 8 bits, is rounded to it
-    too, float16 with powers of two that keep float32's range (``include/sgemm.h``)."""
+    also h, made again from what was kept: (dx, dw_gate, dw_up, h).  Gradients are of dh's type; the
+    gradients of the pre-activations, which the products multiply, are rounded to it too, float16
+    with powers of two that keep float32's range.  The numbers of an ``Act8`` x are taken whole, in
+    two parts (``include/sgemm.h``)."""
     act = _activation(activation)
     if not isinstance(kept, (tuple, list)) or len(kept) != 2:
         raise TypeError("kept must be the (gate, up) that gated_ff(..., keep=...) returned")
