@@ -23,7 +23,7 @@ using mx4::to_float;
 // the smaller part of 1 + e then.  h and what the products take are rounded to 2^-8 or 2^-11 afterwards.
 constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
-constexpr float kHalfLog2E = 0.72134752f;
+constexpr float kHalfLog2E = 0.7213475204444817f;
 
 __device__ __forceinline__ float exp2_fast(float x) {        // 0 where 2^x is below 2^-126
     float r;
@@ -35,11 +35,9 @@ __device__ __forceinline__ float reciprocal_fast(float x) {  // of 1 to 2
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// -bound to bound; a NaN stays one.
-__device__ __forceinline__ float held_to(float x, float bound) {
+__device__ __forceinline__ float smaller(float x, float y) { // (a NaN stays one)
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(-bound));
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(bound));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 
@@ -49,17 +47,20 @@ struct Act {
     __device__ __forceinline__ static Act of(float g) {
         Act a;
         a.g = a.near = g;
-        float z = g;
         a.slope_z = 1.0f;
+        float root;                                          // 2^(-|z| log2(e) / 2)
         if (ACT == kGeluTanh) {
             // From |g| = 30 on s is 0 or 1, and beyond 10^19 g^2 would overflow.
-            const float c = held_to(g, 30.0f), q = c * c;
-            a.near = c;
-            z = kGeluC * c * fmaf(kGeluCube, q, 1.0f);
+            const float c = smaller(fabsf(g), 30.0f), q = c * c;
+            constexpr float line = -kGeluC * kHalfLog2E, cube = line * kGeluCube;
+            root = exp2_fast(c * fmaf(cube, q, line));
+            a.near = copysignf(c, g);
             a.slope_z = kGeluC * fmaf(3.0f * kGeluCube, q, 1.0f);
+        } else {
+            root = exp2_fast(-kHalfLog2E * fabsf(g));
         }
-        const float root = exp2_fast(-kHalfLog2E * fabsf(z)), e = root * root, r = reciprocal_fast(1.0f + e);
-        a.s = z < 0.0f ? e * r : r;
+        const float e = root * root, r = reciprocal_fast(1.0f + e);
+        a.s = g < 0.0f ? e * r : r;
         return a;
     }
     __device__ __forceinline__ float value() const { return g * s; }
