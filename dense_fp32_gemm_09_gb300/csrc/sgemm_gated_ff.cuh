@@ -18,9 +18,9 @@ using mx4::to_float;
 // z leaves fp32 before s does.  (1 / (1 + e^-z) by the fast reciprocal was 0 from z = -87.4 down, where
 // s is 1e-38, and bf16's g s u an ordinary number if u is large.)  e is the square of 2^(-|z| log2(e) / 2),
 // whose smallest numbers are normal ones where e's are not, as the hardware's exponential wants them.
-// The exponent's two roundings make e off by |z| 2^-23 of itself, the exponential and the reciprocal by a
-// few 2^-23: s by about 2^-20 at z = -3, 2^-18.5 at -20 and 2^-16.5 at -80, and less where z > 0, as e is
-// the smaller part of 1 + e then.  h and what the products take are rounded to 2^-8 or 2^-11 afterwards.
+// The exponent's roundings make e off by up to 2 |z| 2^-23 of itself, the exponential and the reciprocal by a
+// few 2^-23: s by at most about 2^-19.5 at z = -3, 2^-17.5 at -20 and 2^-15.5 at -80, and less where z > 0,
+// as e is the smaller part of 1 + e then.  h and what the products take are rounded to 2^-8 or 2^-11 afterwards.
 constexpr float kGeluC = 1.5957691216057308f;      // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 constexpr float kHalfLog2E = 0.7213475204444817f;
