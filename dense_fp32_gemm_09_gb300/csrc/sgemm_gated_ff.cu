@@ -9,8 +9,8 @@
 // is off by the rounding of its terms (half an ulp each, at random) beside its own: in norm, bf16,
 // 2.3e-3 of 64 bits' where the rounding of the result alone is 1.7e-3.  The numbers of an x that comes in
 // 8 bits are code times scale, of more bits than the type has: the products take the rounding and the
-// rounding of what is left, as two halves of one contraction (the rounding alone: 2.8e-3).  fp16 has too few exponents for dg and
-// du and takes them by powers of two for each row and column (ff_gradient_fp16).
+// rounding of what is left, as two halves of one contraction (the rounding alone: 2.8e-3).  fp16 has too few
+// exponents for dg and du and takes them by powers of two for each row and column (ff_gradient_fp16).
 //
 // The products: sgemm_ff_pair.cuh, and sgemm_ff_token.cu for up to 16 tokens.  Rows that are not on
 // 16 bytes cannot be read by tensor maps and, for these, are copied into the workspace first (3001 x 2047 and
