@@ -556,8 +556,8 @@ cudaError_t gradient(const GatedFfBackward& p, const Scaled& q, int sms, cudaStr
                                          q.rows, words);
         if (e != cudaSuccess) return e;
         ++*launches;
-        const dim3 grid(static_cast<unsigned>(tiles),
-                        static_cast<unsigned>(std::max(1LL, std::min(up_to(p.M, kThreads / 32), sms * kBlocksAnSm / tiles))));
+        const long long bands = std::min(up_to(p.M, kThreads / 32), sms * kBlocksAnSm / tiles);
+        const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(std::max(1LL, bands)));
         e = launch_dependent(in8 ? ff_gradient_fp16<ACT, true, false> : ff_gradient_fp16<ACT, false, false>, grid,
                              kThreads, 0, st, p, q, on);
         if (e != cudaSuccess) return e;

@@ -24,7 +24,8 @@
 // Measured (us, kernels alone; of the memory's 6.79 TB/s).  Forward: 16384 x 8192 bf16 92 (0.86),
 // 8192 x 8192 fp32 87 (0.91), 4096 x 16384 bf16 57 (0.70), 3001 x 2047 fp32 10.2 (0.71), with the
 // input kept in 8 bits too 8192 x 8192 bf16 73 (0.68), 3001 x 2047 fp32 14 (0.58); streaming, 4096 x 16384
-// fp32 104 (0.76; with one number of a thread at a time loaded and stored 120).  Gradient, with dy: 8192 x 8192 bf16 92 (0.86), 8192 x 4096 bf16 51.5 (0.77) and fp32
+// fp32 104 (0.76; with one number of a thread at a time loaded and stored 120).  Gradient, with dy:
+// 8192 x 8192 bf16 92 (0.86), 8192 x 4096 bf16 51.5 (0.77) and fp32
 // 84 (0.94), 8192 x 1024 bf16 19.5 (0.51), 4096 x 16384 bf16 136 (0.58), 3001 x 2047 fp32 22.3 (0.65);
 // from a checkpoint 8192 x 4096 bf16 57 (0.61), 3001 x 2047 fp32 20.9 (0.57); ragged 3001 x 5001 bf16
 // forward 19.9 (0.44), gradient 49 (0.36).  The gradient of 2-byte

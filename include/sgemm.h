@@ -524,9 +524,9 @@ SGEMM_API int sgemm_layer_norm_choose_check(int rows, int cols, int dtype, int b
  * checkpoints, and otherwise copied into the workspace first.  `ws` is the caller's
  * device memory: 128-byte aligned, at least as many bytes as sgemm_gated_ff_workspace gives for
  * these sizes (`backward` 0 or 1; `packed`: 1 for an x, 2 for a w_gate, 4 for a w_up that is
- * copied, 1 for an x given in 8 bits too; backward, 8 more for SGEMM_F16); it needs no initialisation and must stay untouched by
- * other work while the call runs; NULL where 0 bytes are needed.  Outputs must not overlap
- * inputs.  Any alignment to the element.  N == 0 or K == 0 is SGEMM_ERR_INVALID_ARG, M == 0 a
+ * copied, 1 for an x given in 8 bits too; backward, 8 more for SGEMM_F16); it needs no
+ * initialisation and must stay untouched by other work while the call runs; NULL where 0 bytes
+ * are needed.  Outputs must not overlap inputs.  Any alignment to the element.  N == 0 or K == 0 is SGEMM_ERR_INVALID_ARG, M == 0 a
  * no-op. */
 typedef enum { SGEMM_SILU = 0, SGEMM_GELU_TANH = 1 } sgemm_activation;
 typedef enum { SGEMM_KEEP_NONE = 0, SGEMM_KEEP_FULL = 1, SGEMM_KEEP_8BIT = 2 } sgemm_keep;
@@ -555,9 +555,9 @@ SGEMM_API int sgemm_gated_ff_choose_check(int M, int N, int K, int keep, int pro
  * what was kept.  For the products dg and du are rounded to `dtype` too, so that dx and the weights'
  * gradients are 1.4 times as far from the formula as by their own rounding alone; the numbers of an x in
  * 8 bits, which have to be in the range of `dtype`, are taken as two of it, their rounding and what it
- * leaves.  dg and du have the range of fp32 for SGEMM_F16 as well: the products take each row of (dg, du), for dx, and each column of dg
- * and of du, for the weights' gradients, times a power of two of its own.  Numbers below 2^-29 of a
- * row's or a column's largest are held to 2^-40 of that.  M == 0 writes zeros to the weights'
+ * leaves.  dg and du have the range of fp32 for SGEMM_F16 as well: the products take each row of
+ * (dg, du), for dx, and each column of dg and of du, for the weights' gradients, times a power of
+ * two of its own.  Numbers below 2^-29 of a row's or a column's largest are held to 2^-40 of that.  M == 0 writes zeros to the weights'
  * gradients. */
 SGEMM_API int sgemm_gated_ff_backward(int M, int N, int K, int dtype, int activation,
                                       const void* dh, int lddh, const void* x, int ldx,
