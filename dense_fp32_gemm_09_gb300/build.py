@@ -100,7 +100,7 @@ def _try_binding(force: bool) -> None:
     try:
         build_binding(force)
     except (ImportError, OSError, RuntimeError) as e:
-        warnings.warn(f"the binding of the operators around the product was not built: {e}")
+        warnings.warn(f"the binding of the 4-bit, norm and feed-forward operators was not built: {e}")
 
 
 def _compile(src: str, verbose: bool) -> str:
